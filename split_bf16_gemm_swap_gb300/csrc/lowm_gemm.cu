@@ -18,6 +18,7 @@
 #include <unordered_map>
 
 #include "../../include/lowm_gemm.h"
+#include "layer_host.h"
 #include "lowm_kernels.h"
 
 namespace lowm {
@@ -66,9 +67,7 @@ constexpr int kSmemPerSm = 233472;         // 228 KiB per SM
 constexpr int kSmemReservedPerCta = 1024;  // the runtime keeps 1 KiB per resident CTA
 
 // ------------------------------------------------------------------ driver entry point
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using lowm::EncodeTiledFn;
 
 EncodeTiledFn get_encode_fn()
 {
@@ -793,6 +792,15 @@ lowm_status_t launch(const void *A, const void *W, void *C, int M, int N, int K,
 }
 
 }  // namespace
+
+namespace lowm {
+
+// For the decoder-layer operators (layer_host.h).
+lowm_status_t host_check_device(int *sms) { return check_device(sms); }
+unsigned int *host_status_word() { return status_word(); }
+EncodeTiledFn host_encode_fn() { return get_encode_fn(); }
+
+}  // namespace lowm
 
 extern "C" {
 

@@ -1,0 +1,275 @@
+// The norms after and before a block, its gate and the residual scale, one
+// pass: r' = s r + g RMS(y; w_post), n = RMS(r'; w_pre) (lowm_layer.h).
+//
+// One CTA owns one token.  Everything the row needs (y, r, gate, weights) is
+// requested before the first reduction, stays in registers as it came (two
+// bytes an element) and r' stays there in fp32, so each byte moves once and
+// the two reductions are the only waits.  At decode sizes the time is the
+// launch, one memory latency and the two reductions; at prompt sizes it is
+// the bandwidth of r, y, r' and n.
+#include <cuda_bf16.h>
+
+#include "layer_host.h"
+#include "ptx.cuh"
+
+namespace lowm {
+namespace {
+
+struct NormParams {
+    const void *residual;
+    const __nv_bfloat16 *block, *post, *gate, *pre;
+    void *out_residual;
+    __nv_bfloat16 *out;
+    int64_t residual_stride, block_stride, gate_stride, out_residual_stride, out_stride;
+    int hidden;
+    float scale, eps, inv_hidden;
+};
+
+// VEC elements of a row starting at i: one 16-byte access of bf16 (two of
+// fp32) when VEC is 8, one element when VEC is 1.
+template <int VEC>
+struct Pack {
+    __nv_bfloat16 v[VEC];
+};
+
+template <int VEC>
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16 *p, Pack<VEC> &o)
+{
+    if constexpr (VEC == 8)
+        *reinterpret_cast<uint4 *>(o.v) = *reinterpret_cast<const uint4 *>(p);
+    else
+        o.v[0] = *p;
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16 *p, const float (&f)[VEC])
+{
+    if constexpr (VEC == 8) {
+        uint4 u;
+        __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        *reinterpret_cast<uint4 *>(p) = u;
+    } else {
+        *p = __float2bfloat16_rn(f[0]);
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_f32(const float *p, float (&o)[VEC])
+{
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(p);
+        *reinterpret_cast<float4 *>(o + 4) = *reinterpret_cast<const float4 *>(p + 4);
+    } else {
+        o[0] = *p;
+    }
+}
+
+// Sum over the block: lanes by shuffles, then warps in index order through
+// shared memory; every thread gets the same value.
+__device__ __forceinline__ float block_sum(float x, float *scratch)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1)
+        return x;
+    if ((threadIdx.x & 31) == 0)
+        scratch[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = (int)(threadIdx.x & 31) < warps ? scratch[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// ELEMS elements a thread in pieces of VEC, piece n at (n * blockDim.x + thread) * VEC.
+template <int VEC, int ELEMS, bool F32>
+__global__ void __launch_bounds__(ELEMS == 8 ? 1024 : 512) residual_norm_kernel(const NormParams p)
+{
+    constexpr int NP = ELEMS / VEC;
+    __shared__ float scratch[2][32];
+    const int64_t t = blockIdx.x;
+    const __nv_bfloat16 one = __float2bfloat16_rn(1.f);
+
+    Pack<VEC> post[NP], pre[NP];
+    const int step = (int)blockDim.x * VEC, first = (int)threadIdx.x * VEC;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+
+    Pack<VEC> y[NP], g[NP];
+    float r[NP][VEC];
+    const bool has_gate = p.gate != nullptr, has_block = p.block != nullptr, has_post = p.post != nullptr,
+               has_pre = p.pre != nullptr;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const int i = n * step + first;
+        const bool in = i < p.hidden;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            y[n].v[j] = __float2bfloat16_rn(0.f);
+            g[n].v[j] = post[n].v[j] = pre[n].v[j] = one;
+            r[n][j] = 0.f;
+        }
+        if (!in)
+            continue;
+        if (has_block)
+            load_bf16(p.block + t * p.block_stride + i, y[n]);
+        if constexpr (F32) {
+            load_f32(static_cast<const float *>(p.residual) + t * p.residual_stride + i, r[n]);
+        } else {
+            Pack<VEC> q;
+            load_bf16(static_cast<const __nv_bfloat16 *>(p.residual) + t * p.residual_stride + i, q);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                r[n][j] = __bfloat162float(q.v[j]);
+        }
+        if (has_gate)
+            load_bf16(p.gate + t * p.gate_stride + i, g[n]);
+        if (has_post)
+            load_bf16(p.post + i, post[n]);
+        if (has_pre)
+            load_bf16(p.pre + i, pre[n]);
+    }
+
+    float inv = 1.f;
+    if (has_post) {
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float v = __bfloat162float(y[n].v[j]);
+                sum = fmaf(v, v, sum);
+            }
+        inv = rsqrtf(fmaf(block_sum(sum, scratch[0]), p.inv_hidden, p.eps));
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            if (has_block) {
+                const float v = __bfloat162float(y[n].v[j]) * inv * __bfloat162float(post[n].v[j]);
+                r[n][j] = fmaf(r[n][j], p.scale, v * __bfloat162float(g[n].v[j]));
+            }
+            sum = fmaf(r[n][j], r[n][j], sum);
+        }
+    if (has_block) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int i = n * step + first;
+            if (i >= p.hidden)
+                continue;
+            if constexpr (F32) {
+                float *o = static_cast<float *>(p.out_residual) + t * p.out_residual_stride + i;
+                if constexpr (VEC == 8) {
+                    reinterpret_cast<float4 *>(o)[0] = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
+                    reinterpret_cast<float4 *>(o)[1] = make_float4(r[n][4], r[n][5], r[n][6], r[n][7]);
+                } else {
+                    *o = r[n][0];
+                }
+            } else {
+                store_bf16(static_cast<__nv_bfloat16 *>(p.out_residual) + t * p.out_residual_stride + i, r[n]);
+            }
+        }
+    }
+    inv = rsqrtf(fmaf(block_sum(sum, scratch[1]), p.inv_hidden, p.eps));
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const int i = n * step + first;
+        if (i >= p.hidden)
+            continue;
+        float o[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            o[j] = r[n][j] * inv * __bfloat162float(pre[n].v[j]);
+        store_bf16(p.out + t * p.out_stride + i, o);
+    }
+}
+
+template <int VEC, int ELEMS>
+lowm_status_t launch_norm(const NormParams &p, int tokens, bool f32, void *stream)
+{
+    const int threads = ((p.hidden + ELEMS - 1) / ELEMS + 31) / 32 * 32;
+    return launch_pdl(f32 ? residual_norm_kernel<VEC, ELEMS, true> : residual_norm_kernel<VEC, ELEMS, false>,
+                      dim3((unsigned)tokens), dim3((unsigned)threads), 0, stream, p);
+}
+
+bool range_overlaps(const void *a, int64_t a_stride, int64_t a_size, const void *b, int64_t b_stride, int64_t b_size,
+                    int tokens, int hidden)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const uintptr_t nx = (uintptr_t)(((tokens - 1) * a_stride + hidden) * a_size);
+    const uintptr_t ny = (uintptr_t)(((tokens - 1) * b_stride + hidden) * b_size);
+    return x < y + ny && y < x + nx;
+}
+
+}  // namespace
+}  // namespace lowm
+
+extern "C" lowm_status_t lowm_residual_norm(const void *residual, int residual_f32, int64_t residual_stride,
+                                            const void *block, int64_t block_stride, const void *post_weight,
+                                            const void *gate, int64_t gate_stride, const void *pre_weight,
+                                            void *out_residual, int64_t out_residual_stride, void *out,
+                                            int64_t out_stride, int tokens, int hidden, float scale, float eps,
+                                            void *stream)
+{
+    using namespace lowm;
+    constexpr int kMaxHidden = 16384;                // 512 threads of 32 elements
+    if (tokens < 0 || hidden <= 0 || !(eps >= 0.f))
+        return LOWM_ERR_INVALID_ARGUMENT;
+    if (hidden > kMaxHidden)
+        return LOWM_ERR_UNSUPPORTED_SHAPE;
+    if (block ? !out_residual : (post_weight || gate || out_residual || scale != 1.f))
+        return LOWM_ERR_INVALID_ARGUMENT;
+    if (tokens == 0)
+        return LOWM_OK;
+    if (!residual || !out)
+        return LOWM_ERR_INVALID_ARGUMENT;
+    if (residual_stride < 0 || block_stride < 0 || gate_stride < 0 || (out_residual && out_residual_stride < hidden) ||
+        out_stride < hidden)
+        return LOWM_ERR_INVALID_ARGUMENT;
+    const int size = residual_f32 ? 4 : 2;
+    if (!is_aligned(residual, size) || !is_aligned(out_residual, size) || !is_aligned(block, 2) ||
+        !is_aligned(post_weight, 2) || !is_aligned(gate, 2) || !is_aligned(pre_weight, 2) || !is_aligned(out, 2))
+        return LOWM_ERR_MISALIGNED;
+    if (out_residual && range_overlaps(out_residual, out_residual_stride, size, out, out_stride, 2, tokens, hidden))
+        return LOWM_ERR_INVALID_ARGUMENT;
+    const lowm_status_t st = host_check_device(nullptr);
+    if (st != LOWM_OK)
+        return st;
+
+    NormParams p;
+    p.residual = residual;
+    p.block = static_cast<const __nv_bfloat16 *>(block);
+    p.post = static_cast<const __nv_bfloat16 *>(post_weight);
+    p.gate = static_cast<const __nv_bfloat16 *>(gate);
+    p.pre = static_cast<const __nv_bfloat16 *>(pre_weight);
+    p.out_residual = out_residual;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.residual_stride = residual_stride;
+    p.block_stride = block_stride;
+    p.gate_stride = gate_stride;
+    p.out_residual_stride = out_residual_stride;
+    p.out_stride = out_stride;
+    p.hidden = hidden;
+    p.scale = scale;
+    p.eps = eps;
+    p.inv_hidden = 1.f / (float)hidden;
+
+    const int64_t rmod = residual_f32 ? 3 : 7;
+    const bool vec = hidden % 8 == 0 && !((residual_stride | out_residual_stride) & rmod) &&
+                     !((block_stride | gate_stride | out_stride) & 7) && is_aligned(residual, 16) &&
+                     is_aligned(block, 16) && is_aligned(post_weight, 16) && is_aligned(gate, 16) &&
+                     is_aligned(pre_weight, 16) && is_aligned(out_residual, 16) && is_aligned(out, 16);
+    if (vec)
+        return hidden <= 8192 ? launch_norm<8, 8>(p, tokens, residual_f32 != 0, stream)
+                              : launch_norm<8, 32>(p, tokens, residual_f32 != 0, stream);
+    return hidden <= 8192 ? launch_norm<1, 8>(p, tokens, residual_f32 != 0, stream)
+                          : launch_norm<1, 32>(p, tokens, residual_f32 != 0, stream);
+}

@@ -1,78 +1,800 @@
 // Attention of each sequence's newest tokens over its paged keys and values
-// (lowm_layer.h).  One warp owns one (token, head): it walks the keys the
-// token sees with a running maximum and sum.
+// (lowm_layer.h), on the tensor cores.
+//
+// Work.  The rows of one key/value head are its queries of one sequence, token
+// by token and head of the group by head (row = token * group + g), so a key is
+// read once for all heads that share it.  An item is up to 128 such rows (one
+// MMA M) and the tiles of 64 keys that any of them sees.  All items' tiles,
+// sequence after sequence, form one line that is cut into equal shares, one
+// for each CTA of a grid of two per SM: a CTA's time does not depend on how
+// the lengths are spread over the batch.  The host knows no length; every warp
+// finds its share from cu_q and kv_lens by itself.  A share that begins or
+// ends inside an item leaves its rows' sum, maximum and weighted values (fp32)
+// in the workspace, and a second small kernel joins the parts in order.
+//
+// A CTA has four softmax warps (a thread owns a row = a TMEM lane), a warp
+// that feeds a ring of 64-key tiles by TMA, page by page, and a warp that
+// issues the MMAs: S = Q K^T into one of two TMEM buffers, then O += P V with
+// P (bf16, written over its S) from TMEM and V as the transposed operand.
+// S of the next tile is computed while the softmax of this one runs, and the
+// two CTAs of an SM fill each other's gaps.  O is rescaled only when a row's
+// maximum has grown by 2^8 (the weights stay below 256, and bf16 and fp32 are
+// relative), so most tiles leave O alone.
+//
+// Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
+// their sum, which divides, adds the unrounded fp32 weights.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "layer_host.h"
-#include "ptx.cuh"
+#include "lowm_kernel.cuh"
 
 namespace lowm {
 namespace {
 
-struct AttnParams {
-    const __nv_bfloat16 *q, *k, *v;
-    __nv_bfloat16 *out;
-    float *lse;
-    int64_t q_ts, q_hs, o_ts, o_hs, k_page, k_place, k_head, v_page, v_place, v_head, num_pages, table_stride;
-    const int32_t *table, *kv_lens, *cu_q;
-    int page_size, table_width, batch, q_tokens, heads, kv_heads, window;
-    float scale;
+constexpr int kTileKeys = 64;
+constexpr int kTileRows = 128;
+constexpr int kAttnThreads = 192;            // softmax warps 0-3, TMA warp 4, MMA warp 5
+constexpr int kMaxAttnCtas = 320;            // two per SM, and a bound for the workspace
+constexpr int kMinShare = 4;                 // tiles: a share below 256 keys costs more in the join than it saves
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kSColumns = 64;           // one S buffer; P takes its first 32 columns
+
+// Bits of the device status word (above those of the GEMM).
+enum : uint32_t {
+    kErrAttnRing = 1u << 12,
+    kErrAttnFull = 1u << 13,
+    kErrAttnScores = 1u << 14,
+    kErrAttnWeights = 1u << 15,
+    kErrAttnOutput = 1u << 16,
+    kErrAttnBase = 1u << 17,                 // dynamic shared memory not on a 1024-byte boundary
 };
 
-template <int DIM>
-__global__ void __launch_bounds__(128) attention_kernel(const AttnParams p)
+struct AttnParams {
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *out;
+    float *lse;
+    int64_t q_ts, q_hs, o_ts, o_hs, table_stride;
+    const int32_t *table, *kv_lens, *cu_q;
+    int page_size, page_shift, table_width, batch, q_tokens, heads, kv_heads, group, window, slot_rows;
+    int capacity;                            // keys a sequence can have: table_width * page_size
+    float scale_log2;                        // |scale| * log2(e); the sign is in Q
+    float q_sign;
+    bool q_vec, out_vec;                     // 16-byte rows
+    float *parts;                            // [2 * ctas][slot_rows][dim] sums, then [2 * ctas][slot_rows][2] (max, sum)
+    unsigned int *status;
+};
+
+// ------------------------------------------------------------------ the line of tiles
+struct Item {
+    int b, head, q_tile;                     // sequence, key/value head, tile of 128 rows
+    int q0, q_len, kv;                       // the sequence's first row of q, new tokens, keys
+    int first_tile, tiles;                   // tiles of 64 keys
+    int64_t start;                           // the item's first tile on the line
+};
+
+__device__ __forceinline__ void load_sequence(const AttnParams &p, int b, int &q0, int &q_len, int &kv)
 {
-    constexpr int E = DIM / 32;
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
+    q0 = min(max(p.cu_q[b], 0), p.q_tokens);
+    q_len = min(max(p.cu_q[b + 1], q0), p.q_tokens) - q0;
+    kv = min(max(p.kv_lens[b], 0), p.capacity);
+}
+
+// Tiles that rows [128 q_tile, 128 q_tile + 128) of a sequence see.  Rows that
+// see nothing still form one (fully masked) tile, so that they are written.
+__device__ __forceinline__ void tile_range(const AttnParams &p, int q_len, int kv, int q_tile, int &first, int &tiles)
+{
+    const int t0 = q_tile * kTileRows / p.group, t1 = min(q_len - 1, (q_tile * kTileRows + kTileRows - 1) / p.group);
+    const int64_t hi = max(0, kv - q_len + t1 + 1);
+    const int64_t lo = p.window > 0 ? max((int64_t)0, (int64_t)kv - q_len + t0 - p.window + 1) : 0;
+    first = lo < hi ? (int)(lo / kTileKeys) : 0;
+    tiles = lo < hi ? (int)((hi + kTileKeys - 1) / kTileKeys) - first : 1;
+}
+
+__device__ __forceinline__ int q_tiles_of(const AttnParams &p, int q_len)
+{
+    return (q_len * p.group + kTileRows - 1) / kTileRows;
+}
+
+// Tiles of one key/value head of sequence b (all its row tiles).
+__device__ __forceinline__ int64_t head_tiles(const AttnParams &p, int b)
+{
+    int q0, q_len, kv, first, n;
+    load_sequence(p, b, q0, q_len, kv);
+    int64_t sum = 0;
+    for (int t = 0; t < q_tiles_of(p, q_len); ++t) {
+        tile_range(p, q_len, kv, t, first, n);
+        sum += n;
+    }
+    return sum;
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t x)
+{
+    for (int o = 16; o > 0; o >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Tiles of the whole line (one warp, lanes over sequences).
+__device__ __forceinline__ int64_t line_length(const AttnParams &p)
+{
+    int64_t sum = 0;
+    for (int b = threadIdx.x & 31; b < p.batch; b += 32)
+        sum += head_tiles(p, b);
+    return warp_sum(sum) * p.kv_heads;
+}
+
+// The item that tile u of the line belongs to (one warp; u below line_length).
+__device__ __forceinline__ Item locate(const AttnParams &p, int64_t u)
+{
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (unit >= (int64_t)p.q_tokens * p.heads)
-        return;
-    const int t = (int)(unit / p.heads), h = (int)(unit % p.heads);
-    int b = 0;
-    while (b < p.batch && p.cu_q[b + 1] <= t)
-        ++b;
-    float o[E] = {}, m = -CUDART_INF_F, l = 0.f;
-    if (b < p.batch) {
-        const int64_t cap = (int64_t)p.table_width * p.page_size;
-        const int64_t kv = min((int64_t)max(p.kv_lens[b], 0), cap);
-        const int64_t pos = kv - (p.cu_q[b + 1] - t);
-        const int g = h / (p.heads / p.kv_heads);
-        float q[E];
-        for (int i = 0; i < E; ++i)
-            q[i] = __bfloat162float(p.q[t * p.q_ts + h * p.q_hs + lane * E + i]) * p.scale;
-        for (int64_t j = p.window > 0 ? max((int64_t)0, pos - p.window + 1) : 0; j <= pos; ++j) {
-            const int64_t page = p.table[b * p.table_stride + j / p.page_size];
-            const bool in = page >= 0 && page < p.num_pages;
-            const __nv_bfloat16 *k = p.k + page * p.k_page + (j % p.page_size) * p.k_place + g * p.k_head + lane * E;
-            const __nv_bfloat16 *v = p.v + page * p.v_page + (j % p.page_size) * p.v_place + g * p.v_head + lane * E;
-            float s = 0.f;
-            for (int i = 0; i < E; ++i)
-                s += in ? q[i] * __bfloat162float(k[i]) : 0.f;
-            for (int x = 16; x > 0; x >>= 1)
-                s += __shfl_xor_sync(0xffffffffu, s, x);
-            const float mn = fmaxf(m, s), a = expf(m - mn), e = expf(s - mn);
-            l = l * a + e;
-            m = mn;
-            for (int i = 0; i < E; ++i)
-                o[i] = o[i] * a + (in ? e * __bfloat162float(v[i]) : 0.f);
+    Item it;
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += 32) {
+        const int64_t mine = b0 + lane < p.batch ? head_tiles(p, b0 + lane) * p.kv_heads : 0;
+        int64_t incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > u);
+        if (past || b0 + 32 >= p.batch) {
+            const int l = past ? __ffs(past) - 1 : 31;
+            it.b = min(b0 + l, p.batch - 1);
+            before += __shfl_sync(0xffffffffu, incl - mine, l);
+            const int64_t all = __shfl_sync(0xffffffffu, mine, l);
+            const int64_t per_head = max(all / p.kv_heads, (int64_t)1);
+            it.head = (int)((u - before) / per_head);
+            it.start = before + it.head * per_head;
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    load_sequence(p, it.b, it.q0, it.q_len, it.kv);
+    for (it.q_tile = 0;; ++it.q_tile) {
+        tile_range(p, it.q_len, it.kv, it.q_tile, it.first_tile, it.tiles);
+        if (u < it.start + it.tiles || it.q_tile + 1 >= q_tiles_of(p, it.q_len))
+            return it;
+        it.start += it.tiles;
+    }
+}
+
+// The item behind `it` on the line.
+__device__ __forceinline__ void advance(const AttnParams &p, Item &it)
+{
+    it.start += it.tiles;
+    if (++it.q_tile >= q_tiles_of(p, it.q_len)) {
+        it.q_tile = 0;
+        if (++it.head == p.kv_heads) {
+            it.head = 0;
+            do {                             // sequences without new tokens have no items
+                ++it.b;
+                load_sequence(p, it.b, it.q0, it.q_len, it.kv);
+            } while (it.q_len == 0 && it.b + 1 < p.batch);
         }
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    for (int i = 0; i < E; ++i)
-        p.out[t * p.o_ts + h * p.o_hs + lane * E + i] = __float2bfloat16_rn(o[i] * inv);
-    if (p.lse && lane == 0)
-        p.lse[(int64_t)t * p.heads + h] = l == 0.f ? -CUDART_INF_F : m + logf(l);
+    tile_range(p, it.q_len, it.kv, it.q_tile, it.first_tile, it.tiles);
+}
+
+__device__ __forceinline__ int64_t share_of(int64_t line, int ctas)
+{
+    return max((line + ctas - 1) / ctas, (int64_t)kMinShare);
+}
+
+// One CTA's share of one item: tiles [from, to) of it.
+#define FOR_EACH_PIECE(p, it, u, end)                                                                            \
+    for (Item it = locate(p, u); u < end; u = it.start + it.tiles, u < end ? advance(p, it) : (void)0)
+
+// ------------------------------------------------------------------ PTX of this kernel
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B[smem desc], bf16 operands, fp32 accumulator.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// Descriptor of V as the MMA's B operand, N (the head's elements) contiguous:
+// 128-byte swizzled atoms of 64 elements x 8 keys; the leading offset leads to
+// the next 64 elements, the stride offset to the next 8 keys.
+__device__ __forceinline__ uint64_t make_sw128_nmajor_desc(uint32_t saddr, uint32_t next_64)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(next_64 >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// ------------------------------------------------------------------ shared memory
+template <int DIM>
+struct AttnSmem {
+    static constexpr uint32_t kHalves = DIM / 64;                       // 128-byte wide pieces of a row
+    static constexpr uint32_t kQ = 0;                                   // [halves][128 rows][64]
+    static constexpr uint32_t kTileBytes = kTileKeys * DIM * 2;
+    static constexpr uint32_t kRing = kTileRows * DIM * 2;              // [stages][halves][64 keys][64]
+    static constexpr uint32_t kStages = DIM == 128 ? 5 : 10;            // 80 KiB: two CTAs fill an SM's 227 KiB
+    static constexpr uint32_t kBars = kRing + kStages * kTileBytes;     // full, empty [stages]; q; s, p, o [2]; drain
+    static constexpr uint32_t kNumBars = 2 * kStages + 8;
+    static constexpr uint32_t kSlot = kBars + kNumBars * 8;
+    static constexpr uint32_t kBytes = kSlot + 16;                      // 112.2 KiB: two CTAs an SM
+};
+
+// Row r of the item belongs to token r / group, query head head * group + r % group.
+struct Row {
+    bool valid;
+    int token, q_head;                       // token: index into q
+    int64_t hi, lo;                          // keys lo..hi are seen
+};
+
+__device__ __forceinline__ Row row_of(const AttnParams &p, const Item &it, int r)
+{
+    Row w;
+    const int row = it.q_tile * kTileRows + r;
+    const int t = row / p.group;
+    w.valid = t < it.q_len;
+    w.token = it.q0 + t;
+    w.q_head = it.head * p.group + row % p.group;
+    w.hi = (int64_t)it.kv - it.q_len + t;
+    w.lo = p.window > 0 ? w.hi - p.window + 1 : 0;
+    return w;
+}
+
+template <int DIM>
+__device__ __forceinline__ void store_row(const AttnParams &p, const Row &w, int col, const float (&v)[32])
+{
+    __nv_bfloat16 *o = p.out + w.token * p.o_ts + w.q_head * p.o_hs + col;
+    if (p.out_vec) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            uint4 u;
+            __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                h[j] = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+            *reinterpret_cast<uint4 *>(o + i) = u;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            o[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kAttnThreads, 2)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                           const AttnParams p)
+{
+    using L = AttnSmem<DIM>;
+    constexpr uint32_t kColumns = 256;       // two S buffers and O (192 or 256 columns), a power of two
+    constexpr uint32_t kOColumn = 2 * kSColumns;
+    // The swizzle repeats every 1024 bytes, so the base must be a multiple; rounding it up at run time
+    // would cost the KiB that the second CTA of the SM needs.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kStages;
+    const uint32_t bar_q = bar_empty + 8 * L::kStages, bar_s = bar_q + 8, bar_p = bar_s + 16, bar_o = bar_p + 16,
+                   bar_drain = bar_o + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (sbase & 1023u) {
+        if (threadIdx.x == 0)
+            atomicOr(p.status, kErrAttnBase);
+        return;
+    }
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < L::kStages; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
+        }
+        ptx::mbar_init(bar_q, kTileRows);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar_s + 8 * i, 1);
+            ptx::mbar_init(bar_p + 8 * i, kTileRows);
+            ptx::mbar_init(bar_o + 8 * i, 1);
+        }
+        ptx::mbar_init(bar_drain, 1);
+        ptx::fence_mbarrier_init_cluster();
+        ptx::fence_proxy_async_shared();
+    }
+    if (warp == 5) {
+        ptx::tmem_alloc(sbase + L::kSlot, kColumns);
+        ptx::tmem_relinquish_alloc_permit();
+        ptx::tcgen05_fence_before_thread_sync();
+    }
+    __syncthreads();
+    ptx::tcgen05_fence_after_thread_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
+
+    ptx::griddep_wait();
+    // The join kernel may be scheduled from here on; what it reads before its
+    // own wait (cu_q, kv_lens) is final now.
+    ptx::griddep_launch_dependents();
+
+    const int64_t line = line_length(p);
+    const int64_t share = share_of(line, gridDim.x);
+    const int64_t begin = share * blockIdx.x, end = min(begin + share, line);
+
+    if (begin < end) {
+        if (warp == 4) {
+            // -------------------------------------------------------- TMA: K0, K1, V0, K2, V1, ...
+            const int box_keys = min(p.page_size, kTileKeys), boxes = kTileKeys / box_keys;
+            const int mine = lane / (int)L::kHalves, half = lane % (int)L::kHalves;   // this lane's box and half
+            uint32_t i = 0;
+            int64_t u = begin;
+            bool ok = true;
+            FOR_EACH_PIECE(p, it, u, end) {
+                const int from = (int)(u - it.start), to = (int)(min(end, it.start + it.tiles) - it.start);
+                const int32_t *pages = p.table + it.b * p.table_stride;
+                const int n = to - from;
+                // Table entries of this lane's box for the newest K tile and the V tile behind it.
+                auto entry = [&](int tile) {
+                    const int64_t key = (int64_t)(it.first_tile + tile) * kTileKeys + mine * box_keys;
+                    return mine < boxes && key < it.kv ? pages[key >> p.page_shift] : -1;
+                };
+                int page_k = entry(from), page_v = page_k, page_next = n > 1 ? entry(from + 1) : -1;
+                auto load = [&](const CUtensorMap *map, int tile, int page) {
+                    const uint32_t s = i % L::kStages;
+                    if (ok && !wait_bounded<false>(bar_empty + 8 * s, ((i / L::kStages) & 1) ^ 1, kDefaultTimeoutNs)) {
+                        ok = false;
+                        atomicOr(p.status, kErrAttnRing);
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok)
+                        return;
+                    const int key0 = (it.first_tile + tile) * kTileKeys;
+                    // Pages past the sequence's end are not requested.
+                    const int used = min(boxes, max(1, (it.kv - key0 + box_keys - 1) / box_keys));
+                    if (lane == 0)
+                        ptx::mbar_arrive_expect_tx(bar_full + 8 * s, (uint32_t)used * box_keys * DIM * 2);
+                    __syncwarp();
+                    if (mine < used)
+                        tma_load_4d(sbase + L::kRing + s * L::kTileBytes + half * (kTileKeys * 128) + mine * box_keys * 128,
+                                    map, half * 64, key0 & (p.page_size - 1), it.head, page, bar_full + 8 * s);
+                    ++i;
+                };
+                load(&map_k, from, page_k);
+                for (int j = 0; j < n; ++j) {
+                    page_v = page_k;
+                    if (j + 1 < n) {
+                        page_k = page_next;
+                        if (j + 2 < n)
+                            page_next = entry(from + j + 2);
+                        load(&map_k, from + j + 1, page_k);
+                    }
+                    load(&map_v, from + j, page_v);
+                }
+                if (!ok)
+                    break;
+            }
+            // No copy may land after the CTA has ended: normally all were consumed long ago.
+            for (uint32_t j = i > L::kStages ? i - L::kStages : 0; j < i; ++j)
+                (void)wait_bounded<false>(bar_full + 8 * (j % L::kStages), (j / L::kStages) & 1, kDrainTimeoutNs);
+        } else if (warp == 5) {
+            // -------------------------------------------------------- MMA
+            constexpr uint32_t kIdescS = make_idesc_bf16(kTileRows, kTileKeys);
+            constexpr uint32_t kIdescO = make_idesc_bf16(kTileRows, DIM) | (1u << 16);   // B: N contiguous
+            uint32_t i = 0, g = 0, items = 0;
+            int64_t u = begin;
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
+                if (ok && !wait_bounded<false>(bar, parity, kDefaultTimeoutNs)) {
+                    ok = false;
+                    if (lane == 0)
+                        atomicOr(p.status, err);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                ptx::tcgen05_fence_after_thread_sync();
+            };
+            auto scores = [&](uint32_t gs) {                            // S[gs & 1] = Q . K^T
+                const uint32_t s = i % L::kStages;
+                wait(bar_full + 8 * s, (i / L::kStages) & 1, kErrAttnFull);
+                ++i;
+                if (lane == 0 && ok) {
+#pragma unroll
+                    for (uint32_t h = 0; h < L::kHalves; ++h) {
+                        const uint64_t a = make_sw128_kmajor_desc(sbase + L::kQ + h * (kTileRows * 128));
+                        const uint64_t b = make_sw128_kmajor_desc(sbase + L::kRing + s * L::kTileBytes + h * (kTileKeys * 128));
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k)
+                            ptx::mma_bf16_ss(tmem + (gs & 1) * kSColumns, a + 2 * k, b + 2 * k, kIdescS, h + k > 0);
+                    }
+                    ptx::tcgen05_commit(bar_empty + 8 * s);
+                    ptx::tcgen05_commit(bar_s + 8 * (gs & 1));
+                }
+                __syncwarp();
+            };
+            FOR_EACH_PIECE(p, it, u, end) {
+                const int n = (int)(min(end, it.start + it.tiles) - u);
+                wait(bar_q, items & 1, kErrAttnWeights);
+                ++items;
+                scores(g);
+                for (int j = 0; j < n; ++j, ++g) {
+                    if (j + 1 < n)
+                        scores(g + 1);
+                    const uint32_t s = i % L::kStages;
+                    wait(bar_full + 8 * s, (i / L::kStages) & 1, kErrAttnFull);
+                    ++i;
+                    wait(bar_p + 8 * (g & 1), (g >> 1) & 1, kErrAttnWeights);
+                    if (lane == 0 && ok) {
+                        const uint64_t b = make_sw128_nmajor_desc(sbase + L::kRing + s * L::kTileBytes, kTileKeys * 128);
+#pragma unroll
+                        for (uint32_t k = 0; k < kTileKeys / 16; ++k)    // 16 keys: 2 KiB of V, 8 columns of P
+                            mma_bf16_ts(tmem + kOColumn, tmem + (g & 1) * kSColumns + 8 * k, b + 128 * k, kIdescO,
+                                        j > 0 || k > 0);
+                        ptx::tcgen05_commit(bar_empty + 8 * s);
+                        ptx::tcgen05_commit(bar_o + 8 * (g & 1));
+                    }
+                    __syncwarp();
+                    if (!ok)
+                        break;
+                }
+                if (!ok)
+                    break;
+            }
+            if (lane == 0)
+                ptx::tcgen05_commit(bar_drain);
+            __syncwarp();
+            (void)wait_bounded<false>(bar_drain, 0, kDrainTimeoutNs);    // nothing reads or writes TMEM any more
+        } else {
+            // -------------------------------------------------------- softmax: thread = row = TMEM lane
+            const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+            const int r = threadIdx.x;
+            uint32_t i = 0, g = 0;
+            int64_t u = begin;
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
+                if (ok && !wait_bounded<false>(bar, parity, kDefaultTimeoutNs)) {
+                    ok = false;
+                    atomicOr(p.status, err);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                ptx::tcgen05_fence_after_thread_sync();
+            };
+            FOR_EACH_PIECE(p, it, u, end) {
+                const int from = (int)(u - it.start), to = (int)(min(end, it.start + it.tiles) - it.start), n = to - from;
+                const Row w = row_of(p, it, r);
+                const bool warp_has_rows = __any_sync(0xffffffffu, w.valid);
+                // This row of Q into the swizzled K-major tile (16-byte chunk c of row r at c ^ (r & 7)).
+                {
+                    const __nv_bfloat16 *q = p.q + (w.valid ? w.token * p.q_ts + w.q_head * p.q_hs : 0);
+                    const uint32_t flip = p.q_sign < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+                    for (int c = 0; c < DIM / 8; ++c) {
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (w.valid) {
+                            if (p.q_vec) {
+                                x = *reinterpret_cast<const uint4 *>(q + 8 * c);
+                            } else {
+                                __nv_bfloat16 *e = reinterpret_cast<__nv_bfloat16 *>(&x);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    e[j] = q[8 * c + j];
+                            }
+                            x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+                        }
+                        *reinterpret_cast<uint4 *>(smem + L::kQ + (c >> 3) * (kTileRows * 128) + r * 128 +
+                                                   (((c & 7) ^ (r & 7)) << 4)) = x;
+                    }
+                    ptx::fence_proxy_async_shared();
+                    ptx::tcgen05_fence_before_thread_sync();
+                    ptx::mbar_arrive(bar_q);
+                }
+                // Keys every row of the tile sees: no mask inside [all_lo, all_hi].
+                const Row w0 = row_of(p, it, 0);
+                const int64_t all_hi = w0.hi;
+                const int last_token = min(it.q_len - 1, (it.q_tile * kTileRows + kTileRows - 1) / p.group);
+                const int64_t all_lo = p.window > 0 ? (int64_t)it.kv - it.q_len + last_token - p.window + 1 : 0;
+
+                float m = -CUDART_INF_F, l = 0.f;                       // maximum (raw score) and sum of this row
+                for (int j = 0; j < n; ++j, ++g) {
+                    // the ring stage of this tile's V: K0 first, then K(j+1), V(j) in turns
+                    const uint32_t v_index = i + (j + 1 < n ? 2 * (uint32_t)j + 2 : 2 * (uint32_t)j + 1);
+                    wait(bar_s + 8 * (g & 1), (g >> 1) & 1, kErrAttnScores);
+                    if (!ok)
+                        break;
+                    const int key0 = (it.first_tile + from + j) * kTileKeys;
+                    uint32_t s0[32], s1[32];
+                    const uint32_t s_addr = lane_base + (g & 1) * kSColumns;
+                    if (warp_has_rows) {
+                        tmem_ld_x32(s_addr, s0);
+                        tmem_ld_x32(s_addr + 32, s1);
+                        ptx::tmem_wait_ld();
+                        if (key0 < all_lo || key0 + kTileKeys - 1 > all_hi) {
+                            const int hi = (int)min((int64_t)kTileKeys, w.hi - key0), lo = (int)max((int64_t)0, min((int64_t)kTileKeys, w.lo - key0));
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                if (k > hi || k < lo || !w.valid)
+                                    s0[k] = 0xff800000u;
+                                if (k + 32 > hi || k + 32 < lo || !w.valid)
+                                    s1[k] = 0xff800000u;
+                            }
+                        }
+                        float t0 = __uint_as_float(s0[0]), t1 = __uint_as_float(s1[0]);
+#pragma unroll
+                        for (int k = 1; k < 32; ++k) {
+                            t0 = fmaxf(t0, __uint_as_float(s0[k]));
+                            t1 = fmaxf(t1, __uint_as_float(s1[k]));
+                        }
+                        const float top = fmaxf(m, fmaxf(t0, t1));
+                        if (j == 0) {
+                            m = top;
+                        } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescaleLog2)) {
+                            // O of the tiles so far is complete once PV of the previous tile is.
+                            wait(bar_o + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, kErrAttnOutput);
+                            if (!ok)
+                                break;
+                            const float a = m == top ? 1.f : ex2((m - top) * p.scale_log2);
+                            l *= a;
+                            m = top;
+#pragma unroll
+                            for (int c = 0; c < DIM; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld_x32(lane_base + kOColumn + c, o);
+                                ptx::tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                                tmem_st_x32(lane_base + kOColumn + c, o);
+                            }
+                        }
+                        const float ms = m == -CUDART_INF_F ? 0.f : m * p.scale_log2;
+                        float sum0 = 0.f, sum1 = 0.f;
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float a = ex2(fmaf(__uint_as_float(s0[k]), p.scale_log2, -ms));
+                            const float b = ex2(fmaf(__uint_as_float(s0[k + 1]), p.scale_log2, -ms));
+                            const float c = ex2(fmaf(__uint_as_float(s1[k]), p.scale_log2, -ms));
+                            const float d = ex2(fmaf(__uint_as_float(s1[k + 1]), p.scale_log2, -ms));
+                            sum0 += a + b;
+                            sum1 += c + d;
+                            const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b), cd = __floats2bfloat162_rn(c, d);
+                            pk[k / 2] = *reinterpret_cast<const uint32_t *>(&ab);
+                            pk[16 + k / 2] = *reinterpret_cast<const uint32_t *>(&cd);
+                        }
+                        l += sum0 + sum1;
+                        tmem_st_x32(s_addr, pk);
+                        ptx::tmem_wait_st();
+                    }
+                    if (key0 + kTileKeys > it.kv) {
+                        // What follows the sequence's end in its last page may be anything: a weight of 0
+                        // would not silence NaN, so those keys' V is cleared.
+                        const uint32_t s = v_index % L::kStages;
+                        wait(bar_full + 8 * s, (v_index / L::kStages) & 1, kErrAttnFull);
+                        if (!ok)
+                            break;
+                        const int keep = max(0, it.kv - key0);
+                        uint8_t *tile = smem + L::kRing + s * L::kTileBytes;
+                        for (int c = r; c < (kTileKeys - keep) * 8 * (int)L::kHalves; c += kTileRows) {
+                            const int half = c / ((kTileKeys - keep) * 8), e = c % ((kTileKeys - keep) * 8);
+                            *reinterpret_cast<uint4 *>(tile + half * (kTileKeys * 128) + keep * 128 + e * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        ptx::fence_proxy_async_shared();
+                    }
+                    ptx::tcgen05_fence_before_thread_sync();
+                    ptx::mbar_arrive(bar_p + 8 * (g & 1));
+                }
+                if (!ok)
+                    break;
+                i += 2 * n;
+                wait(bar_o + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, kErrAttnOutput);
+                if (!ok)
+                    break;
+                // The item's rows: finished here, or a part for the join.
+                const bool whole = n == it.tiles;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                if (warp_has_rows) {
+#pragma unroll
+                    for (int c = 0; c < DIM; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld_x32(lane_base + kOColumn + c, o);
+                        ptx::tmem_wait_ld();
+                        if (!w.valid)
+                            continue;
+                        if (whole) {
+                            float v[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
+                            store_row<DIM>(p, w, c, v);
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(p.parts + (slot * p.slot_rows + r) * DIM + c);
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4)
+                                dst[k / 4] = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                                                         __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
+                        }
+                    }
+                    if (w.valid && whole && p.lse)
+                        p.lse[(int64_t)w.token * p.heads + w.q_head] =
+                            l == 0.f ? -CUDART_INF_F : (m * p.scale_log2 + log2f(l)) * CUDART_LN2_F;
+                    if (w.valid && !whole) {
+                        float2 *ml = reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * DIM);
+                        ml[slot * p.slot_rows + r] = make_float2(m * p.scale_log2, l);
+                    }
+                }
+            }
+        }
+    }
+    ptx::tcgen05_fence_before_thread_sync();
+    __syncthreads();
+    if (warp == 5) {
+        ptx::tcgen05_fence_after_thread_sync();
+        ptx::tmem_dealloc(tmem, kColumns);
+    }
+}
+
+// Joins the parts of the items that shares cut: CTA c owns the item that
+// begins in share c and ends in a later one.  A part's weight is
+// 2^(its maximum - the largest maximum); parts add in the order of the keys.
+template <int DIM>
+__global__ void __launch_bounds__(256) join_parts_kernel(const AttnParams p, int ctas)
+{
+    constexpr int E = DIM / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::griddep_launch_dependents();
+    const int64_t line = p.batch > 0 ? line_length(p) : 0;
+    const int64_t share = share_of(line, ctas);
+    const int64_t end = share * (blockIdx.x + 1);
+    const bool cut = end < line;
+    Item it;
+    if (cut)
+        it = locate(p, end - 1);
+    ptx::griddep_wait();
+    if (blockIdx.x == 0) {                   // rows of no sequence
+        const int first = p.batch > 0 ? min(max(p.cu_q[0], 0), p.q_tokens) : p.q_tokens;
+        const int last = p.batch > 0 ? min(max(p.cu_q[p.batch], 0), p.q_tokens) : p.q_tokens;
+        for (int t = warp; t < p.q_tokens; t += 8)
+            if (t < first || t >= last)
+                for (int h = 0; h < p.heads; ++h) {
+                    for (int d = lane; d < DIM; d += 32)
+                        p.out[t * p.o_ts + h * p.o_hs + d] = __float2bfloat16_rn(0.f);
+                    if (lane == 0 && p.lse)
+                        p.lse[(int64_t)t * p.heads + h] = -CUDART_INF_F;
+                }
+    }
+    if (!cut || it.start < end - share || it.start + it.tiles <= end)
+        return;                              // no item is cut here, or it began in an earlier share
+    const int parts = (int)((it.start + it.tiles - 1) / share - blockIdx.x) + 1;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.parts + 2 * (int64_t)ctas * p.slot_rows * DIM);
+    auto slot = [&](int i) { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
+    for (int r = warp; r < kTileRows; r += 8) {
+        const Row w = row_of(p, it, r);
+        if (!w.valid)
+            break;
+        float top = -CUDART_INF_F;
+        for (int i = lane; i < parts; i += 32)
+            top = fmaxf(top, ml[slot(i) * p.slot_rows + r].x);
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float base = top == -CUDART_INF_F ? 0.f : top;
+        float acc[E] = {}, l = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+            const float2 x = ml[slot(i) * p.slot_rows + r];
+            const float a = ex2(x.x - base);
+            l = fmaf(x.y, a, l);
+            const float *src = p.parts + (slot(i) * p.slot_rows + r) * DIM + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] = fmaf(src[e], a, acc[e]);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        __nv_bfloat16 *o = p.out + w.token * p.o_ts + w.q_head * p.o_hs + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[e] * inv);
+        if (p.lse && lane == 0)
+            p.lse[(int64_t)w.token * p.heads + w.q_head] =
+                l == 0.f ? -CUDART_INF_F : (base + log2f(l)) * CUDART_LN2_F;
+    }
 }
 
 bool attention_shape_ok(int batch, int q_tokens, int heads, int kv_heads, int dim)
 {
     return batch >= 0 && q_tokens >= 0 && heads > 0 && kv_heads > 0 && heads % kv_heads == 0 &&
-           heads / kv_heads <= 128 && (dim == 64 || dim == 128);
+           heads / kv_heads <= kTileRows && (dim == 64 || dim == 128) && (int64_t)q_tokens * heads < INT_MAX / 2;
+}
+
+// Rows a part can have: a tile's, or all there are.
+int slot_rows_of(int q_tokens, int heads, int kv_heads)
+{
+    return (int)std::min<int64_t>(kTileRows, std::max<int64_t>(1, (int64_t)q_tokens * (heads / kv_heads)));
+}
+
+// (dim, place, head, page) view of a cache; a box is one head's 64 elements of
+// up to 64 places of a page, zeros outside.
+lowm_status_t encode_cache(const void *base, int64_t page_stride, int64_t place_stride, int64_t head_stride,
+                           int64_t num_pages, int page_size, int kv_heads, int dim, CUtensorMap *map)
+{
+    EncodeTiledFn enc = host_encode_fn();
+    if (!enc)
+        return LOWM_ERR_CUDA;
+    // A dimension of one never uses its stride, but the encoder checks it.
+    const cuuint64_t unit = 16;
+    const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)page_size, (cuuint64_t)kv_heads, (cuuint64_t)num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)place_stride * 2, kv_heads > 1 ? (cuuint64_t)head_stride * 2 : unit,
+                                   num_pages > 1 ? (cuuint64_t)page_stride * 2 : unit};
+    const cuuint32_t box[4] = {64, (cuuint32_t)std::min(page_size, kTileKeys), 1, 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? LOWM_OK
+               : LOWM_ERR_CUDA;
+}
+
+template <int DIM>
+lowm_status_t launch_attention(const CUtensorMap &map_k, const CUtensorMap &map_v, const AttnParams &p, int sms,
+                               void *stream)
+{
+    // The opt-in to more than 48 KiB is per function and device; setting it again costs under a microsecond.
+    if (cudaFuncSetAttribute(paged_attention_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             AttnSmem<DIM>::kBytes) != cudaSuccess)
+        return LOWM_ERR_CUDA;
+    const int ctas = std::min(2 * sms, kMaxAttnCtas);
+    if (p.batch > 0) {
+        const lowm_status_t st = launch_pdl(paged_attention_kernel<DIM>, dim3((unsigned)ctas), dim3(kAttnThreads),
+                                            AttnSmem<DIM>::kBytes, stream, map_k, map_v, p);
+        if (st != LOWM_OK)
+            return st;
+    }
+    return launch_pdl(join_parts_kernel<DIM>, dim3((unsigned)ctas), dim3(256), 0, stream, p, ctas);
 }
 
 }  // namespace
@@ -80,7 +802,10 @@ bool attention_shape_ok(int batch, int q_tokens, int heads, int kv_heads, int di
 
 extern "C" size_t lowm_paged_attention_workspace(int batch, int q_tokens, int heads, int kv_heads, int dim)
 {
-    return lowm::attention_shape_ok(batch, q_tokens, heads, kv_heads, dim) ? 16 : 0;
+    using namespace lowm;
+    if (!attention_shape_ok(batch, q_tokens, heads, kv_heads, dim))
+        return 0;
+    return (size_t)2 * kMaxAttnCtas * slot_rows_of(q_tokens, heads, kv_heads) * (dim + 2) * sizeof(float);
 }
 
 extern "C" lowm_status_t lowm_paged_attention(
@@ -92,7 +817,7 @@ extern "C" lowm_status_t lowm_paged_attention(
     int dim, float scale, int window, void *workspace, size_t workspace_bytes, void *stream)
 {
     using namespace lowm;
-    if (batch < 0 || q_tokens < 0 || heads <= 0 || kv_heads <= 0 || dim <= 0 || num_pages < 0 || page_size <= 0 ||
+    if (batch < 0 || q_tokens < 0 || heads <= 0 || kv_heads <= 0 || dim <= 0 || num_pages <= 0 || num_pages > INT_MAX || page_size <= 0 ||
         table_width < 0 || window < 0 || !(scale == scale))
         return LOWM_ERR_INVALID_ARGUMENT;
     if (!attention_shape_ok(batch, q_tokens, heads, kv_heads, dim) || page_size < 8 || page_size > 1024 ||
@@ -119,40 +844,56 @@ extern "C" lowm_status_t lowm_paged_attention(
         !is_aligned(out, 2) || !is_aligned(page_table, 4) || !is_aligned(kv_lens, 4) || !is_aligned(cu_q, 4) ||
         !is_aligned(lse, 4))
         return LOWM_ERR_MISALIGNED;
-    const lowm_status_t st = host_check_device(nullptr);
+    // The tensor maps take strides below 2^40 bytes, and no stride of 0 where it is used.
+    const int64_t extents[] = {num_pages, page_size, kv_heads, num_pages, page_size, kv_heads};
+    for (int i = 0; i < 6; ++i)
+        if (extents[i] > 1 && (cache_strides[i] == 0 || cache_strides[i] >= ((int64_t)1 << 39)))
+            return LOWM_ERR_INVALID_ARGUMENT;
+    int sms = 0;
+    lowm_status_t st = host_check_device(&sms);
     if (st != LOWM_OK)
         return st;
 
     AttnParams p;
     p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k = static_cast<const __nv_bfloat16 *>(k_cache);
-    p.v = static_cast<const __nv_bfloat16 *>(v_cache);
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
     p.q_ts = q_token_stride;
     p.q_hs = q_head_stride;
     p.o_ts = out_token_stride;
     p.o_hs = out_head_stride;
-    p.k_page = k_page_stride;
-    p.k_place = k_place_stride;
-    p.k_head = k_cache_head_stride;
-    p.v_page = v_page_stride;
-    p.v_place = v_place_stride;
-    p.v_head = v_cache_head_stride;
-    p.num_pages = num_pages;
     p.table_stride = page_table_stride;
     p.table = page_table;
     p.kv_lens = kv_lens;
     p.cu_q = cu_q;
     p.page_size = page_size;
+    p.page_shift = 0;
+    while ((1 << p.page_shift) < page_size)
+        ++p.page_shift;
     p.table_width = table_width;
     p.batch = batch;
     p.q_tokens = q_tokens;
     p.heads = heads;
     p.kv_heads = kv_heads;
+    p.group = heads / kv_heads;
     p.window = window;
-    p.scale = scale;
-    const int64_t units = (int64_t)q_tokens * heads;
-    return launch_pdl(dim == 64 ? attention_kernel<64> : attention_kernel<128>, dim3((unsigned)((units + 3) / 4)),
-                      dim3(128), 0, stream, p);
+    p.slot_rows = slot_rows_of(q_tokens, heads, kv_heads);
+    p.capacity = (int)std::min<int64_t>((int64_t)table_width * page_size, INT_MAX - 2 * kTileKeys);
+    // Never 0, so that a masked score (-inf) stays one.
+    p.scale_log2 = std::max((scale < 0.f ? -scale : scale) * 1.44269504088896340736f, 1e-30f);
+    p.q_sign = scale < 0.f ? -1.f : 1.f;
+    p.q_vec = is_aligned(q, 16) && !((q_token_stride | q_head_stride) & 7);
+    p.out_vec = is_aligned(out, 16) && !((out_token_stride | out_head_stride) & 7);
+    p.parts = static_cast<float *>(workspace);
+    p.status = host_status_word();
+    if (!p.status)
+        return LOWM_ERR_CUDA;
+    CUtensorMap map_k, map_v;
+    if ((st = encode_cache(k_cache, k_page_stride, k_place_stride, k_cache_head_stride, num_pages, page_size, kv_heads,
+                           dim, &map_k)) != LOWM_OK ||
+        (st = encode_cache(v_cache, v_page_stride, v_place_stride, v_cache_head_stride, num_pages, page_size, kv_heads,
+                           dim, &map_v)) != LOWM_OK)
+        return st;
+    return dim == 64 ? launch_attention<64>(map_k, map_v, p, sms, stream)
+                     : launch_attention<128>(map_k, map_v, p, sms, stream);
 }

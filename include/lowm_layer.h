@@ -146,7 +146,7 @@ size_t lowm_paged_attention_workspace(int batch, int q_tokens, int heads, int kv
  *     w_s = scale * p[e_s]  (/ sum_s p[e_s] when renormalize)
  *     out = sum_s w_s * down[e_s] . (silu(gate[e_s] . x) * (up[e_s] . x))
  *
- *   x, out        [tokens, hidden] bf16 by row stride
+ *   x, out        [tokens, hidden] bf16 by row stride (at least hidden)
  *   router        [experts, hidden] bf16
  *   bias          NULL, or fp32 [experts]: enters the choice only
  *   gate_up       [experts, 2 * inner, hidden] bf16, gate rows before up rows

@@ -1,39 +1,75 @@
-// A mixture-of-experts layer for at most 128 tokens (lowm_layer.h): router and
-// top-k, gated up-projection, down-projection with the weighted sum.
+// A mixture-of-experts layer for at most 128 tokens (lowm_layer.h), in two
+// kernels.
+//
+// router_kernel.  A cluster of 8 CTAs owns 8 tokens: each CTA takes an eighth
+// of the experts for all of them (a weight row is read once for 8 tokens), the
+// logits meet in the workspace, and after the cluster barrier each CTA scores
+// one token and picks its top k.
+//
+// experts_kernel.  The layer reads every reached expert's 3 * inner * hidden
+// weights once, at most 128 times as many operations: HBM bandwidth bounds it.
+// It is one persistent CTA per SM, as the GEMM swapped: 64 weight rows are the
+// MMA's M and an expert's tokens (up to 64 at a time) its N.  A TMA warp keeps
+// a ring of weight tiles full across all of the CTA's work items, an MMA warp
+// issues tcgen05.mma into one of two accumulators, four warps empty the other.
+//   up:    an item is 32 inner elements of one expert, the 32 gate rows and 32
+//          up rows interleaved by 8, so that gate and up of an element sit 8
+//          lanes apart in TMEM and meet by a shuffle; silu(gate) * up goes to
+//          the workspace in bf16 (the next MMA's operand type).
+//   down:  an item is 64 hidden elements of one expert; fp32 products per
+//          (token, choice) go to the workspace.
+//   sum:   the choices of a token, weighted, in order.
+// The tokens of an expert are gathered by TMA (tile::gather4) straight from x
+// and from the activations, so nothing is sorted in memory.  Two grid barriers
+// (a cooperative launch) separate the parts; the first ring of down weights is
+// requested before the barrier, which hides it behind the stream.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
 #include <algorithm>
 
 #include "layer_host.h"
-#include "ptx.cuh"
+#include "lowm_kernel.cuh"
 
 namespace lowm {
 namespace {
 
 constexpr int kMaxTokens = 128, kMaxExperts = 1024, kMaxTopK = 16, kMaxWidth = 32768;
+constexpr int kRouterCluster = 8;            // CTAs (and tokens) of a router cluster
+constexpr int kMoeThreads = 192;             // TMA warp 0, MMA warp 1, epilogue warps 2-5
+constexpr int kMoeRows = 64;                 // weight rows of an item = the MMA's M
+constexpr int kMaxColumns = 64;              // tokens of an item; an expert with more gets several items
+constexpr int kMoeBlocks = 4;                // 64-wide K blocks per ring stage
+constexpr uint32_t kWBlockBytes = kMoeRows * 128u;
+
+// Bits of the device status word (above those of paged_attention.cu).
+enum : uint32_t {
+    kErrMoeRing = 1u << 18,
+    kErrMoeFull = 1u << 19,
+    kErrMoeAccumulator = 1u << 20,
+    kErrMoeGrid = 1u << 21,
+};
 
 struct MoeParams {
-    const __nv_bfloat16 *x, *router, *gate_up, *down;
+    const __nv_bfloat16 *x, *router;
     const float *bias;
     __nv_bfloat16 *out;
     int64_t x_stride, out_stride;
     int tokens, hidden, inner, experts, top_k, scoring, renormalize;
     float scale;
-    int *ids;        // [tokens, top_k]
-    float *weights;  // [tokens, top_k]
-    float *act;      // [tokens, top_k, inner]
+    bool out_vec;        // 8-byte stores of out
+    // workspace
+    __nv_bfloat16 *act;  // [tokens * top_k, inner]
+    float *product;      // [tokens * top_k, hidden]
+    float *logits;       // [tokens, experts]
+    float *weights;      // [tokens * top_k]
+    int *ids;            // [tokens * top_k]
+    unsigned *arrived;   // [2] grid barriers, zeroed by the router
+    // experts_kernel
+    int columns, stages; // most tokens of an item (a multiple of 8), ring depth
+    bool up_blocked, down_blocked;   // K a multiple of 64: one copy brings kMoeBlocks blocks
+    unsigned int *status;
 };
-
-__device__ __forceinline__ float warp_dot(const __nv_bfloat16 *a, const __nv_bfloat16 *b, int n)
-{
-    float s = 0.f;
-    for (int i = threadIdx.x & 31; i < n; i += 32)
-        s = fmaf(__bfloat162float(a[i]), __bfloat162float(b[i]), s);
-    for (int o = 16; o > 0; o >>= 1)
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
-}
 
 // Order-preserving image of a float (NaN above +inf): the choice stays total
 // and distinct whatever the scores hold.
@@ -43,21 +79,58 @@ __device__ __forceinline__ unsigned ordered_bits(float f)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(256) router_kernel(const MoeParams p)
+__device__ __forceinline__ void fma8(float &s, const uint4 &a, const uint4 &b)
+{
+    const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a), *y = reinterpret_cast<const __nv_bfloat162 *>(&b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = __bfloat1622float2(x[i]), v = __bfloat1622float2(y[i]);
+        s = fmaf(u.x, v.x, s);
+        s = fmaf(u.y, v.y, s);
+    }
+}
+
+__global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(256) router_kernel(const MoeParams p)
 {
     __shared__ float prob[kMaxExperts];
     __shared__ unsigned key[kMaxExperts];
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = warp; e < p.experts; e += 8) {
-        const float s = warp_dot(p.x + t * p.x_stride, p.router + (int64_t)e * p.hidden, p.hidden);
-        if (lane == 0)
-            prob[e] = s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)ptx::cluster_ctarank(), t0 = blockIdx.x / kRouterCluster * kRouterCluster;
+    const int nt = min(kRouterCluster, p.tokens - t0);
+    if (blockIdx.x == 0 && threadIdx.x < 2)
+        p.arrived[threadIdx.x] = 0u;
+
+    for (int e = rank + kRouterCluster * warp; e < p.experts; e += kRouterCluster * 8) {
+        float s[kRouterCluster] = {};
+        const __nv_bfloat16 *w = p.router + (int64_t)e * p.hidden, *x = p.x + t0 * p.x_stride;
+#pragma unroll 2
+        for (int i = lane * 8; i < p.hidden; i += 256) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(w + i);
+#pragma unroll
+            for (int t = 0; t < kRouterCluster; ++t)
+                if (t < nt)
+                    fma8(s[t], a, *reinterpret_cast<const uint4 *>(x + t * p.x_stride + i));
+        }
+#pragma unroll
+        for (int t = 0; t < kRouterCluster; ++t) {
+            if (t < nt) {
+                for (int o = 16; o > 0; o >>= 1)
+                    s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
+                if (lane == 0)
+                    p.logits[(int64_t)(t0 + t) * p.experts + e] = s[t];
+            }
+        }
     }
-    __syncthreads();
-    if (warp)
+    ptx::cluster_arrive_release();
+    ptx::cluster_wait_acquire();
+    ptx::griddep_launch_dependents();
+    if (warp || rank >= nt)
         return;
+    const int t = t0 + rank;
+    for (int e = lane; e < p.experts; e += 32)
+        prob[e] = p.logits[(int64_t)t * p.experts + e];
+    __syncwarp();
     if (p.scoring == LOWM_MOE_SOFTMAX) {
         float m = -CUDART_INF_F, l = 0.f;
         for (int e = lane; e < p.experts; e += 32)
@@ -102,42 +175,409 @@ __global__ void __launch_bounds__(256) router_kernel(const MoeParams p)
         p.weights[t * p.top_k + lane] = mine * p.scale / (p.renormalize ? sum : 1.f);
 }
 
-__global__ void __launch_bounds__(256) gate_up_kernel(const MoeParams p)
+// ------------------------------------------------------------------ experts_kernel
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int x, int y, int z, int v, int w,
+                                            uint32_t bar, uint64_t policy)
 {
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int pair = blockIdx.x, i = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (i >= p.inner)
-        return;
-    const __nv_bfloat16 *x = p.x + (pair / p.top_k) * p.x_stride;
-    const __nv_bfloat16 *w = p.gate_up + (int64_t)p.ids[pair] * 2 * p.inner * p.hidden;
-    const float g = warp_dot(x, w + (int64_t)i * p.hidden, p.hidden);
-    const float u = warp_dot(x, w + (int64_t)(p.inner + i) * p.hidden, p.hidden);
-    if ((threadIdx.x & 31) == 0)
-        p.act[(int64_t)pair * p.inner + i] = g / (1.f + expf(-g)) * u;
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w), "r"(bar), "l"(policy)
+        : "memory");
 }
 
-__global__ void __launch_bounds__(256) down_kernel(const MoeParams p)
+// Four rows of a matrix, 64 elements from column x on, to 512 bytes of shared memory.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void *tmap, int x, int r0, int r1, int r2, int r3,
+                                            uint32_t bar)
 {
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int t = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (h >= p.hidden)
-        return;
-    float y = 0.f;
-    for (int s = 0; s < p.top_k; ++s) {
-        const int pair = t * p.top_k + s;
-        const __nv_bfloat16 *w = p.down + ((int64_t)p.ids[pair] * p.hidden + h) * p.inner;
-        const float *a = p.act + (int64_t)pair * p.inner;
-        float d = 0.f;
-        for (int i = lane; i < p.inner; i += 32)
-            d = fmaf(__bfloat162float(w[i]), a[i], d);
-        for (int o = 16; o > 0; o >>= 1)
-            d += __shfl_xor_sync(0xffffffffu, d, o);
-        y = fmaf(p.weights[pair], d, y);
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+        : "memory");
+}
+
+// Shared memory: the ring first (1024-byte tiles), then lists and barriers.
+struct MoeSmem {
+    uint32_t w, b, stage_b, mask, first, sorted, group, bars, slot, bytes;
+};
+
+__host__ __device__ inline int moe_max_groups(int experts, int pairs)
+{
+    return (pairs < experts ? pairs : experts) + pairs / kMaxColumns;
+}
+
+__host__ __device__ inline MoeSmem moe_smem(int experts, int pairs, int columns, int stages)
+{
+    MoeSmem L;
+    L.w = 0;                                                   // [stages][blocks][64 rows][64]
+    L.stage_b = kMoeBlocks * columns * 128u;
+    L.b = stages * kMoeBlocks * kWBlockBytes;                  // [stages][blocks][columns][64]
+    L.bars = L.b + stages * L.stage_b;                         // full, empty [stages]; accumulator full, free [2]; drain
+    L.slot = L.bars + (2 * stages + 5) * 8;
+    L.slot = (L.slot + 15) / 16 * 16;
+    L.mask = L.slot + 16;                                      // u32 [experts][4]: the expert's tokens
+    L.group = L.mask + experts * 16;                           // (expert, first place, tokens) as 3 x u16, 8 bytes
+    L.first = L.group + moe_max_groups(experts, pairs) * 8;    // u16 [experts]: the expert's first place
+    L.sorted = L.first + experts * 2;                          // u16 [pairs]: pair at each place
+    L.bytes = L.sorted + pairs * 2 + 1024;                     // slack to align the base
+    return L;
+}
+
+__device__ __forceinline__ unsigned ld_acquire(const unsigned *p)
+{
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void add_release(unsigned *p)
+{
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
+}
+
+__device__ __forceinline__ bool wait_grid(const unsigned *p, unsigned want)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    for (;;) {
+        for (int i = 0; i < 256; ++i)
+            if (ld_acquire(p) >= want)
+                return true;
+        if (ptx::globaltimer() - t0 > kDefaultTimeoutNs)
+            return false;
     }
-    if (lane == 0)
-        p.out[t * p.out_stride + h] = __float2bfloat16_rn(y);
+}
+
+__device__ __forceinline__ void fence_proxy_async_all()
+{
+    asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    experts_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_down,
+                   const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_act,
+                   const MoeParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const int pairs = p.tokens * p.top_k, stages = p.stages;
+    const MoeSmem L = moe_smem(p.experts, pairs, p.columns, stages);
+    const uint32_t bar_full = sbase + L.bars, bar_empty = bar_full + 8 * stages, bar_acc = bar_empty + 8 * stages,
+                   bar_free = bar_acc + 16, bar_drain = bar_free + 16;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L.mask);
+    ushort4 *group = reinterpret_cast<ushort4 *>(smem + L.group);
+    uint16_t *first = reinterpret_cast<uint16_t *>(smem + L.first), *sorted = reinterpret_cast<uint16_t *>(smem + L.sorted);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr uint32_t kColumnsTmem = 2 * kMaxColumns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar_acc + 8 * i, 1);
+            ptx::mbar_init(bar_free + 8 * i, kEpilogueThreads);
+        }
+        ptx::mbar_init(bar_drain, 1);
+        ptx::fence_mbarrier_init_cluster();
+        ptx::fence_proxy_async_shared();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(sbase + L.slot, kColumnsTmem);
+        ptx::tmem_relinquish_alloc_permit();
+        ptx::tcgen05_fence_before_thread_sync();
+    }
+    for (int e = threadIdx.x; e < 4 * p.experts; e += kMoeThreads)
+        mask[e] = 0;
+    ptx::griddep_wait();
+    __syncthreads();
+    ptx::tcgen05_fence_after_thread_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L.slot);
+
+    // The pairs (token, choice) by expert, tokens in order, the same in every
+    // CTA: an expert's tokens as a bit mask, a token's place the bits below its own.
+    for (int i = threadIdx.x; i < pairs; i += kMoeThreads) {
+        const int t = i / p.top_k;
+        atomicOr(&mask[4 * p.ids[i] + (t >> 5)], 1u << (t & 31));
+    }
+    __syncthreads();
+    int *num_groups = reinterpret_cast<int *>(smem + L.slot + 8);
+    if (warp == 0) {
+        int place = 0, groups = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            for (int j = 0; e < p.experts && j < 4; ++j)
+                n += __popc(mask[4 * e + j]);
+            const int g = (n + p.columns - 1) / p.columns;
+            int sn = n, sg = g;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, sn, o), b = __shfl_up_sync(0xffffffffu, sg, o);
+                if (lane >= o) {
+                    sn += a;
+                    sg += b;
+                }
+            }
+            const int at = place + sn - n;
+            if (e < p.experts)
+                first[e] = (uint16_t)at;
+            for (int j = 0; j < g; ++j)
+                group[groups + sg - g + j] = make_ushort4((unsigned short)e, (unsigned short)(at + j * p.columns),
+                                                          (unsigned short)min(p.columns, n - j * p.columns), 0);
+            place += __shfl_sync(0xffffffffu, sn, 31);
+            groups += __shfl_sync(0xffffffffu, sg, 31);
+        }
+        if (lane == 0)
+            *num_groups = groups;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < pairs; i += kMoeThreads) {
+        const int t = i / p.top_k, e = p.ids[i];
+        int place = first[e] + __popc(mask[4 * e + (t >> 5)] & ((1u << (t & 31)) - 1));
+        for (int j = 0; j < (t >> 5); ++j)
+            place += __popc(mask[4 * e + j]);
+        sorted[place] = (uint16_t)i;
+    }
+    __syncthreads();
+
+    const int up_tiles = (p.inner + 31) / 32, down_tiles = (p.hidden + 63) / 64;
+    const int up_items = *num_groups * up_tiles, down_items = *num_groups * down_tiles;
+    const int up_blocks = (p.hidden + 63) / 64, down_blocks = (p.inner + 63) / 64;
+    const int up_stages = (up_blocks + kMoeBlocks - 1) / kMoeBlocks, down_stages = (down_blocks + kMoeBlocks - 1) / kMoeBlocks;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA
+        const uint64_t once = ptx::policy_evict_first();
+        uint32_t i = 0;
+        bool ok = true;
+        // One stage's weights (and the barrier's byte count), then its tokens.
+        auto weights = [&](bool up, int item, int k) {
+            const int s = i % stages;
+            if (ok && !wait_bounded<false>(bar_empty + 8 * s, ((i / stages) & 1) ^ 1, kDefaultTimeoutNs)) {
+                ok = false;
+                atomicOr(p.status, kErrMoeRing);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                return;
+            const int tiles = up ? up_tiles : down_tiles, blocks = up ? up_blocks : down_blocks;
+            const bool blocked = up ? p.up_blocked : p.down_blocked;
+            const ushort4 g = group[item / tiles];
+            const int used = min(kMoeBlocks, blocks - k * kMoeBlocks);
+            if (lane == 0) {
+                const uint32_t w_bytes = (blocked ? kMoeBlocks : used) * kWBlockBytes;
+                ptx::mbar_arrive_expect_tx(bar_full + 8 * s, w_bytes + used * ((g.z + 3) / 4) * 512u);
+                const int row = up ? g.x * (p.inner / 4) + item % tiles * 4 : g.x * p.hidden + item % tiles * 64;
+                for (int j = 0; j < (blocked ? 1 : used); ++j) {
+                    const uint32_t dst = sbase + L.w + (s * kMoeBlocks + j) * kWBlockBytes;
+                    const int kb = k * kMoeBlocks + j;
+                    if (up)      // (k, 8 rows, gate / up, groups of 8 rows, k block)
+                        tma_load_5d(dst, &map_up, blocked ? 0 : 64 * kb, 0, 0, row, blocked ? kb : 0, bar_full + 8 * s, once);
+                    else         // (k, row, k block)
+                        ptx::tma_load_3d(dst, &map_down, blocked ? 0 : 64 * kb, row, blocked ? kb : 0, bar_full + 8 * s, once);
+                }
+            }
+            __syncwarp();
+            ++i;
+        };
+        auto columns = [&](bool up, int item, int k, uint32_t at) {
+            const int s = at % stages;
+            const int tiles = up ? up_tiles : down_tiles, blocks = up ? up_blocks : down_blocks;
+            const ushort4 g = group[item / tiles];
+            const int used = min(kMoeBlocks, blocks - k * kMoeBlocks), quads = (g.z + 3) / 4;
+            for (int c = lane; c < used * quads; c += 32) {
+                const int j = c / quads, q = c % quads;
+                int r[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int pair = sorted[g.y + min(4 * q + e, g.z - 1)];   // the last token again past the end
+                    r[e] = up ? pair / p.top_k : pair;
+                }
+                tma_gather4(sbase + L.b + s * L.stage_b + j * p.columns * 128 + q * 512, up ? &map_x : &map_act,
+                            (k * kMoeBlocks + j) * 64, r[0], r[1], r[2], r[3], bar_full + 8 * s);
+            }
+            __syncwarp();
+        };
+        for (int item = blockIdx.x; item < up_items && ok; item += gridDim.x)
+            for (int k = 0; k < up_stages && ok; ++k) {
+                const uint32_t at = i;
+                weights(true, item, k);
+                if (ok)
+                    columns(true, item, k, at);
+            }
+        // The first ring of down weights before the activations are complete.
+        const uint32_t base = i;
+        int ahead = 0;
+        for (int item = blockIdx.x, n = 0; item < down_items && ok && n < stages; item += gridDim.x)
+            for (int k = 0; k < down_stages && ok && n < stages; ++k, ++n, ++ahead)
+                weights(false, item, k);
+        if (ok && !wait_grid(&p.arrived[0], gridDim.x)) {
+            ok = false;
+            atomicOr(p.status, kErrMoeGrid);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        fence_proxy_async_all();
+        int n = 0;
+        for (int item = blockIdx.x; item < down_items && ok; item += gridDim.x)
+            for (int k = 0; k < down_stages && ok; ++k, ++n) {
+                if (n >= ahead)
+                    weights(false, item, k);
+                if (ok)
+                    columns(false, item, k, base + n);
+            }
+        if (!ok)        // a stage that was counted but never filled would keep its readers waiting: they give up by themselves
+            for (uint32_t j = i > (uint32_t)stages ? i - stages : 0; j < i; ++j)
+                (void)wait_bounded<false>(bar_full + 8 * (j % stages), (j / stages) & 1, kDrainTimeoutNs);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        uint32_t i = 0, n = 0;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
+            if (ok && !wait_bounded<false>(bar, parity, kDefaultTimeoutNs)) {
+                ok = false;
+                if (lane == 0)
+                    atomicOr(p.status, err);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            ptx::tcgen05_fence_after_thread_sync();
+        };
+        auto item_products = [&](const ushort4 g, int blocks, int num_stages) {
+            const uint32_t d = tmem + (n & 1) * kMaxColumns;
+            const uint32_t idesc = make_idesc_bf16(kMoeRows, (g.z + 7) / 8 * 8);
+            wait(bar_free + 8 * (n & 1), ((n >> 1) & 1) ^ 1, kErrMoeAccumulator);
+            for (int k = 0; k < num_stages && ok; ++k, ++i) {
+                const int s = i % stages;
+                wait(bar_full + 8 * s, (i / stages) & 1, kErrMoeFull);
+                if (lane == 0 && ok) {
+                    const int used = min(kMoeBlocks, blocks - k * kMoeBlocks);
+                    for (int j = 0; j < used; ++j) {
+                        const uint64_t a = make_sw128_kmajor_desc(sbase + L.w + (s * kMoeBlocks + j) * kWBlockBytes);
+                        const uint64_t b = make_sw128_kmajor_desc(sbase + L.b + s * L.stage_b + j * p.columns * 128);
+#pragma unroll
+                        for (uint32_t q = 0; q < 4; ++q)
+                            ptx::mma_bf16_ss(d, a + 2 * q, b + 2 * q, idesc, k + j + (int)q > 0);
+                    }
+                    ptx::tcgen05_commit(bar_empty + 8 * s);
+                    if (k == num_stages - 1)
+                        ptx::tcgen05_commit(bar_acc + 8 * (n & 1));
+                }
+                __syncwarp();
+            }
+            ++n;
+        };
+        for (int item = blockIdx.x; item < up_items && ok; item += gridDim.x)
+            item_products(group[item / up_tiles], up_blocks, up_stages);
+        for (int item = blockIdx.x; item < down_items && ok; item += gridDim.x)
+            item_products(group[item / down_tiles], down_blocks, down_stages);
+        if (lane == 0)
+            ptx::tcgen05_commit(bar_drain);
+        __syncwarp();
+        (void)wait_bounded<false>(bar_drain, 0, kDrainTimeoutNs);   // nothing writes TMEM any more
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int quarter = warp & 3, etid = threadIdx.x - 64;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+        uint32_t n = 0;
+        bool ok = true;
+        auto wait_acc = [&]() {
+            if (ok && !wait_bounded<false>(bar_acc + 8 * (n & 1), (n >> 1) & 1, kDefaultTimeoutNs)) {
+                ok = false;
+                atomicOr(p.status, kErrMoeAccumulator);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            ptx::tcgen05_fence_after_thread_sync();
+        };
+        auto release = [&]() {
+            ptx::tcgen05_fence_before_thread_sync();
+            ptx::mbar_arrive(bar_free + 8 * (n & 1));
+            ++n;
+        };
+        for (int item = blockIdx.x; item < up_items; item += gridDim.x) {
+            wait_acc();
+            if (!ok)
+                break;
+            const ushort4 g = group[item / up_tiles];
+            // Lane l of quarter q: gate (l < 8) or up (8 <= l < 16) of element 32 tile + 8 q + l % 8.
+            const int e = item % up_tiles * 32 + quarter * 8 + lane;
+            for (int c = 0; c < g.z; c += 8) {
+                uint32_t v[8];
+                ptx::tmem_ld_32x32b_x8(lanes + (n & 1) * kMaxColumns + c, v);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float gate = __uint_as_float(v[j]), up = __shfl_down_sync(0xffffffffu, gate, 8);
+                    if (lane < 8 && c + j < g.z && e < p.inner)
+                        p.act[(int64_t)sorted[g.y + c + j] * p.inner + e] =
+                            __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
+                }
+            }
+            release();
+        }
+        // Barrier: every CTA's activations are in memory before any is read by TMA.
+        __threadfence();
+        fence_proxy_async_all();
+        ptx::named_barrier_sync(1, kEpilogueThreads);
+        if (etid == 0)
+            add_release(&p.arrived[0]);
+        for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
+            wait_acc();
+            if (!ok)
+                break;
+            const ushort4 g = group[item / down_tiles];
+            const int h = item % down_tiles * 64 + quarter * 16 + lane;
+            for (int c = 0; c < g.z; c += 8) {
+                uint32_t v[8];
+                ptx::tmem_ld_32x32b_x8(lanes + (n & 1) * kMaxColumns + c, v);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (lane < 16 && c + j < g.z && h < p.hidden)
+                        p.product[(int64_t)sorted[g.y + c + j] * p.hidden + h] = __uint_as_float(v[j]);
+            }
+            release();
+        }
+        __threadfence();
+        ptx::named_barrier_sync(1, kEpilogueThreads);
+        if (etid == 0) {
+            add_release(&p.arrived[1]);
+            if (!wait_grid(&p.arrived[1], gridDim.x))
+                atomicOr(p.status, kErrMoeGrid);
+        }
+        ptx::named_barrier_sync(1, kEpilogueThreads);
+        ptx::griddep_launch_dependents();
+        const int quads = p.hidden / 4, total = p.tokens * quads;
+        for (int c = blockIdx.x * kEpilogueThreads + etid; c < total; c += gridDim.x * kEpilogueThreads) {
+            const int t = c / quads, h = c % quads * 4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int s = 0; s < p.top_k; ++s) {
+                const float w = p.weights[t * p.top_k + s];
+                const float4 d = __ldcg(reinterpret_cast<const float4 *>(p.product + (int64_t)(t * p.top_k + s) * p.hidden + h));
+                y.x = fmaf(w, d.x, y.x);
+                y.y = fmaf(w, d.y, y.y);
+                y.z = fmaf(w, d.z, y.z);
+                y.w = fmaf(w, d.w, y.w);
+            }
+            __nv_bfloat16 *o = p.out + t * p.out_stride + h;
+            const __nv_bfloat162 a = __floats2bfloat162_rn(y.x, y.y), b = __floats2bfloat162_rn(y.z, y.w);
+            if (p.out_vec) {
+                uint2 u;
+                u.x = *reinterpret_cast<const uint32_t *>(&a);
+                u.y = *reinterpret_cast<const uint32_t *>(&b);
+                *reinterpret_cast<uint2 *>(o) = u;
+            } else {
+                o[0] = a.x, o[1] = a.y, o[2] = b.x, o[3] = b.y;
+            }
+        }
+    }
+    ptx::tcgen05_fence_before_thread_sync();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tcgen05_fence_after_thread_sync();
+        ptx::tmem_dealloc(tmem, kColumnsTmem);
+    }
 }
 
 bool moe_shape_ok(int tokens, int hidden, int inner, int experts, int top_k)
@@ -147,6 +587,38 @@ bool moe_shape_ok(int tokens, int hidden, int inner, int experts, int top_k)
            top_k <= std::min(kMaxTopK, experts);
 }
 
+size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
+struct MoeWorkspace {
+    size_t act, product, logits, weights, ids, arrived, bytes;
+};
+
+MoeWorkspace moe_workspace(int tokens, int hidden, int inner, int experts, int top_k)
+{
+    const size_t pairs = (size_t)std::max(tokens, 1) * top_k;
+    MoeWorkspace w;
+    w.act = 0;
+    w.product = w.act + round16(pairs * inner * 2);
+    w.logits = w.product + round16(pairs * hidden * 4);
+    w.weights = w.logits + round16((size_t)std::max(tokens, 1) * experts * 4);
+    w.ids = w.weights + round16(pairs * 4);
+    w.arrived = w.ids + round16(pairs * 4);
+    w.bytes = w.arrived + 16;
+    return w;
+}
+
+lowm_status_t encode_bf16(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                          const cuuint32_t *box)
+{
+    EncodeTiledFn enc = host_encode_fn();
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box,
+                      step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? LOWM_OK
+               : LOWM_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace lowm
 
@@ -154,7 +626,7 @@ extern "C" size_t lowm_moe_workspace(int tokens, int hidden, int inner, int expe
 {
     if (!lowm::moe_shape_ok(tokens, hidden, inner, experts, top_k))
         return 0;
-    return (size_t)std::max(tokens, 1) * (size_t)top_k * ((size_t)inner * 4 + 8) + 16;
+    return lowm::moe_workspace(tokens, hidden, inner, experts, top_k).bytes;
 }
 
 extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *router, const float *bias,
@@ -171,21 +643,23 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     if (tokens == 0)
         return LOWM_OK;
     if (!x || !router || !gate_up || !down || !out || !workspace ||
-        workspace_bytes < lowm_moe_workspace(tokens, hidden, inner, experts, top_k) || x_stride < 0 ||
+        workspace_bytes < lowm_moe_workspace(tokens, hidden, inner, experts, top_k) || x_stride < hidden ||
         out_stride < hidden)
         return LOWM_ERR_INVALID_ARGUMENT;
     if (!is_aligned(x, 16) || !is_aligned(router, 16) || !is_aligned(gate_up, 16) || !is_aligned(down, 16) ||
         !is_aligned(workspace, 16) || !is_aligned(bias, 4) || !is_aligned(out, 2) || (x_stride & 7))
         return LOWM_ERR_MISALIGNED;
-    lowm_status_t st = host_check_device(nullptr);
+    int sms = 0;
+    lowm_status_t st = host_check_device(&sms);
     if (st != LOWM_OK)
         return st;
 
+    const int pairs = tokens * top_k;
+    const MoeWorkspace w = moe_workspace(tokens, hidden, inner, experts, top_k);
+    uint8_t *base = static_cast<uint8_t *>(workspace);
     MoeParams p;
     p.x = static_cast<const __nv_bfloat16 *>(x);
     p.router = static_cast<const __nv_bfloat16 *>(router);
-    p.gate_up = static_cast<const __nv_bfloat16 *>(gate_up);
-    p.down = static_cast<const __nv_bfloat16 *>(down);
     p.bias = bias;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.x_stride = x_stride;
@@ -198,14 +672,70 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     p.scoring = scoring;
     p.renormalize = renormalize;
     p.scale = scale;
-    const int pairs = tokens * top_k;
-    p.act = static_cast<float *>(workspace);
-    p.weights = p.act + (size_t)pairs * inner;
-    p.ids = reinterpret_cast<int *>(p.weights + pairs);
-    if ((st = launch_pdl(router_kernel, dim3((unsigned)tokens), dim3(256), 0, stream, p)) != LOWM_OK)
+    p.out_vec = is_aligned(out, 8) && (out_stride & 3) == 0;
+    p.act = reinterpret_cast<__nv_bfloat16 *>(base + w.act);
+    p.product = reinterpret_cast<float *>(base + w.product);
+    p.logits = reinterpret_cast<float *>(base + w.logits);
+    p.weights = reinterpret_cast<float *>(base + w.weights);
+    p.ids = reinterpret_cast<int *>(base + w.ids);
+    p.arrived = reinterpret_cast<unsigned *>(base + w.arrived);
+    p.columns = std::min(kMaxColumns, (tokens + 7) / 8 * 8);
+    constexpr int kMaxSmem = 232448;
+    for (p.stages = 8; p.stages > 2 && (int)moe_smem(experts, pairs, p.columns, p.stages).bytes > kMaxSmem; --p.stages) {
+    }
+    const int smem = (int)moe_smem(experts, pairs, p.columns, p.stages).bytes;
+    if (smem > kMaxSmem)
+        return LOWM_ERR_UNSUPPORTED_SHAPE;
+    p.up_blocked = hidden % 64 == 0;
+    p.down_blocked = inner % 64 == 0;
+    p.status = host_status_word();
+    if (!p.status)
+        return LOWM_ERR_CUDA;
+
+    // gate_up as (k, 8 rows, gate / up, groups of 8 rows, k block): a box is 4 groups of 8 gate and 8 up rows.
+    // An expert is inner / 4 groups further; the extent ends with the last expert's up rows, so every
+    // element of a box lies inside the tensor or reads as zero.
+    CUtensorMap map_up, map_down, map_x, map_act;
+    const cuuint64_t h2 = (cuuint64_t)hidden * 2, i2 = (cuuint64_t)inner * 2;
+    {
+        const cuuint64_t dims[5] = {p.up_blocked ? 64u : (cuuint64_t)hidden, 8, 2,
+                                    (cuuint64_t)experts * (inner / 4) - inner / 8, p.up_blocked ? hidden / 64u : 1u};
+        const cuuint64_t strides[4] = {h2, h2 * inner, h2 * 8, 128};
+        const cuuint32_t box[5] = {64, 8, 2, 4, p.up_blocked ? (cuuint32_t)kMoeBlocks : 1u};
+        if ((st = encode_bf16(&map_up, gate_up, 5, dims, strides, box)) != LOWM_OK)
+            return st;
+    }
+    {
+        const cuuint64_t dims[3] = {p.down_blocked ? 64u : (cuuint64_t)inner, (cuuint64_t)experts * hidden,
+                                    p.down_blocked ? inner / 64u : 1u};
+        const cuuint64_t strides[2] = {i2, 128};
+        const cuuint32_t box[3] = {64, (cuuint32_t)kMoeRows, p.down_blocked ? (cuuint32_t)kMoeBlocks : 1u};
+        if ((st = encode_bf16(&map_down, down, 3, dims, strides, box)) != LOWM_OK)
+            return st;
+    }
+    const cuuint32_t row_box[2] = {64, 1};
+    const cuuint64_t x_dims[2] = {(cuuint64_t)hidden, (cuuint64_t)tokens}, x_strides[1] = {(cuuint64_t)x_stride * 2};
+    const cuuint64_t a_dims[2] = {(cuuint64_t)inner, (cuuint64_t)pairs}, a_strides[1] = {i2};
+    if ((st = encode_bf16(&map_x, x, 2, x_dims, x_strides, row_box)) != LOWM_OK ||
+        (st = encode_bf16(&map_act, p.act, 2, a_dims, a_strides, row_box)) != LOWM_OK)
         return st;
-    if ((st = launch_pdl(gate_up_kernel, dim3((unsigned)pairs, (unsigned)((inner + 7) / 8)), dim3(256), 0, stream,
-                         p)) != LOWM_OK)
+
+    const int clusters = (tokens + kRouterCluster - 1) / kRouterCluster;
+    if ((st = launch_pdl(router_kernel, dim3((unsigned)(clusters * kRouterCluster)), dim3(256), 0, stream, p)) != LOWM_OK)
         return st;
-    return launch_pdl(down_kernel, dim3((unsigned)tokens, (unsigned)((hidden + 7) / 8)), dim3(256), 0, stream, p);
+    if (cudaFuncSetAttribute(experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
+        return LOWM_ERR_CUDA;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)sms);
+    cfg.blockDim = dim3(kMoeThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeCooperative;      // its CTAs wait for one another
+    attr.val.cooperative = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, experts_kernel, map_up, map_down, map_x, map_act, p) == cudaSuccess ? LOWM_OK
+                                                                                                        : LOWM_ERR_CUDA;
 }

@@ -319,7 +319,7 @@ def moe(x, router_weight, gate_up, down, top_k: int, *, scoring: str = "softmax"
     nbytes = lowm_moe_workspace(tokens, hidden, inner, experts, top_k)
     work = torch.empty(nbytes, dtype=torch.uint8, device=device)
     s = function("lowm_moe")(
-        _ptr(x), x.stride(0), _ptr(router_weight), _ptr(bias), _ptr(gate_up), _ptr(down), _ptr(out),
+        _ptr(x), x.stride(0) if tokens > 1 else hidden, _ptr(router_weight), _ptr(bias), _ptr(gate_up), _ptr(down), _ptr(out),
         out.stride(0) if tokens > 1 else hidden, tokens, hidden, inner, experts, top_k, _SCORING[scoring],
         renormalize, scale, _ptr(work), nbytes, _stream(None))
     if s != LOWM_OK:

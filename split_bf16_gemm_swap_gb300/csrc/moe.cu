@@ -1,28 +1,29 @@
 // A mixture-of-experts layer for at most 128 tokens (lowm_layer.h), in two
 // kernels.
 //
-// router_kernel.  A cluster of 8 CTAs owns 8 tokens: each CTA takes an eighth
-// of the experts for all of them (a weight row is read once for 8 tokens), the
-// logits meet in the workspace, and after the cluster barrier each CTA scores
-// one token and picks its top k.
+// router_kernel.  A cluster of 8 CTAs owns 8 tokens, the N of an
+// mma.m16n8k16: each CTA takes every 8th tile of 16 experts, its 8 warps the
+// 32-wide K steps in turns (all loads of a warp in flight at once: the kernel
+// is one memory latency long), the logits meet in the workspace, and after the
+// cluster barrier each CTA scores one token and picks its top k.
 //
 // experts_kernel.  The layer reads every reached expert's 3 * inner * hidden
 // weights once, at most 128 times as many operations: HBM bandwidth bounds it.
 // It is one persistent CTA per SM, as the GEMM swapped: 64 weight rows are the
 // MMA's M and an expert's tokens (up to 64 at a time) its N.  A TMA warp keeps
-// a ring of weight tiles full across all of the CTA's work items, an MMA warp
-// issues tcgen05.mma into one of two accumulators, four warps empty the other.
+// a ring of weight tiles full across all of the CTA's work items, a loader warp
+// gathers the tokens' rows beside them (cp.async), two MMA warps issue the even
+// and the odd K16 steps (one thread issues an MMA only every ~55 cycles), and
+// four warps empty one pair of accumulators while the other fills.
 //   up:    an item is 32 inner elements of one expert, the 32 gate rows and 32
 //          up rows interleaved by 8, so that gate and up of an element sit 8
 //          lanes apart in TMEM and meet by a shuffle; silu(gate) * up goes to
-//          the workspace in bf16 (the next MMA's operand type).
+//          the workspace in bf16 (the next MMA's operand type), by expert.
 //   down:  an item is 64 hidden elements of one expert; fp32 products per
 //          (token, choice) go to the workspace.
 //   sum:   the choices of a token, weighted, in order.
-// The tokens of an expert are gathered by TMA (tile::gather4) straight from x
-// and from the activations, so nothing is sorted in memory.  Two grid barriers
-// (a cooperative launch) separate the parts; the first ring of down weights is
-// requested before the barrier, which hides it behind the stream.
+// Two grid barriers (a cooperative launch) separate the parts.  The weight
+// stream does not stop at the first: only the loader waits for the activations.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -36,10 +37,11 @@ namespace {
 
 constexpr int kMaxTokens = 128, kMaxExperts = 1024, kMaxTopK = 16, kMaxWidth = 32768;
 constexpr int kRouterCluster = 8;            // CTAs (and tokens) of a router cluster
-constexpr int kMoeThreads = 192;             // TMA warp 0, MMA warp 1, epilogue warps 2-5
+constexpr int kMoeThreads = 256;             // TMA warp 0, MMA warps 1 and 6, epilogue warps 2-5, loader warp 7
 constexpr int kMoeRows = 64;                 // weight rows of an item = the MMA's M
 constexpr int kMaxColumns = 64;              // tokens of an item; an expert with more gets several items
 constexpr int kMoeBlocks = 4;                // 64-wide K blocks per ring stage
+constexpr int kLoaderLag = 1;                // stages whose rows the loader has in flight behind the newest
 constexpr uint32_t kWBlockBytes = kMoeRows * 128u;
 
 // Bits of the device status word (above those of paged_attention.cu).
@@ -59,7 +61,7 @@ struct MoeParams {
     float scale;
     bool out_vec;        // 8-byte stores of out
     // workspace
-    __nv_bfloat16 *act;  // [tokens * top_k, inner]
+    __nv_bfloat16 *act;  // [tokens * top_k, inner], by expert
     float *product;      // [tokens * top_k, hidden]
     float *logits;       // [tokens, experts]
     float *weights;      // [tokens * top_k]
@@ -79,21 +81,23 @@ __device__ __forceinline__ unsigned ordered_bits(float f)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ void fma8(float &s, const uint4 &a, const uint4 &b)
+// D[16 experts][8 tokens] += A[16][16] . B[16][8], bf16 operands, fp32 sums.
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1)
 {
-    const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a), *y = reinterpret_cast<const __nv_bfloat162 *>(&b);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = __bfloat1622float2(x[i]), v = __bfloat1622float2(y[i]);
-        s = fmaf(u.x, v.x, s);
-        s = fmaf(u.y, v.y, s);
-    }
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(256) router_kernel(const MoeParams p)
+constexpr int kRouterWarps = 8;
+
+__global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kRouterWarps) router_kernel(const MoeParams p)
 {
     __shared__ float prob[kMaxExperts];
     __shared__ unsigned key[kMaxExperts];
+    __shared__ float part[kRouterWarps][16][8];
     ptx::griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)ptx::cluster_ctarank(), t0 = blockIdx.x / kRouterCluster * kRouterCluster;
@@ -101,32 +105,48 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(256) ro
     if (blockIdx.x == 0 && threadIdx.x < 2)
         p.arrived[threadIdx.x] = 0u;
 
-    for (int e = rank + kRouterCluster * warp; e < p.experts; e += kRouterCluster * 8) {
-        float s[kRouterCluster] = {};
-        const __nv_bfloat16 *w = p.router + (int64_t)e * p.hidden, *x = p.x + t0 * p.x_stride;
-#pragma unroll 2
-        for (int i = lane * 8; i < p.hidden; i += 256) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(w + i);
-#pragma unroll
-            for (int t = 0; t < kRouterCluster; ++t)
-                if (t < nt)
-                    fma8(s[t], a, *reinterpret_cast<const uint4 *>(x + t * p.x_stride + i));
-        }
-#pragma unroll
-        for (int t = 0; t < kRouterCluster; ++t) {
-            if (t < nt) {
-                for (int o = 16; o > 0; o >>= 1)
-                    s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
-                if (lane == 0)
-                    p.logits[(int64_t)(t0 + t) * p.experts + e] = s[t];
+    // A thread's 8 consecutive k of a 32-wide step serve both K16 products:
+    // the same permutation of k on both operands leaves the sum alone.
+    const int row = lane >> 2, k0 = warp * 32 + (lane & 3) * 8;
+    const __nv_bfloat16 *x = p.x + (t0 + min(row, nt - 1)) * p.x_stride;
+    for (int tile = rank; tile * 16 < p.experts; tile += kRouterCluster) {
+        const int e0 = tile * 16 + row, e1 = e0 + 8;
+        const __nv_bfloat16 *w0 = p.router + (int64_t)min(e0, p.experts - 1) * p.hidden;
+        const __nv_bfloat16 *w1 = p.router + (int64_t)min(e1, p.experts - 1) * p.hidden;
+        float d[4] = {};
+#pragma unroll 8
+        for (int k = k0; k - (lane & 3) * 8 < p.hidden; k += 32 * kRouterWarps) {
+            uint4 a = make_uint4(0, 0, 0, 0), b = a, c = a;
+            if (k < p.hidden) {
+                a = *reinterpret_cast<const uint4 *>(w0 + k);
+                b = *reinterpret_cast<const uint4 *>(w1 + k);
+                c = *reinterpret_cast<const uint4 *>(x + k);
             }
+            mma_16x8x16(d, a.x, b.x, a.y, b.y, c.x, c.y);
+            mma_16x8x16(d, a.z, b.z, a.w, b.w, c.z, c.w);
         }
+        const int col = (lane & 3) * 2;
+        part[warp][row][col] = d[0];
+        part[warp][row][col + 1] = d[1];
+        part[warp][row + 8][col] = d[2];
+        part[warp][row + 8][col + 1] = d[3];
+        __syncthreads();
+        if (threadIdx.x < 128) {
+            const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kRouterWarps; ++w)
+                s += part[w][r][t];
+            if (t < nt && tile * 16 + r < p.experts)
+                p.logits[(int64_t)(t0 + t) * p.experts + tile * 16 + r] = s;
+        }
+        __syncthreads();
     }
     ptx::cluster_arrive_release();
     ptx::cluster_wait_acquire();
     ptx::griddep_launch_dependents();
     if (warp || rank >= nt)
-        return;
+        return;                              // the next kernel starts when all of this one has ended
     const int t = t0 + rank;
     for (int e = lane; e < p.experts; e += 32)
         prob[e] = p.logits[(int64_t)t * p.experts + e];
@@ -154,12 +174,14 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(256) ro
     __syncwarp();
     float sum = 0.f, mine = 0.f;
     for (int s = 0; s < p.top_k; ++s) {
-        unsigned long long best = 0;
-        for (int e = lane; e < p.experts; e += 32)
-            best = max(best, ((unsigned long long)key[e] << 32) | (unsigned)(kMaxExperts - e));
-        for (int o = 16; o > 0; o >>= 1)
-            best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-        const int e = kMaxExperts - (int)(best & 0xffffffffu);
+        unsigned best = 0, at = kMaxExperts;
+        for (int i = lane; i < p.experts; i += 32)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const unsigned top = __reduce_max_sync(0xffffffffu, best);
+        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? at : (unsigned)kMaxExperts);
         const float w = prob[e];
         sum += w;
         if (lane == s)
@@ -186,25 +208,31 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
-// Four rows of a matrix, 64 elements from column x on, to 512 bytes of shared memory.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void *tmap, int x, int r0, int r1, int r2, int r3,
-                                            uint32_t bar)
+// 16 bytes to shared memory past L1; zeros when `bytes` is 0.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, int bytes)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-        : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Shared memory: the ring first (1024-byte tiles), then lists and barriers.
 struct MoeSmem {
-    uint32_t w, b, stage_b, mask, first, sorted, group, bars, slot, bytes;
+    uint32_t w, b, stage_b, mask, first, sorted, group, source, bars, slot, bytes;
 };
 
-__host__ __device__ inline int moe_max_groups(int experts, int pairs)
+__host__ __device__ inline int moe_max_groups(int experts, int pairs, int columns)
 {
-    return (pairs < experts ? pairs : experts) + pairs / kMaxColumns;
+    return (pairs < experts ? pairs : experts) + pairs / columns;
 }
 
 __host__ __device__ inline MoeSmem moe_smem(int experts, int pairs, int columns, int stages)
@@ -216,9 +244,10 @@ __host__ __device__ inline MoeSmem moe_smem(int experts, int pairs, int columns,
     L.bars = L.b + stages * L.stage_b;                         // full, empty [stages]; accumulator full, free [2]; drain
     L.slot = L.bars + (2 * stages + 5) * 8;
     L.slot = (L.slot + 15) / 16 * 16;
-    L.mask = L.slot + 16;                                      // u32 [experts][4]: the expert's tokens
+    L.source = L.slot + 16;                                    // the loader's rows: a pointer each
+    L.mask = L.source + kMaxColumns * 8;                                  // u32 [experts][4]: the expert's tokens
     L.group = L.mask + experts * 16;                           // (expert, first place, tokens) as 3 x u16, 8 bytes
-    L.first = L.group + moe_max_groups(experts, pairs) * 8;    // u16 [experts]: the expert's first place
+    L.first = L.group + moe_max_groups(experts, pairs, columns) * 8;    // u16 [experts]: the expert's first place
     L.sorted = L.first + experts * 2;                          // u16 [pairs]: pair at each place
     L.bytes = L.sorted + pairs * 2 + 1024;                     // slack to align the base
     return L;
@@ -248,14 +277,8 @@ __device__ __forceinline__ bool wait_grid(const unsigned *p, unsigned want)
     }
 }
 
-__device__ __forceinline__ void fence_proxy_async_all()
-{
-    asm volatile("fence.proxy.async;" ::: "memory");
-}
-
 __global__ void __launch_bounds__(kMoeThreads, 1)
     experts_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_down,
-                   const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_act,
                    const MoeParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -269,18 +292,18 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     ushort4 *group = reinterpret_cast<ushort4 *>(smem + L.group);
     uint16_t *first = reinterpret_cast<uint16_t *>(smem + L.first), *sorted = reinterpret_cast<uint16_t *>(smem + L.sorted);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr uint32_t kColumnsTmem = 2 * kMaxColumns;
+    constexpr uint32_t kColumnsTmem = 4 * kMaxColumns;        // two accumulators (one an issuer), twice
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 1);
-            ptx::mbar_init(bar_empty + 8 * s, 1);
+            ptx::mbar_init(bar_full + 8 * s, 2);      // weights, token rows
+            ptx::mbar_init(bar_empty + 8 * s, 2);     // both MMA issuers
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(bar_acc + 8 * i, 1);
+            ptx::mbar_init(bar_acc + 8 * i, 2);
             ptx::mbar_init(bar_free + 8 * i, kEpilogueThreads);
         }
-        ptx::mbar_init(bar_drain, 1);
+        ptx::mbar_init(bar_drain, 2);
         ptx::fence_mbarrier_init_cluster();
         ptx::fence_proxy_async_shared();
     }
@@ -352,86 +375,119 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         const uint64_t once = ptx::policy_evict_first();
         uint32_t i = 0;
         bool ok = true;
-        // One stage's weights (and the barrier's byte count), then its tokens.
         auto weights = [&](bool up, int item, int k) {
             const int s = i % stages;
-            if (ok && !wait_bounded<false>(bar_empty + 8 * s, ((i / stages) & 1) ^ 1, kDefaultTimeoutNs)) {
+            if (!wait_bounded<false>(bar_empty + 8 * s, ((i / stages) & 1) ^ 1, kDefaultTimeoutNs)) {
+                ok = false;
+                atomicOr(p.status, kErrMoeRing);
+                return;
+            }
+            const int tiles = up ? up_tiles : down_tiles, blocks = up ? up_blocks : down_blocks;
+            const bool blocked = up ? p.up_blocked : p.down_blocked;
+            const int e = group[item / tiles].x;
+            const int used = blocked ? 1 : min(kMoeBlocks, blocks - k * kMoeBlocks);
+            ptx::mbar_arrive_expect_tx(bar_full + 8 * s, (blocked ? kMoeBlocks : used) * kWBlockBytes);
+            const int row = up ? e * (p.inner / 4) + item % tiles * 4 : e * p.hidden + item % tiles * kMoeRows;
+            for (int j = 0; j < used; ++j) {
+                const uint32_t dst = sbase + L.w + (s * kMoeBlocks + j) * kWBlockBytes;
+                const int kb = k * kMoeBlocks + j;
+                if (up)      // (k, 8 rows, gate / up, groups of 8 rows, k block)
+                    tma_load_5d(dst, &map_up, blocked ? 0 : 64 * kb, 0, 0, row, blocked ? kb : 0, bar_full + 8 * s, once);
+                else         // (k, row, k block)
+                    ptx::tma_load_3d(dst, &map_down, blocked ? 0 : 64 * kb, row, blocked ? kb : 0, bar_full + 8 * s, once);
+            }
+            ++i;
+        };
+        if (lane == 0) {
+            ptx::prefetch_tensormap(&map_down);
+            for (int item = blockIdx.x; item < up_items && ok; item += gridDim.x)
+                for (int k = 0; k < up_stages && ok; ++k)
+                    weights(true, item, k);
+            for (int item = blockIdx.x; item < down_items && ok; item += gridDim.x)
+                for (int k = 0; k < down_stages && ok; ++k)
+                    weights(false, item, k);
+            if (!ok)        // no copy may land after the CTA has ended (normally the MMAs have consumed all)
+                for (uint32_t j = i > (uint32_t)stages ? i - stages : 0; j < i; ++j)
+                    (void)wait_bounded<false>(bar_full + 8 * (j % stages), (j / stages) & 1, kDrainTimeoutNs);
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // ------------------------------------------------------------ token rows
+        // Eight lanes copy the 128 bytes a row has in a block, each its 16-byte
+        // chunk to the chunk's swizzled place.  The rows' addresses are looked
+        // up once an item (looked up and divided out at every stage they cost
+        // more than the stream: 128 tokens over 32 experts took 367 us).  The
+        // copies of a stage are seen complete kLoaderLag stages later and then
+        // handed to the tensor core (async proxy).
+        uint32_t i = 0, handed = 0;
+        bool ok = true;
+        const int sub = lane >> 3, chunk = lane & 7;
+        const __nv_bfloat16 **source = reinterpret_cast<const __nv_bfloat16 **>(smem + L.source);
+        auto sources = [&](bool up, const ushort4 g) {
+            __syncwarp();
+            for (int r = lane; r < g.z; r += 32)
+                source[r] = up ? p.x + (sorted[g.y + r] / p.top_k) * p.x_stride : p.act + (int64_t)(g.y + r) * p.inner;
+            __syncwarp();
+        };
+        auto hand = [&](uint32_t upto) {
+            for (; handed < upto; ++handed) {
+                if (handed + kLoaderLag < i)
+                    cp_async_wait<kLoaderLag>();
+                else
+                    cp_async_wait<0>();
+                ptx::fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(bar_full + 8 * (handed % stages));
+            }
+        };
+        auto rows = [&](bool up, const ushort4 g, int k) {
+            const int s = i % stages;
+            if (!wait_bounded<false>(bar_empty + 8 * s, ((i / stages) & 1) ^ 1, kDefaultTimeoutNs)) {
                 ok = false;
                 atomicOr(p.status, kErrMoeRing);
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 return;
-            const int tiles = up ? up_tiles : down_tiles, blocks = up ? up_blocks : down_blocks;
-            const bool blocked = up ? p.up_blocked : p.down_blocked;
-            const ushort4 g = group[item / tiles];
-            const int used = min(kMoeBlocks, blocks - k * kMoeBlocks);
-            if (lane == 0) {
-                const uint32_t w_bytes = (blocked ? kMoeBlocks : used) * kWBlockBytes;
-                ptx::mbar_arrive_expect_tx(bar_full + 8 * s, w_bytes + used * ((g.z + 3) / 4) * 512u);
-                const int row = up ? g.x * (p.inner / 4) + item % tiles * 4 : g.x * p.hidden + item % tiles * 64;
-                for (int j = 0; j < (blocked ? 1 : used); ++j) {
-                    const uint32_t dst = sbase + L.w + (s * kMoeBlocks + j) * kWBlockBytes;
-                    const int kb = k * kMoeBlocks + j;
-                    if (up)      // (k, 8 rows, gate / up, groups of 8 rows, k block)
-                        tma_load_5d(dst, &map_up, blocked ? 0 : 64 * kb, 0, 0, row, blocked ? kb : 0, bar_full + 8 * s, once);
-                    else         // (k, row, k block)
-                        ptx::tma_load_3d(dst, &map_down, blocked ? 0 : 64 * kb, row, blocked ? kb : 0, bar_full + 8 * s, once);
-                }
-            }
-            __syncwarp();
-            ++i;
-        };
-        auto columns = [&](bool up, int item, int k, uint32_t at) {
-            const int s = at % stages;
-            const int tiles = up ? up_tiles : down_tiles, blocks = up ? up_blocks : down_blocks;
-            const ushort4 g = group[item / tiles];
-            const int used = min(kMoeBlocks, blocks - k * kMoeBlocks), quads = (g.z + 3) / 4;
-            for (int c = lane; c < used * quads; c += 32) {
-                const int j = c / quads, q = c % quads;
-                int r[4];
+            const int width = up ? p.hidden : p.inner, at = k * (kMoeBlocks * 64) + chunk * 8;
+            for (int r = sub; r < g.z; r += 4) {
+                const __nv_bfloat16 *src = source[r];
+                const uint32_t dst = sbase + L.b + s * L.stage_b + r * 128 + ((chunk ^ (r & 7)) << 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int pair = sorted[g.y + min(4 * q + e, g.z - 1)];   // the last token again past the end
-                    r[e] = up ? pair / p.top_k : pair;
+                for (int j = 0; j < kMoeBlocks; ++j) {
+                    const bool in = at + 64 * j < width;
+                    cp_async_16(dst + j * p.columns * 128, src + (in ? at + 64 * j : 0), in ? 16 : 0);
                 }
-                tma_gather4(sbase + L.b + s * L.stage_b + j * p.columns * 128 + q * 512, up ? &map_x : &map_act,
-                            (k * kMoeBlocks + j) * 64, r[0], r[1], r[2], r[3], bar_full + 8 * s);
             }
             __syncwarp();
+            cp_async_commit();
+            ++i;
+            if (i > kLoaderLag)
+                hand(i - kLoaderLag);
         };
-        for (int item = blockIdx.x; item < up_items && ok; item += gridDim.x)
-            for (int k = 0; k < up_stages && ok; ++k) {
-                const uint32_t at = i;
-                weights(true, item, k);
-                if (ok)
-                    columns(true, item, k, at);
-            }
-        // The first ring of down weights before the activations are complete.
-        const uint32_t base = i;
-        int ahead = 0;
-        for (int item = blockIdx.x, n = 0; item < down_items && ok && n < stages; item += gridDim.x)
-            for (int k = 0; k < down_stages && ok && n < stages; ++k, ++n, ++ahead)
-                weights(false, item, k);
+        for (int item = blockIdx.x; item < up_items && ok; item += gridDim.x) {
+            const ushort4 g = group[item / up_tiles];
+            sources(true, g);
+            for (int k = 0; k < up_stages && ok; ++k)
+                rows(true, g, k);
+        }
+        hand(i);
         if (ok && !wait_grid(&p.arrived[0], gridDim.x)) {
             ok = false;
             atomicOr(p.status, kErrMoeGrid);
         }
         ok = __all_sync(0xffffffffu, ok);
-        fence_proxy_async_all();
-        int n = 0;
-        for (int item = blockIdx.x; item < down_items && ok; item += gridDim.x)
-            for (int k = 0; k < down_stages && ok; ++k, ++n) {
-                if (n >= ahead)
-                    weights(false, item, k);
-                if (ok)
-                    columns(false, item, k, base + n);
-            }
-        if (!ok)        // a stage that was counted but never filled would keep its readers waiting: they give up by themselves
-            for (uint32_t j = i > (uint32_t)stages ? i - stages : 0; j < i; ++j)
-                (void)wait_bounded<false>(bar_full + 8 * (j % stages), (j / stages) & 1, kDrainTimeoutNs);
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA
+        for (int item = blockIdx.x; item < down_items && ok; item += gridDim.x) {
+            const ushort4 g = group[item / down_tiles];
+            sources(false, g);
+            for (int k = 0; k < down_stages && ok; ++k)
+                rows(false, g, k);
+        }
+        hand(i);
+    } else if (warp == 1 || warp == 6) {
+        // ------------------------------------------------------------ MMA: even or odd K16 steps
+        const uint32_t odd = warp == 6;
         uint32_t i = 0, n = 0;
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
@@ -444,7 +500,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             ptx::tcgen05_fence_after_thread_sync();
         };
         auto item_products = [&](const ushort4 g, int blocks, int num_stages) {
-            const uint32_t d = tmem + (n & 1) * kMaxColumns;
+            const uint32_t d = tmem + ((n & 1) * 2 + odd) * kMaxColumns;
             const uint32_t idesc = make_idesc_bf16(kMoeRows, (g.z + 7) / 8 * 8);
             wait(bar_free + 8 * (n & 1), ((n >> 1) & 1) ^ 1, kErrMoeAccumulator);
             for (int k = 0; k < num_stages && ok; ++k, ++i) {
@@ -456,8 +512,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                         const uint64_t a = make_sw128_kmajor_desc(sbase + L.w + (s * kMoeBlocks + j) * kWBlockBytes);
                         const uint64_t b = make_sw128_kmajor_desc(sbase + L.b + s * L.stage_b + j * p.columns * 128);
 #pragma unroll
-                        for (uint32_t q = 0; q < 4; ++q)
-                            ptx::mma_bf16_ss(d, a + 2 * q, b + 2 * q, idesc, k + j + (int)q > 0);
+                        for (uint32_t q = 0; q < 2; ++q)
+                            ptx::mma_bf16_ss(d, a + 2 * (2 * q + odd), b + 2 * (2 * q + odd), idesc, k + j + (int)q > 0);
                     }
                     ptx::tcgen05_commit(bar_empty + 8 * s);
                     if (k == num_stages - 1)
@@ -502,22 +558,20 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             // Lane l of quarter q: gate (l < 8) or up (8 <= l < 16) of element 32 tile + 8 q + l % 8.
             const int e = item % up_tiles * 32 + quarter * 8 + lane;
             for (int c = 0; c < g.z; c += 8) {
-                uint32_t v[8];
-                ptx::tmem_ld_32x32b_x8(lanes + (n & 1) * kMaxColumns + c, v);
-                ptx::tmem_wait_ld();
+                float v[8], u[8];
+                load_accumulator_pair<8>(lanes + (n & 1) * 2 * kMaxColumns + c, lanes + ((n & 1) * 2 + 1) * kMaxColumns + c, v, u);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float gate = __uint_as_float(v[j]), up = __shfl_down_sync(0xffffffffu, gate, 8);
+                    const float gate = v[j] + u[j], up = __shfl_down_sync(0xffffffffu, gate, 8);
                     if (lane < 8 && c + j < g.z && e < p.inner)
-                        p.act[(int64_t)sorted[g.y + c + j] * p.inner + e] =
+                        p.act[(int64_t)(g.y + c + j) * p.inner + e] =
                             __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
                 }
             }
             release();
         }
-        // Barrier: every CTA's activations are in memory before any is read by TMA.
+        // Barrier: every CTA's activations are in memory before any is read.
         __threadfence();
-        fence_proxy_async_all();
         ptx::named_barrier_sync(1, kEpilogueThreads);
         if (etid == 0)
             add_release(&p.arrived[0]);
@@ -528,13 +582,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             const ushort4 g = group[item / down_tiles];
             const int h = item % down_tiles * 64 + quarter * 16 + lane;
             for (int c = 0; c < g.z; c += 8) {
-                uint32_t v[8];
-                ptx::tmem_ld_32x32b_x8(lanes + (n & 1) * kMaxColumns + c, v);
-                ptx::tmem_wait_ld();
+                float v[8], u[8];
+                load_accumulator_pair<8>(lanes + (n & 1) * 2 * kMaxColumns + c, lanes + ((n & 1) * 2 + 1) * kMaxColumns + c, v, u);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (lane < 16 && c + j < g.z && h < p.hidden)
-                        p.product[(int64_t)sorted[g.y + c + j] * p.hidden + h] = __uint_as_float(v[j]);
+                        p.product[(int64_t)sorted[g.y + c + j] * p.hidden + h] = v[j] + u[j];
             }
             release();
         }
@@ -585,6 +638,17 @@ bool moe_shape_ok(int tokens, int hidden, int inner, int experts, int top_k)
     return tokens >= 0 && tokens <= kMaxTokens && hidden > 0 && hidden <= kMaxWidth && hidden % 8 == 0 && inner > 0 &&
            inner <= kMaxWidth && inner % 8 == 0 && experts > 0 && experts <= kMaxExperts && top_k > 0 &&
            top_k <= std::min(kMaxTopK, experts);
+}
+
+// Tokens of an item.  The ring holds that many rows beside the 64 weight rows
+// of every block, so room for 64 leaves half of the weights in flight that room
+// for 16 does; an expert with more tokens reads its weights again (from L2:
+// its items run side by side).  Twice the average and 8 more covers nearly all
+// experts of a balanced router.
+int moe_columns(int tokens, int experts, int top_k)
+{
+    const int usual = 2 * ((tokens * top_k + experts - 1) / experts) + 8;
+    return std::min({kMaxColumns, (tokens + 7) / 8 * 8, (usual + 7) / 8 * 8});
 }
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
@@ -679,7 +743,7 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     p.weights = reinterpret_cast<float *>(base + w.weights);
     p.ids = reinterpret_cast<int *>(base + w.ids);
     p.arrived = reinterpret_cast<unsigned *>(base + w.arrived);
-    p.columns = std::min(kMaxColumns, (tokens + 7) / 8 * 8);
+    p.columns = moe_columns(tokens, experts, top_k);
     constexpr int kMaxSmem = 232448;
     for (p.stages = 8; p.stages > 2 && (int)moe_smem(experts, pairs, p.columns, p.stages).bytes > kMaxSmem; --p.stages) {
     }
@@ -695,7 +759,7 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     // gate_up as (k, 8 rows, gate / up, groups of 8 rows, k block): a box is 4 groups of 8 gate and 8 up rows.
     // An expert is inner / 4 groups further; the extent ends with the last expert's up rows, so every
     // element of a box lies inside the tensor or reads as zero.
-    CUtensorMap map_up, map_down, map_x, map_act;
+    CUtensorMap map_up, map_down;
     const cuuint64_t h2 = (cuuint64_t)hidden * 2, i2 = (cuuint64_t)inner * 2;
     {
         const cuuint64_t dims[5] = {p.up_blocked ? 64u : (cuuint64_t)hidden, 8, 2,
@@ -713,15 +777,10 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
         if ((st = encode_bf16(&map_down, down, 3, dims, strides, box)) != LOWM_OK)
             return st;
     }
-    const cuuint32_t row_box[2] = {64, 1};
-    const cuuint64_t x_dims[2] = {(cuuint64_t)hidden, (cuuint64_t)tokens}, x_strides[1] = {(cuuint64_t)x_stride * 2};
-    const cuuint64_t a_dims[2] = {(cuuint64_t)inner, (cuuint64_t)pairs}, a_strides[1] = {i2};
-    if ((st = encode_bf16(&map_x, x, 2, x_dims, x_strides, row_box)) != LOWM_OK ||
-        (st = encode_bf16(&map_act, p.act, 2, a_dims, a_strides, row_box)) != LOWM_OK)
-        return st;
 
     const int clusters = (tokens + kRouterCluster - 1) / kRouterCluster;
-    if ((st = launch_pdl(router_kernel, dim3((unsigned)(clusters * kRouterCluster)), dim3(256), 0, stream, p)) != LOWM_OK)
+    if ((st = launch_pdl(router_kernel, dim3((unsigned)(clusters * kRouterCluster)), dim3(32 * kRouterWarps), 0, stream, p)) !=
+        LOWM_OK)
         return st;
     if (cudaFuncSetAttribute(experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
         return LOWM_ERR_CUDA;
@@ -736,6 +795,6 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     attr.val.cooperative = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, experts_kernel, map_up, map_down, map_x, map_act, p) == cudaSuccess ? LOWM_OK
+    return cudaLaunchKernelEx(&cfg, experts_kernel, map_up, map_down, p) == cudaSuccess ? LOWM_OK
                                                                                                         : LOWM_ERR_CUDA;
 }

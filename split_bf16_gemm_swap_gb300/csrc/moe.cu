@@ -30,7 +30,7 @@
 #include <algorithm>
 
 #include "layer_host.h"
-#include "lowm_kernel.cuh"
+#include "layer_device.cuh"
 
 namespace lowm {
 namespace {
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         bool ok = true;
         auto weights = [&](bool up, int item, int k) {
             const int s = i % stages;
-            if (!wait_bounded<false>(bar_empty + 8 * s, ((i / stages) & 1) ^ 1, kDefaultTimeoutNs)) {
+            if (!wait_short(bar_empty + 8 * s, ((i / stages) & 1) ^ 1)) {
                 ok = false;
                 atomicOr(p.status, kErrMoeRing);
                 return;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                     weights(false, item, k);
             if (!ok)        // no copy may land after the CTA has ended (normally the MMAs have consumed all)
                 for (uint32_t j = i > (uint32_t)stages ? i - stages : 0; j < i; ++j)
-                    (void)wait_bounded<false>(bar_full + 8 * (j % stages), (j / stages) & 1, kDrainTimeoutNs);
+                    (void)wait_short(bar_full + 8 * (j % stages), (j / stages) & 1);
         }
         __syncwarp();
     } else if (warp == 7) {
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         };
         auto rows = [&](bool up, const ushort4 g, int k) {
             const int s = i % stages;
-            if (!wait_bounded<false>(bar_empty + 8 * s, ((i / stages) & 1) ^ 1, kDefaultTimeoutNs)) {
+            if (!wait_short(bar_empty + 8 * s, ((i / stages) & 1) ^ 1)) {
                 ok = false;
                 atomicOr(p.status, kErrMoeRing);
             }
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         uint32_t i = 0, n = 0;
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
-            if (ok && !wait_bounded<false>(bar, parity, kDefaultTimeoutNs)) {
+            if (ok && !wait_short(bar, parity)) {
                 ok = false;
                 if (lane == 0)
                     atomicOr(p.status, err);
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         if (lane == 0)
             ptx::tcgen05_commit(bar_drain);
         __syncwarp();
-        (void)wait_bounded<false>(bar_drain, 0, kDrainTimeoutNs);   // nothing writes TMEM any more
+        (void)wait_short(bar_drain, 0);   // nothing writes TMEM any more
     } else {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3, etid = threadIdx.x - 64;
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         uint32_t n = 0;
         bool ok = true;
         auto wait_acc = [&]() {
-            if (ok && !wait_bounded<false>(bar_acc + 8 * (n & 1), (n >> 1) & 1, kDefaultTimeoutNs)) {
+            if (ok && !wait_short(bar_acc + 8 * (n & 1), (n >> 1) & 1)) {
                 ok = false;
                 atomicOr(p.status, kErrMoeAccumulator);
             }

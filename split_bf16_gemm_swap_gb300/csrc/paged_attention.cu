@@ -13,9 +13,10 @@
 // in the workspace, and a second small kernel joins the parts in order.
 //
 // A CTA has four softmax warps (a thread owns a row = a TMEM lane), a warp
-// that feeds a ring of 64-key tiles by TMA, page by page, and a warp that
-// issues the MMAs: S = Q K^T into one of two TMEM buffers, then O += P V with
-// P (bf16, written over its S) from TMEM and V as the transposed operand.
+// that feeds a ring of 64-key tiles by TMA, page by page, and two
+// threads that issue the MMAs: S = Q K^T into one of two TMEM buffers, and
+// O += P V with P (bf16, written over its S) from TMEM and V as the transposed
+// operand.
 // S of the next tile is computed while the softmax of this one runs, and the
 // two CTAs of an SM fill each other's gaps.  O is rescaled only when a row's
 // maximum has grown by 2^8 (the weights stay below 256, and bf16 and fp32 are
@@ -30,15 +31,16 @@
 #include <climits>
 
 #include "layer_host.h"
-#include "lowm_kernel.cuh"
+#include "layer_device.cuh"
 
 namespace lowm {
 namespace {
 
 constexpr int kTileKeys = 64;
 constexpr int kTileRows = 128;
-constexpr int kAttnThreads = 192;            // softmax warps 0-3, TMA warp 4, MMA warp 5
+constexpr int kAttnThreads = 224;            // softmax warps 0-3, TMA warp 4, MMA warps 5 (Q K^T) and 6 (P V)
 constexpr int kMaxAttnCtas = 320;            // two per SM, and a bound for the workspace
+constexpr int kMaxKeys = 1 << 30;            // of a sequence
 constexpr int kMinShare = 4;                 // tiles: a share below 256 keys costs more in the join than it saves
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSColumns = 64;           // one S buffer; P takes its first 32 columns
@@ -73,7 +75,7 @@ struct Item {
     int b, head, q_tile;                     // sequence, key/value head, tile of 128 rows
     int q0, q_len, kv;                       // the sequence's first row of q, new tokens, keys
     int first_tile, tiles;                   // tiles of 64 keys
-    int64_t start;                           // the item's first tile on the line
+    int start;                               // the item's first tile on the line
 };
 
 __device__ __forceinline__ void load_sequence(const AttnParams &p, int b, int &q0, int &q_len, int &kv)
@@ -88,10 +90,10 @@ __device__ __forceinline__ void load_sequence(const AttnParams &p, int b, int &q
 __device__ __forceinline__ void tile_range(const AttnParams &p, int q_len, int kv, int q_tile, int &first, int &tiles)
 {
     const int t0 = q_tile * kTileRows / p.group, t1 = min(q_len - 1, (q_tile * kTileRows + kTileRows - 1) / p.group);
-    const int64_t hi = max(0, kv - q_len + t1 + 1);
-    const int64_t lo = p.window > 0 ? max((int64_t)0, (int64_t)kv - q_len + t0 - p.window + 1) : 0;
-    first = lo < hi ? (int)(lo / kTileKeys) : 0;
-    tiles = lo < hi ? (int)((hi + kTileKeys - 1) / kTileKeys) - first : 1;
+    const int hi = max(0, kv - q_len + t1 + 1);
+    const int lo = p.window > 0 ? max(0, kv - q_len + t0 - p.window + 1) : 0;
+    first = lo < hi ? lo / kTileKeys : 0;
+    tiles = lo < hi ? (hi + kTileKeys - 1) / kTileKeys - first : 1;
 }
 
 __device__ __forceinline__ int q_tiles_of(const AttnParams &p, int q_len)
@@ -100,11 +102,10 @@ __device__ __forceinline__ int q_tiles_of(const AttnParams &p, int q_len)
 }
 
 // Tiles of one key/value head of sequence b (all its row tiles).
-__device__ __forceinline__ int64_t head_tiles(const AttnParams &p, int b)
+__device__ __forceinline__ int head_tiles(const AttnParams &p, int b)
 {
-    int q0, q_len, kv, first, n;
+    int q0, q_len, kv, first, n, sum = 0;
     load_sequence(p, b, q0, q_len, kv);
-    int64_t sum = 0;
     for (int t = 0; t < q_tiles_of(p, q_len); ++t) {
         tile_range(p, q_len, kv, t, first, n);
         sum += n;
@@ -112,33 +113,28 @@ __device__ __forceinline__ int64_t head_tiles(const AttnParams &p, int b)
     return sum;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t x)
+// Tiles of the whole line (one warp, lanes over sequences).  The host refuses
+// calls whose line could pass 2^31.
+__device__ __forceinline__ int line_length(const AttnParams &p)
 {
-    for (int o = 16; o > 0; o >>= 1)
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-// Tiles of the whole line (one warp, lanes over sequences).
-__device__ __forceinline__ int64_t line_length(const AttnParams &p)
-{
-    int64_t sum = 0;
+    int sum = 0;
     for (int b = threadIdx.x & 31; b < p.batch; b += 32)
         sum += head_tiles(p, b);
-    return warp_sum(sum) * p.kv_heads;
+    return __reduce_add_sync(0xffffffffu, sum) * p.kv_heads;
 }
 
 // The item that tile u of the line belongs to (one warp; u below line_length).
-__device__ __forceinline__ Item locate(const AttnParams &p, int64_t u)
+__device__ __forceinline__ Item locate(const AttnParams &p, int u)
 {
     const int lane = threadIdx.x & 31;
     Item it;
-    int64_t before = 0;
+    int before = 0;
     for (int b0 = 0;; b0 += 32) {
-        const int64_t mine = b0 + lane < p.batch ? head_tiles(p, b0 + lane) * p.kv_heads : 0;
-        int64_t incl = mine;
+        const int mine = b0 + lane < p.batch ? head_tiles(p, b0 + lane) : 0;
+        int incl = mine * p.kv_heads;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o)
                 incl += y;
         }
@@ -146,10 +142,9 @@ __device__ __forceinline__ Item locate(const AttnParams &p, int64_t u)
         if (past || b0 + 32 >= p.batch) {
             const int l = past ? __ffs(past) - 1 : 31;
             it.b = min(b0 + l, p.batch - 1);
-            before += __shfl_sync(0xffffffffu, incl - mine, l);
-            const int64_t all = __shfl_sync(0xffffffffu, mine, l);
-            const int64_t per_head = max(all / p.kv_heads, (int64_t)1);
-            it.head = (int)((u - before) / per_head);
+            const int per_head = max(__shfl_sync(0xffffffffu, mine, l), 1);
+            before += __shfl_sync(0xffffffffu, incl, l) - per_head * p.kv_heads;
+            it.head = (u - before) / per_head;
             it.start = before + it.head * per_head;
             break;
         }
@@ -181,9 +176,9 @@ __device__ __forceinline__ void advance(const AttnParams &p, Item &it)
     tile_range(p, it.q_len, it.kv, it.q_tile, it.first_tile, it.tiles);
 }
 
-__device__ __forceinline__ int64_t share_of(int64_t line, int ctas)
+__device__ __forceinline__ int share_of(int line, int ctas)
 {
-    return max((line + ctas - 1) / ctas, (int64_t)kMinShare);
+    return max((line - 1) / ctas + 1, kMinShare);
 }
 
 // One CTA's share of one item: tiles [from, to) of it.
@@ -275,7 +270,7 @@ struct AttnSmem {
 struct Row {
     bool valid;
     int token, q_head;                       // token: index into q
-    int64_t hi, lo;                          // keys lo..hi are seen
+    int hi, lo;                              // keys lo..hi are seen
 };
 
 __device__ __forceinline__ Row row_of(const AttnParams &p, const Item &it, int r)
@@ -286,7 +281,7 @@ __device__ __forceinline__ Row row_of(const AttnParams &p, const Item &it, int r
     w.valid = t < it.q_len;
     w.token = it.q0 + t;
     w.q_head = it.head * p.group + row % p.group;
-    w.hi = (int64_t)it.kv - it.q_len + t;
+    w.hi = it.kv - it.q_len + t;
     w.lo = p.window > 0 ? w.hi - p.window + 1 : 0;
     return w;
 }
@@ -313,7 +308,7 @@ __device__ __forceinline__ void store_row(const AttnParams &p, const Row &w, int
 }
 
 template <int DIM>
-__global__ void __launch_bounds__(kAttnThreads, 2)
+__global__ void __launch_bounds__(256, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                            const AttnParams p)
 {
@@ -345,7 +340,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             ptx::mbar_init(bar_p + 8 * i, kTileRows);
             ptx::mbar_init(bar_o + 8 * i, 1);
         }
-        ptx::mbar_init(bar_drain, 1);
+        ptx::mbar_init(bar_drain, 2);
         ptx::fence_mbarrier_init_cluster();
         ptx::fence_proxy_async_shared();
     }
@@ -363,9 +358,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     // own wait (cu_q, kv_lens) is final now.
     ptx::griddep_launch_dependents();
 
-    const int64_t line = line_length(p);
-    const int64_t share = share_of(line, gridDim.x);
-    const int64_t begin = share * blockIdx.x, end = min(begin + share, line);
+    const int line = line_length(p);
+    const int share = share_of(line, gridDim.x);
+    const int begin = (int)min((int64_t)share * blockIdx.x, (int64_t)line), end = min(share, line - begin) + begin;
 
     if (begin < end) {
         if (warp == 4) {
@@ -373,21 +368,21 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             const int box_keys = min(p.page_size, kTileKeys), boxes = kTileKeys / box_keys;
             const int mine = lane / (int)L::kHalves, half = lane % (int)L::kHalves;   // this lane's box and half
             uint32_t i = 0;
-            int64_t u = begin;
+            int u = begin;
             bool ok = true;
             FOR_EACH_PIECE(p, it, u, end) {
-                const int from = (int)(u - it.start), to = (int)(min(end, it.start + it.tiles) - it.start);
+                const int from = u - it.start, to = min(end, it.start + it.tiles) - it.start;
                 const int32_t *pages = p.table + it.b * p.table_stride;
                 const int n = to - from;
                 // Table entries of this lane's box for the newest K tile and the V tile behind it.
                 auto entry = [&](int tile) {
-                    const int64_t key = (int64_t)(it.first_tile + tile) * kTileKeys + mine * box_keys;
+                    const int key = (it.first_tile + tile) * kTileKeys + mine * box_keys;
                     return mine < boxes && key < it.kv ? pages[key >> p.page_shift] : -1;
                 };
                 int page_k = entry(from), page_v = page_k, page_next = n > 1 ? entry(from + 1) : -1;
                 auto load = [&](const CUtensorMap *map, int tile, int page) {
                     const uint32_t s = i % L::kStages;
-                    if (ok && !wait_bounded<false>(bar_empty + 8 * s, ((i / L::kStages) & 1) ^ 1, kDefaultTimeoutNs)) {
+                    if (ok && !wait_short(bar_empty + 8 * s, ((i / L::kStages) & 1) ^ 1)) {
                         ok = false;
                         atomicOr(p.status, kErrAttnRing);
                     }
@@ -421,82 +416,82 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             }
             // No copy may land after the CTA has ended: normally all were consumed long ago.
             for (uint32_t j = i > L::kStages ? i - L::kStages : 0; j < i; ++j)
-                (void)wait_bounded<false>(bar_full + 8 * (j % L::kStages), (j / L::kStages) & 1, kDrainTimeoutNs);
-        } else if (warp == 5) {
-            // -------------------------------------------------------- MMA
+                (void)wait_short(bar_full + 8 * (j % L::kStages), (j / L::kStages) & 1);
+        } else if (warp >= 5) {
+            // -------------------------------------------------------- MMA: one thread for S, one for O
+            // A tile's 12 MMAs, 4 commits and 3 waits in one thread took 2100
+            // cycles, more than its softmax; two threads run them side by side.
             constexpr uint32_t kIdescS = make_idesc_bf16(kTileRows, kTileKeys);
             constexpr uint32_t kIdescO = make_idesc_bf16(kTileRows, DIM) | (1u << 16);   // B: N contiguous
-            uint32_t i = 0, g = 0, items = 0;
-            int64_t u = begin;
-            bool ok = true;
-            auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
-                if (ok && !wait_bounded<false>(bar, parity, kDefaultTimeoutNs)) {
-                    ok = false;
-                    if (lane == 0)
+            int u = begin;
+            Item it = locate(p, u);
+            if (lane == 0) {
+                uint32_t i = 0, g = 0, items = 0;                       // ring stages passed, tiles, items
+                bool ok = true;
+                auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
+                    if (!wait_short(bar, parity)) {
+                        ok = false;
                         atomicOr(p.status, err);
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                ptx::tcgen05_fence_after_thread_sync();
-            };
-            auto scores = [&](uint32_t gs) {                            // S[gs & 1] = Q . K^T
-                const uint32_t s = i % L::kStages;
-                wait(bar_full + 8 * s, (i / L::kStages) & 1, kErrAttnFull);
-                ++i;
-                if (lane == 0 && ok) {
-#pragma unroll
-                    for (uint32_t h = 0; h < L::kHalves; ++h) {
-                        const uint64_t a = make_sw128_kmajor_desc(sbase + L::kQ + h * (kTileRows * 128));
-                        const uint64_t b = make_sw128_kmajor_desc(sbase + L::kRing + s * L::kTileBytes + h * (kTileKeys * 128));
-#pragma unroll
-                        for (uint32_t k = 0; k < 4; ++k)
-                            ptx::mma_bf16_ss(tmem + (gs & 1) * kSColumns, a + 2 * k, b + 2 * k, kIdescS, h + k > 0);
                     }
-                    ptx::tcgen05_commit(bar_empty + 8 * s);
-                    ptx::tcgen05_commit(bar_s + 8 * (gs & 1));
-                }
-                __syncwarp();
-            };
-            FOR_EACH_PIECE(p, it, u, end) {
-                const int n = (int)(min(end, it.start + it.tiles) - u);
-                wait(bar_q, items & 1, kErrAttnWeights);
-                ++items;
-                scores(g);
-                for (int j = 0; j < n; ++j, ++g) {
-                    if (j + 1 < n)
-                        scores(g + 1);
-                    const uint32_t s = i % L::kStages;
-                    wait(bar_full + 8 * s, (i / L::kStages) & 1, kErrAttnFull);
-                    ++i;
-                    wait(bar_p + 8 * (g & 1), (g >> 1) & 1, kErrAttnWeights);
-                    if (lane == 0 && ok) {
-                        const uint64_t b = make_sw128_nmajor_desc(sbase + L::kRing + s * L::kTileBytes, kTileKeys * 128);
+                };
+                while (ok) {
+                    const int n = min(end, it.start + it.tiles) - u;
+                    if (warp == 5) {
+                        wait(bar_q, items & 1, kErrAttnWeights);
+                        for (int j = 0; j < n && ok; ++j, ++g) {        // S[g & 1] = Q . K^T
+                            const uint32_t at = i + (j == 0 ? 0 : 2 * j - 1), s = at % L::kStages;
+                            wait(bar_full + 8 * s, (at / L::kStages) & 1, kErrAttnFull);
+                            if (g > 1)                                  // the weights that lay there have met V
+                                wait(bar_o + 8 * (g & 1), ((g >> 1) & 1) ^ 1, kErrAttnOutput);
+                            ptx::tcgen05_fence_after_thread_sync();
+                            if (!ok)
+                                break;
+                            const uint64_t a0 = make_sw128_kmajor_desc(sbase + L::kQ);
+                            const uint64_t b0 = make_sw128_kmajor_desc(sbase + L::kRing + s * L::kTileBytes);
 #pragma unroll
-                        for (uint32_t k = 0; k < kTileKeys / 16; ++k)    // 16 keys: 2 KiB of V, 8 columns of P
-                            mma_bf16_ts(tmem + kOColumn, tmem + (g & 1) * kSColumns + 8 * k, b + 128 * k, kIdescO,
-                                        j > 0 || k > 0);
-                        ptx::tcgen05_commit(bar_empty + 8 * s);
-                        ptx::tcgen05_commit(bar_o + 8 * (g & 1));
+                            for (uint32_t k = 0; k < 4 * L::kHalves; ++k)
+                                ptx::mma_bf16_ss(tmem + (g & 1) * kSColumns, a0 + (k >> 2) * (kTileRows * 8) + 2 * (k & 3),
+                                                 b0 + (k >> 2) * (kTileKeys * 8) + 2 * (k & 3), kIdescS, k > 0);
+                            ptx::tcgen05_commit(bar_s + 8 * (g & 1));
+                            ptx::tcgen05_commit(bar_empty + 8 * s);
+                        }
+                    } else {
+                        for (int j = 0; j < n && ok; ++j, ++g) {        // O (+)= P . V
+                            const uint32_t at = i + (j + 1 < n ? 2 * j + 2 : 2 * j + 1), s = at % L::kStages;
+                            wait(bar_full + 8 * s, (at / L::kStages) & 1, kErrAttnFull);
+                            wait(bar_p + 8 * (g & 1), (g >> 1) & 1, kErrAttnWeights);
+                            ptx::tcgen05_fence_after_thread_sync();
+                            if (!ok)
+                                break;
+                            const uint64_t b0 = make_sw128_nmajor_desc(sbase + L::kRing + s * L::kTileBytes, kTileKeys * 128);
+#pragma unroll
+                            for (uint32_t k = 0; k < kTileKeys / 16; ++k)    // 16 keys: 2 KiB of V, 8 columns of P
+                                mma_bf16_ts(tmem + kOColumn, tmem + (g & 1) * kSColumns + 8 * k, b0 + 128 * k, kIdescO,
+                                            j > 0 || k > 0);
+                            ptx::tcgen05_commit(bar_o + 8 * (g & 1));
+                            ptx::tcgen05_commit(bar_empty + 8 * s);
+                        }
                     }
-                    __syncwarp();
-                    if (!ok)
+                    i += 2 * n;
+                    ++items;
+                    u = it.start + it.tiles;
+                    if (u >= end)
                         break;
+                    advance(p, it);
                 }
-                if (!ok)
-                    break;
-            }
-            if (lane == 0)
                 ptx::tcgen05_commit(bar_drain);
+            }
             __syncwarp();
-            (void)wait_bounded<false>(bar_drain, 0, kDrainTimeoutNs);    // nothing reads or writes TMEM any more
+            (void)wait_short(bar_drain, 0);                             // nothing reads or writes TMEM any more
         } else {
             // -------------------------------------------------------- softmax: thread = row = TMEM lane
             const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
             const int r = threadIdx.x;
             uint32_t i = 0, g = 0;
-            int64_t u = begin;
+            int u = begin;
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
-                if (ok && !wait_bounded<false>(bar, parity, kDefaultTimeoutNs)) {
+                if (ok && !wait_short(bar, parity)) {
                     ok = false;
                     atomicOr(p.status, err);
                 }
@@ -504,7 +499,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 ptx::tcgen05_fence_after_thread_sync();
             };
             FOR_EACH_PIECE(p, it, u, end) {
-                const int from = (int)(u - it.start), to = (int)(min(end, it.start + it.tiles) - it.start), n = to - from;
+                const int from = u - it.start, to = min(end, it.start + it.tiles) - it.start, n = to - from;
                 const Row w = row_of(p, it, r);
                 const bool warp_has_rows = __any_sync(0xffffffffu, w.valid);
                 // This row of Q into the swizzled K-major tile (16-byte chunk c of row r at c ^ (r & 7)).
@@ -534,9 +529,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 }
                 // Keys every row of the tile sees: no mask inside [all_lo, all_hi].
                 const Row w0 = row_of(p, it, 0);
-                const int64_t all_hi = w0.hi;
+                const int all_hi = w0.hi;
                 const int last_token = min(it.q_len - 1, (it.q_tile * kTileRows + kTileRows - 1) / p.group);
-                const int64_t all_lo = p.window > 0 ? (int64_t)it.kv - it.q_len + last_token - p.window + 1 : 0;
+                const int all_lo = p.window > 0 ? it.kv - it.q_len + last_token - p.window + 1 : 0;
 
                 float m = -CUDART_INF_F, l = 0.f;                       // maximum (raw score) and sum of this row
                 for (int j = 0; j < n; ++j, ++g) {
@@ -553,22 +548,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         tmem_ld_x32(s_addr + 32, s1);
                         ptx::tmem_wait_ld();
                         if (key0 < all_lo || key0 + kTileKeys - 1 > all_hi) {
-                            const int hi = (int)min((int64_t)kTileKeys, w.hi - key0), lo = (int)max((int64_t)0, min((int64_t)kTileKeys, w.lo - key0));
+                            const int hi = w.valid ? w.hi - key0 : -1, lo = w.lo - key0;
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
-                                if (k > hi || k < lo || !w.valid)
+                                if (k > hi || k < lo)
                                     s0[k] = 0xff800000u;
-                                if (k + 32 > hi || k + 32 < lo || !w.valid)
+                                if (k + 32 > hi || k + 32 < lo)
                                     s1[k] = 0xff800000u;
                             }
                         }
-                        float t0 = __uint_as_float(s0[0]), t1 = __uint_as_float(s1[0]);
+                        float t[4] = {m, m, m, m};
 #pragma unroll
-                        for (int k = 1; k < 32; ++k) {
-                            t0 = fmaxf(t0, __uint_as_float(s0[k]));
-                            t1 = fmaxf(t1, __uint_as_float(s1[k]));
-                        }
-                        const float top = fmaxf(m, fmaxf(t0, t1));
+                        for (int k = 0; k < 32; k += 4)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                t[c] = fmaxf(fmaxf(t[c], __uint_as_float(s0[k + c])), __uint_as_float(s1[k + c]));
+                        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                         if (j == 0) {
                             m = top;
                         } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescaleLog2)) {
@@ -580,14 +575,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                             l *= a;
                             m = top;
 #pragma unroll
-                            for (int c = 0; c < DIM; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld_x32(lane_base + kOColumn + c, o);
+                            for (int c = 0; c < DIM; c += 8) {
+                                uint32_t o[8];
+                                ptx::tmem_ld_32x32b_x8(lane_base + kOColumn + c, o);
                                 ptx::tmem_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
+                                for (int k = 0; k < 8; ++k)
                                     o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                                tmem_st_x32(lane_base + kOColumn + c, o);
+                                ptx::tmem_st_32x32b_x8(lane_base + kOColumn + c, o);
                             }
                         }
                         const float ms = m == -CUDART_INF_F ? 0.f : m * p.scale_log2;
@@ -688,10 +683,10 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const AttnParams p, int
     constexpr int E = DIM / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_launch_dependents();
-    const int64_t line = p.batch > 0 ? line_length(p) : 0;
-    const int64_t share = share_of(line, ctas);
-    const int64_t end = share * (blockIdx.x + 1);
-    const bool cut = end < line;
+    const int line = p.batch > 0 ? line_length(p) : 0;
+    const int share = share_of(line, ctas);
+    const bool cut = (int64_t)share * (blockIdx.x + 1) < line;
+    const int end = cut ? share * (int)(blockIdx.x + 1) : line;
     Item it;
     if (cut)
         it = locate(p, end - 1);
@@ -710,7 +705,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const AttnParams p, int
     }
     if (!cut || it.start < end - share || it.start + it.tiles <= end)
         return;                              // no item is cut here, or it began in an earlier share
-    const int parts = (int)((it.start + it.tiles - 1) / share - blockIdx.x) + 1;
+    const int parts = (it.start + it.tiles - 1) / share - (int)blockIdx.x + 1;
     const float2 *ml = reinterpret_cast<const float2 *>(p.parts + 2 * (int64_t)ctas * p.slot_rows * DIM);
     auto slot = [&](int i) { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
     for (int r = warp; r < kTileRows; r += 8) {
@@ -849,6 +844,11 @@ extern "C" lowm_status_t lowm_paged_attention(
     for (int i = 0; i < 6; ++i)
         if (extents[i] > 1 && (cache_strides[i] == 0 || cache_strides[i] >= ((int64_t)1 << 39)))
             return LOWM_ERR_INVALID_ARGUMENT;
+    // Tile counts are 32-bit in the kernels.
+    const int64_t capacity = std::min<int64_t>((int64_t)table_width * page_size, kMaxKeys);
+    const int64_t q_tiles = (int64_t)q_tokens * (heads / kv_heads) / kTileRows + batch;
+    if ((double)q_tiles * kv_heads * (double)(capacity / kTileKeys + 2) > (double)INT_MAX)
+        return LOWM_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     lowm_status_t st = host_check_device(&sms);
     if (st != LOWM_OK)
@@ -876,9 +876,9 @@ extern "C" lowm_status_t lowm_paged_attention(
     p.heads = heads;
     p.kv_heads = kv_heads;
     p.group = heads / kv_heads;
-    p.window = window;
+    p.window = window < kMaxKeys ? window : 0;
     p.slot_rows = slot_rows_of(q_tokens, heads, kv_heads);
-    p.capacity = (int)std::min<int64_t>((int64_t)table_width * page_size, INT_MAX - 2 * kTileKeys);
+    p.capacity = (int)capacity;
     // Never 0, so that a masked score (-inf) stays one.
     p.scale_log2 = std::max((scale < 0.f ? -scale : scale) * 1.44269504088896340736f, 1e-30f);
     p.q_sign = scale < 0.f ? -1.f : 1.f;

@@ -13,10 +13,9 @@
 // in the workspace, and a second small kernel joins the parts in order.
 //
 // A CTA has four softmax warps (a thread owns a row = a TMEM lane), a warp
-// that feeds a ring of 64-key tiles by TMA, page by page, and two
-// threads that issue the MMAs: S = Q K^T into one of two TMEM buffers, and
-// O += P V with P (bf16, written over its S) from TMEM and V as the transposed
-// operand.
+// that feeds a ring of 64-key tiles by TMA, page by page, and two threads that
+// issue the MMAs: S = Q K^T into one of two TMEM buffers, and O += P V with P
+// (bf16, written over its S) from TMEM and V as the transposed operand.
 // S of the next tile is computed while the softmax of this one runs, and the
 // two CTAs of an SM fill each other's gaps.  O is rescaled only when a row's
 // maximum has grown by 2^8 (the weights stay below 256, and bf16 and fp32 are
@@ -41,7 +40,13 @@ constexpr int kTileRows = 128;
 constexpr int kAttnThreads = 224;            // softmax warps 0-3, TMA warp 4, MMA warps 5 (Q K^T) and 6 (P V)
 constexpr int kMaxAttnCtas = 320;            // two per SM, and a bound for the workspace
 constexpr int kMaxKeys = 1 << 30;            // of a sequence
-constexpr int kMinShare = 4;                 // tiles: a share below 256 keys costs more in the join than it saves
+// The line counts time in tiles.  An item costs kItemCost tiles beside its own
+// (its queries' way in, its rows' way out); without it the CTAs with short
+// items ended 20 % after the others (chunks of 512 and fewer tokens of four
+// sequences: 112 us at 3, 107 at 7, 103 at 12; of 1537 tokens 260, 249, 253).
+constexpr int kItemCost = 7;
+constexpr int kMinShare = 4;                 // smaller shares cost more in the join than they save (6: 14.6 us for the
+                                             // short decodes that take 13.2)
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSColumns = 64;           // one S buffer; P takes its first 32 columns
 
@@ -66,7 +71,8 @@ struct AttnParams {
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
     float q_sign;
     bool q_vec, out_vec;                     // 16-byte rows
-    float *parts;                            // [2 * ctas][slot_rows][dim] sums, then [2 * ctas][slot_rows][2] (max, sum)
+    float4 *parts;                           // [2 * ctas][dim / 4][slot_rows] sums, rows side by side as the lanes hold
+                                             // them, then [2 * ctas][slot_rows] (max, sum) pairs
     unsigned int *status;
 };
 
@@ -75,7 +81,7 @@ struct Item {
     int b, head, q_tile;                     // sequence, key/value head, tile of 128 rows
     int q0, q_len, kv;                       // the sequence's first row of q, new tokens, keys
     int first_tile, tiles;                   // tiles of 64 keys
-    int start;                               // the item's first tile on the line
+    int start;                               // the item's place on the line: kItemCost units, then its tiles
 };
 
 __device__ __forceinline__ void load_sequence(const AttnParams &p, int b, int &q0, int &q_len, int &kv)
@@ -101,68 +107,86 @@ __device__ __forceinline__ int q_tiles_of(const AttnParams &p, int q_len)
     return (q_len * p.group + kTileRows - 1) / kTileRows;
 }
 
-// Tiles of one key/value head of sequence b (all its row tiles).
-__device__ __forceinline__ int head_tiles(const AttnParams &p, int b)
+// Units of one key/value head of sequence b (all its row tiles).
+__device__ __forceinline__ int head_units(const AttnParams &p, int b)
 {
     int q0, q_len, kv, first, n, sum = 0;
     load_sequence(p, b, q0, q_len, kv);
     for (int t = 0; t < q_tiles_of(p, q_len); ++t) {
         tile_range(p, q_len, kv, t, first, n);
-        sum += n;
+        sum += n + kItemCost;
     }
     return sum;
 }
 
-// Tiles of the whole line (one warp, lanes over sequences).  The host refuses
-// calls whose line could pass 2^31.
-__device__ __forceinline__ int line_length(const AttnParams &p)
+// The line as one warp sees it: lane l holds the units of a head of sequence l
+// and of all heads of sequences 0..l (of the first 32), and everyone the total.
+// The host refuses calls whose line could pass 2^31.
+struct Line {
+    int head, upto, total;
+};
+
+__device__ __forceinline__ int scan32(int x)
 {
-    int sum = 0;
-    for (int b = threadIdx.x & 31; b < p.batch; b += 32)
-        sum += head_tiles(p, b);
-    return __reduce_add_sync(0xffffffffu, sum) * p.kv_heads;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((threadIdx.x & 31) >= o)
+            x += y;
+    }
+    return x;
 }
 
-// The item that tile u of the line belongs to (one warp; u below line_length).
-__device__ __forceinline__ Item locate(const AttnParams &p, int u)
+__device__ __forceinline__ Line make_line(const AttnParams &p)
+{
+    const int lane = threadIdx.x & 31;
+    Line l;
+    l.head = lane < p.batch ? head_units(p, lane) : 0;
+    l.upto = scan32(l.head * p.kv_heads);
+    l.total = __shfl_sync(0xffffffffu, l.upto, 31);
+    if (p.batch > 32) {
+        int sum = 0;
+        for (int b = 32 + lane; b < p.batch; b += 32)
+            sum += head_units(p, b);
+        l.total += __reduce_add_sync(0xffffffffu, sum) * p.kv_heads;
+    }
+    return l;
+}
+
+// The item that unit u of the line belongs to (one warp; u below the total).
+__device__ __forceinline__ Item locate(const AttnParams &p, Line line, int u)
 {
     const int lane = threadIdx.x & 31;
     Item it;
     int before = 0;
     for (int b0 = 0;; b0 += 32) {
-        const int mine = b0 + lane < p.batch ? head_tiles(p, b0 + lane) : 0;
-        int incl = mine * p.kv_heads;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + incl > u);
+        const unsigned past = __ballot_sync(0xffffffffu, before + line.upto > u);
         if (past || b0 + 32 >= p.batch) {
             const int l = past ? __ffs(past) - 1 : 31;
             it.b = min(b0 + l, p.batch - 1);
-            const int per_head = max(__shfl_sync(0xffffffffu, mine, l), 1);
-            before += __shfl_sync(0xffffffffu, incl, l) - per_head * p.kv_heads;
+            const int per_head = max(__shfl_sync(0xffffffffu, line.head, l), 1);
+            before += __shfl_sync(0xffffffffu, line.upto, l) - per_head * p.kv_heads;
             it.head = (u - before) / per_head;
             it.start = before + it.head * per_head;
             break;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        before += __shfl_sync(0xffffffffu, line.upto, 31);
+        line.head = b0 + 32 + lane < p.batch ? head_units(p, b0 + 32 + lane) : 0;
+        line.upto = scan32(line.head * p.kv_heads);
     }
     load_sequence(p, it.b, it.q0, it.q_len, it.kv);
     for (it.q_tile = 0;; ++it.q_tile) {
         tile_range(p, it.q_len, it.kv, it.q_tile, it.first_tile, it.tiles);
-        if (u < it.start + it.tiles || it.q_tile + 1 >= q_tiles_of(p, it.q_len))
+        if (u < it.start + kItemCost + it.tiles || it.q_tile + 1 >= q_tiles_of(p, it.q_len))
             return it;
-        it.start += it.tiles;
+        it.start += kItemCost + it.tiles;
     }
 }
 
 // The item behind `it` on the line.
 __device__ __forceinline__ void advance(const AttnParams &p, Item &it)
 {
-    it.start += it.tiles;
+    it.start += kItemCost + it.tiles;
     if (++it.q_tile >= q_tiles_of(p, it.q_len)) {
         it.q_tile = 0;
         if (++it.head == p.kv_heads) {
@@ -178,12 +202,42 @@ __device__ __forceinline__ void advance(const AttnParams &p, Item &it)
 
 __device__ __forceinline__ int share_of(int line, int ctas)
 {
-    return max((line - 1) / ctas + 1, kMinShare);
+    return max((line + ctas - 1) / ctas, kMinShare);
 }
 
-// One CTA's share of one item: tiles [from, to) of it.
-#define FOR_EACH_PIECE(p, it, u, end)                                                                            \
-    for (Item it = locate(p, u); u < end; u = it.start + it.tiles, u < end ? advance(p, it) : (void)0)
+// A CTA's part of one item: tiles [from, to) of it, at least one.
+struct Piece {
+    Item it;
+    int from, to;
+};
+
+__device__ __forceinline__ void cut(Piece &c, int u, int end)
+{
+    const int first = c.it.start + kItemCost;          // the item's first tile on the line
+    c.from = max(u - first, 0);
+    c.to = min(end - first, c.it.tiles);
+}
+
+// The first piece of the share [begin, end); false when it has none.
+__device__ __forceinline__ bool next_piece(const AttnParams &p, Piece &c, int end)
+{
+    for (;;) {
+        const int u = c.it.start + kItemCost + c.it.tiles;
+        if (u >= end)
+            return false;
+        advance(p, c.it);
+        cut(c, u, end);
+        if (c.from < c.to)
+            return true;
+    }
+}
+
+__device__ __forceinline__ bool first_piece(const AttnParams &p, Piece &c, const Line &line, int begin, int end)
+{
+    c.it = locate(p, line, begin);
+    cut(c, begin, end);
+    return c.from < c.to || next_piece(p, c, end);
+}
 
 // ------------------------------------------------------------------ PTX of this kernel
 __device__ __forceinline__ float ex2(float x)
@@ -308,7 +362,7 @@ __device__ __forceinline__ void store_row(const AttnParams &p, const Row &w, int
 }
 
 template <int DIM>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(kAttnThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                            const AttnParams p)
 {
@@ -334,10 +388,10 @@ __global__ void __launch_bounds__(256, 2)
             ptx::mbar_init(bar_full + 8 * s, 1);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
-        ptx::mbar_init(bar_q, kTileRows);
+        ptx::mbar_init(bar_q, 4);                // softmax warps
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar_s + 8 * i, 1);
-            ptx::mbar_init(bar_p + 8 * i, kTileRows);
+            ptx::mbar_init(bar_p + 8 * i, 4);
             ptx::mbar_init(bar_o + 8 * i, 1);
         }
         ptx::mbar_init(bar_drain, 2);
@@ -358,22 +412,22 @@ __global__ void __launch_bounds__(256, 2)
     // own wait (cu_q, kv_lens) is final now.
     ptx::griddep_launch_dependents();
 
-    const int line = line_length(p);
-    const int share = share_of(line, gridDim.x);
-    const int begin = (int)min((int64_t)share * blockIdx.x, (int64_t)line), end = min(share, line - begin) + begin;
+    const Line line = make_line(p);
+    const int share = share_of(line.total, gridDim.x);
+    const int begin = (int)min((int64_t)share * blockIdx.x, (int64_t)line.total), end = min(share, line.total - begin) + begin;
 
-    if (begin < end) {
+    Piece c;
+    if (begin < end && first_piece(p, c, line, begin, end)) {
+        const Item &it = c.it;
         if (warp == 4) {
             // -------------------------------------------------------- TMA: K0, K1, V0, K2, V1, ...
             const int box_keys = min(p.page_size, kTileKeys), boxes = kTileKeys / box_keys;
             const int mine = lane / (int)L::kHalves, half = lane % (int)L::kHalves;   // this lane's box and half
             uint32_t i = 0;
-            int u = begin;
             bool ok = true;
-            FOR_EACH_PIECE(p, it, u, end) {
-                const int from = u - it.start, to = min(end, it.start + it.tiles) - it.start;
+            do {
+                const int from = c.from, n = c.to - c.from;
                 const int32_t *pages = p.table + it.b * p.table_stride;
-                const int n = to - from;
                 // Table entries of this lane's box for the newest K tile and the V tile behind it.
                 auto entry = [&](int tile) {
                     const int key = (it.first_tile + tile) * kTileKeys + mine * box_keys;
@@ -411,9 +465,7 @@ __global__ void __launch_bounds__(256, 2)
                     }
                     load(&map_v, from + j, page_v);
                 }
-                if (!ok)
-                    break;
-            }
+            } while (ok && next_piece(p, c, end));
             // No copy may land after the CTA has ended: normally all were consumed long ago.
             for (uint32_t j = i > L::kStages ? i - L::kStages : 0; j < i; ++j)
                 (void)wait_short(bar_full + 8 * (j % L::kStages), (j / L::kStages) & 1);
@@ -423,8 +475,6 @@ __global__ void __launch_bounds__(256, 2)
             // cycles, more than its softmax; two threads run them side by side.
             constexpr uint32_t kIdescS = make_idesc_bf16(kTileRows, kTileKeys);
             constexpr uint32_t kIdescO = make_idesc_bf16(kTileRows, DIM) | (1u << 16);   // B: N contiguous
-            int u = begin;
-            Item it = locate(p, u);
             if (lane == 0) {
                 uint32_t i = 0, g = 0, items = 0;                       // ring stages passed, tiles, items
                 bool ok = true;
@@ -434,8 +484,8 @@ __global__ void __launch_bounds__(256, 2)
                         atomicOr(p.status, err);
                     }
                 };
-                while (ok) {
-                    const int n = min(end, it.start + it.tiles) - u;
+                do {
+                    const int n = c.to - c.from;
                     if (warp == 5) {
                         wait(bar_q, items & 1, kErrAttnWeights);
                         for (int j = 0; j < n && ok; ++j, ++g) {        // S[g & 1] = Q . K^T
@@ -474,11 +524,7 @@ __global__ void __launch_bounds__(256, 2)
                     }
                     i += 2 * n;
                     ++items;
-                    u = it.start + it.tiles;
-                    if (u >= end)
-                        break;
-                    advance(p, it);
-                }
+                } while (ok && next_piece(p, c, end));
                 ptx::tcgen05_commit(bar_drain);
             }
             __syncwarp();
@@ -488,48 +534,61 @@ __global__ void __launch_bounds__(256, 2)
             const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
             const int r = threadIdx.x;
             uint32_t i = 0, g = 0;
-            int u = begin;
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
-                if (ok && !wait_short(bar, parity)) {
+                if (!wait_short(bar, parity)) {
                     ok = false;
                     atomicOr(p.status, err);
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 ptx::tcgen05_fence_after_thread_sync();
             };
-            FOR_EACH_PIECE(p, it, u, end) {
-                const int from = u - it.start, to = min(end, it.start + it.tiles) - it.start, n = to - from;
+            // A warp's 32 rows of Q into the swizzled K-major tile (16-byte chunk c of
+            // row r at c ^ (r & 7)), a row's chunks by neighbouring lanes, all loads
+            // before the first store.
+            auto load_q = [&](const Item &item) {
+                constexpr int kChunks = DIM / 8, kRowsAtOnce = 32 / kChunks, kLoads = 32 / kRowsAtOnce;
+                const Row row = row_of(p, item, r);
+                const int64_t at = row.valid ? row.token * p.q_ts + row.q_head * p.q_hs : -1;
+                const uint32_t flip = p.q_sign < 0.f ? 0x80008000u : 0u;
+                const int c = lane % kChunks, q0 = lane / kChunks;
+                uint4 x[kLoads];
+                if (p.q_vec) {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int64_t from = __shfl_sync(0xffffffffu, at, i * kRowsAtOnce + q0);
+                        x[i] = from >= 0 ? *reinterpret_cast<const uint4 *>(p.q + from + 8 * c) : make_uint4(0, 0, 0, 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int64_t from = __shfl_sync(0xffffffffu, at, i * kRowsAtOnce + q0);
+                        __nv_bfloat16 *e = reinterpret_cast<__nv_bfloat16 *>(&x[i]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            e[j] = from >= 0 ? p.q[from + 8 * c + j] : __float2bfloat16_rn(0.f);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int q = i * kRowsAtOnce + q0;
+                    *reinterpret_cast<uint4 *>(smem + L::kQ + (c >> 3) * (kTileRows * 128) + (32 * warp + q) * 128 +
+                                               (((c & 7) ^ (q & 7)) << 4)) =
+                        make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
+                }
+                ptx::fence_proxy_async_shared();
+                ptx::tcgen05_fence_before_thread_sync();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(bar_q);
+            };
+            load_q(it);
+            for (bool more = true; more;) {
+                const int from = c.from, n = c.to - c.from;
                 const Row w = row_of(p, it, r);
                 const bool warp_has_rows = __any_sync(0xffffffffu, w.valid);
-                // This row of Q into the swizzled K-major tile (16-byte chunk c of row r at c ^ (r & 7)).
-                {
-                    const __nv_bfloat16 *q = p.q + (w.valid ? w.token * p.q_ts + w.q_head * p.q_hs : 0);
-                    const uint32_t flip = p.q_sign < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-                    for (int c = 0; c < DIM / 8; ++c) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (w.valid) {
-                            if (p.q_vec) {
-                                x = *reinterpret_cast<const uint4 *>(q + 8 * c);
-                            } else {
-                                __nv_bfloat16 *e = reinterpret_cast<__nv_bfloat16 *>(&x);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    e[j] = q[8 * c + j];
-                            }
-                            x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-                        }
-                        *reinterpret_cast<uint4 *>(smem + L::kQ + (c >> 3) * (kTileRows * 128) + r * 128 +
-                                                   (((c & 7) ^ (r & 7)) << 4)) = x;
-                    }
-                    ptx::fence_proxy_async_shared();
-                    ptx::tcgen05_fence_before_thread_sync();
-                    ptx::mbar_arrive(bar_q);
-                }
                 // Keys every row of the tile sees: no mask inside [all_lo, all_hi].
-                const Row w0 = row_of(p, it, 0);
-                const int all_hi = w0.hi;
+                const int all_hi = it.kv - it.q_len + it.q_tile * kTileRows / p.group;
                 const int last_token = min(it.q_len - 1, (it.q_tile * kTileRows + kTileRows - 1) / p.group);
                 const int all_lo = p.window > 0 ? it.kv - it.q_len + last_token - p.window + 1 : 0;
 
@@ -621,17 +680,24 @@ __global__ void __launch_bounds__(256, 2)
                         ptx::fence_proxy_async_shared();
                     }
                     ptx::tcgen05_fence_before_thread_sync();
-                    ptx::mbar_arrive(bar_p + 8 * (g & 1));
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(bar_p + 8 * (g & 1));
                 }
                 if (!ok)
                     break;
                 i += 2 * n;
+                // The next item's queries before this one's rows: every S of this one is complete, and the
+                // first products of the next run while its rows are written.
+                const bool whole = n == it.tiles;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0);
+                more = next_piece(p, c, end);
+                if (more)
+                    load_q(it);
                 wait(bar_o + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, kErrAttnOutput);
                 if (!ok)
                     break;
                 // The item's rows: finished here, or a part for the join.
-                const bool whole = n == it.tiles;
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 if (warp_has_rows) {
 #pragma unroll
@@ -648,10 +714,10 @@ __global__ void __launch_bounds__(256, 2)
                                 v[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
                             store_row<DIM>(p, w, c, v);
                         } else {
-                            float4 *dst = reinterpret_cast<float4 *>(p.parts + (slot * p.slot_rows + r) * DIM + c);
+                            float4 *dst = p.parts + (slot * (DIM / 4) + c / 4) * p.slot_rows + r;
 #pragma unroll
                             for (int k = 0; k < 32; k += 4)
-                                dst[k / 4] = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                                dst[k / 4 * p.slot_rows] = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
                                                          __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
                         }
                     }
@@ -659,7 +725,7 @@ __global__ void __launch_bounds__(256, 2)
                         p.lse[(int64_t)w.token * p.heads + w.q_head] =
                             l == 0.f ? -CUDART_INF_F : (m * p.scale_log2 + log2f(l)) * CUDART_LN2_F;
                     if (w.valid && !whole) {
-                        float2 *ml = reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * DIM);
+                        float2 *ml = reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * (DIM / 4));
                         ml[slot * p.slot_rows + r] = make_float2(m * p.scale_log2, l);
                     }
                 }
@@ -674,69 +740,77 @@ __global__ void __launch_bounds__(256, 2)
     }
 }
 
-// Joins the parts of the items that shares cut: CTA c owns the item that
-// begins in share c and ends in a later one.  A part's weight is
-// 2^(its maximum - the largest maximum); parts add in the order of the keys.
+// Joins the parts of the items that shares cut: CTA c owns the item whose
+// first tile is in share c and whose last is in a later one.  A thread owns
+// four elements of a row; neighbouring threads own neighbouring rows, as the
+// parts lie in memory.  Part i counts 2^(its maximum - the largest maximum),
+// and the parts add in the order of the keys.
+constexpr int kJoinThreads = 256, kJoinSplit = 4;   // CTAs of an item: one SM reads about 50 bytes a nanosecond
+
 template <int DIM>
-__global__ void __launch_bounds__(256) join_parts_kernel(const AttnParams p, int ctas)
+__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const AttnParams p, int ctas)
 {
-    constexpr int E = DIM / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_launch_dependents();
-    const int line = p.batch > 0 ? line_length(p) : 0;
-    const int share = share_of(line, ctas);
-    const bool cut = (int64_t)share * (blockIdx.x + 1) < line;
-    const int end = cut ? share * (int)(blockIdx.x + 1) : line;
+    const Line line = make_line(p);
+    const int share = share_of(line.total, ctas);
+    const bool inside = (int64_t)share * (blockIdx.x + 1) < line.total;
+    const int end = inside ? share * (int)(blockIdx.x + 1) : line.total;
     Item it;
-    if (cut)
-        it = locate(p, end - 1);
+    if (inside)
+        it = locate(p, line, end - 1);
     ptx::griddep_wait();
-    if (blockIdx.x == 0) {                   // rows of no sequence
+    if (blockIdx.x == 0 && blockIdx.y == 0) { // rows of no sequence
         const int first = p.batch > 0 ? min(max(p.cu_q[0], 0), p.q_tokens) : p.q_tokens;
         const int last = p.batch > 0 ? min(max(p.cu_q[p.batch], 0), p.q_tokens) : p.q_tokens;
-        for (int t = warp; t < p.q_tokens; t += 8)
+        for (int t = threadIdx.x >> 5; t < p.q_tokens; t += kJoinThreads / 32)
             if (t < first || t >= last)
                 for (int h = 0; h < p.heads; ++h) {
-                    for (int d = lane; d < DIM; d += 32)
+                    for (int d = threadIdx.x & 31; d < DIM; d += 32)
                         p.out[t * p.o_ts + h * p.o_hs + d] = __float2bfloat16_rn(0.f);
-                    if (lane == 0 && p.lse)
+                    if ((threadIdx.x & 31) == 0 && p.lse)
                         p.lse[(int64_t)t * p.heads + h] = -CUDART_INF_F;
                 }
     }
-    if (!cut || it.start < end - share || it.start + it.tiles <= end)
+    const int first_tile = inside ? it.start + kItemCost : 0;
+    if (!inside || first_tile < end - share || first_tile >= end || first_tile + it.tiles <= end)
         return;                              // no item is cut here, or it began in an earlier share
-    const int parts = (it.start + it.tiles - 1) / share - (int)blockIdx.x + 1;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.parts + 2 * (int64_t)ctas * p.slot_rows * DIM);
+    const int parts = (first_tile + it.tiles - 1) / share - (int)blockIdx.x + 1;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.parts + 2 * (int64_t)ctas * p.slot_rows * (DIM / 4));
+    const int rows = min(kTileRows, it.q_len * p.group - it.q_tile * kTileRows);
     auto slot = [&](int i) { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
-    for (int r = warp; r < kTileRows; r += 8) {
+    for (int c = threadIdx.x + blockIdx.y * kJoinThreads; c < rows * (DIM / 4); c += kJoinSplit * kJoinThreads) {
+        const int r = c % rows, e = c / rows;
         const Row w = row_of(p, it, r);
-        if (!w.valid)
-            break;
         float top = -CUDART_INF_F;
-        for (int i = lane; i < parts; i += 32)
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i)
             top = fmaxf(top, ml[slot(i) * p.slot_rows + r].x);
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float base = top == -CUDART_INF_F ? 0.f : top;
-        float acc[E] = {}, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
 #pragma unroll 4
         for (int i = 0; i < parts; ++i) {
             const float2 x = ml[slot(i) * p.slot_rows + r];
+            const float4 o = p.parts[(slot(i) * (DIM / 4) + e) * p.slot_rows + r];
             const float a = ex2(x.x - base);
             l = fmaf(x.y, a, l);
-            const float *src = p.parts + (slot(i) * p.slot_rows + r) * DIM + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                acc[e] = fmaf(src[e], a, acc[e]);
+            acc.x = fmaf(o.x, a, acc.x);
+            acc.y = fmaf(o.y, a, acc.y);
+            acc.z = fmaf(o.z, a, acc.z);
+            acc.w = fmaf(o.w, a, acc.w);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        __nv_bfloat16 *o = p.out + w.token * p.o_ts + w.q_head * p.o_hs + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[e] * inv);
-        if (p.lse && lane == 0)
-            p.lse[(int64_t)w.token * p.heads + w.q_head] =
-                l == 0.f ? -CUDART_INF_F : (base + log2f(l)) * CUDART_LN2_F;
+        __nv_bfloat16 *o = p.out + w.token * p.o_ts + w.q_head * p.o_hs + 4 * e;
+        if (l == 0.f)
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        if (p.out_vec) {
+            *reinterpret_cast<uint2 *>(o) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        } else {
+            o[0] = lo.x, o[1] = lo.y, o[2] = hi.x, o[3] = hi.y;
+        }
+        if (p.lse && e == 0)
+            p.lse[(int64_t)w.token * p.heads + w.q_head] = l == 0.f ? -CUDART_INF_F : (base + log2f(l)) * CUDART_LN2_F;
     }
 }
 
@@ -789,7 +863,7 @@ lowm_status_t launch_attention(const CUtensorMap &map_k, const CUtensorMap &map_
         if (st != LOWM_OK)
             return st;
     }
-    return launch_pdl(join_parts_kernel<DIM>, dim3((unsigned)ctas), dim3(256), 0, stream, p, ctas);
+    return launch_pdl(join_parts_kernel<DIM>, dim3((unsigned)ctas, kJoinSplit), dim3(kJoinThreads), 0, stream, p, ctas);
 }
 
 }  // namespace
@@ -847,7 +921,7 @@ extern "C" lowm_status_t lowm_paged_attention(
     // Tile counts are 32-bit in the kernels.
     const int64_t capacity = std::min<int64_t>((int64_t)table_width * page_size, kMaxKeys);
     const int64_t q_tiles = (int64_t)q_tokens * (heads / kv_heads) / kTileRows + batch;
-    if ((double)q_tiles * kv_heads * (double)(capacity / kTileKeys + 2) > (double)INT_MAX)
+    if ((double)q_tiles * kv_heads * (double)(capacity / kTileKeys + 2 + kItemCost) > (double)INT_MAX)
         return LOWM_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     lowm_status_t st = host_check_device(&sms);
@@ -884,7 +958,7 @@ extern "C" lowm_status_t lowm_paged_attention(
     p.q_sign = scale < 0.f ? -1.f : 1.f;
     p.q_vec = is_aligned(q, 16) && !((q_token_stride | q_head_stride) & 7);
     p.out_vec = is_aligned(out, 16) && !((out_token_stride | out_head_stride) & 7);
-    p.parts = static_cast<float *>(workspace);
+    p.parts = static_cast<float4 *>(workspace);
     p.status = host_status_word();
     if (!p.status)
         return LOWM_ERR_CUDA;

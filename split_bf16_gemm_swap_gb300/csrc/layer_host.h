@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -26,6 +27,27 @@ inline bool is_aligned(const void *p, uintptr_t bytes)
 {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
+
+// The opt-in of one kernel to more than 48 KiB of dynamic shared memory, made
+// once per device.
+class SmemOptIn {
+public:
+    bool set(const void *kernel, int bytes)
+    {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+            return false;
+        if (done_[dev].load(std::memory_order_acquire))
+            return true;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+            return false;
+        done_[dev].store(true, std::memory_order_release);
+        return true;
+    }
+
+private:
+    std::atomic<bool> done_[64] = {};
+};
 
 // One launch on `stream`, allowed to start while its predecessor drains (every
 // kernel here begins with griddepcontrol.wait).

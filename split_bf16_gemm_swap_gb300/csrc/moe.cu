@@ -782,7 +782,8 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     if ((st = launch_pdl(router_kernel, dim3((unsigned)(clusters * kRouterCluster)), dim3(32 * kRouterWarps), 0, stream, p)) !=
         LOWM_OK)
         return st;
-    if (cudaFuncSetAttribute(experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
+    static SmemOptIn opt_in;
+    if (!opt_in.set(reinterpret_cast<const void *>(experts_kernel), kMaxSmem))
         return LOWM_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);

@@ -852,9 +852,8 @@ template <int DIM>
 lowm_status_t launch_attention(const CUtensorMap &map_k, const CUtensorMap &map_v, const AttnParams &p, int sms,
                                void *stream)
 {
-    // The opt-in to more than 48 KiB is per function and device; setting it again costs under a microsecond.
-    if (cudaFuncSetAttribute(paged_attention_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             AttnSmem<DIM>::kBytes) != cudaSuccess)
+    static SmemOptIn opt_in;
+    if (!opt_in.set(reinterpret_cast<const void *>(paged_attention_kernel<DIM>), AttnSmem<DIM>::kBytes))
         return LOWM_ERR_CUDA;
     const int ctas = std::min(2 * sms, kMaxAttnCtas);
     if (p.batch > 0) {

@@ -13,12 +13,13 @@ belong to that stream, and nothing is ordered against torch's current one.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
 
 from . import lowm
-from .lowm import LOWM_OK, LowmError, _ptr, _stream
+from .lowm import LOWM_OK, LowmError
 
 LOWM_MOE_SOFTMAX = 0
 LOWM_MOE_SIGMOID = 1
@@ -83,28 +84,49 @@ def lowm_moe_workspace(tokens: int, hidden: int, inner: int, experts: int, top_k
     return function("lowm_moe_workspace")(tokens, hidden, inner, experts, top_k)
 
 
-def _check(x, name: str, dtype, shape, device, contiguous: bool = False):
-    """One tensor argument: its type, shape, place and (at least) its innermost stride."""
+# Workspace sizes follow from the sizes alone.
+_attention_bytes = functools.lru_cache(maxsize=4096)(lowm_paged_attention_workspace)
+_moe_bytes = functools.lru_cache(maxsize=4096)(lowm_moe_workspace)
+
+
+# A call's checks are plain comparisons; what is wrong is worked out only when one fails.
+def _refuse(x, name: str, dtype, shape, device: int, contiguous: bool = False):
     if x.dtype is not dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, x.dtype))
     if x.shape != shape:
         raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(x.shape)))
-    if x.device != device:
-        raise ValueError("%s must be on %s, not %s" % (name, device, x.device))
-    if contiguous:
-        if not x.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-    elif shape and x.stride(-1) != 1 and shape[-1] > 1:
-        raise ValueError("the last dimension of %s must be contiguous" % name)
+    if not x.is_cuda or x.get_device() != device:
+        raise ValueError("%s must be on cuda:%d, not %s" % (name, device, x.device))
+    raise ValueError("%s must be contiguous" % name if contiguous else "the last dimension of %s must be contiguous" % name)
 
 
-def _cuda(x, name: str):
+def _rows(x, name: str, dtype, shape, device: int):
+    """Check a tensor whose last dimension must be contiguous; returns its strides."""
+    strides = x.stride()
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or (strides[-1] != 1 and shape[-1] > 1):
+        _refuse(x, name, dtype, shape, device)
+    return strides
+
+
+def _dense(x, name: str, dtype, shape, device: int):
+    """Check a contiguous tensor."""
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or not x.is_contiguous():
+        _refuse(x, name, dtype, shape, device, True)
+
+
+def _cuda(x, name: str) -> int:
     if not x.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    return x.device
+    return x.get_device()
 
 
-def _on(stream, device):
+# The raw handle of torch's current stream: torch.cuda.current_stream() makes a stream object first, which
+# takes longer than all checks of a call (2.9 us of a norm's 15.5 us on the host).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(stream, device: int):
     """The context in which a call with an explicit stream runs."""
     if not isinstance(stream, torch.cuda.Stream):
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -123,7 +145,7 @@ def residual_norm(residual, block=None, *, post_weight=None, gate=None, pre_weig
     [tokens, hidden] bf16; gate [hidden] or [tokens, hidden] bf16; weights
     [hidden] bf16.  post_weight None: the block's output is not normed;
     pre_weight None: 1.  Without a block only the norm is taken and ``new`` is
-    ``residual`` itself.  out_residual may be ``residual``.
+    ``residual`` itself.  out_residual may be ``residual``, out may be ``block``.
     """
     device = _cuda(residual, "residual")
     if stream is not None:
@@ -133,41 +155,41 @@ def residual_norm(residual, block=None, *, post_weight=None, gate=None, pre_weig
     shape = residual.shape
     if len(shape) != 2:
         raise ValueError("residual must be [tokens, hidden]")
-    f32 = residual.dtype is torch.float32
-    if not f32 and residual.dtype is not torch.bfloat16:
-        raise TypeError("residual must be bfloat16 or float32, not %s" % residual.dtype)
-    _check(residual, "residual", residual.dtype, shape, device)
+    bf16, dtype = torch.bfloat16, residual.dtype
+    if dtype is not bf16 and dtype is not torch.float32:
+        raise TypeError("residual must be bfloat16 or float32, not %s" % dtype)
+    residual_stride = _rows(residual, "residual", dtype, shape, device)[0]
     tokens, hidden = shape
-    bf16 = torch.bfloat16
     gate_stride = block_stride = out_residual_stride = 0
+    block_ptr = gate_ptr = post_ptr = pre_ptr = out_residual_ptr = None
     if block is not None:
-        _check(block, "block", bf16, shape, device)
-        block_stride = block.stride(0)
+        block_stride = _rows(block, "block", bf16, shape, device)[0]
+        block_ptr = block.data_ptr()
         if out_residual is None:
-            out_residual = torch.empty(shape, dtype=residual.dtype, device=device)
-        else:
-            _check(out_residual, "out_residual", residual.dtype, shape, device)
-        out_residual_stride = out_residual.stride(0) if tokens > 1 else hidden
+            out_residual = torch.empty(shape, dtype=dtype, device=residual.device)
+        out_residual_stride = _rows(out_residual, "out_residual", dtype, shape, device)[0] if tokens > 1 else hidden
+        out_residual_ptr = out_residual.data_ptr()
     elif post_weight is not None or gate is not None or out_residual is not None or scale != 1.0:
         raise ValueError("post_weight, gate, scale and out_residual need a block")
     if gate is not None:
         if gate.dim() == 1:
-            _check(gate, "gate", bf16, shape[1:], device)
+            _rows(gate, "gate", bf16, shape[1:], device)
         else:
-            _check(gate, "gate", bf16, shape, device)
-            gate_stride = gate.stride(0)
+            gate_stride = _rows(gate, "gate", bf16, shape, device)[0]
+        gate_ptr = gate.data_ptr()
     if post_weight is not None:
-        _check(post_weight, "post_weight", bf16, shape[1:], device)
+        _rows(post_weight, "post_weight", bf16, shape[1:], device)
+        post_ptr = post_weight.data_ptr()
     if pre_weight is not None:
-        _check(pre_weight, "pre_weight", bf16, shape[1:], device)
+        _rows(pre_weight, "pre_weight", bf16, shape[1:], device)
+        pre_ptr = pre_weight.data_ptr()
     if out is None:
-        out = torch.empty(shape, dtype=bf16, device=device)
-    else:
-        _check(out, "out", bf16, shape, device)
+        out = torch.empty(shape, dtype=bf16, device=residual.device)
+    out_stride = _rows(out, "out", bf16, shape, device)[0] if tokens > 1 else hidden
     s = function("lowm_residual_norm")(
-        residual.data_ptr(), f32, residual.stride(0), _ptr(block), block_stride, _ptr(post_weight), _ptr(gate),
-        gate_stride, _ptr(pre_weight), _ptr(out_residual), out_residual_stride, out.data_ptr(),
-        out.stride(0) if tokens > 1 else hidden, tokens, hidden, scale, eps, _stream(None))
+        residual.data_ptr(), dtype is not bf16, residual_stride, block_ptr, block_stride, post_ptr, gate_ptr,
+        gate_stride, pre_ptr, out_residual_ptr, out_residual_stride, out.data_ptr(), out_stride, tokens, hidden, scale,
+        eps, _current_stream(device))
     if s != LOWM_OK:
         raise LowmError(s, "lowm_residual_norm")
     return (residual if block is None else out_residual), out
@@ -189,45 +211,45 @@ def rope_append(q, k, v, cos_sin, positions, slots, k_cache, v_cache, *, section
         with _on(stream, device):
             return rope_append(q, k, v, cos_sin, positions, slots, k_cache, v_cache, sections=sections,
                                interleaved=interleaved, out=out)
-    bf16 = torch.bfloat16
+    bf16, i64 = torch.bfloat16, torch.int64
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4 or v_cache.dim() != 4 or cos_sin.dim() != 2:
         raise ValueError("q and k must be [tokens, heads, dim], the caches [num_pages, page_size, kv_heads, dim] "
                          "and cos_sin [table_rows, rotary]")
-    tokens, heads, dim = q.shape
+    q_shape = q.shape
+    tokens, heads, dim = q_shape
     kv_heads = k.shape[1]
-    table_rows, rotary = cos_sin.shape
+    table_shape = cos_sin.shape
+    table_rows, rotary = table_shape
     num_pages, page_size = k_cache.shape[:2]
-    _check(q, "q", bf16, q.shape, device)
-    _check(k, "k", bf16, (tokens, kv_heads, dim), device)
-    _check(v, "v", bf16, k.shape, device)
-    _check(cos_sin, "cos_sin", torch.float32, cos_sin.shape, device, True)
-    _check(slots, "slots", torch.int64, (tokens,), device, True)
-    _check(k_cache, "k_cache", bf16, (num_pages, page_size, kv_heads, dim), device)
-    _check(v_cache, "v_cache", bf16, k_cache.shape, device)
+    kv_shape, cache_shape = (tokens, kv_heads, dim), (num_pages, page_size, kv_heads, dim)
+    qs = _rows(q, "q", bf16, q_shape, device)
+    ks = _rows(k, "k", bf16, kv_shape, device)
+    vs = _rows(v, "v", bf16, kv_shape, device)
+    _dense(cos_sin, "cos_sin", torch.float32, table_shape, device)
+    _dense(slots, "slots", i64, (tokens,), device)
+    kc = _rows(k_cache, "k_cache", bf16, cache_shape, device)
+    vc = _rows(v_cache, "v_cache", bf16, cache_shape, device)
     if positions.dim() == 1:
         axes, positions_stride = 1, 0
-        _check(positions, "positions", torch.int64, (tokens,), device)
+        _dense(positions, "positions", i64, (tokens,), device)
         if sections is not None and tuple(sections) != (rotary // 2,):
             raise ValueError("sections of one axis must be (rotary / 2,)")
-        sections = (rotary // 2,)
+        section0, section1 = rotary // 2, 0
     else:
         axes = positions.shape[0]
-        _check(positions, "positions", torch.int64, (axes, tokens), device)
-        positions_stride = positions.stride(0)
+        positions_stride = _rows(positions, "positions", i64, (axes, tokens), device)[0]
         if sections is None or not 1 <= axes <= 3 or len(sections) != axes or sum(sections) * 2 != rotary:
             raise ValueError("positions [axes, tokens] need one to three axes and a section (rotary pairs) of each, "
                              "rotary / 2 in all")
+        section0, section1 = sections[0], sections[1] if axes > 1 else 0
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=bf16, device=device)
-    else:
-        _check(out, "out", bf16, q.shape, device)
-    kc, vc = k_cache.stride(), v_cache.stride()
-    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+        out = torch.empty(q_shape, dtype=bf16, device=q.device)
+    os = _rows(out, "out", bf16, q_shape, device)
     s = function("lowm_rope_append")(
-        _ptr(q), qs[0], qs[1], _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], _ptr(cos_sin), table_rows,
-        _ptr(positions), positions_stride, axes, sections[0], sections[1] if axes > 1 else 0, interleaved, _ptr(slots),
-        _ptr(out), os[0], os[1], _ptr(k_cache), kc[0], kc[1], kc[2], _ptr(v_cache), vc[0], vc[1], vc[2], num_pages,
-        page_size, tokens, heads, kv_heads, dim, rotary, _stream(None))
+        q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], cos_sin.data_ptr(),
+        table_rows, positions.data_ptr(), positions_stride, axes, section0, section1, interleaved, slots.data_ptr(),
+        out.data_ptr(), os[0], os[1], k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1], vc[2],
+        num_pages, page_size, tokens, heads, kv_heads, dim, rotary, _current_stream(device))
     if s != LOWM_OK:
         raise LowmError(s, "lowm_rope_append")
     return out
@@ -253,28 +275,29 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, *, scale=Non
     if q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError("q must be [q_tokens, heads, dim], the caches [num_pages, page_size, kv_heads, dim] and "
                          "page_table [batch, table_width]")
-    q_tokens, heads, dim = q.shape
-    num_pages, page_size, kv_heads, _ = k_cache.shape
-    batch, table_width = page_table.shape
-    _check(q, "q", bf16, q.shape, device)
-    _check(k_cache, "k_cache", bf16, (num_pages, page_size, kv_heads, dim), device)
-    _check(v_cache, "v_cache", bf16, k_cache.shape, device)
-    _check(page_table, "page_table", i32, page_table.shape, device)
-    _check(kv_lens, "kv_lens", i32, (batch,), device, True)
-    _check(cu_q, "cu_q", i32, (batch + 1,), device, True)
+    q_shape, cache_shape, table_shape = q.shape, k_cache.shape, page_table.shape
+    q_tokens, heads, dim = q_shape
+    num_pages, page_size, kv_heads, cache_dim = cache_shape
+    batch, table_width = table_shape
+    if cache_dim != dim:
+        raise ValueError("q and the caches must have one head size, not %d and %d" % (dim, cache_dim))
+    qs = _rows(q, "q", bf16, q_shape, device)
+    kc = _rows(k_cache, "k_cache", bf16, cache_shape, device)
+    vc = _rows(v_cache, "v_cache", bf16, cache_shape, device)
+    table_stride = _rows(page_table, "page_table", i32, table_shape, device)[0]
+    _dense(kv_lens, "kv_lens", i32, (batch,), device)
+    _dense(cu_q, "cu_q", i32, (batch + 1,), device)
     if out is None:
-        out = torch.empty((q_tokens, heads, dim), dtype=bf16, device=device)
-    else:
-        _check(out, "out", bf16, q.shape, device)
-    lse = torch.empty((q_tokens, heads), dtype=torch.float32, device=device) if return_lse else None
-    nbytes = lowm_paged_attention_workspace(batch, q_tokens, heads, kv_heads, dim)
-    work = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    kc, vc, qs, os = k_cache.stride(), v_cache.stride(), q.stride(), out.stride()
+        out = torch.empty(q_shape, dtype=bf16, device=q.device)
+    os = _rows(out, "out", bf16, q_shape, device)
+    lse = torch.empty((q_tokens, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    nbytes = _attention_bytes(batch, q_tokens, heads, kv_heads, dim)
+    work = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     s = function("lowm_paged_attention")(
-        _ptr(q), qs[0], qs[1], _ptr(k_cache), kc[0], kc[1], kc[2], _ptr(v_cache), vc[0], vc[1], vc[2], num_pages,
-        page_size, _ptr(page_table), page_table.stride(0), table_width, _ptr(kv_lens), _ptr(cu_q), _ptr(out), os[0],
-        os[1], _ptr(lse), batch, q_tokens, heads, kv_heads, dim, 1.0 / math.sqrt(dim) if scale is None else scale,
-        window, _ptr(work), nbytes, _stream(None))
+        q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1], vc[2],
+        num_pages, page_size, page_table.data_ptr(), table_stride, table_width, kv_lens.data_ptr(), cu_q.data_ptr(),
+        out.data_ptr(), os[0], os[1], None if lse is None else lse.data_ptr(), batch, q_tokens, heads, kv_heads, dim,
+        1.0 / math.sqrt(dim) if scale is None else scale, window, work.data_ptr(), nbytes, _current_stream(device))
     if s != LOWM_OK:
         raise LowmError(s, "lowm_paged_attention")
     return (out, lse) if return_lse else out
@@ -302,26 +325,29 @@ def moe(x, router_weight, gate_up, down, top_k: int, *, scoring: str = "softmax"
     bf16 = torch.bfloat16
     if x.dim() != 2 or router_weight.dim() != 2 or down.dim() != 3:
         raise ValueError("x must be [tokens, hidden], router_weight [experts, hidden] and down [experts, hidden, inner]")
-    if scoring not in _SCORING:
+    kind = _SCORING.get(scoring)
+    if kind is None:
         raise ValueError("scoring must be 'softmax' or 'sigmoid'")
-    tokens, hidden = x.shape
+    x_shape = x.shape
+    tokens, hidden = x_shape
     experts, _, inner = down.shape
-    _check(x, "x", bf16, x.shape, device)
-    _check(router_weight, "router_weight", bf16, (experts, hidden), device, True)
-    _check(gate_up, "gate_up", bf16, (experts, 2 * inner, hidden), device, True)
-    _check(down, "down", bf16, (experts, hidden, inner), device, True)
+    x_stride = _rows(x, "x", bf16, x_shape, device)[0] if tokens > 1 else hidden
+    _dense(router_weight, "router_weight", bf16, (experts, hidden), device)
+    _dense(gate_up, "gate_up", bf16, (experts, 2 * inner, hidden), device)
+    _dense(down, "down", bf16, (experts, hidden, inner), device)
+    bias_ptr = None
     if bias is not None:
-        _check(bias, "bias", torch.float32, (experts,), device, True)
+        _dense(bias, "bias", torch.float32, (experts,), device)
+        bias_ptr = bias.data_ptr()
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=bf16, device=device)
-    else:
-        _check(out, "out", bf16, x.shape, device)
-    nbytes = lowm_moe_workspace(tokens, hidden, inner, experts, top_k)
-    work = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        out = torch.empty(x_shape, dtype=bf16, device=x.device)
+    out_stride = _rows(out, "out", bf16, x_shape, device)[0] if tokens > 1 else hidden
+    nbytes = _moe_bytes(tokens, hidden, inner, experts, top_k)
+    work = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     s = function("lowm_moe")(
-        _ptr(x), x.stride(0) if tokens > 1 else hidden, _ptr(router_weight), _ptr(bias), _ptr(gate_up), _ptr(down), _ptr(out),
-        out.stride(0) if tokens > 1 else hidden, tokens, hidden, inner, experts, top_k, _SCORING[scoring],
-        renormalize, scale, _ptr(work), nbytes, _stream(None))
+        x.data_ptr(), x_stride, router_weight.data_ptr(), bias_ptr, gate_up.data_ptr(), down.data_ptr(),
+        out.data_ptr(), out_stride, tokens, hidden, inner, experts, top_k, kind, renormalize, scale, work.data_ptr(),
+        nbytes, _current_stream(device))
     if s != LOWM_OK:
         raise LowmError(s, "lowm_moe")
     return out

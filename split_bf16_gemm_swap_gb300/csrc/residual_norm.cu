@@ -5,8 +5,11 @@
 // requested before the first reduction, stays in registers as it came (two
 // bytes an element) and r' stays there in fp32, so each byte moves once and
 // the two reductions are the only waits.  At decode sizes the time is the
-// launch, one memory latency and the two reductions; at prompt sizes it is
-// the bandwidth of r, y, r' and n.
+// launch, one memory latency and the two reductions (4 x 4096: 2.4 us); at
+// prompt sizes it is the bandwidth of r, y, r' and n (8192 x 4096 bf16: 43.7 us,
+// 6.1 TB/s; with an fp32 residual and a gate per token 73.9 us, 6.4 TB/s).  Rows
+// that cannot be read in 16-byte pieces are bound by their single loads (3000 x
+// 2305: 23.8 us, 2.3 TB/s).
 #include <cuda_bf16.h>
 
 #include "layer_host.h"
@@ -21,14 +24,14 @@ struct NormParams {
     void *out_residual;
     __nv_bfloat16 *out;
     int64_t residual_stride, block_stride, gate_stride, out_residual_stride, out_stride;
-    int hidden;
+    int hidden, tokens;
     float scale, eps, inv_hidden;
 };
 
 // VEC elements of a row starting at i: one 16-byte access of bf16 (two of
 // fp32) when VEC is 8, one element when VEC is 1.
 template <int VEC>
-struct Pack {
+struct alignas(2 * VEC) Pack {
     __nv_bfloat16 v[VEC];
 };
 
@@ -56,16 +59,46 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16 *p, const float (&f)[VE
     }
 }
 
+// VEC elements of the residual stream as they lie in memory.
+template <int VEC, bool F32>
+struct Residual;
+
 template <int VEC>
-__device__ __forceinline__ void load_f32(const float *p, float (&o)[VEC])
-{
-    if constexpr (VEC == 8) {
-        *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(p);
-        *reinterpret_cast<float4 *>(o + 4) = *reinterpret_cast<const float4 *>(p + 4);
-    } else {
-        o[0] = *p;
+struct Residual<VEC, false> {
+    Pack<VEC> p;
+    __device__ void load(const void *base, int64_t at) { load_bf16(static_cast<const __nv_bfloat16 *>(base) + at, p); }
+    __device__ float value(int j) const { return __bfloat162float(p.v[j]); }
+    static __device__ void store(void *base, int64_t at, const float (&f)[VEC])
+    {
+        store_bf16(static_cast<__nv_bfloat16 *>(base) + at, f);
     }
-}
+};
+
+template <int VEC>
+struct Residual<VEC, true> {
+    float f[VEC];
+    __device__ void load(const void *base, int64_t at)
+    {
+        const float *src = static_cast<const float *>(base) + at;
+        if constexpr (VEC == 8) {
+            *reinterpret_cast<float4 *>(f) = reinterpret_cast<const float4 *>(src)[0];
+            *reinterpret_cast<float4 *>(f + 4) = reinterpret_cast<const float4 *>(src)[1];
+        } else {
+            f[0] = *src;
+        }
+    }
+    __device__ float value(int j) const { return f[j]; }
+    static __device__ void store(void *base, int64_t at, const float (&v)[VEC])
+    {
+        float *dst = static_cast<float *>(base) + at;
+        if constexpr (VEC == 8) {
+            reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *dst = v[0];
+        }
+    }
+};
 
 // Sum over the block: lanes by shuffles, then warps in index order through
 // shared memory; every thread gets the same value.
@@ -88,116 +121,122 @@ __device__ __forceinline__ float block_sum(float x, float *scratch)
 }
 
 // ELEMS elements a thread in pieces of VEC, piece n at (n * blockDim.x + thread) * VEC.
-template <int VEC, int ELEMS, bool F32>
-__global__ void __launch_bounds__(ELEMS == 8 ? 1024 : 512) residual_norm_kernel(const NormParams p)
+// A CTA walks rows blockIdx.x, blockIdx.x + gridDim.x, ...: the weights stay in
+// registers, and the next row is requested before this one's reductions.
+// (LOOP false: one row a CTA, without the registers of the second.)
+template <int VEC, int ELEMS, bool F32, bool LOOP>
+__global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
 {
     constexpr int NP = ELEMS / VEC;
-    __shared__ float scratch[2][32];
-    const int64_t t = blockIdx.x;
-    const __nv_bfloat16 one = __float2bfloat16_rn(1.f);
-
-    Pack<VEC> post[NP], pre[NP];
+    __shared__ float scratch[4][32];
+    const bool has_gate = p.gate != nullptr, has_block = p.block != nullptr, has_post = p.post != nullptr;
     const int step = (int)blockDim.x * VEC, first = (int)threadIdx.x * VEC;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
 
-    Pack<VEC> y[NP], g[NP];
-    float r[NP][VEC];
-    const bool has_gate = p.gate != nullptr, has_block = p.block != nullptr, has_post = p.post != nullptr,
-               has_pre = p.pre != nullptr;
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        const int i = n * step + first;
-        const bool in = i < p.hidden;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            y[n].v[j] = __float2bfloat16_rn(0.f);
-            g[n].v[j] = post[n].v[j] = pre[n].v[j] = one;
-            r[n][j] = 0.f;
-        }
-        if (!in)
-            continue;
-        if (has_block)
-            load_bf16(p.block + t * p.block_stride + i, y[n]);
-        if constexpr (F32) {
-            load_f32(static_cast<const float *>(p.residual) + t * p.residual_stride + i, r[n]);
-        } else {
-            Pack<VEC> q;
-            load_bf16(static_cast<const __nv_bfloat16 *>(p.residual) + t * p.residual_stride + i, q);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                r[n][j] = __bfloat162float(q.v[j]);
-        }
-        if (has_gate)
-            load_bf16(p.gate + t * p.gate_stride + i, g[n]);
-        if (has_post)
-            load_bf16(p.post + i, post[n]);
-        if (has_pre)
-            load_bf16(p.pre + i, pre[n]);
-    }
-
-    float inv = 1.f;
-    if (has_post) {
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < NP; ++n)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float v = __bfloat162float(y[n].v[j]);
-                sum = fmaf(v, v, sum);
-            }
-        inv = rsqrtf(fmaf(block_sum(sum, scratch[0]), p.inv_hidden, p.eps));
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int n = 0; n < NP; ++n)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            if (has_block) {
-                const float v = __bfloat162float(y[n].v[j]) * inv * __bfloat162float(post[n].v[j]);
-                r[n][j] = fmaf(r[n][j], p.scale, v * __bfloat162float(g[n].v[j]));
-            }
-            sum = fmaf(r[n][j], r[n][j], sum);
-        }
-    if (has_block) {
+    struct Values {
+        Pack<VEC> y[NP], g[NP];
+        Residual<VEC, F32> r[NP];
+    };
+    auto load = [&](int64_t t, Values &v) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             const int i = n * step + first;
             if (i >= p.hidden)
                 continue;
-            if constexpr (F32) {
-                float *o = static_cast<float *>(p.out_residual) + t * p.out_residual_stride + i;
-                if constexpr (VEC == 8) {
-                    reinterpret_cast<float4 *>(o)[0] = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
-                    reinterpret_cast<float4 *>(o)[1] = make_float4(r[n][4], r[n][5], r[n][6], r[n][7]);
-                } else {
-                    *o = r[n][0];
-                }
-            } else {
-                store_bf16(static_cast<__nv_bfloat16 *>(p.out_residual) + t * p.out_residual_stride + i, r[n]);
-            }
+            if (has_block)
+                load_bf16(p.block + t * p.block_stride + i, v.y[n]);
+            v.r[n].load(p.residual, t * p.residual_stride + i);
+            if (has_gate && p.gate_stride)
+                load_bf16(p.gate + t * p.gate_stride + i, v.g[n]);
         }
+    };
+    Values next;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        next.y[n] = {};
+        next.r[n] = {};
     }
-    inv = rsqrtf(fmaf(block_sum(sum, scratch[1]), p.inv_hidden, p.eps));
+    int64_t t = blockIdx.x;
+    load(t, next);
+    Pack<VEC> post[NP], pre[NP];
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
         const int i = n * step + first;
-        if (i >= p.hidden)
-            continue;
-        float o[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
-            o[j] = r[n][j] * inv * __bfloat162float(pre[n].v[j]);
-        store_bf16(p.out + t * p.out_stride + i, o);
+            post[n].v[j] = pre[n].v[j] = __float2bfloat16_rn(1.f);
+        if (i >= p.hidden)
+            continue;
+        if (has_post)
+            load_bf16(p.post + i, post[n]);
+        if (p.pre != nullptr)
+            load_bf16(p.pre + i, pre[n]);
+        if (has_gate && !p.gate_stride)
+            load_bf16(p.gate + i, next.g[n]);
+    }
+
+    for (int parity = 0;; t += gridDim.x, parity ^= 2) {
+        const Values cur = next;
+        if (LOOP && t + gridDim.x < p.tokens)
+            load(t + gridDim.x, next);
+        float inv = 1.f;
+        if (has_post) {
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float v = __bfloat162float(cur.y[n].v[j]);
+                    sum = fmaf(v, v, sum);
+                }
+            inv = rsqrtf(fmaf(block_sum(sum, scratch[parity]), p.inv_hidden, p.eps));
+        }
+        float r[NP][VEC];
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                r[n][j] = cur.r[n].value(j);
+                if (has_block) {
+                    float v = __bfloat162float(cur.y[n].v[j]) * inv * __bfloat162float(post[n].v[j]);
+                    if (has_gate)
+                        v *= __bfloat162float(cur.g[n].v[j]);
+                    r[n][j] = n * step + first < p.hidden ? fmaf(r[n][j], p.scale, v) : 0.f;
+                }
+                sum = fmaf(r[n][j], r[n][j], sum);
+            }
+        if (has_block) {
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const int i = n * step + first;
+                if (i < p.hidden)
+                    Residual<VEC, F32>::store(p.out_residual, t * p.out_residual_stride + i, r[n]);
+            }
+        }
+        inv = rsqrtf(fmaf(block_sum(sum, scratch[parity + 1]), p.inv_hidden, p.eps));
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int i = n * step + first;
+            if (i >= p.hidden)
+                continue;
+            float o[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                o[j] = r[n][j] * inv * __bfloat162float(pre[n].v[j]);
+            store_bf16(p.out + t * p.out_stride + i, o);
+        }
+        if (!LOOP || t + gridDim.x >= p.tokens)
+            return;
     }
 }
 
-template <int VEC, int ELEMS>
-lowm_status_t launch_norm(const NormParams &p, int tokens, bool f32, void *stream)
+template <int VEC, int ELEMS, bool LOOP>
+lowm_status_t launch_norm(const NormParams &p, bool f32, int grid, int threads, void *stream)
 {
-    const int threads = ((p.hidden + ELEMS - 1) / ELEMS + 31) / 32 * 32;
-    return launch_pdl(f32 ? residual_norm_kernel<VEC, ELEMS, true> : residual_norm_kernel<VEC, ELEMS, false>,
-                      dim3((unsigned)tokens), dim3((unsigned)threads), 0, stream, p);
+    return launch_pdl(f32 ? residual_norm_kernel<VEC, ELEMS, true, LOOP> : residual_norm_kernel<VEC, ELEMS, false, LOOP>,
+                      dim3((unsigned)grid), dim3((unsigned)threads), 0, stream, p);
 }
 
 bool range_overlaps(const void *a, int64_t a_stride, int64_t a_size, const void *b, int64_t b_stride, int64_t b_size,
@@ -240,7 +279,8 @@ extern "C" lowm_status_t lowm_residual_norm(const void *residual, int residual_f
         return LOWM_ERR_MISALIGNED;
     if (out_residual && range_overlaps(out_residual, out_residual_stride, size, out, out_stride, 2, tokens, hidden))
         return LOWM_ERR_INVALID_ARGUMENT;
-    const lowm_status_t st = host_check_device(nullptr);
+    int sms = 0;
+    const lowm_status_t st = host_check_device(&sms);
     if (st != LOWM_OK)
         return st;
 
@@ -258,6 +298,7 @@ extern "C" lowm_status_t lowm_residual_norm(const void *residual, int residual_f
     p.out_residual_stride = out_residual_stride;
     p.out_stride = out_stride;
     p.hidden = hidden;
+    p.tokens = tokens;
     p.scale = scale;
     p.eps = eps;
     p.inv_hidden = 1.f / (float)hidden;
@@ -267,9 +308,21 @@ extern "C" lowm_status_t lowm_residual_norm(const void *residual, int residual_f
                      !((block_stride | gate_stride | out_stride) & 7) && is_aligned(residual, 16) &&
                      is_aligned(block, 16) && is_aligned(post_weight, 16) && is_aligned(gate, 16) &&
                      is_aligned(pre_weight, 16) && is_aligned(out_residual, 16) && is_aligned(out, 16);
-    if (vec)
-        return hidden <= 8192 ? launch_norm<8, 8>(p, tokens, residual_f32 != 0, stream)
-                              : launch_norm<8, 32>(p, tokens, residual_f32 != 0, stream);
-    return hidden <= 8192 ? launch_norm<1, 8>(p, tokens, residual_f32 != 0, stream)
-                          : launch_norm<1, 32>(p, tokens, residual_f32 != 0, stream);
+    const bool f32 = residual_f32 != 0;
+    const int elems = hidden <= 8192 ? 8 : 16, threads = ((hidden + elems - 1) / elems + 31) / 32 * 32;
+    if (elems == 16)
+        return vec ? launch_norm<8, 16, false>(p, f32, tokens, threads, stream)
+                   : launch_norm<1, 16, false>(p, f32, tokens, threads, stream);
+    if (!vec)
+        return launch_norm<1, 8, false>(p, f32, tokens, threads, stream);
+    // Walking rows pays from two rounds of 1024 threads an SM on, for rows of 256
+    // threads and more (GB300, one row a CTA -> walking: 8192 x 4096 57.3 -> 43.7
+    // us, 2000 x 8000 40.3 -> 29.2; 8000 x 600, 96 threads, 10.2 -> 12.5; 600 x
+    // 4096, two rounds, 5.0 both).  768 or 1536 threads an SM lose at 8192 x 4096
+    // (54.9, 52.9 us).
+    const int resident = sms * (1024 / threads);
+    if (threads < 256 || tokens <= 2 * resident)
+        return launch_norm<8, 8, false>(p, f32, tokens, threads, stream);
+    const int rounds = (tokens + resident - 1) / resident;
+    return launch_norm<8, 8, true>(p, f32, (tokens + rounds - 1) / rounds, threads, stream);
 }

@@ -1,13 +1,17 @@
 // Rotary positions (one to three axes) for new queries and keys, and the
 // append of keys and values to the paged cache (lowm_layer.h).
 //
-// Element-wise work bound by its bytes (at few tokens by the launch and two
-// dependent reads, position then table).  One CTA owns one token; a thread
-// owns one group of pairs for several heads, so a token's cosines and sines
-// are read once per thread and serve every head it visits.
+// Element-wise work bound by its bytes (4096 tokens of 32 / 8 heads of 128: 21 us,
+// 4.9 TB/s; at few tokens by the launch and two dependent reads, position then
+// table: 4 tokens 2.6 us).  One CTA owns one token; a thread owns one group of
+// pairs for several heads, so a token's cosines and sines are read once per
+// thread and serve every head it visits.
 #include <cuda_bf16.h>
 
 #include <math_constants.h>
+
+#include <algorithm>
+#include <climits>
 
 #include "layer_host.h"
 #include "ptx.cuh"
@@ -32,6 +36,35 @@ struct RopeParams {
 // pairs in units of GROUP (and one last single element when dim is odd).
 // Rotary units are pairs (j, j + rotary / 2) or (2j, 2j + 1); the units
 // behind them copy 2 * GROUP neighbouring elements.
+template <int GROUP>
+struct alignas(GROUP == 8 ? 16 : 2) Run {
+    __nv_bfloat16 v[GROUP];
+};
+
+// Turns the pairs of one unit: runs a and b are the pairs' halves, or, with
+// INTERLEAVED and GROUP 8, pair i is elements 2i, 2i + 1 of a and b in a row.
+template <int GROUP, bool INTERLEAVED>
+__device__ __forceinline__ void turn(Run<GROUP> &a, Run<GROUP> &b, const float (&c)[GROUP], const float (&s)[GROUP])
+{
+    constexpr bool kMixed = INTERLEAVED && GROUP == 8;
+    const Run<GROUP> x = a, y = b;
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+        const bool lo = i < GROUP / 2;
+        const float u = __bfloat162float(kMixed ? (lo ? x : y).v[(2 * i) & (GROUP - 1)] : x.v[i]);
+        const float v = __bfloat162float(kMixed ? (lo ? x : y).v[(2 * i + 1) & (GROUP - 1)] : y.v[i]);
+        const __nv_bfloat16 nu = __float2bfloat16_rn(u * c[i] - v * s[i]);
+        const __nv_bfloat16 nv = __float2bfloat16_rn(u * s[i] + v * c[i]);
+        if constexpr (kMixed) {
+            (lo ? a : b).v[(2 * i) & (GROUP - 1)] = nu;
+            (lo ? a : b).v[(2 * i + 1) & (GROUP - 1)] = nv;
+        } else {
+            a.v[i] = nu;
+            b.v[i] = nv;
+        }
+    }
+}
+
 template <int GROUP, bool INTERLEAVED>
 __global__ void __launch_bounds__(512) rope_append_kernel(const RopeParams p)
 {
@@ -44,92 +77,80 @@ __global__ void __launch_bounds__(512) rope_append_kernel(const RopeParams p)
     if (lane0 >= lanes)
         return;
 
-    const int64_t slot = p.slots[t];
-    bool append = slot >= 0 && slot < p.capacity;
-    const int64_t page = append ? slot / p.page_size : 0, place = append ? slot % p.page_size : 0;
-    bool known = true;
-    const int64_t pos0 = p.positions[t];
-    const int64_t pos1 = p.axes > 1 ? p.positions[p.positions_stride + t] : pos0;
-    const int64_t pos2 = p.axes > 2 ? p.positions[2 * p.positions_stride + t] : pos0;
-    known = pos0 >= 0 && pos0 < p.table_rows && pos1 >= 0 && pos1 < p.table_rows && pos2 >= 0 && pos2 < p.table_rows;
-    append = append && known;
-
     const bool turns = u0 * GROUP < half;
-    float c[GROUP], s[GROUP];
-    if (turns) {
-#pragma unroll
-        for (int i = 0; i < GROUP; ++i) {
-            const int j = u0 * GROUP + i;
-            const int64_t pos = j < p.section0 ? pos0 : (j < p.section0 + p.section1 ? pos1 : pos2);
-            const float *row = p.cos_sin + pos * p.rotary;
-            c[i] = known ? row[j] : CUDART_NAN_F;
-            s[i] = known ? row[half + j] : CUDART_NAN_F;
-        }
-    }
     // Offsets of the unit's two runs of GROUP elements (the pair halves, or 2 * GROUP neighbours).
     const int e0 = turns && !INTERLEAVED ? u0 * GROUP : (turns ? 2 * u0 * GROUP : p.rotary + 2 * (u0 * GROUP - half));
     const int e1 = turns && !INTERLEAVED ? e0 + half : e0 + GROUP;
     const bool two = e1 < p.dim;                       // false only for the last element of an odd dim
+    const int64_t slot = p.slots[t];
+    const int64_t pos0 = p.positions[t];
+    const int64_t pos1 = p.axes > 1 ? p.positions[p.positions_stride + t] : pos0;
+    const int64_t pos2 = p.axes > 2 ? p.positions[2 * p.positions_stride + t] : pos0;
 
-    struct alignas(GROUP == 8 ? 16 : 2) Run {
-        __nv_bfloat16 v[GROUP];
-    };
-    const int rows = p.heads + 2 * p.kv_heads;
-    for (int h = lane0; h < rows; h += lanes) {
-        const __nv_bfloat16 *src;
-        __nv_bfloat16 *dst;
-        bool turn = turns;
-        if (h < p.heads) {
-            src = p.q + t * p.q_ts + h * p.q_hs;
-            dst = p.q_out + t * p.qo_ts + h * p.qo_hs;
-        } else if (!append) {
-            break;
-        } else if (h < p.heads + p.kv_heads) {
-            const int g = h - p.heads;
-            src = p.k + t * p.k_ts + g * p.k_hs;
-            dst = p.k_cache + page * p.kc_page + place * p.kc_place + g * p.kc_head;
-        } else {
-            const int g = h - p.heads - p.kv_heads;
-            src = p.v + t * p.v_ts + g * p.v_hs;
-            dst = p.v_cache + page * p.vc_page + place * p.vc_place + g * p.vc_head;
-            turn = false;
-        }
-        Run a, b;
-        a = *reinterpret_cast<const Run *>(src + e0);
+    // This thread's heads of one tensor, the next one requested before this one is turned and stored.
+    float c[GROUP], s[GROUP];
+    auto heads = [&](const __nv_bfloat16 *src, int64_t src_step, __nv_bfloat16 *dst, int64_t dst_step, int n, bool turned) {
+        if (lane0 >= n)
+            return;
+        src += lane0 * src_step;
+        dst += lane0 * dst_step;
+        src_step *= lanes;
+        dst_step *= lanes;
+        Run<GROUP> a = *reinterpret_cast<const Run<GROUP> *>(src + e0), b = a;
         if (two)
-            b = *reinterpret_cast<const Run *>(src + e1);
-        if (turn) {
-            Run oa, ob;
+            b = *reinterpret_cast<const Run<GROUP> *>(src + e1);
+        for (int h = lane0; h < n; h += lanes) {
+            Run<GROUP> na = a, nb = b;
+            if (h + lanes < n) {
+                src += src_step;
+                na = *reinterpret_cast<const Run<GROUP> *>(src + e0);
+                if (two)
+                    nb = *reinterpret_cast<const Run<GROUP> *>(src + e1);
+            }
+            if (turned)
+                turn<GROUP, INTERLEAVED>(a, b, c, s);
+            *reinterpret_cast<Run<GROUP> *>(dst + e0) = a;
+            if (two)
+                *reinterpret_cast<Run<GROUP> *>(dst + e1) = b;
+            dst += dst_step;
+            a = na;
+            b = nb;
+        }
+    };
+    const bool known = pos0 >= 0 && pos0 < p.table_rows && pos1 >= 0 && pos1 < p.table_rows && pos2 >= 0 && pos2 < p.table_rows;
+    const bool append = known && slot >= 0 && slot < p.capacity;
+    int64_t page = 0;
+    int place = 0;
+    if (append) {
+        page = slot < INT_MAX ? (int)slot / p.page_size : slot / p.page_size;
+        place = (int)(slot - page * p.page_size);
+    }
+    if (turns) {
+        const int j0 = u0 * GROUP, j1 = j0 + GROUP - 1, end1 = p.section0 + p.section1;
+        const float *rows[3] = {p.cos_sin + pos0 * p.rotary, p.cos_sin + pos1 * p.rotary, p.cos_sin + pos2 * p.rotary};
+        const int axis0 = j0 < p.section0 ? 0 : (j0 < end1 ? 1 : 2), axis1 = j1 < p.section0 ? 0 : (j1 < end1 ? 1 : 2);
+        if (GROUP == 8 && axis0 == axis1 && known) {   // one axis: 16 bytes at a time
+            const float *row = axis0 == 0 ? rows[0] : (axis0 == 1 ? rows[1] : rows[2]);
+#pragma unroll
+            for (int i = 0; i < GROUP; i += 4) {
+                *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(row + j0 + i);
+                *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(row + half + j0 + i);
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < GROUP; ++i) {
-                // interleaved: pair i is elements 2i, 2i + 1 of the 2 * GROUP neighbours
-                constexpr int kHalfGroup = GROUP / 2 > 0 ? GROUP / 2 : 1;
-                const bool lo = i < kHalfGroup || GROUP == 1;
-                float x, y;
-                if constexpr (INTERLEAVED && GROUP == 8) {
-                    x = __bfloat162float(lo ? a.v[(2 * i) & 7] : b.v[(2 * i) & 7]);
-                    y = __bfloat162float(lo ? a.v[(2 * i + 1) & 7] : b.v[(2 * i + 1) & 7]);
-                } else {
-                    x = __bfloat162float(a.v[i]);
-                    y = __bfloat162float(b.v[i]);
-                }
-                const __nv_bfloat16 nx = __float2bfloat16_rn(x * c[i] - y * s[i]);
-                const __nv_bfloat16 ny = __float2bfloat16_rn(x * s[i] + y * c[i]);
-                if constexpr (INTERLEAVED && GROUP == 8) {
-                    (lo ? oa : ob).v[(2 * i) & 7] = nx;
-                    (lo ? oa : ob).v[(2 * i + 1) & 7] = ny;
-                } else {
-                    oa.v[i] = nx;
-                    ob.v[i] = ny;
-                }
+                const int j = j0 + i;
+                const float *row = j < p.section0 ? rows[0] : (j < end1 ? rows[1] : rows[2]);
+                c[i] = known ? row[j] : CUDART_NAN_F;
+                s[i] = known ? row[half + j] : CUDART_NAN_F;
             }
-            a = oa;
-            b = ob;
         }
-        *reinterpret_cast<Run *>(dst + e0) = a;
-        if (two)
-            *reinterpret_cast<Run *>(dst + e1) = b;
     }
+    if (append) {
+        heads(p.v + t * p.v_ts, p.v_hs, p.v_cache + page * p.vc_page + place * p.vc_place, p.vc_head, p.kv_heads, false);
+        heads(p.k + t * p.k_ts, p.k_hs, p.k_cache + page * p.kc_page + place * p.kc_place, p.kc_head, p.kv_heads, turns);
+    }
+    heads(p.q + t * p.q_ts, p.q_hs, p.q_out + t * p.qo_ts, p.qo_hs, p.heads, turns);
 }
 
 }  // namespace
@@ -175,7 +196,8 @@ extern "C" lowm_status_t lowm_rope_append(
     }
     if (!is_aligned(cos_sin, 16) || !is_aligned(positions, 8) || !is_aligned(slots, 8))
         return LOWM_ERR_MISALIGNED;
-    const lowm_status_t st = host_check_device(nullptr);
+    int sms = 0;
+    const lowm_status_t st = host_check_device(&sms);
     if (st != LOWM_OK)
         return st;
 
@@ -217,10 +239,14 @@ extern "C" lowm_status_t lowm_rope_append(
 
     const bool vec = aligned && dim % 16 == 0 && rotary % 16 == 0 && (all & 7) == 0;
     const int units = vec ? dim / 16 : (dim + 1) / 2;
-    const int rows = heads + 2 * kv_heads;
-    int threads = units * rows;                        // a thread for every unit, at most 512
-    if (threads > 512)
-        threads = 512 / units * units;
+    int threads = units * std::max(heads, kv_heads);
+    // Few tokens: a thread for every unit, to be done soonest.  Many: fewer threads
+    // with more heads each, which read a token's cosines and sines fewer times
+    // (GB300, 32 / 8 heads of 128, 512 -> 128 -> 64 threads: 4 tokens 2.6, 2.8, 3.4
+    // us; 1000 tokens 7.7, 5.0, 5.7; 4096 tokens 39.9, 25.3, 21.1).
+    const int most = std::max(units, tokens >= 8 * sms ? 64 : (tokens >= 2 * sms ? 128 : 512));
+    if (threads > most)
+        threads = most / units * units;
     threads = (threads + 31) / 32 * 32;
     auto fn = vec ? (interleaved ? rope_append_kernel<8, true> : rope_append_kernel<8, false>)
                   : (interleaved ? rope_append_kernel<1, true> : rope_append_kernel<1, false>);

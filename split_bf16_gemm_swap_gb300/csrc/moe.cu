@@ -4,8 +4,8 @@
 // router_kernel.  A cluster of 8 CTAs owns 8 tokens, the N of an
 // mma.m16n8k16: each CTA takes every 8th tile of 16 experts, its 8 warps the
 // 32-wide K steps in turns (all loads of a warp in flight at once: the kernel
-// is one memory latency long), the logits meet in the workspace, and after the
-// cluster barrier each CTA scores one token and picks its top k.
+// is one memory latency long), the logits go to the shared memory of the CTA that
+// scores the token, and after the cluster barrier it picks the top k.
 //
 // experts_kernel.  The layer reads every reached expert's 3 * inner * hidden
 // weights once, at most 128 times as many operations: HBM bandwidth bounds it.
@@ -22,8 +22,14 @@
 //   down:  an item is 64 hidden elements of one expert; fp32 products per
 //          (token, choice) go to the workspace.
 //   sum:   the choices of a token, weighted, in order.
-// Two grid barriers (a cooperative launch) separate the parts.  The weight
-// stream does not stop at the first: only the loader waits for the activations.
+// Up and down items form one list that the CTAs take in turns, so that a CTA
+// short of an up item has a down item more.  A down item needs its expert's
+// activations only: a counter per expert says when its up items are done, and
+// the loader waits for it (a cooperative launch: the CTAs run together); the
+// weight stream runs on.  One grid barrier separates the sum.  (A barrier
+// between up and down left HBM idle for 15 us of 203 with 128 tokens; requests
+// of the next weights into L2 ahead of the ring cost more than they hid, 144 to
+// 154 us with 24 tokens.)
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -63,10 +69,10 @@ struct MoeParams {
     // workspace
     __nv_bfloat16 *act;  // [tokens * top_k, inner], by expert
     float *product;      // [tokens * top_k, hidden]
-    float *logits;       // [tokens, experts]
     float *weights;      // [tokens * top_k]
     int *ids;            // [tokens * top_k]
-    unsigned *arrived;   // [2] grid barriers, zeroed by the router
+    unsigned *arrived;   // the grid barrier, then [groups] epilogue warps done with an up item; zeroed by the router
+    int counters;        // words of it
     // experts_kernel
     int columns, stages; // most tokens of an item (a multiple of 8), ring depth
     bool up_blocked, down_blocked;   // K a multiple of 64: one copy brings kMoeBlocks blocks
@@ -91,19 +97,94 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A float into the shared memory of another CTA of the cluster (address from mapa_shared).
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// One warp scores a token from its logits and picks its top k; a lane holds
+// experts lane, lane + 32, ... (128 experts: 4 a lane, all in registers).
+template <int PER>
+__device__ __forceinline__ void score_token(const MoeParams &p, int t, const float *logits)
+{
+    const int lane = threadIdx.x & 31;
+    float prob[PER];
+    unsigned key[PER];
+    float m = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        prob[i] = e < p.experts ? logits[e] : -CUDART_INF_F;
+        m = fmaxf(m, prob[i]);
+    }
+    if (p.scoring == LOWM_MOE_SOFTMAX) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            prob[i] = lane + 32 * i < p.experts ? expf(prob[i] - m) : 0.f;
+            l += prob[i];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        prob[i] = p.scoring == LOWM_MOE_SOFTMAX ? prob[i] / l : 1.f / (1.f + expf(-prob[i]));
+        key[i] = e < p.experts ? ordered_bits(prob[i] + (p.bias ? p.bias[e] : 0.f)) : 0u;
+    }
+    float sum = 0.f, mine = 0.f;
+    int chosen = 0;
+    for (int s = 0; s < p.top_k; ++s) {
+        unsigned best = 0, at = kMaxExperts;
+        float w = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = lane + 32 * i;
+                w = prob[i];
+            }
+        const unsigned top = __reduce_max_sync(0xffffffffu, best);
+        const unsigned e = __reduce_min_sync(0xffffffffu, best == top ? at : (unsigned)kMaxExperts);
+        w = __shfl_sync(0xffffffffu, w, e & 31);
+        sum += w;
+        if (lane == s) {
+            mine = w;
+            chosen = (int)e;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (e == lane + 32 * i)
+                key[i] = 0;
+    }
+    if (lane < p.top_k) {
+        p.ids[t * p.top_k + lane] = chosen;
+        p.weights[t * p.top_k + lane] = mine * p.scale / (p.renormalize ? sum : 1.f);
+    }
+}
+
 constexpr int kRouterWarps = 8;
 
 __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kRouterWarps) router_kernel(const MoeParams p)
 {
     __shared__ float prob[kMaxExperts];
-    __shared__ unsigned key[kMaxExperts];
     __shared__ float part[kRouterWarps][16][8];
+    // Every CTA of the cluster runs before one writes into another's shared memory.
+    ptx::cluster_arrive_release();
+    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    ptx::cluster_wait_acquire();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)ptx::cluster_ctarank(), t0 = blockIdx.x / kRouterCluster * kRouterCluster;
     const int nt = min(kRouterCluster, p.tokens - t0);
-    if (blockIdx.x == 0 && threadIdx.x < 2)
-        p.arrived[threadIdx.x] = 0u;
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < p.counters; i += 32 * kRouterWarps)
+            p.arrived[i] = 0u;
 
     // A thread's 8 consecutive k of a 32-wide step serve both K16 products:
     // the same permutation of k on both operands leaves the sum alone.
@@ -114,16 +195,25 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kR
         const __nv_bfloat16 *w0 = p.router + (int64_t)min(e0, p.experts - 1) * p.hidden;
         const __nv_bfloat16 *w1 = p.router + (int64_t)min(e1, p.experts - 1) * p.hidden;
         float d[4] = {};
-#pragma unroll 8
-        for (int k = k0; k - (lane & 3) * 8 < p.hidden; k += 32 * kRouterWarps) {
-            uint4 a = make_uint4(0, 0, 0, 0), b = a, c = a;
-            if (k < p.hidden) {
-                a = *reinterpret_cast<const uint4 *>(w0 + k);
-                b = *reinterpret_cast<const uint4 *>(w1 + k);
-                c = *reinterpret_cast<const uint4 *>(x + k);
+        constexpr int kSteps = 16, kStride = 32 * kRouterWarps;   // 4096 elements in one go
+        for (int base = 0; base < p.hidden; base += kSteps * kStride) {
+            uint4 a[kSteps], b[kSteps], c[kSteps];
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int k = base + k0 + i * kStride;
+                a[i] = b[i] = c[i] = make_uint4(0, 0, 0, 0);
+                if (k < p.hidden) {
+                    a[i] = *reinterpret_cast<const uint4 *>(w0 + k);
+                    b[i] = *reinterpret_cast<const uint4 *>(w1 + k);
+                    c[i] = *reinterpret_cast<const uint4 *>(x + k);
+                }
             }
-            mma_16x8x16(d, a.x, b.x, a.y, b.y, c.x, c.y);
-            mma_16x8x16(d, a.z, b.z, a.w, b.w, c.z, c.w);
+            asm volatile("" ::: "memory");   // all loads before the first product
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                mma_16x8x16(d, a[i].x, b[i].x, a[i].y, b[i].y, c[i].x, c[i].y);
+                mma_16x8x16(d, a[i].z, b[i].z, a[i].w, b[i].w, c[i].z, c[i].w);
+            }
         }
         const int col = (lane & 3) * 2;
         part[warp][row][col] = d[0];
@@ -137,64 +227,19 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kR
 #pragma unroll
             for (int w = 0; w < kRouterWarps; ++w)
                 s += part[w][r][t];
-            if (t < nt && tile * 16 + r < p.experts)
-                p.logits[(int64_t)(t0 + t) * p.experts + tile * 16 + r] = s;
+            if (t < nt && tile * 16 + r < p.experts)   // to the CTA that scores the token
+                st_cluster(ptx::mapa_shared(ptx::smem_u32(&prob[tile * 16 + r]), (uint32_t)t), s);
         }
         __syncthreads();
     }
     ptx::cluster_arrive_release();
     ptx::cluster_wait_acquire();
-    ptx::griddep_launch_dependents();
     if (warp || rank >= nt)
-        return;                              // the next kernel starts when all of this one has ended
-    const int t = t0 + rank;
-    for (int e = lane; e < p.experts; e += 32)
-        prob[e] = p.logits[(int64_t)t * p.experts + e];
-    __syncwarp();
-    if (p.scoring == LOWM_MOE_SOFTMAX) {
-        float m = -CUDART_INF_F, l = 0.f;
-        for (int e = lane; e < p.experts; e += 32)
-            m = fmaxf(m, prob[e]);
-        for (int o = 16; o > 0; o >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        for (int e = lane; e < p.experts; e += 32) {
-            prob[e] = expf(prob[e] - m);
-            l += prob[e];
-        }
-        for (int o = 16; o > 0; o >>= 1)
-            l += __shfl_xor_sync(0xffffffffu, l, o);
-        for (int e = lane; e < p.experts; e += 32)
-            prob[e] /= l;
-    } else {
-        for (int e = lane; e < p.experts; e += 32)
-            prob[e] = 1.f / (1.f + expf(-prob[e]));
-    }
-    for (int e = lane; e < p.experts; e += 32)
-        key[e] = ordered_bits(prob[e] + (p.bias ? p.bias[e] : 0.f));
-    __syncwarp();
-    float sum = 0.f, mine = 0.f;
-    for (int s = 0; s < p.top_k; ++s) {
-        unsigned best = 0, at = kMaxExperts;
-        for (int i = lane; i < p.experts; i += 32)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        const unsigned top = __reduce_max_sync(0xffffffffu, best);
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? at : (unsigned)kMaxExperts);
-        const float w = prob[e];
-        sum += w;
-        if (lane == s)
-            mine = w;
-        __syncwarp();
-        if (lane == 0) {
-            key[e] = 0;
-            p.ids[t * p.top_k + s] = e;
-        }
-        __syncwarp();
-    }
-    if (lane < p.top_k)
-        p.weights[t * p.top_k + lane] = mine * p.scale / (p.renormalize ? sum : 1.f);
+        return;
+    if (p.experts <= 128)
+        score_token<4>(p, t0 + rank, prob);
+    else
+        score_token<kMaxExperts / 32>(p, t0 + rank, prob);
 }
 
 // ------------------------------------------------------------------ experts_kernel
@@ -301,7 +346,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar_acc + 8 * i, 2);
-            ptx::mbar_init(bar_free + 8 * i, kEpilogueThreads);
+            ptx::mbar_init(bar_free + 8 * i, 4);      // epilogue warps
         }
         ptx::mbar_init(bar_drain, 2);
         ptx::fence_mbarrier_init_cluster();
@@ -366,7 +411,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     __syncthreads();
 
     const int up_tiles = (p.inner + 31) / 32, down_tiles = (p.hidden + 63) / 64;
-    const int up_items = *num_groups * up_tiles, down_items = *num_groups * down_tiles;
+    const int up_items = *num_groups * up_tiles, items = up_items + *num_groups * down_tiles;
     const int up_blocks = (p.hidden + 63) / 64, down_blocks = (p.inner + 63) / 64;
     const int up_stages = (up_blocks + kMoeBlocks - 1) / kMoeBlocks, down_stages = (down_blocks + kMoeBlocks - 1) / kMoeBlocks;
 
@@ -400,12 +445,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         };
         if (lane == 0) {
             ptx::prefetch_tensormap(&map_down);
-            for (int item = blockIdx.x; item < up_items && ok; item += gridDim.x)
-                for (int k = 0; k < up_stages && ok; ++k)
-                    weights(true, item, k);
-            for (int item = blockIdx.x; item < down_items && ok; item += gridDim.x)
-                for (int k = 0; k < down_stages && ok; ++k)
-                    weights(false, item, k);
+            for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+                const bool up = item < up_items;
+                for (int k = 0; k < (up ? up_stages : down_stages) && ok; ++k)
+                    weights(up, up ? item : item - up_items, k);
+            }
             if (!ok)        // no copy may land after the CTA has ended (normally the MMAs have consumed all)
                 for (uint32_t j = i > (uint32_t)stages ? i - stages : 0; j < i; ++j)
                     (void)wait_short(bar_full + 8 * (j % stages), (j / stages) & 1);
@@ -466,23 +510,23 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             if (i > kLoaderLag)
                 hand(i - kLoaderLag);
         };
-        for (int item = blockIdx.x; item < up_items && ok; item += gridDim.x) {
-            const ushort4 g = group[item / up_tiles];
-            sources(true, g);
-            for (int k = 0; k < up_stages && ok; ++k)
-                rows(true, g, k);
-        }
-        hand(i);
-        if (ok && !wait_grid(&p.arrived[0], gridDim.x)) {
-            ok = false;
-            atomicOr(p.status, kErrMoeGrid);
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        for (int item = blockIdx.x; item < down_items && ok; item += gridDim.x) {
-            const ushort4 g = group[item / down_tiles];
-            sources(false, g);
-            for (int k = 0; k < down_stages && ok; ++k)
-                rows(false, g, k);
+        int ready = -1;                                          // the last group known to be complete
+        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+            const bool up = item < up_items;
+            const int n = up ? item / up_tiles : (item - up_items) / down_tiles;
+            const ushort4 g = group[n];
+            if (!up && n != ready) {
+                hand(i);                                         // no one waits for a stage while this warp does
+                if (!wait_grid(&p.arrived[1 + n], 4 * up_tiles)) {
+                    ok = false;
+                    atomicOr(p.status, kErrMoeGrid);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                ready = n;
+            }
+            sources(up, g);
+            for (int k = 0; k < (up ? up_stages : down_stages) && ok; ++k)
+                rows(up, g, k);
         }
         hand(i);
     } else if (warp == 1 || warp == 6) {
@@ -523,17 +567,18 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             }
             ++n;
         };
-        for (int item = blockIdx.x; item < up_items && ok; item += gridDim.x)
-            item_products(group[item / up_tiles], up_blocks, up_stages);
-        for (int item = blockIdx.x; item < down_items && ok; item += gridDim.x)
-            item_products(group[item / down_tiles], down_blocks, down_stages);
+        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+            const bool up = item < up_items;
+            item_products(group[up ? item / up_tiles : (item - up_items) / down_tiles], up ? up_blocks : down_blocks,
+                          up ? up_stages : down_stages);
+        }
         if (lane == 0)
             ptx::tcgen05_commit(bar_drain);
         __syncwarp();
         (void)wait_short(bar_drain, 0);   // nothing writes TMEM any more
     } else {
         // ------------------------------------------------------------ epilogue
-        const int quarter = warp & 3, etid = threadIdx.x - 64;
+        const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
         uint32_t n = 0;
         bool ok = true;
@@ -547,89 +592,81 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         };
         auto release = [&]() {
             ptx::tcgen05_fence_before_thread_sync();
-            ptx::mbar_arrive(bar_free + 8 * (n & 1));
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(bar_free + 8 * (n & 1));
             ++n;
         };
-        for (int item = blockIdx.x; item < up_items; item += gridDim.x) {
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+            const bool up = item < up_items;
+            const int at = up ? item : item - up_items, tiles = up ? up_tiles : down_tiles;
+            const ushort4 g = group[at / tiles];
             wait_acc();
             if (!ok)
                 break;
-            const ushort4 g = group[item / up_tiles];
-            // Lane l of quarter q: gate (l < 8) or up (8 <= l < 16) of element 32 tile + 8 q + l % 8.
-            const int e = item % up_tiles * 32 + quarter * 8 + lane;
+            // up: lane l of quarter q holds gate (l < 8) or up (8 <= l < 16) of element 32 tile + 8 q + l % 8.
+            const int row = up ? at % tiles * 32 + quarter * 8 + lane : at % tiles * kMoeRows + quarter * 16 + lane;
             for (int c = 0; c < g.z; c += 8) {
                 float v[8], u[8];
                 load_accumulator_pair<8>(lanes + (n & 1) * 2 * kMaxColumns + c, lanes + ((n & 1) * 2 + 1) * kMaxColumns + c, v, u);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float gate = v[j] + u[j], up = __shfl_down_sync(0xffffffffu, gate, 8);
-                    if (lane < 8 && c + j < g.z && e < p.inner)
-                        p.act[(int64_t)(g.y + c + j) * p.inner + e] =
-                            __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
+                    const float y = v[j] + u[j], z = __shfl_down_sync(0xffffffffu, y, 8);
+                    if (c + j >= g.z)
+                        continue;
+                    if (up) {
+                        if (lane < 8 && row < p.inner)
+                            p.act[(int64_t)(g.y + c + j) * p.inner + row] = __float2bfloat16_rn(y / (1.f + expf(-y)) * z);
+                    } else if (lane < 16 && row < p.hidden) {
+                        p.product[(int64_t)sorted[g.y + c + j] * p.hidden + row] = y;
+                    }
                 }
             }
             release();
-        }
-        // Barrier: every CTA's activations are in memory before any is read.
-        __threadfence();
-        ptx::named_barrier_sync(1, kEpilogueThreads);
-        if (etid == 0)
-            add_release(&p.arrived[0]);
-        for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
-            wait_acc();
-            if (!ok)
-                break;
-            const ushort4 g = group[item / down_tiles];
-            const int h = item % down_tiles * 64 + quarter * 16 + lane;
-            for (int c = 0; c < g.z; c += 8) {
-                float v[8], u[8];
-                load_accumulator_pair<8>(lanes + (n & 1) * 2 * kMaxColumns + c, lanes + ((n & 1) * 2 + 1) * kMaxColumns + c, v, u);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (lane < 16 && c + j < g.z && h < p.hidden)
-                        p.product[(int64_t)sorted[g.y + c + j] * p.hidden + h] = v[j] + u[j];
-            }
-            release();
-        }
-        __threadfence();
-        ptx::named_barrier_sync(1, kEpilogueThreads);
-        if (etid == 0) {
-            add_release(&p.arrived[1]);
-            if (!wait_grid(&p.arrived[1], gridDim.x))
-                atomicOr(p.status, kErrMoeGrid);
-        }
-        ptx::named_barrier_sync(1, kEpilogueThreads);
-        ptx::griddep_launch_dependents();
-        const int quads = p.hidden / 4, total = p.tokens * quads;
-        for (int c = blockIdx.x * kEpilogueThreads + etid; c < total; c += gridDim.x * kEpilogueThreads) {
-            const int t = c / quads, h = c % quads * 4;
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int s = 0; s < p.top_k; ++s) {
-                const float w = p.weights[t * p.top_k + s];
-                const float4 d = __ldcg(reinterpret_cast<const float4 *>(p.product + (int64_t)(t * p.top_k + s) * p.hidden + h));
-                y.x = fmaf(w, d.x, y.x);
-                y.y = fmaf(w, d.y, y.y);
-                y.z = fmaf(w, d.z, y.z);
-                y.w = fmaf(w, d.w, y.w);
-            }
-            __nv_bfloat16 *o = p.out + t * p.out_stride + h;
-            const __nv_bfloat162 a = __floats2bfloat162_rn(y.x, y.y), b = __floats2bfloat162_rn(y.z, y.w);
-            if (p.out_vec) {
-                uint2 u;
-                u.x = *reinterpret_cast<const uint32_t *>(&a);
-                u.y = *reinterpret_cast<const uint32_t *>(&b);
-                *reinterpret_cast<uint2 *>(o) = u;
-            } else {
-                o[0] = a.x, o[1] = a.y, o[2] = b.x, o[3] = b.y;
+            if (up) {                                            // after the release this warp's quarter of the item is in memory
+                __syncwarp();
+                if (lane == 0)
+                    add_release(&p.arrived[1 + at / tiles]);
             }
         }
     }
+    // Every product of this CTA is in memory; all threads add once every CTA's are.
     ptx::tcgen05_fence_before_thread_sync();
     __syncthreads();
+    if (threadIdx.x == 0) {
+        add_release(&p.arrived[0]);
+        if (!wait_grid(&p.arrived[0], gridDim.x))
+            atomicOr(p.status, kErrMoeGrid);
+    }
     if (warp == 1) {
         ptx::tcgen05_fence_after_thread_sync();
         ptx::tmem_dealloc(tmem, kColumnsTmem);
+    }
+    __syncthreads();
+    ptx::griddep_launch_dependents();
+    const int quads = p.hidden / 4, total = p.tokens * quads;
+    for (int c = blockIdx.x * kMoeThreads + threadIdx.x; c < total; c += gridDim.x * kMoeThreads) {
+        const int t = c / quads, h = c % quads * 4;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < p.top_k; ++s) {
+            const float w = p.weights[t * p.top_k + s];
+            const float4 d = __ldcg(reinterpret_cast<const float4 *>(p.product + (int64_t)(t * p.top_k + s) * p.hidden + h));
+            y.x = fmaf(w, d.x, y.x);
+            y.y = fmaf(w, d.y, y.y);
+            y.z = fmaf(w, d.z, y.z);
+            y.w = fmaf(w, d.w, y.w);
+        }
+        __nv_bfloat16 *o = p.out + t * p.out_stride + h;
+        const __nv_bfloat162 a = __floats2bfloat162_rn(y.x, y.y), b = __floats2bfloat162_rn(y.z, y.w);
+        if (p.out_vec) {
+            uint2 u;
+            u.x = *reinterpret_cast<const uint32_t *>(&a);
+            u.y = *reinterpret_cast<const uint32_t *>(&b);
+            *reinterpret_cast<uint2 *>(o) = u;
+        } else {
+            o[0] = a.x, o[1] = a.y, o[2] = b.x, o[3] = b.y;
+        }
     }
 }
 
@@ -654,7 +691,8 @@ int moe_columns(int tokens, int experts, int top_k)
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct MoeWorkspace {
-    size_t act, product, logits, weights, ids, arrived, bytes;
+    size_t act, product, weights, ids, arrived, bytes;
+    int counters;
 };
 
 MoeWorkspace moe_workspace(int tokens, int hidden, int inner, int experts, int top_k)
@@ -663,11 +701,11 @@ MoeWorkspace moe_workspace(int tokens, int hidden, int inner, int experts, int t
     MoeWorkspace w;
     w.act = 0;
     w.product = w.act + round16(pairs * inner * 2);
-    w.logits = w.product + round16(pairs * hidden * 4);
-    w.weights = w.logits + round16((size_t)std::max(tokens, 1) * experts * 4);
+    w.weights = w.product + round16(pairs * hidden * 4);
     w.ids = w.weights + round16(pairs * 4);
     w.arrived = w.ids + round16(pairs * 4);
-    w.bytes = w.arrived + 16;
+    w.counters = 1 + moe_max_groups(experts, (int)pairs, std::max(8, moe_columns(tokens, experts, top_k)));
+    w.bytes = w.arrived + round16((size_t)w.counters * 4);
     return w;
 }
 
@@ -739,10 +777,10 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     p.out_vec = is_aligned(out, 8) && (out_stride & 3) == 0;
     p.act = reinterpret_cast<__nv_bfloat16 *>(base + w.act);
     p.product = reinterpret_cast<float *>(base + w.product);
-    p.logits = reinterpret_cast<float *>(base + w.logits);
     p.weights = reinterpret_cast<float *>(base + w.weights);
     p.ids = reinterpret_cast<int *>(base + w.ids);
     p.arrived = reinterpret_cast<unsigned *>(base + w.arrived);
+    p.counters = w.counters;
     p.columns = moe_columns(tokens, experts, top_k);
     constexpr int kMaxSmem = 232448;
     for (p.stages = 8; p.stages > 2 && (int)moe_smem(experts, pairs, p.columns, p.stages).bytes > kMaxSmem; --p.stages) {
@@ -791,11 +829,13 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     cfg.blockDim = dim3(kMoeThreads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeCooperative;      // its CTAs wait for one another
-    attr.val.cooperative = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeCooperative;  // its CTAs wait for one another
+    attrs[0].val.cooperative = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, experts_kernel, map_up, map_down, p) == cudaSuccess ? LOWM_OK
                                                                                                         : LOWM_ERR_CUDA;
 }

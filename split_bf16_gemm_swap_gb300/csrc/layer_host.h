@@ -49,8 +49,11 @@ private:
     std::atomic<bool> done_[64] = {};
 };
 
-// One launch on `stream`, allowed to start while its predecessor drains (every
-// kernel here begins with griddepcontrol.wait).
+// One launch on `stream`, allowed to start while its predecessor drains.  Every
+// kernel here waits (griddepcontrol.wait) before it touches what another may
+// write, and lets its successor start only after that wait: what a kernel does
+// before its own wait then sees everything that came before its predecessor,
+// as the GEMM's launch flags for A and W promise.
 template <typename... KArgs, typename... Args>
 lowm_status_t launch_pdl(void (*fn)(KArgs...), dim3 grid, dim3 block, size_t smem, void *stream, Args... args)
 {

@@ -176,8 +176,8 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kR
     __shared__ float part[kRouterWarps][16][8];
     // Every CTA of the cluster runs before one writes into another's shared memory.
     ptx::cluster_arrive_release();
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     ptx::cluster_wait_acquire();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)ptx::cluster_ctarank(), t0 = blockIdx.x / kRouterCluster * kRouterCluster;

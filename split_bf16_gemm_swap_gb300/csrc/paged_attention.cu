@@ -750,7 +750,6 @@ constexpr int kJoinThreads = 256, kJoinSplit = 4;   // CTAs of an item: one SM r
 template <int DIM>
 __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const AttnParams p, int ctas)
 {
-    ptx::griddep_launch_dependents();
     const Line line = make_line(p);
     const int share = share_of(line.total, ctas);
     const bool inside = (int64_t)share * (blockIdx.x + 1) < line.total;
@@ -759,6 +758,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const AttnPara
     if (inside)
         it = locate(p, line, end - 1);
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     if (blockIdx.x == 0 && blockIdx.y == 0) { // rows of no sequence
         const int first = p.batch > 0 ? min(max(p.cu_q[0], 0), p.q_tokens) : p.q_tokens;
         const int last = p.batch > 0 ? min(max(p.cu_q[p.batch], 0), p.q_tokens) : p.q_tokens;

@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
     __shared__ float scratch[4][32];
     const bool has_gate = p.gate != nullptr, has_block = p.block != nullptr, has_post = p.post != nullptr;
     const int step = (int)blockDim.x * VEC, first = (int)threadIdx.x * VEC;
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
 
     struct Values {
         Pack<VEC> y[NP], g[NP];

@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(512) rope_append_kernel(const RopeParams p)
     const int units = (p.dim + 2 * GROUP - 1) / (2 * GROUP);
     const int u0 = threadIdx.x % units, lane0 = threadIdx.x / units, lanes = blockDim.x / units;
     const int half = p.rotary / 2;
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     if (lane0 >= lanes)
         return;
 

@@ -655,3 +655,28 @@ def test_graph_capture_of_a_chain():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_promised_inputs_behind_a_layer_operator():
+    # A GEMM that reads A before its dependency wait (both promises) behind an operator that does not write A,
+    # itself behind the kernel that does: the operator must not let the GEMM start while that kernel runs.
+    from split_bf16_gemm_swap_gb300 import LOWM_FLAG_A_BEFORE_PDL_WAIT, LOWM_FLAG_W_BEFORE_PDL_WAIT
+    flags = LOWM_FLAG_A_BEFORE_PDL_WAIT | LOWM_FLAG_W_BEFORE_PDL_WAIT
+    hidden, n = 4096, 256
+    w = rand(n, hidden, seed=1, std=hidden ** -0.5)
+    small, small_out = rand(4, 512, seed=2), torch.empty(4, 512, dtype=BF, device="cuda")
+    q, k, v, table, pos, kc, vc = small_rope()
+    slots, rows = torch.arange(6, device="cuda"), 4096
+    x, out = rand(rows, hidden, seed=3), torch.empty(rows, hidden, dtype=BF, device="cuda")
+    between = {
+        "norm": lambda: layer.residual_norm(small, out=small_out),
+        "rope": lambda: layer.rope_append(q, k, v, table, pos, slots, kc, vc, out=q),
+    }
+    for name, op in between.items():
+        for i in range(20):
+            out.zero_()
+            layer.residual_norm(x, out=out)                # long enough to be running still
+            op()
+            got = gemm(out[-8:], w, flags=flags)
+            torch.cuda.synchronize()
+            assert torch.equal(got, gemm(out[-8:], w)), (name, i)

@@ -43,10 +43,10 @@ constexpr int kMaxKeys = 1 << 30;            // of a sequence
 // The line counts time in tiles.  An item costs kItemCost tiles beside its own
 // (its queries' way in, its rows' way out); without it the CTAs with short
 // items ended 20 % after the others (chunks of 512 and fewer tokens of four
-// sequences: 112 us at 3, 107 at 7, 103 at 12; of 1537 tokens 260, 249, 253).
+// sequences: 97 us at 4, 91 at 7, 93 at 10; of 1537 tokens 234, 229, 232).
 constexpr int kItemCost = 7;
-constexpr int kMinShare = 4;                 // smaller shares cost more in the join than they save (6: 14.6 us for the
-                                             // short decodes that take 13.2)
+constexpr int kMinShare = 4;                 // smaller shares cost more in the join than they save, larger ones wait
+                                             // longer (short decodes: 14.3 us at 3, 13.8 at 4, 14.4 at 6)
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSColumns = 64;           // one S buffer; P takes its first 32 columns
 
@@ -73,7 +73,14 @@ struct AttnParams {
     bool q_vec, out_vec;                     // 16-byte rows
     float4 *parts;                           // [2 * ctas][dim / 4][slot_rows] sums, rows side by side as the lanes hold
                                              // them, then [2 * ctas][slot_rows] (max, sum) pairs
+    struct CutItem *cuts;                    // [ctas]
     unsigned int *status;
+};
+
+// The item that begins in a CTA's share and ends in a later one, for the join.
+struct CutItem {
+    int parts;                               // shares it lies in; 0: there is none
+    int q0, q_len, head, q_tile;
 };
 
 // ------------------------------------------------------------------ the line of tiles
@@ -408,14 +415,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
 
     ptx::griddep_wait();
-    // The join kernel may be scheduled from here on; what it reads before its
-    // own wait (cu_q, kv_lens) is final now.
     ptx::griddep_launch_dependents();
 
     const Line line = make_line(p);
     const int share = share_of(line.total, gridDim.x);
     const int begin = (int)min((int64_t)share * blockIdx.x, (int64_t)line.total), end = min(share, line.total - begin) + begin;
 
+    if (threadIdx.x == 0)
+        p.cuts[blockIdx.x].parts = 0;        // until this thread finds one
     Piece c;
     if (begin < end && first_piece(p, c, line, begin, end)) {
         const Item &it = c.it;
@@ -691,6 +698,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 // first products of the next run while its rows are written.
                 const bool whole = n == it.tiles;
                 const int64_t slot = 2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0);
+                if (r == 0 && from == 0 && !whole)
+                    p.cuts[blockIdx.x] = {(it.start + kItemCost + it.tiles - 1) / share - (int)blockIdx.x + 1, it.q0, it.q_len,
+                                          it.head, it.q_tile};
                 more = next_piece(p, c, end);
                 if (more)
                     load_q(it);
@@ -740,26 +750,21 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     }
 }
 
-// Joins the parts of the items that shares cut: CTA c owns the item whose
-// first tile is in share c and whose last is in a later one.  A thread owns
-// four elements of a row; neighbouring threads own neighbouring rows, as the
-// parts lie in memory.  Part i counts 2^(its maximum - the largest maximum),
-// and the parts add in the order of the keys.
-constexpr int kJoinThreads = 256, kJoinSplit = 4;   // CTAs of an item: one SM reads about 50 bytes a nanosecond
+// Joins the parts of the items that shares cut: CTA c owns the one that begins
+// in share c and ends in a later one.  A thread owns 16 elements of a row;
+// neighbouring threads own neighbouring rows, as the parts lie in memory.
+// Part i counts 2^(its maximum - the largest maximum), and the parts add in the
+// order of the keys.  The kernel is a few memory latencies long: the item, the
+// maxima, then all sums of up to four parts at once.
+constexpr int kJoinThreads = 256, kJoinSplit = 4;   // kJoinSplit CTAs an item: 128 rows of 128 are a task a thread
 
 template <int DIM>
 __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const AttnParams p, int ctas)
 {
-    const Line line = make_line(p);
-    const int share = share_of(line.total, ctas);
-    const bool inside = (int64_t)share * (blockIdx.x + 1) < line.total;
-    const int end = inside ? share * (int)(blockIdx.x + 1) : line.total;
-    Item it;
-    if (inside)
-        it = locate(p, line, end - 1);
+    constexpr int kGroups = DIM / 16;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0) { // rows of no sequence
+    if (blockIdx.x == 0 && blockIdx.y == 0) {   // rows of no sequence
         const int first = p.batch > 0 ? min(max(p.cu_q[0], 0), p.q_tokens) : p.q_tokens;
         const int last = p.batch > 0 ? min(max(p.cu_q[p.batch], 0), p.q_tokens) : p.q_tokens;
         for (int t = threadIdx.x >> 5; t < p.q_tokens; t += kJoinThreads / 32)
@@ -771,46 +776,62 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const AttnPara
                         p.lse[(int64_t)t * p.heads + h] = -CUDART_INF_F;
                 }
     }
-    const int first_tile = inside ? it.start + kItemCost : 0;
-    if (!inside || first_tile < end - share || first_tile >= end || first_tile + it.tiles <= end)
-        return;                              // no item is cut here, or it began in an earlier share
-    const int parts = (first_tile + it.tiles - 1) / share - (int)blockIdx.x + 1;
+    if (p.batch == 0)
+        return;
+    const CutItem cut = p.cuts[blockIdx.x];
+    const int parts = cut.parts;
+    if (parts == 0)
+        return;
     const float2 *ml = reinterpret_cast<const float2 *>(p.parts + 2 * (int64_t)ctas * p.slot_rows * (DIM / 4));
-    const int rows = min(kTileRows, it.q_len * p.group - it.q_tile * kTileRows);
+    const int rows = min(kTileRows, cut.q_len * p.group - cut.q_tile * kTileRows);
     auto slot = [&](int i) { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
-    for (int c = threadIdx.x + blockIdx.y * kJoinThreads; c < rows * (DIM / 4); c += kJoinSplit * kJoinThreads) {
-        const int r = c % rows, e = c / rows;
-        const Row w = row_of(p, it, r);
+    for (int c = threadIdx.x + blockIdx.y * kJoinThreads; c < rows * kGroups; c += kJoinSplit * kJoinThreads) {
+        const int r = c % rows, e = c / rows * 4;
+        const int row = cut.q_tile * kTileRows + r, t = cut.q0 + row / p.group, h = cut.head * p.group + row % p.group;
         float top = -CUDART_INF_F;
 #pragma unroll 4
         for (int i = 0; i < parts; ++i)
             top = fmaxf(top, ml[slot(i) * p.slot_rows + r].x);
         const float base = top == -CUDART_INF_F ? 0.f : top;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc[4] = {};
         float l = 0.f;
 #pragma unroll 4
         for (int i = 0; i < parts; ++i) {
             const float2 x = ml[slot(i) * p.slot_rows + r];
-            const float4 o = p.parts[(slot(i) * (DIM / 4) + e) * p.slot_rows + r];
+            const float4 *src = p.parts + (slot(i) * (DIM / 4) + e) * p.slot_rows + r;
             const float a = ex2(x.x - base);
             l = fmaf(x.y, a, l);
-            acc.x = fmaf(o.x, a, acc.x);
-            acc.y = fmaf(o.y, a, acc.y);
-            acc.z = fmaf(o.z, a, acc.z);
-            acc.w = fmaf(o.w, a, acc.w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 o = src[k * p.slot_rows];
+                acc[k].x = fmaf(o.x, a, acc[k].x);
+                acc[k].y = fmaf(o.y, a, acc[k].y);
+                acc[k].z = fmaf(o.z, a, acc[k].z);
+                acc[k].w = fmaf(o.w, a, acc[k].w);
+            }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        __nv_bfloat16 *o = p.out + w.token * p.o_ts + w.q_head * p.o_hs + 4 * e;
-        if (l == 0.f)
-            acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        alignas(16) __nv_bfloat162 v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (l == 0.f)
+                acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            v[2 * k] = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
+            v[2 * k + 1] = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
+        }
+        __nv_bfloat16 *o = p.out + t * p.o_ts + h * p.o_hs + 4 * e;
         if (p.out_vec) {
-            *reinterpret_cast<uint2 *>(o) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+            reinterpret_cast<uint4 *>(o)[0] = *reinterpret_cast<const uint4 *>(v);
+            reinterpret_cast<uint4 *>(o)[1] = *reinterpret_cast<const uint4 *>(v + 4);
         } else {
-            o[0] = lo.x, o[1] = lo.y, o[2] = hi.x, o[3] = hi.y;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                o[2 * k] = v[k].x;
+                o[2 * k + 1] = v[k].y;
+            }
         }
         if (p.lse && e == 0)
-            p.lse[(int64_t)w.token * p.heads + w.q_head] = l == 0.f ? -CUDART_INF_F : (base + log2f(l)) * CUDART_LN2_F;
+            p.lse[(int64_t)t * p.heads + h] = l == 0.f ? -CUDART_INF_F : (base + log2f(l)) * CUDART_LN2_F;
     }
 }
 
@@ -873,7 +894,8 @@ extern "C" size_t lowm_paged_attention_workspace(int batch, int q_tokens, int he
     using namespace lowm;
     if (!attention_shape_ok(batch, q_tokens, heads, kv_heads, dim))
         return 0;
-    return (size_t)2 * kMaxAttnCtas * slot_rows_of(q_tokens, heads, kv_heads) * (dim + 2) * sizeof(float);
+    return (size_t)2 * kMaxAttnCtas * slot_rows_of(q_tokens, heads, kv_heads) * (dim + 2) * sizeof(float) +
+           kMaxAttnCtas * sizeof(CutItem);
 }
 
 extern "C" lowm_status_t lowm_paged_attention(
@@ -958,6 +980,8 @@ extern "C" lowm_status_t lowm_paged_attention(
     p.q_vec = is_aligned(q, 16) && !((q_token_stride | q_head_stride) & 7);
     p.out_vec = is_aligned(out, 16) && !((out_token_stride | out_head_stride) & 7);
     p.parts = static_cast<float4 *>(workspace);
+    p.cuts = reinterpret_cast<CutItem *>(static_cast<uint8_t *>(workspace) +
+                                         (size_t)2 * kMaxAttnCtas * p.slot_rows * (dim + 2) * sizeof(float));
     p.status = host_status_word();
     if (!p.status)
         return LOWM_ERR_CUDA;

@@ -2,9 +2,9 @@
 // kernels.
 //
 // router_kernel.  A cluster of 8 CTAs owns 8 tokens, the N of an
-// mma.m16n8k16: each CTA takes every 8th tile of 16 experts, its 8 warps the
-// 32-wide K steps in turns (all loads of a warp in flight at once: the kernel
-// is one memory latency long), the logits go to the shared memory of the CTA that
+// mma.m16n8k16: each CTA takes every 8th tile of 16 experts (or a part of the K
+// steps of one), its 8 warps the 32-wide K steps in turns with eight steps'
+// loads in flight (the kernel is a few memory latencies long), the logits go to the shared memory of the CTA that
 // scores the token, and after the cluster barrier it picks the top k.
 //
 // experts_kernel.  The layer reads every reached expert's 3 * inner * hidden
@@ -103,10 +103,10 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// One warp scores a token from its logits and picks its top k; a lane holds
-// experts lane, lane + 32, ... (128 experts: 4 a lane, all in registers).
+// One warp scores a token from its logits (the sum of `parts` rows) and picks
+// its top k; a lane holds experts lane, lane + 32, ... (128 experts: 4 a lane).
 template <int PER>
-__device__ __forceinline__ void score_token(const MoeParams &p, int t, const float *logits)
+__device__ __forceinline__ void score_token(const MoeParams &p, int t, const float *logits, int parts)
 {
     const int lane = threadIdx.x & 31;
     float prob[PER];
@@ -116,6 +116,8 @@ __device__ __forceinline__ void score_token(const MoeParams &p, int t, const flo
     for (int i = 0; i < PER; ++i) {
         const int e = lane + 32 * i;
         prob[i] = e < p.experts ? logits[e] : -CUDART_INF_F;
+        for (int j = 1; j < parts && e < p.experts; ++j)
+            prob[i] += logits[j * p.experts + e];
         m = fmaxf(m, prob[i]);
     }
     if (p.scoring == LOWM_MOE_SOFTMAX) {
@@ -170,7 +172,7 @@ __device__ __forceinline__ void score_token(const MoeParams &p, int t, const flo
 
 constexpr int kRouterWarps = 8;
 
-__global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kRouterWarps) router_kernel(const MoeParams p)
+__global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kRouterWarps, 2) router_kernel(const MoeParams p)
 {
     __shared__ float prob[kMaxExperts];
     __shared__ float part[kRouterWarps][16][8];
@@ -190,17 +192,21 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kR
     // the same permutation of k on both operands leaves the sum alone.
     const int row = lane >> 2, k0 = warp * 32 + (lane & 3) * 8;
     const __nv_bfloat16 *x = p.x + (t0 + min(row, nt - 1)) * p.x_stride;
-    for (int tile = rank; tile * 16 < p.experts; tile += kRouterCluster) {
+    // Fewer than 8 tiles of experts: the spare CTAs take a part of the K steps each.
+    const int tiles = (p.experts + 15) / 16, parts = max(1, kRouterCluster / tiles);
+    const int share = rank / tiles, first = parts > 1 ? rank % tiles : rank;
+    for (int tile = parts > 1 && share >= parts ? tiles : first; tile < tiles; tile += kRouterCluster) {
         const int e0 = tile * 16 + row, e1 = e0 + 8;
         const __nv_bfloat16 *w0 = p.router + (int64_t)min(e0, p.experts - 1) * p.hidden;
         const __nv_bfloat16 *w1 = p.router + (int64_t)min(e1, p.experts - 1) * p.hidden;
         float d[4] = {};
-        constexpr int kSteps = 16, kStride = 32 * kRouterWarps;   // 4096 elements in one go
-        for (int base = 0; base < p.hidden; base += kSteps * kStride) {
+        constexpr int kSteps = 8;
+        const int stride = 32 * kRouterWarps * parts;
+        for (int base = parts > 1 ? share * 32 * kRouterWarps : 0; base < p.hidden; base += kSteps * stride) {
             uint4 a[kSteps], b[kSteps], c[kSteps];
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int k = base + k0 + i * kStride;
+                const int k = base + k0 + i * stride;
                 a[i] = b[i] = c[i] = make_uint4(0, 0, 0, 0);
                 if (k < p.hidden) {
                     a[i] = *reinterpret_cast<const uint4 *>(w0 + k);
@@ -228,7 +234,7 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kR
             for (int w = 0; w < kRouterWarps; ++w)
                 s += part[w][r][t];
             if (t < nt && tile * 16 + r < p.experts)   // to the CTA that scores the token
-                st_cluster(ptx::mapa_shared(ptx::smem_u32(&prob[tile * 16 + r]), (uint32_t)t), s);
+                st_cluster(ptx::mapa_shared(ptx::smem_u32(&prob[(parts > 1 ? share : 0) * p.experts + tile * 16 + r]), (uint32_t)t), s);
         }
         __syncthreads();
     }
@@ -237,9 +243,9 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(32 * kR
     if (warp || rank >= nt)
         return;
     if (p.experts <= 128)
-        score_token<4>(p, t0 + rank, prob);
+        score_token<4>(p, t0 + rank, prob, parts);
     else
-        score_token<kMaxExperts / 32>(p, t0 + rank, prob);
+        score_token<kMaxExperts / 32>(p, t0 + rank, prob, 1);
 }
 
 // ------------------------------------------------------------------ experts_kernel

@@ -46,7 +46,6 @@ constexpr int kRouterCluster = 8;            // CTAs (and tokens) of a router cl
 constexpr int kMoeThreads = 256;             // TMA warp 0, MMA warps 1 and 6, epilogue warps 2-5, loader warp 7
 constexpr int kMoeRows = 64;                 // weight rows of an item = the MMA's M
 constexpr int kMaxColumns = 64;              // tokens of an item; an expert with more gets several items
-constexpr int kMoeBlocks = 4;                // 64-wide K blocks per ring stage
 constexpr int kLoaderLag = 1;                // stages whose rows the loader has in flight behind the newest
 constexpr uint32_t kWBlockBytes = kMoeRows * 128u;
 
@@ -75,7 +74,6 @@ struct MoeParams {
     int counters;        // words of it
     // experts_kernel
     int columns, stages; // most tokens of an item (a multiple of 8), ring depth
-    bool up_blocked, down_blocked;   // K a multiple of 64: one copy brings kMoeBlocks blocks
     unsigned int *status;
 };
 
@@ -286,12 +284,13 @@ __host__ __device__ inline int moe_max_groups(int experts, int pairs, int column
     return (pairs < experts ? pairs : experts) + pairs / columns;
 }
 
-__host__ __device__ inline MoeSmem moe_smem(int experts, int pairs, int columns, int stages)
+// `blocks` 64-wide K blocks a stage.
+__host__ __device__ inline MoeSmem moe_smem(int experts, int pairs, int columns, int blocks, int stages)
 {
     MoeSmem L;
     L.w = 0;                                                   // [stages][blocks][64 rows][64]
-    L.stage_b = kMoeBlocks * columns * 128u;
-    L.b = stages * kMoeBlocks * kWBlockBytes;                  // [stages][blocks][columns][64]
+    L.stage_b = blocks * columns * 128u;
+    L.b = stages * blocks * kWBlockBytes;                  // [stages][blocks][columns][64]
     L.bars = L.b + stages * L.stage_b;                         // full, empty [stages]; accumulator full, free [2]; drain
     L.slot = L.bars + (2 * stages + 5) * 8;
     L.slot = (L.slot + 15) / 16 * 16;
@@ -328,15 +327,17 @@ __device__ __forceinline__ bool wait_grid(const unsigned *p, unsigned want)
     }
 }
 
+template <int BLOCKS>
 __global__ void __launch_bounds__(kMoeThreads, 1)
     experts_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_down,
+                   const __grid_constant__ CUtensorMap map_up_tail, const __grid_constant__ CUtensorMap map_down_tail,
                    const MoeParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = ptx::smem_u32(smem);
     const int pairs = p.tokens * p.top_k, stages = p.stages;
-    const MoeSmem L = moe_smem(p.experts, pairs, p.columns, stages);
+    const MoeSmem L = moe_smem(p.experts, pairs, p.columns, BLOCKS, stages);
     const uint32_t bar_full = sbase + L.bars, bar_empty = bar_full + 8 * stages, bar_acc = bar_empty + 8 * stages,
                    bar_free = bar_acc + 16, bar_drain = bar_free + 16;
     uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L.mask);
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const int up_tiles = (p.inner + 31) / 32, down_tiles = (p.hidden + 63) / 64;
     const int up_items = *num_groups * up_tiles, items = up_items + *num_groups * down_tiles;
     const int up_blocks = (p.hidden + 63) / 64, down_blocks = (p.inner + 63) / 64;
-    const int up_stages = (up_blocks + kMoeBlocks - 1) / kMoeBlocks, down_stages = (down_blocks + kMoeBlocks - 1) / kMoeBlocks;
+    const int up_stages = (up_blocks + BLOCKS - 1) / BLOCKS, down_stages = (down_blocks + BLOCKS - 1) / BLOCKS;
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA
@@ -434,23 +435,24 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 return;
             }
             const int tiles = up ? up_tiles : down_tiles, blocks = up ? up_blocks : down_blocks;
-            const bool blocked = up ? p.up_blocked : p.down_blocked;
-            const int e = group[item / tiles].x;
-            const int used = blocked ? 1 : min(kMoeBlocks, blocks - k * kMoeBlocks);
-            ptx::mbar_arrive_expect_tx(bar_full + 8 * s, (blocked ? kMoeBlocks : used) * kWBlockBytes);
+            const int e = group[item / tiles].x, width = up ? p.hidden : p.inner;
+            // One copy brings a stage's blocks (those past a K of whole blocks as zeros); the last stage
+            // of a K that ends inside a block comes block by block, so that the rest reads as zeros.
+            const bool whole = width % 64 == 0 || (k + 1) * BLOCKS * 64 <= width;
+            const int used = whole ? 1 : blocks - k * BLOCKS;
+            ptx::mbar_arrive_expect_tx(bar_full + 8 * s, (whole ? BLOCKS : used) * kWBlockBytes);
             const int row = up ? e * (p.inner / 4) + item % tiles * 4 : e * p.hidden + item % tiles * kMoeRows;
             for (int j = 0; j < used; ++j) {
-                const uint32_t dst = sbase + L.w + (s * kMoeBlocks + j) * kWBlockBytes;
-                const int kb = k * kMoeBlocks + j;
+                const uint32_t dst = sbase + L.w + (s * BLOCKS + j) * kWBlockBytes;
+                const int kb = k * BLOCKS + j, x = whole ? 0 : 64 * kb, z = whole ? kb : 0;
                 if (up)      // (k, 8 rows, gate / up, groups of 8 rows, k block)
-                    tma_load_5d(dst, &map_up, blocked ? 0 : 64 * kb, 0, 0, row, blocked ? kb : 0, bar_full + 8 * s, once);
+                    tma_load_5d(dst, whole ? &map_up : &map_up_tail, x, 0, 0, row, z, bar_full + 8 * s, once);
                 else         // (k, row, k block)
-                    ptx::tma_load_3d(dst, &map_down, blocked ? 0 : 64 * kb, row, blocked ? kb : 0, bar_full + 8 * s, once);
+                    ptx::tma_load_3d(dst, whole ? &map_down : &map_down_tail, x, row, z, bar_full + 8 * s, once);
             }
             ++i;
         };
         if (lane == 0) {
-            ptx::prefetch_tensormap(&map_down);
             for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
                 const bool up = item < up_items;
                 for (int k = 0; k < (up ? up_stages : down_stages) && ok; ++k)
@@ -500,12 +502,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 return;
-            const int width = up ? p.hidden : p.inner, at = k * (kMoeBlocks * 64) + chunk * 8;
+            const int width = up ? p.hidden : p.inner, at = k * (BLOCKS * 64) + chunk * 8;
             for (int r = sub; r < g.z; r += 4) {
                 const __nv_bfloat16 *src = source[r];
                 const uint32_t dst = sbase + L.b + s * L.stage_b + r * 128 + ((chunk ^ (r & 7)) << 4);
 #pragma unroll
-                for (int j = 0; j < kMoeBlocks; ++j) {
+                for (int j = 0; j < BLOCKS; ++j) {
                     const bool in = at + 64 * j < width;
                     cp_async_16(dst + j * p.columns * 128, src + (in ? at + 64 * j : 0), in ? 16 : 0);
                 }
@@ -557,9 +559,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 const int s = i % stages;
                 wait(bar_full + 8 * s, (i / stages) & 1, kErrMoeFull);
                 if (lane == 0 && ok) {
-                    const int used = min(kMoeBlocks, blocks - k * kMoeBlocks);
+                    const int used = min(BLOCKS, blocks - k * BLOCKS);
                     for (int j = 0; j < used; ++j) {
-                        const uint64_t a = make_sw128_kmajor_desc(sbase + L.w + (s * kMoeBlocks + j) * kWBlockBytes);
+                        const uint64_t a = make_sw128_kmajor_desc(sbase + L.w + (s * BLOCKS + j) * kWBlockBytes);
                         const uint64_t b = make_sw128_kmajor_desc(sbase + L.b + s * L.stage_b + j * p.columns * 128);
 #pragma unroll
                         for (uint32_t q = 0; q < 2; ++q)
@@ -694,6 +696,21 @@ int moe_columns(int tokens, int experts, int top_k)
     return std::min({kMaxColumns, (tokens + 7) / 8 * 8, (usual + 7) / 8 * 8});
 }
 
+constexpr int kMaxSmem = 232448;             // 227 KiB
+
+// K blocks a stage.  A copy has a fixed cost, so eight blocks (64 KiB of
+// weights) beat four where two such stages fit and K fills its last stage:
+// GB300, 4 -> 8 blocks: 128 tokens over 32 experts of 4096 x 1400 194 -> 185 us,
+// 8 tokens over 64 of 2048 x 768 48.0 -> 45.0; but 37 over 64 of 1544 x 920, whose
+// 25 and 15 blocks would leave a fifth of the stages empty, 56.1 -> 60.8.
+int moe_blocks(int hidden, int inner, int experts, int pairs, int columns)
+{
+    auto rounded = [](int n, int to) { return (n + to - 1) / to * to; };
+    const int up = rounded(hidden, 64) / 64, down = rounded(inner, 64) / 64;
+    const bool filled = 10 * (2 * rounded(up, 8) + rounded(down, 8)) <= 11 * (2 * up + down);
+    return filled && (int)moe_smem(experts, pairs, columns, 8, 2).bytes <= kMaxSmem ? 8 : 4;
+}
+
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct MoeWorkspace {
@@ -788,46 +805,49 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     p.arrived = reinterpret_cast<unsigned *>(base + w.arrived);
     p.counters = w.counters;
     p.columns = moe_columns(tokens, experts, top_k);
-    constexpr int kMaxSmem = 232448;
-    for (p.stages = 8; p.stages > 2 && (int)moe_smem(experts, pairs, p.columns, p.stages).bytes > kMaxSmem; --p.stages) {
+    const int blocks = moe_blocks(hidden, inner, experts, pairs, p.columns);
+    for (p.stages = 8; p.stages > 2 && (int)moe_smem(experts, pairs, p.columns, blocks, p.stages).bytes > kMaxSmem; --p.stages) {
     }
-    const int smem = (int)moe_smem(experts, pairs, p.columns, p.stages).bytes;
+    const int smem = (int)moe_smem(experts, pairs, p.columns, blocks, p.stages).bytes;
     if (smem > kMaxSmem)
         return LOWM_ERR_UNSUPPORTED_SHAPE;
-    p.up_blocked = hidden % 64 == 0;
-    p.down_blocked = inner % 64 == 0;
     p.status = host_status_word();
     if (!p.status)
         return LOWM_ERR_CUDA;
 
     // gate_up as (k, 8 rows, gate / up, groups of 8 rows, k block): a box is 4 groups of 8 gate and 8 up rows.
     // An expert is inner / 4 groups further; the extent ends with the last expert's up rows, so every
-    // element of a box lies inside the tensor or reads as zero.
-    CUtensorMap map_up, map_down;
+    // element of a box lies inside the tensor or reads as zero.  The tail maps see K as one dimension.
+    CUtensorMap maps[4];
     const cuuint64_t h2 = (cuuint64_t)hidden * 2, i2 = (cuuint64_t)inner * 2;
-    {
-        const cuuint64_t dims[5] = {p.up_blocked ? 64u : (cuuint64_t)hidden, 8, 2,
-                                    (cuuint64_t)experts * (inner / 4) - inner / 8, p.up_blocked ? hidden / 64u : 1u};
-        const cuuint64_t strides[4] = {h2, h2 * inner, h2 * 8, 128};
-        const cuuint32_t box[5] = {64, 8, 2, 4, p.up_blocked ? (cuuint32_t)kMoeBlocks : 1u};
-        if ((st = encode_bf16(&map_up, gate_up, 5, dims, strides, box)) != LOWM_OK)
+    const cuuint64_t groups = (cuuint64_t)experts * (inner / 4) - inner / 8, rows = (cuuint64_t)experts * hidden;
+    for (int tail = 0; tail < 2; ++tail) {
+        const cuuint64_t up_dims[5] = {tail ? (cuuint64_t)hidden : 64u, 8, 2, groups,
+                                       tail ? 1u : (cuuint64_t)std::max(1, hidden / 64)};
+        const cuuint64_t up_strides[4] = {h2, h2 * inner, h2 * 8, 128};
+        const cuuint32_t deep = tail ? 1u : (cuuint32_t)blocks, up_box[5] = {64, 8, 2, 4, deep};
+        const cuuint64_t down_dims[3] = {tail ? (cuuint64_t)inner : 64u, rows, tail ? 1u : (cuuint64_t)std::max(1, inner / 64)};
+        const cuuint64_t down_strides[2] = {i2, 128};
+        const cuuint32_t down_box[3] = {64, (cuuint32_t)kMoeRows, deep};
+        // A K of whole blocks has no tail, a K below one block nothing else.
+        const bool up_used = tail ? hidden % 64 != 0 : hidden >= 64, down_used = tail ? inner % 64 != 0 : inner >= 64;
+        if (up_used && (st = encode_bf16(&maps[2 * tail], gate_up, 5, up_dims, up_strides, up_box)) != LOWM_OK)
             return st;
-    }
-    {
-        const cuuint64_t dims[3] = {p.down_blocked ? 64u : (cuuint64_t)inner, (cuuint64_t)experts * hidden,
-                                    p.down_blocked ? inner / 64u : 1u};
-        const cuuint64_t strides[2] = {i2, 128};
-        const cuuint32_t box[3] = {64, (cuuint32_t)kMoeRows, p.down_blocked ? (cuuint32_t)kMoeBlocks : 1u};
-        if ((st = encode_bf16(&map_down, down, 3, dims, strides, box)) != LOWM_OK)
+        if (down_used && (st = encode_bf16(&maps[2 * tail + 1], down, 3, down_dims, down_strides, down_box)) != LOWM_OK)
             return st;
+        if (!up_used)
+            std::memset(&maps[2 * tail], 0, sizeof maps[0]);
+        if (!down_used)
+            std::memset(&maps[2 * tail + 1], 0, sizeof maps[0]);
     }
 
     const int clusters = (tokens + kRouterCluster - 1) / kRouterCluster;
     if ((st = launch_pdl(router_kernel, dim3((unsigned)(clusters * kRouterCluster)), dim3(32 * kRouterWarps), 0, stream, p)) !=
         LOWM_OK)
         return st;
-    static SmemOptIn opt_in;
-    if (!opt_in.set(reinterpret_cast<const void *>(experts_kernel), kMaxSmem))
+    static SmemOptIn opt_in[2];
+    auto *kernel = blocks == 8 ? experts_kernel<8> : experts_kernel<4>;
+    if (!opt_in[blocks == 8].set(reinterpret_cast<const void *>(kernel), kMaxSmem))
         return LOWM_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
@@ -842,6 +862,6 @@ extern "C" lowm_status_t lowm_moe(const void *x, int64_t x_stride, const void *r
     attrs[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, experts_kernel, map_up, map_down, p) == cudaSuccess ? LOWM_OK
+    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], p) == cudaSuccess ? LOWM_OK
                                                                                                         : LOWM_ERR_CUDA;
 }

@@ -21,6 +21,13 @@
 // maximum has grown by 2^8 (the weights stay below 256, and bf16 and fp32 are
 // relative), so most tiles leave O alone.
 //
+// What bounds it.  Decode: the cache's bandwidth (24 sequences of up to 16384
+// keys, 1.0 GB: 159 us, 6.3 TB/s).  Chunks: the MMA issue and the softmax of two
+// CTAs an SM (2048 tokens over 16384 keys: 401 us, 1.29 PFLOP/s; the scores' 8
+// MMAs of N 64 take ~55 cycles each where the arithmetic needs 32, but 128 keys
+// at once do not fit the TMEM beside O in two CTAs).  Few keys: the chain of
+// launch, schedule, first tile and join (4 x 1000 keys: 13.6 us).
+//
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.
 #include <cuda_bf16.h>
@@ -252,6 +259,40 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two fp32 values in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y)
+{
+    return pack2(__uint_as_float(x), __uint_as_float(y));
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar)
@@ -652,21 +693,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                             }
                         }
                         const float ms = m == -CUDART_INF_F ? 0.f : m * p.scale_log2;
-                        float sum0 = 0.f, sum1 = 0.f;
+                        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), shift2 = pack2(-ms, -ms);
+                        uint64_t sum0 = 0, sum1 = 0;
                         uint32_t pk[32];
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            const float a = ex2(fmaf(__uint_as_float(s0[k]), p.scale_log2, -ms));
-                            const float b = ex2(fmaf(__uint_as_float(s0[k + 1]), p.scale_log2, -ms));
-                            const float c = ex2(fmaf(__uint_as_float(s1[k]), p.scale_log2, -ms));
-                            const float d = ex2(fmaf(__uint_as_float(s1[k + 1]), p.scale_log2, -ms));
-                            sum0 += a + b;
-                            sum1 += c + d;
+                            const float2 x = unpack2(fma2(pack2(s0[k], s0[k + 1]), scale2, shift2));
+                            const float2 y = unpack2(fma2(pack2(s1[k], s1[k + 1]), scale2, shift2));
+                            const float a = ex2(x.x), b = ex2(x.y), c = ex2(y.x), d = ex2(y.y);
+                            sum0 = add2(sum0, pack2(a, b));
+                            sum1 = add2(sum1, pack2(c, d));
                             const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b), cd = __floats2bfloat162_rn(c, d);
                             pk[k / 2] = *reinterpret_cast<const uint32_t *>(&ab);
                             pk[16 + k / 2] = *reinterpret_cast<const uint32_t *>(&cd);
                         }
-                        l += sum0 + sum1;
+                        const float2 sums = unpack2(add2(sum0, sum1));
+                        l += sums.x + sums.y;
                         tmem_st_x32(s_addr, pk);
                         ptx::tmem_wait_st();
                     }

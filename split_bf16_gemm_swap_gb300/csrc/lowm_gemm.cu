@@ -855,7 +855,7 @@ const char *lowm_status_string(lowm_status_t s)
     switch (s) {
     case LOWM_OK: return "ok";
     case LOWM_ERR_INVALID_ARGUMENT: return "invalid argument";
-    case LOWM_ERR_UNSUPPORTED_SHAPE: return "unsupported shape (need 1<=M<=128, N>=1, K a multiple of 64 with K/64>=split_k, and a split-K mailbox that fits)";
+    case LOWM_ERR_UNSUPPORTED_SHAPE: return "unsupported shape (GEMM: need 1<=M<=128, N>=1, K a multiple of 64 with K/64>=split_k, and a split-K mailbox that fits; layer operators: see lowm_layer.h)";
     case LOWM_ERR_MISALIGNED: return "pointer not 16-byte aligned";
     case LOWM_ERR_UNSUPPORTED_ARCH: return "current device is not sm_103 (GB300)";
     case LOWM_ERR_CUDA: return "CUDA runtime error";

@@ -108,6 +108,12 @@ def _rows(x, name: str, dtype, shape, device: int):
     return strides
 
 
+def _row_stride(x, name: str, dtype, shape, device: int) -> int:
+    """Check a matrix; returns its row stride (of a single row, whose stride may be anything: its width)."""
+    stride = _rows(x, name, dtype, shape, device)[0]
+    return stride if shape[0] > 1 else shape[1]
+
+
 def _dense(x, name: str, dtype, shape, device: int):
     """Check a contiguous tensor."""
     if x.dtype is not dtype or x.shape != shape or x.get_device() != device or not x.is_contiguous():
@@ -167,7 +173,7 @@ def residual_norm(residual, block=None, *, post_weight=None, gate=None, pre_weig
         block_ptr = block.data_ptr()
         if out_residual is None:
             out_residual = torch.empty(shape, dtype=dtype, device=residual.device)
-        out_residual_stride = _rows(out_residual, "out_residual", dtype, shape, device)[0] if tokens > 1 else hidden
+        out_residual_stride = _row_stride(out_residual, "out_residual", dtype, shape, device)
         out_residual_ptr = out_residual.data_ptr()
     elif post_weight is not None or gate is not None or out_residual is not None or scale != 1.0:
         raise ValueError("post_weight, gate, scale and out_residual need a block")
@@ -185,7 +191,7 @@ def residual_norm(residual, block=None, *, post_weight=None, gate=None, pre_weig
         pre_ptr = pre_weight.data_ptr()
     if out is None:
         out = torch.empty(shape, dtype=bf16, device=residual.device)
-    out_stride = _rows(out, "out", bf16, shape, device)[0] if tokens > 1 else hidden
+    out_stride = _row_stride(out, "out", bf16, shape, device)
     s = function("lowm_residual_norm")(
         residual.data_ptr(), dtype is not bf16, residual_stride, block_ptr, block_stride, post_ptr, gate_ptr,
         gate_stride, pre_ptr, out_residual_ptr, out_residual_stride, out.data_ptr(), out_stride, tokens, hidden, scale,
@@ -331,7 +337,7 @@ def moe(x, router_weight, gate_up, down, top_k: int, *, scoring: str = "softmax"
     x_shape = x.shape
     tokens, hidden = x_shape
     experts, _, inner = down.shape
-    x_stride = _rows(x, "x", bf16, x_shape, device)[0] if tokens > 1 else hidden
+    x_stride = _row_stride(x, "x", bf16, x_shape, device)
     _dense(router_weight, "router_weight", bf16, (experts, hidden), device)
     _dense(gate_up, "gate_up", bf16, (experts, 2 * inner, hidden), device)
     _dense(down, "down", bf16, (experts, hidden, inner), device)
@@ -341,7 +347,7 @@ def moe(x, router_weight, gate_up, down, top_k: int, *, scoring: str = "softmax"
         bias_ptr = bias.data_ptr()
     if out is None:
         out = torch.empty(x_shape, dtype=bf16, device=x.device)
-    out_stride = _rows(out, "out", bf16, x_shape, device)[0] if tokens > 1 else hidden
+    out_stride = _row_stride(out, "out", bf16, x_shape, device)
     nbytes = _moe_bytes(tokens, hidden, inner, experts, top_k)
     work = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     s = function("lowm_moe")(

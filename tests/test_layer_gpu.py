@@ -680,3 +680,21 @@ def test_promised_inputs_behind_a_layer_operator():
             got = gemm(out[-8:], w, flags=flags)
             torch.cuda.synchronize()
             assert torch.equal(got, gemm(out[-8:], w)), (name, i)
+
+
+def test_single_token_outputs_are_checked():
+    x, router, w1, w2 = moe_inputs(1, 64, 32, 8)
+    small, wrong = torch.empty(1, 32, dtype=BF, device="cuda"), torch.empty(1, 64, dtype=torch.float32, device="cuda")
+    for bad in (small, wrong, torch.empty(1, 64, dtype=BF)):
+        with pytest.raises((ValueError, TypeError)):
+            layer.moe(x, router, w1, w2, 2, out=bad)
+        with pytest.raises((ValueError, TypeError)):
+            layer.residual_norm(x, x, out=bad)
+        with pytest.raises((ValueError, TypeError)):
+            layer.residual_norm(x, x, out_residual=bad)
+    with pytest.raises(ValueError):
+        layer.moe(x[:, ::2], router[:, :32].contiguous(), w1[:, :, :32].contiguous(), w2[:, :32].contiguous(), 2)
+    odd = torch.empty(7 * 64, dtype=BF, device="cuda").as_strided((1, 64), (3, 1))     # a single row's stride may be anything
+    assert torch.equal(layer.moe(x, router, w1, w2, 2, out=odd), layer.moe(x, router, w1, w2, 2))
+    new, out = layer.residual_norm(x, x, out=odd)
+    assert torch.equal(out, layer.residual_norm(x, x)[1])

@@ -114,10 +114,10 @@ lowm_status_t lowm_rope_append(const void *q, int64_t q_token_stride, int64_t q_
  *                 multiple of kv_heads with heads / kv_heads <= 128; batch >= 0
  *   workspace     lowm_paged_attention_workspace(...) bytes, 16-byte aligned;
  *                 contents need not survive between calls
- * What a page holds past a sequence's length does not matter, NaN included.
- * A non-finite value inside a sequence reaches the rows that see its token, and
- * may reach rows of the same sequence that do not.  The result is
- * deterministic.
+ * What a page holds past a sequence's length or before its window does not
+ * matter, NaN included, and a value of a token that is not finite reaches the
+ * rows that see the token and no others (in a chunk of several tokens, at the
+ * price of walking those rows' keys one by one).  The result is deterministic.
  */
 lowm_status_t lowm_paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                                    const void *k_cache, int64_t k_page_stride, int64_t k_place_stride,

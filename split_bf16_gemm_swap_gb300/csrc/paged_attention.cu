@@ -68,10 +68,11 @@ enum : uint32_t {
 };
 
 struct AttnParams {
-    const __nv_bfloat16 *q;
+    const __nv_bfloat16 *q, *k, *v;
     __nv_bfloat16 *out;
     float *lse;
-    int64_t q_ts, q_hs, o_ts, o_hs, table_stride;
+    int64_t q_ts, q_hs, o_ts, o_hs, table_stride, num_pages;
+    int64_t k_page, k_place, k_head, v_page, v_place, v_head;
     const int32_t *table, *kv_lens, *cu_q;
     int page_size, page_shift, table_width, batch, q_tokens, heads, kv_heads, group, window, slot_rows;
     int capacity;                            // keys a sequence can have: table_width * page_size
@@ -409,6 +410,51 @@ __device__ __forceinline__ void store_row(const AttnParams &p, const Row &w, int
     }
 }
 
+// The rows of this warp whose bit is set in `rows`, written once more from the
+// keys first..last that they see alone, the whole warp on a row: the weights
+// (2^(score - shift), in bf16 as in the MMA) times `factor` to `out`, or to the
+// row's part.  Far slower than the MMAs; reached only by chunks whose values
+// are not finite.
+template <int DIM>
+__device__ __noinline__ void rows_again(const AttnParams &p, unsigned rows, int sequence, const Row &mine, int first, int last,
+                                        float shift, float factor, int64_t slot, int r)
+{
+    constexpr int E = DIM / 32;
+    const int lane = threadIdx.x & 31, r0 = r - lane;
+    __syncwarp();
+    while (rows) {
+        const int l = __ffs(rows) - 1;
+        rows &= rows - 1;
+        const int token = __shfl_sync(0xffffffffu, mine.token, l), head = __shfl_sync(0xffffffffu, mine.q_head, l);
+        const int lo = __shfl_sync(0xffffffffu, first, l), hi = __shfl_sync(0xffffffffu, last, l);
+        const float base = __shfl_sync(0xffffffffu, shift, l), f = __shfl_sync(0xffffffffu, factor, l);
+        const int g = head / p.group;
+        float q[E], acc[E] = {};
+        for (int e = 0; e < E; ++e)
+            q[e] = p.q_sign * __bfloat162float(p.q[token * p.q_ts + head * p.q_hs + lane * E + e]);
+        for (int key = lo; key <= hi; ++key) {
+            const int64_t page = p.table[sequence * p.table_stride + (key >> p.page_shift)];
+            const int64_t place = key & (p.page_size - 1);
+            const bool in = page >= 0 && page < p.num_pages;
+            float s = 0.f;
+            for (int e = 0; e < E && in; ++e)
+                s = fmaf(q[e], __bfloat162float(p.k[page * p.k_page + place * p.k_place + g * p.k_head + lane * E + e]), s);
+            for (int o = 16; o > 0; o >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+            const float a = __bfloat162float(__float2bfloat16_rn(ex2(fmaf(s, p.scale_log2, -base))));
+            for (int e = 0; e < E && in; ++e)
+                acc[e] = fmaf(a, __bfloat162float(p.v[page * p.v_page + place * p.v_place + g * p.v_head + lane * E + e]), acc[e]);
+        }
+        for (int e = 0; e < E; ++e) {
+            const int d = lane * E + e;
+            if (slot < 0)
+                p.out[token * p.o_ts + head * p.o_hs + d] = __float2bfloat16_rn(acc[e] * f);
+            else
+                reinterpret_cast<float *>(p.parts + (slot * (DIM / 4) + d / 4) * p.slot_rows + r0 + l)[d & 3] = acc[e];
+        }
+    }
+}
+
 template <int DIM>
 __global__ void __launch_bounds__(kAttnThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -639,6 +685,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 const int all_hi = it.kv - it.q_len + it.q_tile * kTileRows / p.group;
                 const int last_token = min(it.q_len - 1, (it.q_tile * kTileRows + kTileRows - 1) / p.group);
                 const int all_lo = p.window > 0 ? it.kv - it.q_len + last_token - p.window + 1 : 0;
+                // Keys some row sees: [seen_lo, seen_end).
+                const int seen_lo = p.window > 0 ? all_hi - p.window + 1 : 0, seen_end = it.kv - it.q_len + last_token + 1;
 
                 float m = -CUDART_INF_F, l = 0.f;                       // maximum (raw score) and sum of this row
                 for (int j = 0; j < n; ++j, ++g) {
@@ -712,19 +760,19 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         tmem_st_x32(s_addr, pk);
                         ptx::tmem_wait_st();
                     }
-                    if (key0 + kTileKeys > it.kv) {
-                        // What follows the sequence's end in its last page may be anything: a weight of 0
-                        // would not silence NaN, so those keys' V is cleared.
+                    if (key0 < seen_lo || key0 + kTileKeys > seen_end) {
+                        // Keys that no row of the item sees may hold anything (the rest of a sequence's last page,
+                        // pages that a window has left behind): a weight of 0 would not silence NaN, so their V is
+                        // cleared.
                         const uint32_t s = v_index % L::kStages;
                         wait(bar_full + 8 * s, (v_index / L::kStages) & 1, kErrAttnFull);
                         if (!ok)
                             break;
-                        const int keep = max(0, it.kv - key0);
-                        uint8_t *tile = smem + L::kRing + s * L::kTileBytes;
-                        for (int c = r; c < (kTileKeys - keep) * 8 * (int)L::kHalves; c += kTileRows) {
-                            const int half = c / ((kTileKeys - keep) * 8), e = c % ((kTileKeys - keep) * 8);
-                            *reinterpret_cast<uint4 *>(tile + half * (kTileKeys * 128) + keep * 128 + e * 16) =
-                                make_uint4(0, 0, 0, 0);
+                        uint4 *tile = reinterpret_cast<uint4 *>(smem + L::kRing + s * L::kTileBytes);
+                        for (int c = r; c < kTileKeys * 8 * (int)L::kHalves; c += kTileRows) {
+                            const int key = key0 + ((c >> 3) & (kTileKeys - 1));
+                            if (key < seen_lo || key >= seen_end)
+                                tile[c] = make_uint4(0, 0, 0, 0);
                         }
                         ptx::fence_proxy_async_shared();
                     }
@@ -743,6 +791,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 if (r == 0 && from == 0 && !whole)
                     p.cuts[blockIdx.x] = {(it.start + kItemCost + it.tiles - 1) / share - (int)blockIdx.x + 1, it.q0, it.q_len,
                                           it.head, it.q_tile};
+                const int sequence = it.b, key_begin = (it.first_tile + from) * kTileKeys, key_end = key_begin + n * kTileKeys;
+                const bool mixed = all_hi + 1 < seen_end;               // the rows' tokens differ, and so do their keys
                 more = next_piece(p, c, end);
                 if (more)
                     load_q(it);
@@ -752,11 +802,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 // The item's rows: finished here, or a part for the join.
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 if (warp_has_rows) {
+                    uint64_t zero = 0;                                  // stays 0 while O is finite
 #pragma unroll
                     for (int c = 0; c < DIM; c += 32) {
                         uint32_t o[32];
                         tmem_ld_x32(lane_base + kOColumn + c, o);
                         ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            zero = fma2(pack2(o[k], o[k + 1]), 0, zero);
                         if (!w.valid)
                             continue;
                         if (whole) {
@@ -780,6 +834,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         float2 *ml = reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * (DIM / 4));
                         ml[slot * p.slot_rows + r] = make_float2(m * p.scale_log2, l);
                     }
+                    // V that is not finite has met the weights 0 of rows that do not see its key: those rows again,
+                    // key by key.
+                    const float2 z = unpack2(zero);
+                    const unsigned again = __ballot_sync(0xffffffffu, mixed && w.valid && !(z.x + z.y == 0.f));
+                    if (again)
+                        rows_again<DIM>(p, again, sequence, w, max(w.lo, key_begin), min(w.hi, key_end - 1),
+                                        m == -CUDART_INF_F ? 0.f : m * p.scale_log2, whole ? inv : 1.f, whole ? -1 : slot, r);
                 }
             }
         }
@@ -1000,6 +1061,15 @@ extern "C" lowm_status_t lowm_paged_attention(
     p.o_ts = out_token_stride;
     p.o_hs = out_head_stride;
     p.table_stride = page_table_stride;
+    p.k = static_cast<const __nv_bfloat16 *>(k_cache);
+    p.v = static_cast<const __nv_bfloat16 *>(v_cache);
+    p.num_pages = num_pages;
+    p.k_page = k_page_stride;
+    p.k_place = k_place_stride;
+    p.k_head = k_cache_head_stride;
+    p.v_page = v_page_stride;
+    p.v_place = v_place_stride;
+    p.v_head = v_cache_head_stride;
     p.table = page_table;
     p.kv_lens = kv_lens;
     p.cu_q = cu_q;

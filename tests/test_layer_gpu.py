@@ -263,8 +263,12 @@ def attention_reference(q, kc, vc, table, kv_lens, cu, scale, window):
         total = p.sum(-1, keepdim=True)
         lse[cu[b]:cu[b + 1]] = (m + total.log())[..., 0].t()
         p = p / total.clamp(min=1e-300)
-        out[cu[b]:cu[b + 1]] = torch.einsum("hij,jhd->ihd", p, v)
-        size[cu[b]:cu[b + 1]] = torch.einsum("hij,jhd->ihd", p, v.abs())
+        finite = torch.where(v.isfinite(), v, 0)
+        out[cu[b]:cu[b + 1]] = torch.einsum("hij,jhd->ihd", p, finite)
+        size[cu[b]:cu[b + 1]] = torch.einsum("hij,jhd->ihd", p, finite.abs())
+        for j in (~v.isfinite()).flatten(1).any(1).nonzero()[:, 0].tolist():     # reaches the rows that see it, no other
+            for i in seen[:, j].nonzero()[:, 0].tolist():
+                out[cu[b] + i] += torch.where(v[j].isfinite(), 0, p[:, i, j, None] * v[j])
     return out, size, lse
 
 
@@ -390,6 +394,32 @@ def test_attention_infinite_scores():
     page, place = int(table[0, 3]), 5
     kc[page, place] = float("-inf")                    # a score of -inf: weight 0
     run_attention(q, kc, vc, table, [300, 40], cu)
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 2, 2), (128, 8, 2), (128, 3, 1)])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("q_len,kv", [(5, 9), (20, 20), (30, 150), (100, 300), (1, 130)])
+def test_attention_values_that_are_not_finite_reach_only_rows_that_see_them(dim, heads, kv_heads, window, q_len, kv):
+    page = 16
+    for bad in ([kv - 1], [kv - q_len // 2 - 1, kv - 2 if kv > 1 else 0], [max(0, kv - q_len - 30), kv - 1], [0],
+                list(range(max(0, kv - 12), kv, 3))):
+        q, kc, vc, table, cu = attention_inputs([q_len, 1], [kv, 70], heads, kv_heads, dim, page, seed=kv + q_len)
+        for n, j in enumerate(bad):
+            vc[int(table[0, j // page]), j % page, :, n::7] = [float("nan"), float("inf"), float("-inf")][n % 3]
+        run_attention(q, kc, vc, table, [kv, 70], cu, window)
+
+
+def test_attention_pages_behind_the_window_may_hold_anything():
+    q, kc, vc, table, cu = attention_inputs([3, 1], [300, 200], 4, 2, 128, 16)
+    clean = run_attention(q, kc, vc, table, [300, 200], cu, window=50)
+    table2, kc2, vc2 = table.clone(), kc.clone(), vc.clone()
+    for b, first in ((0, 300 - 3 - 50 + 1), (1, 200 - 1 - 50 + 1)):      # the first key any new token sees
+        kc2[int(table[b, first // 16]), :first % 16] = float("nan")
+        vc2[int(table[b, first // 16]), :first % 16] = float("inf")
+        table2[b, :first // 16] = table[1 - b, 0] if b else -1
+    lens, cu32 = torch.tensor([300, 200], dtype=torch.int32, device="cuda"), torch.tensor(cu, dtype=torch.int32, device="cuda")
+    kc2[int(table[1, 0])], vc2[int(table[1, 0])] = float("nan"), float("nan")
+    assert torch.equal(layer.paged_attention(q, kc2, vc2, table2, lens, cu32, window=50), clean)
 
 
 @pytest.mark.parametrize("layout", ["head_major", "joined", "padded"])

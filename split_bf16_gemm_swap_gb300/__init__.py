@@ -15,8 +15,8 @@ from .lowm import (  # noqa: F401
     lowm_gemm_query_tactic, lowm_gemm_query_tactic_ex, lowm_gemm_sync_status, lowm_status_string, lowm_tmem_hog_launch,
 )
 
-_LAYER = ("LOWM_MOE_SIGMOID", "LOWM_MOE_SOFTMAX", "moe", "paged_attention", "residual_norm", "rope_append",
-          "lowm_moe", "lowm_moe_workspace", "lowm_paged_attention", "lowm_paged_attention_workspace",
+_LAYER = ("LOWM_MOE_SIGMOID", "LOWM_MOE_SOFTMAX", "moe", "paged_attention", "release_workspaces", "residual_norm",
+          "rope_append", "lowm_moe", "lowm_moe_workspace", "lowm_paged_attention", "lowm_paged_attention_workspace",
           "lowm_residual_norm", "lowm_rope_append")
 
 

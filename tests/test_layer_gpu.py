@@ -728,3 +728,21 @@ def test_single_token_outputs_are_checked():
     assert torch.equal(layer.moe(x, router, w1, w2, 2, out=odd), layer.moe(x, router, w1, w2, 2))
     new, out = layer.residual_norm(x, x, out=odd)
     assert torch.equal(out, layer.residual_norm(x, x)[1])
+
+
+def test_workspaces_are_kept_for_the_default_stream_alone():
+    x, router, w1, w2 = moe_inputs(4, 64, 32, 8)
+    layer.release_workspaces()
+    assert not layer._kept
+    small = layer.moe(x, router, w1, w2, 2)
+    kept = dict(layer._kept)
+    assert len(kept) == 1
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert torch.equal(layer.moe(x, router, w1, w2, 2, stream=side), small) and layer._kept == kept
+    q, kc, vc, table, cu = attention_inputs([1, 30], [500, 300], 16, 2, 128, 64)        # a larger one replaces it
+    run_attention(q, kc, vc, table, [500, 300], cu)
+    assert layer._kept[0][1].numel() > kept[0][1].numel()
+    assert torch.equal(layer.moe(x, router, w1, w2, 2), small)
+    layer.release_workspaces()
+    assert torch.equal(layer.moe(x, router, w1, w2, 2), small)

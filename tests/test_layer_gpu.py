@@ -107,6 +107,28 @@ def test_norm_strided_rows(width, start):
     assert bool((out[:, 0] == 7).all()) and bool((out[:, 601:] == 7).all())
 
 
+@pytest.mark.parametrize("hidden", [1, 5, 9, 255, 257, 2047, 4095, 8185, 8191, 16377, 16383])
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_rows_off_the_16_byte_boundaries(hidden, f32):
+    # contiguous rows of odd width: every row starts elsewhere; enough of them that some CTAs walk several
+    tokens = 23 if hidden > 3000 else 700
+    res = rand(tokens, hidden, seed=1, std=3.0, dtype=torch.float32 if f32 else BF)
+    check_norm(res, rand(tokens, hidden, seed=2), rand(hidden, seed=4), rand(tokens, hidden, seed=3), rand(hidden, seed=5), 0.7)
+    check_norm(res, rand(tokens, hidden, seed=2), None, rand(hidden, seed=3), None)
+    # rows of a wider matrix, and tensors whose rows lie differently
+    wide = rand(tokens, hidden + 8, seed=6)
+    check_norm(wide[:, :hidden] if not f32 else res, wide[:, 8:], None, None, rand(hidden, seed=5))
+    check_norm(res, wide[:, 3:3 + hidden], rand(hidden, seed=4), None, rand(hidden, seed=5))
+
+
+def test_norm_walks_odd_rows():
+    check_norm(rand(5000, 2305, seed=1), rand(5000, 2305, seed=2), rand(2305, seed=3), None, rand(2305, seed=4))
+    out = torch.full((4001, 2313), 7.0, dtype=BF, device="cuda")
+    res, block = rand(4001, 2313, seed=1), rand(4001, 2313, seed=2)
+    check_norm(res[:, 8:], block[:, 8:], rand(2305, seed=3), None, None, out=out[:, 8:])
+    assert bool((out[:, :8] == 7).all())
+
+
 def test_norm_in_place():
     res, block = rand(33, 768, seed=1), rand(33, 768, seed=2)
     want = layer.residual_norm(res, block)

@@ -13,7 +13,7 @@
 // in the workspace, and a second small kernel joins the parts in order.
 //
 // A CTA has four softmax warps (a thread owns a row = a TMEM lane), a warp
-// that feeds a ring of 64-key tiles by TMA, page by page, and two threads that
+// that feeds a ring of 64-key tiles by TMA, page by page, and two warps that
 // issue the MMAs: S = Q K^T into one of two TMEM buffers, and O += P V with P
 // (bf16, written over its S) from TMEM and V as the transposed operand.
 // S of the next tile is computed while the softmax of this one runs, and the
@@ -22,11 +22,14 @@
 // relative), so most tiles leave O alone.
 //
 // What bounds it.  Decode: the cache's bandwidth (24 sequences of up to 16384
-// keys, 1.0 GB: 159 us, 6.3 TB/s).  Chunks: the MMA issue and the softmax of two
-// CTAs an SM (2048 tokens over 16384 keys: 401 us, 1.29 PFLOP/s; the scores' 8
-// MMAs of N 64 take ~55 cycles each where the arithmetic needs 32, but 128 keys
-// at once do not fit the TMEM beside O in two CTAs).  Few keys: the chain of
-// launch, schedule, first tile and join (4 x 1000 keys: 13.6 us).
+// keys, 1.0 GB: 157 us, 6.4 TB/s).  Chunks: the MMA issue, the loads and the
+// softmax of two CTAs an SM, none of them alone (2048 tokens over 16384 keys: 364
+// us, 1.41 PFLOP/s; without the exponentials, with half of the loads or with one
+// page for all 3 to 5 % less each; the scores' MMAs of N 64 read more shared
+// memory than their arithmetic hides).  One CTA an SM with 256 rows and tiles of
+// 128 keys halves the loads and has MMAs of N 128, but one S for each 128 rows: the
+// chain S, softmax, O of one half is not hidden by the other (453 us).  Few keys:
+// the chain of launch, schedule, first tile and join (4 x 1000 keys: 13.3 us).
 //
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.
@@ -294,6 +297,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// A value that all lanes of a warp hold, so that the compiler knows it, too.
+template <typename T>
+__device__ __forceinline__ T uniform(T x)
+{
+    return __shfl_sync(0xffffffffu, x, 0);
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar)
@@ -564,63 +574,75 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             for (uint32_t j = i > L::kStages ? i - L::kStages : 0; j < i; ++j)
                 (void)wait_short(bar_full + 8 * (j % L::kStages), (j / L::kStages) & 1);
         } else if (warp >= 5) {
-            // -------------------------------------------------------- MMA: one thread for S, one for O
+            // -------------------------------------------------------- MMA: one warp for S, one for O
             // A tile's 12 MMAs, 4 commits and 3 waits in one thread took 2100
-            // cycles, more than its softmax; two threads run them side by side.
+            // cycles, more than its softmax; two run them side by side.  The warps
+            // stay converged and elect the issuing thread, and the compiler knows
+            // that the operands are the same in all lanes: from a branch for lane 0
+            // the 8 MMAs of S took 765 cycles to issue, this way 580 (2048 tokens over
+            // 16384 keys: 395 -> 364 us).
             constexpr uint32_t kIdescS = make_idesc_bf16(kTileRows, kTileKeys);
             constexpr uint32_t kIdescO = make_idesc_bf16(kTileRows, DIM) | (1u << 16);   // B: N contiguous
-            if (lane == 0) {
-                uint32_t i = 0, g = 0, items = 0;                       // ring stages passed, tiles, items
-                bool ok = true;
-                auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
-                    if (!wait_short(bar, parity)) {
-                        ok = false;
-                        atomicOr(p.status, err);
-                    }
-                };
-                do {
-                    const int n = c.to - c.from;
-                    if (warp == 5) {
-                        wait(bar_q, items & 1, kErrAttnWeights);
-                        for (int j = 0; j < n && ok; ++j, ++g) {        // S[g & 1] = Q . K^T
-                            const uint32_t at = i + (j == 0 ? 0 : 2 * j - 1), s = at % L::kStages;
-                            wait(bar_full + 8 * s, (at / L::kStages) & 1, kErrAttnFull);
-                            if (g > 1)                                  // the weights that lay there have met V
-                                wait(bar_o + 8 * (g & 1), ((g >> 1) & 1) ^ 1, kErrAttnOutput);
-                            ptx::tcgen05_fence_after_thread_sync();
-                            if (!ok)
-                                break;
-                            const uint64_t a0 = make_sw128_kmajor_desc(sbase + L::kQ);
-                            const uint64_t b0 = make_sw128_kmajor_desc(sbase + L::kRing + s * L::kTileBytes);
+            const bool first = uniform(warp) == 5;
+            const uint32_t base = uniform(tmem);
+            uint32_t i = 0, g = 0, items = 0;                           // ring stages passed, tiles, items
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
+                if (!wait_short(bar, parity)) {
+                    ok = false;
+                    atomicOr(p.status, err);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            };
+            do {
+                const int n = uniform(c.to - c.from);
+                if (first) {
+                    wait(bar_q, items & 1, kErrAttnWeights);
+                    for (int j = 0; j < n && ok; ++j, ++g) {            // S[g & 1] = Q . K^T
+                        const uint32_t at = i + (j == 0 ? 0 : 2 * j - 1), s = at % L::kStages;
+                        wait(bar_full + 8 * s, (at / L::kStages) & 1, kErrAttnFull);
+                        if (g > 1)                                      // the weights that lay there have met V
+                            wait(bar_o + 8 * (g & 1), ((g >> 1) & 1) ^ 1, kErrAttnOutput);
+                        ptx::tcgen05_fence_after_thread_sync();
+                        if (!ok)
+                            break;
+                        const uint64_t a0 = make_sw128_kmajor_desc(sbase + L::kQ);
+                        const uint64_t b0 = make_sw128_kmajor_desc(sbase + L::kRing + s * L::kTileBytes);
+                        if (ptx::elect_one_sync()) {
 #pragma unroll
                             for (uint32_t k = 0; k < 4 * L::kHalves; ++k)
-                                ptx::mma_bf16_ss(tmem + (g & 1) * kSColumns, a0 + (k >> 2) * (kTileRows * 8) + 2 * (k & 3),
+                                ptx::mma_bf16_ss(base + (g & 1) * kSColumns, a0 + (k >> 2) * (kTileRows * 8) + 2 * (k & 3),
                                                  b0 + (k >> 2) * (kTileKeys * 8) + 2 * (k & 3), kIdescS, k > 0);
                             ptx::tcgen05_commit(bar_s + 8 * (g & 1));
                             ptx::tcgen05_commit(bar_empty + 8 * s);
                         }
-                    } else {
-                        for (int j = 0; j < n && ok; ++j, ++g) {        // O (+)= P . V
-                            const uint32_t at = i + (j + 1 < n ? 2 * j + 2 : 2 * j + 1), s = at % L::kStages;
-                            wait(bar_full + 8 * s, (at / L::kStages) & 1, kErrAttnFull);
-                            wait(bar_p + 8 * (g & 1), (g >> 1) & 1, kErrAttnWeights);
-                            ptx::tcgen05_fence_after_thread_sync();
-                            if (!ok)
-                                break;
-                            const uint64_t b0 = make_sw128_nmajor_desc(sbase + L::kRing + s * L::kTileBytes, kTileKeys * 128);
+                        __syncwarp();
+                    }
+                } else {
+                    for (int j = 0; j < n && ok; ++j, ++g) {            // O (+)= P . V
+                        const uint32_t at = i + (j + 1 < n ? 2 * j + 2 : 2 * j + 1), s = at % L::kStages;
+                        wait(bar_full + 8 * s, (at / L::kStages) & 1, kErrAttnFull);
+                        wait(bar_p + 8 * (g & 1), (g >> 1) & 1, kErrAttnWeights);
+                        ptx::tcgen05_fence_after_thread_sync();
+                        if (!ok)
+                            break;
+                        const uint64_t b0 = make_sw128_nmajor_desc(sbase + L::kRing + s * L::kTileBytes, kTileKeys * 128);
+                        if (ptx::elect_one_sync()) {
 #pragma unroll
                             for (uint32_t k = 0; k < kTileKeys / 16; ++k)    // 16 keys: 2 KiB of V, 8 columns of P
-                                mma_bf16_ts(tmem + kOColumn, tmem + (g & 1) * kSColumns + 8 * k, b0 + 128 * k, kIdescO,
+                                mma_bf16_ts(base + kOColumn, base + (g & 1) * kSColumns + 8 * k, b0 + 128 * k, kIdescO,
                                             j > 0 || k > 0);
                             ptx::tcgen05_commit(bar_o + 8 * (g & 1));
                             ptx::tcgen05_commit(bar_empty + 8 * s);
                         }
+                        __syncwarp();
                     }
-                    i += 2 * n;
-                    ++items;
-                } while (ok && next_piece(p, c, end));
+                }
+                i += 2 * n;
+                ++items;
+            } while (ok && uniform(next_piece(p, c, end)));
+            if (ptx::elect_one_sync())
                 ptx::tcgen05_commit(bar_drain);
-            }
             __syncwarp();
             (void)wait_short(bar_drain, 0);                             // nothing reads or writes TMEM any more
         } else {

@@ -6,6 +6,13 @@
 
 namespace lowm {
 
+// A value that all lanes of a warp hold, so that the compiler knows it, too.
+template <typename T>
+__device__ __forceinline__ T uniform(T x)
+{
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // One try_wait that lets the hardware suspend the thread for up to `ns` until the phase completes.
 __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns)
 {

@@ -29,7 +29,7 @@
 // memory than their arithmetic hides).  One CTA an SM with 256 rows and tiles of
 // 128 keys halves the loads and has MMAs of N 128, but one S for each 128 rows: the
 // chain S, softmax, O of one half is not hidden by the other (453 us).  Few keys:
-// the chain of launch, schedule, first tile and join (4 x 1000 keys: 13.3 us).
+// the chain of launch, schedule, first tile and join (4 x 1000 keys: 12.6 us).
 //
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.
@@ -52,11 +52,12 @@ constexpr int kMaxAttnCtas = 320;            // two per SM, and a bound for the 
 constexpr int kMaxKeys = 1 << 30;            // of a sequence
 // The line counts time in tiles.  An item costs kItemCost tiles beside its own
 // (its queries' way in, its rows' way out); without it the CTAs with short
-// items ended 20 % after the others (chunks of 512 and fewer tokens of four
-// sequences: 97 us at 4, 91 at 7, 93 at 10; of 1537 tokens 234, 229, 232).
-constexpr int kItemCost = 7;
-constexpr int kMinShare = 4;                 // smaller shares cost more in the join than they save, larger ones wait
-                                             // longer (short decodes: 14.3 us at 3, 13.8 at 4, 14.4 at 6)
+// items ended 20 % after the others (chunks of 1537 tokens: 209 us at 5, 200 at
+// 7, 198.5 at 8, 199.5 at 10, 202 at 12).
+constexpr int kItemCost = 8;
+// Smaller shares cost more in the join than they save, larger ones wait longer
+// (4 x 1000 keys: 13.6 us at 3, 13.2 at 4, 12.6 at 5, 13.2 at 6).
+constexpr int kMinShare = 5;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSColumns = 64;           // one S buffer; P takes its first 32 columns
 
@@ -297,13 +298,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-
-// A value that all lanes of a warp hold, so that the compiler knows it, too.
-template <typename T>
-__device__ __forceinline__ T uniform(T x)
-{
-    return __shfl_sync(0xffffffffu, x, 0);
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar)

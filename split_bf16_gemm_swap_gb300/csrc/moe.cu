@@ -46,7 +46,8 @@ constexpr int kRouterCluster = 8;            // CTAs (and tokens) of a router cl
 constexpr int kMoeThreads = 256;             // TMA warp 0, MMA warps 1 and 6, epilogue warps 2-5, loader warp 7
 constexpr int kMoeRows = 64;                 // weight rows of an item = the MMA's M
 constexpr int kMaxColumns = 64;              // tokens of an item; an expert with more gets several items
-constexpr int kLoaderLag = 1;                // stages whose rows the loader has in flight behind the newest
+constexpr int kLoaderLag = 1;                // stages whose rows the loader has in flight behind the newest; below
+                                             // the ring's stages, or it waits for one that it has not handed on
 constexpr uint32_t kWBlockBytes = kMoeRows * 128u;
 
 // Bits of the device status word (above those of paged_attention.cu).
@@ -704,9 +705,9 @@ constexpr int kMaxSmem = 232448;             // 227 KiB
 
 // K blocks a stage.  A copy has a fixed cost, so eight blocks (64 KiB of
 // weights) beat four where two such stages fit and K fills its last stage:
-// GB300, 4 -> 8 blocks: 128 tokens over 32 experts of 4096 x 1400 194 -> 185 us,
-// 8 tokens over 64 of 2048 x 768 48.0 -> 45.0; but 37 over 64 of 1544 x 920, whose
-// 25 and 15 blocks would leave a fifth of the stages empty, 56.1 -> 60.8.
+// GB300, 4 -> 8 blocks: 128 tokens over 32 experts of 4096 x 1400 191 -> 175 us,
+// 8 tokens over 64 of 2048 x 768 47.6 -> 43.8; but 37 over 64 of 1544 x 920, whose
+// 25 and 15 blocks would leave a fifth of the stages empty, 90.9 -> 95.8.
 int moe_blocks(int hidden, int inner, int experts, int pairs, int columns)
 {
     auto rounded = [](int n, int to) { return (n + to - 1) / to * to; };

@@ -1,9 +1,9 @@
 // Rotary positions (one to three axes) for new queries and keys, and the
 // append of keys and values to the paged cache (lowm_layer.h).
 //
-// Element-wise work bound by its bytes (4096 tokens of 32 / 8 heads of 128: 21 us,
-// 4.9 TB/s; at few tokens by the launch and two dependent reads, position then
-// table: 4 tokens 2.6 us).  One CTA owns one token; a thread owns one group of
+// Element-wise work bound by its bytes (4096 tokens of 32 / 8 heads of 128: 20 us,
+// 5.1 TB/s; at few tokens by the launch and two dependent reads, position then
+// table: 4 tokens 2.5 us).  One CTA owns one token; a thread owns one group of
 // pairs for several heads, so a token's cosines and sines are read once per
 // thread and serve every head it visits.
 #include <cuda_bf16.h>
@@ -65,8 +65,11 @@ __device__ __forceinline__ void turn(Run<GROUP> &a, Run<GROUP> &b, const float (
     }
 }
 
+// At most 64 registers a thread: more threads an SM are worth more than more
+// heads in flight (4096 tokens of 32 / 8 heads of 128: 20.1 us, at 70 registers
+// 21.1, with four heads of q and one of k and v in flight at 128 29.8).
 template <int GROUP, bool INTERLEAVED>
-__global__ void __launch_bounds__(512) rope_append_kernel(const RopeParams p)
+__global__ void __launch_bounds__(512, 2) rope_append_kernel(const RopeParams p)
 {
     const int64_t t = blockIdx.x;
     const int units = (p.dim + 2 * GROUP - 1) / (2 * GROUP);
@@ -239,15 +242,16 @@ extern "C" lowm_status_t lowm_rope_append(
 
     const bool vec = aligned && dim % 16 == 0 && rotary % 16 == 0 && (all & 7) == 0;
     const int units = vec ? dim / 16 : (dim + 1) / 2;
-    int threads = units * std::max(heads, kv_heads);
     // Few tokens: a thread for every unit, to be done soonest.  Many: fewer threads
     // with more heads each, which read a token's cosines and sines fewer times
     // (GB300, 32 / 8 heads of 128, 512 -> 128 -> 64 threads: 4 tokens 2.6, 2.8, 3.4
-    // us; 1000 tokens 7.7, 5.0, 5.7; 4096 tokens 39.9, 25.3, 21.1).
-    const int most = std::max(units, tokens >= 8 * sms ? 64 : (tokens >= 2 * sms ? 128 : 512));
-    if (threads > most)
-        threads = most / units * units;
-    threads = (threads + 31) / 32 * 32;
+    // us; 1000 tokens 7.7, 5.0, 5.7; 4096 tokens 39.9, 25.3, 21.1), four heads at
+    // least (4096 tokens, 64 -> 32 threads: 8 / 2 heads of 128 8.4 -> 6.5 us, 32 / 8
+    // of 64 13.5 -> 11.2; but 2048 tokens of 32 / 32 of 128, eight heads, 19.5 -> 24.8).
+    const int most = std::max(heads, kv_heads);
+    const int lanes = tokens >= 8 * sms ? std::min(64 / units, (most + 3) / 4)
+                                        : std::min((tokens >= 2 * sms ? 128 : 512) / units, most);
+    const int threads = (std::max(lanes, 1) * units + 31) / 32 * 32;
     auto fn = vec ? (interleaved ? rope_append_kernel<8, true> : rope_append_kernel<8, false>)
                   : (interleaved ? rope_append_kernel<1, true> : rope_append_kernel<1, false>);
     return launch_pdl(fn, dim3((unsigned)tokens), dim3((unsigned)threads), 0, stream, p);

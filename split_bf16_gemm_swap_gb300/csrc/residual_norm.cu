@@ -8,9 +8,11 @@
 // launch, one memory latency and the two reductions (4 x 4096: 2.4 us); at
 // prompt sizes it is the bandwidth of r, y, r' and n (8192 x 4096 bf16: 43.7 us,
 // 6.1 TB/s; with an fp32 residual and a gate per token 73.9 us, 6.4 TB/s).  Rows
-// that cannot be read in 16-byte pieces are bound by their single loads (3000 x
-// 2305: 23.8 us, 2.3 TB/s).
+// of odd widths have their weights by single loads and a warp more, and cost up
+// to twice as much (8192 x 4095: 85 us, one CTA an SM; 8000 x 3001: 63 us).
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "layer_host.h"
 #include "ptx.cuh"
@@ -67,10 +69,15 @@ template <int VEC>
 struct Residual<VEC, false> {
     Pack<VEC> p;
     __device__ void load(const void *base, int64_t at) { load_bf16(static_cast<const __nv_bfloat16 *>(base) + at, p); }
+    __device__ void load_one(const void *base, int64_t at) { p.v[0] = static_cast<const __nv_bfloat16 *>(base)[at]; }
     __device__ float value(int j) const { return __bfloat162float(p.v[j]); }
     static __device__ void store(void *base, int64_t at, const float (&f)[VEC])
     {
         store_bf16(static_cast<__nv_bfloat16 *>(base) + at, f);
+    }
+    static __device__ void store_one(void *base, int64_t at, float f)
+    {
+        static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(f);
     }
 };
 
@@ -87,7 +94,9 @@ struct Residual<VEC, true> {
             f[0] = *src;
         }
     }
+    __device__ void load_one(const void *base, int64_t at) { f[0] = static_cast<const float *>(base)[at]; }
     __device__ float value(int j) const { return f[j]; }
+    static __device__ void store_one(void *base, int64_t at, float v) { static_cast<float *>(base)[at] = v; }
     static __device__ void store(void *base, int64_t at, const float (&v)[VEC])
     {
         float *dst = static_cast<float *>(base) + at;
@@ -120,17 +129,55 @@ __device__ __forceinline__ float block_sum(float x, float *scratch)
     return x;
 }
 
-// ELEMS elements a thread in pieces of VEC, piece n at (n * blockDim.x + thread) * VEC.
+// ELEMS elements a thread in pieces of VEC, piece n at (n * threads + thread) * VEC.
+// EDGES: rows of any width that lie alike in all tensors.  The pieces begin at
+// the row's first 16-byte boundary; the up to 14 elements before the first and
+// behind the last piece are a lane's each of one more warp, so that no warp
+// runs both forms of an access.  (Rows of one CTA lie alike: a grid that walks
+// is a multiple of 8.)  Against one element at a time: 150 x 2305 3.2 -> 2.5 us,
+// 300 x 999 with an fp32 residual 4.6 -> 2.8, 8000 x 3001 85 -> 63; narrow rows by
+// the thousand gain nothing or lose (8000 x 601 15.7 for 17.2 us; with an fp32
+// residual and a gate per token 21.0 for 18.6).
 // A CTA walks rows blockIdx.x, blockIdx.x + gridDim.x, ...: the weights stay in
 // registers, and the next row is requested before this one's reductions.
 // (LOOP false: one row a CTA, without the registers of the second.)
-template <int VEC, int ELEMS, bool F32, bool LOOP>
+template <int VEC, int ELEMS, bool F32, bool LOOP, bool EDGES>
 __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
 {
     constexpr int NP = ELEMS / VEC;
     __shared__ float scratch[4][32];
     const bool has_gate = p.gate != nullptr, has_block = p.block != nullptr, has_post = p.post != nullptr;
-    const int step = (int)blockDim.x * VEC, first = (int)threadIdx.x * VEC;
+    int step = (int)blockDim.x * VEC, first = (int)threadIdx.x * VEC, end = p.hidden;
+    bool single = false;                     // a thread of the last warp: one element
+    if constexpr (EDGES) {
+        const int before = (int)(-((int64_t)blockIdx.x * p.out_stride) & 7), inner = before + (max(p.hidden - before, 0) & ~7);
+        step -= 32 * VEC;
+        single = threadIdx.x >= blockDim.x - 32;
+        const int lane = threadIdx.x & 31;
+        first = !single ? first + before : lane < before ? lane : inner + lane - before;
+        if (!single)
+            end = inner;
+    }
+    // Piece n of this thread lies in the row.
+    auto has = [&](int n) { return (!EDGES || !single || n == 0) && n * step + first < end; };
+    auto load_row = [&](const __nv_bfloat16 *x, Pack<VEC> &o) {
+        if (EDGES && single)
+            o.v[0] = *x;
+        else
+            load_bf16(x, o);
+    };
+    auto load_weight = [&](const __nv_bfloat16 *w, Pack<VEC> &o) {   // they lie apart from the rows
+        if constexpr (EDGES) {
+            o.v[0] = w[0];
+            if (!single) {
+#pragma unroll
+                for (int j = 1; j < VEC; ++j)
+                    o.v[j] = w[j];
+            }
+        } else {
+            load_bf16(w, o);
+        }
+    };
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
@@ -142,13 +189,16 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             const int i = n * step + first;
-            if (i >= p.hidden)
+            if (!has(n))
                 continue;
             if (has_block)
-                load_bf16(p.block + t * p.block_stride + i, v.y[n]);
-            v.r[n].load(p.residual, t * p.residual_stride + i);
+                load_row(p.block + t * p.block_stride + i, v.y[n]);
+            if (EDGES && single)
+                v.r[n].load_one(p.residual, t * p.residual_stride + i);
+            else
+                v.r[n].load(p.residual, t * p.residual_stride + i);
             if (has_gate && p.gate_stride)
-                load_bf16(p.gate + t * p.gate_stride + i, v.g[n]);
+                load_row(p.gate + t * p.gate_stride + i, v.g[n]);
         }
     };
     Values next;
@@ -156,6 +206,8 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
     for (int n = 0; n < NP; ++n) {
         next.y[n] = {};
         next.r[n] = {};
+        if (EDGES)
+            next.g[n] = {};
     }
     int64_t t = blockIdx.x;
     load(t, next);
@@ -166,14 +218,14 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
             post[n].v[j] = pre[n].v[j] = __float2bfloat16_rn(1.f);
-        if (i >= p.hidden)
+        if (!has(n))
             continue;
         if (has_post)
-            load_bf16(p.post + i, post[n]);
+            load_weight(p.post + i, post[n]);
         if (p.pre != nullptr)
-            load_bf16(p.pre + i, pre[n]);
+            load_weight(p.pre + i, pre[n]);
         if (has_gate && !p.gate_stride)
-            load_bf16(p.gate + i, next.g[n]);
+            load_weight(p.gate + i, next.g[n]);
     }
 
     for (int parity = 0;; t += gridDim.x, parity ^= 2) {
@@ -203,7 +255,7 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
                     float v = __bfloat162float(cur.y[n].v[j]) * inv * __bfloat162float(post[n].v[j]);
                     if (has_gate)
                         v *= __bfloat162float(cur.g[n].v[j]);
-                    r[n][j] = n * step + first < p.hidden ? fmaf(r[n][j], p.scale, v) : 0.f;
+                    r[n][j] = has(n) && (!EDGES || !single || j == 0) ? fmaf(r[n][j], p.scale, v) : 0.f;
                 }
                 sum = fmaf(r[n][j], r[n][j], sum);
             }
@@ -211,7 +263,11 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
                 const int i = n * step + first;
-                if (i < p.hidden)
+                if (!has(n))
+                    continue;
+                if (EDGES && single)
+                    Residual<VEC, F32>::store_one(p.out_residual, t * p.out_residual_stride + i, r[n][0]);
+                else
                     Residual<VEC, F32>::store(p.out_residual, t * p.out_residual_stride + i, r[n]);
             }
         }
@@ -219,23 +275,27 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormParams p)
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             const int i = n * step + first;
-            if (i >= p.hidden)
+            if (!has(n))
                 continue;
             float o[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j)
                 o[j] = r[n][j] * inv * __bfloat162float(pre[n].v[j]);
-            store_bf16(p.out + t * p.out_stride + i, o);
+            if (EDGES && single)
+                p.out[t * p.out_stride + i] = __float2bfloat16_rn(o[0]);
+            else
+                store_bf16(p.out + t * p.out_stride + i, o);
         }
         if (!LOOP || t + gridDim.x >= p.tokens)
             return;
     }
 }
 
-template <int VEC, int ELEMS, bool LOOP>
+template <int VEC, int ELEMS, bool LOOP, bool EDGES>
 lowm_status_t launch_norm(const NormParams &p, bool f32, int grid, int threads, void *stream)
 {
-    return launch_pdl(f32 ? residual_norm_kernel<VEC, ELEMS, true, LOOP> : residual_norm_kernel<VEC, ELEMS, false, LOOP>,
+    return launch_pdl(f32 ? residual_norm_kernel<VEC, ELEMS, true, LOOP, EDGES>
+                          : residual_norm_kernel<VEC, ELEMS, false, LOOP, EDGES>,
                       dim3((unsigned)grid), dim3((unsigned)threads), 0, stream, p);
 }
 
@@ -303,26 +363,37 @@ extern "C" lowm_status_t lowm_residual_norm(const void *residual, int residual_f
     p.eps = eps;
     p.inv_hidden = 1.f / (float)hidden;
 
+    // 16-byte pieces: rows on 16-byte boundaries throughout, or (edges) rows that lie alike in all tensors.
+    const bool bases = is_aligned(residual, 16) && is_aligned(block, 16) && is_aligned(out_residual, 16) &&
+                       is_aligned(out, 16) && (!gate_stride || is_aligned(gate, 16));
     const int64_t rmod = residual_f32 ? 3 : 7;
-    const bool vec = hidden % 8 == 0 && !((residual_stride | out_residual_stride) & rmod) &&
-                     !((block_stride | gate_stride | out_stride) & 7) && is_aligned(residual, 16) &&
-                     is_aligned(block, 16) && is_aligned(post_weight, 16) && is_aligned(gate, 16) &&
-                     is_aligned(pre_weight, 16) && is_aligned(out_residual, 16) && is_aligned(out, 16);
+    const bool vec = bases && hidden % 8 == 0 && !((residual_stride | out_residual_stride) & rmod) &&
+                     !((block_stride | gate_stride | out_stride) & 7) && is_aligned(post_weight, 16) &&
+                     is_aligned(gate, 16) && is_aligned(pre_weight, 16);
+    auto alike = [&](bool used, int64_t stride) { return !used || ((stride - out_stride) & 7) == 0; };
+    const bool edges = !vec && bases && alike(true, residual_stride) && alike(block != nullptr, block_stride) &&
+                       alike(out_residual != nullptr, out_residual_stride) && alike(gate_stride != 0, gate_stride) &&
+                       hidden <= kMaxHidden - 512;   // 31 warps and the edges'
     const bool f32 = residual_f32 != 0;
-    const int elems = hidden <= 8192 ? 8 : 16, threads = ((hidden + elems - 1) / elems + 31) / 32 * 32;
+    const int elems = hidden <= (edges ? kMaxHidden - 512 : kMaxHidden) / 2 ? 8 : 16;
+    const int threads = ((hidden + elems - 1) / elems + 31) / 32 * 32 + (edges ? 32 : 0);
     if (elems == 16)
-        return vec ? launch_norm<8, 16, false>(p, f32, tokens, threads, stream)
-                   : launch_norm<1, 16, false>(p, f32, tokens, threads, stream);
-    if (!vec)
-        return launch_norm<1, 8, false>(p, f32, tokens, threads, stream);
+        return vec     ? launch_norm<8, 16, false, false>(p, f32, tokens, threads, stream)
+               : edges ? launch_norm<8, 16, false, true>(p, f32, tokens, threads, stream)
+                       : launch_norm<1, 16, false, false>(p, f32, tokens, threads, stream);
+    if (!vec && !edges)
+        return launch_norm<1, 8, false, false>(p, f32, tokens, threads, stream);
     // Walking rows pays from two rounds of 1024 threads an SM on, for rows of 256
     // threads and more (GB300, one row a CTA -> walking: 8192 x 4096 57.3 -> 43.7
     // us, 2000 x 8000 40.3 -> 29.2; 8000 x 600, 96 threads, 10.2 -> 12.5; 600 x
-    // 4096, two rounds, 5.0 both).  768 or 1536 threads an SM lose at 8192 x 4096
-    // (54.9, 52.9 us).
+    // 4096, two rounds, 5.0 both), and of 192 where it saves single loads of
+    // weights (6293 x 1313 35.7 -> 30.2; 2000 x 1001, 160 threads, 7.3 -> 8.4).  768
+    // or 1536 threads an SM lose at 8192 x 4096 (54.9, 52.9 us).
     const int resident = sms * (1024 / threads);
-    if (threads < 256 || tokens <= 2 * resident)
-        return launch_norm<8, 8, false>(p, f32, tokens, threads, stream);
-    const int rounds = (tokens + resident - 1) / resident;
-    return launch_norm<8, 8, true>(p, f32, (tokens + rounds - 1) / rounds, threads, stream);
+    if (threads < (edges ? 192 : 256) || tokens <= 2 * resident)
+        return vec ? launch_norm<8, 8, false, false>(p, f32, tokens, threads, stream)
+                   : launch_norm<8, 8, false, true>(p, f32, tokens, threads, stream);
+    const int rounds = (tokens + resident - 1) / resident, grid = (tokens + rounds - 1) / rounds;
+    return vec ? launch_norm<8, 8, true, false>(p, f32, grid, threads, stream)
+               : launch_norm<8, 8, true, true>(p, f32, std::max(8, grid / 8 * 8), threads, stream);
 }

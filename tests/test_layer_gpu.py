@@ -139,6 +139,23 @@ def test_norm_in_place():
     assert out is block and torch.equal(block, want[1]) and torch.equal(new, want[0])
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("tokens,hidden", [(5, 999), (4001, 1313)])
+def test_norm_in_place_odd_rows(tokens, hidden, dtype):
+    res, block = rand(tokens, hidden, seed=1, dtype=dtype), rand(tokens, hidden, seed=2)
+    kw = dict(post_weight=rand(hidden, seed=3), gate=rand(hidden, seed=4), scale=0.5)
+    want = layer.residual_norm(res, block, **kw)
+    new, out = layer.residual_norm(res, block, out_residual=res, out=block, **kw)
+    assert new is res and out is block and torch.equal(res, want[0]) and torch.equal(block, want[1])
+
+
+def test_norm_broadcast_odd_rows():
+    # one residual row for all tokens, then one block row: they lie differently from the outputs' rows
+    row = rand(1, 2305, seed=1)
+    check_norm(row.expand(700, -1), rand(700, 2305, seed=2), rand(2305, seed=3), None, None)
+    check_norm(rand(700, 2305, seed=2), row.expand(700, -1), rand(2305, seed=3), rand(700, 2305, seed=4), None)
+
+
 def test_norm_zero_rows_and_nan():
     res, block = rand(4, 512, seed=1), rand(4, 512, seed=2)
     res[1], block[1] = 0, 0

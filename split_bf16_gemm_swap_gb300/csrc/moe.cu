@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             item_products(group[up ? item / up_tiles : (item - up_items) / down_tiles], up ? up_blocks : down_blocks,
                           up ? up_stages : down_stages);
         }
-        if (lane == 0)
+        if (ptx::elect_one_sync())        // the thread that issued the MMAs
             ptx::tcgen05_commit(bar_drain);
         __syncwarp();
         (void)wait_short(bar_drain, 0);   // nothing writes TMEM any more

@@ -10,13 +10,14 @@ none of them records a gradient.
 ``with torch.cuda.stream(stream)``: the outputs and workspaces that it makes
 belong to that stream, and nothing is ordered against torch's current one.
 Calls on a device's default stream share one workspace that is kept between
-them (:func:`release_workspaces`).
+them (:func:`release_workspaces`); they may come from several host threads.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
 import math
+import threading
 
 import torch
 
@@ -134,27 +135,36 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-# The workspace of the calls on each device's default stream, which run one after another; a call on another stream
-# allocates its own.  (The default stream is never destroyed nor captured.  Allocated at every call, a workspace cost
-# paged_attention 4 of 20 us on the host.)
+# The workspace of the calls on each device's default stream.  An operator with a workspace is two launches, and ctypes
+# lets other threads run during a call: the lock is held until both are enqueued, so that the stream runs all of one
+# call's kernels before the next call's.  (A lock that the thread may take again: a finaliser can call an operator.)  A
+# call on another stream allocates its own.  The default stream is never destroyed nor captured.  Allocated at every
+# call, a workspace cost paged_attention 4 of 20 us on the host.
 _kept: dict = {}
+_kept_lock = threading.RLock()
 
 
-def _scratch(nbytes: int, device: int, stream: int):
-    """(address, owner) of scratch memory for a call on `stream`; the owner lives until the call has been enqueued."""
+def _launch(name: str, args, nbytes: int, device: int, stream: int) -> None:
+    """Call the library's function `name` with `args`, `nbytes` of scratch memory and `stream`."""
+    fn = function(name)
     if stream:
         own = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-        return own.data_ptr(), own
-    kept = _kept.get(device)
-    if kept is None or kept[1].numel() < nbytes:
-        own = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-        kept = _kept[device] = (own.data_ptr(), own)
-    return kept
+        s = fn(*args, own.data_ptr(), nbytes, stream)
+    else:
+        with _kept_lock:
+            kept = _kept.get(device)
+            if kept is None or kept[1].numel() < nbytes:
+                own = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+                kept = _kept[device] = (own.data_ptr(), own)
+            s = fn(*args, kept[0], nbytes, stream)
+    if s != LOWM_OK:
+        raise LowmError(s, name)
 
 
 def release_workspaces() -> None:
     """Give the workspaces kept for the default streams back to torch's allocator."""
-    _kept.clear()
+    with _kept_lock:
+        _kept.clear()
 
 
 def _on(stream, device: int):
@@ -323,15 +333,11 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, *, scale=Non
     os = _rows(out, "out", bf16, q_shape, device)
     lse = torch.empty((q_tokens, heads), dtype=torch.float32, device=q.device) if return_lse else None
     nbytes = _attention_bytes(batch, q_tokens, heads, kv_heads, dim)
-    raw = _current_stream(device)
-    work, owner = _scratch(nbytes, device, raw)
-    s = function("lowm_paged_attention")(
+    _launch("lowm_paged_attention", (
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1], vc[2],
         num_pages, page_size, page_table.data_ptr(), table_stride, table_width, kv_lens.data_ptr(), cu_q.data_ptr(),
         out.data_ptr(), os[0], os[1], None if lse is None else lse.data_ptr(), batch, q_tokens, heads, kv_heads, dim,
-        1.0 / math.sqrt(dim) if scale is None else scale, window, work, nbytes, raw)
-    if s != LOWM_OK:
-        raise LowmError(s, "lowm_paged_attention")
+        1.0 / math.sqrt(dim) if scale is None else scale, window), nbytes, device, _current_stream(device))
     return (out, lse) if return_lse else out
 
 
@@ -375,11 +381,8 @@ def moe(x, router_weight, gate_up, down, top_k: int, *, scoring: str = "softmax"
         out = torch.empty(x_shape, dtype=bf16, device=x.device)
     out_stride = _row_stride(out, "out", bf16, x_shape, device)
     nbytes = _moe_bytes(tokens, hidden, inner, experts, top_k)
-    raw = _current_stream(device)
-    work, owner = _scratch(nbytes, device, raw)
-    s = function("lowm_moe")(
+    _launch("lowm_moe", (
         x.data_ptr(), x_stride, router_weight.data_ptr(), bias_ptr, gate_up.data_ptr(), down.data_ptr(),
-        out.data_ptr(), out_stride, tokens, hidden, inner, experts, top_k, kind, renormalize, scale, work, nbytes, raw)
-    if s != LOWM_OK:
-        raise LowmError(s, "lowm_moe")
+        out.data_ptr(), out_stride, tokens, hidden, inner, experts, top_k, kind, renormalize, scale),
+        nbytes, device, _current_stream(device))
     return out

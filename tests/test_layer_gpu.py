@@ -9,6 +9,7 @@ sum of the terms it enters.
 from __future__ import annotations
 
 import math
+import threading
 
 import pytest
 import torch
@@ -785,3 +786,36 @@ def test_workspaces_are_kept_for_the_default_stream_alone():
     assert torch.equal(layer.moe(x, router, w1, w2, 2), small)
     layer.release_workspaces()
     assert torch.equal(layer.moe(x, router, w1, w2, 2), small)
+
+
+def test_threads_on_the_default_stream():
+    # every thread's calls give what they give alone: attention with many cut items, and experts, on one workspace
+    def attention(seed):
+        q_lens, kv_lens = [1, 30, 5], [4000 + 100 * seed, 2000, 70]
+        q, kc, vc, table, cu = attention_inputs(q_lens, kv_lens, 8, 2, 128, 64, seed=seed)
+        lens, cu = (torch.tensor(z, dtype=torch.int32, device="cuda") for z in (kv_lens, cu))
+        return lambda: layer.paged_attention(q, kc, vc, table, lens, cu)
+
+    def experts(seed):
+        x, router, w1, w2 = moe_inputs(30 + seed, 512, 264, 40, seed=seed)
+        return lambda: layer.moe(x, router, w1, w2, 4)
+
+    calls = [attention(0), experts(1), attention(2), experts(3)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    outs = [[] for _ in calls]
+
+    def run(i):
+        for _ in range(60):
+            outs[i].append(calls[i]())
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    st, detail = lowm_gemm_sync_status()
+    assert st == 0, "a wait gave up: %#x" % detail
+    for w, o in zip(want, outs):
+        assert len(o) == 60 and all(torch.equal(w, z) for z in o)

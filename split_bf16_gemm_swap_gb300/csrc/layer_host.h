@@ -21,7 +21,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 // Defined in lowm_gemm.cu, which caches what they look up.
 lowm_status_t host_check_device(int *sms);   // LOWM_OK on sm_103; the SM count
 unsigned int *host_status_word();            // device address of the status word, or nullptr
-EncodeTiledFn host_encode_fn();              // cuTensorMapEncodeTiled, or nullptr
+EncodeTiledFn host_encode_fn();              // cuTensorMapEncodeTiled (for any host thread), or nullptr
 
 inline bool is_aligned(const void *p, uintptr_t bytes)
 {

@@ -69,9 +69,26 @@ constexpr int kSmemReservedPerCta = 1024;  // the runtime keeps 1 KiB per reside
 // ------------------------------------------------------------------ driver entry point
 using lowm::EncodeTiledFn;
 
+EncodeTiledFn g_encode = nullptr;   // the driver's cuTensorMapEncodeTiled
+
+// The encoder wants a current context, and a host thread has none before its
+// first runtime call that needs the device (looking the device up does not
+// make one).  Such a thread's first map fails with CUDA_ERROR_INVALID_CONTEXT:
+// make its device's primary context current, as a launch would, and encode again.
+CUresult encode_tiled(CUtensorMap *map, CUtensorMapDataType type, cuuint32_t rank, void *base, const cuuint64_t *dims,
+                      const cuuint64_t *strides, const cuuint32_t *box, const cuuint32_t *step,
+                      CUtensorMapInterleave interleave, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion,
+                      CUtensorMapFloatOOBfill fill)
+{
+    CUresult r = g_encode(map, type, rank, base, dims, strides, box, step, interleave, swizzle, promotion, fill);
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+        r = g_encode(map, type, rank, base, dims, strides, box, step, interleave, swizzle, promotion, fill);
+    return r;
+}
+
 EncodeTiledFn get_encode_fn()
 {
-    static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
         void *p = nullptr;
@@ -79,9 +96,9 @@ EncodeTiledFn get_encode_fn()
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
+            g_encode = reinterpret_cast<EncodeTiledFn>(p);
     });
-    return fn;
+    return g_encode ? encode_tiled : nullptr;
 }
 
 // ------------------------------------------------------------------ device checks

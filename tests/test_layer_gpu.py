@@ -788,6 +788,30 @@ def test_workspaces_are_kept_for_the_default_stream_alone():
     assert torch.equal(layer.moe(x, router, w1, w2, 2), small)
 
 
+def in_a_new_thread(call):
+    """`call()`'s result from a host thread that has made no CUDA call before."""
+    out = []
+    t = threading.Thread(target=lambda: out.append(call()))
+    t.start()
+    t.join()
+    assert out, "the thread's call raised"
+    return out[0]
+
+
+def test_first_calls_of_a_host_thread():
+    # all instances and their attributes are ready, so that nothing before the tensor maps gives the thread a context
+    x, router, w1, w2 = moe_inputs(4, 64, 32, 8)
+    want, got = (run(lambda: layer.moe(x, router, w1, w2, 2)) for run in (lambda f: f(), in_a_new_thread))
+    assert torch.equal(want, got)
+    q, kc, vc, table, cu = attention_inputs([1, 3], [50, 30], 8, 2, 128, 64)
+    lens, cu = torch.tensor([50, 30], dtype=torch.int32, device="cuda"), torch.tensor(cu, dtype=torch.int32, device="cuda")
+    want, got = (run(lambda: layer.paged_attention(q, kc, vc, table, lens, cu)) for run in (lambda f: f(), in_a_new_thread))
+    assert torch.equal(want, got)
+    want = gemm(x, rand(256, 64, seed=1))
+    fresh, out = rand(256, 64, seed=1), torch.empty_like(want)         # an operand whose map is not cached
+    assert torch.equal(in_a_new_thread(lambda: gemm(x, fresh, out)), want)
+
+
 def test_threads_on_the_default_stream():
     # every thread's calls give what they give alone: attention with many cut items, and experts, on one workspace
     def attention(seed):

@@ -9,6 +9,7 @@ none of them records a gradient.
 ``stream`` is as in :mod:`.lowm`.  A call with a stream runs as under
 ``with torch.cuda.stream(stream)``: the outputs and workspaces that it makes
 belong to that stream, and nothing is ordered against torch's current one.
+The tensors' device need not be torch's current one.
 Calls on a device's default stream share one workspace that is kept between
 them (:func:`release_workspaces`); they may come from several host threads.
 """
@@ -133,6 +134,7 @@ def _cuda(x, name: str) -> int:
 # takes longer than all checks of a call (2.9 us of a norm's 15.5 us on the host).
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 # The workspace of the calls on each device's default stream.  An operator with a workspace is two launches, and ctypes
@@ -168,7 +170,13 @@ def release_workspaces() -> None:
 
 
 def _on(stream, device: int):
-    """The context in which a call with an explicit stream runs."""
+    """The context in which a call on tensors of `device` runs: that device current, and `stream` if there is one.
+
+    The library launches on the current device and takes its SM count and status word from there, whatever device the
+    pointers belong to; a handle of 0 is the default stream of whichever device is current.
+    """
+    if stream is None:
+        return torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         stream = torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
@@ -189,7 +197,7 @@ def residual_norm(residual, block=None, *, post_weight=None, gate=None, pre_weig
     ``residual`` itself.  out_residual may be ``residual``, out may be ``block``.
     """
     device = _cuda(residual, "residual")
-    if stream is not None:
+    if stream is not None or _current_device() != device:
         with _on(stream, device):
             return residual_norm(residual, block, post_weight=post_weight, gate=gate, pre_weight=pre_weight,
                                  scale=scale, eps=eps, out_residual=out_residual, out=out)
@@ -248,7 +256,7 @@ def rope_append(q, k, v, cos_sin, positions, slots, k_cache, v_cache, *, section
     `out` may be q.
     """
     device = _cuda(q, "q")
-    if stream is not None:
+    if stream is not None or _current_device() != device:
         with _on(stream, device):
             return rope_append(q, k, v, cos_sin, positions, slots, k_cache, v_cache, sections=sections,
                                interleaved=interleaved, out=out)
@@ -308,7 +316,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, *, scale=Non
     dim ** -0.5.  Returns out, or (out, lse fp32 [q_tokens, heads]).
     """
     device = _cuda(q, "q")
-    if stream is not None:
+    if stream is not None or _current_device() != device:
         with _on(stream, device):
             return paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale=scale, window=window,
                                    out=out, return_lse=return_lse)
@@ -356,7 +364,7 @@ def moe(x, router_weight, gate_up, down, top_k: int, *, scoring: str = "softmax"
     experts' outputs down . (silu(gate . x) * (up . x)).
     """
     device = _cuda(x, "x")
-    if stream is not None:
+    if stream is not None or _current_device() != device:
         with _on(stream, device):
             return moe(x, router_weight, gate_up, down, top_k, scoring=scoring, bias=bias, renormalize=renormalize,
                        scale=scale, out=out)

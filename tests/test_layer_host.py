@@ -135,3 +135,26 @@ def test_a_call_made_while_another_is_enqueued_by_the_same_thread_goes_through(l
     library.call = call
     operators()["moe"]()
     assert calls == ["lowm_moe", "lowm_paged_attention"]
+
+
+@pytest.mark.parametrize("name", sorted(operators()))
+@pytest.mark.parametrize("current,device", [(0, 0), (0, 1), (1, 0)])
+def test_the_tensors_device_is_current_during_a_call(library, monkeypatch, name, current, device):
+    # the library launches on the current device, whatever device its pointers belong to
+    now, seen, entered = [current], [], []
+
+    @contextlib.contextmanager
+    def guard(index):
+        entered.append(index)
+        before, now[0] = now[0], index
+        try:
+            yield
+        finally:
+            now[0] = before
+
+    monkeypatch.setattr(layer, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", guard)
+    library.call = lambda n, args: seen.append((n, now[0])) or 0
+    operators(device)[name]()
+    assert seen == [("lowm_" + name, device)] and now == [current]
+    assert entered == ([] if current == device else [device])

@@ -180,6 +180,8 @@ def _on(stream, device: int):
     if not isinstance(stream, torch.cuda.Stream):
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         stream = torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
+    elif stream.device.index != device:
+        raise ValueError("stream must be on cuda:%d like the tensors, not %s" % (device, stream.device))
     return torch.cuda.stream(stream)
 
 

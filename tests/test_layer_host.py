@@ -158,3 +158,23 @@ def test_the_tensors_device_is_current_during_a_call(library, monkeypatch, name,
     operators(device)[name]()
     assert seen == [("lowm_" + name, device)] and now == [current]
     assert entered == ([] if current == device else [device])
+
+
+@pytest.mark.parametrize("name", sorted(operators()))
+def test_a_stream_of_another_device_is_refused(library, monkeypatch, name):
+    # its device would become current, and the call would take the current stream of the tensors' device instead
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 1234
+
+    entered = []
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: entered.append(s) or contextlib.nullcontext())
+    library.call = lambda n, args: pytest.fail("launched")
+    with pytest.raises(ValueError, match="stream"):
+        operators(0, stream=Stream())[name]()
+    assert not entered
+    library.call = lambda n, args: 0
+    monkeypatch.setattr(layer, "_current_device", lambda: 1)
+    stream = Stream()
+    operators(1, stream=stream)[name]()
+    assert entered == [stream]

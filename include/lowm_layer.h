@@ -116,8 +116,9 @@ lowm_status_t lowm_rope_append(const void *q, int64_t q_token_stride, int64_t q_
  *                 contents need not survive between calls
  * What a page holds past a sequence's length or before its window does not
  * matter, NaN included, and a value of a token that is not finite reaches the
- * rows that see the token and no others (in a chunk of several tokens, at the
- * price of walking those rows' keys one by one).  The result is deterministic.
+ * rows that see the token and no others (where only some rows of a chunk see
+ * it, at the price of a walk over at most 254 keys a row, some milliseconds
+ * whatever the lengths).  The result is deterministic.
  */
 lowm_status_t lowm_paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                                    const void *k_cache, int64_t k_page_stride, int64_t k_place_stride,

@@ -15,7 +15,9 @@
 // A CTA has four softmax warps (a thread owns a row = a TMEM lane), a warp
 // that feeds a ring of 64-key tiles by TMA, page by page, and two warps that
 // issue the MMAs: S = Q K^T into one of two TMEM buffers, and O += P V with P
-// (bf16, written over its S) from TMEM and V as the transposed operand.
+// (bf16, written over its S) from TMEM and V as the transposed operand.  The
+// second of them, while it waits for P, also clears from V what some rows must
+// not meet, weight 0 or not (in the softmax warps 2 to 7 % slower).
 // S of the next tile is computed while the softmax of this one runs, and the
 // two CTAs of an SM fill each other's gaps.  O is rescaled only when a row's
 // maximum has grown by 2^8 (the weights stay below 256, and bf16 and fp32 are
@@ -367,9 +369,16 @@ struct AttnSmem {
     static constexpr uint32_t kTileBytes = kTileKeys * DIM * 2;
     static constexpr uint32_t kRing = kTileRows * DIM * 2;              // [stages][halves][64 keys][64]
     static constexpr uint32_t kStages = DIM == 128 ? 5 : 10;            // 80 KiB: two CTAs fill an SM's 227 KiB
-    static constexpr uint32_t kBars = kRing + kStages * kTileBytes;     // full, empty [stages]; q; s, p, o [2]; drain
-    static constexpr uint32_t kNumBars = 2 * kStages + 8;
-    static constexpr uint32_t kSlot = kBars + kNumBars * 8;
+    // A wait for a full stage passes too early when the load before it in that stage has not landed yet: the
+    // barrier's parity is then still that of the phase before.  Loads (K0, K1, V0, K2, V1, ..., V of the last tile, then
+    // the next item's) may land in any order, so it must follow from what the waiting warp has seen.  At K of tile g
+    // that is K up to g - 1 and, by the O of g - 3, V up to there: not V of g - 1 and g - 2, which are among the three
+    // loads before.  At V of tile g it is V up to g - 1 and, by the weights of g - 1, K up to there: not K of g and
+    // g + 1, among the three loads before as well.
+    static_assert(kStages >= 4, "a warp would wait for a stage whose previous load may be under way");
+    static constexpr uint32_t kBars = kRing + kStages * kTileBytes;     // full, empty [stages]; q; s, p, o [2]; edges; drain
+    static constexpr uint32_t kNumBars = 2 * kStages + 9;
+    static constexpr uint32_t kSlot = kBars + kNumBars * 8;             // TMEM address, edge word
     static constexpr uint32_t kBytes = kSlot + 16;                      // 112.2 KiB: two CTAs an SM
 };
 
@@ -393,6 +402,25 @@ __device__ __forceinline__ Row row_of(const AttnParams &p, const Item &it, int r
     return w;
 }
 
+// Keys that all rows of an item see, [all_lo, all_hi] (none when all_lo > all_hi),
+// and those that some row sees, [lo, end).
+struct Seen {
+    int all_lo, all_hi, lo, end;
+    __device__ bool mixed() const { return all_hi + 1 < end; }   // the rows' tokens differ, and so do their keys
+};
+
+__device__ __forceinline__ Seen seen_by(const AttnParams &p, const Item &it)
+{
+    const int first = it.q_tile * kTileRows / p.group;
+    const int last = min(it.q_len - 1, (it.q_tile * kTileRows + kTileRows - 1) / p.group);
+    Seen s;
+    s.all_hi = it.kv - it.q_len + first;
+    s.end = it.kv - it.q_len + last + 1;
+    s.all_lo = p.window > 0 ? s.end - p.window : 0;
+    s.lo = p.window > 0 ? s.all_hi - p.window + 1 : 0;
+    return s;
+}
+
 template <int DIM>
 __device__ __forceinline__ void store_row(const AttnParams &p, const Row &w, int col, const float (&v)[32])
 {
@@ -414,14 +442,98 @@ __device__ __forceinline__ void store_row(const AttnParams &p, const Row &w, int
     }
 }
 
-// The rows of this warp whose bit is set in `rows`, written once more from the
-// keys first..last that they see alone, the whole warp on a row: the weights
-// (2^(score - shift), in bf16 as in the MMA) times `factor` to `out`, or to the
-// row's part.  Far slower than the MMAs; reached only by chunks whose values
-// are not finite.
+constexpr int kCleanKeys = 16;                       // looked at at once: all loads before the first use
+
+// x * 0 + sum for two bf16: 0 while x is finite, else NaN.
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t sum)
+{
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
+    return sum;
+}
+
+// Clears the values that are not finite of this lane's part of 16 keys from
+// `key` on, where only some rows see them.
 template <int DIM>
-__device__ __noinline__ void rows_again(const AttnParams &p, unsigned rows, int sequence, const Row &mine, int first, int last,
-                                        float shift, float factor, int64_t slot, int r)
+__device__ __noinline__ void take_out(uint4 *at, const Seen &seen, int key)
+{
+    key += (threadIdx.x & 31) >> 3;
+#pragma unroll 1
+    for (int i = 0; i < kCleanKeys / 4; ++i, key += 4)
+#pragma unroll 1
+        for (int half = 0; half < DIM / 64; ++half) {
+            if (key >= seen.all_lo && key <= seen.all_hi)
+                continue;
+            uint32_t *words = reinterpret_cast<uint32_t *>(at + half * (kTileKeys * 8) + i * 32);
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t sign = ((words[w] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;   // exponent all ones
+                words[w] &= ~(sign | (sign - (sign >> 15)));                                    // and the 15 bits below
+            }
+        }
+}
+
+// Makes a tile of V (keys key0.., 128-byte swizzled) fit to meet the weights of
+// all rows, by one warp: a weight of 0 does not silence what is not finite.  Keys
+// that no row of the item sees may hold anything (the rest of a sequence's last
+// page, pages that a window has left behind) and are cleared.  Of keys that some
+// rows see and others do not, the values that are not finite are taken out, to be
+// added to the rows that see them at the item's end; true when there were any.
+template <int DIM>
+__device__ __forceinline__ bool clean_values(uint8_t *tile, const Seen &seen, int key0)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t found = 0;
+#pragma unroll 1
+    for (int k0 = 0; k0 < kTileKeys; k0 += kCleanKeys) {
+        if (key0 + k0 >= seen.all_lo && key0 + k0 + kCleanKeys - 1 <= seen.all_hi)
+            continue;
+        uint4 *at = reinterpret_cast<uint4 *>(tile + k0 * 128) + lane;   // 4 keys of 64 elements a step
+        uint4 x[kCleanKeys / 4][DIM / 64];
+#pragma unroll
+        for (int i = 0; i < kCleanKeys / 4; ++i)
+#pragma unroll
+            for (int half = 0; half < DIM / 64; ++half)
+                x[i][half] = at[half * (kTileKeys * 8) + i * 32];
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < kCleanKeys / 4; ++i) {
+            const int key = key0 + k0 + 4 * i + (lane >> 3);
+            uint32_t here = 0;                       // stays 0 (or -0) while all are finite
+#pragma unroll
+            for (int half = 0; half < DIM / 64; ++half) {
+                here = times_zero(x[i][half].x, here);
+                here = times_zero(x[i][half].y, here);
+                here = times_zero(x[i][half].z, here);
+                here = times_zero(x[i][half].w, here);
+            }
+            if (key < seen.lo || key >= seen.end) {
+#pragma unroll
+                for (int half = 0; half < DIM / 64; ++half)
+                    at[half * (kTileKeys * 8) + i * 32] = make_uint4(0, 0, 0, 0);
+            } else if (key < seen.all_lo || key > seen.all_hi) {
+                bad |= here & 0x7fff7fffu;
+            }
+        }
+        if (bad)
+            take_out<DIM>(at, seen, key0 + k0);
+        found |= bad;
+    }
+    ptx::fence_proxy_async_shared();
+    return __any_sync(0xffffffffu, found != 0);
+}
+
+// Adds the values that are not finite of keys that only some rows of the item
+// see, which were taken out of V for the MMA: for each row of this warp whose bit
+// is set in `rows`, those of the keys key_begin..key_end - 1 that it sees, times
+// their weight (2^(score - shift), in bf16 as in the MMA) and `factor`, onto `out`
+// or the row's part.  The whole warp is on a row.  An item has at most 128 tokens,
+// so these keys are among the last 127 that a row sees, or the first 127 of its
+// window; among them are keys that all rows see, whose infinities are in O already
+// and change nothing a second time.  A warp's 32 rows take some milliseconds at
+// worst, whatever the lengths: far below the limit of the other warps' waits.
+template <int DIM>
+__device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows, int sequence, const Row &mine, int key_begin,
+                                             int key_end, float shift, float factor, int64_t slot, int r)
 {
     constexpr int E = DIM / 32;
     const int lane = threadIdx.x & 31, r0 = r - lane;
@@ -430,31 +542,54 @@ __device__ __noinline__ void rows_again(const AttnParams &p, unsigned rows, int 
         const int l = __ffs(rows) - 1;
         rows &= rows - 1;
         const int token = __shfl_sync(0xffffffffu, mine.token, l), head = __shfl_sync(0xffffffffu, mine.q_head, l);
-        const int lo = __shfl_sync(0xffffffffu, first, l), hi = __shfl_sync(0xffffffffu, last, l);
+        const int lo = __shfl_sync(0xffffffffu, mine.lo, l), hi = __shfl_sync(0xffffffffu, mine.hi, l);
         const float base = __shfl_sync(0xffffffffu, shift, l), f = __shfl_sync(0xffffffffu, factor, l);
         const int g = head / p.group;
-        float q[E], acc[E] = {};
-        for (int e = 0; e < E; ++e)
-            q[e] = p.q_sign * __bfloat162float(p.q[token * p.q_ts + head * p.q_hs + lane * E + e]);
-        for (int key = lo; key <= hi; ++key) {
+        float acc[E] = {};
+        bool any = false;
+        const int first_end = p.window > 0 ? lo + kTileRows - 2 : -1, last_begin = max(lo, hi - kTileRows + 2);
+#pragma unroll 1
+        for (int key = max(max(lo, 0), key_begin); key <= hi && key < key_end; ++key) {
+            if (key > first_end && key < last_begin) {
+                key = last_begin - 1;
+                continue;
+            }
             const int64_t page = p.table[sequence * p.table_stride + (key >> p.page_shift)];
             const int64_t place = key & (p.page_size - 1);
-            const bool in = page >= 0 && page < p.num_pages;
+            if (page < 0 || page >= p.num_pages)     // reads as zeros
+                continue;
+            float v[E];
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                v[e] = __bfloat162float(p.v[page * p.v_page + place * p.v_place + g * p.v_head + lane * E + e]);
+                bad = bad || !(fabsf(v[e]) < CUDART_INF_F);
+            }
+            if (!__any_sync(0xffffffffu, bad))
+                continue;
+            any = true;
             float s = 0.f;
-            for (int e = 0; e < E && in; ++e)
-                s = fmaf(q[e], __bfloat162float(p.k[page * p.k_page + place * p.k_place + g * p.k_head + lane * E + e]), s);
+            for (int e = 0; e < E; ++e)
+                s = fmaf(__bfloat162float(p.q[token * p.q_ts + head * p.q_hs + lane * E + e]),
+                         __bfloat162float(p.k[page * p.k_page + place * p.k_place + g * p.k_head + lane * E + e]), s);
             for (int o = 16; o > 0; o >>= 1)
                 s += __shfl_xor_sync(0xffffffffu, s, o);
-            const float a = __bfloat162float(__float2bfloat16_rn(ex2(fmaf(s, p.scale_log2, -base))));
-            for (int e = 0; e < E && in; ++e)
-                acc[e] = fmaf(a, __bfloat162float(p.v[page * p.v_page + place * p.v_place + g * p.v_head + lane * E + e]), acc[e]);
+            // (a weight too small for a float still carries an infinity)
+            const float a = s == -p.q_sign * CUDART_INF_F
+                                ? 0.f
+                                : fmaxf(__bfloat162float(__float2bfloat16_rn(ex2(fmaf(p.q_sign * s, p.scale_log2, -base)))), 1e-30f);
+            for (int e = 0; e < E; ++e)
+                if (!(fabsf(v[e]) < CUDART_INF_F))
+                    acc[e] = fmaf(a, v[e], acc[e]);
         }
-        for (int e = 0; e < E; ++e) {
+        for (int e = 0; e < E && any; ++e) {
             const int d = lane * E + e;
-            if (slot < 0)
-                p.out[token * p.o_ts + head * p.o_hs + d] = __float2bfloat16_rn(acc[e] * f);
-            else
-                reinterpret_cast<float *>(p.parts + (slot * (DIM / 4) + d / 4) * p.slot_rows + r0 + l)[d & 3] = acc[e];
+            if (slot < 0) {
+                __nv_bfloat16 *o = p.out + token * p.o_ts + head * p.o_hs + d;
+                *o = __float2bfloat16_rn(fmaf(acc[e], f, __bfloat162float(*o)));
+            } else {
+                reinterpret_cast<float *>(p.parts + (slot * (DIM / 4) + d / 4) * p.slot_rows + r0 + l)[d & 3] += acc[e];
+            }
         }
     }
 }
@@ -473,7 +608,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     const uint32_t sbase = ptx::smem_u32(smem);
     const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kStages;
     const uint32_t bar_q = bar_empty + 8 * L::kStages, bar_s = bar_q + 8, bar_p = bar_s + 16, bar_o = bar_p + 16,
-                   bar_drain = bar_o + 16;
+                   bar_edges = bar_o + 16, bar_drain = bar_edges + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (sbase & 1023u) {
         if (threadIdx.x == 0)
@@ -492,6 +627,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             ptx::mbar_init(bar_p + 8 * i, 4);
             ptx::mbar_init(bar_o + 8 * i, 1);
         }
+        ptx::mbar_init(bar_edges, 1);
         ptx::mbar_init(bar_drain, 2);
         ptx::fence_mbarrier_init_cluster();
         ptx::fence_proxy_async_shared();
@@ -613,9 +749,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         __syncwarp();
                     }
                 } else {
+                    const Seen seen = seen_by(p, c.it);
+                    bool edges = false;
                     for (int j = 0; j < n && ok; ++j, ++g) {            // O (+)= P . V
                         const uint32_t at = i + (j + 1 < n ? 2 * j + 2 : 2 * j + 1), s = at % L::kStages;
                         wait(bar_full + 8 * s, (at / L::kStages) & 1, kErrAttnFull);
+                        // (while the softmax warps are at the tile's weights)
+                        const int key0 = (c.it.first_tile + c.from + j) * kTileKeys;
+                        if (ok && (key0 < seen.all_lo || key0 + kTileKeys - 1 > seen.all_hi))
+                            edges |= clean_values<DIM>(smem + L::kRing + s * L::kTileBytes, seen, key0);
                         wait(bar_p + 8 * (g & 1), (g >> 1) & 1, kErrAttnWeights);
                         ptx::tcgen05_fence_after_thread_sync();
                         if (!ok)
@@ -631,6 +773,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         }
                         __syncwarp();
                     }
+                    if (ok && lane == 0) {
+                        *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot + 4) = edges;
+                        ptx::mbar_arrive(bar_edges);
+                    }
+                    __syncwarp();
                 }
                 i += 2 * n;
                 ++items;
@@ -643,7 +790,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             // -------------------------------------------------------- softmax: thread = row = TMEM lane
             const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
             const int r = threadIdx.x;
-            uint32_t i = 0, g = 0;
+            uint32_t g = 0, items = 0;
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
                 if (!wait_short(bar, parity)) {
@@ -697,17 +844,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 const int from = c.from, n = c.to - c.from;
                 const Row w = row_of(p, it, r);
                 const bool warp_has_rows = __any_sync(0xffffffffu, w.valid);
-                // Keys every row of the tile sees: no mask inside [all_lo, all_hi].
-                const int all_hi = it.kv - it.q_len + it.q_tile * kTileRows / p.group;
-                const int last_token = min(it.q_len - 1, (it.q_tile * kTileRows + kTileRows - 1) / p.group);
-                const int all_lo = p.window > 0 ? it.kv - it.q_len + last_token - p.window + 1 : 0;
-                // Keys some row sees: [seen_lo, seen_end).
-                const int seen_lo = p.window > 0 ? all_hi - p.window + 1 : 0, seen_end = it.kv - it.q_len + last_token + 1;
-
+                const Seen seen = seen_by(p, it);
+                const int all_lo = seen.all_lo, all_hi = seen.all_hi;   // no mask inside
                 float m = -CUDART_INF_F, l = 0.f;                       // maximum (raw score) and sum of this row
                 for (int j = 0; j < n; ++j, ++g) {
-                    // the ring stage of this tile's V: K0 first, then K(j+1), V(j) in turns
-                    const uint32_t v_index = i + (j + 1 < n ? 2 * (uint32_t)j + 2 : 2 * (uint32_t)j + 1);
                     wait(bar_s + 8 * (g & 1), (g >> 1) & 1, kErrAttnScores);
                     if (!ok)
                         break;
@@ -776,22 +916,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         tmem_st_x32(s_addr, pk);
                         ptx::tmem_wait_st();
                     }
-                    if (key0 < seen_lo || key0 + kTileKeys > seen_end) {
-                        // Keys that no row of the item sees may hold anything (the rest of a sequence's last page,
-                        // pages that a window has left behind): a weight of 0 would not silence NaN, so their V is
-                        // cleared.
-                        const uint32_t s = v_index % L::kStages;
-                        wait(bar_full + 8 * s, (v_index / L::kStages) & 1, kErrAttnFull);
-                        if (!ok)
-                            break;
-                        uint4 *tile = reinterpret_cast<uint4 *>(smem + L::kRing + s * L::kTileBytes);
-                        for (int c = r; c < kTileKeys * 8 * (int)L::kHalves; c += kTileRows) {
-                            const int key = key0 + ((c >> 3) & (kTileKeys - 1));
-                            if (key < seen_lo || key >= seen_end)
-                                tile[c] = make_uint4(0, 0, 0, 0);
-                        }
-                        ptx::fence_proxy_async_shared();
-                    }
                     ptx::tcgen05_fence_before_thread_sync();
                     __syncwarp();
                     if (lane == 0)
@@ -799,7 +923,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 }
                 if (!ok)
                     break;
-                i += 2 * n;
                 // The next item's queries before this one's rows: every S of this one is complete, and the
                 // first products of the next run while its rows are written.
                 const bool whole = n == it.tiles;
@@ -808,25 +931,31 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                     p.cuts[blockIdx.x] = {(it.start + kItemCost + it.tiles - 1) / share - (int)blockIdx.x + 1, it.q0, it.q_len,
                                           it.head, it.q_tile};
                 const int sequence = it.b, key_begin = (it.first_tile + from) * kTileKeys, key_end = key_begin + n * kTileKeys;
-                const bool mixed = all_hi + 1 < seen_end;               // the rows' tokens differ, and so do their keys
+                const bool mixed = seen.mixed();
                 more = next_piece(p, c, end);
                 if (more)
                     load_q(it);
                 wait(bar_o + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, kErrAttnOutput);
                 if (!ok)
                     break;
+                // Values were taken out of this item's V.  (The word is written again only after this warp's weights of the
+                // next item's last tile.)
+                bool edges = false;
+                if (mixed) {
+                    wait(bar_edges, items & 1, kErrAttnOutput);
+                    if (!ok)
+                        break;
+                    edges = ptx::ld_volatile_shared(sbase + L::kSlot + 4) != 0;
+                }
+                ++items;
                 // The item's rows: finished here, or a part for the join.
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 if (warp_has_rows) {
-                    uint64_t zero = 0;                                  // stays 0 while O is finite
 #pragma unroll
                     for (int c = 0; c < DIM; c += 32) {
                         uint32_t o[32];
                         tmem_ld_x32(lane_base + kOColumn + c, o);
                         ptx::tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-                            zero = fma2(pack2(o[k], o[k + 1]), 0, zero);
                         if (!w.valid)
                             continue;
                         if (whole) {
@@ -850,13 +979,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         float2 *ml = reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * (DIM / 4));
                         ml[slot * p.slot_rows + r] = make_float2(m * p.scale_log2, l);
                     }
-                    // V that is not finite has met the weights 0 of rows that do not see its key: those rows again,
-                    // key by key.
-                    const float2 z = unpack2(zero);
-                    const unsigned again = __ballot_sync(0xffffffffu, mixed && w.valid && !(z.x + z.y == 0.f));
-                    if (again)
-                        rows_again<DIM>(p, again, sequence, w, max(w.lo, key_begin), min(w.hi, key_end - 1),
-                                        m == -CUDART_INF_F ? 0.f : m * p.scale_log2, whole ? inv : 1.f, whole ? -1 : slot, r);
+                    if (edges)
+                        add_edge_values<DIM>(p, __ballot_sync(0xffffffffu, w.valid), sequence, w, key_begin, key_end,
+                                             m == -CUDART_INF_F ? 0.f : m * p.scale_log2, whole ? inv : 1.f,
+                                             whole ? -1 : slot, r);
                 }
             }
         }

@@ -449,6 +449,47 @@ def test_attention_values_that_are_not_finite_reach_only_rows_that_see_them(dim,
         run_attention(q, kc, vc, table, [kv, 70], cu, window)
 
 
+def least_time(call, n=10):
+    """Shortest device time in us of `n` calls."""
+    best = math.inf
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        best = min(best, 1e3 * a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(128, 8, 8), (64, 16, 4)])
+@pytest.mark.parametrize("window", [0, 1500])
+def test_attention_values_that_are_not_finite_in_a_long_prefix(dim, heads, kv_heads, window):
+    # A value that all rows of a tile see costs nothing: the products give what it gives.  One in the part that only
+    # some rows see (by the chunk's own keys, or where the window ends) costs a walk over that part, at most 128 keys at
+    # each end, whatever the length: 32 rows of 256 keys a warp at a few thousand cycles each are below 20 ms.
+    kv, q_len, page = 4096, 64, 64
+    q, kc, vc, table, cu = attention_inputs([q_len], [kv], heads, kv_heads, dim, page, seed=dim)
+    lens, cu32 = torch.tensor([kv], dtype=torch.int32, device="cuda"), torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+    def call():
+        return layer.paged_attention(q, kc, vc, table, lens, cu32, window=window)
+
+    call()
+    clean = least_time(call)
+    first = max(0, kv - window) if window else 0                  # the last new token's first key
+    where = {"common": [first + 100, kv - q_len - 200], "edges": [kv - 40, kv - 2] + ([first - 30] if window else []),
+             "both": [first + 100, kv - 40]}
+    for name, keys in where.items():
+        kept = vc.clone()
+        for n, j in enumerate(keys):
+            vc[int(table[0, j // page]), j % page, :, n::5] = [float("inf"), float("nan"), float("-inf")][n % 3]
+        run_attention(q, kc, vc, table, [kv], cu, window)
+        took = least_time(call)
+        assert took < (2 * clean + 20 if name == "common" else 20e3), (name, took, clean)
+        vc.copy_(kept)
+
+
 def test_attention_pages_behind_the_window_may_hold_anything():
     q, kc, vc, table, cu = attention_inputs([3, 1], [300, 200], 4, 2, 128, 16)
     clean = run_attention(q, kc, vc, table, [300, 200], cu, window=50)

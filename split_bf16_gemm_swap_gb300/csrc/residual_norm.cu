@@ -299,13 +299,21 @@ lowm_status_t launch_norm(const NormParams &p, bool f32, int grid, int threads, 
                       dim3((unsigned)grid), dim3((unsigned)threads), 0, stream, p);
 }
 
-bool range_overlaps(const void *a, int64_t a_stride, int64_t a_size, const void *b, int64_t b_stride, int64_t b_size,
-                    int tokens, int hidden)
+// Rows a of one tensor share bytes with rows b of another.  Rows of one stride may
+// lie between each other (halves of a wider matrix); other strides are told
+// apart by their extents alone.
+bool rows_overlap(const void *a, int64_t a_stride, int64_t a_size, const void *b, int64_t b_stride, int64_t b_size,
+                  int tokens, int hidden)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     const uintptr_t nx = (uintptr_t)(((tokens - 1) * a_stride + hidden) * a_size);
     const uintptr_t ny = (uintptr_t)(((tokens - 1) * b_stride + hidden) * b_size);
-    return x < y + ny && y < x + nx;
+    if (x >= y + ny || y >= x + nx)
+        return false;
+    if (a_stride * a_size != b_stride * b_size)
+        return true;
+    const uintptr_t stride = (uintptr_t)(a_stride * a_size), apart = y >= x ? (y - x) % stride : (stride - (x - y) % stride) % stride;
+    return apart < (uintptr_t)(hidden * a_size) || stride - apart < (uintptr_t)(hidden * b_size);
 }
 
 }  // namespace
@@ -337,7 +345,7 @@ extern "C" lowm_status_t lowm_residual_norm(const void *residual, int residual_f
     if (!is_aligned(residual, size) || !is_aligned(out_residual, size) || !is_aligned(block, 2) ||
         !is_aligned(post_weight, 2) || !is_aligned(gate, 2) || !is_aligned(pre_weight, 2) || !is_aligned(out, 2))
         return LOWM_ERR_MISALIGNED;
-    if (out_residual && range_overlaps(out_residual, out_residual_stride, size, out, out_stride, 2, tokens, hidden))
+    if (out_residual && rows_overlap(out_residual, out_residual_stride, size, out, out_stride, 2, tokens, hidden))
         return LOWM_ERR_INVALID_ARGUMENT;
     int sms = 0;
     const lowm_status_t st = host_check_device(&sms);

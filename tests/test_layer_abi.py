@@ -75,6 +75,9 @@ def norm(**kw):
     (dict(os=63), INVALID), (dict(ors=63), INVALID), (dict(rs=-1), INVALID), (dict(bs=-64), INVALID),
     (dict(residual=PTR + 1), MISALIGNED), (dict(f32=1, residual=PTR + 2), MISALIGNED), (dict(out=PTR + 1), MISALIGNED),
     (dict(out=2 * PTR + 128), INVALID),                # out inside out_residual
+    (dict(out=2 * PTR + 64, ors=128, os=128), INVALID), (dict(out=2 * PTR - 64, ors=128, os=128), INVALID),
+    (dict(out=2 * PTR + 256, ors=128, os=128), INVALID), (dict(out=2 * PTR - 256, ors=128, os=128), INVALID),
+    (dict(out=2 * PTR + 128, f32=1, ors=96, os=192), INVALID), (dict(out=2 * PTR + 128, ors=128, os=136), INVALID),
 ])
 def test_norm_refusals(kw, want):
     assert norm(**kw) == want

@@ -140,6 +140,23 @@ def test_norm_in_place():
     assert out is block and torch.equal(block, want[1]) and torch.equal(new, want[0])
 
 
+@pytest.mark.parametrize("hidden", [64, 98])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("swapped", [False, True])
+def test_norm_outputs_side_by_side(hidden, f32, swapped):
+    # both outputs' rows in the rows of one buffer
+    t, size = 37, 4 if f32 else 2
+    row = hidden * (size + 2)
+    buf = torch.zeros(t * row, dtype=torch.uint8, device="cuda")
+    at_new, at_out = (2 * hidden, 0) if swapped else (0, hidden * size)
+    new = buf.view(torch.float32 if f32 else BF).as_strided((t, hidden), (row // size, 1), at_new // size)
+    out = buf.view(BF).as_strided((t, hidden), (row // 2, 1), at_out // 2)
+    res, block = rand(t, hidden, seed=1, dtype=torch.float32 if f32 else BF), rand(t, hidden, seed=2)
+    want = layer.residual_norm(res, block)
+    layer.residual_norm(res, block, out_residual=new, out=out)
+    assert torch.equal(new, want[0]) and torch.equal(out, want[1])
+
+
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
 @pytest.mark.parametrize("tokens,hidden", [(5, 999), (4001, 1313)])
 def test_norm_in_place_odd_rows(tokens, hidden, dtype):

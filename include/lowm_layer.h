@@ -104,7 +104,7 @@ lowm_status_t lowm_rope_append(const void *q, int64_t q_token_stride, int64_t q_
  * A row that sees no key (p < 0) gets zeros and lse = -inf.
  *   q, out        [q_tokens, heads, dim] bf16 by token and head stride
  *   k_cache, v_cache  as in lowm_rope_append; base 16-byte aligned, strides
- *                 multiples of 8
+ *                 multiples of 8 (of a dimension of one they may be anything)
  *   page_table    int32 [batch, table_width] by page_table_stride: the pages of
  *                 a sequence in order.  An entry outside the cache reads as zeros
  *   kv_lens       int32 [batch]; taken as at most table_width * page_size

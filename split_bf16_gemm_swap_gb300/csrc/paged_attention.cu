@@ -1167,10 +1167,13 @@ extern "C" lowm_status_t lowm_paged_attention(
         return LOWM_ERR_INVALID_ARGUMENT;
     const int64_t cache_strides[] = {k_page_stride, k_place_stride, k_cache_head_stride,
                                      v_page_stride, v_place_stride, v_cache_head_stride};
-    for (int64_t s : cache_strides) {
-        if (s < 0)
+    const int64_t extents[] = {num_pages, page_size, kv_heads, num_pages, page_size, kv_heads};
+    for (int i = 0; i < 6; ++i) {
+        if (extents[i] == 1)                     // the stride of a single one is not used
+            continue;
+        if (cache_strides[i] < 0)
             return LOWM_ERR_INVALID_ARGUMENT;
-        if (s & 7)
+        if (cache_strides[i] & 7)
             return LOWM_ERR_MISALIGNED;
     }
     if (q_token_stride < 0 || q_head_stride < 0 || out_token_stride < 0 || out_head_stride < 0 || page_table_stride < 0)
@@ -1180,7 +1183,6 @@ extern "C" lowm_status_t lowm_paged_attention(
         !is_aligned(lse, 4))
         return LOWM_ERR_MISALIGNED;
     // The tensor maps take strides below 2^40 bytes, and no stride of 0 where it is used.
-    const int64_t extents[] = {num_pages, page_size, kv_heads, num_pages, page_size, kv_heads};
     for (int i = 0; i < 6; ++i)
         if (extents[i] > 1 && (cache_strides[i] == 0 || cache_strides[i] >= ((int64_t)1 << 39)))
             return LOWM_ERR_INVALID_ARGUMENT;

@@ -544,6 +544,15 @@ def test_attention_strides(layout):
                                                   torch.tensor(cu, dtype=torch.int32, device="cuda")))
 
 
+def test_attention_strides_of_single_dimensions():
+    # a cache of one page and one head: their strides mean nothing
+    page, dim = 64, 64
+    q, kc, vc, table, cu = attention_inputs([2], [60], 4, 1, dim, page, spare=0)
+    assert kc.shape == (1, page, 1, dim)
+    kc, vc = kc.as_strided(kc.shape, (3, dim, 5, 1)), vc.as_strided(vc.shape, (0, dim, 1, 1))
+    run_attention(q, kc, vc, table, [60], cu)
+
+
 def test_attention_and_append_past_32_bits():
     # one buffer of 2^32 + elements serves as both caches; the sequence's pages straddle and follow 2^31 and 2^32
     kv_heads, dim, page = 2, 64, 64

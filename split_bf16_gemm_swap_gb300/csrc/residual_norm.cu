@@ -8,8 +8,9 @@
 // launch, one memory latency and the two reductions (4 x 4096: 2.4 us); at
 // prompt sizes it is the bandwidth of r, y, r' and n (8192 x 4096 bf16: 43.7 us,
 // 6.1 TB/s; with an fp32 residual and a gate per token 73.9 us, 6.4 TB/s).  Rows
-// of odd widths have their weights by single loads and a warp more, and cost up
-// to twice as much (8192 x 4095: 85 us, one CTA an SM; 8000 x 3001: 63 us).
+// of odd widths have their weights by single loads and a warp more, or all by
+// single loads, and cost up to twice as much (8000 x 4095 with a post weight
+// 102 us; 8000 x 3001 64 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -134,10 +135,7 @@ __device__ __forceinline__ float block_sum(float x, float *scratch)
 // the row's first 16-byte boundary; the up to 14 elements before the first and
 // behind the last piece are a lane's each of one more warp, so that no warp
 // runs both forms of an access.  (Rows of one CTA lie alike: a grid that walks
-// is a multiple of 8.)  Against one element at a time: 150 x 2305 3.2 -> 2.5 us,
-// 300 x 999 with an fp32 residual 4.6 -> 2.8, 8000 x 3001 85 -> 63; narrow rows by
-// the thousand gain nothing or lose (8000 x 601 15.7 for 17.2 us; with an fp32
-// residual and a gate per token 21.0 for 18.6).
+// is a multiple of 8.)  Not for every width: lowm_residual_norm has the rule.
 // A CTA walks rows blockIdx.x, blockIdx.x + gridDim.x, ...: the weights stay in
 // registers, and the next row is requested before this one's reductions.
 // (LOOP false: one row a CTA, without the registers of the second.)
@@ -379,12 +377,29 @@ extern "C" lowm_status_t lowm_residual_norm(const void *residual, int residual_f
                      !((block_stride | gate_stride | out_stride) & 7) && is_aligned(post_weight, 16) &&
                      is_aligned(gate, 16) && is_aligned(pre_weight, 16);
     auto alike = [&](bool used, int64_t stride) { return !used || ((stride - out_stride) & 7) == 0; };
-    const bool edges = !vec && bases && alike(true, residual_stride) && alike(block != nullptr, block_stride) &&
-                       alike(out_residual != nullptr, out_residual_stride) && alike(gate_stride != 0, gate_stride) &&
-                       hidden <= kMaxHidden - 512;   // 31 warps and the edges'
+    const bool lie_alike = bases && alike(true, residual_stride) && alike(block != nullptr, block_stride) &&
+                           alike(out_residual != nullptr, out_residual_stride) && alike(gate_stride != 0, gate_stride) &&
+                           hidden <= kMaxHidden - 512;   // 31 warps and the edges'
     const bool f32 = residual_f32 != 0;
-    const int elems = hidden <= (edges ? kMaxHidden - 512 : kMaxHidden) / 2 ? 8 : 16;
-    const int threads = ((hidden + elems - 1) / elems + 31) / 32 * 32 + (edges ? 32 : 0);
+    auto elems_of = [&](bool e) { return hidden <= (e ? kMaxHidden - 512 : kMaxHidden) / 2 ? 8 : 16; };
+    auto threads_of = [&](bool e) { return ((hidden + elems_of(e) - 1) / elems_of(e) + 31) / 32 * 32 + (e ? 32 : 0); };
+    // With edges or element by element?  The pieces save instructions and the edges cost a warp, which can cost an SM
+    // one of its CTAs (of 1024 threads) and then loses where rows are many and bring much (GB300, element by element ->
+    // edges; fp32 residual and a gate per token: 8000 x 4095 105 -> 143 us, 8000 x 601 18.0 -> 20.2, 1000 x 999 5.0 -> 5.7,
+    // but 8000 x 3001, as many CTAs, 87.1 -> 81.8, and 1000 x 513, one round, 4.3 -> 3.5).  Rows that bring little gain
+    // all the same down to two CTAs an SM (bf16 without a gate: 8000 x 2305 53.3 -> 44.7, 8000 x 601 15.1 -> 12.0; with a
+    // post weight 17.3 -> 15.7, but 8000 x 4095, one CTA, 102 -> 114); those of one warp do not (8000 x 65 8.6 -> 9.1), and
+    // below 128 elements nothing does.  Where the edges' warp makes it 16 elements a thread instead of 8, bare rows alone
+    // gain (8000 x 8191 208 -> 192, with a post weight 239 -> 245, with all 255 -> 331).
+    bool edges = !vec && lie_alike && hidden > 128;
+    if (edges) {
+        const int with = threads_of(true), ctas = 1024 / with;
+        const int streams = 1 + f32 + (gate_stride != 0) + (post_weight != nullptr);
+        edges = elems_of(true) != elems_of(false) ? streams == 1
+                                                  : tokens <= sms * ctas || ctas == 1024 / threads_of(false) ||
+                                                        (streams <= 2 && with > 64 && ctas >= 2);
+    }
+    const int elems = elems_of(edges), threads = threads_of(edges);
     if (elems == 16)
         return vec     ? launch_norm<8, 16, false, false>(p, f32, tokens, threads, stream)
                : edges ? launch_norm<8, 16, false, true>(p, f32, tokens, threads, stream)

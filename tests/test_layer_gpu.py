@@ -167,6 +167,16 @@ def test_norm_in_place_odd_rows(tokens, hidden, dtype):
     assert new is res and out is block and torch.equal(res, want[0]) and torch.equal(block, want[1])
 
 
+@pytest.mark.parametrize("tokens,hidden", [(700, 65), (1300, 129), (3000, 385), (2500, 1313), (1100, 2305), (400, 3001),
+                                           (900, 4095), (330, 8191), (330, 12001)])
+@pytest.mark.parametrize("f32,gated", [(False, False), (False, True), (True, False), (True, True)])
+def test_norm_odd_rows_with_and_without_edges(tokens, hidden, f32, gated):
+    # widths, batches and operands on both sides of the rule that chooses between the two forms
+    res = rand(tokens, hidden, seed=1, dtype=torch.float32 if f32 else BF)
+    check_norm(res, rand(tokens, hidden, seed=2), rand(hidden, seed=4) if gated else None,
+               rand(tokens, hidden, seed=3) if gated else None, rand(hidden, seed=5), 0.7)
+
+
 def test_norm_broadcast_odd_rows():
     # one residual row for all tokens, then one block row: they lie differently from the outputs' rows
     row = rand(1, 2305, seed=1)

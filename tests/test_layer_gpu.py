@@ -249,6 +249,19 @@ def test_rope_append(tokens, heads, kv_heads, dim, rotary, sections, interleaved
     check_rope(tokens, heads, kv_heads, dim, rotary, sections, interleaved, 16)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens", [303, 304, 400, 1216, 1300])
+@pytest.mark.parametrize("heads,kv_heads,dim,rotary,sections", [
+    (8, 2, 128, 128, (64,)), (7, 7, 64, 32, (5, 6, 5)), (9, 3, 96, 48, (11, 13)), (1, 1, 1024, 1024, (512,)),
+    (33, 11, 48, 48, (24,)),                                                    # 16-byte pieces
+    (5, 5, 17, 10, (2, 0, 3)), (5, 1, 70, 40, (20,)), (3, 1, 300, 300, (100, 50)), (11, 2, 30, 24, (12,)),   # single pairs
+])
+def test_rope_append_many_tokens(tokens, heads, kv_heads, dim, rotary, sections, interleaved):
+    # from 2 tokens an SM on, and again from 8, a token has fewer threads with more heads each (152 SMs: 304, 1216),
+    # down to one head at a time where a head alone has more pairs than that, and with a ragged last round
+    check_rope(tokens, heads, kv_heads, dim, rotary, sections, interleaved, 16)
+
+
 @pytest.mark.parametrize("shift", [1, 8])
 def test_rope_strided(shift):
     check_rope(11, 4, 2, 64, 64, (32,), False, 7, shift=shift)

@@ -842,6 +842,31 @@ def test_promised_inputs_behind_a_layer_operator():
             assert torch.equal(got, gemm(out[-8:], w)), (name, i)
 
 
+@pytest.mark.parametrize("name", ["attention", "moe"])
+def test_promised_inputs_behind_an_operator_of_two_launches(name):
+    from split_bf16_gemm_swap_gb300 import LOWM_FLAG_A_BEFORE_PDL_WAIT, LOWM_FLAG_W_BEFORE_PDL_WAIT
+    flags = LOWM_FLAG_A_BEFORE_PDL_WAIT | LOWM_FLAG_W_BEFORE_PDL_WAIT
+    hidden, n, rows = 4096, 256, 4096
+    w = rand(n, hidden, seed=1, std=hidden ** -0.5)
+    x, out = rand(rows, hidden, seed=3), torch.empty(rows, hidden, dtype=BF, device="cuda")
+    if name == "moe":
+        small, router, w1, w2 = moe_inputs(4, 64, 32, 8)
+        result = torch.empty_like(small)
+        op = lambda: layer.moe(small, router, w1, w2, 2, out=result)  # noqa: E731
+    else:
+        q, kc, vc, table, cu = attention_inputs([1, 2], [70, 30], 4, 2, 64, 16)
+        lens, cu = torch.tensor([70, 30], dtype=torch.int32, device="cuda"), torch.tensor(cu, dtype=torch.int32, device="cuda")
+        result = torch.empty_like(q)
+        op = lambda: layer.paged_attention(q, kc, vc, table, lens, cu, out=result)  # noqa: E731
+    for i in range(20):
+        out.zero_()
+        layer.residual_norm(x, out=out)                    # long enough to be running still
+        op()
+        got = gemm(out[-8:], w, flags=flags)
+        torch.cuda.synchronize()
+        assert torch.equal(got, gemm(out[-8:], w)), i
+
+
 def test_single_token_outputs_are_checked():
     x, router, w1, w2 = moe_inputs(1, 64, 32, 8)
     small, wrong = torch.empty(1, 32, dtype=BF, device="cuda"), torch.empty(1, 64, dtype=torch.float32, device="cuda")

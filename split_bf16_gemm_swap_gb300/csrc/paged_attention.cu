@@ -1186,10 +1186,10 @@ extern "C" lowm_status_t lowm_paged_attention(
     for (int i = 0; i < 6; ++i)
         if (extents[i] > 1 && (cache_strides[i] == 0 || cache_strides[i] >= ((int64_t)1 << 39)))
             return LOWM_ERR_INVALID_ARGUMENT;
-    // Tile counts are 32-bit in the kernels.
+    // Tile counts are 32-bit in the kernels, rounding up to equal shares included.
     const int64_t capacity = std::min<int64_t>((int64_t)table_width * page_size, kMaxKeys);
     const int64_t q_tiles = (int64_t)q_tokens * (heads / kv_heads) / kTileRows + batch;
-    if ((double)q_tiles * kv_heads * (double)(capacity / kTileKeys + 2 + kItemCost) > (double)INT_MAX)
+    if ((double)q_tiles * kv_heads * (double)(capacity / kTileKeys + 2 + kItemCost) > (double)(INT_MAX - kMaxAttnCtas))
         return LOWM_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     lowm_status_t st = host_check_device(&sms);

@@ -75,12 +75,18 @@ def norm(**kw):
     (dict(os=63), INVALID), (dict(ors=63), INVALID), (dict(rs=-1), INVALID), (dict(bs=-64), INVALID),
     (dict(residual=PTR + 1), MISALIGNED), (dict(f32=1, residual=PTR + 2), MISALIGNED), (dict(out=PTR + 1), MISALIGNED),
     (dict(out=2 * PTR + 128), INVALID),                # out inside out_residual
-    (dict(out=2 * PTR + 64, ors=128, os=128), INVALID), (dict(out=2 * PTR - 64, ors=128, os=128), INVALID),
-    (dict(out=2 * PTR + 256, ors=128, os=128), INVALID), (dict(out=2 * PTR - 256, ors=128, os=128), INVALID),
-    (dict(out=2 * PTR + 128, f32=1, ors=96, os=192), INVALID), (dict(out=2 * PTR + 128, ors=128, os=136), INVALID),
 ])
 def test_norm_refusals(kw, want):
     assert norm(**kw) == want
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=2 * PTR + 64, ors=128, os=128), dict(out=2 * PTR - 64, ors=128, os=128),
+    dict(out=2 * PTR + 256, ors=128, os=128), dict(out=2 * PTR - 256, ors=128, os=128),
+    dict(out=2 * PTR + 128, f32=1, ors=96, os=192), dict(out=2 * PTR + 128, ors=128, os=136),
+])
+def test_norm_refuses_outputs_that_share_rows(kw):
+    assert norm(**kw) == INVALID
 
 
 def rope(**kw):
@@ -125,6 +131,11 @@ def attention(**kw):
 ])
 def test_attention_refusals(kw, want):
     assert attention(**kw) == want
+
+
+def test_attention_refuses_a_line_of_tiles_past_32_bits():
+    # 128 (2^24 - 1) places: 2^31 - 128, which rounding up to equal shares takes past 2^31
+    assert attention(batch=128, q_tokens=1, heads=1, kv_heads=1, width=16777205, ts=16777205, page=64) == SHAPE
 
 
 def moe(**kw):

@@ -35,7 +35,8 @@ extern "C" {
  * r' stays in fp32 between the two lines; out_residual and out are each
  * rounded once.
  *   residual, out_residual  [tokens, hidden], fp32 when residual_f32 else bf16;
- *                 they may be the same buffer
+ *                 they may be the same buffer.  out may lie between the rows of
+ *                 out_residual, but share none of them
  *   block         [tokens, hidden] bf16, or NULL: no block precedes the norm
  *                 (post_weight, gate and out_residual must then be NULL and
  *                 scale 1; out = RMS(residual; pre_weight))
@@ -46,9 +47,12 @@ extern "C" {
  *   out           [tokens, hidden] bf16
  *   tokens        >= 0 (0: nothing is launched); hidden 1..16384
  * Rows are read and written in 16-byte pieces when hidden and the strides are
- * multiples of 8 (4 for an fp32 residual) and the pointers 16-byte aligned,
- * else element by element.  Two reductions per row in a fixed order: the same
- * arguments give the same bits.
+ * multiples of 8 (4 for an fp32 residual) and the pointers 16-byte aligned.  With
+ * other widths and strides they are, too, where that is faster, from the first
+ * 16-byte boundary of a row on, if the pointers of the row tensors are 16-byte
+ * aligned and their strides differ by multiples of 8 (hidden at most 15872); else
+ * element by element.  Two reductions per row in a fixed order: the same
+ * arguments, alignment included, give the same bits.
  */
 lowm_status_t lowm_residual_norm(const void *residual, int residual_f32, int64_t residual_stride,
                                  const void *block, int64_t block_stride, const void *post_weight,
@@ -75,8 +79,8 @@ lowm_status_t lowm_residual_norm(const void *residual, int residual_f32, int64_t
  *   q_out         [tokens, heads, dim] bf16 by strides; may be q itself
  *   k_cache, v_cache  [num_pages, page_size, kv_heads, dim] bf16, by page,
  *                 place and head strides; offsets are 64-bit
- * A position outside the table gives NaN (q_out) and appends nothing; a slot
- * outside the cache appends nothing.  Two tokens with one slot: one of them is
+ * A position outside the table gives NaN (in the elements of q_out that turn)
+ * and appends nothing; a slot outside the cache appends nothing.  Two tokens with one slot: one of them is
  * kept, element by element unspecified.  q, k and v are rounded once.
  *   dim, rotary   1..1024, 0..dim, rotary even
  */

@@ -80,7 +80,7 @@ struct AttnParams {
     int64_t q_ts, q_hs, o_ts, o_hs, table_stride, num_pages;
     int64_t k_page, k_place, k_head, v_page, v_place, v_head;
     const int32_t *table, *kv_lens, *cu_q;
-    int page_size, page_shift, table_width, batch, q_tokens, heads, kv_heads, group, window, slot_rows;
+    int page_size, page_shift, batch, q_tokens, heads, kv_heads, group, window, slot_rows;
     int capacity;                            // keys a sequence can have: table_width * page_size
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
     float q_sign;
@@ -1221,7 +1221,6 @@ extern "C" lowm_status_t lowm_paged_attention(
     p.page_shift = 0;
     while ((1 << p.page_shift) < page_size)
         ++p.page_shift;
-    p.table_width = table_width;
     p.batch = batch;
     p.q_tokens = q_tokens;
     p.heads = heads;

@@ -325,7 +325,7 @@ extern "C" lowm_status_t lowm_residual_norm(const void *residual, int residual_f
                                             void *stream)
 {
     using namespace lowm;
-    constexpr int kMaxHidden = 16384;                // 512 threads of 32 elements
+    constexpr int kMaxHidden = 16384;                // 1024 threads of 16 elements
     if (tokens < 0 || hidden <= 0 || !(eps >= 0.f))
         return LOWM_ERR_INVALID_ARGUMENT;
     if (hidden > kMaxHidden)

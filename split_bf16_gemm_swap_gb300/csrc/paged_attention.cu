@@ -26,12 +26,13 @@
 // What bounds it.  Decode: the cache's bandwidth (24 sequences of up to 16384
 // keys, 1.0 GB: 157 us, 6.4 TB/s).  Chunks: the MMA issue, the loads and the
 // softmax of two CTAs an SM, none of them alone (2048 tokens over 16384 keys: 364
-// us, 1.41 PFLOP/s; without the exponentials, with half of the loads or with one
-// page for all 3 to 5 % less each; the scores' MMAs of N 64 read more shared
-// memory than their arithmetic hides).  One CTA an SM with 256 rows and tiles of
-// 128 keys halves the loads and has MMAs of N 128, but one S for each 128 rows: the
-// chain S, softmax, O of one half is not hidden by the other (453 us).  Few keys:
-// the chain of launch, schedule, first tile and join (4 x 1000 keys: 12.6 us).
+// us, 1.41 PFLOP/s, to 392 from box to box; without the exponentials, with half of
+// the loads or with one page for all 3 to 5 % less each; the scores' MMAs of N 64
+// read more shared memory than their arithmetic hides).  One CTA an SM with 256
+// rows and tiles of 128 keys halves the loads and has MMAs of N 128, but one S for
+// each 128 rows: the chain S, softmax, O of one half is not hidden by the other
+// (453 us).  Few keys: the chain of launch, schedule, first tile and join (4 x 1000
+// keys: 12.6 us).
 //
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.

@@ -531,7 +531,8 @@ __device__ __forceinline__ bool clean_values(uint8_t *tile, const Seen &seen, in
 // so these keys are among the last 127 that a row sees, or the first 127 of its
 // window; among them are keys that all rows see, whose infinities are in O already
 // and change nothing a second time.  A warp's 32 rows take some milliseconds at
-// worst, whatever the lengths: far below the limit of the other warps' waits.
+// worst, whatever the lengths (3 ms an item with nothing but NaN in V): far below
+// the limit of the other warps' waits.
 template <int DIM>
 __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows, int sequence, const Row &mine, int key_begin,
                                              int key_end, float shift, float factor, int64_t slot, int r)

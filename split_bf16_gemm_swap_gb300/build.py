@@ -1,14 +1,16 @@
 """Compile the CUDA library ``liblowm_gemm.so`` in-tree for sm_103a.
 
-Ten translation units compiled in parallel with nvcc (one ``-gencode``,
+Fourteen translation units compiled in parallel with nvcc (one ``-gencode``,
 no CMake): the GEMM's host launcher and C ABI (``csrc/lowm_gemm.cu``), its
 kernel instances for 64- and 128-column tiles (``csrc/kernels_tile64.cu``,
 ``csrc/kernels_tile128.cu``) and for m_pad 128, 96 and 48
 (``csrc/kernels_mpad128.cu``, ``csrc/kernels_mpad96.cu``,
-``csrc/kernels_mpad48.cu``), and the decoder-layer operators
+``csrc/kernels_mpad48.cu``), the decoder-layer operators
 (``csrc/residual_norm.cu``, ``csrc/rope_append.cu``,
-``csrc/paged_attention.cu``, ``csrc/moe.cu``), then linked into one shared
-library.
+``csrc/paged_attention.cu``, ``csrc/moe.cu``), the 8-bit forms
+(``csrc/gemm_fp8.cu``, ``csrc/rope_append_fp8.cu``,
+``csrc/paged_attention_fp8.cu``) and the pages (``csrc/cache_pages.cu``), then
+linked into one shared library.
 """
 from __future__ import annotations
 
@@ -23,9 +25,10 @@ LIB = os.path.join(HERE, "liblowm_gemm.so")
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("lowm_gemm.cu", "kernels_tile64.cu", "kernels_tile128.cu",
                                            "kernels_mpad128.cu", "kernels_mpad96.cu", "kernels_mpad48.cu",
-                                           "residual_norm.cu", "rope_append.cu", "paged_attention.cu", "moe.cu")]
+                                           "residual_norm.cu", "rope_append.cu", "paged_attention.cu", "moe.cu",
+                                           "gemm_fp8.cu", "rope_append_fp8.cu", "paged_attention_fp8.cu", "cache_pages.cu")]
 DEPS = SOURCES + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
-    os.path.join(ROOT, "include", "lowm_gemm.h"), os.path.join(ROOT, "include", "lowm_layer.h")]
+    os.path.join(ROOT, "include", f) for f in ("lowm_gemm.h", "lowm_layer.h", "lowm_fp8.h", "lowm_pages.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

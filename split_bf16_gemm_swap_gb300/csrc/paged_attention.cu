@@ -42,17 +42,16 @@
 #include <algorithm>
 #include <climits>
 
+#include "attention_line.cuh"
 #include "layer_host.h"
 #include "layer_device.cuh"
 
 namespace lowm {
 namespace {
 
-constexpr int kTileKeys = 64;
 constexpr int kTileRows = 128;
 constexpr int kAttnThreads = 224;            // softmax warps 0-3, TMA warp 4, MMA warps 5 (Q K^T) and 6 (P V)
 constexpr int kMaxAttnCtas = 320;            // two per SM, and a bound for the workspace
-constexpr int kMaxKeys = 1 << 30;            // of a sequence
 // The line counts time in tiles.  An item costs kItemCost tiles beside its own
 // (its queries' way in, its rows' way out); without it the CTAs with short
 // items ended 20 % after the others (chunks of 1537 tokens: 209 us at 5, 200 at
@@ -74,15 +73,14 @@ enum : uint32_t {
     kErrAttnBase = 1u << 17,                 // dynamic shared memory not on a 1024-byte boundary
 };
 
-struct AttnParams {
+struct AttnParams : LineParams<kTileRows, kItemCost, kMinShare> {
     const __nv_bfloat16 *q, *k, *v;
     __nv_bfloat16 *out;
     float *lse;
     int64_t q_ts, q_hs, o_ts, o_hs, table_stride, num_pages;
     int64_t k_page, k_place, k_head, v_page, v_place, v_head;
-    const int32_t *table, *kv_lens, *cu_q;
-    int page_size, page_shift, batch, q_tokens, heads, kv_heads, group, window, slot_rows;
-    int capacity;                            // keys a sequence can have: table_width * page_size
+    const int32_t *table;
+    int page_size, page_shift, heads, slot_rows;
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
     float q_sign;
     bool q_vec, out_vec;                     // 16-byte rows
@@ -91,175 +89,6 @@ struct AttnParams {
     struct CutItem *cuts;                    // [ctas]
     unsigned int *status;
 };
-
-// The item that begins in a CTA's share and ends in a later one, for the join.
-struct CutItem {
-    int parts;                               // shares it lies in; 0: there is none
-    int q0, q_len, head, q_tile;
-};
-
-// ------------------------------------------------------------------ the line of tiles
-struct Item {
-    int b, head, q_tile;                     // sequence, key/value head, tile of 128 rows
-    int q0, q_len, kv;                       // the sequence's first row of q, new tokens, keys
-    int first_tile, tiles;                   // tiles of 64 keys
-    int start;                               // the item's place on the line: kItemCost units, then its tiles
-};
-
-__device__ __forceinline__ void load_sequence(const AttnParams &p, int b, int &q0, int &q_len, int &kv)
-{
-    q0 = min(max(p.cu_q[b], 0), p.q_tokens);
-    q_len = min(max(p.cu_q[b + 1], q0), p.q_tokens) - q0;
-    kv = min(max(p.kv_lens[b], 0), p.capacity);
-}
-
-// Tiles that rows [128 q_tile, 128 q_tile + 128) of a sequence see.  Rows that
-// see nothing still form one (fully masked) tile, so that they are written.
-__device__ __forceinline__ void tile_range(const AttnParams &p, int q_len, int kv, int q_tile, int &first, int &tiles)
-{
-    const int t0 = q_tile * kTileRows / p.group, t1 = min(q_len - 1, (q_tile * kTileRows + kTileRows - 1) / p.group);
-    const int hi = max(0, kv - q_len + t1 + 1);
-    const int lo = p.window > 0 ? max(0, kv - q_len + t0 - p.window + 1) : 0;
-    first = lo < hi ? lo / kTileKeys : 0;
-    tiles = lo < hi ? (hi + kTileKeys - 1) / kTileKeys - first : 1;
-}
-
-__device__ __forceinline__ int q_tiles_of(const AttnParams &p, int q_len)
-{
-    return (q_len * p.group + kTileRows - 1) / kTileRows;
-}
-
-// Units of one key/value head of sequence b (all its row tiles).
-__device__ __forceinline__ int head_units(const AttnParams &p, int b)
-{
-    int q0, q_len, kv, first, n, sum = 0;
-    load_sequence(p, b, q0, q_len, kv);
-    for (int t = 0; t < q_tiles_of(p, q_len); ++t) {
-        tile_range(p, q_len, kv, t, first, n);
-        sum += n + kItemCost;
-    }
-    return sum;
-}
-
-// The line as one warp sees it: lane l holds the units of a head of sequence l
-// and of all heads of sequences 0..l (of the first 32), and everyone the total.
-// The host refuses calls whose line could pass 2^31.
-struct Line {
-    int head, upto, total;
-};
-
-__device__ __forceinline__ int scan32(int x)
-{
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if ((threadIdx.x & 31) >= o)
-            x += y;
-    }
-    return x;
-}
-
-__device__ __forceinline__ Line make_line(const AttnParams &p)
-{
-    const int lane = threadIdx.x & 31;
-    Line l;
-    l.head = lane < p.batch ? head_units(p, lane) : 0;
-    l.upto = scan32(l.head * p.kv_heads);
-    l.total = __shfl_sync(0xffffffffu, l.upto, 31);
-    if (p.batch > 32) {
-        int sum = 0;
-        for (int b = 32 + lane; b < p.batch; b += 32)
-            sum += head_units(p, b);
-        l.total += __reduce_add_sync(0xffffffffu, sum) * p.kv_heads;
-    }
-    return l;
-}
-
-// The item that unit u of the line belongs to (one warp; u below the total).
-__device__ __forceinline__ Item locate(const AttnParams &p, Line line, int u)
-{
-    const int lane = threadIdx.x & 31;
-    Item it;
-    int before = 0;
-    for (int b0 = 0;; b0 += 32) {
-        const unsigned past = __ballot_sync(0xffffffffu, before + line.upto > u);
-        if (past || b0 + 32 >= p.batch) {
-            const int l = past ? __ffs(past) - 1 : 31;
-            it.b = min(b0 + l, p.batch - 1);
-            const int per_head = max(__shfl_sync(0xffffffffu, line.head, l), 1);
-            before += __shfl_sync(0xffffffffu, line.upto, l) - per_head * p.kv_heads;
-            it.head = (u - before) / per_head;
-            it.start = before + it.head * per_head;
-            break;
-        }
-        before += __shfl_sync(0xffffffffu, line.upto, 31);
-        line.head = b0 + 32 + lane < p.batch ? head_units(p, b0 + 32 + lane) : 0;
-        line.upto = scan32(line.head * p.kv_heads);
-    }
-    load_sequence(p, it.b, it.q0, it.q_len, it.kv);
-    for (it.q_tile = 0;; ++it.q_tile) {
-        tile_range(p, it.q_len, it.kv, it.q_tile, it.first_tile, it.tiles);
-        if (u < it.start + kItemCost + it.tiles || it.q_tile + 1 >= q_tiles_of(p, it.q_len))
-            return it;
-        it.start += kItemCost + it.tiles;
-    }
-}
-
-// The item behind `it` on the line.
-__device__ __forceinline__ void advance(const AttnParams &p, Item &it)
-{
-    it.start += kItemCost + it.tiles;
-    if (++it.q_tile >= q_tiles_of(p, it.q_len)) {
-        it.q_tile = 0;
-        if (++it.head == p.kv_heads) {
-            it.head = 0;
-            do {                             // sequences without new tokens have no items
-                ++it.b;
-                load_sequence(p, it.b, it.q0, it.q_len, it.kv);
-            } while (it.q_len == 0 && it.b + 1 < p.batch);
-        }
-    }
-    tile_range(p, it.q_len, it.kv, it.q_tile, it.first_tile, it.tiles);
-}
-
-__device__ __forceinline__ int share_of(int line, int ctas)
-{
-    return max((line + ctas - 1) / ctas, kMinShare);
-}
-
-// A CTA's part of one item: tiles [from, to) of it, at least one.
-struct Piece {
-    Item it;
-    int from, to;
-};
-
-__device__ __forceinline__ void cut(Piece &c, int u, int end)
-{
-    const int first = c.it.start + kItemCost;          // the item's first tile on the line
-    c.from = max(u - first, 0);
-    c.to = min(end - first, c.it.tiles);
-}
-
-// The first piece of the share [begin, end); false when it has none.
-__device__ __forceinline__ bool next_piece(const AttnParams &p, Piece &c, int end)
-{
-    for (;;) {
-        const int u = c.it.start + kItemCost + c.it.tiles;
-        if (u >= end)
-            return false;
-        advance(p, c.it);
-        cut(c, u, end);
-        if (c.from < c.to)
-            return true;
-    }
-}
-
-__device__ __forceinline__ bool first_piece(const AttnParams &p, Piece &c, const Line &line, int begin, int end)
-{
-    c.it = locate(p, line, begin);
-    cut(c, begin, end);
-    return c.from < c.to || next_piece(p, c, end);
-}
 
 // ------------------------------------------------------------------ PTX of this kernel
 __device__ __forceinline__ float ex2(float x)
@@ -382,45 +211,6 @@ struct AttnSmem {
     static constexpr uint32_t kSlot = kBars + kNumBars * 8;             // TMEM address, edge word
     static constexpr uint32_t kBytes = kSlot + 16;                      // 112.2 KiB: two CTAs an SM
 };
-
-// Row r of the item belongs to token r / group, query head head * group + r % group.
-struct Row {
-    bool valid;
-    int token, q_head;                       // token: index into q
-    int hi, lo;                              // keys lo..hi are seen
-};
-
-__device__ __forceinline__ Row row_of(const AttnParams &p, const Item &it, int r)
-{
-    Row w;
-    const int row = it.q_tile * kTileRows + r;
-    const int t = row / p.group;
-    w.valid = t < it.q_len;
-    w.token = it.q0 + t;
-    w.q_head = it.head * p.group + row % p.group;
-    w.hi = it.kv - it.q_len + t;
-    w.lo = p.window > 0 ? w.hi - p.window + 1 : 0;
-    return w;
-}
-
-// Keys that all rows of an item see, [all_lo, all_hi] (none when all_lo > all_hi),
-// and those that some row sees, [lo, end).
-struct Seen {
-    int all_lo, all_hi, lo, end;
-    __device__ bool mixed() const { return all_hi + 1 < end; }   // the rows' tokens differ, and so do their keys
-};
-
-__device__ __forceinline__ Seen seen_by(const AttnParams &p, const Item &it)
-{
-    const int first = it.q_tile * kTileRows / p.group;
-    const int last = min(it.q_len - 1, (it.q_tile * kTileRows + kTileRows - 1) / p.group);
-    Seen s;
-    s.all_hi = it.kv - it.q_len + first;
-    s.end = it.kv - it.q_len + last + 1;
-    s.all_lo = p.window > 0 ? s.end - p.window : 0;
-    s.lo = p.window > 0 ? s.all_hi - p.window + 1 : 0;
-    return s;
-}
 
 template <int DIM>
 __device__ __forceinline__ void store_row(const AttnParams &p, const Row &w, int col, const float (&v)[32])
@@ -647,7 +437,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     ptx::griddep_launch_dependents();
 
     const Line line = make_line(p);
-    const int share = share_of(line.total, gridDim.x);
+    const int share = share_of(p, line.total, gridDim.x);
     const int begin = (int)min((int64_t)share * blockIdx.x, (int64_t)line.total), end = min(share, line.total - begin) + begin;
 
     if (threadIdx.x == 0)

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "../../include/lowm_fp8.h"
 #include "fp8_device.cuh"
@@ -454,12 +455,19 @@ lowm_status_t launch_gemm_fp8(const void *A, const void *W, Gemm8Params &p, int 
     int split = 1;
     while (split < kMaxSplit && tiles * split * 2 <= 2 * sms && p.blocks >= 4 * split)
         split *= 2;
+    if (const char *e = getenv("LOWM8_SPLIT"))
+        split = atoi(e);
     const bool two = tiles * split > sms;                                // CTAs an SM
     const int share = (p.blocks + split - 1) / split;
     p.per_stage = 1;
+    if (const char *e = getenv("LOWM8_KB"))
+        p.per_stage = atoi(e);
     const int overhead = 1024;                                           // barriers
-    const int stage = (int)S::stage_bytes(p.per_stage) + p.per_stage * (int)S::kScaleBytes;
-    int budget = two ? kSmem / 2 - 1024 : kSmem;
+    const int budget = two ? kSmem / 2 - 1024 : kSmem;
+    auto bytes_of = [](int blocks) { return (int)S::stage_bytes(blocks) + blocks * (int)S::kScaleBytes; };
+    while (p.per_stage > 1 && 2 * bytes_of(p.per_stage) > budget - overhead)
+        p.per_stage /= 2;
+    const int stage = bytes_of(p.per_stage);
     p.stages = std::min({(budget - overhead) / stage, (share + p.per_stage - 1) / p.per_stage, 16});
     p.planes = K % kBlock == 0;
     // The ring is the mailbox, too.

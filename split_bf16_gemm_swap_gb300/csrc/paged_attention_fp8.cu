@@ -5,30 +5,23 @@
 //
 // with codes k, v and the scales a_j, b_j of the blocks that key j lies in.
 //
-// Products.  Both run on the 8-bit tensor cores from registers (m16n8k32), the
-// codes as they lie in the cache: nothing is widened.  The other operand is the
-// sum of two e4m3 numbers, one product each into the same sums.  q, times a power
-// of two for its row, is such a sum exactly but for elements below 2^-17 of the
-// row's largest (a bf16 number has 8 significant bits, an e4m3 number 4).  A
-// weight w_j = 2^(t_j - max + 8) with t_j = s_j log2(e) + log2(b_j), the maximum
-// over the 32 keys at hand, is one to 2^-9 of itself (or 2^-18 of the maximum).
-// The 32 keys' product is then added in fp32, times 2^(max - row maximum), so that
-// small weights keep their digits whatever other keys weigh.  The softmax's sum is
-// that of w_j / b_j.  (One thread's row of a tcgen05 product would have to be
-// scaled alike for all keys: its sums stay in the tensor memory.)
+// Products.  An e4m3 number is an fp16 number, so the codes are widened in registers (cvt, two at a time) and both products
+// run on the tensor cores from registers (m16n8k16, fp32 sums) with the keys, then the head's elements, on their 16 rows and
+// eight rows of q on their columns: a decoding step's few rows waste nothing.  q is divided by a power of two for its row,
+// which fp16 holds exactly but for elements below 2^-24 of the row's largest.  A weight is 2^(t_j - m + 8) with
+// t_j = s_j log2(e) + log2(b_j) and m the row's largest t at the last rescaling, which follows when it has grown by 2^7:
+// at most 2^15, rounded to fp16 (2^-11 of itself, or 2^-32 of the largest), whatever the scales are.  The softmax's sum is
+// that of weight / b_j in fp32.  (mma.sync takes e4m3 operands, too, but widens them itself, and adds in separate
+// instructions: 1280 a 32 keys and 16 rows against 300 a 32 keys and 8 rows here.)
 //
-// Work.  Items, shares and parts are those of attention_line.cuh.  Eight warps
-// have R rows each (8: decoding; 16: chunks).  Where an item has fewer rows, warps
-// share them and each takes every KS-th 32 keys; their sums are joined through
-// shared memory in a fixed order.  A ninth warp feeds a ring of 64-key tiles: codes
-// by TMA, page by page (swizzled, so that the fragments' 16-byte reads meet no bank
-// twice), scales by 4-byte asynchronous copies.
+// Work.  Items, shares and parts are those of attention_line.cuh.  Four warps have R rows each (8: decoding; 16).  Where an
+// item has fewer rows, warps share them and each takes every second or fourth 32 keys; their sums are joined through shared
+// memory in a fixed order.  A fifth warp feeds a ring of 64-key tiles: codes by TMA, page by page (swizzled, so that the
+// fragments' 16-byte reads meet no bank twice), scales by 4-byte asynchronous copies.
 //
-// V is the product's B operand with its keys in a row: four keys' words are
-// transposed in registers by byte permutes.  The orders of the head's elements
-// (for q.k) and of the 32 keys (for w.v) within a product are free; they are
-// chosen so that a thread's fragments are neighbouring bytes of the cache and the
-// scores it holds are the weights that it needs.
+// The orders of the head's elements (for q.k) and of the elements' rows (for w.v) within a product are free; they are chosen
+// so that a thread's fragments are neighbouring bytes of the cache.  V's keys are paired by byte permutes before they are
+// widened, the weights transposed by movmatrix.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -44,12 +37,12 @@
 namespace lowm {
 namespace {
 
-constexpr int kWarps = 8;                    // that compute
+constexpr int kWarps = 4;                    // that compute
 constexpr int kThreads8 = 32 * (kWarps + 1);
 constexpr int kUnitKeys = 32;                // of one product
-constexpr int kMaxCtas = 320;
+constexpr int kMaxCtas = 480;                // three per SM, and a bound for the workspace
 constexpr int kItemCost8 = 4, kMinShare8 = 4;
-constexpr float kWeightLog2 = 8.f;           // the largest weight is 2^8 (e4m3 ends at 448)
+constexpr float kWeightLog2 = 8.f, kRescaleLog2 = 7.f;   // the largest weight is 2^15 (fp16 ends at 65504)
 constexpr float kMaxScale = 1.125899906842624e15f;   // 2^50: scales are taken as 2^-50 .. 2^50
 
 // Bits of the device status word (above those of the other operators).
@@ -89,13 +82,33 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// c += A . B, e4m3, A [16 x 32] row-major, B [32 x 8] column-major.
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// c += A . B, fp16, A [16 x 16] row-major, B [16 x 8] column-major.
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes the 8 x 8 matrix of which thread 4 g + t holds elements 2 t, 2 t + 1 of row g.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Two codes as two fp16 numbers: the low or the high half of a word.
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w)
+{
+    const __half2 h = e4m3x2_to_half2(w & 0xffffu);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w)
+{
+    const __half2 h = e4m3x2_to_half2(w >> 16);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar)
@@ -118,25 +131,30 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-template <int BYTES>
-__device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&w)[BYTES / 4])
+template <int WORDS>
+__device__ __forceinline__ void load_shared(const uint8_t *at, uint32_t (&w)[WORDS])
 {
-    if constexpr (BYTES == 16)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
-    else
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    if constexpr (WORDS == 4) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(at);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(at);
+        w[0] = u.x, w[1] = u.y;
+    }
 }
 
 // ------------------------------------------------------------------ shared memory
 template <int DIM, int R>
 struct Attn8Smem {
+    static constexpr int kCtas = R == 8 ? 3 : 2;                        // an SM
     static constexpr uint32_t kTileBytes = kTileKeys * DIM;             // of K or V; 1024-byte multiples
-    static constexpr uint32_t kStages = (R == 8 ? 5 : 10) * (128 / DIM);
+    static constexpr uint32_t kStages = (R == 8 ? 3 : 5) * (128 / DIM);
     static constexpr uint32_t kOut = R * DIM / 32;                      // sums a thread holds
+    static constexpr uint32_t kSums = R / 2;                            // and maxima and sums of weights
     static constexpr uint32_t kScales = kStages * 2 * kTileBytes;       // [stages][K, V][64]
-    static constexpr uint32_t kMerge = kScales + kStages * 2 * kTileKeys * 4;   // [4 warps][kOut + 4][32]
-    static constexpr uint32_t kKeys = kMerge + 4 * (kOut + 4) * 32 * 4;         // [warps][3][32] of the 32 keys at hand
-    static constexpr uint32_t kBars = kKeys + kWarps * 3 * kUnitKeys * 4;       // full, empty [stages]
+    static constexpr uint32_t kMerge = kScales + kStages * 2 * kTileKeys * 4;       // [warps / 2][kOut + kSums][32]
+    static constexpr uint32_t kKeys = kMerge + kWarps / 2 * (kOut + kSums) * 32 * 4;    // [warps][32 keys at hand][4]
+    static constexpr uint32_t kBars = kKeys + kWarps * kUnitKeys * 16;  // full, empty [stages]
     static constexpr uint32_t kBytes = kBars + 2 * kStages * 8;
 };
 
@@ -146,46 +164,32 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w)
     return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// Transposes 4 x 4 bytes: out word d holds byte d of w[0], w[1], w[2], w[3].
-__device__ __forceinline__ void transpose_bytes(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t (&out)[4])
-{
-    const uint32_t a = __byte_perm(w0, w1, 0x5140), b = __byte_perm(w0, w1, 0x7362);
-    const uint32_t c = __byte_perm(w2, w3, 0x5140), d = __byte_perm(w2, w3, 0x7362);
-    out[0] = __byte_perm(a, c, 0x5410);
-    out[1] = __byte_perm(a, c, 0x7632);
-    out[2] = __byte_perm(b, d, 0x5410);
-    out[3] = __byte_perm(b, d, 0x7632);
-}
-
-// One warp's R rows of an item: q, running maximum, sum and weighted values.  Thread 4 g + t holds row g (and g + 8):
-// of q elements [DIM / 4 t, DIM / 4 (t + 1)), of the sums the same ones, sums[e] being element e, then, from DIM / 8 on,
-// DIM / 8 + e of them.
+// One warp's R rows of an item, eight a set.  Thread 4 g + t has of row g of a set elements [DIM / 4 t, DIM / 4 (t + 1)) of
+// q, and of rows 2 t and 2 t + 1 the maximum, the sum of its keys' weights and elements [DIM / 8 g, DIM / 8 (g + 1)) of the
+// weighted values: out[e] holds elements 2 e and 2 e + 1 of those, of row 2 t, row 2 t + 1, row 2 t, row 2 t + 1.
 template <int DIM, int R>
 struct Rows8 {
-    static constexpr int kSets = R / 8;      // rows a thread holds
-    uint32_t q[2][DIM / 32][4];              // two terms
-    float unit[kSets];                       // power of two that q was divided by
-    float top[kSets], sum[kSets];            // (sum: this thread's keys)
-    float out[DIM / 8][2 * kSets];
+    static constexpr int kSets = R / 8;
+    uint32_t q[kSets][DIM / 16][2];
+    float unit[kSets][2];                    // power of two that q was divided by
+    int hi[kSets][2], lo[kSets][2];          // keys that a row sees (none: hi < lo)
+    float top[kSets][2], sum[kSets][2];
+    float out[kSets][DIM / 16][4];
 };
 
 template <int DIM, int R, class P>
-__device__ __forceinline__ void load_rows(const P &p, const Row (&rows)[R / 8], Rows8<DIM, R> &x)
+__device__ __forceinline__ void load_rows(const P &p, const Item &it, int row0, Rows8<DIM, R> &x)
 {
-    constexpr int N = DIM / 4;               // elements a thread holds of a row
-    const int t = threadIdx.x & 3;
-#pragma unroll
-    for (int i = 0; i < DIM / 32; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            x.q[0][i][j] = x.q[1][i][j] = 0;
+    constexpr int N = DIM / 4;               // elements a thread holds of a row of q
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
     for (int set = 0; set < R / 8; ++set) {
+        const Row row = row_of(p, it, row0 + 8 * set + g);
         alignas(16) __nv_bfloat16 v[N];
-        const __nv_bfloat16 *from = p.q + rows[set].token * p.q_ts + rows[set].q_head * p.q_hs + N * t;
+        const __nv_bfloat16 *from = p.q + row.token * p.q_ts + row.q_head * p.q_hs + N * t;
 #pragma unroll
         for (int i = 0; i < N; i += 8) {
-            if (!rows[set].valid) {
+            if (!row.valid) {
                 *reinterpret_cast<uint4 *>(v + i) = make_uint4(0, 0, 0, 0);
             } else if (p.q_vec) {
                 *reinterpret_cast<uint4 *>(v + i) = *reinterpret_cast<const uint4 *>(from + i);
@@ -202,253 +206,273 @@ __device__ __forceinline__ void load_rows(const P &p, const Row (&rows)[R / 8], 
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int e = scale_exponent(amax);
-        x.unit[set] = power_of_two(e);
         const float inverse = power_of_two(-e);
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {     // four elements: one word of each term
-            uint32_t w0 = 0, w1 = 0;
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const float a = nan_unless_finite(__bfloat162float(v[i + j])) * inverse;
-                const float b = nan_unless_finite(__bfloat162float(v[i + j + 1])) * inverse;
-                const uint32_t first = to_e4m3x2(a, b);
-                const float2 back = __half22float2(e4m3x2_to_half2(first));
-                w0 |= first << (8 * j);
-                w1 |= to_e4m3x2(a - back.x, b - back.y) << (8 * j);
-            }
-            x.q[0][i / 8][(i & 4) / 2 + set] = w0;
-            x.q[1][i / 8][(i & 4) / 2 + set] = w1;
+        for (int i = 0; i < N; i += 2) {
+            const __half2 h = __floats2half2_rn(__bfloat162float(v[i]) * inverse, __bfloat162float(v[i + 1]) * inverse);
+            x.q[set][i / 4][i / 2 & 1] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        x.top[set] = -CUDART_INF_F;
-        x.sum[set] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int from_lane = 4 * (2 * t + c);
+            x.unit[set][c] = power_of_two(__shfl_sync(0xffffffffu, e, from_lane));
+            x.hi[set][c] = __shfl_sync(0xffffffffu, row.valid ? row.hi : -1, from_lane);
+            x.lo[set][c] = __shfl_sync(0xffffffffu, row.valid ? row.lo : 0, from_lane);
+            x.top[set][c] = -CUDART_INF_F;
+            x.sum[set][c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < DIM / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x.out[set][i][j] = 0.f;
     }
+}
+
+// Key i of this thread's four among 16 of V.
+__device__ __forceinline__ int value_key(int i, int t) { return 8 * (i >> 1) + 2 * t + (i & 1); }
+
+// out += V^T . w for the rows of all sets: 16 keys, elements 4 w .. 4 w + 3 of the thread's from its keys' words; b0, b1:
+// the weights of keys 2 t, 2 t + 1 and 8 + those of row g.
+template <int SETS, int TILES>
+__device__ __forceinline__ void weigh(float (&out)[SETS][TILES][4], const uint32_t (&v)[4], int w, const uint32_t (&b0)[SETS],
+                                      const uint32_t (&b1)[SETS])
+{
+    const uint32_t lo0 = __byte_perm(v[0], v[1], 0x5140), hi0 = __byte_perm(v[0], v[1], 0x7362);   // elements 0, 1 and 2, 3
+    const uint32_t lo1 = __byte_perm(v[2], v[3], 0x5140), hi1 = __byte_perm(v[2], v[3], 0x7362);
 #pragma unroll
-    for (int i = 0; i < DIM / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 2 * (R / 8); ++j)
-            x.out[i][j] = 0.f;
+    for (int set = 0; set < SETS; ++set) {
+        mma_f16(out[set][2 * w], widen_lo(lo0), widen_hi(lo0), widen_lo(lo1), widen_hi(lo1), b0[set], b1[set]);
+        mma_f16(out[set][2 * w + 1], widen_lo(hi0), widen_hi(hi0), widen_lo(hi1), widen_hi(hi1), b0[set], b1[set]);
+    }
 }
 
 // The 32 keys from key0 on (rows `first` to `first` + 31 of the tile) for one warp's rows.
 template <int DIM, int R>
-__device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Row (&rows)[R / 8], const Seen &seen, int key0, int first,
-                                       uint32_t k_tile, uint32_t v_tile, const float *scales, float *mine, float scale_log2)
+__device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Seen &seen, int key0, int first, const uint8_t *k_tile,
+                                       const uint8_t *v_tile, const float *scales, float4 *mine, float scale_log2)
 {
-    constexpr int kSets = R / 8;
+    constexpr int kSets = R / 8, kWords = DIM / 32;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // Scales of the 32 keys, a key a lane; those that no row sees count nothing.
     {
         const int key = key0 + lane;
         const bool known = key >= seen.lo && key < seen.end;
-        const float a = known ? scales[first + lane] * scale_log2 : 0.f;
         const float b = known ? fminf(fmaxf(scales[kTileKeys + first + lane], 1.f / kMaxScale), kMaxScale) : 1.f;
-        mine[lane] = a;
-        mine[32 + lane] = __log2f(b);
-        mine[64 + lane] = __fdividef(1.f, b);
+        mine[lane] = make_float4(known ? scales[first + lane] * scale_log2 : 0.f, __log2f(b), __fdividef(1.f, b), 0.f);
         __syncwarp();
     }
-    // Scores: thread 4 g + t has keys 8 j + 2 t, 8 j + 2 t + 1 of rows g and g + 8.
-    float s[4][4];
+    // Scores: thread 4 g + t has keys g + 8 j of rows 2 t and 2 t + 1.
+    float s[kSets][2][4] = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-        const int row = first + 8 * j + g;
-#pragma unroll
-        for (int i = 0; i < DIM / 64; ++i) {
-            uint32_t w[4];
-            const uint32_t chunk = DIM == 128 ? (uint32_t)((2 * t + i) ^ (row & 7)) : (uint32_t)(t ^ ((row >> 1) & 3));
-            load_shared<16>(k_tile + row * DIM + chunk * 16, w);
-#pragma unroll
-            for (int term = 0; term < 2; ++term) {
-                mma_e4m3(s[j], x.q[term][2 * i], w[0], w[1]);
-                mma_e4m3(s[j], x.q[term][2 * i + 1], w[2], w[3]);
-            }
-        }
-    }
-    float2 inverse[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 a = *reinterpret_cast<const float2 *>(mine + 8 * j + 2 * t);
-        const float2 b = *reinterpret_cast<const float2 *>(mine + 32 + 8 * j + 2 * t);
-        inverse[j] = *reinterpret_cast<const float2 *>(mine + 64 + 8 * j + 2 * t);
-#pragma unroll
-        for (int set = 0; set < kSets; ++set) {
-            s[j][2 * set] = fmaf(s[j][2 * set] * a.x, x.unit[set], b.x);
-            s[j][2 * set + 1] = fmaf(s[j][2 * set + 1] * a.y, x.unit[set], b.y);
-        }
-    }
-    const bool edge = key0 < seen.all_lo || key0 + kUnitKeys - 1 > seen.all_hi;
-    if (edge) {
-#pragma unroll
-        for (int set = 0; set < kSets; ++set) {
-            const int hi = rows[set].valid ? rows[set].hi - key0 : -1, lo = rows[set].lo - key0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int k = 8 * j + 2 * t + c;
-                    if (k > hi || k < lo)
-                        s[j][2 * set + c] = -CUDART_INF_F;
-                }
-        }
-    }
-    // Weights, as two terms.
-    uint32_t w0[4] = {}, w1[4] = {};
-    float factor[kSets];
-#pragma unroll
-    for (int set = 0; set < kSets; ++set) {
-        float top = -CUDART_INF_F;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            top = fmaxf(top, fmaxf(s[j][2 * set], s[j][2 * set + 1]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float shift = top == -CUDART_INF_F ? 0.f : top - kWeightLog2;
-        float sum = 0.f;
+    for (int i = 0; i < DIM / 64; ++i) {
+        uint32_t w[4][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float a = ex2(s[j][2 * set] - shift), b = ex2(s[j][2 * set + 1] - shift);
-            sum = fmaf(a, inverse[j].x, fmaf(b, inverse[j].y, sum));
-            const __half2 h = __floats2half2_rn(a, b);
-            const uint32_t one = half2_to_e4m3x2(h);
-            const uint32_t two = half2_to_e4m3x2(__hsub2(h, e4m3x2_to_half2(one)));
-            w0[(j & 2) + set] |= one << (16 * (j & 1));
-            w1[(j & 2) + set] |= two << (16 * (j & 1));
+            const int row = first + 8 * j + g;
+            const uint32_t chunk = DIM == 128 ? (uint32_t)((2 * t + i) ^ (row & 7)) : (uint32_t)(t ^ ((row >> 1) & 3));
+            load_shared<4>(k_tile + row * DIM + chunk * 16, w[j]);
         }
-        // Into the row's sums, at the scale of its largest weight so far.
-        const float now = fmaxf(x.top[set], top);
-        const float before = now == x.top[set] ? 1.f : ex2(x.top[set] - now);
-        factor[set] = top == -CUDART_INF_F ? 0.f : ex2(top - now);
-        x.top[set] = now;
-        x.sum[set] = fmaf(sum, factor[set], x.sum[set] * before);
-        if (__any_sync(0xffffffffu, before != 1.f)) {
 #pragma unroll
-            for (int e = 0; e < DIM / 8; ++e) {
-                x.out[e][2 * set] *= before;
-                x.out[e][2 * set + 1] *= before;
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t a0 = widen_lo(w[2 * m][k]), a1 = widen_lo(w[2 * m + 1][k]), a2 = widen_hi(w[2 * m][k]),
+                               a3 = widen_hi(w[2 * m + 1][k]);
+#pragma unroll
+                for (int set = 0; set < kSets; ++set)
+                    mma_f16(s[set][m], a0, a1, a2, a3, x.q[set][4 * i + k][0], x.q[set][4 * i + k][1]);
             }
-        }
-        if (sum != sum)                      // a score that is not a number
-            factor[set] = CUDART_NAN_F;
     }
-    // Values.  Keys 4 t .. 4 t + 3 of the product's 32 are 2 t, 2 t + 1, 8 + 2 t, 9 + 2 t, and 16 + those for the second half.
-    constexpr int kWords = DIM / 32;         // words of a key that a thread holds: elements DIM / 8 g ..
-    uint32_t v[8][kWords];
+    const bool edge = key0 < seen.all_lo || key0 + kUnitKeys - 1 > seen.all_hi;
+    float inverse[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = first + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + 2 * t + (i & 1);
-        if constexpr (DIM == 128)
-            load_shared<16>(v_tile + row * DIM + ((g ^ (row & 7)) << 4), v[i]);
-        else
-            load_shared<8>(v_tile + row * DIM + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8, v[i]);
-    }
-    // A weight of 0 does not silence a NaN: keys that no row sees may hold anything and are cleared; NaN codes of keys
-    // that some rows see and others do not are found apart, by counting for each row those that it sees.
-    bool apart = false;
-    uint32_t sees[4] = {};
-    if (edge) {
-        uint32_t bad = 0;
+    for (int j = 0; j < 4; ++j) {            // key g + 8 j
+        const float4 a = mine[g + 8 * j];
+        inverse[j] = a.z;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int key = key0 + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + 2 * t + (i & 1);
-            const bool known = key >= seen.lo && key < seen.end;
+        for (int set = 0; set < kSets; ++set)
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                v[i][w] = known ? v[i][w] : 0u;
-                bad |= nan_codes(v[i][w]);
+            for (int c = 0; c < 2; ++c) {
+                float &y = s[set][j >> 1][2 * (j & 1) + c];
+                y = fmaf(y * a.x, x.unit[set][c], a.y);
+                if (edge && (key0 + g + 8 * j > x.hi[set][c] || key0 + g + 8 * j < x.lo[set][c]))
+                    y = -CUDART_INF_F;
             }
+    }
+    __syncwarp();                            // `mine` may be written again
+    // Weights.
+    uint32_t weights[kSets][4];              // of keys 8 i + 2 t, 8 i + 2 t + 1 and row g
+#pragma unroll
+    for (int set = 0; set < kSets; ++set) {
+        float top[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            top[c] = fmaxf(fmaxf(s[set][0][c], s[set][0][2 + c]), fmaxf(s[set][1][c], s[set][1][2 + c]));
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2)
+                top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
         }
-        apart = __any_sync(0xffffffffu, bad != 0);
-        if (apart) {
+        if (__any_sync(0xffffffffu, top[0] > x.top[set][0] + kRescaleLog2 || top[1] > x.top[set][1] + kRescaleLog2)) {
 #pragma unroll
-            for (int set = 0; set < kSets; ++set)
+            for (int c = 0; c < 2; ++c) {
+                const float now = fmaxf(x.top[set][c], top[c]);
+                const float before = now == x.top[set][c] ? 1.f : ex2(x.top[set][c] - now);
+                x.top[set][c] = now;
+                x.sum[set][c] *= before;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int key = key0 + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + 2 * t + (i & 1);
-                    if (rows[set].valid && key <= rows[set].hi && key >= rows[set].lo)
-                        sees[2 * (i >> 2) + set] |= 0x38u << (8 * (i & 3));      // 1.0
+                for (int e = 0; e < DIM / 16; ++e) {
+                    x.out[set][e][c] *= before;
+                    x.out[set][e][2 + c] *= before;
                 }
-        }
-    }
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-        uint32_t b0[4], b1[4];
-        transpose_bytes(v[0][w], v[1][w], v[2][w], v[3][w], b0);
-        transpose_bytes(v[4][w], v[5][w], v[6][w], v[7][w], b1);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float o[4] = {0.f, 0.f, 0.f, 0.f};
-            if (apart) {
-                const uint32_t n0 = nan_codes(b0[e]), n1 = nan_codes(b1[e]);
-                mma_e4m3(o, sees, n0 & 0x38383838u, n1 & 0x38383838u);
-                b0[e] &= ~n0;
-                b1[e] &= ~n1;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    o[c] = o[c] > 0.f ? CUDART_NAN_F : 0.f;
-            }
-            mma_e4m3(o, w0, b0[e], b1[e]);
-            mma_e4m3(o, w1, b0[e], b1[e]);
-#pragma unroll
-            for (int set = 0; set < kSets; ++set) {
-                x.out[4 * w + e][2 * set] = fmaf(o[2 * set], factor[set], x.out[4 * w + e][2 * set]);
-                x.out[4 * w + e][2 * set + 1] = fmaf(o[2 * set + 1], factor[set], x.out[4 * w + e][2 * set + 1]);
             }
         }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float shift = x.top[set][c] == -CUDART_INF_F ? 0.f : x.top[set][c] - kWeightLog2;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float &y = s[set][j >> 1][2 * (j & 1) + c];
+                y = ex2(y - shift);
+                x.sum[set][c] = fmaf(y, inverse[j], x.sum[set][c]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __half2 h = __floats2half2_rn(s[set][j >> 1][2 * (j & 1)], s[set][j >> 1][2 * (j & 1) + 1]);
+            weights[set][j] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&h));
+        }
     }
-    __syncwarp();                            // before `mine` is written again
+    // Values, 16 keys at a time.
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t v[4][kWords], b0[kSets], b1[kSets];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = first + 16 * half + value_key(i, t);
+            if constexpr (DIM == 128)
+                load_shared<4>(v_tile + row * DIM + ((g ^ (row & 7)) << 4), v[i]);
+            else
+                load_shared<2>(v_tile + row * DIM + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8, v[i]);
+        }
+        // A weight of 0 does not silence a NaN: keys that no row sees may hold anything and are cleared.  NaN codes of keys
+        // that some rows see and others do not are taken out; how many of them a row sees is a product of its own, of ones.
+        if (edge) {
+            const int k0 = key0 + 16 * half;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = k0 + value_key(i, t);
+                const bool known = key >= seen.lo && key < seen.end;
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    v[i][w] = known ? v[i][w] : 0u;
+                    bad |= nan_codes(v[i][w]);
+                }
+            }
+            if (__any_sync(0xffffffffu, bad != 0)) {
+#pragma unroll
+                for (int set = 0; set < kSets; ++set) {
+                    uint32_t ones[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int key = k0 + g + 8 * j;
+                        ones[j] = key <= x.hi[set][0] && key >= x.lo[set][0] ? 0x3c00u : 0u;
+                        ones[j] |= key <= x.hi[set][1] && key >= x.lo[set][1] ? 0x3c000000u : 0u;
+                    }
+                    b0[set] = transpose_8x8(ones[0]);
+                    b1[set] = transpose_8x8(ones[1]);
+                }
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    uint32_t flags[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t nan = nan_codes(v[i][w]);
+                        flags[i] = nan & 0x38383838u;         // 1.0
+                        v[i][w] &= ~nan;
+                    }
+                    float count[kSets][2][4] = {};
+                    weigh(count, flags, 0, b0, b1);
+#pragma unroll
+                    for (int set = 0; set < kSets; ++set)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (count[set][e][c] > 0.f)
+                                    x.out[set][2 * w + e][c] = CUDART_NAN_F;
+                }
+            }
+        }
+#pragma unroll
+        for (int set = 0; set < kSets; ++set) {
+            b0[set] = weights[set][2 * half];
+            b1[set] = weights[set][2 * half + 1];
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const uint32_t word[4] = {v[0][w], v[1][w], v[2][w], v[3][w]};
+            weigh(x.out, word, w, b0, b1);
+        }
+    }
 }
 
-// Joins the sums of the warps that share rows: in each step the upper half of them hand theirs over.  The warps'
-// number is the same for the whole CTA; all of its kWarps warps come here.
+// Joins the sums of the warps that share rows: in each step the upper half of them hand theirs over.  Their number is the
+// same for the whole CTA; all of its kWarps warps come here.
 template <int DIM, int R>
-__device__ __forceinline__ void join_warps(Rows8<DIM, R> &x, float *merge, int warps, int row_tiles, int warp)
+__device__ __forceinline__ void join_warps(Rows8<DIM, R> &x, float *merge, int sharing, int row_tiles, int warp)
 {
-    constexpr int kSets = R / 8, kOut = R * DIM / 32;
+    constexpr int kSets = R / 8, kOut = R * DIM / 32, kAll = kOut + R / 2;
     const int lane = threadIdx.x & 31;
     const int rt = warp % row_tiles, part = warp / row_tiles;
-    for (int half = warps / 2; half > 0; half /= 2) {
-        float *at = merge + ((part & (half - 1)) * row_tiles + rt) * (kOut + 4) * 32 + lane;
+    for (int half = sharing / 2; half > 0; half /= 2) {
+        float *at = merge + ((part & (half - 1)) * row_tiles + rt) * kAll * 32 + lane;
         if (part >= half && part < 2 * half) {
 #pragma unroll
-            for (int e = 0; e < DIM / 8; ++e)
-#pragma unroll
-                for (int c = 0; c < 2 * kSets; ++c)
-                    at[(e * 2 * kSets + c) * 32] = x.out[e][c];
-#pragma unroll
             for (int set = 0; set < kSets; ++set) {
-                at[(kOut + 2 * set) * 32] = x.top[set];
-                at[(kOut + 2 * set + 1) * 32] = x.sum[set];
+#pragma unroll
+                for (int e = 0; e < DIM / 16; ++e)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        at[((set * (DIM / 16) + e) * 4 + c) * 32] = x.out[set][e][c];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    at[(kOut + 4 * set + c) * 32] = x.top[set][c];
+                    at[(kOut + 4 * set + 2 + c) * 32] = x.sum[set][c];
+                }
             }
         }
         ptx::named_barrier_sync(1, 32 * kWarps);
         if (part < half) {
 #pragma unroll
-            for (int set = 0; set < kSets; ++set) {
-                const float top = at[(kOut + 2 * set) * 32];
-                const float now = fmaxf(x.top[set], top);
-                const float base = now == -CUDART_INF_F ? 0.f : now;
-                const float a = ex2(x.top[set] - base), b = ex2(top - base);
-                x.top[set] = now;
-                x.sum[set] = fmaf(x.sum[set], a, at[(kOut + 2 * set + 1) * 32] * b);
+            for (int set = 0; set < kSets; ++set)
 #pragma unroll
-                for (int e = 0; e < DIM / 8; ++e)
+                for (int c = 0; c < 2; ++c) {
+                    const float top = at[(kOut + 4 * set + c) * 32];
+                    const float now = fmaxf(x.top[set][c], top);
+                    const float base = now == -CUDART_INF_F ? 0.f : now;
+                    const float a = ex2(x.top[set][c] - base), b = ex2(top - base);
+                    x.top[set][c] = now;
+                    x.sum[set][c] = fmaf(x.sum[set][c], a, at[(kOut + 4 * set + 2 + c) * 32] * b);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        x.out[e][2 * set + c] = fmaf(x.out[e][2 * set + c], a, at[(e * 2 * kSets + 2 * set + c) * 32] * b);
-            }
+                    for (int e = 0; e < DIM / 16; ++e)
+#pragma unroll
+                        for (int h = 0; h < 4; h += 2)
+                            x.out[set][e][h + c] =
+                                fmaf(x.out[set][e][h + c], a, at[((set * (DIM / 16) + e) * 4 + h + c) * 32] * b);
+                }
         }
         ptx::named_barrier_sync(1, 32 * kWarps);
     }
 }
 
 template <int DIM, int R>
-__global__ void __launch_bounds__(kThreads8, R == 8 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM, R>::kCtas)
     paged_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                const Attn8Params<kWarps * R> p)
 {
     using L = Attn8Smem<DIM, R>;
-    constexpr int kSets = R / 8;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_u32(smem);
     const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kStages;
@@ -538,7 +562,7 @@ __global__ void __launch_bounds__(kThreads8, R == 8 ? 2 : 1)
         return;
     }
     // ---------------------------------------------------------------- rows
-    float *keys = reinterpret_cast<float *>(smem + L::kKeys) + warp * 3 * kUnitKeys;
+    float4 *keys = reinterpret_cast<float4 *>(smem + L::kKeys) + warp * kUnitKeys;
     float *merge = reinterpret_cast<float *>(smem + L::kMerge);
     const int g = lane >> 2, t = lane & 3;
     do {
@@ -548,14 +572,10 @@ __global__ void __launch_bounds__(kThreads8, R == 8 ? 2 : 1)
         while (row_tiles * R < in_item)
             row_tiles *= 2;
         const int sharing = kWarps / row_tiles, rt = warp % row_tiles, part = warp / row_tiles;
-        Row rows[kSets];
-#pragma unroll
-        for (int set = 0; set < kSets; ++set)
-            rows[set] = row_of(p, it, rt * R + 8 * set + g);
-        const bool has_rows = __any_sync(0xffffffffu, rows[0].valid);
+        const bool has_rows = rt * R < in_item;
         const Seen seen = seen_by(p, it);
         Rows8<DIM, R> x;
-        load_rows<DIM, R>(p, rows, x);
+        load_rows<DIM, R>(p, it, rt * R, x);
         for (int j = 0; j < n; ++j, ++i) {
             const uint32_t s = i % L::kStages;
             if (ok && !wait_short(bar_full + 8 * s, (i / L::kStages) & 1)) {
@@ -563,12 +583,12 @@ __global__ void __launch_bounds__(kThreads8, R == 8 ? 2 : 1)
                 atomicOr(p.status, kErrAttn8Full);
             }
             ok = __all_sync(0xffffffffu, ok);
-            const uint32_t k_tile = sbase + s * 2 * L::kTileBytes;
+            const uint8_t *k_tile = smem + s * 2 * L::kTileBytes;
             const float *scales = reinterpret_cast<const float *>(smem + L::kScales) + s * 2 * kTileKeys;
 #pragma unroll 1
             for (int h = 0; h < kTileKeys / kUnitKeys; ++h)
                 if (ok && has_rows && ((2 * j + h) & (sharing - 1)) == part)
-                    attend<DIM, R>(x, rows, seen, (it.first_tile + from + j) * kTileKeys + kUnitKeys * h, kUnitKeys * h, k_tile,
+                    attend<DIM, R>(x, seen, (it.first_tile + from + j) * kTileKeys + kUnitKeys * h, kUnitKeys * h, k_tile,
                                    k_tile + L::kTileBytes, scales, keys, p.scale_log2);
             __syncwarp();
             if (lane == 0)
@@ -582,55 +602,53 @@ __global__ void __launch_bounds__(kThreads8, R == 8 ? 2 : 1)
         if (threadIdx.x == 0 && from == 0 && !whole)
             p.cuts[blockIdx.x] = {(it.start + p.kCost + it.tiles - 1) / share - (int)blockIdx.x + 1, it.q0, it.q_len, it.head,
                                   it.q_tile};
-        if (part == 0) {
+        if (part > 0)
+            continue;
+        constexpr int N = DIM / 8;           // elements a thread holds of a row
 #pragma unroll
-            for (int set = 0; set < kSets; ++set) {
-                float sum = x.sum[set];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (!rows[set].valid)
+        for (int set = 0; set < R / 8; ++set)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float sum = x.sum[set][c];
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const int r = rt * R + 8 * set + 2 * t + c;
+                const Row row = row_of(p, it, r);
+                if (!row.valid)
                     continue;
-                constexpr int N = DIM / 8;
                 if (whole) {
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    __nv_bfloat16 *o = p.out + rows[set].token * p.o_ts + rows[set].q_head * p.o_hs + 2 * N * t;
+                    alignas(16) __nv_bfloat162 v[N / 2];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        alignas(16) __nv_bfloat162 v[N / 2];
+                    for (int e = 0; e < N / 2; ++e)
+                        v[e] = __floats2bfloat162_rn(x.out[set][e][c] * inv, x.out[set][e][2 + c] * inv);
+                    __nv_bfloat16 *o = p.out + row.token * p.o_ts + row.q_head * p.o_hs + N * g;
+                    if (p.out_vec) {
 #pragma unroll
-                        for (int e = 0; e < N; e += 2)
-                            v[e / 2] = __floats2bfloat162_rn(x.out[e][2 * set + half] * inv, x.out[e + 1][2 * set + half] * inv);
-                        if (p.out_vec) {
+                        for (int e = 0; e < N; e += 8)
+                            *reinterpret_cast<uint4 *>(o + e) = *reinterpret_cast<const uint4 *>(v + e / 2);
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < N; e += 8)
-                                *reinterpret_cast<uint4 *>(o + N * half + e) = *reinterpret_cast<const uint4 *>(v + e / 2);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < N; e += 2) {
-                                o[N * half + e] = v[e / 2].x;
-                                o[N * half + e + 1] = v[e / 2].y;
-                            }
+                        for (int e = 0; e < N / 2; ++e) {
+                            o[2 * e] = v[e].x;
+                            o[2 * e + 1] = v[e].y;
                         }
                     }
-                    if (p.lse && t == 0)
-                        p.lse[(int64_t)rows[set].token * p.heads + rows[set].q_head] =
-                            sum == 0.f ? -CUDART_INF_F : (x.top[set] - kWeightLog2 + log2f(sum)) * CUDART_LN2_F;
+                    if (p.lse && g == 0)
+                        p.lse[(int64_t)row.token * p.heads + row.q_head] =
+                            sum == 0.f ? -CUDART_INF_F : (x.top[set][c] - kWeightLog2 + log2f(sum)) * CUDART_LN2_F;
                 } else {
-                    const int64_t row = slot * p.slot_rows + rt * R + 8 * set + g;
-                    float *o = p.parts + row * DIM + 2 * N * t;
+                    float *o = p.parts + (slot * p.slot_rows + r) * DIM + N * g;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int e = 0; e < N; e += 4)
-                            *reinterpret_cast<float4 *>(o + N * half + e) =
-                                make_float4(x.out[e][2 * set + half], x.out[e + 1][2 * set + half], x.out[e + 2][2 * set + half],
-                                            x.out[e + 3][2 * set + half]);
-                    if (t == 0)
-                        reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * DIM)[row] =
-                            make_float2(x.top[set], sum);
+                    for (int e = 0; e < N / 2; e += 2)
+                        *reinterpret_cast<float4 *>(o + 2 * e) = make_float4(x.out[set][e][c], x.out[set][e][2 + c],
+                                                                             x.out[set][e + 1][c], x.out[set][e + 1][2 + c]);
+                    if (g == 0)
+                        reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * DIM)[slot * p.slot_rows + r] =
+                            make_float2(x.top[set][c], sum);
                 }
             }
-        }
     } while (next_piece(p, c, end));
 }
 
@@ -742,7 +760,7 @@ lowm_status_t launch_fp8(const CUtensorMap &map_k, const CUtensorMap &map_v, con
     static SmemOptIn opt_in;
     if (!opt_in.set(reinterpret_cast<const void *>(paged_attention_fp8_kernel<DIM, R>), Attn8Smem<DIM, R>::kBytes))
         return LOWM_ERR_CUDA;
-    const int ctas = std::min((R == 8 ? 2 : 1) * sms, kMaxCtas);
+    const int ctas = std::min(Attn8Smem<DIM, R>::kCtas * sms, kMaxCtas);
     if (p.batch > 0) {
         const lowm_status_t st = launch_pdl(paged_attention_fp8_kernel<DIM, R>, dim3((unsigned)ctas), dim3(kThreads8),
                                             Attn8Smem<DIM, R>::kBytes, stream, map_k, map_v, p);

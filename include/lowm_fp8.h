@@ -120,7 +120,8 @@ lowm_status_t lowm_paged_attention_fp8(const void *q, int64_t q_token_stride, in
                                        void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace lowm_paged_attention_fp8 needs (0 for sizes it refuses). */
-size_t lowm_paged_attention_fp8_workspace(int batch, int q_tokens, int heads, int kv_heads, int dim);
+size_t lowm_paged_attention_fp8_workspace(int batch, int q_tokens, int heads, int kv_heads, int dim, int page_size,
+                                          int table_width);
 
 #ifdef __cplusplus
 }

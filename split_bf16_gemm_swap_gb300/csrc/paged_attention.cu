@@ -34,6 +34,9 @@
 // (453 us).  Few keys: the chain of launch, schedule, first tile and join (4 x 1000
 // keys: 12.6 us).
 //
+// FACTOR: keys come with a number each that multiplies their scores (what a cache of codes, widened to bf16, has of its
+// scales beside powers of two; paged_attention_fp8.cu).  Pages then have 64 tokens, and a tile's numbers arrive with its K.
+//
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.
 #include <cuda_bf16.h>
@@ -80,6 +83,7 @@ struct AttnParams : LineParams<kTileRows, kItemCost, kMinShare> {
     int64_t q_ts, q_hs, o_ts, o_hs, table_stride, num_pages;
     int64_t k_page, k_place, k_head, v_page, v_place, v_head;
     const int32_t *table;
+    const float *k_factor;                   // FACTOR: [num_pages][kv_heads][64] what a key's scores are multiplied by
     int page_size, page_shift, heads, slot_rows;
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
     float q_sign;
@@ -125,6 +129,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
+__device__ __forceinline__ void times2(uint32_t &x, uint32_t &y, float a, float b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(x, y)), "l"(pack2(a, b)));
+    const float2 v = unpack2(r);
+    x = __float_as_uint(v.x);
+    y = __float_as_uint(v.y);
+}
+
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t r;
@@ -138,6 +151,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int 
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
+}
+
+// `bytes` (a multiple of 16) from 16-byte aligned global memory, complete on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // D[tmem] (+)= A[tmem] . B[smem desc], bf16 operands, fp32 accumulator.
@@ -192,13 +213,13 @@ __device__ __forceinline__ uint64_t make_sw128_nmajor_desc(uint32_t saddr, uint3
 }
 
 // ------------------------------------------------------------------ shared memory
-template <int DIM>
+template <int DIM, bool FACTOR>
 struct AttnSmem {
     static constexpr uint32_t kHalves = DIM / 64;                       // 128-byte wide pieces of a row
     static constexpr uint32_t kQ = 0;                                   // [halves][128 rows][64]
     static constexpr uint32_t kTileBytes = kTileKeys * DIM * 2;
     static constexpr uint32_t kRing = kTileRows * DIM * 2;              // [stages][halves][64 keys][64]
-    static constexpr uint32_t kStages = DIM == 128 ? 5 : 10;            // 80 KiB: two CTAs fill an SM's 227 KiB
+    static constexpr uint32_t kStages = DIM == 128 ? (FACTOR ? 4 : 5) : 10;     // 80 KiB: two CTAs fill an SM's 227 KiB
     // A wait for a full stage passes too early when the load before it in that stage has not landed yet: the
     // barrier's parity is then still that of the phase before.  Loads (K0, K1, V0, K2, V1, ..., V of the last tile, then
     // the next item's) may land in any order, so it must follow from what the waiting warp has seen.  At K of tile g
@@ -209,7 +230,12 @@ struct AttnSmem {
     static constexpr uint32_t kBars = kRing + kStages * kTileBytes;     // full, empty [stages]; q; s, p, o [2]; edges; drain
     static constexpr uint32_t kNumBars = 2 * kStages + 9;
     static constexpr uint32_t kSlot = kBars + kNumBars * 8;             // TMEM address, edge word
-    static constexpr uint32_t kBytes = kSlot + 16;                      // 112.2 KiB: two CTAs an SM
+    static constexpr uint32_t kFactors = FACTOR ? (kSlot + 16 + 127) / 128 * 128 : kSlot + 16;   // [slots][64 keys]; copied in bulk
+    // While the softmax is at tile j its weights are missing, so V of tile j keeps its stage, and K of tile
+    // j + 2 + (kStages - 2) / 2 is the last that the ring lets in behind it.
+    static constexpr uint32_t kFactorSlots = FACTOR ? (DIM == 128 ? 4 : 8) : 0;
+    static_assert(!FACTOR || kFactorSlots > 2 + (kStages - 2) / 2, "a tile's factors would be overwritten while they are read");
+    static constexpr uint32_t kBytes = kFactors + kFactorSlots * kTileKeys * 4;    // 112.2 KiB: two CTAs an SM
 };
 
 template <int DIM>
@@ -323,7 +349,7 @@ __device__ __forceinline__ bool clean_values(uint8_t *tile, const Seen &seen, in
 // and change nothing a second time.  A warp's 32 rows take some milliseconds at
 // worst, whatever the lengths (3 ms an item with nothing but NaN in V): far below
 // the limit of the other warps' waits.
-template <int DIM>
+template <int DIM, bool FACTOR>
 __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows, int sequence, const Row &mine, int key_begin,
                                              int key_end, float shift, float factor, int64_t slot, int r)
 {
@@ -366,6 +392,8 @@ __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows,
                          __bfloat162float(p.k[page * p.k_page + place * p.k_place + g * p.k_head + lane * E + e]), s);
             for (int o = 16; o > 0; o >>= 1)
                 s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (FACTOR)
+                s *= p.k_factor[(page * p.kv_heads + g) * kTileKeys + place];
             // (a weight too small for a float still carries an infinity)
             const float a = s == -p.q_sign * CUDART_INF_F
                                 ? 0.f
@@ -386,12 +414,12 @@ __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows,
     }
 }
 
-template <int DIM>
+template <int DIM, bool FACTOR>
 __global__ void __launch_bounds__(kAttnThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                            const AttnParams p)
 {
-    using L = AttnSmem<DIM>;
+    using L = AttnSmem<DIM, FACTOR>;
     constexpr uint32_t kColumns = 256;       // two S buffers and O (192 or 256 columns), a power of two
     constexpr uint32_t kOColumn = 2 * kSColumns;
     // The swizzle repeats every 1024 bytes, so the base must be a multiple; rounding it up at run time
@@ -449,7 +477,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             // -------------------------------------------------------- TMA: K0, K1, V0, K2, V1, ...
             const int box_keys = min(p.page_size, kTileKeys), boxes = kTileKeys / box_keys;
             const int mine = lane / (int)L::kHalves, half = lane % (int)L::kHalves;   // this lane's box and half
-            uint32_t i = 0;
+            uint32_t i = 0, keys_loaded = 0;                            // (tiles of K: the softmax's count, too)
             bool ok = true;
             do {
                 const int from = c.from, n = c.to - c.from;
@@ -472,9 +500,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                     const int key0 = (it.first_tile + tile) * kTileKeys;
                     // Pages past the sequence's end are not requested.
                     const int used = min(boxes, max(1, (it.kv - key0 + box_keys - 1) / box_keys));
+                    const bool factors = FACTOR && map == &map_k && __shfl_sync(0xffffffffu, page, 0) >= 0;   // (a tile is a page)
                     if (lane == 0)
-                        ptx::mbar_arrive_expect_tx(bar_full + 8 * s, (uint32_t)used * box_keys * DIM * 2);
+                        ptx::mbar_arrive_expect_tx(bar_full + 8 * s,
+                                                   (uint32_t)used * box_keys * DIM * 2 + (factors ? kTileKeys * 4 : 0));
                     __syncwarp();
+                    if constexpr (FACTOR) {
+                        if (factors && lane == 0)
+                            bulk_load(sbase + L::kFactors + keys_loaded % L::kFactorSlots * (kTileKeys * 4),
+                                      p.k_factor + ((int64_t)page * p.kv_heads + it.head) * kTileKeys, kTileKeys * 4, bar_full + 8 * s);
+                        keys_loaded += map == &map_k;
+                    }
                     if (mine < used)
                         tma_load_4d(sbase + L::kRing + s * L::kTileBytes + half * (kTileKeys * 128) + mine * box_keys * 128,
                                     map, half * 64, key0 & (p.page_size - 1), it.head, page, bar_full + 8 * s);
@@ -650,6 +686,18 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         tmem_ld_x32(s_addr, s0);
                         tmem_ld_x32(s_addr + 32, s1);
                         ptx::tmem_wait_ld();
+                        if constexpr (FACTOR) {
+                            const float4 *f = reinterpret_cast<const float4 *>(smem + L::kFactors) +
+                                              g % L::kFactorSlots * (kTileKeys / 4);
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                const float4 a = f[k / 4], b = f[8 + k / 4];
+                                times2(s0[k], s0[k + 1], a.x, a.y);
+                                times2(s0[k + 2], s0[k + 3], a.z, a.w);
+                                times2(s1[k], s1[k + 1], b.x, b.y);
+                                times2(s1[k + 2], s1[k + 3], b.z, b.w);
+                            }
+                        }
                         if (key0 < all_lo || key0 + kTileKeys - 1 > all_hi) {
                             const int hi = w.valid ? w.hi - key0 : -1, lo = w.lo - key0;
 #pragma unroll
@@ -772,7 +820,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         ml[slot * p.slot_rows + r] = make_float2(m * p.scale_log2, l);
                     }
                     if (edges)
-                        add_edge_values<DIM>(p, __ballot_sync(0xffffffffu, w.valid), sequence, w, key_begin, key_end,
+                        add_edge_values<DIM, FACTOR>(p, __ballot_sync(0xffffffffu, w.valid), sequence, w, key_begin, key_end,
                                              m == -CUDART_INF_F ? 0.f : m * p.scale_log2, whole ? inv : 1.f,
                                              whole ? -1 : slot, r);
                 }
@@ -906,17 +954,17 @@ lowm_status_t encode_cache(const void *base, int64_t page_stride, int64_t place_
                : LOWM_ERR_CUDA;
 }
 
-template <int DIM>
+template <int DIM, bool FACTOR>
 lowm_status_t launch_attention(const CUtensorMap &map_k, const CUtensorMap &map_v, const AttnParams &p, int sms,
                                void *stream)
 {
     static SmemOptIn opt_in;
-    if (!opt_in.set(reinterpret_cast<const void *>(paged_attention_kernel<DIM>), AttnSmem<DIM>::kBytes))
+    if (!opt_in.set(reinterpret_cast<const void *>(paged_attention_kernel<DIM, FACTOR>), AttnSmem<DIM, FACTOR>::kBytes))
         return LOWM_ERR_CUDA;
     const int ctas = std::min(2 * sms, kMaxAttnCtas);
     if (p.batch > 0) {
-        const lowm_status_t st = launch_pdl(paged_attention_kernel<DIM>, dim3((unsigned)ctas), dim3(kAttnThreads),
-                                            AttnSmem<DIM>::kBytes, stream, map_k, map_v, p);
+        const lowm_status_t st = launch_pdl(paged_attention_kernel<DIM, FACTOR>, dim3((unsigned)ctas), dim3(kAttnThreads),
+                                            AttnSmem<DIM, FACTOR>::kBytes, stream, map_k, map_v, p);
         if (st != LOWM_OK)
             return st;
     }
@@ -935,15 +983,14 @@ extern "C" size_t lowm_paged_attention_workspace(int batch, int q_tokens, int he
            kMaxAttnCtas * sizeof(CutItem);
 }
 
-extern "C" lowm_status_t lowm_paged_attention(
+lowm_status_t lowm::attend_pages(
     const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache, int64_t k_page_stride,
     int64_t k_place_stride, int64_t k_cache_head_stride, const void *v_cache, int64_t v_page_stride,
     int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size, const int32_t *page_table,
     int64_t page_table_stride, int table_width, const int32_t *kv_lens, const int32_t *cu_q, void *out,
     int64_t out_token_stride, int64_t out_head_stride, float *lse, int batch, int q_tokens, int heads, int kv_heads,
-    int dim, float scale, int window, void *workspace, size_t workspace_bytes, void *stream)
+    int dim, float scale, int window, const float *k_factor, void *workspace, size_t workspace_bytes, void *stream)
 {
-    using namespace lowm;
     if (batch < 0 || q_tokens < 0 || heads <= 0 || kv_heads <= 0 || dim <= 0 || num_pages <= 0 || num_pages > INT_MAX || page_size <= 0 ||
         table_width < 0 || window < 0 || !(scale == scale))
         return LOWM_ERR_INVALID_ARGUMENT;
@@ -1007,6 +1054,7 @@ extern "C" lowm_status_t lowm_paged_attention(
     p.v_place = v_place_stride;
     p.v_head = v_cache_head_stride;
     p.table = page_table;
+    p.k_factor = k_factor;
     p.kv_lens = kv_lens;
     p.cu_q = cu_q;
     p.page_size = page_size;
@@ -1038,6 +1086,23 @@ extern "C" lowm_status_t lowm_paged_attention(
         (st = encode_cache(v_cache, v_page_stride, v_place_stride, v_cache_head_stride, num_pages, page_size, kv_heads,
                            dim, &map_v)) != LOWM_OK)
         return st;
-    return dim == 64 ? launch_attention<64>(map_k, map_v, p, sms, stream)
-                     : launch_attention<128>(map_k, map_v, p, sms, stream);
+    if (k_factor)
+        return dim == 64 ? launch_attention<64, true>(map_k, map_v, p, sms, stream)
+                         : launch_attention<128, true>(map_k, map_v, p, sms, stream);
+    return dim == 64 ? launch_attention<64, false>(map_k, map_v, p, sms, stream)
+                     : launch_attention<128, false>(map_k, map_v, p, sms, stream);
+}
+
+extern "C" lowm_status_t lowm_paged_attention(
+    const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache, int64_t k_page_stride,
+    int64_t k_place_stride, int64_t k_cache_head_stride, const void *v_cache, int64_t v_page_stride,
+    int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size, const int32_t *page_table,
+    int64_t page_table_stride, int table_width, const int32_t *kv_lens, const int32_t *cu_q, void *out,
+    int64_t out_token_stride, int64_t out_head_stride, float *lse, int batch, int q_tokens, int heads, int kv_heads,
+    int dim, float scale, int window, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return lowm::attend_pages(q, q_token_stride, q_head_stride, k_cache, k_page_stride, k_place_stride, k_cache_head_stride,
+                              v_cache, v_page_stride, v_place_stride, v_cache_head_stride, num_pages, page_size, page_table,
+                              page_table_stride, table_width, kv_lens, cu_q, out, out_token_stride, out_head_stride, lse, batch,
+                              q_tokens, heads, kv_heads, dim, scale, window, nullptr, workspace, workspace_bytes, stream);
 }

@@ -719,6 +719,114 @@ __global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Att
     }
 }
 
+// ------------------------------------------------------------------ chunks: the cache widened first
+// Where sequences bring many rows a head, the keys and values that they see are written out in bf16 once, in pages of 64
+// tokens, and the tcgen05 attention of paged_attention.cu runs on those: it does 1.2 PFLOP/s where the registers' products
+// reach 0.15, and writing and reading 2 bytes an element instead of reading 1 costs what 64 rows cost there.  A code times a power of two is
+// a bf16 number, so K keeps its scales' powers of two, and their mantissas, in [1, 2), multiply the scores (rounded into K
+// they made three quarters of the result's error); V is rounded with its scale, as bf16 weights and outputs are.
+constexpr int kWideRows = 64;                // rows a sequence and head bring on average, at least
+constexpr int64_t kWideBytes = (int64_t)8 << 30;   // of scratch memory at most
+constexpr int kWideKeys = 64;                // tokens of a page of the copy
+
+struct WidenParams {
+    const uint8_t *k, *v;
+    const float *k_scale, *v_scale;
+    int64_t k_page, k_place, k_head, v_page, v_place, v_head, ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
+    int64_t table_stride, num_pages;
+    const int32_t *table, *kv_lens, *cu_q;
+    __nv_bfloat16 *wide_k, *wide_v;          // [batch * pages][kv_heads][64][dim]
+    float *factor;                           // [batch * pages][kv_heads][64]
+    int32_t *wide_table;                     // [batch][pages]
+    int page_shift, block_shift, batch, q_tokens, kv_heads, dim, window, capacity, pages;
+};
+
+__device__ __forceinline__ void widen_16(uint4 codes, float scale, uint4 *to)
+{
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    alignas(16) __nv_bfloat162 out[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = __half22float2(e4m3x2_to_half2(w[i] & 0xffffu)), b = __half22float2(e4m3x2_to_half2(w[i] >> 16));
+        out[2 * i] = __floats2bfloat162_rn(a.x * scale, a.y * scale);
+        out[2 * i + 1] = __floats2bfloat162_rn(b.x * scale, b.y * scale);
+    }
+    to[0] = reinterpret_cast<const uint4 *>(out)[0];
+    to[1] = reinterpret_cast<const uint4 *>(out)[1];
+}
+
+// A CTA widens 64 tokens of a sequence at a time, 16 elements a thread.
+constexpr int kWidenThreads = 256;
+
+__global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int chunks = p.dim / 16, per_token = p.kv_heads * chunks, work = kWideKeys * per_token;
+    for (int64_t task = blockIdx.x; task < (int64_t)p.batch * p.pages; task += gridDim.x) {
+        const int b = (int)(task / p.pages), j = (int)(task - (int64_t)b * p.pages);
+        if (threadIdx.x == 0)
+            p.wide_table[task] = (int)task;
+        const int q0 = min(max(p.cu_q[b], 0), p.q_tokens), q_len = min(max(p.cu_q[b + 1], q0), p.q_tokens) - q0;
+        const int kv = min(max(p.kv_lens[b], 0), p.capacity);
+        const int first = p.window > 0 ? kv - q_len - p.window + 1 : 0;      // no row sees a key before it
+        const int key0 = j * kWideKeys, end = min(kv, key0 + kWideKeys);
+        if (q_len == 0 || key0 >= kv || key0 + kWideKeys <= first)
+            continue;
+        // The scale of K: a power of two for the codes, and the rest (any number but those: the rest alone).
+        auto k_scale_of = [&](int64_t page, int key, int head, float &rest) {
+            const int block = (key & ((1 << p.page_shift) - 1)) >> p.block_shift;
+            const float a = p.k_scale[page * p.ks_page + block * p.ks_block + head * p.ks_head];
+            const uint32_t exponent = __float_as_uint(a) & 0x7f800000u;
+            const bool normal = exponent != 0 && exponent != 0x7f800000u;
+            rest = normal ? __uint_as_float((__float_as_uint(a) & 0x807fffffu) | 0x3f800000u) : a;
+            return normal ? __uint_as_float(exponent) : 1.f;
+        };
+        for (int i = threadIdx.x; i < p.kv_heads * kWideKeys; i += kWidenThreads) {
+            const int head = i / kWideKeys, key = key0 + i % kWideKeys;
+            float rest = 1.f;
+            if (key < end) {
+                const int64_t page = p.table[b * p.table_stride + (key >> p.page_shift)];
+                if (page >= 0 && page < p.num_pages)
+                    (void)k_scale_of(page, key, head, rest);
+            }
+            p.factor[(task * p.kv_heads + head) * kWideKeys + i % kWideKeys] = rest;
+        }
+        for (int i0 = threadIdx.x; i0 < work; i0 += 4 * kWidenThreads) {
+            uint4 k[4], v[4];
+            float ks[4], vs[4];
+            int64_t to[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * kWidenThreads, key = key0 + i / per_token;
+                to[u] = -1;
+                if (i >= work || key >= end)
+                    continue;
+                const int head = i % per_token / chunks, chunk = i % chunks;
+                const int64_t page = p.table[b * p.table_stride + (key >> p.page_shift)];
+                const int place = key & ((1 << p.page_shift) - 1), block = place >> p.block_shift;
+                to[u] = ((task * p.kv_heads + head) * kWideKeys + (key - key0)) * p.dim + 16 * chunk;
+                if (page < 0 || page >= p.num_pages) {
+                    k[u] = v[u] = make_uint4(0, 0, 0, 0);
+                    ks[u] = vs[u] = 0.f;
+                } else {
+                    k[u] = *reinterpret_cast<const uint4 *>(p.k + page * p.k_page + place * p.k_place + head * p.k_head + 16 * chunk);
+                    v[u] = *reinterpret_cast<const uint4 *>(p.v + page * p.v_page + place * p.v_place + head * p.v_head + 16 * chunk);
+                    float rest;
+                    ks[u] = k_scale_of(page, key, head, rest);
+                    vs[u] = fminf(fmaxf(p.v_scale[page * p.vs_page + block * p.vs_block + head * p.vs_head], 1.f / kMaxScale), kMaxScale);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (to[u] >= 0) {
+                    widen_16(k[u], ks[u], reinterpret_cast<uint4 *>(p.wide_k + to[u]));
+                    widen_16(v[u], vs[u], reinterpret_cast<uint4 *>(p.wide_v + to[u]));
+                }
+        }
+    }
+}
+
 constexpr int kMaxGroup = 128;
 
 bool attention_fp8_shape_ok(int batch, int q_tokens, int heads, int kv_heads, int dim)
@@ -774,11 +882,50 @@ lowm_status_t launch_fp8(const CUtensorMap &map_k, const CUtensorMap &map_v, con
 }  // namespace
 }  // namespace lowm
 
-extern "C" size_t lowm_paged_attention_fp8_workspace(int batch, int q_tokens, int heads, int kv_heads, int dim)
+namespace lowm {
+namespace {
+
+int64_t wide_pages(int page_size, int table_width)
+{
+    const int64_t capacity = std::min<int64_t>((int64_t)table_width * page_size, kMaxKeys);
+    return (capacity + kWideKeys - 1) / kWideKeys;
+}
+
+// Bytes of one widened tensor.
+int64_t wide_bytes(int batch, int kv_heads, int dim, int page_size, int table_width)
+{
+    return batch * wide_pages(page_size, table_width) * kWideKeys * kv_heads * dim * 2;
+}
+
+// Whether a call widens the cache first.
+bool widens(int batch, int q_tokens, int heads, int kv_heads, int dim, int page_size, int table_width)
+{
+    return (int64_t)q_tokens * (heads / kv_heads) >= (int64_t)kWideRows * std::max(batch, 1) && table_width > 0 &&
+           2.0 * batch * wide_pages(page_size, table_width) * kWideKeys * kv_heads * dim * 2 <= (double)kWideBytes;
+}
+
+size_t wide_table_bytes(int batch, int page_size, int table_width)
+{
+    return (size_t)(batch * wide_pages(page_size, table_width) * 4 + 15) / 16 * 16;
+}
+
+size_t factor_bytes(int batch, int kv_heads, int page_size, int table_width)
+{
+    return (size_t)(batch * wide_pages(page_size, table_width) * kWideKeys * kv_heads * 4);
+}
+
+}  // namespace
+}  // namespace lowm
+
+extern "C" size_t lowm_paged_attention_fp8_workspace(int batch, int q_tokens, int heads, int kv_heads, int dim, int page_size,
+                                                     int table_width)
 {
     using namespace lowm;
-    if (!attention_fp8_shape_ok(batch, q_tokens, heads, kv_heads, dim))
+    if (!attention_fp8_shape_ok(batch, q_tokens, heads, kv_heads, dim) || page_size <= 0 || table_width < 0)
         return 0;
+    if (widens(batch, q_tokens, heads, kv_heads, dim, page_size, table_width))
+        return (size_t)2 * wide_bytes(batch, kv_heads, dim, page_size, table_width) + wide_table_bytes(batch, page_size, table_width) +
+               factor_bytes(batch, kv_heads, page_size, table_width) + lowm_paged_attention_workspace(batch, q_tokens, heads, kv_heads, dim);
     return (size_t)2 * kMaxCtas * slot_rows_fp8(q_tokens, heads, kv_heads) * (dim + 2) * sizeof(float) + kMaxCtas * sizeof(CutItem8);
 }
 
@@ -803,7 +950,7 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
     if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !cu_q || !out || !workspace || (batch && !kv_lens) ||
         (batch && table_width && !page_table))
         return LOWM_ERR_INVALID_ARGUMENT;
-    if (workspace_bytes < lowm_paged_attention_fp8_workspace(batch, q_tokens, heads, kv_heads, dim))
+    if (workspace_bytes < lowm_paged_attention_fp8_workspace(batch, q_tokens, heads, kv_heads, dim, page_size, table_width))
         return LOWM_ERR_INVALID_ARGUMENT;
     const int64_t cache_strides[] = {k_page_stride, k_place_stride, k_cache_head_stride,
                                      v_page_stride, v_place_stride, v_cache_head_stride};
@@ -839,6 +986,61 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
     lowm_status_t st = host_check_device(&sms);
     if (st != LOWM_OK)
         return st;
+    auto log2_of = [](int n) {
+        int shift = 0;
+        while ((1 << shift) < n)
+            ++shift;
+        return shift;
+    };
+    if (widens(batch, q_tokens, heads, kv_heads, dim, page_size, table_width)) {
+        WidenParams w;
+        w.k = static_cast<const uint8_t *>(k_cache);
+        w.v = static_cast<const uint8_t *>(v_cache);
+        w.k_scale = k_scale;
+        w.v_scale = v_scale;
+        w.k_page = k_page_stride;
+        w.k_place = k_place_stride;
+        w.k_head = k_cache_head_stride;
+        w.v_page = v_page_stride;
+        w.v_place = v_place_stride;
+        w.v_head = v_cache_head_stride;
+        w.ks_page = ks_page_stride;
+        w.ks_block = ks_block_stride;
+        w.ks_head = ks_head_stride;
+        w.vs_page = vs_page_stride;
+        w.vs_block = vs_block_stride;
+        w.vs_head = vs_head_stride;
+        w.table_stride = page_table_stride;
+        w.num_pages = num_pages;
+        w.table = page_table;
+        w.kv_lens = kv_lens;
+        w.cu_q = cu_q;
+        w.page_shift = log2_of(page_size);
+        w.block_shift = log2_of(block);
+        w.batch = batch;
+        w.q_tokens = q_tokens;
+        w.kv_heads = kv_heads;
+        w.dim = dim;
+        w.window = window < kMaxKeys ? window : 0;
+        w.capacity = (int)capacity;
+        w.pages = (int)wide_pages(page_size, table_width);
+        uint8_t *at = static_cast<uint8_t *>(workspace);
+        const int64_t bytes = wide_bytes(batch, kv_heads, dim, page_size, table_width);
+        w.wide_k = reinterpret_cast<__nv_bfloat16 *>(at);
+        w.wide_v = reinterpret_cast<__nv_bfloat16 *>(at + bytes);
+        w.factor = reinterpret_cast<float *>(at + 2 * bytes);
+        const size_t tables = (size_t)2 * bytes + factor_bytes(batch, kv_heads, page_size, table_width);
+        w.wide_table = reinterpret_cast<int32_t *>(at + tables);
+        const size_t used = tables + wide_table_bytes(batch, page_size, table_width);
+        const int64_t tasks = (int64_t)batch * w.pages, head = (int64_t)kWideKeys * dim;
+        st = launch_pdl(widen_kernel, dim3((unsigned)std::min<int64_t>(tasks, 8 * sms)), dim3(kWidenThreads), 0, stream, w);
+        if (st != LOWM_OK)
+            return st;
+        return attend_pages(q, q_token_stride, q_head_stride, w.wide_k, kv_heads * head, dim, head, w.wide_v, kv_heads * head, dim,
+                            head, tasks, kWideKeys, w.wide_table, w.pages, w.pages, kv_lens, cu_q, out, out_token_stride,
+                            out_head_stride, lse, batch, q_tokens, heads, kv_heads, dim, scale, window, w.factor, at + used,
+                            workspace_bytes - used, stream);
+    }
     unsigned int *status = host_status_word();
     if (!status)
         return LOWM_ERR_CUDA;
@@ -871,11 +1073,8 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
         p.kv_lens = kv_lens;
         p.cu_q = cu_q;
         p.page_size = page_size;
-        p.page_shift = p.block_shift = 0;
-        while ((1 << p.page_shift) < page_size)
-            ++p.page_shift;
-        while ((1 << p.block_shift) < block)
-            ++p.block_shift;
+        p.page_shift = log2_of(page_size);
+        p.block_shift = log2_of(block);
         p.batch = batch;
         p.q_tokens = q_tokens;
         p.heads = heads;

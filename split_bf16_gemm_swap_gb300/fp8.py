@@ -34,7 +34,7 @@ layer._ARGTYPES.update({
                              *_cache, *_cache, *_cache, *_cache, _l, _i, _i, _i, _i, _i, _i, _i, _p],
     "lowm_paged_attention_fp8": [_p, _l, _l, *_cache, *_cache, *_cache, *_cache, _l, _i, _i, _p, _l, _i, _p, _p, _p, _l, _l,
                                  _p, _i, _i, _i, _i, _i, _f, _i, _p, _z, _p],
-    "lowm_paged_attention_fp8_workspace": [_i, _i, _i, _i, _i],
+    "lowm_paged_attention_fp8_workspace": [_i] * 7,
 })
 
 FP8 = torch.float8_e4m3fn
@@ -57,8 +57,9 @@ def lowm_paged_attention_fp8(*args) -> int:
     return function("lowm_paged_attention_fp8")(*args)
 
 
-def lowm_paged_attention_fp8_workspace(batch: int, q_tokens: int, heads: int, kv_heads: int, dim: int) -> int:
-    return function("lowm_paged_attention_fp8_workspace")(batch, q_tokens, heads, kv_heads, dim)
+def lowm_paged_attention_fp8_workspace(batch: int, q_tokens: int, heads: int, kv_heads: int, dim: int, page_size: int,
+                                       table_width: int) -> int:
+    return function("lowm_paged_attention_fp8_workspace")(batch, q_tokens, heads, kv_heads, dim, page_size, table_width)
 
 
 _attention_bytes = functools.lru_cache(maxsize=4096)(lowm_paged_attention_fp8_workspace)
@@ -263,7 +264,7 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_le
         out = torch.empty(q_shape, dtype=bf16, device=q.device)
     os = _rows(out, "out", bf16, q_shape, device)
     lse = torch.empty((q_tokens, heads), dtype=torch.float32, device=q.device) if return_lse else None
-    nbytes = _attention_bytes(batch, q_tokens, heads, kv_heads, dim)
+    nbytes = _attention_bytes(batch, q_tokens, heads, kv_heads, dim, k_cache.shape[1], table_width)
     _launch("lowm_paged_attention_fp8", (
         q.data_ptr(), qs[0], qs[1], *cache, page_table.data_ptr(), table_stride, table_width, kv_lens.data_ptr(),
         cu_q.data_ptr(), out.data_ptr(), os[0], os[1], None if lse is None else lse.data_ptr(), batch, q_tokens, heads, kv_heads,

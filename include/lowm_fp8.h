@@ -55,6 +55,20 @@ lowm_status_t lowm_gemm_fp8(const void *A, const float *a_scale, const void *W, 
                             int M, int N, int K, unsigned flags, void *stream);
 
 /*
+ * lowm_gemm_fp8 of bf16 activations, which are quantised on the way as by
+ * lowm_quantize_fp8 with block_rows 1.
+ *   x             [M, K] bf16 by row stride
+ *   workspace     lowm_gemm_fp8_bf16_workspace(M, K) bytes, 16-byte aligned; contents
+ *                 need not survive between calls
+ */
+lowm_status_t lowm_gemm_fp8_bf16(const void *x, int64_t x_stride, const void *W, const float *w_scale, void *C,
+                                 int M, int N, int K, unsigned flags, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* Bytes of workspace lowm_gemm_fp8_bf16 needs (0 for sizes it refuses). */
+size_t lowm_gemm_fp8_bf16_workspace(int M, int K);
+
+/*
  * lowm_rope_append for a cache of codes.  k_cache and v_cache are e4m3
  * [num_pages, page_size, kv_heads, dim], k_scale and v_scale fp32 [num_pages,
  * page_size / block, kv_heads], all by strides.  A block is `block` places of a

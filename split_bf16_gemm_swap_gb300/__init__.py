@@ -22,7 +22,8 @@ _LAYER = ("LOWM_MOE_SIGMOID", "LOWM_MOE_SOFTMAX", "moe", "paged_attention", "rel
           "lowm_residual_norm", "lowm_rope_append")
 
 
-_FP8 = ("gemm_fp8", "paged_attention_fp8", "quantize_fp8", "rope_append_fp8", "lowm_gemm_fp8", "lowm_paged_attention_fp8",
+_FP8 = ("gemm_fp8", "paged_attention_fp8", "quantize_fp8", "rope_append_fp8", "lowm_gemm_fp8",
+        "lowm_gemm_fp8_bf16", "lowm_gemm_fp8_bf16_workspace", "lowm_paged_attention_fp8",
         "lowm_paged_attention_fp8_workspace", "lowm_quantize_fp8", "lowm_rope_append_fp8")
 _PAGES = ("compact_pages", "copy_pages", "extend_pages", "fork_pages", "lowm_compact_pages", "lowm_compact_pages_workspace",
           "lowm_copy_pages", "lowm_extend_pages", "lowm_extend_pages_workspace", "lowm_fork_pages", "lowm_page_span_t")

@@ -16,7 +16,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "../../include/lowm_fp8.h"
 #include "fp8_device.cuh"
@@ -28,6 +27,12 @@ namespace {
 
 constexpr int kTileN = 128, kBlock = 128;    // rows of W a tile, K a block
 constexpr int kMaxSplit = 8;
+constexpr int kBuffers = 4;                  // of a K block's sums in TMEM: two stages of two blocks, or four of one
+// A stage's scales stay until they have been used: behind the ring's stages, those of the sums in TMEM and one more, since a
+// load of stage i means that stage i - stages has been multiplied, so that the sums of the kBuffers before it have been
+// read and all but the last of those used.
+constexpr uint32_t kMaxStages = 16, kMaxScales = kMaxStages + kBuffers + 1;
+constexpr uint32_t kRingAt = 1024;           // (the barriers take 520 bytes)
 
 // Bits of the device status word (above those of the other operators).
 enum : uint32_t {
@@ -36,28 +41,34 @@ enum : uint32_t {
     kErrGemm8Sums = 1u << 27,
     kErrGemm8Free = 1u << 28,
     kErrGemm8Base = 1u << 29,                // dynamic shared memory not on a 1024-byte boundary
+    kErrGemm8Mail = 1u << 30,
 };
 
 struct Gemm8Params {
-    const float *a_scale, *w_scale;
+    const float *a_scale, *w_scale;          // a_scale: codes
+    const __nv_bfloat16 *x;                  // or the activations themselves (QUANT)
+    int64_t x_stride;
+    bool x_vec;                              // 8-byte loads
     __nv_bfloat16 *c;
-    int M, N, blocks;                        // blocks of K
+    int M, N, K, blocks;                     // blocks of K
     int per_stage, stages;                   // K blocks a ring stage, ring stages
     int planes;                              // the tensor maps have the K blocks as a third dimension
+    int mailbox, apart;                      // offset of the ranks' mailbox; not the drained ring
     unsigned flags;
     unsigned int *status;
 };
 
-template <int M_PAD>
+// Warps: 0 requests W, 1 issues MMAs, then the epilogue's, then those that bring A and the scales.
+template <int M_PAD, bool QUANT>
 struct Gemm8Shape {
-    static constexpr int kEpilogueWarps = M_PAD > 64 ? 8 : 4;
-    static constexpr int kThreads = 64 + 32 * kEpilogueWarps;
-    static constexpr int kColumns = M_PAD / (kEpilogueWarps / 4);        // tokens a thread sums
-    static constexpr int kBuffers = M_PAD > 64 ? 2 : 4;                  // of TMEM
-    static constexpr uint32_t kTmem = kBuffers * M_PAD < 32 ? 32 : kBuffers * M_PAD;
+    static constexpr int kColumns = M_PAD < 32 ? M_PAD : (M_PAD < 128 ? 32 : 64);    // tokens a thread sums
+    static constexpr int kEpilogueWarps = 4 * (M_PAD / kColumns);
+    static constexpr int kLoadWarp = 2 + kEpilogueWarps, kLoadWarps = QUANT ? 4 : 1;
+    static constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+    static constexpr uint32_t kTmem = kBuffers * M_PAD;
     static constexpr uint32_t kWBytes = kTileN * kBlock, kABytes = M_PAD * kBlock;   // of a K block
-    static constexpr uint32_t kScaleBytes = (M_PAD + 4) * 4;             // a K block's scales: tokens, then the tile's
-    __host__ __device__ static constexpr uint32_t stage_bytes(int per_stage) { return per_stage * (kWBytes + kABytes); }
+    static constexpr uint32_t kScaleBytes = M_PAD * 4;                   // a K block's: each token's scale times the tile's
+    static_assert(!QUANT || M_PAD == 16, "four rows a warp");
 };
 
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B, both K-major.
@@ -74,21 +85,6 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-__device__ __forceinline__ void copy_async_4(uint32_t dst, const float *src, uint32_t bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void copies_arrive(uint32_t bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v)
-{
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_size()
@@ -108,25 +104,84 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
         : "memory");
 }
 
-template <int M_PAD>
-__global__ void __launch_bounds__(Gemm8Shape<M_PAD>::kThreads)
+// A place in a ring and the parity of its phase, without a division a step (two of them took 200 of a stage's 1000 cycles).
+struct RingPlace {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void step(uint32_t places)
+    {
+        if (++at == places) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Four rows of activations, 128 columns each, as one warp quantises them: a lane has four columns.
+struct FourRows {
+    uint2 v[4];
+
+    __device__ __forceinline__ void load(const Gemm8Params &p, int row0, int column)
+    {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            v[r] = make_uint2(0, 0);
+            if (row0 + r >= p.M || column >= p.K)            // (K is a multiple of 16)
+                continue;
+            const __nv_bfloat16 *x = p.x + (row0 + r) * p.x_stride + column;
+            if (p.x_vec) {
+                v[r] = *reinterpret_cast<const uint2 *>(x);
+            } else {
+                const uint16_t *e = reinterpret_cast<const uint16_t *>(x);
+                v[r] = make_uint2(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16);
+            }
+        }
+    }
+
+    // Codes into rows row0.. of a swizzled block, and their scales times w.
+    __device__ __forceinline__ void store(uint8_t *block, float *scales, int row0, float w) const
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v[r].x));
+            const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v[r].y));
+            float amax = fmaxf(fmaxf(finite_magnitude(a.x), finite_magnitude(a.y)), fmaxf(finite_magnitude(b.x), finite_magnitude(b.y)));
+            // (magnitudes order as their bits do)
+            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+            const int e = scale_exponent(amax);
+            const float inverse = power_of_two(-e);
+            const uint32_t word = to_e4m3x2(nan_unless_finite(a.x) * inverse, nan_unless_finite(a.y) * inverse) |
+                                  to_e4m3x2(nan_unless_finite(b.x) * inverse, nan_unless_finite(b.y) * inverse) << 16;
+            const int row = row0 + r;
+            *reinterpret_cast<uint32_t *>(block + row * kBlock + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) = word;
+            if (lane == 0)
+                scales[row] = power_of_two(e) * w;
+        }
+    }
+};
+
+template <int M_PAD, bool QUANT>
+__global__ void __launch_bounds__(Gemm8Shape<M_PAD, QUANT>::kThreads, M_PAD > 32 ? 1 : 2)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const Gemm8Params p)
 {
-    using S = Gemm8Shape<M_PAD>;
-    constexpr uint32_t kMaxStages = 16;
+    using S = Gemm8Shape<M_PAD, QUANT>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    const uint32_t sbase = ptx::smem_u32(smem);
-    const uint32_t stage_bytes = S::stage_bytes(p.per_stage), a_at = p.per_stage * S::kWBytes;
-    const uint32_t scales_at = p.stages * stage_bytes, scale_stage = p.per_stage * S::kScaleBytes;
-    const uint32_t bars = sbase + scales_at + p.stages * scale_stage;
-    const uint32_t bar_full = bars, bar_empty = bars + 8 * kMaxStages, bar_sums = bar_empty + 8 * kMaxStages,
-                   bar_free = bar_sums + 8 * S::kBuffers, bar_drain = bar_free + 8 * S::kBuffers, slot = bar_drain + 8;
+    // [barriers, 1 KiB][ring of W and A][ring of scales][mailbox, if apart].
+    const uint32_t sbase = ptx::smem_u32(smem), ring = sbase + kRingAt;
+    const uint32_t a_at = p.per_stage * S::kWBytes, stage_bytes = a_at + p.per_stage * S::kABytes;
+    const uint32_t scales_at = kRingAt + p.stages * stage_bytes, scale_stage = p.per_stage * S::kScaleBytes;
+    const uint32_t bar_full = sbase, bar_empty = sbase + 8 * kMaxStages, bar_sums = bar_empty + 8 * kMaxStages,
+                   bar_free = bar_sums + 8 * kBuffers, bar_drain = bar_free + 8 * kBuffers, bar_mail = bar_drain + 8,
+                   bar_scales = bar_mail + 8, slot = bar_scales + 8 * kMaxScales;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ranks = (int)cluster_size(), rank = (int)ptx::cluster_ctarank();
     const int n0 = (int)(blockIdx.x / ranks) * kTileN;
-    // This rank's stages of K.
+    // This rank's stages of K, and its share of the tokens.
     const int all = (p.blocks + p.per_stage - 1) / p.per_stage;
     const int begin = (int)((int64_t)all * rank / ranks), end = (int)((int64_t)all * (rank + 1) / ranks);
+    const int buffers = kBuffers / p.per_stage;              // stages' sums in TMEM
+    const uint32_t scale_slots = p.stages + buffers + 1;
+    const int tokens = M_PAD / ranks, mine = min(max(p.M - rank * tokens, 0), tokens);
     if (sbase & 1023u) {                     // (the same for every CTA)
         if (threadIdx.x == 0)
             atomicOr(p.status, kErrGemm8Base);
@@ -134,16 +189,21 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD>::kThreads)
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 1 + 32);                     // codes, and each lane's scales
-            ptx::mbar_init(bar_empty + 8 * s, 1 + S::kEpilogueWarps);
+            ptx::mbar_init(bar_full + 8 * s, 1 + S::kLoadWarps);         // W, A
+            ptx::mbar_init(bar_empty + 8 * s, 1);
         }
-        for (int b = 0; b < S::kBuffers; ++b) {
+        for (uint32_t s = 0; s < scale_slots; ++s)
+            ptx::mbar_init(bar_scales + 8 * s, S::kLoadWarps);
+        for (int b = 0; b < kBuffers; ++b) {
             ptx::mbar_init(bar_sums + 8 * b, 1);
             ptx::mbar_init(bar_free + 8 * b, S::kEpilogueWarps);
         }
         ptx::mbar_init(bar_drain, 1);
+        ptx::mbar_init(bar_mail, 1);
         ptx::fence_mbarrier_init_cluster();
         ptx::fence_proxy_async_shared();
+        if (ranks > 1 && mine > 0)           // four tokens of 128 rows a store, from every rank
+            ptx::mbar_arrive_expect_tx(bar_mail, ranks * ((mine + 3) / 4) * kTileN * 16);
     }
     if (warp == 1) {
         ptx::tmem_alloc(slot, S::kTmem);
@@ -153,8 +213,10 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD>::kThreads)
     __syncthreads();
     ptx::tcgen05_fence_after_thread_sync();
     const uint32_t tmem = ptx::ld_volatile_shared(slot);
+    if (ranks > 1 && p.apart)                // the others wait for this before they send
+        ptx::cluster_arrive_release();
 
-    float acc[S::kColumns] = {};
+    uint64_t acc[S::kColumns / 2] = {};      // pairs of tokens
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity, uint32_t err) {
         if (!wait_short(bar, parity)) {
@@ -163,92 +225,149 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD>::kThreads)
         }
         ok = __all_sync(0xffffffffu, ok);
     };
+    // One of the two operands' blocks of a stage.
+    auto load = [&](const CUtensorMap *map, uint32_t to, uint32_t block_bytes, int row, int stage, uint32_t bar, uint64_t policy) {
+        const int n = p.planes ? p.per_stage : min(p.per_stage, p.blocks - stage * p.per_stage);
+        ptx::mbar_arrive_expect_tx(bar, n * block_bytes);
+        if (p.planes) {
+            ptx::tma_load_3d(to, map, 0, row, stage * p.per_stage, bar, policy);
+        } else {
+            for (int b = 0; b < n; ++b)
+                ptx::tma_load_2d(to + b * block_bytes, map, (stage * p.per_stage + b) * kBlock, row, bar, policy);
+        }
+    };
     if (warp == 0) {
-        // ------------------------------------------------------------ loads
-        const uint64_t first = ptx::policy_evict_first(), last = ptx::policy_evict_last();
-        auto load = [&](const CUtensorMap *map, uint32_t to, uint32_t block_bytes, int row, int stage, uint32_t bar, uint64_t policy) {
-            if (p.planes) {
-                ptx::tma_load_3d(to, map, 0, row, stage * p.per_stage, bar, policy);
-            } else {
-                for (int b = 0; b < p.per_stage && stage * p.per_stage + b < p.blocks; ++b)
-                    ptx::tma_load_2d(to + b * block_bytes, map, (stage * p.per_stage + b) * kBlock, row, bar, policy);
-            }
-        };
-        auto expect = [&](int stage, uint32_t bar) {
-            const int n = p.planes ? p.per_stage : min(p.per_stage, p.blocks - stage * p.per_stage);
-            ptx::mbar_arrive_expect_tx(bar, n * (S::kWBytes + S::kABytes));
-        };
-        // What does not depend on the kernel before this one: with the caller's promise W of the first ring.
+        // ------------------------------------------------------------ W
+        const uint64_t policy = ptx::policy_evict_first();
+        // With the caller's promise the first ring does not wait for the kernel before this one.
         const int early = p.flags & LOWM_FLAG_W_BEFORE_PDL_WAIT ? min(p.stages, end - begin) : 0;
         if (lane == 0) {
             ptx::prefetch_tensormap(&map_w);
-            ptx::prefetch_tensormap(&map_a);
-            for (int i = 0; i < early; ++i) {
-                expect(begin + i, bar_full + 8 * i);
-                load(&map_w, sbase + i * stage_bytes, S::kWBytes, n0, begin + i, bar_full + 8 * i, first);
-            }
+            for (int i = 0; i < early; ++i)
+                load(&map_w, ring + i * stage_bytes, S::kWBytes, n0, begin + i, bar_full + 8 * i, policy);
+            // Without it the ring's W is requested into L2, where a later write would find it.
+            for (int i = early; i < min(p.stages, end - begin) && p.planes; ++i)
+                ptx::tma_prefetch_3d(&map_w, 0, n0, (begin + i) * p.per_stage);
         }
         ptx::griddep_wait();
-        int i = 0;
-        for (; begin + i < end; ++i) {
-            const int s = i % p.stages;
-            wait(bar_empty + 8 * s, ((i / p.stages) & 1) ^ 1, kErrGemm8Ring);
+        RingPlace r;
+        int i = begin;
+        for (; i < end; ++i, r.step(p.stages)) {
+            if (i - begin < early)
+                continue;
+            wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
             if (!ok)
                 break;
-            if (lane == 0) {
-                const uint32_t bar = bar_full + 8 * s, to = sbase + s * stage_bytes;
-                if (i >= early) {
-                    expect(begin + i, bar);
-                    load(&map_w, to, S::kWBytes, n0, begin + i, bar, first);
-                }
-                load(&map_a, to + a_at, S::kABytes, 0, begin + i, bar, last);
-            }
+            if (lane == 0)
+                load(&map_w, ring + r.at * stage_bytes, S::kWBytes, n0, i, bar_full + 8 * r.at, policy);
             __syncwarp();
-            for (int b = 0; b < p.per_stage; ++b) {
-                const int block = (begin + i) * p.per_stage + b;
-                const uint32_t to = sbase + scales_at + s * scale_stage + b * S::kScaleBytes;
-                if (block >= p.blocks)
-                    break;
-                for (int m = lane; m < M_PAD; m += 32)
-                    copy_async_4(to + 4 * m, p.a_scale + (int64_t)min(m, p.M - 1) * p.blocks + block, m < p.M ? 4 : 0);
-                if (lane == 0)
-                    copy_async_4(to + 4 * M_PAD, p.w_scale + (int64_t)(n0 / kTileN) * p.blocks + block, 4);
-            }
-            copies_arrive(bar_full + 8 * s);
         }
         ptx::griddep_launch_dependents();
-        // No copy may land after the ring has become the mailbox: normally all were consumed.
-        for (int j = max(i - p.stages, 0); j < i; ++j)
-            (void)wait_short(bar_full + 8 * (j % p.stages), (j / p.stages) & 1);
-        if (!ok && i < early)                // W that was requested before a wait gave up: its barrier stays open
-            (void)wait_short(bar_full + 8 * i, 0);
+    } else if (warp >= S::kLoadWarp) {
+        // ------------------------------------------------------------ A and the scales
+        RingPlace r, q;                      // of the ring, of the scales
+        const float *w_scale = p.w_scale + (int64_t)(n0 / kTileN) * p.blocks + begin * p.per_stage;
+        int left = min(p.blocks - begin * p.per_stage, (end - begin) * p.per_stage);            // K blocks
+        if constexpr (QUANT) {
+            const int row0 = 4 * (warp - S::kLoadWarp);
+            ptx::griddep_wait();
+            FourRows x;
+            int column = begin * p.per_stage * kBlock + 4 * lane;
+            float w = 0.f;
+            if (left > 0) {
+                x.load(p, row0, column);
+                w = *w_scale++;
+            }
+            for (int i = begin; i < end; ++i, r.step(p.stages), q.step(scale_slots)) {
+                wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
+                if (!ok)
+                    break;
+                uint8_t *block = smem + kRingAt + r.at * stage_bytes + a_at;
+                float *scales = reinterpret_cast<float *>(smem + scales_at + q.at * scale_stage);
+                for (int b = 0; b < p.per_stage && left > 0; ++b, block += S::kABytes, scales += M_PAD) {
+                    const FourRows now = x;
+                    const float scale = w;
+                    column += kBlock;
+                    if (--left > 0) {        // the next block's
+                        x.load(p, row0, column);
+                        w = *w_scale++;
+                    }
+                    now.store(block, scales, row0, scale);
+                }
+                ptx::fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(bar_full + 8 * r.at);
+                    ptx::mbar_arrive(bar_scales + 8 * q.at);
+                }
+            }
+        } else {
+            const uint64_t policy = ptx::policy_evict_last();
+            if (lane == 0)
+                ptx::prefetch_tensormap(&map_a);
+            ptx::griddep_wait();
+            // This lane's tokens' scales (a token past the last counts 0).
+            constexpr int kEach = (M_PAD + 31) / 32;
+            const float *a_scale[kEach];
+            float next[kEach], w = 0.f;      // the next block's
+            auto fetch = [&]() {
+#pragma unroll
+                for (int k = 0; k < kEach; ++k)
+                    next[k] = lane + 32 * k < p.M ? *a_scale[k]++ : 0.f;
+                w = *w_scale++;
+            };
+#pragma unroll
+            for (int k = 0; k < kEach; ++k)
+                a_scale[k] = p.a_scale + (int64_t)min(lane + 32 * k, p.M - 1) * p.blocks + begin * p.per_stage;
+            if (left > 0)
+                fetch();
+            for (int i = begin; i < end; ++i, r.step(p.stages), q.step(scale_slots)) {
+                const uint32_t bar = bar_full + 8 * r.at;
+                wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
+                if (!ok)
+                    break;
+                if (lane == 0)
+                    load(&map_a, ring + r.at * stage_bytes + a_at, S::kABytes, 0, i, bar, policy);
+                __syncwarp();
+                float *scales = reinterpret_cast<float *>(smem + scales_at + q.at * scale_stage);
+                for (int b = 0; b < p.per_stage && left > 0; ++b, scales += M_PAD) {
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k)
+                        if (lane + 32 * k < M_PAD)
+                            scales[lane + 32 * k] = next[k] * w;
+                    if (--left > 0)
+                        fetch();
+                }
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(bar_scales + 8 * q.at);
+            }
+        }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t kIdesc = make_idesc_e4m3(kTileN, M_PAD);
         const uint32_t base = uniform(tmem);
-        int g = 0;                           // K blocks
-        for (int i = 0; begin + i < end && ok; ++i) {
-            const int s = i % p.stages;
-            wait(bar_full + 8 * s, (i / p.stages) & 1, kErrGemm8Full);
-            const int n = min(p.per_stage, p.blocks - (begin + i) * p.per_stage);
-            for (int b = 0; b < n && ok; ++b, ++g) {
-                const uint32_t buffer = g % S::kBuffers;
-                wait(bar_free + 8 * buffer, ((g / S::kBuffers) & 1) ^ 1, kErrGemm8Free);
-                if (!ok)
-                    break;
-                ptx::tcgen05_fence_after_thread_sync();
-                const uint64_t w = make_sw128_kmajor_desc(sbase + s * stage_bytes + b * S::kWBytes);
-                const uint64_t a = make_sw128_kmajor_desc(sbase + s * stage_bytes + a_at + b * S::kABytes);
-                if (ptx::elect_one_sync()) {
+        RingPlace r, d;                      // of the ring, of the buffers
+        for (int i = begin; i < end && ok; ++i, r.step(p.stages), d.step(buffers)) {
+            wait(bar_full + 8 * r.at, r.phase, kErrGemm8Full);
+            const int n = min(p.per_stage, p.blocks - i * p.per_stage);
+            wait(bar_free + 8 * d.at, d.phase ^ 1, kErrGemm8Free);
+            if (!ok)
+                break;
+            ptx::tcgen05_fence_after_thread_sync();
+            uint64_t w = make_sw128_kmajor_desc(ring + r.at * stage_bytes);
+            uint64_t a = make_sw128_kmajor_desc(ring + r.at * stage_bytes + a_at);
+            uint32_t to = base + d.at * p.per_stage * M_PAD;
+            if (ptx::elect_one_sync()) {
+                for (int b = 0; b < n; ++b, w += S::kWBytes / 16, a += S::kABytes / 16, to += M_PAD) {
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
-                        mma_e4m3_ss(base + buffer * M_PAD, w + 2 * k, a + 2 * k, kIdesc, k > 0);
-                    ptx::tcgen05_commit(bar_sums + 8 * buffer);
-                    if (b + 1 == n)
-                        ptx::tcgen05_commit(bar_empty + 8 * s);
+                        mma_e4m3_ss(to, w + 2 * k, a + 2 * k, kIdesc, k > 0);
                 }
-                __syncwarp();
+                ptx::tcgen05_commit(bar_sums + 8 * d.at);
+                ptx::tcgen05_commit(bar_empty + 8 * r.at);
             }
+            __syncwarp();
         }
         if (ptx::elect_one_sync())
             ptx::tcgen05_commit(bar_drain);
@@ -256,83 +375,131 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD>::kThreads)
         (void)wait_short(bar_drain, 0);      // nothing writes TMEM any more
     } else {
         // ------------------------------------------------------------ sums: thread = row of W = TMEM lane
-        const int quarter = warp & 3, column0 = (warp - 2) / 4 * S::kColumns;
-        const uint32_t from = tmem + ((uint32_t)(32 * quarter) << 16) + column0;
-        int g = 0;
-        for (int i = 0; begin + i < end && ok; ++i) {
-            const int s = i % p.stages;
-            wait(bar_full + 8 * s, (i / p.stages) & 1, kErrGemm8Full);    // the scales
-            const int n = min(p.per_stage, p.blocks - (begin + i) * p.per_stage);
-            for (int b = 0; b < n && ok; ++b, ++g) {
-                const uint32_t buffer = g % S::kBuffers;
-                wait(bar_sums + 8 * buffer, (g / S::kBuffers) & 1, kErrGemm8Sums);
-                if (!ok)
-                    break;
-                ptx::tcgen05_fence_after_thread_sync();
-                const float *scales = reinterpret_cast<const float *>(smem + scales_at + s * scale_stage + b * S::kScaleBytes);
-                const float w = scales[M_PAD];
-                uint32_t d[S::kColumns / 16][16];
+        const int column0 = (warp - 2) / 4 * S::kColumns;
+        const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + column0;
+        // 16 tokens at a time, the next ones on their way while these are multiplied (the last ones of a block: the next
+        // block's first).
+        RingPlace q, d;                      // of the scales, of the buffers
+        uint32_t v[2][16];
+        const float *last = nullptr;         // scales of the block before
+        auto multiply = [&](const uint32_t (&x)[16], const float *scales, int c0) {
 #pragma unroll
-                for (int c = 0; c < S::kColumns / 16; ++c)
-                    tmem_ld_x16(from + buffer * M_PAD + 16 * c, d[c]);
-                ptx::tmem_wait_ld();
-                ptx::tcgen05_fence_before_thread_sync();
-                __syncwarp();
-                if (lane == 0)
-                    ptx::mbar_arrive(bar_free + 8 * buffer);
-#pragma unroll
-                for (int c = 0; c < S::kColumns; c += 4) {
-                    const float4 a = *reinterpret_cast<const float4 *>(scales + column0 + c);
-                    acc[c] = fmaf(__uint_as_float(d[c / 16][c % 16]), a.x * w, acc[c]);
-                    acc[c + 1] = fmaf(__uint_as_float(d[c / 16][c % 16 + 1]), a.y * w, acc[c + 1]);
-                    acc[c + 2] = fmaf(__uint_as_float(d[c / 16][c % 16 + 2]), a.z * w, acc[c + 2]);
-                    acc[c + 3] = fmaf(__uint_as_float(d[c / 16][c % 16 + 3]), a.w * w, acc[c + 3]);
-                }
+            for (int c = 0; c < 16; c += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(scales + column0 + c0 + c);
+                uint64_t *to = acc + (c0 + c) / 2;
+                to[0] = fma2(pack2(x[c], x[c + 1]), pack2(a.x, a.y), to[0]);
+                to[1] = fma2(pack2(x[c + 2], x[c + 3]), pack2(a.z, a.w), to[1]);
             }
+        };
+        auto give_back = [&](uint32_t bar) {
             __syncwarp();
             if (lane == 0)
-                ptx::mbar_arrive(bar_empty + 8 * s);
+                ptx::mbar_arrive(bar);
+        };
+        for (int i = begin; i < end && ok; ++i, q.step(scale_slots), d.step(buffers)) {
+            wait(bar_sums + 8 * d.at, d.phase, kErrGemm8Sums);
+            if (ok)
+                wait(bar_scales + 8 * q.at, q.phase, kErrGemm8Full);
+            if (!ok)
+                break;
+            ptx::tcgen05_fence_after_thread_sync();
+            const int n = min(p.per_stage, p.blocks - i * p.per_stage);
+            const float *scales = reinterpret_cast<const float *>(smem + scales_at + q.at * scale_stage);
+            uint32_t at = from + d.at * p.per_stage * M_PAD;
+            for (int b = 0; b < n; ++b, scales += M_PAD, at += M_PAD) {
+#pragma unroll
+                for (int c = 0; c < S::kColumns; c += 16) {
+                    tmem_ld_x16(at + c, v[c / 16 & 1]);
+                    if (S::kColumns > 16) {
+                        if (c > 0)
+                            multiply(v[~(c / 16) & 1], scales, c - 16);
+                        else if (last)
+                            multiply(v[1], last, S::kColumns - 16);
+                    }
+                    if (c + 16 < S::kColumns)
+                        ptx::tmem_wait_ld();
+                }
+                last = scales;
+                ptx::tmem_wait_ld();
+                if (b + 1 == n) {
+                    ptx::tcgen05_fence_before_thread_sync();
+                    give_back(bar_free + 8 * d.at);
+                }
+                if constexpr (S::kColumns == 16)
+                    multiply(v[0], scales, 0);
+            }
         }
+        if (S::kColumns > 16 && last && ok)
+            multiply(v[1], last, S::kColumns - 16);
     }
     __syncwarp();
     ptx::tcgen05_fence_before_thread_sync();
-    __syncthreads();                         // every MMA has been read, every copy has landed
+    if (!__syncthreads_and(ok)) {
+        // A wait gave up (reported): no copy may land after the CTA has ended, nor in the mailbox.  Whatever is still
+        // under way has landed long before this gives up, too.
+        (void)wait_short(bar_drain, 1);
+    }
+    // Every sum has been read, every copy has landed.
     if (warp == 1) {
         ptx::tcgen05_fence_after_thread_sync();
         ptx::tmem_dealloc(tmem, S::kTmem);
     }
-    const int quarter = warp & 3, column0 = (warp - 2) / 4 * S::kColumns;
-    const int row = 32 * quarter + lane;
+    const int column0 = (warp - 2) / 4 * S::kColumns;
+    const int row = 32 * (warp & 3) + lane;
+    const bool sums = warp >= 2 && warp < S::kLoadWarp;
     if (ranks == 1) {
-        if (warp >= 2 && n0 + row < p.N) {
+        if (sums && n0 + row < p.N) {
 #pragma unroll
             for (int c = 0; c < S::kColumns; ++c)
-                if (column0 + c < p.M)
-                    p.c[(int64_t)(column0 + c) * p.N + n0 + row] = __float2bfloat16_rn(acc[c]);
+                if (column0 + c < p.M) {
+                    const float2 x = unpack2(acc[c / 2]);
+                    p.c[(int64_t)(column0 + c) * p.N + n0 + row] = __float2bfloat16_rn(c & 1 ? x.y : x.x);
+                }
         }
         return;
     }
-    // Rank q's mailbox: [source rank][its tokens][128 rows].
-    const int tokens = M_PAD / ranks;
-    ptx::cluster_arrive_release();
+    // Rank q's mailbox: [source rank][128 rows][its tokens], four tokens at a place that depends on the row, so that
+    // neighbouring rows' are on different banks.  Each rank's barrier counts the bytes that it waits for.
+    if (!p.apart)
+        ptx::cluster_arrive_release();
     ptx::cluster_wait_acquire();
-    if (warp >= 2) {
+    const int groups = tokens / 4;
+    auto place = [&](int source, int group) { return ((source * kTileN + row) * groups + (group ^ (row & (groups - 1)))) * 16; };
+    if (sums) {
 #pragma unroll
-        for (int c = 0; c < S::kColumns; ++c) {
-            const int m = column0 + c, to = m / tokens;
-            if (m < p.M)
-                st_cluster(ptx::mapa_shared(sbase + ((rank * tokens + m - to * tokens) * kTileN + row) * 4, to), acc[c]);
+        for (int c = 0; c < S::kColumns; c += 4) {
+            const int m = column0 + c, to = m / tokens, group = (m - to * tokens) / 4;
+            if (m >= p.M)
+                continue;
+            const float2 x = unpack2(acc[c / 2]), y = unpack2(acc[c / 2 + 1]);
+            ptx::st_async_v4(ptx::mapa_shared(sbase + p.mailbox + place(rank, group), to), ptx::mapa_shared(bar_mail, to), x.x, x.y, y.x,
+                             y.y);
         }
-    }
-    ptx::cluster_arrive_release();
-    ptx::cluster_wait_acquire();
-    if (warp >= 2 && n0 + row < p.N) {
-        for (int m = (warp - 2) / 4; m < tokens && rank * tokens + m < p.M; m += S::kEpilogueWarps / 4) {
-            float sum = 0.f;
-            for (int r = 0; r < ranks; ++r)
-                sum += reinterpret_cast<const float *>(smem)[(r * tokens + m) * kTileN + row];
-            p.c[(int64_t)(rank * tokens + m) * p.N + n0 + row] = __float2bfloat16_rn(sum);
-        }
+        if (mine == 0)
+            return;
+        const uint64_t t0 = ptx::globaltimer();
+        while (!ptx::mbar_try_wait_relaxed_cluster(bar_mail, 0))
+            if (ptx::globaltimer() - t0 > kDefaultTimeoutNs) {
+                atomicOr(p.status, kErrGemm8Mail);
+                return;
+            }
+        ptx::fence_acquire_shared_cluster();
+        if (n0 + row < p.N)
+            for (int group = (warp - 2) / 4; 4 * group < mine; group += S::kEpilogueWarps / 4) {
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int r = 0; r < ranks; ++r) {
+                    const float4 x = *reinterpret_cast<const float4 *>(smem + p.mailbox + place(r, group));
+                    sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+                }
+                __nv_bfloat16 *c = p.c + (int64_t)(rank * tokens + 4 * group) * p.N + n0 + row;
+                c[0] = __float2bfloat16_rn(sum.x);
+                if (4 * group + 1 < mine)
+                    c[p.N] = __float2bfloat16_rn(sum.y);
+                if (4 * group + 2 < mine)
+                    c[2 * (int64_t)p.N] = __float2bfloat16_rn(sum.z);
+                if (4 * group + 3 < mine)
+                    c[3 * (int64_t)p.N] = __float2bfloat16_rn(sum.w);
+            }
     }
 }
 
@@ -447,40 +614,45 @@ lowm_status_t encode_matrix(const void *base, int rows, int K, int box_rows, int
 
 constexpr int kSmem = 227 * 1024;
 
-template <int M_PAD>
-lowm_status_t launch_gemm_fp8(const void *A, const void *W, Gemm8Params &p, int K, int sms, void *stream)
+template <int M_PAD, bool QUANT>
+lowm_status_t launch_gemm_fp8(const void *A, const void *W, Gemm8Params &p, int sms, void *stream)
 {
-    using S = Gemm8Shape<M_PAD>;
+    using S = Gemm8Shape<M_PAD, QUANT>;
     const int tiles = (p.N + kTileN - 1) / kTileN;
+    // Ranks along K as long as the CTAs find an SM, or, with up to 16 tokens, half of one (us at N 6144, K 4096, split 1, 2, 4:
+    // 4 tokens 10.1, 7.4, 6.6; 32 tokens 11.9, 9.3, 9.7; 64 tokens 13.4, 11.4, 18.7; 128 tokens 18.5, 15.6, 26.5).
     int split = 1;
-    while (split < kMaxSplit && tiles * split * 2 <= 2 * sms && p.blocks >= 4 * split)
+    while (split < std::min(M_PAD / 4, kMaxSplit) && tiles * split * 2 <= (M_PAD <= 16 ? 2 : 1) * sms && p.blocks >= 4 * split)
         split *= 2;
-    if (const char *e = getenv("LOWM8_SPLIT"))
-        split = atoi(e);
-    const bool two = tiles * split > sms;                                // CTAs an SM
-    const int share = (p.blocks + split - 1) / split;
-    p.per_stage = 1;
-    if (const char *e = getenv("LOWM8_KB"))
-        p.per_stage = atoi(e);
-    const int overhead = 1024;                                           // barriers
-    const int budget = two ? kSmem / 2 - 1024 : kSmem;
-    auto bytes_of = [](int blocks) { return (int)S::stage_bytes(blocks) + blocks * (int)S::kScaleBytes; };
-    while (p.per_stage > 1 && 2 * bytes_of(p.per_stage) > budget - overhead)
+    // Two CTAs an SM hide each other's ends (4 tokens, N 49152: 37.7 -> 36.2 us); more tokens take an SM's registers.
+    const bool two = M_PAD <= 32 && tiles * split > sms;
+    // A copy costs much the same whatever its size (K blocks a copy 1, 2: 4 tokens, N 49152 48.1, 37.7 us).
+    p.per_stage = 2;
+    const int mailbox = split > 1 ? M_PAD * kTileN * 4 : 0;
+    p.apart = M_PAD <= 32;                                               // else the mailbox is the drained ring
+    const int budget = (two ? kSmem / 2 - 1024 : kSmem) - (int)kRingAt - (p.apart ? mailbox : 0) - 64 - (kBuffers + 4) * (int)S::kScaleBytes;
+    // (the scales' extra slots: those of kBuffers + 1 blocks at most)
+    const int extra = (kBuffers + p.per_stage) * (int)S::kScaleBytes;
+    auto bytes_of = [](int blocks) { return blocks * (int)(S::kWBytes + S::kABytes + S::kScaleBytes); };
+    while (p.per_stage > 1 && (2 * bytes_of(p.per_stage) > budget || p.blocks < p.per_stage * split))
         p.per_stage /= 2;
-    const int stage = bytes_of(p.per_stage);
-    p.stages = std::min({(budget - overhead) / stage, (share + p.per_stage - 1) / p.per_stage, 16});
-    p.planes = K % kBlock == 0;
-    // The ring is the mailbox, too.
-    const int ring = std::max(p.stages * stage, split > 1 ? M_PAD * kTileN * 4 : 0);
-    const int bytes = std::max(ring, p.stages * stage) + overhead;
+    const int stage = bytes_of(p.per_stage), share = ((p.blocks + p.per_stage - 1) / p.per_stage + split - 1) / split;
+    p.stages = std::min({budget / stage, share, (int)kMaxStages});
+    if (p.stages < 1)
+        return LOWM_ERR_UNSUPPORTED_SHAPE;
+    p.planes = p.K % kBlock == 0;
+    const int used = (int)kRingAt + p.stages * stage + extra;            // (a multiple of 16)
+    p.mailbox = p.apart ? used : (int)kRingAt;
+    const int bytes = std::max(used, p.mailbox + mailbox);
     CUtensorMap map_w, map_a;
-    lowm_status_t st = encode_matrix(W, p.N, K, kTileN, p.per_stage, p.planes, &map_w);
-    if (st == LOWM_OK)
-        st = encode_matrix(A, p.M, K, M_PAD, p.per_stage, p.planes, &map_a);
+    lowm_status_t st = encode_matrix(W, p.N, p.K, kTileN, p.per_stage, p.planes, &map_w);
     if (st != LOWM_OK)
         return st;
+    map_a = map_w;                                                       // (not read)
+    if (!QUANT && (st = encode_matrix(A, p.M, p.K, M_PAD, p.per_stage, p.planes, &map_a)) != LOWM_OK)
+        return st;
     static SmemOptIn opt_in;
-    if (!opt_in.set(reinterpret_cast<const void *>(gemm_fp8_kernel<M_PAD>), kSmem))
+    if (!opt_in.set(reinterpret_cast<const void *>(gemm_fp8_kernel<M_PAD, QUANT>), kSmem))
         return LOWM_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
@@ -496,8 +668,44 @@ lowm_status_t launch_gemm_fp8(const void *A, const void *W, Gemm8Params &p, int 
     attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<M_PAD>, map_w, map_a, p) == cudaSuccess ? LOWM_OK : LOWM_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<M_PAD, QUANT>, map_w, map_a, p) == cudaSuccess ? LOWM_OK : LOWM_ERR_CUDA;
 }
+
+// The checks that both forms share, and what they fill in.
+lowm_status_t prepare_gemm(const void *A, const void *W, const float *w_scale, void *C, int M, int N, int K, unsigned flags,
+                           Gemm8Params &p, int &sms)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || (flags & ~(unsigned)LOWM_FLAG_W_BEFORE_PDL_WAIT))
+        return LOWM_ERR_INVALID_ARGUMENT;
+    if (M > 128 || K % 16 || N > (1 << 30))
+        return LOWM_ERR_UNSUPPORTED_SHAPE;
+    if (!A || !W || !w_scale || !C)
+        return LOWM_ERR_INVALID_ARGUMENT;
+    if (!is_aligned(W, 16) || !is_aligned(C, 2) || !is_aligned(w_scale, 4))
+        return LOWM_ERR_MISALIGNED;
+    std::memset(&p, 0, sizeof p);
+    p.w_scale = w_scale;
+    p.c = static_cast<__nv_bfloat16 *>(C);
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.blocks = (K + kBlock - 1) / kBlock;
+    p.flags = flags;
+    return LOWM_OK;
+}
+
+lowm_status_t launch_codes(const void *A, const void *W, Gemm8Params &p, int sms, void *stream)
+{
+    return p.M <= 16   ? launch_gemm_fp8<16, false>(A, W, p, sms, stream)
+           : p.M <= 32 ? launch_gemm_fp8<32, false>(A, W, p, sms, stream)
+           : p.M <= 64 ? launch_gemm_fp8<64, false>(A, W, p, sms, stream)
+                       : launch_gemm_fp8<128, false>(A, W, p, sms, stream);
+}
+
+// Up to 16 tokens are quantised by the GEMM itself, a CTA its share of them; more by a kernel before it.
+constexpr int kQuantTokens = 16;
+
+size_t code_bytes(int M, int K) { return ((size_t)M * K + 15) / 16 * 16; }
 
 }  // namespace
 }  // namespace lowm
@@ -532,32 +740,60 @@ extern "C" lowm_status_t lowm_gemm_fp8(const void *A, const float *a_scale, cons
                                        int N, int K, unsigned flags, void *stream)
 {
     using namespace lowm;
-    if (M <= 0 || N <= 0 || K <= 0 || (flags & ~(unsigned)LOWM_FLAG_W_BEFORE_PDL_WAIT))
-        return LOWM_ERR_INVALID_ARGUMENT;
-    if (M > 128 || K % 16 || N > (1 << 30))
-        return LOWM_ERR_UNSUPPORTED_SHAPE;
-    if (!A || !a_scale || !W || !w_scale || !C)
-        return LOWM_ERR_INVALID_ARGUMENT;
-    if (!is_aligned(A, 16) || !is_aligned(W, 16) || !is_aligned(C, 2) || !is_aligned(a_scale, 4) || !is_aligned(w_scale, 4))
-        return LOWM_ERR_MISALIGNED;
+    Gemm8Params p;
     int sms = 0;
-    const lowm_status_t st = host_check_device(&sms);
+    lowm_status_t st = prepare_gemm(A, W, w_scale, C, M, N, K, flags, p, sms);
     if (st != LOWM_OK)
         return st;
-    Gemm8Params p;
-    std::memset(&p, 0, sizeof p);
+    if (!a_scale)
+        return LOWM_ERR_INVALID_ARGUMENT;
+    if (!is_aligned(A, 16) || !is_aligned(a_scale, 4))
+        return LOWM_ERR_MISALIGNED;
+    if ((st = host_check_device(&sms)) != LOWM_OK)
+        return st;
     p.a_scale = a_scale;
-    p.w_scale = w_scale;
-    p.c = static_cast<__nv_bfloat16 *>(C);
-    p.M = M;
-    p.N = N;
-    p.blocks = (K + kBlock - 1) / kBlock;
-    p.flags = flags;
+    p.status = host_status_word();
+    return p.status ? launch_codes(A, W, p, sms, stream) : LOWM_ERR_CUDA;
+}
+
+extern "C" size_t lowm_gemm_fp8_bf16_workspace(int M, int K)
+{
+    using namespace lowm;
+    if (M <= 0 || M > 128 || K <= 0 || K % 16)
+        return 0;
+    return M <= kQuantTokens ? 16 : code_bytes(M, K) + (size_t)M * ((K + kBlock - 1) / kBlock) * sizeof(float);
+}
+
+extern "C" lowm_status_t lowm_gemm_fp8_bf16(const void *x, int64_t x_stride, const void *W, const float *w_scale, void *C, int M,
+                                            int N, int K, unsigned flags, void *workspace, size_t workspace_bytes, void *stream)
+{
+    using namespace lowm;
+    Gemm8Params p;
+    int sms = 0;
+    lowm_status_t st = prepare_gemm(x, W, w_scale, C, M, N, K, flags, p, sms);
+    if (st != LOWM_OK)
+        return st;
+    if (x_stride < 0 || !workspace || workspace_bytes < lowm_gemm_fp8_bf16_workspace(M, K))
+        return LOWM_ERR_INVALID_ARGUMENT;
+    if (!is_aligned(x, 2) || !is_aligned(workspace, 16))
+        return LOWM_ERR_MISALIGNED;
+    if ((st = host_check_device(&sms)) != LOWM_OK)
+        return st;
     p.status = host_status_word();
     if (!p.status)
         return LOWM_ERR_CUDA;
-    return M <= 16   ? launch_gemm_fp8<16>(A, W, p, K, sms, stream)
-           : M <= 32 ? launch_gemm_fp8<32>(A, W, p, K, sms, stream)
-           : M <= 64 ? launch_gemm_fp8<64>(A, W, p, K, sms, stream)
-                     : launch_gemm_fp8<128>(A, W, p, K, sms, stream);
+    if (M <= kQuantTokens) {
+        p.x = static_cast<const __nv_bfloat16 *>(x);
+        p.x_stride = x_stride;
+        p.x_vec = is_aligned(x, 8) && x_stride % 4 == 0;
+        return launch_gemm_fp8<16, true>(nullptr, W, p, sms, stream);
+    }
+    float *scales = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + code_bytes(M, K));
+    st = lowm_quantize_fp8(x, x_stride, workspace, scales, M, K, 1, stream);
+    if (st != LOWM_OK)
+        return st;
+    // The quantisation does not write W, and it begins only after what came before it has ended.
+    p.a_scale = scales;
+    p.flags |= LOWM_FLAG_W_BEFORE_PDL_WAIT;
+    return launch_codes(workspace, W, p, sms, stream);
 }

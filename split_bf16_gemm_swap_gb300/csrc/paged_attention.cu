@@ -102,47 +102,11 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Two fp32 values in one register pair: one instruction for both.
-__device__ __forceinline__ uint64_t pack2(float x, float y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y)
-{
-    return pack2(__uint_as_float(x), __uint_as_float(y));
-}
-
-__device__ __forceinline__ float2 unpack2(uint64_t v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 __device__ __forceinline__ void times2(uint32_t &x, uint32_t &y, float a, float b)
 {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(x, y)), "l"(pack2(a, b)));
-    const float2 v = unpack2(r);
+    const float2 v = unpack2(mul2(pack2(x, y), pack2(a, b)));
     x = __float_as_uint(v.x);
     y = __float_as_uint(v.y);
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar)

@@ -15,12 +15,14 @@ import torch
 
 from . import layer
 from .layer import _cuda, _current_device, _current_stream, _dense, _f, _i, _l, _launch, _on, _p, _row_stride, _rows, _z, function
-from .lowm import LOWM_OK, LowmError, LOWM_FLAG_W_BEFORE_PDL_WAIT
+from .lowm import LOWM_OK, LowmError
 
 # Exported C functions, in header order.
 ABI_FUNCTIONS = (
     "lowm_quantize_fp8",
     "lowm_gemm_fp8",
+    "lowm_gemm_fp8_bf16",
+    "lowm_gemm_fp8_bf16_workspace",
     "lowm_rope_append_fp8",
     "lowm_paged_attention_fp8",
     "lowm_paged_attention_fp8_workspace",
@@ -30,6 +32,8 @@ _cache = [_p, _l, _l, _l]                  # a pointer and three strides
 layer._ARGTYPES.update({
     "lowm_quantize_fp8": [_p, _l, _p, _p, _i, _i, _i, _p],
     "lowm_gemm_fp8": [_p, _p, _p, _p, _p, _i, _i, _i, _i, _p],
+    "lowm_gemm_fp8_bf16": [_p, _l, _p, _p, _p, _i, _i, _i, _i, _p, _z, _p],
+    "lowm_gemm_fp8_bf16_workspace": [_i, _i],
     "lowm_rope_append_fp8": [_p, _l, _l, _p, _l, _l, _p, _l, _l, _p, _l, _p, _l, _i, _i, _i, _i, _p, _p, _l, _l,
                              *_cache, *_cache, *_cache, *_cache, _l, _i, _i, _i, _i, _i, _i, _i, _p],
     "lowm_paged_attention_fp8": [_p, _l, _l, *_cache, *_cache, *_cache, *_cache, _l, _i, _i, _p, _l, _i, _p, _p, _p, _l, _l,
@@ -49,6 +53,14 @@ def lowm_gemm_fp8(*args) -> int:
     return function("lowm_gemm_fp8")(*args)
 
 
+def lowm_gemm_fp8_bf16(*args) -> int:
+    return function("lowm_gemm_fp8_bf16")(*args)
+
+
+def lowm_gemm_fp8_bf16_workspace(M: int, K: int) -> int:
+    return function("lowm_gemm_fp8_bf16_workspace")(M, K)
+
+
 def lowm_rope_append_fp8(*args) -> int:
     return function("lowm_rope_append_fp8")(*args)
 
@@ -62,6 +74,7 @@ def lowm_paged_attention_fp8_workspace(batch: int, q_tokens: int, heads: int, kv
     return function("lowm_paged_attention_fp8_workspace")(batch, q_tokens, heads, kv_heads, dim, page_size, table_width)
 
 
+_gemm_bytes = functools.lru_cache(maxsize=4096)(lowm_gemm_fp8_bf16_workspace)
 _attention_bytes = functools.lru_cache(maxsize=4096)(lowm_paged_attention_fp8_workspace)
 
 
@@ -138,21 +151,9 @@ def gemm_fp8(A, W, W_scale, A_scale=None, *, out=None, flags: int = 0, stream=No
             raise LowmError(s, "lowm_gemm_fp8")
         return out
     stride = _row_stride(A, "A", torch.bfloat16, shape, device)
-    if K % 16 or not 0 < M <= 128:             # before the first of the two launches
-        raise ValueError("M must be 1 to 128 and K a multiple of 16, not %d and %d" % (M, K))
-    codes = -(-M * K // 16) * 16               # the workspace: codes, then scales
-    _launch("lowm_gemm_fp8", (), codes + 4 * M * blocks, device, _current_stream(device),
-            lambda work, nbytes, stream: _quantized_gemm(A, stride, W, W_scale, out, M, N, K, work, work + codes, flags, stream))
+    _launch("lowm_gemm_fp8_bf16", (A.data_ptr(), stride, W.data_ptr(), W_scale.data_ptr(), out.data_ptr(), M, N, K, flags),
+            _gemm_bytes(M, K), device, _current_stream(device))
     return out
-
-
-def _quantized_gemm(A, stride, W, W_scale, out, M, N, K, codes, scales, flags, stream) -> int:
-    s = function("lowm_quantize_fp8")(A.data_ptr(), stride, codes, scales, M, K, 1, stream)
-    if s != LOWM_OK:
-        return s
-    # The quantisation does not write W, and it begins only after what came before it has ended.
-    return function("lowm_gemm_fp8")(codes, scales, W.data_ptr(), W_scale.data_ptr(), out.data_ptr(), M, N, K,
-                                     flags | LOWM_FLAG_W_BEFORE_PDL_WAIT, stream)
 
 
 def _codes(k_cache, v_cache, k_scale, v_scale, device: int):

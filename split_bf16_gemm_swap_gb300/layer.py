@@ -146,12 +146,9 @@ _kept: dict = {}
 _kept_lock = threading.RLock()
 
 
-def _launch(name: str, args, nbytes: int, device: int, stream: int, call=None) -> None:
-    """Call the library's function `name` with `args`, `nbytes` of scratch memory and `stream`.
-
-    call: what to call instead of it, with the same arguments.
-    """
-    fn = function(name) if call is None else call
+def _launch(name: str, args, nbytes: int, device: int, stream: int) -> None:
+    """Call the library's function `name` with `args`, `nbytes` of scratch memory and `stream`."""
+    fn = function(name)
     if stream:
         own = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
         s = fn(*args, own.data_ptr(), nbytes, stream)

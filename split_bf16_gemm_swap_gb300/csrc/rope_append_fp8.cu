@@ -3,12 +3,11 @@
 // (lowm_fp8.h).
 //
 // A block's scale depends on all of its tokens, so the unit of work is a run: the
-// neighbouring tokens of the call that lie in one block.  A warp has one head of a
-// run, of k or of v, a lane every 32nd pair of a row (or element behind the pairs):
-// it finds the run's largest magnitude, the block's scale, moves the block's older
-// codes to it where it has grown, and writes the new ones.  The rows are turned
-// twice rather than kept: a run may be as long as a page.  q's rows are turned by
-// further warps of the same launch.
+// neighbouring tokens of the call that lie in one block.  For one head of a run, of k
+// or of v, a warp finds the run's largest magnitude, the block's scale, moves the
+// block's older codes to it where it has grown, and writes the new ones.  q's rows are
+// turned by warps of the same launch.  Two kernels: of heads of 64, 128 or 256 elements
+// and 16-byte rows in 16-byte pieces, else element by element.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -34,7 +33,7 @@ struct Rope8Params {
     const float *cos_sin;
     const int64_t *positions, *slots;
     int64_t table_rows, positions_stride, capacity;
-    int page_size, block, axes, section0, section1, interleaved;
+    int page_size, block, block_shift, axes, section0, section1, interleaved;
     int tokens, heads, kv_heads, dim, rotary;
 };
 
@@ -106,18 +105,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_fp8_kernel(const Rop
         const int64_t slot = p.slots[i];
         return slot >= 0 && slot < p.capacity && position_of(p, i).known ? slot : -1;
     };
-    const int64_t slot = slot_of(t), block = slot / p.block;
+    const int64_t slot = slot_of(t), block = slot >> p.block_shift;
     if (slot < 0)
         return;
     if (t > 0) {                             // the token before has the run, if it is part of it
         const int64_t before = slot_of(t - 1);
-        if (before >= 0 && before < slot && before / p.block == block)
+        if (before >= 0 && before < slot && before >> p.block_shift == block)
             return;
     }
     int n = 1;
     for (int64_t last = slot; n < p.block && t + n < p.tokens; ++n) {
         const int64_t next = slot_of(t + n);
-        if (next <= last || next / p.block != block)
+        if (next <= last || next >> p.block_shift != block)
             break;
         last = next;
     }
@@ -126,10 +125,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_fp8_kernel(const Rop
     const __nv_bfloat16 *x = is_k ? p.k + t * p.k_ts + h * p.k_hs : p.v + t * p.v_ts + h * p.v_hs;
     const int64_t step = is_k ? p.k_ts : p.v_ts, place_step = is_k ? p.kc_place : p.vc_place;
     const int64_t page = slot / p.page_size;
-    const int place = (int)(slot - page * p.page_size), first = place / p.block * p.block;
+    const int place = (int)(slot - page * p.page_size), first = place >> p.block_shift << p.block_shift;
     uint8_t *cells = is_k ? p.k_cache + page * p.kc_page + h * p.kc_head : p.v_cache + page * p.vc_page + h * p.vc_head;
-    float *scale = is_k ? p.k_scale + page * p.ks_page + place / p.block * p.ks_block + h * p.ks_head
-                        : p.v_scale + page * p.vs_page + place / p.block * p.vs_block + h * p.vs_head;
+    float *scale = is_k ? p.k_scale + page * p.ks_page + (place >> p.block_shift) * p.ks_block + h * p.ks_head
+                        : p.v_scale + page * p.vs_page + (place >> p.block_shift) * p.vs_block + h * p.vs_head;
 
     float amax = 0.f;
     for (int i = 0; i < n; ++i)
@@ -163,6 +162,364 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_fp8_kernel(const Rop
     __syncwarp();                            // every lane has read the old scale
     if (lane == 0)
         *scale = now;
+}
+
+// ------------------------------------------------------------------ 16-byte pieces
+// A lane has a unit of 16 elements of a token: eight pairs of the rotation, or what lies behind them; DIM / 16 lanes have a
+// token, so a warp has 512 / DIM tokens at a time.  The first CTAs of the grid have k and v: each looks at kTokens tokens of
+// the call and has the runs that begin among them, for some of the heads: of a run of one token (decoding) such a group of
+// lanes has a head, of a longer one a warp.  What they need of the slots and the table comes into shared memory first, all
+// at once (one by one these were chains of latencies).  The other CTAs turn q.  Chunks of 1501 tokens (3751 in all, 32 / 8
+// heads of 128): 34 us with 128 registers a thread; 39 with 80 or 64, which spill; one kind of CTA for all heads, k and v
+// kept in registers for their second use, took 47.
+constexpr int kTokens = 16, kWideWarps = 8, kWideThreads = 32 * kWideWarps;
+constexpr int kWideBlock = 128;              // the longest run
+constexpr int kAngleTokens = 2 * kTokens;    // whose angles are kept
+
+template <int DIM, bool INTERLEAVED>
+struct RopeUnit {
+    static constexpr int kLanes = DIM / 16, kAtOnce = 32 / kLanes;
+    int e0, e1, j0;                          // the unit's two runs of eight elements; its first pair
+    bool turns;
+
+    __device__ RopeUnit(const Rope8Params &p, bool turned)
+    {
+        const int u = threadIdx.x % kLanes, half = p.rotary / 2;
+        turns = turned && 8 * u < half;
+        j0 = 8 * u;
+        e0 = !turned ? 16 * u : (turns ? (INTERLEAVED ? 16 * u : 8 * u) : p.rotary + 2 * (8 * u - half));
+        e1 = turns && !INTERLEAVED ? e0 + half : e0 + 8;
+    }
+
+    // The cosines and sines of token t (of a unit that turns), from the row kept in shared memory or the table.
+    __device__ __forceinline__ void angles(const Rope8Params &p, const float *kept, int64_t t, float (&c)[8], float (&s)[8]) const
+    {
+        const int half = p.rotary / 2;
+        if (kept) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(kept + j0 + i), y = *reinterpret_cast<const float4 *>(kept + half + j0 + i);
+                c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+                s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+            }
+            return;
+        }
+        const Position at = position_of(p, t);
+        const int end1 = p.section0 + p.section1;
+        const int axis0 = j0 < p.section0 ? 0 : (j0 < end1 ? 1 : 2), axis1 = j0 + 7 < p.section0 ? 0 : (j0 + 7 < end1 ? 1 : 2);
+        if (axis0 == axis1 && at.known) {
+            const float *row = (axis0 == 0 ? at.rows[0] : (axis0 == 1 ? at.rows[1] : at.rows[2])) + j0;
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(row + i), y = *reinterpret_cast<const float4 *>(row + half + i);
+                c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+                s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + i;
+            const float *row = j < p.section0 ? at.rows[0] : (j < end1 ? at.rows[1] : at.rows[2]);
+            c[i] = at.known ? row[j] : CUDART_NAN_F;
+            s[i] = at.known ? row[half + j] : CUDART_NAN_F;
+        }
+    }
+
+    __device__ __forceinline__ void load(const __nv_bfloat16 *x, uint4 (&v)[2]) const
+    {
+        v[0] = *reinterpret_cast<const uint4 *>(x + e0);
+        v[1] = *reinterpret_cast<const uint4 *>(x + e1);
+    }
+
+    __device__ __forceinline__ void turn(const uint4 (&v)[2], const float (&c)[8], const float (&s)[8], float (&y)[16]) const
+    {
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            y[2 * i] = __uint_as_float(w[i] << 16);
+            y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+        if (!turns)
+            return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float &a = y[INTERLEAVED ? 2 * i : i], &b = y[INTERLEAVED ? 2 * i + 1 : 8 + i];
+            const float u = a, x = b;
+            a = u * c[i] - x * s[i];
+            b = u * s[i] + x * c[i];
+        }
+    }
+
+    // The largest magnitude as its bits (what is not finite is above the finite ones), and of the finite ones.
+    __device__ __forceinline__ static uint32_t largest(const float (&y)[16])
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+        return m;
+    }
+
+    __device__ __forceinline__ static uint32_t largest_finite(const float (&y)[16])
+    {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            m = fmaxf(m, finite_magnitude(y[i]));
+        return __float_as_uint(m);
+    }
+
+    // Codes y / scale; `plain`: all are finite and the scale is a power of two with this inverse.
+    __device__ __forceinline__ void store(uint8_t *to, const float (&y)[16], float scale, bool plain, float inverse) const
+    {
+        uint32_t w[4] = {};
+        if (plain) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = to_e4m3x2(y[4 * i] * inverse, y[4 * i + 1] * inverse) |
+                       to_e4m3x2(y[4 * i + 2] * inverse, y[4 * i + 3] * inverse) << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i / 4] |= (to_e4m3x2(nan_unless_finite(y[i]) / scale, 0.f) & 0xffu) << (8 * (i & 3));
+        }
+        *reinterpret_cast<uint2 *>(to + e0) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(to + e1) = make_uint2(w[2], w[3]);
+    }
+
+    // Moves the unit's codes of a token to another scale.
+    __device__ __forceinline__ void move(uint8_t *at, float ratio) const
+    {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint2 *c = reinterpret_cast<uint2 *>(at + (half ? e1 : e0));
+            uint2 w = *c;
+            uint32_t out[2] = {w.x, w.y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 lo = __half22float2(e4m3x2_to_half2(out[i] & 0xffffu)), hi = __half22float2(e4m3x2_to_half2(out[i] >> 16));
+                out[i] = to_e4m3x2(lo.x * ratio, lo.y * ratio) | to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16;
+            }
+            *c = make_uint2(out[0], out[1]);
+        }
+    }
+};
+
+// One head of k's or v's cache.
+struct HeadCache {
+    const __nv_bfloat16 *x;
+    uint8_t *cells;
+    float *scales;
+    int64_t step, page, place, s_page, s_block;
+};
+
+__device__ __forceinline__ HeadCache head_cache(const Rope8Params &p, int head)
+{
+    const bool is_k = head < p.kv_heads;
+    const int h = is_k ? head : head - p.kv_heads;
+    HeadCache c;
+    c.x = is_k ? p.k + h * p.k_hs : p.v + h * p.v_hs;
+    c.step = is_k ? p.k_ts : p.v_ts;
+    c.cells = is_k ? p.k_cache + h * p.kc_head : p.v_cache + h * p.vc_head;
+    c.scales = is_k ? p.k_scale + h * p.ks_head : p.v_scale + h * p.vs_head;
+    c.page = is_k ? p.kc_page : p.vc_page;
+    c.place = is_k ? p.kc_place : p.vc_place;
+    c.s_page = is_k ? p.ks_page : p.vs_page;
+    c.s_block = is_k ? p.ks_block : p.vs_block;
+    return c;
+}
+
+// q's rows: `at_once` tokens of the call by as many equal parts of the CTA; a thread has one unit of every so manieth head.
+template <int DIM, bool INTERLEAVED>
+__device__ __forceinline__ void turn_queries(const Rope8Params &p, int64_t cta, int at_once)
+{
+    using Unit = RopeUnit<DIM, INTERLEAVED>;
+    const int part = kWideThreads / at_once, lanes = part / Unit::kLanes;
+    const int64_t t = cta * at_once + threadIdx.x / part;
+    if (t >= p.tokens)
+        return;
+    const Unit unit(p, true);
+    int h = threadIdx.x % part / Unit::kLanes;
+    if (h >= p.heads)
+        return;
+    uint4 next[2];
+    unit.load(p.q + t * p.q_ts + h * p.q_hs, next);
+    float cosines[8], sines[8];
+    if (unit.turns)
+        unit.angles(p, nullptr, t, cosines, sines);
+    for (; h < p.heads; h += lanes) {
+        const uint4 now[2] = {next[0], next[1]};
+        if (h + lanes < p.heads)
+            unit.load(p.q + t * p.q_ts + (h + lanes) * p.q_hs, next);
+        float y[16];
+        unit.turn(now, cosines, sines, y);
+        alignas(16) __nv_bfloat162 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+        __nv_bfloat16 *out = p.q_out + t * p.qo_ts + h * p.qo_hs;
+        *reinterpret_cast<uint4 *>(out + unit.e0) = reinterpret_cast<const uint4 *>(v)[0];
+        *reinterpret_cast<uint4 *>(out + unit.e1) = reinterpret_cast<const uint4 *>(v)[1];
+    }
+}
+
+template <int DIM, bool INTERLEAVED>
+__global__ void __launch_bounds__(kWideThreads, 2)
+    rope_append_fp8_wide_kernel(const Rope8Params p, int windows, int kv_ctas, int at_once)
+{
+    using Unit = RopeUnit<DIM, INTERLEAVED>;
+    constexpr int kLanes = Unit::kLanes, kAtOnce = Unit::kAtOnce;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (blockIdx.x >= kv_ctas) {
+        turn_queries<DIM, INTERLEAVED>(p, blockIdx.x - kv_ctas, at_once);
+        return;
+    }
+    extern __shared__ __align__(16) float angles[];     // [kAngleTokens][rotary]
+    __shared__ int64_t slots[1 + kTokens + kWideBlock]; // from the token before the first on; -1: not appended
+    __shared__ int rows[3][kAngleTokens];    // of the table, by axis; -1: not one of its rows
+    __shared__ int starts[kTokens], lengths[kTokens], counts[2];    // the runs that begin here, those of one token first
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / kLanes;
+    const int64_t t0 = (int64_t)(blockIdx.x % windows) * kTokens;
+    const int column = blockIdx.x / windows, columns = kv_ctas / windows;
+    const int here = (int)min((int64_t)kTokens, p.tokens - t0);
+    const int kept = (int)min((int64_t)min(kAngleTokens, kTokens - 1 + p.block), p.tokens - t0);      // tokens
+    for (int i = threadIdx.x; i < 1 + kTokens + p.block; i += kWideThreads) {
+        const int64_t t = t0 - 1 + i;
+        int64_t slot = -1;
+        if (t >= 0 && t < p.tokens) {
+            int64_t at[3];
+            slot = p.slots[t];
+#pragma unroll
+            for (int a = 0; a < 3; ++a)
+                at[a] = p.positions[a < p.axes ? a * p.positions_stride + t : t];
+            bool known = true;
+#pragma unroll
+            for (int a = 0; a < 3; ++a)
+                known = known && at[a] >= 0 && at[a] < p.table_rows;
+            if (i > 0 && i <= kAngleTokens)
+#pragma unroll
+                for (int a = 0; a < 3; ++a)
+                    rows[a][i - 1] = known ? (int)at[a] : -1;
+            slot = known && slot >= 0 && slot < p.capacity ? slot : -1;
+        }
+        slots[i] = slot;
+    }
+    __syncthreads();
+    const int quads = p.rotary / 4, half = p.rotary / 2;     // four of a row's cosines or sines
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kept * quads; i += kWideThreads) {
+        const int token = i / quads, j = (i - token * quads) * 4, pair = j < half ? j : j - half;
+        auto row_of_pair = [&](int k) {
+            return (int64_t)rows[k < p.section0 ? 0 : (k < p.section0 + p.section1 ? 1 : 2)][token] * p.rotary;
+        };
+        const int64_t row = row_of_pair(pair), last = row_of_pair(pair + 3);
+        float4 x = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
+        if (row >= 0)
+            x = row == last ? *reinterpret_cast<const float4 *>(p.cos_sin + row + j)
+                            : make_float4(p.cos_sin[row + j], p.cos_sin[row_of_pair(pair + 1) + j + 1],
+                                          p.cos_sin[row_of_pair(pair + 2) + j + 2], p.cos_sin[last + j + 3]);
+        *reinterpret_cast<float4 *>(angles + token * p.rotary + j) = x;
+    }
+    __syncthreads();
+    if (warp == 0) {                         // a lane a token
+        int n = 0;
+        if (lane < here) {
+            const int64_t before = slots[lane], slot = slots[1 + lane];
+            if (slot >= 0 && !(before >= 0 && before < slot && before >> p.block_shift == slot >> p.block_shift)) {
+                n = 1;
+                for (int64_t last = slot; n < p.block; ++n) {
+                    const int64_t next = slots[1 + lane + n];
+                    if (next <= last || next >> p.block_shift != slot >> p.block_shift)
+                        break;
+                    last = next;
+                }
+            }
+        }
+        const unsigned single = __ballot_sync(0xffffffffu, n == 1), longer = __ballot_sync(0xffffffffu, n > 1);
+        if (n > 0) {
+            const unsigned before = (1u << lane) - 1;
+            const int at = n == 1 ? __popc(single & before) : __popc(single) + __popc(longer & before);
+            starts[at] = lane;
+            lengths[at] = n;
+        }
+        if (lane == 0) {
+            counts[0] = __popc(single);
+            counts[1] = __popc(longer);
+        }
+    }
+    __syncthreads();
+    const int singles = counts[0], longer = counts[1], batches = (singles + kAtOnce - 1) / kAtOnce;
+    auto kept_of = [&](int token) { return token < kept ? angles + token * p.rotary : nullptr; };
+    // Its heads of k and v: the runs' tasks, warp after warp.
+    int task = warp;
+    for (int head = column; head < 2 * p.kv_heads; head += columns) {
+        const HeadCache c = head_cache(p, head);
+        const Unit unit(p, head < p.kv_heads);
+        for (int work = 0; work < batches + longer; ++work) {
+            if (task-- != 0)                 // (whose turn it is)
+                continue;
+            task = kWideWarps - 1;
+            const bool one = work < batches;         // a batch of runs of one token, a group of lanes each; or a longer run
+            const int run = one ? work * kAtOnce + group : singles + work - batches;
+            const bool mine = !one || run < singles;
+            const int start = mine ? starts[run] : 0;
+            const int64_t t = t0 + start, slot = mine ? slots[1 + start] : 0;
+            const int n = mine ? lengths[run] : 0;
+            const int64_t page = slot < INT_MAX ? (int)slot / p.page_size : slot / p.page_size;
+            const int place = (int)(slot - page * p.page_size), block = place >> p.block_shift, older = place - block * p.block;
+            uint8_t *cells = c.cells + page * c.page;
+            float *scale = c.scales + page * c.s_page + block * c.s_block;
+            const float before = mine && older > 0 ? *scale : 0.f;
+            const int first = one ? 0 : group, step = one ? 1 : kAtOnce;      // this group's tokens of the run
+            uint32_t top = 0;
+            // Calls with(k, values) for this group's tokens of the run.
+            auto each_token = [&](auto with) {
+#pragma unroll 1
+                for (int k = first; k < n; k += step) {
+                    uint4 raw[2];
+                    float cosines[8], sines[8], y[16];
+                    unit.load(c.x + (t + k) * c.step, raw);
+                    if (unit.turns)
+                        unit.angles(p, kept_of(start + k), t + k, cosines, sines);
+                    unit.turn(raw, cosines, sines, y);
+                    with(k, y);
+                }
+            };
+            auto agree = [&]() {             // the group's largest, or the warp's
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, top, o);
+                    if (o < kLanes || !one)
+                        top = max(top, other);
+                }
+            };
+            each_token([&](int, const float(&y)[16]) { top = max(top, Unit::largest(y)); });
+            agree();
+            const bool finite = top < 0x7f800000u;
+            if (__any_sync(0xffffffffu, !finite)) {
+                top = 0;
+                each_token([&](int, const float(&y)[16]) { top = max(top, Unit::largest_finite(y)); });
+                agree();
+            }
+            if (!mine)
+                continue;
+            float now = power_of_two(scale_exponent(__uint_as_float(top)));
+            now = before > now ? before : now;       // (a scale that is not a number is replaced)
+            if (older > 0 && now != before)
+                for (int l = (one ? 0 : group); l < older; l += step)
+                    unit.move(cells + (block * p.block + l) * c.place, before / now);
+            const bool plain = finite && !(__float_as_uint(now) & 0x7fffffu) && now >= power_of_two(kMinScaleExponent) &&
+                               now <= power_of_two(kMaxScaleExponent);
+            const float inverse = plain ? 1.f / now : 0.f;
+            each_token([&](int k, const float(&y)[16]) {
+                unit.store(cells + (slots[1 + start + k] - page * p.page_size) * c.place, y, now, plain, inverse);
+            });
+            if (one ? lane % kLanes == 0 : lane == 0)
+                *scale = now;
+        }
+    }
 }
 
 }  // namespace
@@ -248,6 +605,9 @@ extern "C" lowm_status_t lowm_rope_append_fp8(
     p.capacity = num_pages * page_size;
     p.page_size = page_size;
     p.block = block;
+    p.block_shift = 0;
+    while ((1 << p.block_shift) < block)
+        ++p.block_shift;
     p.axes = axes;
     p.section0 = section0;
     p.section1 = section1;
@@ -257,5 +617,28 @@ extern "C" lowm_status_t lowm_rope_append_fp8(
     p.kv_heads = kv_heads;
     p.dim = dim;
     p.rotary = rotary;
+    int64_t rows = 0, codes = 0;             // strides
+    for (int i = 0; i < 8; ++i)
+        rows |= strides[i];
+    for (int i = 8; i < 14; ++i)
+        codes |= strides[i];
+    const bool wide = block <= kWideBlock && table_rows <= INT_MAX && (dim == 64 || dim == 128 || dim == 256) && rotary % 16 == 0 && !(rows & 7) && !(codes & 7) && is_aligned(q, 16) &&
+                      is_aligned(k, 16) && is_aligned(v, 16) && is_aligned(q_out, 16) && is_aligned(k_cache, 8) && is_aligned(v_cache, 8);
+    if (wide) {
+        const int windows = (int)(((int64_t)tokens + kTokens - 1) / kTokens);
+        // A head a CTA while there are SMs, a head a warp at most.
+        const int columns = std::max((2 * kv_heads + kWideWarps - 1) / kWideWarps,
+                                     std::min(2 * kv_heads, (sms + windows - 1) / windows));
+        // Few tokens: a CTA each, to be done soonest.  Many: fewer threads with more heads, which read the angles once.
+        const int at_once = tokens >= 4 * sms ? 4 : 1;
+        const int64_t all = (int64_t)windows * columns + ((int64_t)tokens + at_once - 1) / at_once;
+        if (all > INT_MAX)
+            return LOWM_ERR_UNSUPPORTED_SHAPE;
+        auto fn = dim == 64    ? (interleaved ? rope_append_fp8_wide_kernel<64, true> : rope_append_fp8_wide_kernel<64, false>)
+                  : dim == 128 ? (interleaved ? rope_append_fp8_wide_kernel<128, true> : rope_append_fp8_wide_kernel<128, false>)
+                               : (interleaved ? rope_append_fp8_wide_kernel<256, true> : rope_append_fp8_wide_kernel<256, false>);
+        return launch_pdl(fn, dim3((unsigned)all), dim3(kWideThreads), (size_t)kAngleTokens * rotary * sizeof(float), stream, p,
+                          windows, windows * columns, at_once);
+    }
     return launch_pdl(rope_append_fp8_kernel, dim3((unsigned)ctas), dim3(kRopeThreads), 0, stream, p);
 }

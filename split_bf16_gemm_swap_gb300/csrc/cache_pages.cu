@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kPageThreads = 1024;           // of the CTA that ranks free pages
 constexpr int kMaxRows = 8192;
+constexpr int kFewRows = 64;                 // that one CTA forks, two a warp
 
 struct Table {
     int32_t *entries;
@@ -108,37 +109,49 @@ __device__ __forceinline__ int free_pages(const Pool &pool, int want, Found foun
 }
 
 // ------------------------------------------------------------------ fork
-// One CTA a row, old rows first: their pages are given up, the new rows' are counted.
-__global__ void __launch_bounds__(128) fork_rows_kernel(const Table old, const int32_t *parents, const Table next, int32_t *new_lens,
-                                                        const Pool pool)
+// An old row's pages are given up, a new row's counted and listed, by threads first, first + step, ... of the row.
+__device__ __forceinline__ void fork_row(const Table &old, const int32_t *parents, const Table &next, int32_t *new_lens, const Pool &pool,
+                                         int row, int first, int step)
 {
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    const int row = (int)blockIdx.x;
     const bool gone = row < old.rows;
     const int i = gone ? row : row - old.rows;
     const int from = gone ? row : parents[i];
     const int len = from >= 0 && from < old.rows ? old.lens[from] : 0;
     const int used = used_of(len, pool, old.width);
     const int32_t *src = old.entries + from * old.stride;
-    for (int j = threadIdx.x; j < (gone ? used : old.width); j += blockDim.x) {
+    for (int j = first; j < (gone ? used : old.width); j += step) {
         const int page = j < used ? src[j] : -1;
         if (!gone)
             next.entries[i * next.stride + j] = page;
         if (in_pool(page, pool))
             atomicAdd(pool.refs + page, gone ? -1 : 1);
     }
-    if (!gone && threadIdx.x == 0)
+    if (!gone && first == 0)
         new_lens[i] = len;
 }
 
+__global__ void __launch_bounds__(128) fork_rows_kernel(const Table old, const int32_t *parents, const Table next, int32_t *new_lens,
+                                                        const Pool pool)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    fork_row(old, parents, next, new_lens, pool, (int)blockIdx.x, threadIdx.x, blockDim.x);
+}
+
 // The unfinished last pages that several new rows have: the first of the rows keeps it.
-__global__ void __launch_bounds__(kPageThreads) fork_tails_kernel(const Table next, const Pool pool, int32_t *src, int32_t *dst,
-                                                                  int32_t *missing)
+// With `old`, the rows themselves come first, a warp each (few of them: a launch less).
+__global__ void __launch_bounds__(kPageThreads) fork_tails_kernel(const Table old, const int32_t *parents, const Table next,
+                                                                  int32_t *new_lens, const Pool pool, int32_t *src, int32_t *dst,
+                                                                  int32_t *missing, int rows_first)
 {
     extern __shared__ int32_t tails[];       // [rows]
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    if (rows_first) {
+        for (int row = threadIdx.x >> 5; row < old.rows + next.rows; row += kPageThreads / 32)
+            fork_row(old, parents, next, new_lens, pool, row, threadIdx.x & 31, 32);
+        __syncthreads();
+    }
     const int each = (next.rows + kPageThreads - 1) / kPageThreads, row0 = threadIdx.x * each;
     auto tail_at = [&](int i) { return next.entries + i * next.stride + used_of(next.lens[i], pool, next.width) - 1; };
     for (int i = threadIdx.x; i < next.rows; i += kPageThreads) {
@@ -471,11 +484,13 @@ extern "C" lowm_status_t lowm_fork_pages(const int32_t *page_table, int64_t tabl
     const Table old = {const_cast<int32_t *>(page_table), table_stride, lens, rows, width};
     const Table next = {new_table, new_table_stride, new_lens, new_rows, width};
     const Pool pool = {refs, num_pages, page_size};
-    if (rows + new_rows > 0 &&
+    const bool few = rows + new_rows <= kFewRows;
+    if (!few &&
         (st = launch_pdl(fork_rows_kernel, dim3((unsigned)(rows + new_rows)), dim3(128), 0, stream, old, parents, next, new_lens,
                          pool)) != LOWM_OK)
         return st;
-    return launch_pdl(fork_tails_kernel, dim3(1), dim3(kPageThreads), (size_t)new_rows * 4, stream, next, pool, src, dst, missing);
+    return launch_pdl(fork_tails_kernel, dim3(1), dim3(kPageThreads), (size_t)new_rows * 4, stream, old, parents, next, new_lens, pool,
+                      src, dst, missing, (int)few);
 }
 
 extern "C" size_t lowm_extend_pages_workspace(int num_pages) { return num_pages > 0 ? (size_t)num_pages * 4 : 0; }

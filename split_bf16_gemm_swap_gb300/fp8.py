@@ -157,23 +157,35 @@ def gemm_fp8(A, W, W_scale, A_scale=None, *, out=None, flags: int = 0, stream=No
 
 
 def _codes(k_cache, v_cache, k_scale, v_scale, device: int):
-    """Checks of a cache of codes; its sizes and strides."""
-    cache_shape, scale_shape = k_cache.shape, k_scale.shape
-    if len(cache_shape) != 4 or len(scale_shape) != 3:
+    """Checks of a cache of codes; its arguments for the library, from the pointer of k_cache to the block."""
+    shape, scale_shape, f32 = k_cache.shape, k_scale.shape, torch.float32
+    if len(shape) != 4 or len(scale_shape) != 3:
         raise ValueError("the caches must be [num_pages, page_size, kv_heads, dim] and the scales [num_pages, page_size / block, "
                          "kv_heads]")
-    num_pages, page_size, kv_heads, _ = cache_shape
-    blocks = scale_shape[1]
+    num_pages, page_size, kv_heads, dim = shape
+    scale_pages, blocks, scale_heads = scale_shape
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    if (k_cache.dtype is not FP8 or v_cache.dtype is not FP8 or k_scale.dtype is not f32 or v_scale.dtype is not f32
+            or v_cache.shape != shape or v_scale.shape != scale_shape or scale_pages != num_pages or scale_heads != kv_heads
+            or blocks < 1 or page_size % blocks or (dim > 1 and (k3 != 1 or v3 != 1)) or k_cache.get_device() != device
+            or v_cache.get_device() != device or k_scale.get_device() != device or v_scale.get_device() != device):
+        _refuse_codes(k_cache, v_cache, k_scale, v_scale, device)
+    return (k_cache.data_ptr(), k0, k1, k2, v_cache.data_ptr(), v0, v1, v2, k_scale.data_ptr(), *k_scale.stride(),
+            v_scale.data_ptr(), *v_scale.stride(), num_pages, page_size, page_size // blocks)
+
+
+def _refuse_codes(k_cache, v_cache, k_scale, v_scale, device: int):
+    num_pages, page_size, kv_heads, _ = k_cache.shape
+    blocks = k_scale.shape[1]
+    _rows(k_cache, "k_cache", FP8, k_cache.shape, device)
+    _rows(v_cache, "v_cache", FP8, k_cache.shape, device)
     if blocks < 1 or page_size % blocks:
         raise ValueError("page_size %d is not a whole number of %d blocks" % (page_size, blocks))
-    kc = _rows(k_cache, "k_cache", FP8, cache_shape, device)
-    vc = _rows(v_cache, "v_cache", FP8, cache_shape, device)
-    if scale_shape != (num_pages, blocks, kv_heads) or k_scale.dtype is not torch.float32 or k_scale.get_device() != device:
-        layer._refuse(k_scale, "k_scale", torch.float32, (num_pages, blocks, kv_heads), device)
-    if v_scale.shape != scale_shape or v_scale.dtype is not torch.float32 or v_scale.get_device() != device:
-        layer._refuse(v_scale, "v_scale", torch.float32, tuple(scale_shape), device)
-    return (k_cache.data_ptr(), *kc[:3], v_cache.data_ptr(), *vc[:3], k_scale.data_ptr(), *k_scale.stride(),
-            v_scale.data_ptr(), *v_scale.stride(), num_pages, page_size, page_size // blocks)
+    for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if x.dtype is not torch.float32 or x.shape != (num_pages, blocks, kv_heads) or x.get_device() != device:
+            layer._refuse(x, name, torch.float32, torch.Size((num_pages, blocks, kv_heads)), device)
+    raise AssertionError("unreachable")
 
 
 def rope_append_fp8(q, k, v, cos_sin, positions, slots, k_cache, v_cache, k_scale, v_scale, *, sections=None,

@@ -8,6 +8,7 @@ int32 [rows, width]; ``lens`` int32 [rows] says how many tokens each row has;
 """
 from __future__ import annotations
 
+import array
 import ctypes
 
 import torch
@@ -66,13 +67,14 @@ def lowm_copy_pages(*args) -> int:
 
 def _table(page_table, lens, refs, device: int):
     """Checks of a table, its lengths and the counts; (rows, width, stride, num_pages)."""
-    if page_table.dim() != 2 or refs.dim() != 1:
+    shape, counted = page_table.shape, refs.shape
+    if len(shape) != 2 or len(counted) != 1:
         raise ValueError("page_table must be [rows, width] and refs [num_pages]")
-    rows, width = page_table.shape
-    stride = _row_stride(page_table, "page_table", torch.int32, page_table.shape, device)
+    rows, width = shape
+    stride = _row_stride(page_table, "page_table", torch.int32, shape, device)
     _dense(lens, "lens", torch.int32, (rows,), device)
-    _dense(refs, "refs", torch.int32, refs.shape, device)
-    return rows, width, stride, refs.shape[0]
+    _dense(refs, "refs", torch.int32, counted, device)
+    return rows, width, stride, counted[0]
 
 
 def fork_pages(page_table, lens, parents, refs, page_size: int, *, out=None, stream=None):
@@ -174,9 +176,9 @@ def copy_pages(caches, src, dst, *, stream=None) -> None:
     _dense(src, "src", torch.int32, shape, device)
     _dense(dst, "dst", torch.int32, shape, device)
     spans = []
-    num_pages = caches[0].shape[0] if caches else 0
+    num_pages = caches[0].size(0) if len(caches) and caches[0].dim() else 0
     for x in caches:
-        if x.get_device() != device or x.dim() == 0 or x.shape[0] != num_pages:
+        if x.get_device() != device or x.dim() == 0 or x.size(0) != num_pages:
             raise ValueError("caches must be on cuda:%d and have one number of pages" % device)
         if x.is_contiguous():
             page_bytes = page_stride = x.nbytes // num_pages if num_pages else 0
@@ -186,7 +188,8 @@ def copy_pages(caches, src, dst, *, stream=None) -> None:
             page_bytes = x[0].nbytes if num_pages else 0
             page_stride = x.stride(0) * x.element_size()
         spans += (x.data_ptr(), page_stride, page_bytes)
-    packed = (ctypes.c_int64 * len(spans))(*spans)      # as lowm_page_span_t lies in memory
+    held = array.array("q", spans)                       # as lowm_page_span_t lies in memory
+    packed = held.buffer_info()[0]
     s = function("lowm_copy_pages")(packed, len(caches), src.data_ptr(), dst.data_ptr(), shape[0], num_pages,
                                     _current_stream(device))
     if s != LOWM_OK:

@@ -75,7 +75,8 @@ size_t lowm_gemm_fp8_bf16_workspace(int M, int K);
  * page; its scale covers the tokens of one head in it.
  *
  * Tokens that share a block are to be neighbouring tokens of the call with rising
- * places, as a sequence's are.  The first of them says what the block holds: at
+ * places, as a sequence's are; fewer than `block` tokens that are not appended may
+ * lie between two of them.  The first of them says what the block holds: at
  * the block's first place the block begins anew, else the tokens at the places
  * before it stay, and when the new ones need a larger scale their codes are moved
  * to it (code * old / new, rounded).  What lies behind the last new token is of no

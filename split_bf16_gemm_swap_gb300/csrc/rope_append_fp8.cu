@@ -79,6 +79,36 @@ __device__ __forceinline__ void each(const Rope8Params &p, bool turns, const Pos
         put(e, __bfloat162float(x[e]), -1, 0.f);
 }
 
+// A run: the tokens of one block, each with a higher slot than the one before it, fewer than `block` tokens of the call apart
+// (those between them are not appended).  slot_of(t) is the slot of token t, -1 where it is not appended or not one.  The
+// tokens from t to the last one of the run that begins there; 0 when none begins.
+template <typename SlotOf>
+__device__ __forceinline__ int64_t run_at(const Rope8Params &p, int64_t t, SlotOf slot_of)
+{
+    const int64_t slot = slot_of(t), block = slot >> p.block_shift;
+    if (slot < 0)
+        return 0;
+    for (int back = 1; back < p.block && back <= t; ++back) {
+        const int64_t before = slot_of(t - back);
+        if (before >= 0) {
+            if (before < slot && before >> p.block_shift == block)
+                return 0;                    // it is part of that token's
+            break;
+        }
+    }
+    int64_t last = t, highest = slot;
+    for (int64_t next = t + 1; next - last < p.block && next < p.tokens; ++next) {
+        const int64_t at = slot_of(next);
+        if (at < 0)
+            continue;
+        if (at <= highest || at >> p.block_shift != block)
+            break;
+        last = next;
+        highest = at;
+    }
+    return last - t + 1;
+}
+
 __global__ void __launch_bounds__(kRopeThreads) rope_append_fp8_kernel(const Rope8Params p)
 {
     const int lane = threadIdx.x & 31;
@@ -102,24 +132,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_fp8_kernel(const Rop
     }
     // The slot of a token that is appended, or -1.
     auto slot_of = [&](int64_t i) {
+        if (i < 0 || i >= p.tokens)
+            return (int64_t)-1;
         const int64_t slot = p.slots[i];
-        return slot >= 0 && slot < p.capacity && position_of(p, i).known ? slot : -1;
+        return slot >= 0 && slot < p.capacity && position_of(p, i).known ? slot : (int64_t)-1;
     };
-    const int64_t slot = slot_of(t), block = slot >> p.block_shift;
-    if (slot < 0)
+    const int64_t n = run_at(p, t, slot_of), slot = slot_of(t);
+    if (n == 0)
         return;
-    if (t > 0) {                             // the token before has the run, if it is part of it
-        const int64_t before = slot_of(t - 1);
-        if (before >= 0 && before < slot && before >> p.block_shift == block)
-            return;
-    }
-    int n = 1;
-    for (int64_t last = slot; n < p.block && t + n < p.tokens; ++n) {
-        const int64_t next = slot_of(t + n);
-        if (next <= last || next >> p.block_shift != block)
-            break;
-        last = next;
-    }
     const bool is_k = head < p.kv_heads;
     const int h = is_k ? head : head - p.kv_heads;
     const __nv_bfloat16 *x = is_k ? p.k + t * p.k_ts + h * p.k_hs : p.v + t * p.v_ts + h * p.v_hs;
@@ -131,9 +151,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_fp8_kernel(const Rop
                         : p.v_scale + page * p.vs_page + (place >> p.block_shift) * p.vs_block + h * p.vs_head;
 
     float amax = 0.f;
-    for (int i = 0; i < n; ++i)
-        each(p, is_k, position_of(p, t + i), x + i * step,
-             [&](int, float a, int, float b) { amax = fmaxf(amax, fmaxf(finite_magnitude(a), finite_magnitude(b))); });
+    for (int64_t i = 0; i < n; ++i)
+        if (slot_of(t + i) >= 0)
+            each(p, is_k, position_of(p, t + i), x + i * step,
+                 [&](int, float a, int, float b) { amax = fmaxf(amax, fmaxf(finite_magnitude(a), finite_magnitude(b))); });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -150,8 +171,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_fp8_kernel(const Rop
                 }
         }
     }
-    for (int i = 0; i < n; ++i) {
-        uint8_t *to = cells + (p.slots[t + i] - page * p.page_size) * place_step;
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t at = slot_of(t + i);
+        if (at < 0)
+            continue;
+        uint8_t *to = cells + (at - page * p.page_size) * place_step;
         each(p, is_k, position_of(p, t + i), x + i * step, [&](int e0, float a, int e1, float b) {
             const uint32_t w = to_e4m3x2(nan_unless_finite(a) / now, nan_unless_finite(b) / now);
             to[e0] = (uint8_t)w;
@@ -377,7 +401,7 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         return;
     }
     extern __shared__ __align__(16) float angles[];     // [kAngleTokens][rotary]
-    __shared__ int64_t slots[1 + kTokens + kWideBlock]; // from the token before the first on; -1: not appended
+    __shared__ int64_t slots[kTokens + 2 * kWideBlock]; // from token t0 - block on; -1: not appended
     __shared__ int rows[3][kAngleTokens];    // of the table, by axis; -1: not one of its rows
     __shared__ int starts[kTokens], lengths[kTokens], counts[2];    // the runs that begin here, those of one token first
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / kLanes;
@@ -385,8 +409,9 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     const int column = blockIdx.x / windows, columns = kv_ctas / windows;
     const int here = (int)min((int64_t)kTokens, p.tokens - t0);
     const int kept = (int)min((int64_t)min(kAngleTokens, kTokens - 1 + p.block), p.tokens - t0);      // tokens
-    for (int i = threadIdx.x; i < 1 + kTokens + p.block; i += kWideThreads) {
-        const int64_t t = t0 - 1 + i;
+    const int cached = kTokens + 2 * p.block;
+    for (int i = threadIdx.x; i < cached; i += kWideThreads) {
+        const int64_t t = t0 - p.block + i;
         int64_t slot = -1;
         if (t >= 0 && t < p.tokens) {
             int64_t at[3];
@@ -398,10 +423,10 @@ __global__ void __launch_bounds__(kWideThreads, 2)
 #pragma unroll
             for (int a = 0; a < 3; ++a)
                 known = known && at[a] >= 0 && at[a] < p.table_rows;
-            if (i > 0 && i <= kAngleTokens)
+            if (i >= p.block && i < p.block + kAngleTokens)
 #pragma unroll
                 for (int a = 0; a < 3; ++a)
-                    rows[a][i - 1] = known ? (int)at[a] : -1;
+                    rows[a][i - p.block] = known ? (int)at[a] : -1;
             slot = known && slot >= 0 && slot < p.capacity ? slot : -1;
         }
         slots[i] = slot;
@@ -423,20 +448,17 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         *reinterpret_cast<float4 *>(angles + token * p.rotary + j) = x;
     }
     __syncthreads();
+    auto slot_of = [&](int64_t t) {          // (what lies further away is of a run with gaps)
+        const int64_t i = t - t0 + p.block;
+        if (i >= 0 && i < cached)
+            return slots[i];
+        if (t < 0 || t >= p.tokens)
+            return (int64_t)-1;
+        const int64_t slot = p.slots[t];
+        return slot >= 0 && slot < p.capacity && position_of(p, t).known ? slot : (int64_t)-1;
+    };
     if (warp == 0) {                         // a lane a token
-        int n = 0;
-        if (lane < here) {
-            const int64_t before = slots[lane], slot = slots[1 + lane];
-            if (slot >= 0 && !(before >= 0 && before < slot && before >> p.block_shift == slot >> p.block_shift)) {
-                n = 1;
-                for (int64_t last = slot; n < p.block; ++n) {
-                    const int64_t next = slots[1 + lane + n];
-                    if (next <= last || next >> p.block_shift != slot >> p.block_shift)
-                        break;
-                    last = next;
-                }
-            }
-        }
+        const int n = lane < here ? (int)min(run_at(p, t0 + lane, slot_of), (int64_t)INT_MAX) : 0;
         const unsigned single = __ballot_sync(0xffffffffu, n == 1), longer = __ballot_sync(0xffffffffu, n > 1);
         if (n > 0) {
             const unsigned before = (1u << lane) - 1;
@@ -465,7 +487,7 @@ __global__ void __launch_bounds__(kWideThreads, 2)
             const int run = one ? work * kAtOnce + group : singles + work - batches;
             const bool mine = !one || run < singles;
             const int start = mine ? starts[run] : 0;
-            const int64_t t = t0 + start, slot = mine ? slots[1 + start] : 0;
+            const int64_t t = t0 + start, slot = mine ? slots[p.block + start] : 0;
             const int n = mine ? lengths[run] : 0;
             const int64_t page = slot < INT_MAX ? (int)slot / p.page_size : slot / p.page_size;
             const int place = (int)(slot - page * p.page_size), block = place >> p.block_shift, older = place - block * p.block;
@@ -478,6 +500,8 @@ __global__ void __launch_bounds__(kWideThreads, 2)
             auto each_token = [&](auto with) {
 #pragma unroll 1
                 for (int k = first; k < n; k += step) {
+                    if (slot_of(t + k) < 0)
+                        continue;
                     uint4 raw[2];
                     float cosines[8], sines[8], y[16];
                     unit.load(c.x + (t + k) * c.step, raw);
@@ -514,7 +538,7 @@ __global__ void __launch_bounds__(kWideThreads, 2)
                                now <= power_of_two(kMaxScaleExponent);
             const float inverse = plain ? 1.f / now : 0.f;
             each_token([&](int k, const float(&y)[16]) {
-                unit.store(cells + (slots[1 + start + k] - page * p.page_size) * c.place, y, now, plain, inverse);
+                unit.store(cells + (slot_of(t + k) - page * p.page_size) * c.place, y, now, plain, inverse);
             });
             if (one ? lane % kLanes == 0 : lane == 0)
                 *scale = now;

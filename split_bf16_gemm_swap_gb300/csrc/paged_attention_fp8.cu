@@ -14,10 +14,13 @@
 // that of weight / b_j in fp32.  (mma.sync takes e4m3 operands, too, but widens them itself, and adds in separate
 // instructions: 1280 a 32 keys and 16 rows against 300 a 32 keys and 8 rows here.)
 //
-// Work.  Items, shares and parts are those of attention_line.cuh.  Four warps have R rows each (8: decoding; 16).  Where an
-// item has fewer rows, warps share them and each takes every second or fourth 32 keys; their sums are joined through shared
-// memory in a fixed order.  A fifth warp feeds a ring of 64-key tiles: codes by TMA, page by page (swizzled, so that the
-// fragments' 16-byte reads meet no bank twice), scales by 4-byte asynchronous copies.
+// Work.  Items, shares and parts are those of attention_line.cuh, with items of 32 rows.  Four warps have eight rows each;
+// where an item has fewer, warps share them and each takes every second or fourth 32 keys, and their sums are joined through
+// shared memory in a fixed order.  A fifth warp feeds a ring of 64-key tiles: codes by TMA, page by page (swizzled, so that the
+// fragments' 16-byte reads meet no bank twice), scales by 4-byte asynchronous copies.  Two CTAs an SM with rings of five
+// tiles: 24 sequences of up to 16384 keys 90.5 us (floor 74.4), with three CTAs and three tiles, whose registers do not
+// suffice, 96, with four and two 123.  Sixteen rows a warp (a key widened once for two products) were slower for any number
+// of rows: 8 sequences of 8 tokens over 4000 keys 39.5 us for 29.7.  L2 promotion of 256 bytes: 123 us for 96.
 //
 // The orders of the head's elements (for q.k) and of the elements' rows (for w.v) within a product are free; they are chosen
 // so that a thread's fragments are neighbouring bytes of the cache.  V's keys are paired by byte permutes before they are
@@ -38,9 +41,10 @@ namespace lowm {
 namespace {
 
 constexpr int kWarps = 4;                    // that compute
+constexpr int kWarpRows = 8;                 // rows of a warp, the columns of its products
 constexpr int kThreads8 = 32 * (kWarps + 1);
 constexpr int kUnitKeys = 32;                // of one product
-constexpr int kMaxCtas = 480;                // three per SM, and a bound for the workspace
+constexpr int kMaxCtas = 320;                // two per SM, and a bound for the workspace
 constexpr int kItemCost8 = 4, kMinShare8 = 4;
 constexpr float kWeightLog2 = 8.f, kRescaleLog2 = 7.f;   // the largest weight is 2^15 (fp16 ends at 65504)
 constexpr float kMaxScale = 1.125899906842624e15f;   // 2^50: scales are taken as 2^-50 .. 2^50
@@ -57,8 +61,7 @@ struct CutItem8 {
     int q0, q_len, head, q_tile;
 };
 
-template <int ROWS>
-struct Attn8Params : LineParams<ROWS, kItemCost8, kMinShare8> {
+struct Attn8Params : LineParams<kWarps * kWarpRows, kItemCost8, kMinShare8> {
     const __nv_bfloat16 *q;
     const float *k_scale, *v_scale;
     __nv_bfloat16 *out;
@@ -144,13 +147,13 @@ __device__ __forceinline__ void load_shared(const uint8_t *at, uint32_t (&w)[WOR
 }
 
 // ------------------------------------------------------------------ shared memory
-template <int DIM, int R>
+template <int DIM>
 struct Attn8Smem {
-    static constexpr int kCtas = R == 8 ? 3 : 2;                        // an SM
+    static constexpr int kCtas = 2;                                     // an SM
     static constexpr uint32_t kTileBytes = kTileKeys * DIM;             // of K or V; 1024-byte multiples
-    static constexpr uint32_t kStages = (R == 8 ? 3 : 5) * (128 / DIM);
-    static constexpr uint32_t kOut = R * DIM / 32;                      // sums a thread holds
-    static constexpr uint32_t kSums = R / 2;                            // and maxima and sums of weights
+    static constexpr uint32_t kStages = 5 * (128 / DIM);
+    static constexpr uint32_t kOut = DIM / 4;                           // sums a thread holds
+    static constexpr uint32_t kSums = 4;                                // and maxima and sums of weights
     static constexpr uint32_t kScales = kStages * 2 * kTileBytes;       // [stages][K, V][64]
     static constexpr uint32_t kMerge = kScales + kStages * 2 * kTileKeys * 4;       // [warps / 2][kOut + kSums][32]
     static constexpr uint32_t kKeys = kMerge + kWarps / 2 * (kOut + kSums) * 32 * 4;    // [warps][32 keys at hand][4]
@@ -164,69 +167,65 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w)
     return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// One warp's R rows of an item, eight a set.  Thread 4 g + t has of row g of a set elements [DIM / 4 t, DIM / 4 (t + 1)) of
+// One warp's rows of an item.  Thread 4 g + t has of row g elements [DIM / 4 t, DIM / 4 (t + 1)) of
 // q, and of rows 2 t and 2 t + 1 the maximum, the sum of its keys' weights and elements [DIM / 8 g, DIM / 8 (g + 1)) of the
 // weighted values: out[e] holds elements 2 e and 2 e + 1 of those, of row 2 t, row 2 t + 1, row 2 t, row 2 t + 1.
-template <int DIM, int R>
+template <int DIM>
 struct Rows8 {
-    static constexpr int kSets = R / 8;
-    uint32_t q[kSets][DIM / 16][2];
-    float unit[kSets][2];                    // power of two that q was divided by
-    int hi[kSets][2], lo[kSets][2];          // keys that a row sees (none: hi < lo)
-    float top[kSets][2], sum[kSets][2];
-    float out[kSets][DIM / 16][4];
+    uint32_t q[DIM / 16][2];
+    float unit[2];                    // power of two that q was divided by
+    int hi[2], lo[2];          // keys that a row sees (none: hi < lo)
+    float top[2], sum[2];
+    float out[DIM / 16][4];
 };
 
-template <int DIM, int R, class P>
-__device__ __forceinline__ void load_rows(const P &p, const Item &it, int row0, Rows8<DIM, R> &x)
+template <int DIM, class P>
+__device__ __forceinline__ void load_rows(const P &p, const Item &it, int row0, Rows8<DIM> &x)
 {
     constexpr int N = DIM / 4;               // elements a thread holds of a row of q
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const Row row = row_of(p, it, row0 + g);
+    alignas(16) __nv_bfloat16 v[N];
+    const __nv_bfloat16 *from = p.q + row.token * p.q_ts + row.q_head * p.q_hs + N * t;
 #pragma unroll
-    for (int set = 0; set < R / 8; ++set) {
-        const Row row = row_of(p, it, row0 + 8 * set + g);
-        alignas(16) __nv_bfloat16 v[N];
-        const __nv_bfloat16 *from = p.q + row.token * p.q_ts + row.q_head * p.q_hs + N * t;
+    for (int i = 0; i < N; i += 8) {
+        if (!row.valid) {
+            *reinterpret_cast<uint4 *>(v + i) = make_uint4(0, 0, 0, 0);
+        } else if (p.q_vec) {
+            *reinterpret_cast<uint4 *>(v + i) = *reinterpret_cast<const uint4 *>(from + i);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; i += 8) {
-            if (!row.valid) {
-                *reinterpret_cast<uint4 *>(v + i) = make_uint4(0, 0, 0, 0);
-            } else if (p.q_vec) {
-                *reinterpret_cast<uint4 *>(v + i) = *reinterpret_cast<const uint4 *>(from + i);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[i + j] = from[i + j];
-            }
+            for (int j = 0; j < 8; ++j)
+                v[i + j] = from[i + j];
         }
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            amax = fmaxf(amax, finite_magnitude(__bfloat162float(v[i])));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = scale_exponent(amax);
-        const float inverse = power_of_two(-e);
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const __half2 h = __floats2half2_rn(__bfloat162float(v[i]) * inverse, __bfloat162float(v[i + 1]) * inverse);
-            x.q[set][i / 4][i / 2 & 1] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int from_lane = 4 * (2 * t + c);
-            x.unit[set][c] = power_of_two(__shfl_sync(0xffffffffu, e, from_lane));
-            x.hi[set][c] = __shfl_sync(0xffffffffu, row.valid ? row.hi : -1, from_lane);
-            x.lo[set][c] = __shfl_sync(0xffffffffu, row.valid ? row.lo : 0, from_lane);
-            x.top[set][c] = -CUDART_INF_F;
-            x.sum[set][c] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < DIM / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x.out[set][i][j] = 0.f;
     }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        amax = fmaxf(amax, finite_magnitude(__bfloat162float(v[i])));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int e = scale_exponent(amax);
+    const float inverse = power_of_two(-e);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const __half2 h = __floats2half2_rn(__bfloat162float(v[i]) * inverse, __bfloat162float(v[i + 1]) * inverse);
+        x.q[i / 4][i / 2 & 1] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int from_lane = 4 * (2 * t + c);
+        x.unit[c] = power_of_two(__shfl_sync(0xffffffffu, e, from_lane));
+        x.hi[c] = __shfl_sync(0xffffffffu, row.valid ? row.hi : -1, from_lane);
+        x.lo[c] = __shfl_sync(0xffffffffu, row.valid ? row.lo : 0, from_lane);
+        x.top[c] = -CUDART_INF_F;
+        x.sum[c] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < DIM / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x.out[i][j] = 0.f;
 }
 
 // Key i of this thread's four among 16 of V.
@@ -234,25 +233,22 @@ __device__ __forceinline__ int value_key(int i, int t) { return 8 * (i >> 1) + 2
 
 // out += V^T . w for the rows of all sets: 16 keys, elements 4 w .. 4 w + 3 of the thread's from its keys' words; b0, b1:
 // the weights of keys 2 t, 2 t + 1 and 8 + those of row g.
-template <int SETS, int TILES>
-__device__ __forceinline__ void weigh(float (&out)[SETS][TILES][4], const uint32_t (&v)[4], int w, const uint32_t (&b0)[SETS],
-                                      const uint32_t (&b1)[SETS])
+template <int TILES>
+__device__ __forceinline__ void weigh(float (&out)[TILES][4], const uint32_t (&v)[4], int w, const uint32_t (&b0),
+                                      const uint32_t (&b1))
 {
     const uint32_t lo0 = __byte_perm(v[0], v[1], 0x5140), hi0 = __byte_perm(v[0], v[1], 0x7362);   // elements 0, 1 and 2, 3
     const uint32_t lo1 = __byte_perm(v[2], v[3], 0x5140), hi1 = __byte_perm(v[2], v[3], 0x7362);
-#pragma unroll
-    for (int set = 0; set < SETS; ++set) {
-        mma_f16(out[set][2 * w], widen_lo(lo0), widen_hi(lo0), widen_lo(lo1), widen_hi(lo1), b0[set], b1[set]);
-        mma_f16(out[set][2 * w + 1], widen_lo(hi0), widen_hi(hi0), widen_lo(hi1), widen_hi(hi1), b0[set], b1[set]);
-    }
+    mma_f16(out[2 * w], widen_lo(lo0), widen_hi(lo0), widen_lo(lo1), widen_hi(lo1), b0, b1);
+    mma_f16(out[2 * w + 1], widen_lo(hi0), widen_hi(hi0), widen_lo(hi1), widen_hi(hi1), b0, b1);
 }
 
 // The 32 keys from key0 on (rows `first` to `first` + 31 of the tile) for one warp's rows.
-template <int DIM, int R>
-__device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Seen &seen, int key0, int first, const uint8_t *k_tile,
+template <int DIM>
+__device__ __forceinline__ void attend(Rows8<DIM> &x, const Seen &seen, int key0, int first, const uint8_t *k_tile,
                                        const uint8_t *v_tile, const float *scales, float4 *mine, float scale_log2)
 {
-    constexpr int kSets = R / 8, kWords = DIM / 32;
+    constexpr int kWords = DIM / 32;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // Scales of the 32 keys, a key a lane; those that no row sees count nothing.
     {
@@ -263,7 +259,7 @@ __device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Seen &seen, int k
         __syncwarp();
     }
     // Scores: thread 4 g + t has keys g + 8 j of rows 2 t and 2 t + 1.
-    float s[kSets][2][4] = {};
+    float s[2][4] = {};
 #pragma unroll
     for (int i = 0; i < DIM / 64; ++i) {
         uint32_t w[4][4];
@@ -279,9 +275,7 @@ __device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Seen &seen, int k
             for (int m = 0; m < 2; ++m) {
                 const uint32_t a0 = widen_lo(w[2 * m][k]), a1 = widen_lo(w[2 * m + 1][k]), a2 = widen_hi(w[2 * m][k]),
                                a3 = widen_hi(w[2 * m + 1][k]);
-#pragma unroll
-                for (int set = 0; set < kSets; ++set)
-                    mma_f16(s[set][m], a0, a1, a2, a3, x.q[set][4 * i + k][0], x.q[set][4 * i + k][1]);
+                mma_f16(s[m], a0, a1, a2, a3, x.q[4 * i + k][0], x.q[4 * i + k][1]);
             }
     }
     const bool edge = key0 < seen.all_lo || key0 + kUnitKeys - 1 > seen.all_hi;
@@ -291,62 +285,57 @@ __device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Seen &seen, int k
         const float4 a = mine[g + 8 * j];
         inverse[j] = a.z;
 #pragma unroll
-        for (int set = 0; set < kSets; ++set)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float &y = s[set][j >> 1][2 * (j & 1) + c];
-                y = fmaf(y * a.x, x.unit[set][c], a.y);
-                if (edge && (key0 + g + 8 * j > x.hi[set][c] || key0 + g + 8 * j < x.lo[set][c]))
-                    y = -CUDART_INF_F;
-            }
+        for (int c = 0; c < 2; ++c) {
+            float &y = s[j >> 1][2 * (j & 1) + c];
+            y = fmaf(y * a.x, x.unit[c], a.y);
+            if (edge && (key0 + g + 8 * j > x.hi[c] || key0 + g + 8 * j < x.lo[c]))
+                y = -CUDART_INF_F;
+        }
     }
     __syncwarp();                            // `mine` may be written again
     // Weights.
-    uint32_t weights[kSets][4];              // of keys 8 i + 2 t, 8 i + 2 t + 1 and row g
+    uint32_t weights[4];              // of keys 8 i + 2 t, 8 i + 2 t + 1 and row g
+    float top[2];
 #pragma unroll
-    for (int set = 0; set < kSets; ++set) {
-        float top[2];
+    for (int c = 0; c < 2; ++c) {
+        top[c] = fmaxf(fmaxf(s[0][c], s[0][2 + c]), fmaxf(s[1][c], s[1][2 + c]));
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            top[c] = fmaxf(fmaxf(s[set][0][c], s[set][0][2 + c]), fmaxf(s[set][1][c], s[set][1][2 + c]));
-#pragma unroll
-            for (int o = 4; o < 32; o *= 2)
-                top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
-        }
-        if (__any_sync(0xffffffffu, top[0] > x.top[set][0] + kRescaleLog2 || top[1] > x.top[set][1] + kRescaleLog2)) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float now = fmaxf(x.top[set][c], top[c]);
-                const float before = now == x.top[set][c] ? 1.f : ex2(x.top[set][c] - now);
-                x.top[set][c] = now;
-                x.sum[set][c] *= before;
-#pragma unroll
-                for (int e = 0; e < DIM / 16; ++e) {
-                    x.out[set][e][c] *= before;
-                    x.out[set][e][2 + c] *= before;
-                }
-            }
-        }
+        for (int o = 4; o < 32; o *= 2)
+            top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
+    }
+    if (__any_sync(0xffffffffu, top[0] > x.top[0] + kRescaleLog2 || top[1] > x.top[1] + kRescaleLog2)) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const float shift = x.top[set][c] == -CUDART_INF_F ? 0.f : x.top[set][c] - kWeightLog2;
+            const float now = fmaxf(x.top[c], top[c]);
+            const float before = now == x.top[c] ? 1.f : ex2(x.top[c] - now);
+            x.top[c] = now;
+            x.sum[c] *= before;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float &y = s[set][j >> 1][2 * (j & 1) + c];
-                y = ex2(y - shift);
-                x.sum[set][c] = fmaf(y, inverse[j], x.sum[set][c]);
+            for (int e = 0; e < DIM / 16; ++e) {
+                x.out[e][c] *= before;
+                x.out[e][2 + c] *= before;
             }
         }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const float shift = x.top[c] == -CUDART_INF_F ? 0.f : x.top[c] - kWeightLog2;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const __half2 h = __floats2half2_rn(s[set][j >> 1][2 * (j & 1)], s[set][j >> 1][2 * (j & 1) + 1]);
-            weights[set][j] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&h));
+            float &y = s[j >> 1][2 * (j & 1) + c];
+            y = ex2(y - shift);
+            x.sum[c] = fmaf(y, inverse[j], x.sum[c]);
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2 h = __floats2half2_rn(s[j >> 1][2 * (j & 1)], s[j >> 1][2 * (j & 1) + 1]);
+        weights[j] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&h));
     }
     // Values, 16 keys at a time.
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        uint32_t v[4][kWords], b0[kSets], b1[kSets];
+        uint32_t v[4][kWords], b0, b1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = first + 16 * half + value_key(i, t);
@@ -371,18 +360,15 @@ __device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Seen &seen, int k
                 }
             }
             if (__any_sync(0xffffffffu, bad != 0)) {
+                uint32_t ones[2];
 #pragma unroll
-                for (int set = 0; set < kSets; ++set) {
-                    uint32_t ones[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int key = k0 + g + 8 * j;
-                        ones[j] = key <= x.hi[set][0] && key >= x.lo[set][0] ? 0x3c00u : 0u;
-                        ones[j] |= key <= x.hi[set][1] && key >= x.lo[set][1] ? 0x3c000000u : 0u;
-                    }
-                    b0[set] = transpose_8x8(ones[0]);
-                    b1[set] = transpose_8x8(ones[1]);
+                for (int j = 0; j < 2; ++j) {
+                    const int key = k0 + g + 8 * j;
+                    ones[j] = key <= x.hi[0] && key >= x.lo[0] ? 0x3c00u : 0u;
+                    ones[j] |= key <= x.hi[1] && key >= x.lo[1] ? 0x3c000000u : 0u;
                 }
+                b0 = transpose_8x8(ones[0]);
+                b1 = transpose_8x8(ones[1]);
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
                     uint32_t flags[4];
@@ -392,24 +378,19 @@ __device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Seen &seen, int k
                         flags[i] = nan & 0x38383838u;         // 1.0
                         v[i][w] &= ~nan;
                     }
-                    float count[kSets][2][4] = {};
+                    float count[2][4] = {};
                     weigh(count, flags, 0, b0, b1);
 #pragma unroll
-                    for (int set = 0; set < kSets; ++set)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                if (count[set][e][c] > 0.f)
-                                    x.out[set][2 * w + e][c] = CUDART_NAN_F;
+                        for (int c = 0; c < 4; ++c)
+                            if (count[e][c] > 0.f)
+                                x.out[2 * w + e][c] = CUDART_NAN_F;
                 }
             }
         }
-#pragma unroll
-        for (int set = 0; set < kSets; ++set) {
-            b0[set] = weights[set][2 * half];
-            b1[set] = weights[set][2 * half + 1];
-        }
+        b0 = weights[2 * half];
+        b1 = weights[2 * half + 1];
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
             const uint32_t word[4] = {v[0][w], v[1][w], v[2][w], v[3][w]};
@@ -420,59 +401,54 @@ __device__ __forceinline__ void attend(Rows8<DIM, R> &x, const Seen &seen, int k
 
 // Joins the sums of the warps that share rows: in each step the upper half of them hand theirs over.  Their number is the
 // same for the whole CTA; all of its kWarps warps come here.
-template <int DIM, int R>
-__device__ __forceinline__ void join_warps(Rows8<DIM, R> &x, float *merge, int sharing, int row_tiles, int warp)
+template <int DIM>
+__device__ __forceinline__ void join_warps(Rows8<DIM> &x, float *merge, int sharing, int row_tiles, int warp)
 {
-    constexpr int kSets = R / 8, kOut = R * DIM / 32, kAll = kOut + R / 2;
+    constexpr int kOut = DIM / 4, kAll = kOut + 4;
     const int lane = threadIdx.x & 31;
     const int rt = warp % row_tiles, part = warp / row_tiles;
     for (int half = sharing / 2; half > 0; half /= 2) {
         float *at = merge + ((part & (half - 1)) * row_tiles + rt) * kAll * 32 + lane;
         if (part >= half && part < 2 * half) {
 #pragma unroll
-            for (int set = 0; set < kSets; ++set) {
+            for (int e = 0; e < DIM / 16; ++e)
 #pragma unroll
-                for (int e = 0; e < DIM / 16; ++e)
+                for (int c = 0; c < 4; ++c)
+                    at[(e * 4 + c) * 32] = x.out[e][c];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        at[((set * (DIM / 16) + e) * 4 + c) * 32] = x.out[set][e][c];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    at[(kOut + 4 * set + c) * 32] = x.top[set][c];
-                    at[(kOut + 4 * set + 2 + c) * 32] = x.sum[set][c];
-                }
+            for (int c = 0; c < 2; ++c) {
+                at[(kOut + c) * 32] = x.top[c];
+                at[(kOut + 2 + c) * 32] = x.sum[c];
             }
         }
         ptx::named_barrier_sync(1, 32 * kWarps);
         if (part < half) {
 #pragma unroll
-            for (int set = 0; set < kSets; ++set)
+            for (int c = 0; c < 2; ++c) {
+                const float top = at[(kOut + c) * 32];
+                const float now = fmaxf(x.top[c], top);
+                const float base = now == -CUDART_INF_F ? 0.f : now;
+                const float a = ex2(x.top[c] - base), b = ex2(top - base);
+                x.top[c] = now;
+                x.sum[c] = fmaf(x.sum[c], a, at[(kOut + 2 + c) * 32] * b);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float top = at[(kOut + 4 * set + c) * 32];
-                    const float now = fmaxf(x.top[set][c], top);
-                    const float base = now == -CUDART_INF_F ? 0.f : now;
-                    const float a = ex2(x.top[set][c] - base), b = ex2(top - base);
-                    x.top[set][c] = now;
-                    x.sum[set][c] = fmaf(x.sum[set][c], a, at[(kOut + 4 * set + 2 + c) * 32] * b);
+                for (int e = 0; e < DIM / 16; ++e)
 #pragma unroll
-                    for (int e = 0; e < DIM / 16; ++e)
-#pragma unroll
-                        for (int h = 0; h < 4; h += 2)
-                            x.out[set][e][h + c] =
-                                fmaf(x.out[set][e][h + c], a, at[((set * (DIM / 16) + e) * 4 + h + c) * 32] * b);
-                }
+                    for (int h = 0; h < 4; h += 2)
+                        x.out[e][h + c] =
+                            fmaf(x.out[e][h + c], a, at[(e * 4 + h + c) * 32] * b);
+            }
         }
         ptx::named_barrier_sync(1, 32 * kWarps);
     }
 }
 
-template <int DIM, int R>
-__global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM, R>::kCtas)
+template <int DIM>
+__global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM>::kCtas)
     paged_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                               const Attn8Params<kWarps * R> p)
+                               const Attn8Params p)
 {
-    using L = Attn8Smem<DIM, R>;
+    using L = Attn8Smem<DIM>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_u32(smem);
     const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kStages;
@@ -569,13 +545,13 @@ __global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM, R>::kCtas)
         const int from = c.from, n = c.to - c.from;
         const int in_item = min(p.kRows, it.q_len * p.group - it.q_tile * p.kRows);
         int row_tiles = 1;
-        while (row_tiles * R < in_item)
+        while (row_tiles * kWarpRows < in_item)
             row_tiles *= 2;
         const int sharing = kWarps / row_tiles, rt = warp % row_tiles, part = warp / row_tiles;
-        const bool has_rows = rt * R < in_item;
+        const bool has_rows = rt * kWarpRows < in_item;
         const Seen seen = seen_by(p, it);
-        Rows8<DIM, R> x;
-        load_rows<DIM, R>(p, it, rt * R, x);
+        Rows8<DIM> x;
+        load_rows<DIM>(p, it, rt * kWarpRows, x);
         for (int j = 0; j < n; ++j, ++i) {
             const uint32_t s = i % L::kStages;
             if (ok && !wait_short(bar_full + 8 * s, (i / L::kStages) & 1)) {
@@ -588,14 +564,14 @@ __global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM, R>::kCtas)
 #pragma unroll 1
             for (int h = 0; h < kTileKeys / kUnitKeys; ++h)
                 if (ok && has_rows && ((2 * j + h) & (sharing - 1)) == part)
-                    attend<DIM, R>(x, seen, (it.first_tile + from + j) * kTileKeys + kUnitKeys * h, kUnitKeys * h, k_tile,
+                    attend<DIM>(x, seen, (it.first_tile + from + j) * kTileKeys + kUnitKeys * h, kUnitKeys * h, k_tile,
                                    k_tile + L::kTileBytes, scales, keys, p.scale_log2);
             __syncwarp();
             if (lane == 0)
                 ptx::mbar_arrive(bar_empty + 8 * s);
         }
         if (sharing > 1)
-            join_warps<DIM, R>(x, merge, sharing, row_tiles, warp);
+            join_warps<DIM>(x, merge, sharing, row_tiles, warp);
         // The item's rows: finished here, or a part for the join.
         const bool whole = n == it.tiles;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0);
@@ -606,49 +582,47 @@ __global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM, R>::kCtas)
             continue;
         constexpr int N = DIM / 8;           // elements a thread holds of a row
 #pragma unroll
-        for (int set = 0; set < R / 8; ++set)
+        for (int c = 0; c < 2; ++c) {
+            float sum = x.sum[c];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float sum = x.sum[set][c];
+            for (int o = 4; o < 32; o *= 2)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const int r = rt * kWarpRows + 2 * t + c;
+            const Row row = row_of(p, it, r);
+            if (!row.valid)
+                continue;
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                alignas(16) __nv_bfloat162 v[N / 2];
 #pragma unroll
-                for (int o = 4; o < 32; o *= 2)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                const int r = rt * R + 8 * set + 2 * t + c;
-                const Row row = row_of(p, it, r);
-                if (!row.valid)
-                    continue;
-                if (whole) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    alignas(16) __nv_bfloat162 v[N / 2];
+                for (int e = 0; e < N / 2; ++e)
+                    v[e] = __floats2bfloat162_rn(x.out[e][c] * inv, x.out[e][2 + c] * inv);
+                __nv_bfloat16 *o = p.out + row.token * p.o_ts + row.q_head * p.o_hs + N * g;
+                if (p.out_vec) {
 #pragma unroll
-                    for (int e = 0; e < N / 2; ++e)
-                        v[e] = __floats2bfloat162_rn(x.out[set][e][c] * inv, x.out[set][e][2 + c] * inv);
-                    __nv_bfloat16 *o = p.out + row.token * p.o_ts + row.q_head * p.o_hs + N * g;
-                    if (p.out_vec) {
-#pragma unroll
-                        for (int e = 0; e < N; e += 8)
-                            *reinterpret_cast<uint4 *>(o + e) = *reinterpret_cast<const uint4 *>(v + e / 2);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < N / 2; ++e) {
-                            o[2 * e] = v[e].x;
-                            o[2 * e + 1] = v[e].y;
-                        }
-                    }
-                    if (p.lse && g == 0)
-                        p.lse[(int64_t)row.token * p.heads + row.q_head] =
-                            sum == 0.f ? -CUDART_INF_F : (x.top[set][c] - kWeightLog2 + log2f(sum)) * CUDART_LN2_F;
+                    for (int e = 0; e < N; e += 8)
+                        *reinterpret_cast<uint4 *>(o + e) = *reinterpret_cast<const uint4 *>(v + e / 2);
                 } else {
-                    float *o = p.parts + (slot * p.slot_rows + r) * DIM + N * g;
 #pragma unroll
-                    for (int e = 0; e < N / 2; e += 2)
-                        *reinterpret_cast<float4 *>(o + 2 * e) = make_float4(x.out[set][e][c], x.out[set][e][2 + c],
-                                                                             x.out[set][e + 1][c], x.out[set][e + 1][2 + c]);
-                    if (g == 0)
-                        reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * DIM)[slot * p.slot_rows + r] =
-                            make_float2(x.top[set][c], sum);
+                    for (int e = 0; e < N / 2; ++e) {
+                        o[2 * e] = v[e].x;
+                        o[2 * e + 1] = v[e].y;
+                    }
                 }
+                if (p.lse && g == 0)
+                    p.lse[(int64_t)row.token * p.heads + row.q_head] =
+                        sum == 0.f ? -CUDART_INF_F : (x.top[c] - kWeightLog2 + log2f(sum)) * CUDART_LN2_F;
+            } else {
+                float *o = p.parts + (slot * p.slot_rows + r) * DIM + N * g;
+#pragma unroll
+                for (int e = 0; e < N / 2; e += 2)
+                    *reinterpret_cast<float4 *>(o + 2 * e) = make_float4(x.out[e][c], x.out[e][2 + c],
+                                                                         x.out[e + 1][c], x.out[e + 1][2 + c]);
+                if (g == 0)
+                    reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * DIM)[slot * p.slot_rows + r] =
+                        make_float2(x.top[c], sum);
             }
+        }
     } while (next_piece(p, c, end));
 }
 
@@ -657,8 +631,8 @@ __global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM, R>::kCtas)
 // of the keys.
 constexpr int kJoinThreads8 = 256, kJoinSplit8 = 4;
 
-template <int DIM, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Attn8Params<ROWS> p, int ctas)
+template <int DIM>
+__global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Attn8Params p, int ctas)
 {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -680,11 +654,11 @@ __global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Att
     if (cut.parts == 0)
         return;
     const float2 *ml = reinterpret_cast<const float2 *>(p.parts + 2 * (int64_t)ctas * p.slot_rows * DIM);
-    const int rows = min(ROWS, cut.q_len * p.group - cut.q_tile * ROWS);
+    const int rows = min(p.kRows, cut.q_len * p.group - cut.q_tile * p.kRows);
     auto slot = [&](int i) { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
     for (int c = threadIdx.x + blockIdx.y * kJoinThreads8; c < rows * (DIM / 4); c += kJoinSplit8 * kJoinThreads8) {
         const int r = c / (DIM / 4), d = c % (DIM / 4) * 4;
-        const int row = cut.q_tile * ROWS + r, t = cut.q0 + row / p.group, h = cut.head * p.group + row % p.group;
+        const int row = cut.q_tile * p.kRows + r, t = cut.q0 + row / p.group, h = cut.head * p.group + row % p.group;
         float top = -CUDART_INF_F;
 #pragma unroll 4
         for (int i = 0; i < cut.parts; ++i)
@@ -722,10 +696,14 @@ __global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Att
 // ------------------------------------------------------------------ chunks: the cache widened first
 // Where sequences bring many rows a head, the keys and values that they see are written out in bf16 once, in pages of 64
 // tokens, and the tcgen05 attention of paged_attention.cu runs on those: it does 1.2 PFLOP/s where the registers' products
-// reach 0.15, and writing and reading 2 bytes an element instead of reading 1 costs what 64 rows cost there.  A code times a power of two is
+// reach 0.15; but writing and reading 2 bytes an element takes its time, and a launch more.  A code times a power of two is
 // a bf16 number, so K keeps its scales' powers of two, and their mantissas, in [1, 2), multiply the scores (rounded into K
 // they made three quarters of the result's error); V is rounded with its scale, as bf16 weights and outputs are.
-constexpr int kWideRows = 64;                // rows a sequence and head bring on average, at least
+// The rule counts the multiply-adds of all rows with all keys that the table has room for (a key's exponentials as 64 of
+// them): us in the registers and widened at 8 sequences x 16 tokens x 4000 keys (of 32 / 8 heads of 128) 40, 58; 8 x 32 x
+// 16000 175, 141; 8 x 64 x 8000 250, 135; 2 x 64 x 4000 54, 47; 1 x 300 x 1000 (16 / 8 heads) 30, 35.
+constexpr int kWideRows = 96;                // rows a sequence and head bring on average, at least
+constexpr double kWideWork = 1.3e10;         // and multiply-adds in all, times four
 constexpr int64_t kWideBytes = (int64_t)8 << 30;   // of scratch memory at most
 constexpr int kWideKeys = 64;                // tokens of a page of the copy
 
@@ -838,7 +816,7 @@ bool attention_fp8_shape_ok(int batch, int q_tokens, int heads, int kv_heads, in
 // Rows a part can have: a tile's, or all there are.
 int slot_rows_fp8(int q_tokens, int heads, int kv_heads)
 {
-    return (int)std::min<int64_t>(16 * kWarps, std::max<int64_t>(1, (int64_t)q_tokens * (heads / kv_heads)));
+    return (int)std::min<int64_t>(kWarps * kWarpRows, std::max<int64_t>(1, (int64_t)q_tokens * (heads / kv_heads)));
 }
 
 // (dim, place, head, page) view of a cache of codes; a box is one head's row of up to 64 places of a page, zeros outside.
@@ -862,20 +840,20 @@ lowm_status_t encode_codes(const void *base, int64_t page_stride, int64_t place_
                : LOWM_ERR_CUDA;
 }
 
-template <int DIM, int R>
-lowm_status_t launch_fp8(const CUtensorMap &map_k, const CUtensorMap &map_v, const Attn8Params<kWarps * R> &p, int sms, void *stream)
+template <int DIM>
+lowm_status_t launch_fp8(const CUtensorMap &map_k, const CUtensorMap &map_v, const Attn8Params &p, int sms, void *stream)
 {
     static SmemOptIn opt_in;
-    if (!opt_in.set(reinterpret_cast<const void *>(paged_attention_fp8_kernel<DIM, R>), Attn8Smem<DIM, R>::kBytes))
+    if (!opt_in.set(reinterpret_cast<const void *>(paged_attention_fp8_kernel<DIM>), Attn8Smem<DIM>::kBytes))
         return LOWM_ERR_CUDA;
-    const int ctas = std::min(Attn8Smem<DIM, R>::kCtas * sms, kMaxCtas);
+    const int ctas = std::min(Attn8Smem<DIM>::kCtas * sms, kMaxCtas);
     if (p.batch > 0) {
-        const lowm_status_t st = launch_pdl(paged_attention_fp8_kernel<DIM, R>, dim3((unsigned)ctas), dim3(kThreads8),
-                                            Attn8Smem<DIM, R>::kBytes, stream, map_k, map_v, p);
+        const lowm_status_t st = launch_pdl(paged_attention_fp8_kernel<DIM>, dim3((unsigned)ctas), dim3(kThreads8),
+                                            Attn8Smem<DIM>::kBytes, stream, map_k, map_v, p);
         if (st != LOWM_OK)
             return st;
     }
-    return launch_pdl(join_parts_fp8_kernel<DIM, kWarps * R>, dim3((unsigned)ctas, kJoinSplit8), dim3(kJoinThreads8), 0, stream, p,
+    return launch_pdl(join_parts_fp8_kernel<DIM>, dim3((unsigned)ctas, kJoinSplit8), dim3(kJoinThreads8), 0, stream, p,
                       ctas);
 }
 
@@ -900,7 +878,9 @@ int64_t wide_bytes(int batch, int kv_heads, int dim, int page_size, int table_wi
 // Whether a call widens the cache first.
 bool widens(int batch, int q_tokens, int heads, int kv_heads, int dim, int page_size, int table_width)
 {
-    return (int64_t)q_tokens * (heads / kv_heads) >= (int64_t)kWideRows * std::max(batch, 1) && table_width > 0 &&
+    const double keys = (double)wide_pages(page_size, table_width) * kWideKeys;
+    return (int64_t)q_tokens * (heads / kv_heads) >= (int64_t)kWideRows * std::max(batch, 1) &&
+           4.0 * q_tokens * heads * keys * (dim + 64) >= kWideWork &&
            2.0 * batch * wide_pages(page_size, table_width) * kWideKeys * kv_heads * dim * 2 <= (double)kWideBytes;
 }
 
@@ -979,7 +959,7 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
     // Tile counts are 32-bit in the kernels, rounding up to equal shares included.
     const int group = heads / kv_heads;
     const int64_t capacity = std::min<int64_t>((int64_t)table_width * page_size, kMaxKeys);
-    const int64_t q_tiles = (int64_t)q_tokens * group / (8 * kWarps) + batch;
+    const int64_t q_tiles = (int64_t)q_tokens * group / (kWarps * kWarpRows) + batch;
     if ((double)q_tiles * kv_heads * (double)(capacity / kTileKeys + 2 + kItemCost8) > (double)(INT_MAX - kMinShare8 * kMaxCtas))
         return LOWM_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
@@ -1051,53 +1031,44 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
                            &map_v)) != LOWM_OK)
         return st;
 
-    auto fill = [&](auto &p) {
-        p.q = static_cast<const __nv_bfloat16 *>(q);
-        p.out = static_cast<__nv_bfloat16 *>(out);
-        p.lse = lse;
-        p.q_ts = q_token_stride;
-        p.q_hs = q_head_stride;
-        p.o_ts = out_token_stride;
-        p.o_hs = out_head_stride;
-        p.k_scale = k_scale;
-        p.ks_page = ks_page_stride;
-        p.ks_block = ks_block_stride;
-        p.ks_head = ks_head_stride;
-        p.v_scale = v_scale;
-        p.vs_page = vs_page_stride;
-        p.vs_block = vs_block_stride;
-        p.vs_head = vs_head_stride;
-        p.table = page_table;
-        p.table_stride = page_table_stride;
-        p.num_pages = num_pages;
-        p.kv_lens = kv_lens;
-        p.cu_q = cu_q;
-        p.page_size = page_size;
-        p.page_shift = log2_of(page_size);
-        p.block_shift = log2_of(block);
-        p.batch = batch;
-        p.q_tokens = q_tokens;
-        p.heads = heads;
-        p.kv_heads = kv_heads;
-        p.group = group;
-        p.window = window < kMaxKeys ? window : 0;
-        p.capacity = (int)capacity;
-        p.slot_rows = slot_rows_fp8(q_tokens, heads, kv_heads);
-        p.scale_log2 = scale * 1.44269504088896340736f;
-        p.q_vec = is_aligned(q, 16) && !((q_token_stride | q_head_stride) & 7);
-        p.out_vec = is_aligned(out, 16) && !((out_token_stride | out_head_stride) & 7);
-        p.parts = static_cast<float *>(workspace);
-        p.cuts = reinterpret_cast<CutItem8 *>(static_cast<uint8_t *>(workspace) +
-                                              (size_t)2 * kMaxCtas * p.slot_rows * (dim + 2) * sizeof(float));
-        p.status = status;
-    };
-    // Rows that a sequence brings on average: few go to warps of 8 rows, two CTAs an SM.
-    if ((int64_t)q_tokens * group <= 32 * (int64_t)std::max(batch, 1)) {
-        Attn8Params<8 * kWarps> p;
-        fill(p);
-        return dim == 64 ? launch_fp8<64, 8>(map_k, map_v, p, sms, stream) : launch_fp8<128, 8>(map_k, map_v, p, sms, stream);
-    }
-    Attn8Params<16 * kWarps> p;
-    fill(p);
-    return dim == 64 ? launch_fp8<64, 16>(map_k, map_v, p, sms, stream) : launch_fp8<128, 16>(map_k, map_v, p, sms, stream);
+    Attn8Params p;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse = lse;
+    p.q_ts = q_token_stride;
+    p.q_hs = q_head_stride;
+    p.o_ts = out_token_stride;
+    p.o_hs = out_head_stride;
+    p.k_scale = k_scale;
+    p.ks_page = ks_page_stride;
+    p.ks_block = ks_block_stride;
+    p.ks_head = ks_head_stride;
+    p.v_scale = v_scale;
+    p.vs_page = vs_page_stride;
+    p.vs_block = vs_block_stride;
+    p.vs_head = vs_head_stride;
+    p.table = page_table;
+    p.table_stride = page_table_stride;
+    p.num_pages = num_pages;
+    p.kv_lens = kv_lens;
+    p.cu_q = cu_q;
+    p.page_size = page_size;
+    p.page_shift = log2_of(page_size);
+    p.block_shift = log2_of(block);
+    p.batch = batch;
+    p.q_tokens = q_tokens;
+    p.heads = heads;
+    p.kv_heads = kv_heads;
+    p.group = group;
+    p.window = window < kMaxKeys ? window : 0;
+    p.capacity = (int)capacity;
+    p.slot_rows = slot_rows_fp8(q_tokens, heads, kv_heads);
+    p.scale_log2 = scale * 1.44269504088896340736f;
+    p.q_vec = is_aligned(q, 16) && !((q_token_stride | q_head_stride) & 7);
+    p.out_vec = is_aligned(out, 16) && !((out_token_stride | out_head_stride) & 7);
+    p.parts = static_cast<float *>(workspace);
+    p.cuts = reinterpret_cast<CutItem8 *>(static_cast<uint8_t *>(workspace) +
+                                          (size_t)2 * kMaxCtas * p.slot_rows * (dim + 2) * sizeof(float));
+    p.status = status;
+    return dim == 64 ? launch_fp8<64>(map_k, map_v, p, sms, stream) : launch_fp8<128>(map_k, map_v, p, sms, stream);
 }

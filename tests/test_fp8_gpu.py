@@ -477,7 +477,7 @@ def check_attention(kv_lens, q_lens, heads, kv_heads, dim, page, block, window=0
         change(*cache, q)
     scale = dim ** -0.5 if scale is None else scale
     if wide is None:
-        wide = cu[-1] * (heads // kv_heads) >= 64 * max(len(kv_lens), 1)
+        wide = widened(len(kv_lens), cu[-1], heads, kv_heads, dim, page, cache[4].shape[1])
     want, tol, lse = attention64(q, *cache, kv_lens, cu_q, scale, window, wide)
     out, got = fp8.paged_attention_fp8(q, *cache, lens, cu_q, scale=scale, window=window, return_lse=True)
     bounded(out, want, tol, "attention")
@@ -487,6 +487,16 @@ def check_attention(kv_lens, q_lens, heads, kv_heads, dim, page, block, window=0
     assert float((got[ok] - lse[ok]).abs().max() if ok.any() else 0) <= 1e-3
     in_order()
     return out, cache
+
+
+def widened(batch, q_tokens, heads, kv_heads, dim, page, width):
+    """Whether the cache is widened to bf16 first: that takes other workspace than a table without room."""
+    size = lambda w: fp8.lowm_paged_attention_fp8_workspace(batch, q_tokens, heads, kv_heads, dim, page, w)   # noqa: E731
+    return size(width) != size(0)
+
+
+# A table with room for so many tokens makes a chunk's call worth widening; a narrow one does not.
+ROOM = 60000
 
 
 LENGTHS = [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 500]
@@ -513,12 +523,15 @@ def test_attention_windows_and_drafted_tokens(dim, window):
 @pytest.mark.parametrize("dim,heads,kv_heads", [(128, 8, 2), (64, 4, 4), (128, 4, 1)])
 @pytest.mark.parametrize("window", [0, 77])
 @pytest.mark.parametrize("block", [1, 16])
-def test_attention_of_chunks(dim, heads, kv_heads, window, block):
-    check_attention([400, 130, 700], [200, 130, 333], heads, kv_heads, dim, 32, block, window=window, seed=dim + window)
+@pytest.mark.parametrize("room", [None, ROOM])
+def test_attention_of_chunks(dim, heads, kv_heads, window, block, room):
+    lens, q_lens, width = [400, 130, 700], [200, 130, 333], room and room // 32
+    check_attention(lens, q_lens, heads, kv_heads, dim, 32, block, window=window, seed=dim + window, width=width, wide=bool(room))
+    assert widened(3, 663, heads, kv_heads, dim, 32, width or 22) == bool(room)
 
 
-def test_attention_of_chunks_without_room_to_widen():
-    # a table that could hold 2^27 tokens: the widened copy would pass the limit
+def test_attention_of_chunks_without_memory_to_widen():
+    # a table with room for 2^27 tokens: the widened copy would pass the limit
     lens, page = [300], 64
     kc, vc, ks, vs, table = make_cache(lens, page, 16, 2, 128, seed=3)
     wide = torch.zeros(1, 1 << 21, dtype=torch.int32, device="cuda")
@@ -532,13 +545,14 @@ def test_attention_of_chunks_without_room_to_widen():
 
 def test_attention_rows_that_see_nothing():
     # more new tokens than keys, no keys, no new tokens, rows behind the last sequence
-    for q_lens in ([5, 3, 0, 2], [100, 70, 0, 80]):
+    for q_lens, width in (([5, 3, 0, 2], None), ([100, 70, 0, 80], None), ([200, 170, 0, 180], ROOM // 16)):
         lens = [2, 0, 40, 60]
-        kc, vc, ks, vs, table = make_cache(lens, 16, 8, 2, 64, seed=1)
+        kc, vc, ks, vs, table = make_cache(lens, 16, 8, 2, 64, seed=1, width=width)
+        assert widened(4, sum(q_lens) + 3, 4, 2, 64, 16, table.shape[1]) == bool(width)
         cu = [sum(q_lens[:i]) for i in range(5)]
         q = rand(cu[-1] + 3, 4, 64, seed=2)
         cu_q = torch.tensor(cu, device="cuda", dtype=torch.int32)
-        want, tol, lse = attention64(q, kc, vc, ks, vs, table, lens, cu_q, 0.125, 0, q_lens[0] > 5)
+        want, tol, lse = attention64(q, kc, vc, ks, vs, table, lens, cu_q, 0.125, 0, bool(width))
         out, got = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, torch.tensor(lens, device="cuda", dtype=torch.int32), cu_q,
                                            scale=0.125, return_lse=True)
         bounded(out, want, tol, "attention")
@@ -555,8 +569,8 @@ def test_attention_of_an_empty_batch():
     assert fp8.paged_attention_fp8(rand(0, 4, 64), kc, vc, ks, vs, table[:0], none, cu).shape == (0, 4, 64)
 
 
-@pytest.mark.parametrize("q_lens", [[1, 1, 1], [9, 5, 7], [100, 90, 70]])
-def test_attention_what_no_row_sees_may_hold_anything(q_lens):
+@pytest.mark.parametrize("q_lens,width", [([1, 1, 1], None), ([9, 5, 7], None), ([100, 90, 70], None), ([100, 90, 70], ROOM // 64)])
+def test_attention_what_no_row_sees_may_hold_anything(q_lens, width):
     lens, page, block = [100, 130, 71], 64, 16
 
     def change(kc, vc, ks, vs, table, q):
@@ -570,20 +584,20 @@ def test_attention_what_no_row_sees_may_hold_anything(q_lens):
         free = [i for i in range(kc.shape[0]) if i not in table.flatten().tolist()]
         for c in (kc, vc):
             c.view(torch.uint8)[free] = 0xff
-    check_attention(lens, q_lens, 4, 2, 128, page, block, seed=5, change=change)
+    check_attention(lens, q_lens, 4, 2, 128, page, block, seed=5, change=change, width=width)
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("q_lens", [[1, 1], [6, 20], [120, 80]])
+@pytest.mark.parametrize("q_lens,width", [([1, 1], None), ([6, 20], None), ([120, 80], None), ([120, 80], ROOM // 32)])
 @pytest.mark.parametrize("window", [0, 30])
-def test_attention_nan_codes_reach_the_rows_that_see_them(dim, q_lens, window):
+def test_attention_nan_codes_reach_the_rows_that_see_them(dim, q_lens, window, width):
     lens, page = [200, 150], 32
 
     def change(kc, vc, ks, vs, table, q):
         for b, n in enumerate(lens):
             for key, d in ((n - 3, 5), (n - 15, 6), (n - q_lens[b], 7), (n - 40, 8), (2, 9)):
                 vc.view(torch.uint8)[int(table[b, key // page]), key % page, 0, d] = 0xff
-    out, _ = check_attention(lens, q_lens, 4, 2, dim, page, 8, window=window, seed=6, change=change)
+    out, _ = check_attention(lens, q_lens, 4, 2, dim, page, 8, window=window, seed=6, change=change, width=width)
     assert torch.isnan(out).any() and not torch.isnan(out).all()
 
 
@@ -605,14 +619,14 @@ def test_attention_nan_keys_and_queries():
 def test_attention_pages_outside_the_cache_read_as_zeros():
     def change(kc, vc, ks, vs, table, q):
         table[0, 1], table[1, 0] = -1, kc.shape[0]
-    for q_lens in ([1, 2], [80, 70]):
-        check_attention([150, 120], q_lens, 4, 2, 64, 32, 16, seed=8, change=change)
+    for q_lens, width in (([1, 2], None), ([80, 70], None), ([120, 110], ROOM // 32)):
+        check_attention([150, 120], q_lens, 4, 2, 64, 32, 16, seed=8, change=change, width=width)
 
 
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
-@pytest.mark.parametrize("q_lens", [[1, 4], [90, 70]])
-def test_attention_scales_of_scores(scale, q_lens):
-    check_attention([300, 100], q_lens, 4, 2, 64, 16, 8, scale=scale, seed=9)
+@pytest.mark.parametrize("q_lens,width", [([1, 4], None), ([190, 90], None), ([190, 90], ROOM // 16)])
+def test_attention_scales_of_scores(scale, q_lens, width):
+    check_attention([300, 100], q_lens, 4, 2, 64, 16, 8, scale=scale, seed=9, width=width)
 
 
 @pytest.mark.parametrize("block", [1, 16])
@@ -665,8 +679,8 @@ def test_attention_strides():
 
 
 def test_attention_repeats_its_bits():
-    for lens, q_lens in (([3000, 50, 1200], [1, 1, 1]), ([500, 300, 400], [200, 100, 90])):
-        kc, vc, ks, vs, table = make_cache(lens, 64, 16, 4, 128, seed=15)
+    for lens, q_lens, width in (([3000, 50, 1200], [1, 1, 1], None), ([500, 300, 400], [200, 100, 90], ROOM // 64)):
+        kc, vc, ks, vs, table = make_cache(lens, 64, 16, 4, 128, seed=15, width=width)
         cu = torch.tensor([0, q_lens[0], q_lens[0] + q_lens[1], sum(q_lens)], device="cuda", dtype=torch.int32)
         q, kv = rand(sum(q_lens), 16, 128, seed=16), torch.tensor(lens, device="cuda", dtype=torch.int32)
         first = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu)
@@ -677,7 +691,7 @@ def test_attention_repeats_its_bits():
 # ---------------------------------------------------------------------------- streams, graphs, refusals
 def test_streams_threads_and_graphs():
     lens = [700, 90, 300]
-    kc, vc, ks, vs, table = make_cache(lens, 32, 8, 2, 128, seed=17)
+    kc, vc, ks, vs, table = make_cache(lens, 32, 8, 2, 128, seed=17, width=ROOM // 32)
     kv = torch.tensor(lens, device="cuda", dtype=torch.int32)
     x, (w, sw) = rand(20, 512, seed=18), fp8.quantize_fp8(rand(768, 512, seed=19, std=0.05), 128)
 

@@ -716,7 +716,7 @@ struct WidenParams {
     __nv_bfloat16 *wide_k, *wide_v;          // [batch * pages][kv_heads][64][dim]
     float *factor;                           // [batch * pages][kv_heads][64]
     int32_t *wide_table;                     // [batch][pages]
-    int page_shift, block_shift, batch, q_tokens, kv_heads, dim, window, capacity, pages;
+    int page_shift, block_shift, batch, q_tokens, kv_heads, window, capacity, pages;
 };
 
 __device__ __forceinline__ void widen_16(uint4 codes, float scale, uint4 *to)
@@ -733,74 +733,60 @@ __device__ __forceinline__ void widen_16(uint4 codes, float scale, uint4 *to)
     to[1] = reinterpret_cast<const uint4 *>(out)[1];
 }
 
-// A CTA widens 64 tokens of a sequence at a time, 16 elements a thread.
+// A CTA widens one head of 64 tokens of a sequence at a time, 16 elements a thread and step.
 constexpr int kWidenThreads = 256;
 
+template <int DIM>
 __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams p)
 {
+    constexpr int kChunks = DIM / 16, kKeysAtOnce = kWidenThreads / kChunks, kSteps = kWideKeys / kKeysAtOnce;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int chunks = p.dim / 16, per_token = p.kv_heads * chunks, work = kWideKeys * per_token;
-    for (int64_t task = blockIdx.x; task < (int64_t)p.batch * p.pages; task += gridDim.x) {
-        const int b = (int)(task / p.pages), j = (int)(task - (int64_t)b * p.pages);
-        if (threadIdx.x == 0)
-            p.wide_table[task] = (int)task;
+    const int chunk = threadIdx.x % kChunks, mine = threadIdx.x / kChunks;
+    const int64_t tasks = (int64_t)p.batch * p.pages * p.kv_heads;
+    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const int64_t wide = task / p.kv_heads;                              // page of the copy
+        const int head = (int)(task - wide * p.kv_heads);
+        const int b = (int)(wide / p.pages), j = (int)(wide - (int64_t)b * p.pages);
+        if (threadIdx.x == 0 && head == 0)
+            p.wide_table[wide] = (int)wide;
         const int q0 = min(max(p.cu_q[b], 0), p.q_tokens), q_len = min(max(p.cu_q[b + 1], q0), p.q_tokens) - q0;
         const int kv = min(max(p.kv_lens[b], 0), p.capacity);
         const int first = p.window > 0 ? kv - q_len - p.window + 1 : 0;      // no row sees a key before it
         const int key0 = j * kWideKeys, end = min(kv, key0 + kWideKeys);
         if (q_len == 0 || key0 >= kv || key0 + kWideKeys <= first)
             continue;
-        // The scale of K: a power of two for the codes, and the rest (any number but those: the rest alone).
-        auto k_scale_of = [&](int64_t page, int key, int head, float &rest) {
-            const int block = (key & ((1 << p.page_shift) - 1)) >> p.block_shift;
-            const float a = p.k_scale[page * p.ks_page + block * p.ks_block + head * p.ks_head];
-            const uint32_t exponent = __float_as_uint(a) & 0x7f800000u;
-            const bool normal = exponent != 0 && exponent != 0x7f800000u;
-            rest = normal ? __uint_as_float((__float_as_uint(a) & 0x807fffffu) | 0x3f800000u) : a;
-            return normal ? __uint_as_float(exponent) : 1.f;
-        };
-        for (int i = threadIdx.x; i < p.kv_heads * kWideKeys; i += kWidenThreads) {
-            const int head = i / kWideKeys, key = key0 + i % kWideKeys;
-            float rest = 1.f;
-            if (key < end) {
-                const int64_t page = p.table[b * p.table_stride + (key >> p.page_shift)];
-                if (page >= 0 && page < p.num_pages)
-                    (void)k_scale_of(page, key, head, rest);
-            }
-            p.factor[(task * p.kv_heads + head) * kWideKeys + i % kWideKeys] = rest;
+        uint4 k[kSteps], v[kSteps];
+        float ks[kSteps], vs[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int key = key0 + u * kKeysAtOnce + mine;
+            k[u] = v[u] = make_uint4(0, 0, 0, 0);
+            ks[u] = vs[u] = 1.f;
+            if (key >= end)
+                continue;
+            const int64_t page = p.table[b * p.table_stride + (key >> p.page_shift)];
+            const int place = key & ((1 << p.page_shift) - 1), block = place >> p.block_shift;
+            if (page < 0 || page >= p.num_pages)                             // reads as zeros
+                continue;
+            k[u] = *reinterpret_cast<const uint4 *>(p.k + page * p.k_page + place * p.k_place + head * p.k_head + 16 * chunk);
+            v[u] = *reinterpret_cast<const uint4 *>(p.v + page * p.v_page + place * p.v_place + head * p.v_head + 16 * chunk);
+            ks[u] = p.k_scale[page * p.ks_page + block * p.ks_block + head * p.ks_head];
+            vs[u] = p.v_scale[page * p.vs_page + block * p.vs_block + head * p.vs_head];
         }
-        for (int i0 = threadIdx.x; i0 < work; i0 += 4 * kWidenThreads) {
-            uint4 k[4], v[4];
-            float ks[4], vs[4];
-            int64_t to[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * kWidenThreads, key = key0 + i / per_token;
-                to[u] = -1;
-                if (i >= work || key >= end)
-                    continue;
-                const int head = i % per_token / chunks, chunk = i % chunks;
-                const int64_t page = p.table[b * p.table_stride + (key >> p.page_shift)];
-                const int place = key & ((1 << p.page_shift) - 1), block = place >> p.block_shift;
-                to[u] = ((task * p.kv_heads + head) * kWideKeys + (key - key0)) * p.dim + 16 * chunk;
-                if (page < 0 || page >= p.num_pages) {
-                    k[u] = v[u] = make_uint4(0, 0, 0, 0);
-                    ks[u] = vs[u] = 0.f;
-                } else {
-                    k[u] = *reinterpret_cast<const uint4 *>(p.k + page * p.k_page + place * p.k_place + head * p.k_head + 16 * chunk);
-                    v[u] = *reinterpret_cast<const uint4 *>(p.v + page * p.v_page + place * p.v_place + head * p.v_head + 16 * chunk);
-                    float rest;
-                    ks[u] = k_scale_of(page, key, head, rest);
-                    vs[u] = fminf(fmaxf(p.v_scale[page * p.vs_page + block * p.vs_block + head * p.vs_head], 1.f / kMaxScale), kMaxScale);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (to[u] >= 0) {
-                    widen_16(k[u], ks[u], reinterpret_cast<uint4 *>(p.wide_k + to[u]));
-                    widen_16(v[u], vs[u], reinterpret_cast<uint4 *>(p.wide_v + to[u]));
-                }
+        for (int u = 0; u < kSteps; ++u) {
+            const int key = u * kKeysAtOnce + mine;
+            // The scale of K: a power of two for the codes, and the rest (any number but those: the rest alone).
+            const uint32_t bits = __float_as_uint(ks[u]), exponent = bits & 0x7f800000u;
+            const bool normal = exponent != 0 && exponent != 0x7f800000u;
+            if (chunk == 0)
+                p.factor[task * kWideKeys + key] = normal ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u) : ks[u];
+            if (key0 + key >= end)
+                continue;
+            const int64_t to = (task * kWideKeys + key) * DIM + 16 * chunk;
+            widen_16(k[u], normal ? __uint_as_float(exponent) : 1.f, reinterpret_cast<uint4 *>(p.wide_k + to));
+            widen_16(v[u], fminf(fmaxf(vs[u], 1.f / kMaxScale), kMaxScale), reinterpret_cast<uint4 *>(p.wide_v + to));
         }
     }
 }
@@ -1000,7 +986,6 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
         w.batch = batch;
         w.q_tokens = q_tokens;
         w.kv_heads = kv_heads;
-        w.dim = dim;
         w.window = window < kMaxKeys ? window : 0;
         w.capacity = (int)capacity;
         w.pages = (int)wide_pages(page_size, table_width);
@@ -1013,7 +998,8 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
         w.wide_table = reinterpret_cast<int32_t *>(at + tables);
         const size_t used = tables + wide_table_bytes(batch, page_size, table_width);
         const int64_t tasks = (int64_t)batch * w.pages, head = (int64_t)kWideKeys * dim;
-        st = launch_pdl(widen_kernel, dim3((unsigned)std::min<int64_t>(tasks, 8 * sms)), dim3(kWidenThreads), 0, stream, w);
+        st = launch_pdl(dim == 64 ? widen_kernel<64> : widen_kernel<128>, dim3((unsigned)std::min<int64_t>(tasks * kv_heads, 16 * sms)),
+                        dim3(kWidenThreads), 0, stream, w);
         if (st != LOWM_OK)
             return st;
         return attend_pages(q, q_token_stride, q_head_stride, w.wide_k, kv_heads * head, dim, head, w.wide_v, kv_heads * head, dim,

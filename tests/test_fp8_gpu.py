@@ -448,7 +448,11 @@ def attention64(q, kc, vc, ks, vs, table, kv_lens, cu_q, scale, window, wide):
             # rounding (fp16; with the cache widened bf16, and V's values by a rounding more) and by the hardware's exponential.
             ds = ((dim + 16) * 2 * E * torch.where(seen, size, 0.0)).amax(1, keepdim=True).nan_to_num() + 2.0 ** -20
             weight = 2 * ds + (2 * U if wide else H) + 16 * E
-            tol[q0:q1, h] = U * out[q0:q1, h].abs().nan_to_num() + weight * (w @ vh.abs()) + 1e-37
+            # What a weight meets V with, w_j b_j (b_j: the scale of V), is at most 2^15 and at least 2^8 where it is the largest,
+            # and fp16 numbers are 2^-24 apart below 2^-14: off by 2^-25 at most, 2^-33 of the largest, times a code.
+            b_j = torch.where(inside, vs[pg, place // block, g].to(F64), 1.0)
+            faint = 2.0 ** -33 * (w * b_j).amax(1, keepdim=True) * (seen.to(F64) @ (vh / b_j[:, None]).abs())
+            tol[q0:q1, h] = U * out[q0:q1, h].abs().nan_to_num() + weight * (w @ vh.abs()) + faint + 1e-37
             lse[q0:q1, h] = torch.where(some, s.amax(1).nan_to_num(neginf=0.0) + l[:, 0].clamp(min=1e-300).log(), -math.inf)
     return out, tol, lse
 

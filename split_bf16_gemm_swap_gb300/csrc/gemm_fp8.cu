@@ -94,14 +94,26 @@ __device__ __forceinline__ uint32_t cluster_size()
     return n;
 }
 
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
 {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
+    if constexpr (N == 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr)
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+              "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+              "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(taddr)
+            : "memory");
 }
 
 // A place in a ring and the parity of its phase, without a division a step (two of them took 200 of a stage's 1000 cycles).
@@ -141,19 +153,28 @@ struct FourRows {
     __device__ __forceinline__ void store(uint8_t *block, float *scales, int row0, float w) const
     {
         const int lane = threadIdx.x & 31;
+        uint32_t top[4];                     // bits of the largest magnitudes (which order as these do)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            top[r] = __vmaxu2(v[r].x & 0x7fff7fffu, v[r].y & 0x7fff7fffu);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            top[r] = __reduce_max_sync(0xffffffffu, max(top[r] << 16, top[r] & 0xffff0000u));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v[r].x));
-            const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v[r].y));
-            float amax = fmaxf(fmaxf(finite_magnitude(a.x), finite_magnitude(a.y)), fmaxf(finite_magnitude(b.x), finite_magnitude(b.y)));
-            // (magnitudes order as their bits do)
-            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-            const int e = scale_exponent(amax);
+            float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v[r].x));
+            float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v[r].y));
+            if (top[r] >= 0x7f800000u) {     // not all are finite
+                const float m = fmaxf(fmaxf(finite_magnitude(a.x), finite_magnitude(a.y)),
+                                      fmaxf(finite_magnitude(b.x), finite_magnitude(b.y)));
+                top[r] = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+                a = make_float2(nan_unless_finite(a.x), nan_unless_finite(a.y));
+                b = make_float2(nan_unless_finite(b.x), nan_unless_finite(b.y));
+            }
+            const int e = scale_exponent(__uint_as_float(top[r])), row = row0 + r;
             const float inverse = power_of_two(-e);
-            const uint32_t word = to_e4m3x2(nan_unless_finite(a.x) * inverse, nan_unless_finite(a.y) * inverse) |
-                                  to_e4m3x2(nan_unless_finite(b.x) * inverse, nan_unless_finite(b.y) * inverse) << 16;
-            const int row = row0 + r;
-            *reinterpret_cast<uint32_t *>(block + row * kBlock + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) = word;
+            *reinterpret_cast<uint32_t *>(block + row * kBlock + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) =
+                to_e4m3x2(a.x * inverse, a.y * inverse) | to_e4m3x2(b.x * inverse, b.y * inverse) << 16;
             if (lane == 0)
                 scales[row] = power_of_two(e) * w;
         }
@@ -175,8 +196,8 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD, QUANT>::kThreads, M_PAD > 32
                    bar_scales = bar_mail + 8, slot = bar_scales + 8 * kMaxScales;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ranks = (int)cluster_size(), rank = (int)ptx::cluster_ctarank();
-    const int n0 = (int)(blockIdx.x / ranks) * kTileN;
-    // This rank's stages of K, and its share of the tokens.
+    // A cluster has a tile; CTAs on their own have every gridDim-th one.  This rank's stages of K, and its share of the tokens.
+    const int first_tile = (int)(blockIdx.x / ranks), tile_step = (int)(gridDim.x / ranks), tiles = (p.N + kTileN - 1) / kTileN;
     const int all = (p.blocks + p.per_stage - 1) / p.per_stage;
     const int begin = (int)((int64_t)all * rank / ranks), end = (int)((int64_t)all * (rank + 1) / ranks);
     const int buffers = kBuffers / p.per_stage;              // stages' sums in TMEM
@@ -244,103 +265,107 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD, QUANT>::kThreads, M_PAD > 32
         if (lane == 0) {
             ptx::prefetch_tensormap(&map_w);
             for (int i = 0; i < early; ++i)
-                load(&map_w, ring + i * stage_bytes, S::kWBytes, n0, begin + i, bar_full + 8 * i, policy);
+                load(&map_w, ring + i * stage_bytes, S::kWBytes, first_tile * kTileN, begin + i, bar_full + 8 * i, policy);
             // Without it the ring's W is requested into L2, where a later write would find it.
             for (int i = early; i < min(p.stages, end - begin) && p.planes; ++i)
-                ptx::tma_prefetch_3d(&map_w, 0, n0, (begin + i) * p.per_stage);
+                ptx::tma_prefetch_3d(&map_w, 0, first_tile * kTileN, (begin + i) * p.per_stage);
         }
         ptx::griddep_wait();
         RingPlace r;
-        int i = begin;
-        for (; i < end; ++i, r.step(p.stages)) {
-            if (i - begin < early)
-                continue;
-            wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
-            if (!ok)
-                break;
-            if (lane == 0)
-                load(&map_w, ring + r.at * stage_bytes, S::kWBytes, n0, i, bar_full + 8 * r.at, policy);
-            __syncwarp();
-        }
+        for (int tile = first_tile; tile < tiles && ok; tile += tile_step)
+            for (int i = begin; i < end; ++i, r.step(p.stages)) {
+                if (tile == first_tile && i - begin < early)
+                    continue;
+                wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
+                if (!ok)
+                    break;
+                if (lane == 0)
+                    load(&map_w, ring + r.at * stage_bytes, S::kWBytes, tile * kTileN, i, bar_full + 8 * r.at, policy);
+                __syncwarp();
+            }
         ptx::griddep_launch_dependents();
     } else if (warp >= S::kLoadWarp) {
         // ------------------------------------------------------------ A and the scales
         RingPlace r, q;                      // of the ring, of the scales
-        const float *w_scale = p.w_scale + (int64_t)(n0 / kTileN) * p.blocks + begin * p.per_stage;
-        int left = min(p.blocks - begin * p.per_stage, (end - begin) * p.per_stage);            // K blocks
-        if constexpr (QUANT) {
-            const int row0 = 4 * (warp - S::kLoadWarp);
-            ptx::griddep_wait();
-            FourRows x;
-            int column = begin * p.per_stage * kBlock + 4 * lane;
-            float w = 0.f;
-            if (left > 0) {
-                x.load(p, row0, column);
-                w = *w_scale++;
-            }
-            for (int i = begin; i < end; ++i, r.step(p.stages), q.step(scale_slots)) {
-                wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
-                if (!ok)
-                    break;
-                uint8_t *block = smem + kRingAt + r.at * stage_bytes + a_at;
-                float *scales = reinterpret_cast<float *>(smem + scales_at + q.at * scale_stage);
-                for (int b = 0; b < p.per_stage && left > 0; ++b, block += S::kABytes, scales += M_PAD) {
-                    const FourRows now = x;
-                    const float scale = w;
-                    column += kBlock;
-                    if (--left > 0) {        // the next block's
-                        x.load(p, row0, column);
-                        w = *w_scale++;
-                    }
-                    now.store(block, scales, row0, scale);
-                }
-                ptx::fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::mbar_arrive(bar_full + 8 * r.at);
-                    ptx::mbar_arrive(bar_scales + 8 * q.at);
-                }
-            }
-        } else {
-            const uint64_t policy = ptx::policy_evict_last();
-            if (lane == 0)
-                ptx::prefetch_tensormap(&map_a);
-            ptx::griddep_wait();
-            // This lane's tokens' scales (a token past the last counts 0).
-            constexpr int kEach = (M_PAD + 31) / 32;
-            const float *a_scale[kEach];
-            float next[kEach], w = 0.f;      // the next block's
-            auto fetch = [&]() {
+        ptx::griddep_wait();
+        for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
+            const float *w_scale = p.w_scale + (int64_t)tile * p.blocks + begin * p.per_stage;
+            int left = min(p.blocks - begin * p.per_stage, (end - begin) * p.per_stage);            // K blocks
+            if constexpr (QUANT) {
+                // A stage's rows (two blocks at most) are requested while those of the stage before are quantised.
+                const int row0 = 4 * (warp - S::kLoadWarp);
+                FourRows x[2];
+                float w[2] = {};
+                int column = begin * p.per_stage * kBlock + 4 * lane;
+                auto fetch = [&]() {
 #pragma unroll
-                for (int k = 0; k < kEach; ++k)
-                    next[k] = lane + 32 * k < p.M ? *a_scale[k]++ : 0.f;
-                w = *w_scale++;
-            };
-#pragma unroll
-            for (int k = 0; k < kEach; ++k)
-                a_scale[k] = p.a_scale + (int64_t)min(lane + 32 * k, p.M - 1) * p.blocks + begin * p.per_stage;
-            if (left > 0)
+                    for (int b = 0; b < 2; ++b)
+                        if (b < p.per_stage && left > 0) {
+                            x[b].load(p, row0, column);
+                            w[b] = *w_scale++;
+                            column += kBlock;
+                            --left;
+                        }
+                };
                 fetch();
-            for (int i = begin; i < end; ++i, r.step(p.stages), q.step(scale_slots)) {
-                const uint32_t bar = bar_full + 8 * r.at;
-                wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
-                if (!ok)
-                    break;
-                if (lane == 0)
-                    load(&map_a, ring + r.at * stage_bytes + a_at, S::kABytes, 0, i, bar, policy);
-                __syncwarp();
-                float *scales = reinterpret_cast<float *>(smem + scales_at + q.at * scale_stage);
-                for (int b = 0; b < p.per_stage && left > 0; ++b, scales += M_PAD) {
+                for (int i = begin; i < end; ++i, r.step(p.stages), q.step(scale_slots)) {
+                    wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
+                    if (!ok)
+                        break;
+                    const FourRows now[2] = {x[0], x[1]};
+                    const float scale[2] = {w[0], w[1]};
+                    const int n = min(p.per_stage, p.blocks - i * p.per_stage);
+                    fetch();
+                    uint8_t *block = smem + kRingAt + r.at * stage_bytes + a_at;
+                    float *scales = reinterpret_cast<float *>(smem + scales_at + q.at * scale_stage);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        if (b < n)
+                            now[b].store(block + b * S::kABytes, scales + b * M_PAD, row0, scale[b]);
+                    ptx::fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(bar_full + 8 * r.at);
+                        ptx::mbar_arrive(bar_scales + 8 * q.at);
+                    }
+                }
+            } else {
+                const uint64_t policy = ptx::policy_evict_last();
+                // This lane's tokens' scales (a token past the last counts 0).
+                constexpr int kEach = (M_PAD + 31) / 32;
+                const float *a_scale[kEach];
+                float next[kEach], w = 0.f;  // the next block's
+                auto fetch = [&]() {
 #pragma unroll
                     for (int k = 0; k < kEach; ++k)
-                        if (lane + 32 * k < M_PAD)
-                            scales[lane + 32 * k] = next[k] * w;
-                    if (--left > 0)
-                        fetch();
+                        next[k] = lane + 32 * k < p.M ? *a_scale[k]++ : 0.f;
+                    w = *w_scale++;
+                };
+#pragma unroll
+                for (int k = 0; k < kEach; ++k)
+                    a_scale[k] = p.a_scale + (int64_t)min(lane + 32 * k, p.M - 1) * p.blocks + begin * p.per_stage;
+                if (left > 0)
+                    fetch();
+                for (int i = begin; i < end; ++i, r.step(p.stages), q.step(scale_slots)) {
+                    wait(bar_empty + 8 * r.at, r.phase ^ 1, kErrGemm8Ring);
+                    if (!ok)
+                        break;
+                    if (lane == 0)
+                        load(&map_a, ring + r.at * stage_bytes + a_at, S::kABytes, 0, i, bar_full + 8 * r.at, policy);
+                    __syncwarp();
+                    float *scales = reinterpret_cast<float *>(smem + scales_at + q.at * scale_stage);
+                    for (int b = 0; b < p.per_stage && left > 0; ++b, scales += M_PAD) {
+#pragma unroll
+                        for (int k = 0; k < kEach; ++k)
+                            if (lane + 32 * k < M_PAD)
+                                scales[lane + 32 * k] = next[k] * w;
+                        if (--left > 0)
+                            fetch();
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(bar_scales + 8 * q.at);
                 }
-                __syncwarp();
-                if (lane == 0)
-                    ptx::mbar_arrive(bar_scales + 8 * q.at);
             }
         }
     } else if (warp == 1) {
@@ -348,6 +373,7 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD, QUANT>::kThreads, M_PAD > 32
         constexpr uint32_t kIdesc = make_idesc_e4m3(kTileN, M_PAD);
         const uint32_t base = uniform(tmem);
         RingPlace r, d;                      // of the ring, of the buffers
+        for (int tile = first_tile; tile < tiles && ok; tile += tile_step)
         for (int i = begin; i < end && ok; ++i, r.step(p.stages), d.step(buffers)) {
             wait(bar_full + 8 * r.at, r.phase, kErrGemm8Full);
             const int n = min(p.per_stage, p.blocks - i * p.per_stage);
@@ -377,60 +403,77 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD, QUANT>::kThreads, M_PAD > 32
         // ------------------------------------------------------------ sums: thread = row of W = TMEM lane
         const int column0 = (warp - 2) / 4 * S::kColumns;
         const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + column0;
-        // 16 tokens at a time, the next ones on their way while these are multiplied (the last ones of a block: the next
-        // block's first).
+        // kAtOnce tokens at a time, the next ones on their way while these are multiplied (the last ones of a stage: the next
+        // stage's first).
+        constexpr int kAtOnce = M_PAD < 64 ? 16 : 32, kPieces = S::kColumns / kAtOnce;
         RingPlace q, d;                      // of the scales, of the buffers
-        uint32_t v[2][16];
-        const float *last = nullptr;         // scales of the block before
-        auto multiply = [&](const uint32_t (&x)[16], const float *scales, int c0) {
+        uint32_t v[2][kAtOnce];
+        auto multiply = [&](const uint32_t (&x)[kAtOnce], const float *scales, int c0) {
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) {
+            for (int c = 0; c < kAtOnce; c += 4) {
                 const float4 a = *reinterpret_cast<const float4 *>(scales + column0 + c0 + c);
                 uint64_t *to = acc + (c0 + c) / 2;
                 to[0] = fma2(pack2(x[c], x[c + 1]), pack2(a.x, a.y), to[0]);
                 to[1] = fma2(pack2(x[c + 2], x[c + 3]), pack2(a.z, a.w), to[1]);
             }
         };
-        auto give_back = [&](uint32_t bar) {
-            __syncwarp();
-            if (lane == 0)
-                ptx::mbar_arrive(bar);
-        };
-        for (int i = begin; i < end && ok; ++i, q.step(scale_slots), d.step(buffers)) {
-            wait(bar_sums + 8 * d.at, d.phase, kErrGemm8Sums);
-            if (ok)
-                wait(bar_scales + 8 * q.at, q.phase, kErrGemm8Full);
-            if (!ok)
-                break;
-            ptx::tcgen05_fence_after_thread_sync();
-            const int n = min(p.per_stage, p.blocks - i * p.per_stage);
-            const float *scales = reinterpret_cast<const float *>(smem + scales_at + q.at * scale_stage);
-            uint32_t at = from + d.at * p.per_stage * M_PAD;
-            for (int b = 0; b < n; ++b, scales += M_PAD, at += M_PAD) {
+        for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
+            const float *last = nullptr;     // scales of the tokens in v[1], the last ones of their block
+            for (int i = begin; i < end && ok; ++i, q.step(scale_slots), d.step(buffers)) {
+                // Both at once: each takes 200 cycles, passed or not.
+                const bool sums = mbar_try_wait_for(bar_sums + 8 * d.at, d.phase, 1000000u);
+                const bool known = mbar_try_wait_for(bar_scales + 8 * q.at, q.phase, 1000000u);
+                if (!__all_sync(0xffffffffu, sums && known)) {
+                    wait(bar_sums + 8 * d.at, d.phase, kErrGemm8Sums);
+                    if (ok)
+                        wait(bar_scales + 8 * q.at, q.phase, kErrGemm8Full);
+                    if (!ok)
+                        break;
+                }
+                ptx::tcgen05_fence_after_thread_sync();
+                const int n = min(p.per_stage, p.blocks - i * p.per_stage);
+                const float *scales = reinterpret_cast<const float *>(smem + scales_at + q.at * scale_stage);
+                const uint32_t at = from + d.at * p.per_stage * M_PAD;
 #pragma unroll
-                for (int c = 0; c < S::kColumns; c += 16) {
-                    tmem_ld_x16(at + c, v[c / 16 & 1]);
-                    if (S::kColumns > 16) {
-                        if (c > 0)
-                            multiply(v[~(c / 16) & 1], scales, c - 16);
-                        else if (last)
-                            multiply(v[1], last, S::kColumns - 16);
-                    }
-                    if (c + 16 < S::kColumns)
-                        ptx::tmem_wait_ld();
+                for (int k = 0; k < 2 * kPieces; ++k) {              // (two blocks a stage at most)
+                    constexpr int kLast = (kPieces - 1) * kAtOnce;
+                    const int b = k / kPieces, c0 = k % kPieces * kAtOnce;
+                    if (b >= n)
+                        break;
+                    tmem_ld<kAtOnce>(at + b * M_PAD + c0, v[k & 1]);
+                    if (k > 0)
+                        multiply(v[~k & 1], scales + (k - 1) / kPieces * M_PAD, (k - 1) % kPieces * kAtOnce);
+                    else if (last)
+                        multiply(v[1], last, kLast);
+                    ptx::tmem_wait_ld();
                 }
-                last = scales;
-                ptx::tmem_wait_ld();
-                if (b + 1 == n) {
-                    ptx::tcgen05_fence_before_thread_sync();
-                    give_back(bar_free + 8 * d.at);
+                ptx::tcgen05_fence_before_thread_sync();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(bar_free + 8 * d.at);
+                if ((n * kPieces) & 1) {     // they are in v[0], where the next ones come
+                    multiply(v[0], scales + (n - 1) * M_PAD, (kPieces - 1) * kAtOnce);
+                    last = nullptr;
+                } else {
+                    last = scales + (n - 1) * M_PAD;
                 }
-                if constexpr (S::kColumns == 16)
-                    multiply(v[0], scales, 0);
             }
+            if (last && ok)
+                multiply(v[1], last, (kPieces - 1) * kAtOnce);
+            const int n0 = tile * kTileN, row = 32 * (warp & 3) + lane;
+            if (ranks > 1 || !ok)
+                break;
+#pragma unroll
+            for (int c = 0; c < S::kColumns; ++c) {
+                if (column0 + c < p.M && n0 + row < p.N) {
+                    const float2 x = unpack2(acc[c / 2]);
+                    p.c[(int64_t)(column0 + c) * p.N + n0 + row] = __float2bfloat16_rn(c & 1 ? x.y : x.x);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < S::kColumns / 2; ++c)
+                acc[c] = 0;
         }
-        if (S::kColumns > 16 && last && ok)
-            multiply(v[1], last, S::kColumns - 16);
     }
     __syncwarp();
     ptx::tcgen05_fence_before_thread_sync();
@@ -447,17 +490,9 @@ __global__ void __launch_bounds__(Gemm8Shape<M_PAD, QUANT>::kThreads, M_PAD > 32
     const int column0 = (warp - 2) / 4 * S::kColumns;
     const int row = 32 * (warp & 3) + lane;
     const bool sums = warp >= 2 && warp < S::kLoadWarp;
-    if (ranks == 1) {
-        if (sums && n0 + row < p.N) {
-#pragma unroll
-            for (int c = 0; c < S::kColumns; ++c)
-                if (column0 + c < p.M) {
-                    const float2 x = unpack2(acc[c / 2]);
-                    p.c[(int64_t)(column0 + c) * p.N + n0 + row] = __float2bfloat16_rn(c & 1 ? x.y : x.x);
-                }
-        }
+    if (ranks == 1)
         return;
-    }
+    const int n0 = first_tile * kTileN;
     // Rank q's mailbox: [source rank][128 rows][its tokens], four tokens at a place that depends on the row, so that
     // neighbouring rows' are on different banks.  Each rank's barrier counts the bytes that it waits for.
     if (!p.apart)
@@ -656,7 +691,8 @@ lowm_status_t launch_gemm_fp8(const void *A, const void *W, Gemm8Params &p, int 
         return LOWM_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3((unsigned)(tiles * split));
+    // CTAs on their own keep their SM, so that the next tile's loads do not wait for this one's end.
+    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min(tiles, (two ? 2 : 1) * sms)));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);

@@ -2,17 +2,28 @@
 // quantisation that feeds it.
 //
 // C^T tiles: N lies on the MMA's M (128 rows of W, one block row of its scales),
-// the few tokens on its N.  A CTA streams its share of K for one tile: a TMA warp
-// fills a ring of K blocks (128 bytes a row, 128-byte swizzled) of W and A, one
-// thread issues four tcgen05.mma (kind::f8f6f4, K = 32) a block into one of a ring
-// of TMEM buffers, and the epilogue warps add the block's sums, times the block's
-// two scales, to fp32 sums in registers.  So a block's products are summed by the
-// tensor cores and blocks in fp32, which the scales require anyway.
+// the few tokens on its N.  A CTA streams its share of K for a tile: a TMA warp
+// fills a ring of W, another (or four that quantise bf16 rows on the way) of A and
+// of the scales, each token's times the tile's; one thread issues four tcgen05.mma
+// (kind::f8f6f4, K = 32) a block of 128 into one of a ring of TMEM buffers, and the
+// epilogue warps multiply the block's sums by its scales and add them to fp32 sums
+// in registers.  So a block's products are summed by the tensor cores and blocks in
+// fp32, which scales of any size require anyway.
 //
-// K is split over the CTAs of a cluster where the tiles alone would leave SMs
-// idle.  They exchange their sums through distributed shared memory, the drained
-// ring serving as mailbox: rank q adds those of its share of the tokens, in the
-// order of the ranks, and stores them.
+// Where the tiles alone would leave SMs idle K is split over the CTAs of a cluster.
+// They exchange their sums by asynchronous stores into distributed shared memory (at
+// 64 tokens and more into the drained ring): rank q adds those of its share of the
+// tokens, in the order of the ranks, and stores them.  Else a CTA keeps its SM and
+// has every so manieth tile.
+//
+// What bounds it.  Few tokens: the bandwidth of W (4 tokens, N 49152, K 4096: 34 us,
+// 88 % of the copy rate) and, with few tiles, the chain from the launch to the first
+// block and from the last to the exchange (N 6144: 6.7 us, floor 3.7).  128 tokens: the
+// epilogue, 128 x 128 sums a block (N 49152: 46.6 us, floor 31.8).  What a step was
+// worth: no divisions for the ring's places (a stage 1000 -> 800 cycles), two blocks a
+// copy, scales on a ring of their own, so that W's stages come back with the MMAs (64
+// tokens 73 -> 45 us), 32 sums a tcgen05.ld and the stage's two waits at once (128
+// tokens 59 -> 47 us).  Sixteen epilogue warps instead of eight lost (69 us for 62).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -649,16 +660,22 @@ lowm_status_t encode_matrix(const void *base, int rows, int K, int box_rows, int
 
 constexpr int kSmem = 227 * 1024;
 
+// Ranks along K as long as the CTAs find an SM, or, with up to 16 tokens, half of one (us at N 6144, K 4096, split 1, 2, 4: 4
+// tokens 10.1, 7.4, 6.6; 32 tokens 11.9, 9.3, 9.7; 64 tokens 13.4, 11.4, 18.7; 128 tokens 18.5, 15.6, 26.5).
+int split_of(int m_pad, int tiles, int blocks, int sms)
+{
+    int split = 1;
+    while (split < std::min(m_pad / 4, kMaxSplit) && tiles * split * 2 <= (m_pad <= 16 ? 2 : 1) * sms && blocks >= 4 * split)
+        split *= 2;
+    return split;
+}
+
 template <int M_PAD, bool QUANT>
 lowm_status_t launch_gemm_fp8(const void *A, const void *W, Gemm8Params &p, int sms, void *stream)
 {
     using S = Gemm8Shape<M_PAD, QUANT>;
     const int tiles = (p.N + kTileN - 1) / kTileN;
-    // Ranks along K as long as the CTAs find an SM, or, with up to 16 tokens, half of one (us at N 6144, K 4096, split 1, 2, 4:
-    // 4 tokens 10.1, 7.4, 6.6; 32 tokens 11.9, 9.3, 9.7; 64 tokens 13.4, 11.4, 18.7; 128 tokens 18.5, 15.6, 26.5).
-    int split = 1;
-    while (split < std::min(M_PAD / 4, kMaxSplit) && tiles * split * 2 <= (M_PAD <= 16 ? 2 : 1) * sms && p.blocks >= 4 * split)
-        split *= 2;
+    const int split = split_of(M_PAD, tiles, p.blocks, sms);
     // Two CTAs an SM hide each other's ends (4 tokens, N 49152: 37.7 -> 36.2 us); more tokens take an SM's registers.
     const bool two = M_PAD <= 32 && tiles * split > sms;
     // A copy costs much the same whatever its size (K blocks a copy 1, 2: 4 tokens, N 49152 48.1, 37.7 us).
@@ -738,8 +755,17 @@ lowm_status_t launch_codes(const void *A, const void *W, Gemm8Params &p, int sms
                        : launch_gemm_fp8<128, false>(A, W, p, sms, stream);
 }
 
-// Up to 16 tokens are quantised by the GEMM itself, a CTA its share of them; more by a kernel before it.
-constexpr int kQuantTokens = 16;
+// Up to 16 tokens are quantised by the GEMM itself, every CTA its share of K for each of its tiles: 0.2 us a K block that
+// way, against a launch of its own (us inside, apart: N 6144, K 4096, 8 blocks a CTA 8.3, 10.1; N 2304, K 12288, 24 blocks
+// 14.4, 11.6; N 49152, K 4096, 64 and 32 blocks 40.0, 35.4).  More tokens are too much for it.
+constexpr int kQuantTokens = 16, kQuantBlocks = 12;
+
+bool quantises_inside(const Gemm8Params &p, int sms)
+{
+    const int tiles = (p.N + kTileN - 1) / kTileN, split = split_of(16, tiles, p.blocks, sms);
+    const int64_t turns = ((int64_t)tiles * split + 2 * sms - 1) / (2 * sms);
+    return p.M <= kQuantTokens && turns * ((p.blocks + split - 1) / split) <= kQuantBlocks;
+}
 
 size_t code_bytes(int M, int K) { return ((size_t)M * K + 15) / 16 * 16; }
 
@@ -797,7 +823,7 @@ extern "C" size_t lowm_gemm_fp8_bf16_workspace(int M, int K)
     using namespace lowm;
     if (M <= 0 || M > 128 || K <= 0 || K % 16)
         return 0;
-    return M <= kQuantTokens ? 16 : code_bytes(M, K) + (size_t)M * ((K + kBlock - 1) / kBlock) * sizeof(float);
+    return code_bytes(M, K) + (size_t)M * ((K + kBlock - 1) / kBlock) * sizeof(float);
 }
 
 extern "C" lowm_status_t lowm_gemm_fp8_bf16(const void *x, int64_t x_stride, const void *W, const float *w_scale, void *C, int M,
@@ -818,7 +844,7 @@ extern "C" lowm_status_t lowm_gemm_fp8_bf16(const void *x, int64_t x_stride, con
     p.status = host_status_word();
     if (!p.status)
         return LOWM_ERR_CUDA;
-    if (M <= kQuantTokens) {
+    if (quantises_inside(p, sms)) {
         p.x = static_cast<const __nv_bfloat16 *>(x);
         p.x_stride = x_stride;
         p.x_vec = is_aligned(x, 8) && x_stride % 4 == 0;

@@ -23,15 +23,17 @@ lowm_status_t host_check_device(int *sms);   // LOWM_OK on sm_103; the SM count
 unsigned int *host_status_word();            // device address of the status word, or nullptr
 EncodeTiledFn host_encode_fn();              // cuTensorMapEncodeTiled (for any host thread), or nullptr
 
-// Defined in paged_attention.cu: lowm_paged_attention with, when k_factor is not NULL (pages of 64 tokens then), a number
-// for each key, [num_pages][kv_heads][64] fp32 and 16-byte aligned, that its scores are multiplied by.
+// Defined in paged_attention.cu: lowm_paged_attention with, when factors is not NULL (pages of 64 tokens then), factors
+// in [1, 2) of a key's scores (f) and of its value (v), fp32 and 16-byte aligned: one pair for each page and head
+// (tokens_a_factor 64), [num_pages][kv_heads] of f, log2(v), 1 / v and an unused number; or one for each key (1),
+// [num_pages][kv_heads][64 of f, 64 of v].
 lowm_status_t attend_pages(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache, int64_t k_page_stride,
                            int64_t k_place_stride, int64_t k_cache_head_stride, const void *v_cache, int64_t v_page_stride,
                            int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size,
                            const int32_t *page_table, int64_t page_table_stride, int table_width, const int32_t *kv_lens,
                            const int32_t *cu_q, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, int batch,
-                           int q_tokens, int heads, int kv_heads, int dim, float scale, int window, const float *k_factor,
-                           void *workspace, size_t workspace_bytes, void *stream);
+                           int q_tokens, int heads, int kv_heads, int dim, float scale, int window, const float *factors,
+                           int tokens_a_factor, void *workspace, size_t workspace_bytes, void *stream);
 
 inline bool is_aligned(const void *p, uintptr_t bytes)
 {

@@ -34,8 +34,12 @@
 // (453 us).  Few keys: the chain of launch, schedule, first tile and join (4 x 1000
 // keys: 12.6 us).
 //
-// FACTOR: keys come with a number each that multiplies their scores (what a cache of codes, widened to bf16, has of its
-// scales beside powers of two; paged_attention_fp8.cu).  Pages then have 64 tokens, and a tile's numbers arrive with its K.
+// FACTORS: keys come with two factors in [1, 2), f for their scores and v for their values (what a cache of codes, widened to
+// bf16, has of its scales beside powers of two; paged_attention_fp8.cu).  v multiplies the weights before they are rounded,
+// and their sum leaves it out.  Pages then have 64 tokens, and a tile's factors arrive with its K.  Where a tile has one pair
+// (kTileFactors) they cost nothing; a pair for each key (kKeyFactors) costs 32 loads of 16 bytes and 64 packed multiplications
+// a row and tile (chunks of 1537 tokens over 9000 keys: 231 and 257 us,
+// the copy included).
 //
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.
@@ -83,9 +87,11 @@ struct AttnParams : LineParams<kTileRows, kItemCost, kMinShare> {
     int64_t q_ts, q_hs, o_ts, o_hs, table_stride, num_pages;
     int64_t k_page, k_place, k_head, v_page, v_place, v_head;
     const int32_t *table;
-    const float *k_factor;                   // FACTOR: [num_pages][kv_heads][64] what a key's scores are multiplied by
+    const float *factors;                    // kTileFactors: [num_pages][kv_heads] of f, log2(v), 1 / v, unused;
+                                             // kKeyFactors: [num_pages][kv_heads][f, v][64]
     int page_size, page_shift, heads, slot_rows;
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
+    float scale_inverse;                     // 1 / scale_log2
     float q_sign;
     bool q_vec, out_vec;                     // 16-byte rows
     float4 *parts;                           // [2 * ctas][dim / 4][slot_rows] sums, rows side by side as the lanes hold
@@ -177,13 +183,15 @@ __device__ __forceinline__ uint64_t make_sw128_nmajor_desc(uint32_t saddr, uint3
 }
 
 // ------------------------------------------------------------------ shared memory
-template <int DIM, bool FACTOR>
+enum { kNoFactors, kTileFactors, kKeyFactors };
+
+template <int DIM, int FACTORS>
 struct AttnSmem {
     static constexpr uint32_t kHalves = DIM / 64;                       // 128-byte wide pieces of a row
     static constexpr uint32_t kQ = 0;                                   // [halves][128 rows][64]
     static constexpr uint32_t kTileBytes = kTileKeys * DIM * 2;
     static constexpr uint32_t kRing = kTileRows * DIM * 2;              // [stages][halves][64 keys][64]
-    static constexpr uint32_t kStages = DIM == 128 ? (FACTOR ? 4 : 5) : 10;     // 80 KiB: two CTAs fill an SM's 227 KiB
+    static constexpr uint32_t kStages = DIM == 128 ? (FACTORS == kKeyFactors ? 4 : 5) : 10;     // 80 KiB: two CTAs fill an SM's 227 KiB
     // A wait for a full stage passes too early when the load before it in that stage has not landed yet: the
     // barrier's parity is then still that of the phase before.  Loads (K0, K1, V0, K2, V1, ..., V of the last tile, then
     // the next item's) may land in any order, so it must follow from what the waiting warp has seen.  At K of tile g
@@ -194,12 +202,13 @@ struct AttnSmem {
     static constexpr uint32_t kBars = kRing + kStages * kTileBytes;     // full, empty [stages]; q; s, p, o [2]; edges; drain
     static constexpr uint32_t kNumBars = 2 * kStages + 9;
     static constexpr uint32_t kSlot = kBars + kNumBars * 8;             // TMEM address, edge word
-    static constexpr uint32_t kFactors = FACTOR ? (kSlot + 16 + 127) / 128 * 128 : kSlot + 16;   // [slots][64 keys]; copied in bulk
+    static constexpr uint32_t kFactors = FACTORS ? (kSlot + 16 + 127) / 128 * 128 : kSlot + 16;   // [slots]; copied in bulk
+    static constexpr uint32_t kFactorBytes = FACTORS == kTileFactors ? 16 : 2 * kTileKeys * 4;
     // While the softmax is at tile j its weights are missing, so V of tile j keeps its stage, and K of tile
     // j + 2 + (kStages - 2) / 2 is the last that the ring lets in behind it.
-    static constexpr uint32_t kFactorSlots = FACTOR ? (DIM == 128 ? 4 : 8) : 0;
-    static_assert(!FACTOR || kFactorSlots > 2 + (kStages - 2) / 2, "a tile's factors would be overwritten while they are read");
-    static constexpr uint32_t kBytes = kFactors + kFactorSlots * kTileKeys * 4;    // 112.2 KiB: two CTAs an SM
+    static constexpr uint32_t kFactorSlots = FACTORS ? (DIM == 128 ? 4 : 8) : 0;
+    static_assert(!FACTORS || kFactorSlots > 2 + (kStages - 2) / 2, "a tile's factors would be overwritten while they are read");
+    static constexpr uint32_t kBytes = kFactors + kFactorSlots * kFactorBytes;    // 112.2 KiB: two CTAs an SM
 };
 
 template <int DIM>
@@ -313,7 +322,7 @@ __device__ __forceinline__ bool clean_values(uint8_t *tile, const Seen &seen, in
 // and change nothing a second time.  A warp's 32 rows take some milliseconds at
 // worst, whatever the lengths (3 ms an item with nothing but NaN in V): far below
 // the limit of the other warps' waits.
-template <int DIM, bool FACTOR>
+template <int DIM, int FACTORS>
 __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows, int sequence, const Row &mine, int key_begin,
                                              int key_end, float shift, float factor, int64_t slot, int r)
 {
@@ -356,8 +365,10 @@ __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows,
                          __bfloat162float(p.k[page * p.k_page + place * p.k_place + g * p.k_head + lane * E + e]), s);
             for (int o = 16; o > 0; o >>= 1)
                 s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (FACTOR)
-                s *= p.k_factor[(page * p.kv_heads + g) * kTileKeys + place];
+            if (FACTORS == kTileFactors)
+                s *= p.factors[(page * p.kv_heads + g) * 4];
+            if (FACTORS == kKeyFactors)
+                s *= p.factors[(page * p.kv_heads + g) * (2 * kTileKeys) + place];
             // (a weight too small for a float still carries an infinity)
             const float a = s == -p.q_sign * CUDART_INF_F
                                 ? 0.f
@@ -378,12 +389,12 @@ __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows,
     }
 }
 
-template <int DIM, bool FACTOR>
+template <int DIM, int FACTORS>
 __global__ void __launch_bounds__(kAttnThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                            const AttnParams p)
 {
-    using L = AttnSmem<DIM, FACTOR>;
+    using L = AttnSmem<DIM, FACTORS>;
     constexpr uint32_t kColumns = 256;       // two S buffers and O (192 or 256 columns), a power of two
     constexpr uint32_t kOColumn = 2 * kSColumns;
     // The swizzle repeats every 1024 bytes, so the base must be a multiple; rounding it up at run time
@@ -464,15 +475,16 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                     const int key0 = (it.first_tile + tile) * kTileKeys;
                     // Pages past the sequence's end are not requested.
                     const int used = min(boxes, max(1, (it.kv - key0 + box_keys - 1) / box_keys));
-                    const bool factors = FACTOR && map == &map_k && __shfl_sync(0xffffffffu, page, 0) >= 0;   // (a tile is a page)
+                    const bool factors = FACTORS && map == &map_k && __shfl_sync(0xffffffffu, page, 0) >= 0;   // (a tile is a page)
                     if (lane == 0)
                         ptx::mbar_arrive_expect_tx(bar_full + 8 * s,
-                                                   (uint32_t)used * box_keys * DIM * 2 + (factors ? kTileKeys * 4 : 0));
+                                                   (uint32_t)used * box_keys * DIM * 2 + (factors ? L::kFactorBytes : 0));
                     __syncwarp();
-                    if constexpr (FACTOR) {
+                    if constexpr (FACTORS != kNoFactors) {
                         if (factors && lane == 0)
-                            bulk_load(sbase + L::kFactors + keys_loaded % L::kFactorSlots * (kTileKeys * 4),
-                                      p.k_factor + ((int64_t)page * p.kv_heads + it.head) * kTileKeys, kTileKeys * 4, bar_full + 8 * s);
+                            bulk_load(sbase + L::kFactors + keys_loaded % L::kFactorSlots * L::kFactorBytes,
+                                      p.factors + ((int64_t)page * p.kv_heads + it.head) * (L::kFactorBytes / 4), L::kFactorBytes,
+                                      bar_full + 8 * s);
                         keys_loaded += map == &map_k;
                     }
                     if (mine < used)
@@ -650,9 +662,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         tmem_ld_x32(s_addr, s0);
                         tmem_ld_x32(s_addr + 32, s1);
                         ptx::tmem_wait_ld();
-                        if constexpr (FACTOR) {
-                            const float4 *f = reinterpret_cast<const float4 *>(smem + L::kFactors) +
-                                              g % L::kFactorSlots * (kTileKeys / 4);
+                        [[maybe_unused]] const float4 *f = nullptr;          // this tile's factors
+                        if constexpr (FACTORS != kNoFactors)
+                            f = reinterpret_cast<const float4 *>(smem + L::kFactors + g % L::kFactorSlots * L::kFactorBytes);
+                        if constexpr (FACTORS == kKeyFactors) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) {
                                 const float4 a = f[k / 4], b = f[8 + k / 4];
@@ -672,13 +685,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                                     s1[k] = 0xff800000u;
                             }
                         }
-                        float t[4] = {m, m, m, m};
+                        float k_factor = 1.f, v_log2 = 0.f, v_inverse = 1.f;
+                        if constexpr (FACTORS == kTileFactors) {
+                            k_factor = f->x;
+                            v_log2 = f->y;
+                            v_inverse = f->z;
+                        }
+                        const float before = FACTORS == kTileFactors ? -CUDART_INF_F : m;
+                        float t[4] = {before, before, before, before};
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
                                 t[c] = fmaxf(fmaxf(t[c], __uint_as_float(s0[k + c])), __uint_as_float(s1[k + c]));
-                        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                        float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                        if (FACTORS == kTileFactors)         // of scores times v: the largest weight, 1, is not rounded
+                            top = fmaxf(m, fmaf(top, k_factor, v_log2 * p.scale_inverse));
                         if (j == 0) {
                             m = top;
                         } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescaleLog2)) {
@@ -701,9 +723,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                             }
                         }
                         const float ms = m == -CUDART_INF_F ? 0.f : m * p.scale_log2;
-                        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), shift2 = pack2(-ms, -ms);
+                        const uint64_t scale2 = pack2(p.scale_log2 * k_factor, p.scale_log2 * k_factor),
+                                       shift2 = pack2(v_log2 - ms, v_log2 - ms);
                         uint64_t sum0 = 0, sum1 = 0;
                         uint32_t pk[32];
+                        [[maybe_unused]] float4 v0, v1;
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
                             const float2 x = unpack2(fma2(pack2(s0[k], s0[k + 1]), scale2, shift2));
@@ -711,12 +735,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                             const float a = ex2(x.x), b = ex2(x.y), c = ex2(y.x), d = ex2(y.y);
                             sum0 = add2(sum0, pack2(a, b));
                             sum1 = add2(sum1, pack2(c, d));
-                            const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b), cd = __floats2bfloat162_rn(c, d);
+                            __nv_bfloat162 ab = __floats2bfloat162_rn(a, b), cd = __floats2bfloat162_rn(c, d);
+                            if constexpr (FACTORS == kKeyFactors) {
+                                if (k % 4 == 0) {
+                                    v0 = f[kTileKeys / 4 + k / 4];
+                                    v1 = f[kTileKeys / 4 + 8 + k / 4];
+                                }
+                                const float2 u = unpack2(mul2(pack2(a, b), k % 4 ? pack2(v0.z, v0.w) : pack2(v0.x, v0.y)));
+                                const float2 w = unpack2(mul2(pack2(c, d), k % 4 ? pack2(v1.z, v1.w) : pack2(v1.x, v1.y)));
+                                ab = __floats2bfloat162_rn(u.x, u.y);
+                                cd = __floats2bfloat162_rn(w.x, w.y);
+                            }
                             pk[k / 2] = *reinterpret_cast<const uint32_t *>(&ab);
                             pk[16 + k / 2] = *reinterpret_cast<const uint32_t *>(&cd);
                         }
                         const float2 sums = unpack2(add2(sum0, sum1));
-                        l += sums.x + sums.y;
+                        l += FACTORS == kTileFactors ? (sums.x + sums.y) * v_inverse : sums.x + sums.y;
                         tmem_st_x32(s_addr, pk);
                         ptx::tmem_wait_st();
                     }
@@ -784,7 +818,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         ml[slot * p.slot_rows + r] = make_float2(m * p.scale_log2, l);
                     }
                     if (edges)
-                        add_edge_values<DIM, FACTOR>(p, __ballot_sync(0xffffffffu, w.valid), sequence, w, key_begin, key_end,
+                        add_edge_values<DIM, FACTORS>(p, __ballot_sync(0xffffffffu, w.valid), sequence, w, key_begin, key_end,
                                              m == -CUDART_INF_F ? 0.f : m * p.scale_log2, whole ? inv : 1.f,
                                              whole ? -1 : slot, r);
                 }
@@ -918,17 +952,17 @@ lowm_status_t encode_cache(const void *base, int64_t page_stride, int64_t place_
                : LOWM_ERR_CUDA;
 }
 
-template <int DIM, bool FACTOR>
+template <int DIM, int FACTORS>
 lowm_status_t launch_attention(const CUtensorMap &map_k, const CUtensorMap &map_v, const AttnParams &p, int sms,
                                void *stream)
 {
     static SmemOptIn opt_in;
-    if (!opt_in.set(reinterpret_cast<const void *>(paged_attention_kernel<DIM, FACTOR>), AttnSmem<DIM, FACTOR>::kBytes))
+    if (!opt_in.set(reinterpret_cast<const void *>(paged_attention_kernel<DIM, FACTORS>), AttnSmem<DIM, FACTORS>::kBytes))
         return LOWM_ERR_CUDA;
     const int ctas = std::min(2 * sms, kMaxAttnCtas);
     if (p.batch > 0) {
-        const lowm_status_t st = launch_pdl(paged_attention_kernel<DIM, FACTOR>, dim3((unsigned)ctas), dim3(kAttnThreads),
-                                            AttnSmem<DIM, FACTOR>::kBytes, stream, map_k, map_v, p);
+        const lowm_status_t st = launch_pdl(paged_attention_kernel<DIM, FACTORS>, dim3((unsigned)ctas), dim3(kAttnThreads),
+                                            AttnSmem<DIM, FACTORS>::kBytes, stream, map_k, map_v, p);
         if (st != LOWM_OK)
             return st;
     }
@@ -953,7 +987,7 @@ lowm_status_t lowm::attend_pages(
     int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size, const int32_t *page_table,
     int64_t page_table_stride, int table_width, const int32_t *kv_lens, const int32_t *cu_q, void *out,
     int64_t out_token_stride, int64_t out_head_stride, float *lse, int batch, int q_tokens, int heads, int kv_heads,
-    int dim, float scale, int window, const float *k_factor, void *workspace, size_t workspace_bytes, void *stream)
+    int dim, float scale, int window, const float *factors, int tokens_a_factor, void *workspace, size_t workspace_bytes, void *stream)
 {
     if (batch < 0 || q_tokens < 0 || heads <= 0 || kv_heads <= 0 || dim <= 0 || num_pages <= 0 || num_pages > INT_MAX || page_size <= 0 ||
         table_width < 0 || window < 0 || !(scale == scale))
@@ -1018,7 +1052,7 @@ lowm_status_t lowm::attend_pages(
     p.v_place = v_place_stride;
     p.v_head = v_cache_head_stride;
     p.table = page_table;
-    p.k_factor = k_factor;
+    p.factors = factors;
     p.kv_lens = kv_lens;
     p.cu_q = cu_q;
     p.page_size = page_size;
@@ -1035,6 +1069,7 @@ lowm_status_t lowm::attend_pages(
     p.capacity = (int)capacity;
     // Never 0, so that a masked score (-inf) stays one.
     p.scale_log2 = std::max((scale < 0.f ? -scale : scale) * 1.44269504088896340736f, 1e-30f);
+    p.scale_inverse = 1.f / p.scale_log2;
     p.q_sign = scale < 0.f ? -1.f : 1.f;
     p.q_vec = is_aligned(q, 16) && !((q_token_stride | q_head_stride) & 7);
     p.out_vec = is_aligned(out, 16) && !((out_token_stride | out_head_stride) & 7);
@@ -1050,11 +1085,14 @@ lowm_status_t lowm::attend_pages(
         (st = encode_cache(v_cache, v_page_stride, v_place_stride, v_cache_head_stride, num_pages, page_size, kv_heads,
                            dim, &map_v)) != LOWM_OK)
         return st;
-    if (k_factor)
-        return dim == 64 ? launch_attention<64, true>(map_k, map_v, p, sms, stream)
-                         : launch_attention<128, true>(map_k, map_v, p, sms, stream);
-    return dim == 64 ? launch_attention<64, false>(map_k, map_v, p, sms, stream)
-                     : launch_attention<128, false>(map_k, map_v, p, sms, stream);
+    if (!factors)
+        return dim == 64 ? launch_attention<64, kNoFactors>(map_k, map_v, p, sms, stream)
+                         : launch_attention<128, kNoFactors>(map_k, map_v, p, sms, stream);
+    if (tokens_a_factor == kTileKeys)
+        return dim == 64 ? launch_attention<64, kTileFactors>(map_k, map_v, p, sms, stream)
+                         : launch_attention<128, kTileFactors>(map_k, map_v, p, sms, stream);
+    return dim == 64 ? launch_attention<64, kKeyFactors>(map_k, map_v, p, sms, stream)
+                     : launch_attention<128, kKeyFactors>(map_k, map_v, p, sms, stream);
 }
 
 extern "C" lowm_status_t lowm_paged_attention(
@@ -1068,5 +1106,5 @@ extern "C" lowm_status_t lowm_paged_attention(
     return lowm::attend_pages(q, q_token_stride, q_head_stride, k_cache, k_page_stride, k_place_stride, k_cache_head_stride,
                               v_cache, v_page_stride, v_place_stride, v_cache_head_stride, num_pages, page_size, page_table,
                               page_table_stride, table_width, kv_lens, cu_q, out, out_token_stride, out_head_stride, lse, batch,
-                              q_tokens, heads, kv_heads, dim, scale, window, nullptr, workspace, workspace_bytes, stream);
+                              q_tokens, heads, kv_heads, dim, scale, window, nullptr, 0, workspace, workspace_bytes, stream);
 }

@@ -697,8 +697,9 @@ __global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Att
 // Where sequences bring many rows a head, the keys and values that they see are written out in bf16 once, in pages of 64
 // tokens, and the tcgen05 attention of paged_attention.cu runs on those: it does 1.2 PFLOP/s where the registers' products
 // reach 0.15; but writing and reading 2 bytes an element takes its time, and a launch more.  A code times a power of two is
-// a bf16 number, so K keeps its scales' powers of two, and their mantissas, in [1, 2), multiply the scores (rounded into K
-// they made three quarters of the result's error); V is rounded with its scale, as bf16 weights and outputs are.
+// a bf16 number, so K and V keep their scales' powers of two, and the mantissas, in [1, 2), multiply scores and weights (V
+// rounded with its scale made the result's error 0.0027 of it where its own rounding is 0.0017).  A tile of the copy has one
+// scale where a block is not shorter, else one for each key.
 // The rule counts the multiply-adds of all rows with all keys that the table has room for (a key's exponentials as 64 of
 // them): us in the registers and widened at 8 sequences x 16 tokens x 4000 keys (of 32 / 8 heads of 128) 40, 58; 8 x 32 x
 // 16000 175, 141; 8 x 64 x 8000 250, 135; 2 x 64 x 4000 54, 47; 1 x 300 x 1000 (16 / 8 heads) 30, 35.
@@ -714,9 +715,10 @@ struct WidenParams {
     int64_t table_stride, num_pages;
     const int32_t *table, *kv_lens, *cu_q;
     __nv_bfloat16 *wide_k, *wide_v;          // [batch * pages][kv_heads][64][dim]
-    float *factor;                           // [batch * pages][kv_heads][64]
+    float *factors;                          // [batch * pages][kv_heads] of what attend_pages takes
     int32_t *wide_table;                     // [batch][pages]
     int page_shift, block_shift, batch, q_tokens, kv_heads, window, capacity, pages;
+    bool tile_factors;
 };
 
 __device__ __forceinline__ void widen_16(uint4 codes, float scale, uint4 *to)
@@ -731,6 +733,15 @@ __device__ __forceinline__ void widen_16(uint4 codes, float scale, uint4 *to)
     }
     to[0] = reinterpret_cast<const uint4 *>(out)[0];
     to[1] = reinterpret_cast<const uint4 *>(out)[1];
+}
+
+// A scale as a power of two, with its sign, times the rest in [1, 2); 0, infinities, NaN and what is below 2^-126 are left whole.
+__device__ __forceinline__ float split_scale(float scale, float &rest)
+{
+    const uint32_t bits = __float_as_uint(scale), exponent = bits & 0x7f800000u;
+    const bool normal = exponent != 0 && exponent != 0x7f800000u;
+    rest = normal ? __uint_as_float((bits & 0x007fffffu) | 0x3f800000u) : 1.f;
+    return normal ? __uint_as_float(bits & 0xff800000u) : scale;
 }
 
 // A CTA widens one head of 64 tokens of a sequence at a time, 16 elements a thread and step.
@@ -777,16 +788,21 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams 
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
             const int key = u * kKeysAtOnce + mine;
-            // The scale of K: a power of two for the codes, and the rest (any number but those: the rest alone).
-            const uint32_t bits = __float_as_uint(ks[u]), exponent = bits & 0x7f800000u;
-            const bool normal = exponent != 0 && exponent != 0x7f800000u;
-            if (chunk == 0)
-                p.factor[task * kWideKeys + key] = normal ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u) : ks[u];
+            float k_rest, v_rest;
+            const float k_power = split_scale(ks[u], k_rest);
+            const float v_power = split_scale(fminf(fmaxf(vs[u], 1.f / kMaxScale), kMaxScale), v_rest);
+            if (chunk == 0 && p.tile_factors) {
+                if (key == 0)
+                    reinterpret_cast<float4 *>(p.factors)[task] = make_float4(k_rest, log2f(v_rest), 1.f / v_rest, 0.f);
+            } else if (chunk == 0) {
+                p.factors[2 * task * kWideKeys + key] = k_rest;
+                p.factors[(2 * task + 1) * kWideKeys + key] = v_rest;
+            }
             if (key0 + key >= end)
                 continue;
             const int64_t to = (task * kWideKeys + key) * DIM + 16 * chunk;
-            widen_16(k[u], normal ? __uint_as_float(exponent) : 1.f, reinterpret_cast<uint4 *>(p.wide_k + to));
-            widen_16(v[u], fminf(fmaxf(vs[u], 1.f / kMaxScale), kMaxScale), reinterpret_cast<uint4 *>(p.wide_v + to));
+            widen_16(k[u], k_power, reinterpret_cast<uint4 *>(p.wide_k + to));
+            widen_16(v[u], v_power, reinterpret_cast<uint4 *>(p.wide_v + to));
         }
     }
 }
@@ -877,7 +893,7 @@ size_t wide_table_bytes(int batch, int page_size, int table_width)
 
 size_t factor_bytes(int batch, int kv_heads, int page_size, int table_width)
 {
-    return (size_t)(batch * wide_pages(page_size, table_width) * kWideKeys * kv_heads * 4);
+    return (size_t)(batch * wide_pages(page_size, table_width) * 2 * kWideKeys * kv_heads * 4);
 }
 
 }  // namespace
@@ -981,6 +997,7 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
         w.table = page_table;
         w.kv_lens = kv_lens;
         w.cu_q = cu_q;
+        w.tile_factors = block >= kWideKeys;
         w.page_shift = log2_of(page_size);
         w.block_shift = log2_of(block);
         w.batch = batch;
@@ -993,7 +1010,7 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
         const int64_t bytes = wide_bytes(batch, kv_heads, dim, page_size, table_width);
         w.wide_k = reinterpret_cast<__nv_bfloat16 *>(at);
         w.wide_v = reinterpret_cast<__nv_bfloat16 *>(at + bytes);
-        w.factor = reinterpret_cast<float *>(at + 2 * bytes);
+        w.factors = reinterpret_cast<float *>(at + 2 * bytes);
         const size_t tables = (size_t)2 * bytes + factor_bytes(batch, kv_heads, page_size, table_width);
         w.wide_table = reinterpret_cast<int32_t *>(at + tables);
         const size_t used = tables + wide_table_bytes(batch, page_size, table_width);
@@ -1004,8 +1021,8 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
             return st;
         return attend_pages(q, q_token_stride, q_head_stride, w.wide_k, kv_heads * head, dim, head, w.wide_v, kv_heads * head, dim,
                             head, tasks, kWideKeys, w.wide_table, w.pages, w.pages, kv_lens, cu_q, out, out_token_stride,
-                            out_head_stride, lse, batch, q_tokens, heads, kv_heads, dim, scale, window, w.factor, at + used,
-                            workspace_bytes - used, stream);
+                            out_head_stride, lse, batch, q_tokens, heads, kv_heads, dim, scale, window, w.factors, w.tile_factors ? kWideKeys : 1,
+                            at + used, workspace_bytes - used, stream);
     }
     unsigned int *status = host_status_word();
     if (!status)

@@ -445,9 +445,9 @@ def attention64(q, kc, vc, ks, vs, table, kv_lens, cu_q, scale, window, wide):
             rows = torch.isfinite(size).all(1) | ~some
             out[q0:q1, h] = torch.where(some[:, None], o, 0.0)
             # A score is off by dim additions in fp32 and a few roundings of its size; a weight by twice that, by its own
-            # rounding (fp16; with the cache widened bf16, and V's values by a rounding more) and by the hardware's exponential.
+            # rounding (fp16; with the cache widened bf16) and by the hardware's exponential.
             ds = ((dim + 16) * 2 * E * torch.where(seen, size, 0.0)).amax(1, keepdim=True).nan_to_num() + 2.0 ** -20
-            weight = 2 * ds + (2 * U if wide else H) + 16 * E
+            weight = 2 * ds + (U if wide else H) + 16 * E
             # What a weight meets V with, w_j b_j (b_j: the scale of V), is at most 2^15 and at least 2^8 where it is the largest,
             # and fp16 numbers are 2^-24 apart below 2^-14: off by 2^-25 at most, 2^-33 of the largest, times a code.
             b_j = torch.where(inside, vs[pg, place // block, g].to(F64), 1.0)
@@ -532,6 +532,31 @@ def test_attention_of_chunks(dim, heads, kv_heads, window, block, room):
     lens, q_lens, width = [400, 130, 700], [200, 130, 333], room and room // 32
     check_attention(lens, q_lens, heads, kv_heads, dim, 32, block, window=window, seed=dim + window, width=width, wide=bool(room))
     assert widened(3, 663, heads, kv_heads, dim, 32, width or 22) == bool(room)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page,block", [(64, 64), (128, 64), (128, 128), (256, 32)])
+@pytest.mark.parametrize("window,scale", [(0, None), (50, -0.2), (0, 0.0)])
+def test_attention_of_chunks_with_blocks_as_long_as_a_tile(dim, page, block, window, scale):
+    lens, q_lens = [400, 130, 700], [200, 130, 333]
+
+    def change(kc, vc, ks, vs, table, q):
+        vs[::2] *= 2.0 ** 20
+        ks[1::3] *= -1.0
+        vc.view(torch.uint8)[int(table[2, 600 // page]), 600 % page, 0, 5] = 0x7f
+        vc.view(torch.uint8)[int(table[1, 0]), 3, 1, 6] = 0xff
+    check_attention(lens, q_lens, 8, 2, dim, page, block, window=window, scale=scale, seed=dim + page, change=change,
+                    width=ROOM // page, wide=True)
+    assert widened(3, 663, 8, 2, dim, page, ROOM // page)
+
+
+@pytest.mark.parametrize("block", [1, 16, 64])
+def test_attention_of_chunks_of_very_different_value_scales(block):
+    def change(kc, vc, ks, vs, table, q):
+        vs[:, ::2] *= 2.0 ** -30
+        vs[0] *= 2.0 ** 30
+    check_attention([400, 130], [300, 130], 8, 2, 128, 64, block, seed=10, change=change, width=ROOM // 64, wide=True)
+    assert widened(2, 430, 8, 2, 128, 64, ROOM // 64)
 
 
 def test_attention_of_chunks_without_memory_to_widen():

@@ -20,7 +20,9 @@
 // fragments' 16-byte reads meet no bank twice), scales by 4-byte asynchronous copies.  Two CTAs an SM with rings of five
 // tiles: 24 sequences of up to 16384 keys 90.5 us (floor 74.4), with three CTAs and three tiles, whose registers do not
 // suffice, 96, with four and two 123.  Sixteen rows a warp (a key widened once for two products) were slower for any number
-// of rows: 8 sequences of 8 tokens over 4000 keys 39.5 us for 29.7.  L2 promotion of 256 bytes: 123 us for 96.
+// of rows: 8 sequences of 8 tokens over 4000 keys 39.5 us for 29.7.  Heads of 64 leave registers for three CTAs of seven tiles
+// (24 such sequences: 83 us, with two 103, with four of five 82, but 8 sequences of 7 tokens 26.5 for 24.6).  L2 fetches what a
+// row has: from 64-byte rows with 128 bytes half of what came was not used (83 us for 63); 256 at 128: 123 us for 96.
 //
 // The orders of the head's elements (for q.k) and of the elements' rows (for w.v) within a product are free; they are chosen
 // so that a thread's fragments are neighbouring bytes of the cache.  V's keys are paired by byte permutes before they are
@@ -44,7 +46,7 @@ constexpr int kWarps = 4;                    // that compute
 constexpr int kWarpRows = 8;                 // rows of a warp, the columns of its products
 constexpr int kThreads8 = 32 * (kWarps + 1);
 constexpr int kUnitKeys = 32;                // of one product
-constexpr int kMaxCtas = 320;                // two per SM, and a bound for the workspace
+constexpr int kMaxCtas = 480;                // three per SM, and a bound for the workspace
 constexpr int kItemCost8 = 4, kMinShare8 = 4;
 constexpr float kWeightLog2 = 8.f, kRescaleLog2 = 7.f;   // the largest weight is 2^15 (fp16 ends at 65504)
 constexpr float kMaxScale = 1.125899906842624e15f;   // 2^50: scales are taken as 2^-50 .. 2^50
@@ -149,9 +151,9 @@ __device__ __forceinline__ void load_shared(const uint8_t *at, uint32_t (&w)[WOR
 // ------------------------------------------------------------------ shared memory
 template <int DIM>
 struct Attn8Smem {
-    static constexpr int kCtas = 2;                                     // an SM
+    static constexpr int kCtas = DIM == 128 ? 2 : 3;                    // an SM
     static constexpr uint32_t kTileBytes = kTileKeys * DIM;             // of K or V; 1024-byte multiples
-    static constexpr uint32_t kStages = 5 * (128 / DIM);
+    static constexpr uint32_t kStages = DIM == 128 ? 5 : 7;
     static constexpr uint32_t kOut = DIM / 4;                           // sums a thread holds
     static constexpr uint32_t kSums = 4;                                // and maxima and sums of weights
     static constexpr uint32_t kScales = kStages * 2 * kTileBytes;       // [stages][K, V][64]
@@ -490,19 +492,20 @@ __global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM>::kCtas)
         do {
             const int from = c.from, n = c.to - c.from;
             const int32_t *pages = p.table + it.b * p.table_stride;
-            // The page of a key: -1 past the sequence's end.
-            auto entry = [&](int key) { return key < it.kv ? pages[key >> p.page_shift] : -1; };
-            auto box_key = [&](int j) { return (it.first_tile + j) * kTileKeys + mine * box_keys; };
-            auto key_at = [&](int j, int h) { return (it.first_tile + j) * kTileKeys + 32 * h + lane; };
-            int box = mine < boxes ? entry(box_key(from)) : -1;
-            int page[2] = {entry(key_at(from, 0)), entry(key_at(from, 1))};
+            // Entries of the table, 32 at a time (a tile has at most 8) and those behind them under way: the loop does not wait
+            // for a load (pages of 16: 111 us for 103).  -1 past the sequence's end.
+            const int known_pages = (it.kv + p.page_size - 1) >> p.page_shift;
+            auto entry = [&](int index) { return index < known_pages ? pages[index] : -1; };
+            int window = ((it.first_tile + from) * kTileKeys >> p.page_shift) >> 5;
+            int held = entry(32 * window + lane), ahead = entry(32 * window + 32 + lane);
             for (int j = from; j < from + n; ++j, ++i) {
-                int next_box = -1, next[2] = {-1, -1};
-                if (j + 1 < from + n) {
-                    next_box = mine < boxes ? entry(box_key(j + 1)) : -1;
-                    next[0] = entry(key_at(j + 1, 0));
-                    next[1] = entry(key_at(j + 1, 1));
+                const int key0 = (it.first_tile + j) * kTileKeys, index = key0 >> p.page_shift;
+                if (index >> 5 != window) {
+                    ++window;
+                    held = ahead;
+                    ahead = entry(32 * window + 32 + lane);
                 }
+                const int box = __shfl_sync(0xffffffffu, held, boxes > 1 ? index + mine : index);
                 const uint32_t s = i % L::kStages;
                 if (!wait_short(bar_empty + 8 * s, ((i / L::kStages) & 1) ^ 1)) {
                     ok = false;
@@ -511,7 +514,6 @@ __global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM>::kCtas)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
-                const int key0 = (it.first_tile + j) * kTileKeys;
                 const int used = min(boxes, max(1, (it.kv - key0 + box_keys - 1) / box_keys));   // pages past the end are not requested
                 if (lane == 0)
                     ptx::mbar_arrive_expect_tx(bar_full + 8 * s, 2u * used * box_keys * DIM);
@@ -520,16 +522,16 @@ __global__ void __launch_bounds__(kThreads8, Attn8Smem<DIM>::kCtas)
                     tma_load_4d(sbase + s * 2 * L::kTileBytes + at, map, 0, key0 & (p.page_size - 1), it.head, box, bar_full + 8 * s);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const bool known = page[h] >= 0 && page[h] < p.num_pages;
-                    const int64_t pg = known ? page[h] : 0;
-                    const int64_t block = (key_at(j, h) & (p.page_size - 1)) >> p.block_shift;
+                    const int key = key0 + 32 * h + lane;
+                    const int page = __shfl_sync(0xffffffffu, held, key >> p.page_shift);
+                    const bool known = page >= 0 && page < p.num_pages;
+                    const int64_t pg = known ? page : 0;
+                    const int64_t block = (key & (p.page_size - 1)) >> p.block_shift;
                     const uint32_t to = sbase + L::kScales + (s * 2 * kTileKeys + 32 * h + lane) * 4;
                     copy_async_4(to, p.k_scale + pg * p.ks_page + block * p.ks_block + it.head * p.ks_head, known ? 4 : 0);
                     copy_async_4(to + kTileKeys * 4, p.v_scale + pg * p.vs_page + block * p.vs_block + it.head * p.vs_head, known ? 4 : 0);
-                    page[h] = next[h];
                 }
                 copies_arrive(bar_full + 8 * s);
-                box = next_box;
             }
         } while (ok && next_piece(p, c, end));
         // No copy may land after the CTA has ended: normally all were consumed long ago.
@@ -837,7 +839,7 @@ lowm_status_t encode_codes(const void *base, int64_t page_stride, int64_t place_
     const cuuint32_t step[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, step,
                CU_TENSOR_MAP_INTERLEAVE_NONE, dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? LOWM_OK
                : LOWM_ERR_CUDA;
 }

@@ -193,12 +193,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_fp8_kernel(const Rop
 // token, so a warp has 512 / DIM tokens at a time.  The first CTAs of the grid have k and v: each looks at kTokens tokens of
 // the call and has the runs that begin among them, for some of the heads: of a run of one token (decoding) such a group of
 // lanes has a head, of a longer one a warp.  What they need of the slots and the table comes into shared memory first, all
-// at once (one by one these were chains of latencies).  The other CTAs turn q.  Chunks of 1501 tokens (3751 in all, 32 / 8
-// heads of 128): 34 us with 128 registers a thread; 39 with 80 or 64, which spill; one kind of CTA for all heads, k and v
-// kept in registers for their second use, took 47.
-constexpr int kTokens = 16, kWideWarps = 8, kWideThreads = 32 * kWideWarps;
+// at once (one by one these were chains of latencies), the table's rows while one warp finds the runs.  The other CTAs turn q.
+// Chunks of 1501 tokens (3831 in all, 88 MB, 32 / 8 heads of 128): 22.8 us, 3.9 TB/s; k and v alone 18, whose CTAs are a chain
+// of five latencies (slots, table, runs, values, codes) and of instructions that four warps a scheduler hide in part; q alone
+// 15.  With 16 tokens a CTA 26, with three CTAs an SM, which spill, 31, with the values loaded one after another 36.
+constexpr int kTokens = 32, kWideWarps = 8, kWideThreads = 32 * kWideWarps;
 constexpr int kWideBlock = 128;              // the longest run
-constexpr int kAngleTokens = 2 * kTokens;    // whose angles are kept
+__host__ __device__ constexpr int angle_tokens(int dim) { return dim == 256 ? kTokens : 2 * kTokens; }    // whose angles are kept: 32 KiB at most
+constexpr int kAtHand = 4;                   // units a thread loads at once
 
 template <int DIM, bool INTERLEAVED>
 struct RopeUnit {
@@ -215,19 +217,22 @@ struct RopeUnit {
         e1 = turns && !INTERLEAVED ? e0 + half : e0 + 8;
     }
 
-    // The cosines and sines of token t (of a unit that turns), from the row kept in shared memory or the table.
-    __device__ __forceinline__ void angles(const Rope8Params &p, const float *kept, int64_t t, float (&c)[8], float (&s)[8]) const
+    // The cosines and sines of a unit that turns, from a row kept in shared memory.
+    __device__ __forceinline__ void kept_angles(const Rope8Params &p, const float *kept, float (&c)[8], float (&s)[8]) const
     {
         const int half = p.rotary / 2;
-        if (kept) {
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(kept + j0 + i), y = *reinterpret_cast<const float4 *>(kept + half + j0 + i);
-                c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-                s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-            }
-            return;
+        for (int i = 0; i < 8; i += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(kept + j0 + i), y = *reinterpret_cast<const float4 *>(kept + half + j0 + i);
+            c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+            s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
         }
+    }
+
+    // Those of token t from the table.
+    __device__ __forceinline__ void angles(const Rope8Params &p, int64_t t, float (&c)[8], float (&s)[8]) const
+    {
+        const int half = p.rotary / 2;
         const Position at = position_of(p, t);
         const int end1 = p.section0 + p.section1;
         const int axis0 = j0 < p.section0 ? 0 : (j0 < end1 ? 1 : 2), axis1 = j0 + 7 < p.section0 ? 0 : (j0 + 7 < end1 ? 1 : 2);
@@ -275,23 +280,17 @@ struct RopeUnit {
         }
     }
 
-    // The largest magnitude as its bits (what is not finite is above the finite ones), and of the finite ones.
-    __device__ __forceinline__ static uint32_t largest(const float (&y)[16])
+    // The bits of the largest finite magnitude; whether there are others.
+    __device__ __forceinline__ static void largest(const float (&y)[16], uint32_t &top, bool &other)
     {
-        uint32_t m = 0;
+        uint32_t all = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
-        return m;
-    }
-
-    __device__ __forceinline__ static uint32_t largest_finite(const float (&y)[16])
-    {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            m = fmaxf(m, finite_magnitude(y[i]));
-        return __float_as_uint(m);
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t m = __float_as_uint(y[i]) & 0x7fffffffu;
+            all = max(all, m);
+            top = max(top, m < 0x7f800000u ? m : 0u);
+        }
+        other = other || all >= 0x7f800000u;
     }
 
     // Codes y / scale; `plain`: all are finite and the scale is a power of two with this inverse.
@@ -303,10 +302,18 @@ struct RopeUnit {
             for (int i = 0; i < 4; ++i)
                 w[i] = to_e4m3x2(y[4 * i] * inverse, y[4 * i + 1] * inverse) |
                        to_e4m3x2(y[4 * i + 2] * inverse, y[4 * i + 3] * inverse) << 16;
-        } else {
+        } else {                             // (rare, and kept short)
+            float z[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                w[i / 4] |= (to_e4m3x2(nan_unless_finite(y[i]) / scale, 0.f) & 0xffu) << (8 * (i & 3));
+                z[i] = y[i];
+#pragma unroll 1
+            for (int i = 15; i >= 0; --i) {
+                w[3] = w[3] << 8 | w[2] >> 24;
+                w[2] = w[2] << 8 | w[1] >> 24;
+                w[1] = w[1] << 8 | w[0] >> 24;
+                w[0] = w[0] << 8 | (to_e4m3x2(nan_unless_finite(z[i]) / scale, 0.f) & 0xffu);
+            }
         }
         *reinterpret_cast<uint2 *>(to + e0) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2 *>(to + e1) = make_uint2(w[2], w[3]);
@@ -329,6 +336,32 @@ struct RopeUnit {
         }
     }
 };
+
+// (Not in line: few calls come here, and four copies of it would be in the loop.)
+template <int DIM, bool INTERLEAVED>
+__device__ __noinline__ void far_angles_of(const Rope8Params &p, const RopeUnit<DIM, INTERLEAVED> &unit, int64_t t, float *to)
+{
+    float c[8], s[8];
+    unit.angles(p, t, c, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        to[i] = c[i];
+        to[8 + i] = s[i];
+    }
+}
+
+template <int DIM, bool INTERLEAVED>
+__device__ __forceinline__ void far_angles(const Rope8Params &p, const RopeUnit<DIM, INTERLEAVED> &unit, int64_t t, float (&c)[8],
+                                           float (&s)[8])
+{
+    float both[16];
+    far_angles_of(p, unit, t, both);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        c[i] = both[i];
+        s[i] = both[8 + i];
+    }
+}
 
 // One head of k's or v's cache.
 struct HeadCache {
@@ -367,24 +400,29 @@ __device__ __forceinline__ void turn_queries(const Rope8Params &p, int64_t cta, 
     int h = threadIdx.x % part / Unit::kLanes;
     if (h >= p.heads)
         return;
-    uint4 next[2];
-    unit.load(p.q + t * p.q_ts + h * p.q_hs, next);
     float cosines[8], sines[8];
-    if (unit.turns)
-        unit.angles(p, nullptr, t, cosines, sines);
-    for (; h < p.heads; h += lanes) {
-        const uint4 now[2] = {next[0], next[1]};
-        if (h + lanes < p.heads)
-            unit.load(p.q + t * p.q_ts + (h + lanes) * p.q_hs, next);
-        float y[16];
-        unit.turn(now, cosines, sines, y);
-        alignas(16) __nv_bfloat162 v[8];
+    for (bool begin = true; h < p.heads; h += kAtHand * lanes, begin = false) {
+        uint4 raw[kAtHand][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-        __nv_bfloat16 *out = p.q_out + t * p.qo_ts + h * p.qo_hs;
-        *reinterpret_cast<uint4 *>(out + unit.e0) = reinterpret_cast<const uint4 *>(v)[0];
-        *reinterpret_cast<uint4 *>(out + unit.e1) = reinterpret_cast<const uint4 *>(v)[1];
+        for (int u = 0; u < kAtHand; ++u)
+            if (h + u * lanes < p.heads)
+                unit.load(p.q + t * p.q_ts + (h + u * lanes) * p.q_hs, raw[u]);
+        if (begin && unit.turns)
+            unit.angles(p, t, cosines, sines);
+#pragma unroll
+        for (int u = 0; u < kAtHand; ++u) {
+            if (h + u * lanes >= p.heads)
+                break;
+            float y[16];
+            unit.turn(raw[u], cosines, sines, y);
+            alignas(16) __nv_bfloat162 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            __nv_bfloat16 *out = p.q_out + t * p.qo_ts + (h + u * lanes) * p.qo_hs;
+            *reinterpret_cast<uint4 *>(out + unit.e0) = reinterpret_cast<const uint4 *>(v)[0];
+            *reinterpret_cast<uint4 *>(out + unit.e1) = reinterpret_cast<const uint4 *>(v)[1];
+        }
     }
 }
 
@@ -393,7 +431,7 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     rope_append_fp8_wide_kernel(const Rope8Params p, int windows, int kv_ctas, int at_once)
 {
     using Unit = RopeUnit<DIM, INTERLEAVED>;
-    constexpr int kLanes = Unit::kLanes, kAtOnce = Unit::kAtOnce;
+    constexpr int kLanes = Unit::kLanes, kAtOnce = Unit::kAtOnce, kAngleTokens = angle_tokens(DIM);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (blockIdx.x >= kv_ctas) {
@@ -406,7 +444,9 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     __shared__ int starts[kTokens], lengths[kTokens], counts[2];    // the runs that begin here, those of one token first
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / kLanes;
     const int64_t t0 = (int64_t)(blockIdx.x % windows) * kTokens;
-    const int column = blockIdx.x / windows, columns = kv_ctas / windows;
+    // The heads of k, then v, in equal parts.
+    const int columns = kv_ctas / windows, a_column = (2 * p.kv_heads + columns - 1) / columns;
+    const int head0 = (int)(blockIdx.x / windows) * a_column, heads_here = min(a_column, 2 * p.kv_heads - head0);
     const int here = (int)min((int64_t)kTokens, p.tokens - t0);
     const int kept = (int)min((int64_t)min(kAngleTokens, kTokens - 1 + p.block), p.tokens - t0);      // tokens
     const int cached = kTokens + 2 * p.block;
@@ -432,22 +472,6 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         slots[i] = slot;
     }
     __syncthreads();
-    const int quads = p.rotary / 4, half = p.rotary / 2;     // four of a row's cosines or sines
-#pragma unroll 4
-    for (int i = threadIdx.x; i < kept * quads; i += kWideThreads) {
-        const int token = i / quads, j = (i - token * quads) * 4, pair = j < half ? j : j - half;
-        auto row_of_pair = [&](int k) {
-            return (int64_t)rows[k < p.section0 ? 0 : (k < p.section0 + p.section1 ? 1 : 2)][token] * p.rotary;
-        };
-        const int64_t row = row_of_pair(pair), last = row_of_pair(pair + 3);
-        float4 x = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
-        if (row >= 0)
-            x = row == last ? *reinterpret_cast<const float4 *>(p.cos_sin + row + j)
-                            : make_float4(p.cos_sin[row + j], p.cos_sin[row_of_pair(pair + 1) + j + 1],
-                                          p.cos_sin[row_of_pair(pair + 2) + j + 2], p.cos_sin[last + j + 3]);
-        *reinterpret_cast<float4 *>(angles + token * p.rotary + j) = x;
-    }
-    __syncthreads();
     auto slot_of = [&](int64_t t) {          // (what lies further away is of a run with gaps)
         const int64_t i = t - t0 + p.block;
         if (i >= 0 && i < cached)
@@ -470,79 +494,124 @@ __global__ void __launch_bounds__(kWideThreads, 2)
             counts[0] = __popc(single);
             counts[1] = __popc(longer);
         }
+    } else if (head0 < p.kv_heads) {         // v is not turned
+        // A warp a token, a lane an element of its row; loads before stores, to be under way together.
+        constexpr int kLoad = 4;
+        const int half = p.rotary / 2;
+#pragma unroll 1
+        for (int token0 = warp - 1; token0 < kept; token0 += kLoad * (kWideWarps - 1)) {
+            float x[kLoad][DIM / 32];
+#pragma unroll
+            for (int u = 0; u < kLoad; ++u)
+#pragma unroll
+                for (int j = 0; j < DIM / 32; ++j) {
+                    const int token = token0 + u * (kWideWarps - 1), e = lane + 32 * j, pair = e < half ? e : e - half;
+                    const int row = token < kept ? rows[pair < p.section0 ? 0 : (pair < p.section0 + p.section1 ? 1 : 2)][token] : -1;
+                    x[u][j] = row >= 0 && e < p.rotary ? p.cos_sin[(int64_t)row * p.rotary + e] : CUDART_NAN_F;
+                }
+#pragma unroll
+            for (int u = 0; u < kLoad; ++u)
+#pragma unroll
+                for (int j = 0; j < DIM / 32; ++j) {
+                    const int token = token0 + u * (kWideWarps - 1), e = lane + 32 * j;
+                    if (token < kept && e < p.rotary)
+                        angles[token * p.rotary + e] = x[u][j];
+                }
+        }
     }
     __syncthreads();
     const int singles = counts[0], longer = counts[1], batches = (singles + kAtOnce - 1) / kAtOnce;
-    auto kept_of = [&](int token) { return token < kept ? angles + token * p.rotary : nullptr; };
     // Its heads of k and v: the runs' tasks, warp after warp.
-    int task = warp;
-    for (int head = column; head < 2 * p.kv_heads; head += columns) {
+    const int a_head = batches + longer, tasks = a_head * heads_here;
+#pragma unroll 1
+    for (int task = warp; task < tasks; task += kWideWarps) {
+        const int nth = task / a_head, work = task - nth * a_head, head = head0 + nth;
         const HeadCache c = head_cache(p, head);
         const Unit unit(p, head < p.kv_heads);
-        for (int work = 0; work < batches + longer; ++work) {
-            if (task-- != 0)                 // (whose turn it is)
-                continue;
-            task = kWideWarps - 1;
-            const bool one = work < batches;         // a batch of runs of one token, a group of lanes each; or a longer run
-            const int run = one ? work * kAtOnce + group : singles + work - batches;
-            const bool mine = !one || run < singles;
-            const int start = mine ? starts[run] : 0;
-            const int64_t t = t0 + start, slot = mine ? slots[p.block + start] : 0;
-            const int n = mine ? lengths[run] : 0;
-            const int64_t page = slot < INT_MAX ? (int)slot / p.page_size : slot / p.page_size;
-            const int place = (int)(slot - page * p.page_size), block = place >> p.block_shift, older = place - block * p.block;
-            uint8_t *cells = c.cells + page * c.page;
-            float *scale = c.scales + page * c.s_page + block * c.s_block;
-            const float before = mine && older > 0 ? *scale : 0.f;
-            const int first = one ? 0 : group, step = one ? 1 : kAtOnce;      // this group's tokens of the run
-            uint32_t top = 0;
-            // Calls with(k, values) for this group's tokens of the run.
-            auto each_token = [&](auto with) {
-#pragma unroll 1
-                for (int k = first; k < n; k += step) {
-                    if (slot_of(t + k) < 0)
-                        continue;
-                    uint4 raw[2];
-                    float cosines[8], sines[8], y[16];
-                    unit.load(c.x + (t + k) * c.step, raw);
-                    if (unit.turns)
-                        unit.angles(p, kept_of(start + k), t + k, cosines, sines);
-                    unit.turn(raw, cosines, sines, y);
-                    with(k, y);
-                }
-            };
-            auto agree = [&]() {             // the group's largest, or the warp's
+        const bool one = work < batches;         // a batch of runs of one token, a group of lanes each; or a longer run
+        const int run = one ? work * kAtOnce + group : singles + work - batches;
+        const bool mine = !one || run < singles;
+        const int start = mine ? starts[run] : 0;
+        const int64_t t = t0 + start, slot = mine ? slots[p.block + start] : 0;
+        const int n = mine ? lengths[run] : 0;
+        const int64_t page = slot < INT_MAX ? (int)slot / p.page_size : slot / p.page_size;
+        const int place = (int)(slot - page * p.page_size), block = place >> p.block_shift, older = place - block * p.block;
+        uint8_t *cells = c.cells + page * c.page;
+        float *scale = c.scales + page * c.s_page + block * c.s_block;
+        const float before = mine && older > 0 ? *scale : 0.f;
+        const int first = one ? 0 : group, step = one ? 1 : kAtOnce;      // this group's tokens of the run
+        // This group's next tokens of the run, their loads all under way at once; those of a short run stay.
+        uint4 raw[kAtHand][2];
+        unsigned has = 0;
+        auto fetch = [&](int k0) {
+            has = 0;
 #pragma unroll
-                for (int o = 1; o < 32; o *= 2) {
-                    const uint32_t other = __shfl_xor_sync(0xffffffffu, top, o);
-                    if (o < kLanes || !one)
-                        top = max(top, other);
+            for (int u = 0; u < kAtHand; ++u) {
+                const int k = k0 + u * step;
+                if (k < n && slot_of(t + k) >= 0) {
+                    has |= 1u << u;
+                    unit.load(c.x + (t + k) * c.step, raw[u]);
                 }
-            };
-            each_token([&](int, const float(&y)[16]) { top = max(top, Unit::largest(y)); });
-            agree();
-            const bool finite = top < 0x7f800000u;
-            if (__any_sync(0xffffffffu, !finite)) {
-                top = 0;
-                each_token([&](int, const float(&y)[16]) { top = max(top, Unit::largest_finite(y)); });
-                agree();
+            }
+        };
+        const bool stays = n <= kAtHand * step;
+        if (stays)
+            fetch(first);
+        uint32_t top = 0;
+        bool other = false, plain = false;
+        float now = 0.f, inverse = 0.f;
+        // First the largest magnitude, then the codes: one loop, whose instructions fit the caches (two copies and a third
+        // for what is not finite, and the kernel waited for instructions a third of its time).
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+            for (int k0 = first; k0 < n; k0 += kAtHand * step) {
+                if (!stays)
+                    fetch(k0);
+#pragma unroll
+                for (int u = 0; u < kAtHand; ++u) {
+                    if (!(has >> u & 1))
+                        continue;
+                    const int k = k0 + u * step;
+                    float cosines[8], sines[8], y[16];
+                    if (unit.turns) {
+                        if (start + k < kept)
+                            unit.kept_angles(p, angles + (start + k) * p.rotary, cosines, sines);
+                        else
+                            far_angles(p, unit, t + k, cosines, sines);
+                    }
+                    unit.turn(raw[u], cosines, sines, y);
+                    if (pass == 0)
+                        Unit::largest(y, top, other);
+                    else
+                        unit.store(cells + (slot_of(t + k) - page * p.page_size) * c.place, y, now, plain, inverse);
+                }
+            }
+            if (pass == 1)
+                break;
+            const unsigned others = __ballot_sync(0xffffffffu, other);
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {    // the group's largest, or the warp's
+                const uint32_t far = __shfl_xor_sync(0xffffffffu, top, o);
+                if (o < kLanes || !one)
+                    top = max(top, far);
             }
             if (!mine)
-                continue;
-            float now = power_of_two(scale_exponent(__uint_as_float(top)));
-            now = before > now ? before : now;       // (a scale that is not a number is replaced)
+                break;
+            now = power_of_two(scale_exponent(__uint_as_float(top)));
+            now = before > now ? before : now;   // (a scale that is not a number is replaced)
             if (older > 0 && now != before)
                 for (int l = (one ? 0 : group); l < older; l += step)
                     unit.move(cells + (block * p.block + l) * c.place, before / now);
-            const bool plain = finite && !(__float_as_uint(now) & 0x7fffffu) && now >= power_of_two(kMinScaleExponent) &&
-                               now <= power_of_two(kMaxScaleExponent);
-            const float inverse = plain ? 1.f / now : 0.f;
-            each_token([&](int k, const float(&y)[16]) {
-                unit.store(cells + (slot_of(t + k) - page * p.page_size) * c.place, y, now, plain, inverse);
-            });
-            if (one ? lane % kLanes == 0 : lane == 0)
-                *scale = now;
+            const unsigned of_run = one ? ((1u << kLanes) - 1) << (group * kLanes) : 0xffffffffu;
+            plain = !(others & of_run) && !(__float_as_uint(now) & 0x7fffffu) && now >= power_of_two(kMinScaleExponent) &&
+                    now <= power_of_two(kMaxScaleExponent);
+            inverse = plain ? 1.f / now : 0.f;
         }
+        if (!mine)
+            continue;
+        if (one ? lane % kLanes == 0 : lane == 0)
+            *scale = now;
     }
 }
 
@@ -661,7 +730,7 @@ extern "C" lowm_status_t lowm_rope_append_fp8(
         auto fn = dim == 64    ? (interleaved ? rope_append_fp8_wide_kernel<64, true> : rope_append_fp8_wide_kernel<64, false>)
                   : dim == 128 ? (interleaved ? rope_append_fp8_wide_kernel<128, true> : rope_append_fp8_wide_kernel<128, false>)
                                : (interleaved ? rope_append_fp8_wide_kernel<256, true> : rope_append_fp8_wide_kernel<256, false>);
-        return launch_pdl(fn, dim3((unsigned)all), dim3(kWideThreads), (size_t)kAngleTokens * rotary * sizeof(float), stream, p,
+        return launch_pdl(fn, dim3((unsigned)all), dim3(kWideThreads), (size_t)angle_tokens(dim) * rotary * sizeof(float), stream, p,
                           windows, windows * columns, at_once);
     }
     return launch_pdl(rope_append_fp8_kernel, dim3((unsigned)ctas), dim3(kRopeThreads), 0, stream, p);

@@ -77,6 +77,12 @@ def _table(page_table, lens, refs, device: int):
     return rows, width, stride, counted[0]
 
 
+def _ints(device: int, *sizes, dtype=torch.int32):
+    """A tensor of each size (views of one tensor that goes out of sight take the host four times as long)."""
+    on = torch.device("cuda", device)
+    return [torch.empty(n, dtype=dtype, device=on) for n in sizes]
+
+
 def fork_pages(page_table, lens, parents, refs, page_size: int, *, out=None, stream=None):
     """Rows that continue others (beam search, sampling several answers), begin empty, or end.
 
@@ -97,8 +103,7 @@ def fork_pages(page_table, lens, parents, refs, page_size: int, *, out=None, str
         raise ValueError("parents must be [rows]")
     new_rows = parents.shape[0]
     _dense(parents, "parents", torch.int32, parents.shape, device)
-    made = torch.empty(3 * new_rows + 1, dtype=torch.int32, device=page_table.device)
-    new_lens, src, dst, missing = made.split_with_sizes((new_rows, new_rows, new_rows, 1))
+    new_lens, src, dst, missing = _ints(device, new_rows, new_rows, new_rows, 1)
     if out is None:
         out = torch.empty((new_rows, width), dtype=torch.int32, device=page_table.device)
     elif out.data_ptr() == page_table.data_ptr() and out.numel():
@@ -128,8 +133,8 @@ def extend_pages(page_table, lens, cu_new, refs, page_size: int, tokens: int, *,
     _dense(cu_new, "cu_new", torch.int32, (rows + 1,), device)
     if tokens < 0:
         raise ValueError("tokens must not be negative")
-    positions, slots = torch.empty((2, tokens), dtype=torch.int64, device=page_table.device).unbind(0)
-    missing = torch.empty(1, dtype=torch.int32, device=page_table.device)
+    positions, slots = _ints(device, tokens, tokens, dtype=torch.int64)
+    missing, = _ints(device, 1)
     _launch("lowm_extend_pages", (
         page_table.data_ptr(), stride, lens.data_ptr(), rows, width, cu_new.data_ptr(), tokens, refs.data_ptr(), num_pages,
         page_size, positions.data_ptr(), slots.data_ptr(), missing.data_ptr()), max(4 * num_pages, 4), device,
@@ -150,8 +155,7 @@ def compact_pages(page_table, lens, refs, page_size: int, *, stream=None):
             return compact_pages(page_table, lens, refs, page_size)
     rows, width, stride, num_pages = _table(page_table, lens, refs, device)
     moves = num_pages // 2
-    made = torch.empty(2 * moves + 1, dtype=torch.int32, device=page_table.device)
-    src, dst, used = made.split_with_sizes((moves, moves, 1))
+    src, dst, used = _ints(device, moves, moves, 1)
     _launch("lowm_compact_pages", (
         page_table.data_ptr(), stride, lens.data_ptr(), rows, width, refs.data_ptr(), num_pages, page_size, src.data_ptr(),
         dst.data_ptr(), used.data_ptr()), lowm_compact_pages_workspace(num_pages), device, _current_stream(device))
@@ -177,17 +181,19 @@ def copy_pages(caches, src, dst, *, stream=None) -> None:
     _dense(dst, "dst", torch.int32, shape, device)
     spans = []
     num_pages = caches[0].size(0) if len(caches) and caches[0].dim() else 0
+    nbytes = page_bytes = -1                             # of the tensor before, mostly another layer's like it
     for x in caches:
-        if x.get_device() != device or x.dim() == 0 or x.size(0) != num_pages:
+        if x.get_device() != device or x.dim() == 0 or x.shape[0] != num_pages:
             raise ValueError("caches must be on cuda:%d and have one number of pages" % device)
         if x.is_contiguous():
-            page_bytes = page_stride = x.nbytes // num_pages if num_pages else 0
+            if x.nbytes != nbytes:
+                nbytes = x.nbytes
+                page_bytes = nbytes // num_pages if num_pages else 0
+            spans += (x.data_ptr(), page_bytes, page_bytes)
         else:
             if num_pages and not x[0].is_contiguous():
                 raise ValueError("the pages of a cache must be contiguous")
-            page_bytes = x[0].nbytes if num_pages else 0
-            page_stride = x.stride(0) * x.element_size()
-        spans += (x.data_ptr(), page_stride, page_bytes)
+            spans += (x.data_ptr(), x.stride(0) * x.element_size(), x[0].nbytes if num_pages else 0)
     held = array.array("q", spans)                       # as lowm_page_span_t lies in memory
     packed = held.buffer_info()[0]
     s = function("lowm_copy_pages")(packed, len(caches), src.data_ptr(), dst.data_ptr(), shape[0], num_pages,

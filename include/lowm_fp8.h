@@ -115,7 +115,8 @@ lowm_status_t lowm_rope_append_fp8(const void *q, int64_t q_token_stride, int64_
  * those of lowm_paged_attention.  What a page or a scale holds past a sequence's
  * length or before its window does not matter, NaN included; a NaN code reaches the
  * rows that see its token and no others.  An element of q that is not finite makes
- * its row NaN.  The result is deterministic.
+ * its row NaN, or zeros where it makes all of the row's scores -inf.  The result is
+ * deterministic.
  */
 lowm_status_t lowm_paged_attention_fp8(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                                        const void *k_cache, int64_t k_page_stride, int64_t k_place_stride,

@@ -25,8 +25,8 @@ EncodeTiledFn host_encode_fn();              // cuTensorMapEncodeTiled (for any 
 
 // Defined in paged_attention.cu: lowm_paged_attention with, when factors is not NULL (pages of 64 tokens then), factors
 // in [1, 2) of a key's scores (f) and of its value (v), fp32 and 16-byte aligned: one pair for each page and head
-// (tokens_a_factor 64), [num_pages][kv_heads] of f, log2(v), 1 / v and an unused number; or one for each key (1),
-// [num_pages][kv_heads][64 of f, 64 of v].
+// (tokens_a_factor 64), [num_pages][kv_heads] of f, log2(v), 1 / v and an unused number; one for each four keys (4),
+// [num_pages][kv_heads][16 of f, 16 of v]; or one for each key (1), [num_pages][kv_heads][64 of f, 64 of v].
 lowm_status_t attend_pages(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache, int64_t k_page_stride,
                            int64_t k_place_stride, int64_t k_cache_head_stride, const void *v_cache, int64_t v_page_stride,
                            int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size,

@@ -37,9 +37,9 @@
 // FACTORS: keys come with two factors in [1, 2), f for their scores and v for their values (what a cache of codes, widened to
 // bf16, has of its scales beside powers of two; paged_attention_fp8.cu).  v multiplies the weights before they are rounded,
 // and their sum leaves it out.  Pages then have 64 tokens, and a tile's factors arrive with its K.  Where a tile has one pair
-// (kTileFactors) they cost nothing; a pair for each key (kKeyFactors) costs 32 loads of 16 bytes and 64 packed multiplications
-// a row and tile (chunks of 1537 tokens over 9000 keys: 231 and 257 us,
-// the copy included).
+// (kTileFactors) they cost nothing; a pair for each key (kKeyFactors) costs 64 packed multiplications and 32 loads of 16 bytes
+// a row and tile, of which one for four keys (kQuadFactors) spares 24 (chunks of 1537 tokens over 9000 keys, the copy included:
+// 231, 257 and QUAD us).
 //
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.
@@ -88,7 +88,7 @@ struct AttnParams : LineParams<kTileRows, kItemCost, kMinShare> {
     int64_t k_page, k_place, k_head, v_page, v_place, v_head;
     const int32_t *table;
     const float *factors;                    // kTileFactors: [num_pages][kv_heads] of f, log2(v), 1 / v, unused;
-                                             // kKeyFactors: [num_pages][kv_heads][f, v][64]
+                                             // kQuadFactors, kKeyFactors: [num_pages][kv_heads][f, v][16 or 64]
     int page_size, page_shift, heads, slot_rows;
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
     float scale_inverse;                     // 1 / scale_log2
@@ -183,7 +183,7 @@ __device__ __forceinline__ uint64_t make_sw128_nmajor_desc(uint32_t saddr, uint3
 }
 
 // ------------------------------------------------------------------ shared memory
-enum { kNoFactors, kTileFactors, kKeyFactors };
+enum { kNoFactors, kTileFactors, kQuadFactors, kKeyFactors };
 
 template <int DIM, int FACTORS>
 struct AttnSmem {
@@ -203,13 +203,26 @@ struct AttnSmem {
     static constexpr uint32_t kNumBars = 2 * kStages + 9;
     static constexpr uint32_t kSlot = kBars + kNumBars * 8;             // TMEM address, edge word
     static constexpr uint32_t kFactors = FACTORS ? (kSlot + 16 + 127) / 128 * 128 : kSlot + 16;   // [slots]; copied in bulk
-    static constexpr uint32_t kFactorBytes = FACTORS == kTileFactors ? 16 : 2 * kTileKeys * 4;
+    static constexpr uint32_t kFactorBytes = FACTORS == kTileFactors ? 16 : 2 * kTileKeys * (FACTORS == kQuadFactors ? 1 : 4);
     // While the softmax is at tile j its weights are missing, so V of tile j keeps its stage, and K of tile
     // j + 2 + (kStages - 2) / 2 is the last that the ring lets in behind it.
     static constexpr uint32_t kFactorSlots = FACTORS ? (DIM == 128 ? 4 : 8) : 0;
     static_assert(!FACTORS || kFactorSlots > 2 + (kStages - 2) / 2, "a tile's factors would be overwritten while they are read");
     static constexpr uint32_t kBytes = kFactors + kFactorSlots * kFactorBytes;    // 112.2 KiB: two CTAs an SM
 };
+
+// The factors of keys k .. k + 3 of a tile (k a constant, a multiple of 4); from k = 64 on those of the values.
+template <int FACTORS>
+__device__ __forceinline__ float4 factors_of(const float4 *f, int k)
+{
+    if constexpr (FACTORS == kKeyFactors) {
+        return f[k / 4];
+    } else {
+        const float4 four = f[k / 16];           // (one load for the four calls of a 16)
+        const float x = k % 16 == 0 ? four.x : (k % 16 == 4 ? four.y : (k % 16 == 8 ? four.z : four.w));
+        return make_float4(x, x, x, x);
+    }
+}
 
 template <int DIM>
 __device__ __forceinline__ void store_row(const AttnParams &p, const Row &w, int col, const float (&v)[32])
@@ -367,6 +380,8 @@ __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows,
                 s += __shfl_xor_sync(0xffffffffu, s, o);
             if (FACTORS == kTileFactors)
                 s *= p.factors[(page * p.kv_heads + g) * 4];
+            if (FACTORS == kQuadFactors)
+                s *= p.factors[(page * p.kv_heads + g) * (kTileKeys / 2) + place / 4];
             if (FACTORS == kKeyFactors)
                 s *= p.factors[(page * p.kv_heads + g) * (2 * kTileKeys) + place];
             // (a weight too small for a float still carries an infinity)
@@ -665,10 +680,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         [[maybe_unused]] const float4 *f = nullptr;          // this tile's factors
                         if constexpr (FACTORS != kNoFactors)
                             f = reinterpret_cast<const float4 *>(smem + L::kFactors + g % L::kFactorSlots * L::kFactorBytes);
-                        if constexpr (FACTORS == kKeyFactors) {
+                        if constexpr (FACTORS == kKeyFactors || FACTORS == kQuadFactors) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) {
-                                const float4 a = f[k / 4], b = f[8 + k / 4];
+                                const float4 a = factors_of<FACTORS>(f, k), b = factors_of<FACTORS>(f, 32 + k);
                                 times2(s0[k], s0[k + 1], a.x, a.y);
                                 times2(s0[k + 2], s0[k + 3], a.z, a.w);
                                 times2(s1[k], s1[k + 1], b.x, b.y);
@@ -736,10 +751,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                             sum0 = add2(sum0, pack2(a, b));
                             sum1 = add2(sum1, pack2(c, d));
                             __nv_bfloat162 ab = __floats2bfloat162_rn(a, b), cd = __floats2bfloat162_rn(c, d);
-                            if constexpr (FACTORS == kKeyFactors) {
+                            if constexpr (FACTORS == kKeyFactors || FACTORS == kQuadFactors) {
                                 if (k % 4 == 0) {
-                                    v0 = f[kTileKeys / 4 + k / 4];
-                                    v1 = f[kTileKeys / 4 + 8 + k / 4];
+                                    v0 = factors_of<FACTORS>(f, kTileKeys + k);
+                                    v1 = factors_of<FACTORS>(f, kTileKeys + 32 + k);
                                 }
                                 const float2 u = unpack2(mul2(pack2(a, b), k % 4 ? pack2(v0.z, v0.w) : pack2(v0.x, v0.y)));
                                 const float2 w = unpack2(mul2(pack2(c, d), k % 4 ? pack2(v1.z, v1.w) : pack2(v1.x, v1.y)));
@@ -1091,6 +1106,9 @@ lowm_status_t lowm::attend_pages(
     if (tokens_a_factor == kTileKeys)
         return dim == 64 ? launch_attention<64, kTileFactors>(map_k, map_v, p, sms, stream)
                          : launch_attention<128, kTileFactors>(map_k, map_v, p, sms, stream);
+    if (tokens_a_factor == 4)
+        return dim == 64 ? launch_attention<64, kQuadFactors>(map_k, map_v, p, sms, stream)
+                         : launch_attention<128, kQuadFactors>(map_k, map_v, p, sms, stream);
     return dim == 64 ? launch_attention<64, kKeyFactors>(map_k, map_v, p, sms, stream)
                      : launch_attention<128, kKeyFactors>(map_k, map_v, p, sms, stream);
 }

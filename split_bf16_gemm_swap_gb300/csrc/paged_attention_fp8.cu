@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Att
 // reach 0.15; but writing and reading 2 bytes an element takes its time, and a launch more.  A code times a power of two is
 // a bf16 number, so K and V keep their scales' powers of two, and the mantissas, in [1, 2), multiply scores and weights (V
 // rounded with its scale made the result's error 0.0027 of it where its own rounding is 0.0017).  A tile of the copy has one
-// scale where a block is not shorter, else one for each key.
+// scale where a block is not shorter, else one for each four keys, or for each.
 // The rule counts the multiply-adds of all rows with all keys that the table has room for (a key's exponentials as 64 of
 // them): us in the registers and widened at 8 sequences x 16 tokens x 4000 keys (of 32 / 8 heads of 128) 40, 58; 8 x 32 x
 // 16000 175, 141; 8 x 64 x 8000 250, 135; 2 x 64 x 4000 54, 47; 1 x 300 x 1000 (16 / 8 heads) 30, 35.
@@ -720,7 +720,7 @@ struct WidenParams {
     float *factors;                          // [batch * pages][kv_heads] of what attend_pages takes
     int32_t *wide_table;                     // [batch][pages]
     int page_shift, block_shift, batch, q_tokens, kv_heads, window, capacity, pages;
-    bool tile_factors;
+    int tokens_a_factor;                     // 64, 4 or 1
 };
 
 __device__ __forceinline__ void widen_16(uint4 codes, float scale, uint4 *to)
@@ -793,12 +793,14 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams 
             float k_rest, v_rest;
             const float k_power = split_scale(ks[u], k_rest);
             const float v_power = split_scale(fminf(fmaxf(vs[u], 1.f / kMaxScale), kMaxScale), v_rest);
-            if (chunk == 0 && p.tile_factors) {
-                if (key == 0)
+            if (chunk == 0 && key % p.tokens_a_factor == 0) {
+                if (p.tokens_a_factor == kWideKeys) {
                     reinterpret_cast<float4 *>(p.factors)[task] = make_float4(k_rest, log2f(v_rest), 1.f / v_rest, 0.f);
-            } else if (chunk == 0) {
-                p.factors[2 * task * kWideKeys + key] = k_rest;
-                p.factors[(2 * task + 1) * kWideKeys + key] = v_rest;
+                } else {
+                    const int n = kWideKeys / p.tokens_a_factor, at = key / p.tokens_a_factor;
+                    p.factors[2 * task * n + at] = k_rest;
+                    p.factors[(2 * task + 1) * n + at] = v_rest;
+                }
             }
             if (key0 + key >= end)
                 continue;
@@ -999,7 +1001,7 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
         w.table = page_table;
         w.kv_lens = kv_lens;
         w.cu_q = cu_q;
-        w.tile_factors = block >= kWideKeys;
+        w.tokens_a_factor = block >= kWideKeys ? kWideKeys : (block >= 4 ? 4 : 1);
         w.page_shift = log2_of(page_size);
         w.block_shift = log2_of(block);
         w.batch = batch;
@@ -1023,7 +1025,7 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
             return st;
         return attend_pages(q, q_token_stride, q_head_stride, w.wide_k, kv_heads * head, dim, head, w.wide_v, kv_heads * head, dim,
                             head, tasks, kWideKeys, w.wide_table, w.pages, w.pages, kv_lens, cu_q, out, out_token_stride,
-                            out_head_stride, lse, batch, q_tokens, heads, kv_heads, dim, scale, window, w.factors, w.tile_factors ? kWideKeys : 1,
+                            out_head_stride, lse, batch, q_tokens, heads, kv_heads, dim, scale, window, w.factors, w.tokens_a_factor,
                             at + used, workspace_bytes - used, stream);
     }
     unsigned int *status = host_status_word();

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstring>
@@ -23,10 +24,16 @@ lowm_status_t host_check_device(int *sms);   // LOWM_OK on sm_103; the SM count
 unsigned int *host_status_word();            // device address of the status word, or nullptr
 EncodeTiledFn host_encode_fn();              // cuTensorMapEncodeTiled (for any host thread), or nullptr
 
+// What attend_pages takes scores to exponents of 2 with; their sign is in Q.  Never 0, so that a masked score (-inf) stays one.
+inline float attend_scale_log2(float scale)
+{
+    return std::max((scale < 0.f ? -scale : scale) * 1.44269504088896340736f, 1e-30f);
+}
+
 // Defined in paged_attention.cu: lowm_paged_attention with, when factors is not NULL (pages of 64 tokens then), factors
-// in [1, 2) of a key's scores (f) and of its value (v), fp32 and 16-byte aligned: one pair for each page and head
-// (tokens_a_factor 64), [num_pages][kv_heads] of f, log2(v), 1 / v and an unused number; one for each four keys (4),
-// [num_pages][kv_heads][16 of f, 16 of v]; or one for each key (1), [num_pages][kv_heads][64 of f, 64 of v].
+// in [1, 2) of a key's scores (f) and of its value (v), fp32 and 16-byte aligned, [num_pages][kv_heads] of: f, log2(v), 1 / v
+// and an unused number for the page (tokens_a_factor 64); 16 f, 16 log2(v) / attend_scale_log2 and 16 1 / v, for four keys
+// each (4); 64 f and 64 v (1).
 lowm_status_t attend_pages(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache, int64_t k_page_stride,
                            int64_t k_place_stride, int64_t k_cache_head_stride, const void *v_cache, int64_t v_page_stride,
                            int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size,

@@ -36,10 +36,11 @@
 //
 // FACTORS: keys come with two factors in [1, 2), f for their scores and v for their values (what a cache of codes, widened to
 // bf16, has of its scales beside powers of two; paged_attention_fp8.cu).  v multiplies the weights before they are rounded,
-// and their sum leaves it out.  Pages then have 64 tokens, and a tile's factors arrive with its K.  Where a tile has one pair
-// (kTileFactors) they cost nothing; a pair for each key (kKeyFactors) costs 64 packed multiplications and 32 loads of 16 bytes
-// a row and tile, of which one for four keys (kQuadFactors) spares 24 (chunks of 1537 tokens over 9000 keys, the copy included:
-// 231, 257 and QUAD us).
+// and their sum leaves it out.  Pages then have 64 tokens, and a tile's factors arrive with its K.  A pair for the tile
+// (kTileFactors) costs nothing, and v is in the exponent, where the largest weight, v included, is 1 and not rounded.  So it is
+// with a pair for four keys (kQuadFactors): a multiply-add for each score, one for the sum, and 12 loads of 16 bytes a row and
+// tile.  A pair for each key (kKeyFactors) would take 48 loads that way (270 us); it has 32 and multiplies the weights.  Chunks
+// of 1537 tokens over 9000 keys, the copy included: 231, 248 and 259 us; errors 0.0021, 0.0022 and 0.0024 of the result.
 //
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.
@@ -87,8 +88,7 @@ struct AttnParams : LineParams<kTileRows, kItemCost, kMinShare> {
     int64_t q_ts, q_hs, o_ts, o_hs, table_stride, num_pages;
     int64_t k_page, k_place, k_head, v_page, v_place, v_head;
     const int32_t *table;
-    const float *factors;                    // kTileFactors: [num_pages][kv_heads] of f, log2(v), 1 / v, unused;
-                                             // kQuadFactors, kKeyFactors: [num_pages][kv_heads][f, v][16 or 64]
+    const float *factors;                    // as for attend_pages
     int page_size, page_shift, heads, slot_rows;
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
     float scale_inverse;                     // 1 / scale_log2
@@ -111,6 +111,13 @@ __device__ __forceinline__ float ex2(float x)
 __device__ __forceinline__ void times2(uint32_t &x, uint32_t &y, float a, float b)
 {
     const float2 v = unpack2(mul2(pack2(x, y), pack2(a, b)));
+    x = __float_as_uint(v.x);
+    y = __float_as_uint(v.y);
+}
+
+__device__ __forceinline__ void times_plus2(uint32_t &x, uint32_t &y, float a, float b)
+{
+    const float2 v = unpack2(fma2(pack2(x, y), pack2(a, a), pack2(b, b)));
     x = __float_as_uint(v.x);
     y = __float_as_uint(v.y);
 }
@@ -203,7 +210,7 @@ struct AttnSmem {
     static constexpr uint32_t kNumBars = 2 * kStages + 9;
     static constexpr uint32_t kSlot = kBars + kNumBars * 8;             // TMEM address, edge word
     static constexpr uint32_t kFactors = FACTORS ? (kSlot + 16 + 127) / 128 * 128 : kSlot + 16;   // [slots]; copied in bulk
-    static constexpr uint32_t kFactorBytes = FACTORS == kTileFactors ? 16 : 2 * kTileKeys * (FACTORS == kQuadFactors ? 1 : 4);
+    static constexpr uint32_t kFactorBytes = FACTORS == kTileFactors ? 16 : (FACTORS == kQuadFactors ? 3 * kTileKeys : 8 * kTileKeys);
     // While the softmax is at tile j its weights are missing, so V of tile j keeps its stage, and K of tile
     // j + 2 + (kStages - 2) / 2 is the last that the ring lets in behind it.
     static constexpr uint32_t kFactorSlots = FACTORS ? (DIM == 128 ? 4 : 8) : 0;
@@ -211,17 +218,11 @@ struct AttnSmem {
     static constexpr uint32_t kBytes = kFactors + kFactorSlots * kFactorBytes;    // 112.2 KiB: two CTAs an SM
 };
 
-// The factors of keys k .. k + 3 of a tile (k a constant, a multiple of 4); from k = 64 on those of the values.
-template <int FACTORS>
-__device__ __forceinline__ float4 factors_of(const float4 *f, int k)
+// kQuadFactors: number k / 4 of a tile's (k a constant; one load serves four of them).
+__device__ __forceinline__ float quad_of(const float4 *f, int k)
 {
-    if constexpr (FACTORS == kKeyFactors) {
-        return f[k / 4];
-    } else {
-        const float4 four = f[k / 16];           // (one load for the four calls of a 16)
-        const float x = k % 16 == 0 ? four.x : (k % 16 == 4 ? four.y : (k % 16 == 8 ? four.z : four.w));
-        return make_float4(x, x, x, x);
-    }
+    const float4 four = f[k / 16];
+    return k % 16 < 4 ? four.x : (k % 16 < 8 ? four.y : (k % 16 < 12 ? four.z : four.w));
 }
 
 template <int DIM>
@@ -381,7 +382,7 @@ __device__ __noinline__ void add_edge_values(const AttnParams &p, unsigned rows,
             if (FACTORS == kTileFactors)
                 s *= p.factors[(page * p.kv_heads + g) * 4];
             if (FACTORS == kQuadFactors)
-                s *= p.factors[(page * p.kv_heads + g) * (kTileKeys / 2) + place / 4];
+                s *= p.factors[(page * p.kv_heads + g) * (3 * kTileKeys / 4) + place / 4];
             if (FACTORS == kKeyFactors)
                 s *= p.factors[(page * p.kv_heads + g) * (2 * kTileKeys) + place];
             // (a weight too small for a float still carries an infinity)
@@ -680,14 +681,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         [[maybe_unused]] const float4 *f = nullptr;          // this tile's factors
                         if constexpr (FACTORS != kNoFactors)
                             f = reinterpret_cast<const float4 *>(smem + L::kFactors + g % L::kFactorSlots * L::kFactorBytes);
-                        if constexpr (FACTORS == kKeyFactors || FACTORS == kQuadFactors) {
+                        if constexpr (FACTORS == kKeyFactors) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) {
-                                const float4 a = factors_of<FACTORS>(f, k), b = factors_of<FACTORS>(f, 32 + k);
+                                const float4 a = f[k / 4], b = f[8 + k / 4];
                                 times2(s0[k], s0[k + 1], a.x, a.y);
                                 times2(s0[k + 2], s0[k + 3], a.z, a.w);
                                 times2(s1[k], s1[k + 1], b.x, b.y);
                                 times2(s1[k + 2], s1[k + 3], b.z, b.w);
+                            }
+                        }
+                        if constexpr (FACTORS == kQuadFactors) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                const float a = quad_of(f, k), b = quad_of(f, 32 + k), x = quad_of(f, 64 + k), y = quad_of(f, 96 + k);
+                                times_plus2(s0[k], s0[k + 1], a, x);
+                                times_plus2(s0[k + 2], s0[k + 3], a, x);
+                                times_plus2(s1[k], s1[k + 1], b, y);
+                                times_plus2(s1[k + 2], s1[k + 3], b, y);
                             }
                         }
                         if (key0 < all_lo || key0 + kTileKeys - 1 > all_hi) {
@@ -748,13 +759,19 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                             const float2 x = unpack2(fma2(pack2(s0[k], s0[k + 1]), scale2, shift2));
                             const float2 y = unpack2(fma2(pack2(s1[k], s1[k + 1]), scale2, shift2));
                             const float a = ex2(x.x), b = ex2(x.y), c = ex2(y.x), d = ex2(y.y);
-                            sum0 = add2(sum0, pack2(a, b));
-                            sum1 = add2(sum1, pack2(c, d));
+                            if constexpr (FACTORS == kQuadFactors) {
+                                const float v = quad_of(f, 128 + k), w = quad_of(f, 160 + k);
+                                sum0 = fma2(pack2(a, b), pack2(v, v), sum0);
+                                sum1 = fma2(pack2(c, d), pack2(w, w), sum1);
+                            } else {
+                                sum0 = add2(sum0, pack2(a, b));
+                                sum1 = add2(sum1, pack2(c, d));
+                            }
                             __nv_bfloat162 ab = __floats2bfloat162_rn(a, b), cd = __floats2bfloat162_rn(c, d);
-                            if constexpr (FACTORS == kKeyFactors || FACTORS == kQuadFactors) {
+                            if constexpr (FACTORS == kKeyFactors) {
                                 if (k % 4 == 0) {
-                                    v0 = factors_of<FACTORS>(f, kTileKeys + k);
-                                    v1 = factors_of<FACTORS>(f, kTileKeys + 32 + k);
+                                    v0 = f[kTileKeys / 4 + k / 4];
+                                    v1 = f[kTileKeys / 4 + 8 + k / 4];
                                 }
                                 const float2 u = unpack2(mul2(pack2(a, b), k % 4 ? pack2(v0.z, v0.w) : pack2(v0.x, v0.y)));
                                 const float2 w = unpack2(mul2(pack2(c, d), k % 4 ? pack2(v1.z, v1.w) : pack2(v1.x, v1.y)));
@@ -1082,8 +1099,7 @@ lowm_status_t lowm::attend_pages(
     p.window = window < kMaxKeys ? window : 0;
     p.slot_rows = slot_rows_of(q_tokens, heads, kv_heads);
     p.capacity = (int)capacity;
-    // Never 0, so that a masked score (-inf) stays one.
-    p.scale_log2 = std::max((scale < 0.f ? -scale : scale) * 1.44269504088896340736f, 1e-30f);
+    p.scale_log2 = attend_scale_log2(scale);
     p.scale_inverse = 1.f / p.scale_log2;
     p.q_sign = scale < 0.f ? -1.f : 1.f;
     p.q_vec = is_aligned(q, 16) && !((q_token_stride | q_head_stride) & 7);

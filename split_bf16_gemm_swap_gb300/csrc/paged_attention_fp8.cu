@@ -721,6 +721,7 @@ struct WidenParams {
     int32_t *wide_table;                     // [batch][pages]
     int page_shift, block_shift, batch, q_tokens, kv_heads, window, capacity, pages;
     int tokens_a_factor;                     // 64, 4 or 1
+    float scale_inverse;                     // of attend_pages
 };
 
 __device__ __forceinline__ void widen_16(uint4 codes, float scale, uint4 *to)
@@ -796,10 +797,14 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams 
             if (chunk == 0 && key % p.tokens_a_factor == 0) {
                 if (p.tokens_a_factor == kWideKeys) {
                     reinterpret_cast<float4 *>(p.factors)[task] = make_float4(k_rest, log2f(v_rest), 1.f / v_rest, 0.f);
+                } else if (p.tokens_a_factor == 4) {
+                    float *to = p.factors + 3 * task * (kWideKeys / 4) + key / 4;
+                    to[0] = k_rest;
+                    to[kWideKeys / 4] = log2f(v_rest) * p.scale_inverse;
+                    to[2 * kWideKeys / 4] = 1.f / v_rest;
                 } else {
-                    const int n = kWideKeys / p.tokens_a_factor, at = key / p.tokens_a_factor;
-                    p.factors[2 * task * n + at] = k_rest;
-                    p.factors[(2 * task + 1) * n + at] = v_rest;
+                    p.factors[2 * task * kWideKeys + key] = k_rest;
+                    p.factors[(2 * task + 1) * kWideKeys + key] = v_rest;
                 }
             }
             if (key0 + key >= end)
@@ -1001,6 +1006,7 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
         w.table = page_table;
         w.kv_lens = kv_lens;
         w.cu_q = cu_q;
+        w.scale_inverse = 1.f / attend_scale_log2(scale);
         w.tokens_a_factor = block >= kWideKeys ? kWideKeys : (block >= 4 ? 4 : 1);
         w.page_shift = log2_of(page_size);
         w.block_shift = log2_of(block);

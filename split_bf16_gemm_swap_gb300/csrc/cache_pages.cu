@@ -2,12 +2,12 @@
 // compact page tables, and copy pages.
 //
 // The tables are whole numbers and small; what these kernels cost is the chain of
-// launches and memory latencies, so each operator is one to three launches.
+// launches and memory latencies, so each operator is one launch where it is small, three at most.
 // Reference counts change by integer atomics, whose order does not matter; free
 // pages are ranked by scans over the counts, in rising order, by one CTA (fork,
 // extend: it stops at the last page it needs) or by chunks (compact).  Copies are
 // bound by bandwidth.  A fork with its copies and growth: 8 rows on 149 pages, 16
-// tensors 13 us, 128 rows, 32 tensors 25; a pool of 4096 pages brought together 61,
+// tensors 13 us, 128 rows, 32 tensors 25; a pool of 4096 pages brought together 58,
 // 46 of them its copies (250 MB, 5.4 TB/s).
 #include <algorithm>
 #include <climits>
@@ -375,6 +375,22 @@ __global__ void __launch_bounds__(kChunkThreads) rank_pages_kernel(const Pool po
         *used = total;
 }
 
+// The entries first, first + step, ... of a row, whose pages may have moved.
+__device__ __forceinline__ void move_row(const Table &table, const Pool &pool, const int32_t *ranks, const int32_t *src,
+                                         const int32_t *dst, int total, int row, int first, int step)
+{
+    const int n = used_of(table.lens[row], pool, table.width);
+    for (int j = first; j < n; j += step) {
+        int32_t *e = table.entries + row * table.stride + j;
+        // (a page that no count knows has no place to go to)
+        if (*e >= total && *e < pool.pages) {
+            const int r = ranks[*e];
+            if (r >= 0 && r < pool.pages / 2 && src[r] == *e)
+                *e = dst[r];
+        }
+    }
+}
+
 // The first `rows` CTAs have a row of the table each, the others the counts of the pages that move.
 __global__ void __launch_bounds__(128) move_entries_kernel(const Table table, const Pool pool, const int32_t *ranks, const int32_t *src,
                                                            const int32_t *dst, const int32_t *used)
@@ -383,22 +399,63 @@ __global__ void __launch_bounds__(128) move_entries_kernel(const Table table, co
     ptx::griddep_launch_dependents();
     const int row = (int)blockIdx.x;
     if (row < table.rows) {
-        const int n = used_of(table.lens[row], pool, table.width), total = *used;
-        for (int j = threadIdx.x; j < n; j += 128) {
-            int32_t *e = table.entries + row * table.stride + j;
-            // (a page that no count knows has no place to go to)
-            if (*e >= total && *e < pool.pages) {
-                const int r = ranks[*e];
-                if (r >= 0 && r < pool.pages / 2 && src[r] == *e)
-                    *e = dst[r];
-            }
-        }
+        move_row(table, pool, ranks, src, dst, *used, row, threadIdx.x, 128);
         return;
     }
     for (int64_t i = (int64_t)(row - table.rows) * 128 + threadIdx.x; i < pool.pages / 2; i += (int64_t)(gridDim.x - table.rows) * 128) {
         const int from = src[i];
         if (from < 0)
             break;
+        pool.refs[dst[i]] = pool.refs[from];
+        pool.refs[from] = 0;
+    }
+}
+
+// A small pool and table: all of it by one CTA, whose threads have kHereEach pages each.  us, one launch and three: 8 rows of 25
+// on 200 pages 3.2, 5.3; 41 of 100 on 4096 5.2, 7.0; 64 of 256 on 8192 7.8, 7.1; 128 of 512 16.8, 6.8.
+constexpr int kHereEach = 4, kHerePages = kHereEach * kPageThreads, kHereEntries = 4096;
+
+__global__ void __launch_bounds__(kPageThreads) compact_here_kernel(const Table table, const Pool pool, int32_t *ranks, int32_t *src,
+                                                                    int32_t *dst, int32_t *used)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int first = threadIdx.x * kHereEach;
+    bool full[kHereEach];
+    int n = 0, total, stay;
+#pragma unroll
+    for (int k = 0; k < kHereEach; ++k) {
+        full[k] = first + k < pool.pages && pool.refs[first + k] != 0;
+        n += full[k];
+    }
+    int rank = scan_block(n, total), before = 0;
+#pragma unroll
+    for (int k = 0; k < kHereEach; ++k)
+        before += full[k] && first + k < total;
+    (void)scan_block(before, stay);
+    const int moves = total - stay;
+#pragma unroll
+    for (int k = 0; k < kHereEach; ++k) {
+        const int i = first + k;
+        if (i >= pool.pages)
+            break;
+        if (full[k] && i >= total) {
+            ranks[i] = rank - stay;
+            src[rank - stay] = i;
+        } else if (!full[k] && i < total) {
+            dst[i - rank] = i;
+        }
+        rank += full[k];
+    }
+    for (int i = moves + threadIdx.x; i < pool.pages / 2; i += kPageThreads)
+        src[i] = dst[i] = -1;
+    if (threadIdx.x == 0)
+        *used = total;
+    __syncthreads();
+    for (int row = threadIdx.x >> 5; row < table.rows; row += kPageThreads / 32)
+        move_row(table, pool, ranks, src, dst, total, row, threadIdx.x & 31, 32);
+    for (int i = threadIdx.x; i < moves; i += kPageThreads) {
+        const int from = src[i];
         pool.refs[dst[i]] = pool.refs[from];
         pool.refs[from] = 0;
     }
@@ -554,6 +611,8 @@ extern "C" lowm_status_t lowm_compact_pages(int32_t *page_table, int64_t table_s
     const Table table = {page_table, table_stride, lens, rows, width};
     const Pool pool = {refs, num_pages, page_size};
     int32_t *ranks = static_cast<int32_t *>(workspace), *counts = ranks + num_pages;
+    if (num_pages <= kHerePages && (int64_t)rows * width <= kHereEntries)
+        return launch_pdl(compact_here_kernel, dim3(1), dim3(kPageThreads), 0, stream, table, pool, ranks, src, dst, used);
     const unsigned chunks = (unsigned)((num_pages - 1) / kChunk + 1);
     if ((st = launch_pdl(count_used_kernel, dim3(chunks), dim3(kChunkThreads), 0, stream, pool, counts)) != LOWM_OK ||
         (st = launch_pdl(rank_pages_kernel, dim3(chunks), dim3(kChunkThreads), 0, stream, pool, counts, ranks, src, dst, used)) != LOWM_OK)

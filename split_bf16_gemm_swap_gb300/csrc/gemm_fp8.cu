@@ -660,12 +660,21 @@ lowm_status_t encode_matrix(const void *base, int rows, int K, int box_rows, int
 
 constexpr int kSmem = 227 * 1024;
 
+// CTAs that find an SM each in clusters of `split`: a cluster lies in one GPC (of 152 SMs 144 in fours and 120 in eights, by
+// cudaOccupancyMaxActiveClusters).
+int room_of(int split, int sms) { return split >= 8 ? sms * 15 / 19 : (split >= 4 ? sms * 18 / 19 : sms); }
+
 // Ranks along K as long as the CTAs find an SM, or, with up to 16 tokens, half of one (us at N 6144, K 4096, split 1, 2, 4: 4
-// tokens 10.1, 7.4, 6.6; 32 tokens 11.9, 9.3, 9.7; 64 tokens 13.4, 11.4, 18.7; 128 tokens 18.5, 15.6, 26.5).
+// tokens 10.1, 7.4, 6.6; 32 tokens 11.9, 9.3, 9.7; 64 tokens 13.4, 11.4, 18.7; 128 tokens 18.5, 15.6, 26.5), and with 32 half
+// of one where clusters leave SMs out.  The exchange grows with the tokens (N 1024, K 4096, split 4, 8: 64 tokens 10.6, 9.9; 128
+// tokens 13.7, 14.5), and clusters that have to wait cost most (N 2304, K 4096, split 4, 8: 32 tokens, two CTAs an SM, 9.1, 8.3;
+// 64 tokens 10.8, 17.8; 128 tokens 14.0, 25.7).
 int split_of(int m_pad, int tiles, int blocks, int sms)
 {
+    const int most = m_pad <= 64 ? std::min(m_pad / 4, kMaxSplit) : 4;
+    auto room = [&](int split) { return m_pad <= 16 ? 2 * room_of(split, sms) : (m_pad <= 32 ? sms : room_of(split, sms)); };
     int split = 1;
-    while (split < std::min(m_pad / 4, kMaxSplit) && tiles * split * 2 <= (m_pad <= 16 ? 2 : 1) * sms && blocks >= 4 * split)
+    while (split < most && tiles * split * 2 <= room(split * 2) && blocks >= 4 * split)
         split *= 2;
     return split;
 }
@@ -677,7 +686,7 @@ lowm_status_t launch_gemm_fp8(const void *A, const void *W, Gemm8Params &p, int 
     const int tiles = (p.N + kTileN - 1) / kTileN;
     const int split = split_of(M_PAD, tiles, p.blocks, sms);
     // Two CTAs an SM hide each other's ends (4 tokens, N 49152: 37.7 -> 36.2 us); more tokens take an SM's registers.
-    const bool two = M_PAD <= 32 && tiles * split > sms;
+    const bool two = M_PAD <= 32 && tiles * split > room_of(split, sms);
     // A copy costs much the same whatever its size (K blocks a copy 1, 2: 4 tokens, N 49152 48.1, 37.7 us).
     p.per_stage = 2;
     const int mailbox = split > 1 ? M_PAD * kTileN * 4 : 0;

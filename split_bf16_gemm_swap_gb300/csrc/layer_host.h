@@ -33,7 +33,8 @@ inline float attend_scale_log2(float scale)
 // Defined in paged_attention.cu: lowm_paged_attention with, when factors is not NULL (pages of 64 tokens then), factors
 // in [1, 2) of a key's scores (f) and of its value (v), fp32 and 16-byte aligned, [num_pages][kv_heads] of: f, log2(v), 1 / v
 // and an unused number for the page (tokens_a_factor 64); 16 f, 16 log2(v) / attend_scale_log2 and 16 1 / v, for four keys
-// each (4); 64 f and 64 v (1).
+// each (4); 64 f and 64 v (1).  The first page of a sequence with new tokens is read even where it has no keys: its factors
+// are finite.
 lowm_status_t attend_pages(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache, int64_t k_page_stride,
                            int64_t k_place_stride, int64_t k_cache_head_stride, const void *v_cache, int64_t v_page_stride,
                            int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size,

@@ -473,10 +473,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             do {
                 const int from = c.from, n = c.to - c.from;
                 const int32_t *pages = p.table + it.b * p.table_stride;
-                // Table entries of this lane's box for the newest K tile and the V tile behind it.
+                // Table entries of this lane's box for the newest K tile and the V tile behind it.  (With factors a sequence without
+                // keys has a page, too, for its masked tile's.)
                 auto entry = [&](int tile) {
                     const int key = (it.first_tile + tile) * kTileKeys + mine * box_keys;
-                    return mine < boxes && key < it.kv ? pages[key >> p.page_shift] : -1;
+                    return mine < boxes && (FACTORS || key < it.kv) ? pages[key >> p.page_shift] : -1;
                 };
                 int page_k = entry(from), page_v = page_k, page_next = n > 1 ? entry(from + 1) : -1;
                 auto load = [&](const CUtensorMap *map, int tile, int page) {
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                     const int key0 = (it.first_tile + tile) * kTileKeys;
                     // Pages past the sequence's end are not requested.
                     const int used = min(boxes, max(1, (it.kv - key0 + box_keys - 1) / box_keys));
-                    const bool factors = FACTORS && map == &map_k && __shfl_sync(0xffffffffu, page, 0) >= 0;   // (a tile is a page)
+                    const bool factors = FACTORS && map == &map_k;           // (a tile is a page)
                     if (lane == 0)
                         ptx::mbar_arrive_expect_tx(bar_full + 8 * s,
                                                    (uint32_t)used * box_keys * DIM * 2 + (factors ? L::kFactorBytes : 0));
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                             bulk_load(sbase + L::kFactors + keys_loaded % L::kFactorSlots * L::kFactorBytes,
                                       p.factors + ((int64_t)page * p.kv_heads + it.head) * (L::kFactorBytes / 4), L::kFactorBytes,
                                       bar_full + 8 * s);
-                        keys_loaded += map == &map_k;
+                        keys_loaded += factors;
                     }
                     if (mine < used)
                         tma_load_4d(sbase + L::kRing + s * L::kTileBytes + half * (kTileKeys * 128) + mine * box_keys * 128,

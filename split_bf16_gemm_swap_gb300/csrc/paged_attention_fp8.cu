@@ -768,7 +768,8 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams 
         const int kv = min(max(p.kv_lens[b], 0), p.capacity);
         const int first = p.window > 0 ? kv - q_len - p.window + 1 : 0;      // no row sees a key before it
         const int key0 = j * kWideKeys, end = min(kv, key0 + kWideKeys);
-        if (q_len == 0 || key0 >= kv || key0 + kWideKeys <= first)
+        // (the first page of a sequence without keys has no keys either, but factors, which its rows' masked tile meets)
+        if (q_len == 0 || key0 >= max(kv, 1) || key0 + kWideKeys <= first)
             continue;
         uint4 k[kSteps], v[kSteps];
         float ks[kSteps], vs[kSteps];

@@ -792,3 +792,31 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         fp8.rope_append_fp8(q, q, q, torch.ones(4, 64, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda"),
                             torch.zeros(2, dtype=torch.int64, device="cuda"), kc, vc, ks, vs)
+
+
+def left_in_shared_memory(byte):
+    """Leaves `byte` in most of every SM's shared memory: the ring of a product whose weights hold nothing else."""
+    w = torch.full((152 * 128, 4096), byte, dtype=torch.uint8, device="cuda").view(FP8)
+    a, sa = fp8.quantize_fp8(rand(64, 4096, seed=1))
+    fp8.gemm_fp8(a, w, torch.ones(152, 32, device="cuda"), sa)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("block", [1, 4, 16, 64, 128])
+@pytest.mark.parametrize("byte", [0x00, 0xbf, 0xff])                # of fp32 words: 0, a negative number, NaN
+def test_attention_of_chunks_without_keys(dim, block, byte):
+    page = max(block, 16)
+    lens, q_lens = [0, -3, 40, 0, 300, 0], [150, 120, 200, 0, 100, 500]
+    kc, vc, ks, vs, table = make_cache(lens, page, block, 2, dim, seed=1, width=ROOM // page)
+    cu = [sum(q_lens[:i]) for i in range(7)]
+    assert widened(6, cu[-1] + 3, 8, 2, dim, page, ROOM // page)
+    q = rand(cu[-1] + 3, 8, dim, seed=2)
+    kv, cu_q = torch.tensor(lens, device="cuda", dtype=torch.int32), torch.tensor(cu, device="cuda", dtype=torch.int32)
+    for window in (0, 50):
+        want, tol, lse = attention64(q, kc, vc, ks, vs, table, lens, cu_q, 0.125, window, True)
+        for _ in range(3):
+            left_in_shared_memory(byte)
+            out, got = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu_q, scale=0.125, window=window, return_lse=True)
+            bounded(out, want, tol, "attention")
+            assert torch.equal(torch.isneginf(got), torch.isneginf(lse)) and not torch.isnan(got).any()
+    in_order()

@@ -891,7 +891,7 @@ int64_t wide_bytes(int batch, int kv_heads, int dim, int page_size, int table_wi
 bool widens(int batch, int q_tokens, int heads, int kv_heads, int dim, int page_size, int table_width)
 {
     const double keys = (double)wide_pages(page_size, table_width) * kWideKeys;
-    return (int64_t)q_tokens * (heads / kv_heads) >= (int64_t)kWideRows * std::max(batch, 1) &&
+    return batch > 0 && (int64_t)q_tokens * (heads / kv_heads) >= (int64_t)kWideRows * batch &&
            4.0 * q_tokens * heads * keys * (dim + 64) >= kWideWork &&
            2.0 * batch * wide_pages(page_size, table_width) * kWideKeys * kv_heads * dim * 2 <= (double)kWideBytes;
 }

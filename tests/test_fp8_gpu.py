@@ -820,3 +820,11 @@ def test_attention_of_chunks_without_keys(dim, block, byte):
             bounded(out, want, tol, "attention")
             assert torch.equal(torch.isneginf(got), torch.isneginf(lse)) and not torch.isnan(got).any()
     in_order()
+
+
+@pytest.mark.parametrize("rows,width", [(3, 4), (700, 4), (700, ROOM // 16)])
+def test_attention_of_an_empty_batch_with_many_rows(rows, width):
+    kc, vc, ks, vs, table = make_cache([5], 16, 8, 2, 64, width=width)
+    none, cu = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = fp8.paged_attention_fp8(rand(rows, 4, 64), kc, vc, ks, vs, table[:0], none, cu, return_lse=True)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())

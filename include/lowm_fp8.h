@@ -112,7 +112,8 @@ lowm_status_t lowm_rope_append_fp8(const void *q, int64_t q_token_stride, int64_
  *   k_scale, v_scale  any fp32 numbers; v_scale is taken as 2^-50 .. 2^50
  *   block         a power of two, at most page_size
  * The other arguments, their limits and what a row that sees nothing gets are
- * those of lowm_paged_attention.  What a page or a scale holds past a sequence's
+ * those of lowm_paged_attention.  A length that the table has no room for counts as the
+ * table's room.  What a page or a scale holds past a sequence's
  * length or before its window does not matter, NaN included; a NaN code reaches the
  * rows that see its token and no others.  An element of q that is not finite makes
  * its row NaN, or zeros where it makes all of the row's scores -inf.  The result is

@@ -30,18 +30,24 @@ inline float attend_scale_log2(float scale)
     return std::max((scale < 0.f ? -scale : scale) * 1.44269504088896340736f, 1e-30f);
 }
 
-// Defined in paged_attention.cu: lowm_paged_attention with, when factors is not NULL (pages of 64 tokens then), factors
-// in [1, 2) of a key's scores (f) and of its value (v), fp32 and 16-byte aligned, [num_pages][kv_heads] of: f, log2(v), 1 / v
-// and an unused number for the page (tokens_a_factor 64); 16 f, 16 log2(v) / attend_scale_log2 and 16 1 / v, for four keys
-// each (4); 64 f and 64 v (1).  The first page of a sequence with new tokens is read even where it has no keys: its factors
-// are finite.
+// A cache that was copied to pages of 64 tokens with factors in [1, 2) of a key's scores (f) and of its value (v).
+struct CacheCopy {
+    // fp32 and 16-byte aligned, [num_pages][kv_heads] of: f, log2(v), 1 / v and an unused number for the page
+    // (tokens_a_factor 64); 16 f, 16 log2(v) / attend_scale_log2 and 16 1 / v, for four keys each (4); 64 f and 64 v (1).  The
+    // first page of a sequence with new tokens is read even where it has no keys: its factors are finite.
+    const float *factors;
+    int tokens_a_factor;
+    int64_t capacity;                        // keys a sequence can have
+};
+
+// Defined in paged_attention.cu: lowm_paged_attention, of a copy when that is not NULL.
 lowm_status_t attend_pages(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache, int64_t k_page_stride,
                            int64_t k_place_stride, int64_t k_cache_head_stride, const void *v_cache, int64_t v_page_stride,
                            int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size,
                            const int32_t *page_table, int64_t page_table_stride, int table_width, const int32_t *kv_lens,
                            const int32_t *cu_q, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, int batch,
-                           int q_tokens, int heads, int kv_heads, int dim, float scale, int window, const float *factors,
-                           int tokens_a_factor, void *workspace, size_t workspace_bytes, void *stream);
+                           int q_tokens, int heads, int kv_heads, int dim, float scale, int window, const CacheCopy *copy,
+                           void *workspace, size_t workspace_bytes, void *stream);
 
 inline bool is_aligned(const void *p, uintptr_t bytes)
 {

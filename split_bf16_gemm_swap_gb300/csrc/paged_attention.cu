@@ -88,7 +88,7 @@ struct AttnParams : LineParams<kTileRows, kItemCost, kMinShare> {
     int64_t q_ts, q_hs, o_ts, o_hs, table_stride, num_pages;
     int64_t k_page, k_place, k_head, v_page, v_place, v_head;
     const int32_t *table;
-    const float *factors;                    // as for attend_pages
+    const float *factors;                    // as in CacheCopy
     int page_size, page_shift, heads, slot_rows;
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
     float scale_inverse;                     // 1 / scale_log2
@@ -1020,7 +1020,7 @@ lowm_status_t lowm::attend_pages(
     int64_t v_place_stride, int64_t v_cache_head_stride, int64_t num_pages, int page_size, const int32_t *page_table,
     int64_t page_table_stride, int table_width, const int32_t *kv_lens, const int32_t *cu_q, void *out,
     int64_t out_token_stride, int64_t out_head_stride, float *lse, int batch, int q_tokens, int heads, int kv_heads,
-    int dim, float scale, int window, const float *factors, int tokens_a_factor, void *workspace, size_t workspace_bytes, void *stream)
+    int dim, float scale, int window, const CacheCopy *copy, void *workspace, size_t workspace_bytes, void *stream)
 {
     if (batch < 0 || q_tokens < 0 || heads <= 0 || kv_heads <= 0 || dim <= 0 || num_pages <= 0 || num_pages > INT_MAX || page_size <= 0 ||
         table_width < 0 || window < 0 || !(scale == scale))
@@ -1057,7 +1057,7 @@ lowm_status_t lowm::attend_pages(
         if (extents[i] > 1 && (cache_strides[i] == 0 || cache_strides[i] >= ((int64_t)1 << 39)))
             return LOWM_ERR_INVALID_ARGUMENT;
     // Tile counts are 32-bit in the kernels, rounding up to equal shares included.
-    const int64_t capacity = std::min<int64_t>((int64_t)table_width * page_size, kMaxKeys);
+    const int64_t capacity = copy ? copy->capacity : std::min<int64_t>((int64_t)table_width * page_size, kMaxKeys);
     const int64_t q_tiles = (int64_t)q_tokens * (heads / kv_heads) / kTileRows + batch;
     if ((double)q_tiles * kv_heads * (double)(capacity / kTileKeys + 2 + kItemCost) > (double)(INT_MAX - kMaxAttnCtas))
         return LOWM_ERR_UNSUPPORTED_SHAPE;
@@ -1085,7 +1085,7 @@ lowm_status_t lowm::attend_pages(
     p.v_place = v_place_stride;
     p.v_head = v_cache_head_stride;
     p.table = page_table;
-    p.factors = factors;
+    p.factors = copy ? copy->factors : nullptr;
     p.kv_lens = kv_lens;
     p.cu_q = cu_q;
     p.page_size = page_size;
@@ -1117,13 +1117,13 @@ lowm_status_t lowm::attend_pages(
         (st = encode_cache(v_cache, v_page_stride, v_place_stride, v_cache_head_stride, num_pages, page_size, kv_heads,
                            dim, &map_v)) != LOWM_OK)
         return st;
-    if (!factors)
+    if (!copy)
         return dim == 64 ? launch_attention<64, kNoFactors>(map_k, map_v, p, sms, stream)
                          : launch_attention<128, kNoFactors>(map_k, map_v, p, sms, stream);
-    if (tokens_a_factor == kTileKeys)
+    if (copy->tokens_a_factor == kTileKeys)
         return dim == 64 ? launch_attention<64, kTileFactors>(map_k, map_v, p, sms, stream)
                          : launch_attention<128, kTileFactors>(map_k, map_v, p, sms, stream);
-    if (tokens_a_factor == 4)
+    if (copy->tokens_a_factor == 4)
         return dim == 64 ? launch_attention<64, kQuadFactors>(map_k, map_v, p, sms, stream)
                          : launch_attention<128, kQuadFactors>(map_k, map_v, p, sms, stream);
     return dim == 64 ? launch_attention<64, kKeyFactors>(map_k, map_v, p, sms, stream)
@@ -1141,5 +1141,5 @@ extern "C" lowm_status_t lowm_paged_attention(
     return lowm::attend_pages(q, q_token_stride, q_head_stride, k_cache, k_page_stride, k_place_stride, k_cache_head_stride,
                               v_cache, v_page_stride, v_place_stride, v_cache_head_stride, num_pages, page_size, page_table,
                               page_table_stride, table_width, kv_lens, cu_q, out, out_token_stride, out_head_stride, lse, batch,
-                              q_tokens, heads, kv_heads, dim, scale, window, nullptr, 0, workspace, workspace_bytes, stream);
+                              q_tokens, heads, kv_heads, dim, scale, window, nullptr, workspace, workspace_bytes, stream);
 }

@@ -717,7 +717,7 @@ struct WidenParams {
     int64_t table_stride, num_pages;
     const int32_t *table, *kv_lens, *cu_q;
     __nv_bfloat16 *wide_k, *wide_v;          // [batch * pages][kv_heads][64][dim]
-    float *factors;                          // [batch * pages][kv_heads] of what attend_pages takes
+    float *factors;                          // [batch * pages][kv_heads], as in CacheCopy
     int32_t *wide_table;                     // [batch][pages]
     int page_shift, block_shift, batch, q_tokens, kv_heads, window, capacity, pages;
     int tokens_a_factor;                     // 64, 4 or 1
@@ -1030,10 +1030,11 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
                         dim3(kWidenThreads), 0, stream, w);
         if (st != LOWM_OK)
             return st;
+        const CacheCopy copy = {w.factors, w.tokens_a_factor, capacity};
         return attend_pages(q, q_token_stride, q_head_stride, w.wide_k, kv_heads * head, dim, head, w.wide_v, kv_heads * head, dim,
                             head, tasks, kWideKeys, w.wide_table, w.pages, w.pages, kv_lens, cu_q, out, out_token_stride,
-                            out_head_stride, lse, batch, q_tokens, heads, kv_heads, dim, scale, window, w.factors, w.tokens_a_factor,
-                            at + used, workspace_bytes - used, stream);
+                            out_head_stride, lse, batch, q_tokens, heads, kv_heads, dim, scale, window, &copy, at + used,
+                            workspace_bytes - used, stream);
     }
     unsigned int *status = host_status_word();
     if (!status)

@@ -828,3 +828,25 @@ def test_attention_of_an_empty_batch_with_many_rows(rows, width):
     none, cu = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
     out, lse = fp8.paged_attention_fp8(rand(rows, 4, 64), kc, vc, ks, vs, table[:0], none, cu, return_lse=True)
     assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("block", [1, 8])
+@pytest.mark.parametrize("q_lens,room", [([1, 1], 0), ([400, 300], 0), ([400, 300], ROOM // 8)])
+def test_attention_of_lengths_past_the_table(block, q_lens, room):
+    # what does not fit the table is not there: the rows stand at the end of what does
+    page, wide = 8, bool(room)
+    width = room + 3                                                # the last 64 keys' place in the table is not whole
+    lens = [width * page + 5, width * page + 60]
+    kc, vc, ks, vs, table = make_cache([width * page] * 2, page, block, 2, 64, seed=21)
+    cu = [0, q_lens[0], sum(q_lens)]
+    assert widened(2, cu[-1], 8, 2, 64, page, width) == wide
+    q = rand(cu[-1], 8, 64, seed=22)
+    kv, cu_q = torch.tensor(lens, device="cuda", dtype=torch.int32), torch.tensor(cu, device="cuda", dtype=torch.int32)
+    layer.release_workspaces()
+    junk = torch.full((1 << 28,), 0xff, dtype=torch.uint8, device="cuda")      # memory that a workspace may get
+    del junk
+    want, tol, lse = attention64(q, kc, vc, ks, vs, table, lens, cu_q, 0.125, 0, wide)
+    out, got = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu_q, scale=0.125, return_lse=True)
+    bounded(out, want, tol, "attention")
+    seen = torch.isfinite(lse)
+    assert torch.equal(torch.isneginf(got), ~seen) and float((got[seen] - lse[seen]).abs().max()) <= 1e-3

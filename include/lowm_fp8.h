@@ -109,7 +109,9 @@ lowm_status_t lowm_rope_append_fp8(const void *q, int64_t q_token_stride, int64_
  * lowm_rope_append_fp8): key j counts as k_scale * k[j], its value as v_scale * v[j].
  *   k_cache, v_cache  base 16-byte aligned, strides multiples of 16 (of a dimension
  *                 of one they may be anything)
- *   k_scale, v_scale  any fp32 numbers; v_scale is taken as 2^-50 .. 2^50
+ *   k_scale       any fp32 numbers
+ *   v_scale       0 .. 2^50, where less than 2^-50 counts as 2^-50; another one makes
+ *                 the rows that see its tokens NaN
  *   block         a power of two, at most page_size
  * The other arguments, their limits and what a row that sees nothing gets are
  * those of lowm_paged_attention.  A length that the table has no room for counts as the

@@ -49,7 +49,7 @@ constexpr int kUnitKeys = 32;                // of one product
 constexpr int kMaxCtas = 480;                // three per SM, and a bound for the workspace
 constexpr int kItemCost8 = 4, kMinShare8 = 4;
 constexpr float kWeightLog2 = 8.f, kRescaleLog2 = 7.f;   // the largest weight is 2^15 (fp16 ends at 65504)
-constexpr float kMaxScale = 1.125899906842624e15f;   // 2^50: scales are taken as 2^-50 .. 2^50
+constexpr float kMaxScale = 1.125899906842624e15f;   // 2^50: V's scales are taken as 2^-50 .. 2^50
 
 // Bits of the device status word (above those of the other operators).
 enum : uint32_t {
@@ -169,6 +169,9 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w)
     return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
+// Whether b is a scale of V; less than 2^-50 counts as that.
+__device__ __forceinline__ bool is_value_scale(float b) { return b >= 0.f && b <= kMaxScale; }
+
 // One warp's rows of an item.  Thread 4 g + t has of row g elements [DIM / 4 t, DIM / 4 (t + 1)) of
 // q, and of rows 2 t and 2 t + 1 the maximum, the sum of its keys' weights and elements [DIM / 8 g, DIM / 8 (g + 1)) of the
 // weighted values: out[e] holds elements 2 e and 2 e + 1 of those, of row 2 t, row 2 t + 1, row 2 t, row 2 t + 1.
@@ -252,12 +255,14 @@ __device__ __forceinline__ void attend(Rows8<DIM> &x, const Seen &seen, int key0
 {
     constexpr int kWords = DIM / 32;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    // Scales of the 32 keys, a key a lane; those that no row sees count nothing.
+    // Scales of the 32 keys, a key a lane; those that no row sees count nothing.  (One of V that is none makes the key's scores
+    // NaN, which the mask still takes out of the rows that do not see it.)
     {
         const int key = key0 + lane;
         const bool known = key >= seen.lo && key < seen.end;
-        const float b = known ? fminf(fmaxf(scales[kTileKeys + first + lane], 1.f / kMaxScale), kMaxScale) : 1.f;
-        mine[lane] = make_float4(known ? scales[first + lane] * scale_log2 : 0.f, __log2f(b), __fdividef(1.f, b), 0.f);
+        const float of_v = known ? scales[kTileKeys + first + lane] : 1.f, b = fminf(fmaxf(of_v, 1.f / kMaxScale), kMaxScale);
+        const float of_k = known ? scales[first + lane] * scale_log2 : 0.f;
+        mine[lane] = make_float4(is_value_scale(of_v) ? of_k : CUDART_NAN_F, __log2f(b), __fdividef(1.f, b), 0.f);
         __syncwarp();
     }
     // Scores: thread 4 g + t has keys g + 8 j of rows 2 t and 2 t + 1.
@@ -794,7 +799,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams 
             const int key = u * kKeysAtOnce + mine;
             float k_rest, v_rest;
             const float k_power = split_scale(ks[u], k_rest);
-            const float v_power = split_scale(fminf(fmaxf(vs[u], 1.f / kMaxScale), kMaxScale), v_rest);
+            const float v_power = split_scale(is_value_scale(vs[u]) ? fmaxf(vs[u], 1.f / kMaxScale) : CUDART_NAN_F, v_rest);
             if (chunk == 0 && key % p.tokens_a_factor == 0) {
                 if (p.tokens_a_factor == kWideKeys) {
                     reinterpret_cast<float4 *>(p.factors)[task] = make_float4(k_rest, log2f(v_rest), 1.f / v_rest, 0.f);

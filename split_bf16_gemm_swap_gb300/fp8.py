@@ -254,7 +254,8 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_le
     """:func:`.layer.paged_attention` over a cache of codes with their scales, as :func:`rope_append_fp8` keeps it.
 
     q and the result are bf16; k_cache, v_cache float8_e4m3fn; k_scale, v_scale
-    [num_pages, page_size / block, kv_heads] fp32, any positive numbers.
+    [num_pages, page_size / block, kv_heads] fp32.  v_scale is from 0 to 2^50 (less
+    than 2^-50 counts as 2^-50); another one makes the rows that see its tokens NaN.
     """
     device = _cuda(q, "q")
     if stream is not None or _current_device() != device:

@@ -850,3 +850,32 @@ def test_attention_of_lengths_past_the_table(block, q_lens, room):
     bounded(out, want, tol, "attention")
     seen = torch.isfinite(lse)
     assert torch.equal(torch.isneginf(got), ~seen) and float((got[seen] - lse[seen]).abs().max()) <= 1e-3
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("block", [1, 16, 64])
+@pytest.mark.parametrize("q_lens,room", [([1, 3], 0), ([40, 30], 0), ([250, 180], 0), ([250, 180], ROOM)])
+@pytest.mark.parametrize("window", [0, 60])
+def test_attention_value_scales_that_are_none(dim, block, q_lens, room, window):
+    # NaN, infinite, negative and too large ones make the rows that see them NaN; those from 0 to 2^-50 count as 2^-50
+    lens, page, bad = [400, 260], 64, [math.nan, math.inf, -math.inf, -1.0, 2.0 ** 51, -math.nan]
+    kc, vc, ks, vs, table = make_cache(lens, page, block, 2, dim, seed=23, width=room // page if room else None)
+    cu = [0, q_lens[0], sum(q_lens)]
+    assert widened(2, cu[-1], 8, 2, dim, page, table.shape[1]) == bool(room)
+    at = lambda b, key: (int(table[b, key // page]), key % page // block)                  # noqa: E731
+    vs[at(0, 130)] = torch.tensor([0.0, 2.0 ** -60], device="cuda")                        # a scale a head
+    vs[at(1, 70)] = torch.tensor([2.0 ** -149, 2.0 ** 50], device="cuda")
+    for i, key in enumerate((200, 385, 399)):
+        vs[at(0, key)] = torch.tensor([bad[2 * i], bad[2 * i + 1]], device="cuda")
+    q = rand(cu[-1], 8, dim, seed=24)
+    kv, cu_q = torch.tensor(lens, device="cuda", dtype=torch.int32), torch.tensor(cu, device="cuda", dtype=torch.int32)
+    taken = (vs >= 0) & (vs <= 2.0 ** 50)
+    floor = vs.clamp(min=2.0 ** -50)
+    _, tol, _ = attention64(q, kc, vc, ks, torch.where(taken, floor, 1.0), table, lens, cu_q, 0.125, window, bool(room))
+    want, _, lse = attention64(q, kc, vc, ks, torch.where(taken, floor, math.nan), table, lens, cu_q, 0.125, window, False)
+    out, got = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu_q, scale=0.125, window=window, return_lse=True)
+    assert torch.isnan(want).any() and not torch.isnan(want).all()
+    bounded(out, want, tol, "attention")
+    ok = torch.isfinite(want).all(-1)
+    assert float((got[ok] - lse[ok]).abs().max()) <= 1e-3
+    in_order()

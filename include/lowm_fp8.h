@@ -138,7 +138,13 @@ lowm_status_t lowm_paged_attention_fp8(const void *q, int64_t q_token_stride, in
                                        float scale, int window,
                                        void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace lowm_paged_attention_fp8 needs (0 for sizes it refuses). */
+/*
+ * Bytes of workspace lowm_paged_attention_fp8 needs (0 for sizes it refuses), 1.1 GiB
+ * at most.  Calls with 96 rows a sequence and head and much room in the table take a
+ * bf16 copy of what their rows see into it, for some sequences and heads at a time
+ * where it has no room for all; weights meet values rounded to bf16 then, else to
+ * fp16.
+ */
 size_t lowm_paged_attention_fp8_workspace(int batch, int q_tokens, int heads, int kv_heads, int dim, int page_size,
                                           int table_width);
 

@@ -30,7 +30,8 @@ inline float attend_scale_log2(float scale)
     return std::max((scale < 0.f ? -scale : scale) * 1.44269504088896340736f, 1e-30f);
 }
 
-// A cache that was copied to pages of 64 tokens with factors in [1, 2) of a key's scores (f) and of its value (v).
+// A cache that was copied to pages of 64 tokens with factors in [1, 2) of a key's scores (f) and of its value (v), for some of
+// a call's sequences (the others have no rows in the cu_q that goes with it) and heads.
 struct CacheCopy {
     // fp32 and 16-byte aligned, [num_pages][kv_heads] of: f, log2(v), 1 / v and an unused number for the page
     // (tokens_a_factor 64); 16 f, 16 log2(v) / attend_scale_log2 and 16 1 / v, for four keys each (4); 64 f and 64 v (1).  The
@@ -38,6 +39,8 @@ struct CacheCopy {
     const float *factors;
     int tokens_a_factor;
     int64_t capacity;                        // keys a sequence can have
+    const int32_t *cu_q;                     // the whole call's: rows of none of its sequences become zeros
+    int heads;                               // the whole call's
 };
 
 // Defined in paged_attention.cu: lowm_paged_attention, of a copy when that is not NULL.

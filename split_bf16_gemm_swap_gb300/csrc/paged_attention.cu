@@ -90,6 +90,8 @@ struct AttnParams : LineParams<kTileRows, kItemCost, kMinShare> {
     const int32_t *table;
     const float *factors;                    // as in CacheCopy
     int page_size, page_shift, heads, slot_rows;
+    const int32_t *all_cu_q;                 // of the whole call, whose sequences and heads these may be some of
+    int all_heads;
     float scale_log2;                        // |scale| * log2(e); the sign is in Q
     float scale_inverse;                     // 1 / scale_log2
     float q_sign;
@@ -844,7 +846,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         }
                     }
                     if (w.valid && whole && p.lse)
-                        p.lse[(int64_t)w.token * p.heads + w.q_head] =
+                        p.lse[(int64_t)w.token * p.all_heads + w.q_head] =
                             l == 0.f ? -CUDART_INF_F : (m * p.scale_log2 + log2f(l)) * CUDART_LN2_F;
                     if (w.valid && !whole) {
                         float2 *ml = reinterpret_cast<float2 *>(p.parts + 2 * (int64_t)gridDim.x * p.slot_rows * (DIM / 4));
@@ -881,15 +883,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const AttnPara
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (blockIdx.x == 0 && blockIdx.y == 0) {   // rows of no sequence
-        const int first = p.batch > 0 ? min(max(p.cu_q[0], 0), p.q_tokens) : p.q_tokens;
-        const int last = p.batch > 0 ? min(max(p.cu_q[p.batch], 0), p.q_tokens) : p.q_tokens;
+        const int first = p.batch > 0 ? min(max(p.all_cu_q[0], 0), p.q_tokens) : p.q_tokens;
+        const int last = p.batch > 0 ? min(max(p.all_cu_q[p.batch], 0), p.q_tokens) : p.q_tokens;
         for (int t = threadIdx.x >> 5; t < p.q_tokens; t += kJoinThreads / 32)
             if (t < first || t >= last)
                 for (int h = 0; h < p.heads; ++h) {
                     for (int d = threadIdx.x & 31; d < DIM; d += 32)
                         p.out[t * p.o_ts + h * p.o_hs + d] = __float2bfloat16_rn(0.f);
                     if ((threadIdx.x & 31) == 0 && p.lse)
-                        p.lse[(int64_t)t * p.heads + h] = -CUDART_INF_F;
+                        p.lse[(int64_t)t * p.all_heads + h] = -CUDART_INF_F;
                 }
     }
     if (p.batch == 0)
@@ -947,7 +949,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const AttnPara
             }
         }
         if (p.lse && e == 0)
-            p.lse[(int64_t)t * p.heads + h] = l == 0.f ? -CUDART_INF_F : (base + log2f(l)) * CUDART_LN2_F;
+            p.lse[(int64_t)t * p.all_heads + h] = l == 0.f ? -CUDART_INF_F : (base + log2f(l)) * CUDART_LN2_F;
     }
 }
 
@@ -1095,6 +1097,8 @@ lowm_status_t lowm::attend_pages(
     p.batch = batch;
     p.q_tokens = q_tokens;
     p.heads = heads;
+    p.all_cu_q = copy ? copy->cu_q : cu_q;
+    p.all_heads = copy ? copy->heads : heads;
     p.kv_heads = kv_heads;
     p.group = heads / kv_heads;
     p.window = window < kMaxKeys ? window : 0;

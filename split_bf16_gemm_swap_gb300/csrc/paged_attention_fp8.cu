@@ -712,7 +712,10 @@ __global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Att
 // 16000 175, 141; 8 x 64 x 8000 250, 135; 2 x 64 x 4000 54, 47; 1 x 300 x 1000 (16 / 8 heads) 30, 35.
 constexpr int kWideRows = 96;                // rows a sequence and head bring on average, at least
 constexpr double kWideWork = 1.3e10;         // and multiply-adds in all, times four
-constexpr int64_t kWideBytes = (int64_t)8 << 30;   // of scratch memory at most
+// The copy has room for as many keys as the table (or, with a window, as its rows can see), in kWideBytes at most: where that
+// is not enough for all, sequences and heads take turns, three launches each.  The host only knows how many turns it may take;
+// the device gives a turn as many sequences as there is room for, and turns without any do nothing.
+constexpr int64_t kWideBytes = (int64_t)1 << 30;
 constexpr int kWideKeys = 64;                // tokens of a page of the copy
 
 struct WidenParams {
@@ -721,13 +724,59 @@ struct WidenParams {
     int64_t k_page, k_place, k_head, v_page, v_place, v_head, ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
     int64_t table_stride, num_pages;
     const int32_t *table, *kv_lens, *cu_q;
-    __nv_bfloat16 *wide_k, *wide_v;          // [batch * pages][kv_heads][64][dim]
-    float *factors;                          // [batch * pages][kv_heads], as in CacheCopy
-    int32_t *wide_table;                     // [batch][pages]
-    int page_shift, block_shift, batch, q_tokens, kv_heads, window, capacity, pages;
+    __nv_bfloat16 *wide_k, *wide_v;          // [pages][kv_heads][64][dim]
+    float *factors;                          // [pages][kv_heads], as in CacheCopy
+    int32_t *wide_table;                     // [batch][table_pages]
+    int page_shift, block_shift, batch, q_tokens, kv_heads, window, capacity, table_pages;
+    int pages;                               // of the copy that a sequence needs at most: the first of sequence b is b * pages,
+    int32_t *places, *turns;                 // or, in turns, places[b]; a turn's sequences are turns[turn] .. turns[turn + 1] - 1,
+    int32_t *turn_cu_q;                      // and this is cu_q with the others' rows left out
+    int turn, room;                          // pages of a turn
     int tokens_a_factor;                     // 64, 4 or 1
     float scale_inverse;                     // of attend_pages
 };
+
+// The pages of the copy that a sequence has, from `first` on: those with keys that its rows see, and one where it has new
+// tokens but no keys (for the factors, which its rows' masked tile meets).
+__device__ __forceinline__ int pages_to_widen(const WidenParams &p, int b, int &first, int &kv)
+{
+    const int q0 = min(max(p.cu_q[b], 0), p.q_tokens), q_len = min(max(p.cu_q[b + 1], q0), p.q_tokens) - q0;
+    kv = min(max(p.kv_lens[b], 0), p.capacity);
+    first = p.window > 0 ? max(kv - q_len - p.window + 1, 0) / kWideKeys : 0;
+    return q_len == 0 ? 0 : (max(kv, 1) + kWideKeys - 1) / kWideKeys - first;
+}
+
+// The turns: in order, as many sequences each as there is room for.
+constexpr int kPlanThreads = 256;
+
+__global__ void __launch_bounds__(kPlanThreads) plan_turns_kernel(const WidenParams p, int turns)
+{
+    __shared__ int pages[kPlanThreads];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    int turn = 0, used = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+        int first, kv;
+        const int b = b0 + threadIdx.x;
+        pages[threadIdx.x] = b < p.batch ? pages_to_widen(p, b, first, kv) : 0;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int i = 0; i < min(kPlanThreads, p.batch - b0); ++i) {
+                if (used + pages[i] > p.room && turn + 1 < turns) {      // (never more turns than the host counted)
+                    p.turns[++turn] = b0 + i;
+                    used = 0;
+                }
+                p.places[b0 + i] = used;
+                used += pages[i];
+            }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        p.turns[0] = 0;
+        while (turn < turns)
+            p.turns[++turn] = p.batch;
+    }
+}
 
 __device__ __forceinline__ void widen_16(uint4 codes, float scale, uint4 *to)
 {
@@ -762,62 +811,66 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams 
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int chunk = threadIdx.x % kChunks, mine = threadIdx.x / kChunks;
-    const int64_t tasks = (int64_t)p.batch * p.pages * p.kv_heads;
-    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-        const int64_t wide = task / p.kv_heads;                              // page of the copy
-        const int head = (int)(task - wide * p.kv_heads);
-        const int b = (int)(wide / p.pages), j = (int)(wide - (int64_t)b * p.pages);
-        if (threadIdx.x == 0 && head == 0)
-            p.wide_table[wide] = (int)wide;
-        const int q0 = min(max(p.cu_q[b], 0), p.q_tokens), q_len = min(max(p.cu_q[b + 1], q0), p.q_tokens) - q0;
-        const int kv = min(max(p.kv_lens[b], 0), p.capacity);
-        const int first = p.window > 0 ? kv - q_len - p.window + 1 : 0;      // no row sees a key before it
-        const int key0 = j * kWideKeys, end = min(kv, key0 + kWideKeys);
-        // (the first page of a sequence without keys has no keys either, but factors, which its rows' masked tile meets)
-        if (q_len == 0 || key0 >= max(kv, 1) || key0 + kWideKeys <= first)
-            continue;
-        uint4 k[kSteps], v[kSteps];
-        float ks[kSteps], vs[kSteps];
+    int begin = 0, stop = p.batch;
+    if (p.places) {
+        begin = p.turns[p.turn];
+        stop = p.turns[p.turn + 1];
+        for (int i = (int)((blockIdx.y * gridDim.x + blockIdx.x) * kWidenThreads + threadIdx.x); i <= p.batch;
+             i += (int)(gridDim.x * gridDim.y * kWidenThreads))
+            p.turn_cu_q[i] = min(max(p.cu_q[i], p.cu_q[begin]), p.cu_q[stop]);
+    }
+    for (int b = begin + (int)blockIdx.y; b < stop; b += (int)gridDim.y) {
+        int first, kv;
+        const int tasks = pages_to_widen(p, b, first, kv) * p.kv_heads, place = p.places ? p.places[b] : b * p.pages;
+        for (int i = (int)blockIdx.x; i < tasks; i += (int)gridDim.x) {
+            const int nth = i / p.kv_heads, head = i - nth * p.kv_heads, j = first + nth, wide = place + nth;    // page of the copy
+            const int64_t task = (int64_t)wide * p.kv_heads + head;
+            if (threadIdx.x == 0 && head == 0)
+                p.wide_table[(int64_t)b * p.table_pages + j] = wide;
+            const int key0 = j * kWideKeys, end = min(kv, key0 + kWideKeys);
+            uint4 k[kSteps], v[kSteps];
+            float ks[kSteps], vs[kSteps];
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            const int key = key0 + u * kKeysAtOnce + mine;
-            k[u] = v[u] = make_uint4(0, 0, 0, 0);
-            ks[u] = vs[u] = 1.f;
-            if (key >= end)
-                continue;
-            const int64_t page = p.table[b * p.table_stride + (key >> p.page_shift)];
-            const int place = key & ((1 << p.page_shift) - 1), block = place >> p.block_shift;
-            if (page < 0 || page >= p.num_pages)                             // reads as zeros
-                continue;
-            k[u] = *reinterpret_cast<const uint4 *>(p.k + page * p.k_page + place * p.k_place + head * p.k_head + 16 * chunk);
-            v[u] = *reinterpret_cast<const uint4 *>(p.v + page * p.v_page + place * p.v_place + head * p.v_head + 16 * chunk);
-            ks[u] = p.k_scale[page * p.ks_page + block * p.ks_block + head * p.ks_head];
-            vs[u] = p.v_scale[page * p.vs_page + block * p.vs_block + head * p.vs_head];
-        }
-#pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            const int key = u * kKeysAtOnce + mine;
-            float k_rest, v_rest;
-            const float k_power = split_scale(ks[u], k_rest);
-            const float v_power = split_scale(is_value_scale(vs[u]) ? fmaxf(vs[u], 1.f / kMaxScale) : CUDART_NAN_F, v_rest);
-            if (chunk == 0 && key % p.tokens_a_factor == 0) {
-                if (p.tokens_a_factor == kWideKeys) {
-                    reinterpret_cast<float4 *>(p.factors)[task] = make_float4(k_rest, log2f(v_rest), 1.f / v_rest, 0.f);
-                } else if (p.tokens_a_factor == 4) {
-                    float *to = p.factors + 3 * task * (kWideKeys / 4) + key / 4;
-                    to[0] = k_rest;
-                    to[kWideKeys / 4] = log2f(v_rest) * p.scale_inverse;
-                    to[2 * kWideKeys / 4] = 1.f / v_rest;
-                } else {
-                    p.factors[2 * task * kWideKeys + key] = k_rest;
-                    p.factors[(2 * task + 1) * kWideKeys + key] = v_rest;
-                }
+            for (int u = 0; u < kSteps; ++u) {
+                const int key = key0 + u * kKeysAtOnce + mine;
+                k[u] = v[u] = make_uint4(0, 0, 0, 0);
+                ks[u] = vs[u] = 1.f;
+                if (key >= end)
+                    continue;
+                const int64_t page = p.table[b * p.table_stride + (key >> p.page_shift)];
+                const int place = key & ((1 << p.page_shift) - 1), block = place >> p.block_shift;
+                if (page < 0 || page >= p.num_pages)                             // reads as zeros
+                    continue;
+                k[u] = *reinterpret_cast<const uint4 *>(p.k + page * p.k_page + place * p.k_place + head * p.k_head + 16 * chunk);
+                v[u] = *reinterpret_cast<const uint4 *>(p.v + page * p.v_page + place * p.v_place + head * p.v_head + 16 * chunk);
+                ks[u] = p.k_scale[page * p.ks_page + block * p.ks_block + head * p.ks_head];
+                vs[u] = p.v_scale[page * p.vs_page + block * p.vs_block + head * p.vs_head];
             }
-            if (key0 + key >= end)
-                continue;
-            const int64_t to = (task * kWideKeys + key) * DIM + 16 * chunk;
-            widen_16(k[u], k_power, reinterpret_cast<uint4 *>(p.wide_k + to));
-            widen_16(v[u], v_power, reinterpret_cast<uint4 *>(p.wide_v + to));
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                const int key = u * kKeysAtOnce + mine;
+                float k_rest, v_rest;
+                const float k_power = split_scale(ks[u], k_rest);
+                const float v_power = split_scale(is_value_scale(vs[u]) ? fmaxf(vs[u], 1.f / kMaxScale) : CUDART_NAN_F, v_rest);
+                if (chunk == 0 && key % p.tokens_a_factor == 0) {
+                    if (p.tokens_a_factor == kWideKeys) {
+                        reinterpret_cast<float4 *>(p.factors)[task] = make_float4(k_rest, log2f(v_rest), 1.f / v_rest, 0.f);
+                    } else if (p.tokens_a_factor == 4) {
+                        float *to = p.factors + 3 * task * (kWideKeys / 4) + key / 4;
+                        to[0] = k_rest;
+                        to[kWideKeys / 4] = log2f(v_rest) * p.scale_inverse;
+                        to[2 * kWideKeys / 4] = 1.f / v_rest;
+                    } else {
+                        p.factors[2 * task * kWideKeys + key] = k_rest;
+                        p.factors[(2 * task + 1) * kWideKeys + key] = v_rest;
+                    }
+                }
+                if (key0 + key >= end)
+                    continue;
+                const int64_t to = (task * kWideKeys + key) * DIM + 16 * chunk;
+                widen_16(k[u], k_power, reinterpret_cast<uint4 *>(p.wide_k + to));
+                widen_16(v[u], v_power, reinterpret_cast<uint4 *>(p.wide_v + to));
+            }
         }
     }
 }
@@ -886,10 +939,40 @@ int64_t wide_pages(int page_size, int table_width)
     return (capacity + kWideKeys - 1) / kWideKeys;
 }
 
-// Bytes of one widened tensor.
-int64_t wide_bytes(int batch, int kv_heads, int dim, int page_size, int table_width)
+// A call's scratch memory for the copy and how it is used.
+struct WidePlan {
+    int64_t head_pages;                      // 64 keys of one head each
+    int64_t tensor, factors, tables, lists;  // bytes of K or V, of the factors, of the table, of what the turns need
+    int heads, turns;                        // at a time; of the sequences
+    int64_t pages;                           // of a turn
+
+    int64_t bytes() const { return 2 * tensor + factors + tables + lists; }
+};
+
+int64_t sixteens(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// `pages` of the copy a sequence and `table_pages` in its table.  Without room for one head of a sequence: no heads.
+WidePlan plan_copy(int batch, int kv_heads, int dim, int64_t pages, int64_t table_pages)
 {
-    return batch * wide_pages(page_size, table_width) * kWideKeys * kv_heads * dim * 2;
+    const int64_t one = 2 * kWideKeys * dim * 2 + 2 * kWideKeys * 4;         // bytes of a head's page
+    WidePlan plan;
+    plan.tables = sixteens(batch * table_pages * 4);
+    plan.lists = 3 * sixteens((int64_t)(batch + 1) * 4);                     // places, turns, turn_cu_q
+    plan.head_pages = std::min(batch * kv_heads * table_pages, std::max<int64_t>(kWideBytes - plan.tables - plan.lists, 0) / one);
+    plan.tensor = plan.head_pages * kWideKeys * dim * 2;
+    plan.factors = plan.head_pages * 2 * kWideKeys * 4;
+    plan.heads = (int)std::min<int64_t>(kv_heads, plan.head_pages / pages);
+    plan.pages = plan.heads ? plan.head_pages / plan.heads : 0;
+    const int64_t sequences = plan.pages / pages;                            // in one turn, at least
+    plan.turns = plan.heads ? (int)((batch + sequences - 1) / sequences) : 0;
+    return plan;
+}
+
+// The plan of a call whose rows may see all of the table; with a window they need less of the same memory.
+WidePlan plan_whole_copy(int batch, int kv_heads, int dim, int page_size, int table_width)
+{
+    const int64_t pages = wide_pages(page_size, table_width);
+    return plan_copy(batch, kv_heads, dim, pages, pages);
 }
 
 // Whether a call widens the cache first.
@@ -898,17 +981,7 @@ bool widens(int batch, int q_tokens, int heads, int kv_heads, int dim, int page_
     const double keys = (double)wide_pages(page_size, table_width) * kWideKeys;
     return batch > 0 && (int64_t)q_tokens * (heads / kv_heads) >= (int64_t)kWideRows * batch &&
            4.0 * q_tokens * heads * keys * (dim + 64) >= kWideWork &&
-           2.0 * batch * wide_pages(page_size, table_width) * kWideKeys * kv_heads * dim * 2 <= (double)kWideBytes;
-}
-
-size_t wide_table_bytes(int batch, int page_size, int table_width)
-{
-    return (size_t)(batch * wide_pages(page_size, table_width) * 4 + 15) / 16 * 16;
-}
-
-size_t factor_bytes(int batch, int kv_heads, int page_size, int table_width)
-{
-    return (size_t)(batch * wide_pages(page_size, table_width) * 2 * kWideKeys * kv_heads * 4);
+           plan_whole_copy(batch, kv_heads, dim, page_size, table_width).heads > 0;
 }
 
 }  // namespace
@@ -921,8 +994,8 @@ extern "C" size_t lowm_paged_attention_fp8_workspace(int batch, int q_tokens, in
     if (!attention_fp8_shape_ok(batch, q_tokens, heads, kv_heads, dim) || page_size <= 0 || table_width < 0)
         return 0;
     if (widens(batch, q_tokens, heads, kv_heads, dim, page_size, table_width))
-        return (size_t)2 * wide_bytes(batch, kv_heads, dim, page_size, table_width) + wide_table_bytes(batch, page_size, table_width) +
-               factor_bytes(batch, kv_heads, page_size, table_width) + lowm_paged_attention_workspace(batch, q_tokens, heads, kv_heads, dim);
+        return (size_t)plan_whole_copy(batch, kv_heads, dim, page_size, table_width).bytes() +
+               lowm_paged_attention_workspace(batch, q_tokens, heads, kv_heads, dim);
     return (size_t)2 * kMaxCtas * slot_rows_fp8(q_tokens, heads, kv_heads) * (dim + 2) * sizeof(float) + kMaxCtas * sizeof(CutItem8);
 }
 
@@ -991,10 +1064,6 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
     };
     if (widens(batch, q_tokens, heads, kv_heads, dim, page_size, table_width)) {
         WidenParams w;
-        w.k = static_cast<const uint8_t *>(k_cache);
-        w.v = static_cast<const uint8_t *>(v_cache);
-        w.k_scale = k_scale;
-        w.v_scale = v_scale;
         w.k_page = k_page_stride;
         w.k_place = k_place_stride;
         w.k_head = k_cache_head_stride;
@@ -1009,37 +1078,67 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
         w.vs_head = vs_head_stride;
         w.table_stride = page_table_stride;
         w.num_pages = num_pages;
-        w.table = page_table;
-        w.kv_lens = kv_lens;
-        w.cu_q = cu_q;
         w.scale_inverse = 1.f / attend_scale_log2(scale);
         w.tokens_a_factor = block >= kWideKeys ? kWideKeys : (block >= 4 ? 4 : 1);
         w.page_shift = log2_of(page_size);
         w.block_shift = log2_of(block);
-        w.batch = batch;
         w.q_tokens = q_tokens;
-        w.kv_heads = kv_heads;
         w.window = window < kMaxKeys ? window : 0;
         w.capacity = (int)capacity;
-        w.pages = (int)wide_pages(page_size, table_width);
+        w.table_pages = (int)wide_pages(page_size, table_width);
+        // With a window a sequence's rows see window + q_len - 1 keys at most.
+        w.pages = w.window ? (int)std::min<int64_t>(w.table_pages, ((int64_t)w.window + q_tokens) / kWideKeys + 2) : w.table_pages;
+        const WidePlan plan = plan_copy(batch, kv_heads, dim, w.pages, w.table_pages);
         uint8_t *at = static_cast<uint8_t *>(workspace);
-        const int64_t bytes = wide_bytes(batch, kv_heads, dim, page_size, table_width);
-        w.wide_k = reinterpret_cast<__nv_bfloat16 *>(at);
-        w.wide_v = reinterpret_cast<__nv_bfloat16 *>(at + bytes);
-        w.factors = reinterpret_cast<float *>(at + 2 * bytes);
-        const size_t tables = (size_t)2 * bytes + factor_bytes(batch, kv_heads, page_size, table_width);
-        w.wide_table = reinterpret_cast<int32_t *>(at + tables);
-        const size_t used = tables + wide_table_bytes(batch, page_size, table_width);
-        const int64_t tasks = (int64_t)batch * w.pages, head = (int64_t)kWideKeys * dim;
-        st = launch_pdl(dim == 64 ? widen_kernel<64> : widen_kernel<128>, dim3((unsigned)std::min<int64_t>(tasks * kv_heads, 16 * sms)),
-                        dim3(kWidenThreads), 0, stream, w);
-        if (st != LOWM_OK)
+        auto take = [&](int64_t bytes) {
+            uint8_t *here = at;
+            at += bytes;
+            return here;
+        };
+        w.wide_k = reinterpret_cast<__nv_bfloat16 *>(take(plan.tensor));
+        w.wide_v = reinterpret_cast<__nv_bfloat16 *>(take(plan.tensor));
+        w.factors = reinterpret_cast<float *>(take(plan.factors));
+        w.wide_table = reinterpret_cast<int32_t *>(take(plan.tables));
+        int32_t *lists = reinterpret_cast<int32_t *>(take(plan.lists));
+        const int list = (int)(plan.lists / 3 / 4);
+        const bool turns = plan.turns > 1;
+        w.places = turns ? lists : nullptr;
+        w.turns = lists + list;
+        w.turn_cu_q = lists + 2 * list;
+        w.table = page_table;
+        w.kv_lens = kv_lens;
+        w.cu_q = cu_q;
+        w.batch = batch;
+        w.room = (int)plan.pages;
+        const int32_t *rows = turns ? w.turn_cu_q : cu_q;
+        const CacheCopy copy = {w.factors, w.tokens_a_factor, capacity, cu_q, heads};
+        const int64_t head = (int64_t)kWideKeys * dim;
+        const int y = std::min(batch, 1024), x = (int)std::min<int64_t>((16 * sms + y - 1) / y, (int64_t)w.pages * plan.heads);
+        if (turns && (st = launch_pdl(plan_turns_kernel, dim3(1), dim3(kPlanThreads), 0, stream, w, plan.turns)) != LOWM_OK)
             return st;
-        const CacheCopy copy = {w.factors, w.tokens_a_factor, capacity};
-        return attend_pages(q, q_token_stride, q_head_stride, w.wide_k, kv_heads * head, dim, head, w.wide_v, kv_heads * head, dim,
-                            head, tasks, kWideKeys, w.wide_table, w.pages, w.pages, kv_lens, cu_q, out, out_token_stride,
-                            out_head_stride, lse, batch, q_tokens, heads, kv_heads, dim, scale, window, &copy, at + used,
-                            workspace_bytes - used, stream);
+        for (int h = 0; h < kv_heads; h += plan.heads)
+            for (w.turn = 0; w.turn < plan.turns; ++w.turn) {
+                const int some = std::min(plan.heads, kv_heads - h);
+                const int64_t q_head = (int64_t)h * group;
+                w.k = static_cast<const uint8_t *>(k_cache) + h * k_cache_head_stride;
+                w.v = static_cast<const uint8_t *>(v_cache) + h * v_cache_head_stride;
+                w.k_scale = k_scale + h * ks_head_stride;
+                w.v_scale = v_scale + h * vs_head_stride;
+                w.kv_heads = some;
+                st = launch_pdl(dim == 64 ? widen_kernel<64> : widen_kernel<128>, dim3((unsigned)x, (unsigned)y), dim3(kWidenThreads), 0,
+                                stream, w);
+                if (st != LOWM_OK)
+                    return st;
+                st = attend_pages(static_cast<const __nv_bfloat16 *>(q) + q_head * q_head_stride, q_token_stride, q_head_stride, w.wide_k,
+                                  some * head, dim, head, w.wide_v, some * head, dim, head, plan.pages, kWideKeys, w.wide_table,
+                                  w.table_pages, w.table_pages, kv_lens, rows,
+                                  static_cast<__nv_bfloat16 *>(out) + q_head * out_head_stride, out_token_stride, out_head_stride,
+                                  lse ? lse + q_head : nullptr, batch, q_tokens, some * group, some, dim, scale, window, &copy, at,
+                                  workspace_bytes - plan.bytes(), stream);
+                if (st != LOWM_OK)
+                    return st;
+            }
+        return LOWM_OK;
     }
     unsigned int *status = host_status_word();
     if (!status)

@@ -179,6 +179,13 @@ def test_workspace_sizes():
     assert pages.lowm_compact_pages_workspace(5000) >= 5000 * 4 + 8 and pages.lowm_compact_pages_workspace(-1) == 0
 
 
+@pytest.mark.parametrize("batch,width", [(8, 2048), (17, 2048), (64, 2048), (3, 16384), (1000, 64)])
+def test_the_attention_workspace_is_bounded(batch, width):
+    # copies of 1 to 16 GiB in all; never more than one at a time, and every call is still widened
+    size = lambda w: fp8.lowm_paged_attention_fp8_workspace(batch, 30 * batch, 32, 8, 128, 64, w)   # noqa: E731
+    assert size(0) < 1 << 26 and 1 << 29 < size(width) < (1 << 30) + (1 << 26)
+
+
 # ----------------------------------------------------------------------------------------------- pages
 def fork(**kw):
     a = dict(table=PTR, ts=4, lens=PTR, rows=2, parents=PTR, new_rows=2, width=4, refs=PTR, pages=8, page=16, out=2 * PTR, os=4,

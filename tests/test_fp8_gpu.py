@@ -879,3 +879,50 @@ def test_attention_value_scales_that_are_none(dim, block, q_lens, room, window):
     ok = torch.isfinite(want).all(-1)
     assert float((got[ok] - lse[ok]).abs().max()) <= 1e-3
     in_order()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("batch,kv_heads,room", [(5, 4, 1 << 18), (3, 4, 1 << 20), (2, 2, 1 << 20), (7, 1, 1 << 19)])
+@pytest.mark.parametrize("window,block", [(0, 64), (0, 16), (90, 16), (0, 1), (90, 1)])
+def test_attention_of_chunks_whose_copies_take_turns(dim, batch, kv_heads, room, window, block):
+    # the table has room for far more than the scratch memory: sequences and heads one after the other
+    lens = [700, 3, 0, 290, 64, 200, 1000][:batch]
+    q_lens = [250, 120, 100, 100, 64, 0, 200][:batch]
+    page, heads = 64, 4 * kv_heads
+    kc, vc, ks, vs, table = make_cache(lens, page, block, kv_heads, dim, seed=25, width=room // page)
+    cu = [3 + sum(q_lens[:i]) for i in range(batch + 1)]
+    q = rand(cu[-1] + 5, heads, dim, seed=26)                       # rows of no sequence before and behind
+    size = fp8.lowm_paged_attention_fp8_workspace(batch, len(q), heads, kv_heads, dim, page, room // page)
+    copies = 4 * batch * kv_heads * room * dim
+    assert size > 100 << 20 and size < (1 << 30) + (64 << 20)
+    kv, cu_q = torch.tensor(lens, device="cuda", dtype=torch.int32), torch.tensor(cu, device="cuda", dtype=torch.int32)
+    want, tol, lse = attention64(q, kc, vc, ks, vs, table[:, :16], lens, cu_q, 0.125, window, True)
+    for _ in range(2):
+        out, got = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu_q, scale=0.125, window=window, return_lse=True)
+        bounded(out, want, tol, "attention of copies of %.1f GiB" % (copies / 2 ** 30))
+        seen = torch.isfinite(lse)
+        assert torch.equal(torch.isneginf(got), ~seen) and float((got[seen] - lse[seen]).abs().max()) <= 1e-3
+    in_order()
+
+
+@pytest.mark.parametrize("window", [200, 1500])
+def test_attention_of_chunks_of_a_long_cache_with_a_window(window):
+    # far behind the beginning: the copy holds the window only, in pages that take turns
+    check_attention([9000, 20011, 300], [300, 130, 290], 8, 2, 64, 64, 16, window=window, seed=27, width=1 << 14, wide=True)
+
+
+def test_attention_of_very_many_sequences_in_turns():
+    # more of them than a launch has rows of CTAs, and more room in the table than one turn has
+    batch, page, room = 1100, 64, 1 << 13
+    lens = [(37 * b) % 190 for b in range(batch)]
+    q_lens = [0 if b % 9 == 4 else 27 + b % 4 for b in range(batch)]
+    kc, vc, ks, vs, table = make_cache(lens, page, 16, 1, 64, seed=30, width=room // page)
+    cu = [sum(q_lens[:i]) for i in range(batch + 1)]
+    q = rand(cu[-1], 4, 64, seed=31)
+    assert widened(batch, cu[-1], 4, 1, 64, page, room // page)
+    kv, cu_q = torch.tensor(lens, device="cuda", dtype=torch.int32), torch.tensor(cu, device="cuda", dtype=torch.int32)
+    want, tol, lse = attention64(q, kc, vc, ks, vs, table[:, :3], lens, cu, 0.125, 0, True)
+    out, got = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu_q, scale=0.125, return_lse=True)
+    bounded(out, want, tol, "attention")
+    assert torch.equal(torch.isneginf(got), torch.isneginf(lse))
+    in_order()

@@ -11,7 +11,8 @@ none of them records a gradient.
 belong to that stream, and nothing is ordered against torch's current one.
 The tensors' device need not be torch's current one.
 Calls on a device's default stream share one workspace that is kept between
-them (:func:`release_workspaces`); they may come from several host threads.
+them (:func:`release_workspaces`; one of more than 128 MiB is given back after
+the call); they may come from several host threads.
 """
 from __future__ import annotations
 
@@ -141,7 +142,8 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 # lets other threads run during a call: the lock is held until both are enqueued, so that the stream runs all of one
 # call's kernels before the next call's.  (A lock that the thread may take again: a finaliser can call an operator.)  A
 # call on another stream allocates its own.  The default stream is never destroyed nor captured.  Allocated at every
-# call, a workspace cost paged_attention 4 of 20 us on the host.
+# call, a workspace cost paged_attention 4 of 20 us on the host; calls that need more than is kept take far longer.
+_KEPT_MOST = 128 << 20
 _kept: dict = {}
 _kept_lock = threading.RLock()
 
@@ -149,7 +151,7 @@ _kept_lock = threading.RLock()
 def _launch(name: str, args, nbytes: int, device: int, stream: int) -> None:
     """Call the library's function `name` with `args`, `nbytes` of scratch memory and `stream`."""
     fn = function(name)
-    if stream:
+    if stream or nbytes > _KEPT_MOST:
         own = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
         s = fn(*args, own.data_ptr(), nbytes, stream)
     else:

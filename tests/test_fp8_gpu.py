@@ -926,3 +926,16 @@ def test_attention_of_very_many_sequences_in_turns():
     bounded(out, want, tol, "attention")
     assert torch.equal(torch.isneginf(got), torch.isneginf(lse))
     in_order()
+
+
+def test_large_workspaces_are_not_kept():
+    layer.release_workspaces()
+    lens, page = [300], 64
+    kc, vc, ks, vs, table = make_cache(lens, page, 16, 8, 128, seed=28, width=1 << 11)
+    q = rand(150, 8, 128, seed=29)
+    kv, cu = torch.tensor(lens, device="cuda", dtype=torch.int32), torch.tensor([0, 150], device="cuda", dtype=torch.int32)
+    assert fp8.lowm_paged_attention_fp8_workspace(1, 150, 8, 8, 128, page, 1 << 11) > 1 << 29
+    fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu)
+    assert not layer._kept
+    fp8.paged_attention_fp8(q[:1], kc, vc, ks, vs, table, kv, torch.tensor([0, 1], device="cuda", dtype=torch.int32))
+    assert len(layer._kept) == 1

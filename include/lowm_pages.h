@@ -50,7 +50,10 @@ lowm_status_t lowm_fork_pages(const int32_t *page_table, int64_t table_stride, c
  *   missing       int32 [1]: pages that were not to be had (their entries become -1)
  *   workspace     lowm_extend_pages_workspace(num_pages) bytes, 4-byte aligned
  *   rows          0..8192
- * The rows' unfinished last pages must be their own, as lowm_fork_pages leaves them.
+ * An unfinished last page that other rows list as the same entry (lowm_fork_pages found
+ * none free, or a row was cut back) goes on in the longest of them, of equal ones the
+ * first; in the others the tokens that would lie in it have slot -1, and missing counts
+ * a page for each such row.
  */
 lowm_status_t lowm_extend_pages(int32_t *page_table, int64_t table_stride, int32_t *lens, int rows, int width,
                                 const int32_t *cu_new, int tokens, int32_t *refs, int num_pages, int page_size,

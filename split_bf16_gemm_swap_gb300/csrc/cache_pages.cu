@@ -214,8 +214,22 @@ struct NewTokens {
     int64_t *positions, *slots;
 };
 
-// Positions and slots of tokens `first`, first + step, ...; lens are the rows' new ones.
-__device__ __forceinline__ void place_tokens(const Table &table, const Pool &pool, const NewTokens &fresh, int first, int step)
+// Whether another row has page `page`, entry j of a row of `len` tokens, and goes on in it in that row's place: a longer one,
+// or an equally long one before it.  (Rare: a fork found no free page, or a row was cut back.)  lens are the new ones.
+__device__ __noinline__ bool is_anothers(const Table &table, const Pool &pool, const NewTokens &fresh, int row, int len, int j, int page)
+{
+    for (int r = 0; r < table.rows; ++r) {
+        const int old = table.lens[r] - max(fresh.cu[r + 1] - fresh.cu[r], 0);
+        if (r != row && old >= len && (old > len || r < row) && used_of(old, pool, table.width) > j && table.entries[r * table.stride + j] == page)
+            return true;
+    }
+    return false;
+}
+
+// Positions and slots of tokens `first`, first + step, ...; lens are the rows' new ones.  `missing` counts the rows that cannot
+// go on in a page that they share.
+__device__ __forceinline__ void place_tokens(const Table &table, const Pool &pool, const NewTokens &fresh, int32_t *missing, int first,
+                                             int step)
 {
     for (int t = first; t < fresh.tokens; t += step) {
         int lo = 0, hi = table.rows;         // the last row that begins at t or before
@@ -231,8 +245,15 @@ __device__ __forceinline__ void place_tokens(const Table &table, const Pool &poo
             position = (int64_t)table.lens[lo] - (fresh.cu[lo + 1] - t);
             const int64_t j = position / pool.page_size;
             const int page = j < table.width ? table.entries[lo * table.stride + j] : -1;
-            if (in_pool(page, pool))
+            if (in_pool(page, pool)) {
                 slot = (int64_t)page * pool.page_size + position % pool.page_size;
+                const int len = table.lens[lo] - (fresh.cu[lo + 1] - fresh.cu[lo]);
+                if (j * pool.page_size < len && pool.refs[page] > 1 && is_anothers(table, pool, fresh, lo, len, (int)j, page)) {
+                    slot = -1;
+                    if (t == fresh.cu[lo])
+                        atomicAdd(missing, 1);
+                }
+            }
         }
         fresh.positions[t] = position;
         fresh.slots[t] = slot;
@@ -295,14 +316,14 @@ __global__ void __launch_bounds__(kPageThreads) extend_kernel(const Table table,
         *missing = want - have + lost;
     __syncthreads();
     if (place_here)
-        place_tokens(table, pool, fresh, threadIdx.x, kPageThreads);
+        place_tokens(table, pool, fresh, missing, threadIdx.x, kPageThreads);
 }
 
-__global__ void __launch_bounds__(256) place_kernel(const Table table, const Pool pool, const NewTokens fresh)
+__global__ void __launch_bounds__(256) place_kernel(const Table table, const Pool pool, const NewTokens fresh, int32_t *missing)
 {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    place_tokens(table, pool, fresh, (int)(blockIdx.x * 256 + threadIdx.x), (int)(gridDim.x * 256));
+    place_tokens(table, pool, fresh, missing, (int)(blockIdx.x * 256 + threadIdx.x), (int)(gridDim.x * 256));
 }
 
 // ------------------------------------------------------------------ compact
@@ -583,7 +604,8 @@ extern "C" lowm_status_t lowm_extend_pages(int32_t *page_table, int64_t table_st
     st = launch_pdl(extend_kernel, dim3(1), dim3(kPageThreads), (size_t)(rows + 1) * 4, stream, table, lens, pool, fresh, missing,
                     static_cast<int32_t *>(workspace), (int)here);
     if (st == LOWM_OK && !here)
-        st = launch_pdl(place_kernel, dim3((unsigned)std::min((tokens + 255) / 256, 8 * sms)), dim3(256), 0, stream, table, pool, fresh);
+        st = launch_pdl(place_kernel, dim3((unsigned)std::min((tokens + 255) / 256, 8 * sms)), dim3(256), 0, stream, table, pool, fresh,
+                        missing);
     return st;
 }
 

@@ -123,7 +123,8 @@ def extend_pages(page_table, lens, cu_new, refs, page_size: int, tokens: int, *,
 
     page_table, lens and refs are updated in place.  Returns ``(positions, slots,
     missing)`` for :func:`.layer.rope_append`: int64 [tokens] each, and an int32 [1]
-    count of pages that were not to be had (their tokens have slot -1).
+    count of pages that were not to be had (their tokens have slot -1), among them
+    those of rows that :func:`fork_pages` left on another's unfinished page.
     """
     device = _cuda(page_table, "page_table")
     if stream is not None or _current_device() != device:

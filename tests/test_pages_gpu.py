@@ -245,6 +245,57 @@ def test_extend_tokens_behind_the_last_row():
     assert positions.tolist() == [3, 4, 0, 0, 0] and slots.tolist() == [3, 4, -1, -1, -1] and missing.tolist() == [0]
 
 
+class SharedPool(Pool):
+    """Extend where rows share unfinished pages: the longest of them, of equal ones the first, goes on in it."""
+
+    def extend(self, counts):
+        old, shared = list(self.lens), {}
+        for i, n in enumerate(counts):
+            e = old[i] // self.page
+            p = self.table[i][e] if n and old[i] % self.page and e < self.width else -1
+            if self.inside(p) and any(j != i and self.used(j) > e and self.table[j][e] == p and (old[j], -j) > (old[i], -i)
+                                      for j in range(len(old))):
+                shared[i] = e
+        positions, slots, missing = super().extend(counts)
+        rows = [i for i, n in enumerate(counts) for _ in range(n)]
+        slots = [-1 if p // self.page == shared.get(i, -1) else s for i, p, s in zip(rows, positions, slots)]
+        self.slots = slots
+        return positions, slots, missing + len(shared)
+
+
+@pytest.mark.parametrize("step", [1, 3, 20, 2000])
+@pytest.mark.parametrize("spare", [0, 1, 40])
+def test_extend_of_rows_that_a_fork_left_on_one_page(step, spare):
+    lens = [20, 7, 33]
+    table, refs = make(lens, 16, 6 + spare, seed=4, width=140)
+    pool = SharedPool(table, lens, refs, 16)
+    check_fork(pool, [0, 0, 0, 1, 1, 2])
+    for i in range(4):
+        lens, used = list(pool.lens), [pool.table[j][:pool.used(j)] for j in range(6)]
+        counts = [step, step + i % 2, 0 if i == 1 else step, step, 2 * step, step]
+        check_extend(pool, counts)
+        written = [s for s in pool.slots if s >= 0]
+        assert len(set(written)) == len(written)                    # no place twice, and none that a row holds already
+        held = {row[p // 16] * 16 + p % 16 for row, n in zip(used, lens) for p in range(min(n, 16 * len(row))) if row[p // 16] >= 0}
+        assert not held & set(written)
+
+
+def test_extend_of_a_row_that_was_cut_back_into_a_shared_page():
+    # row 0 holds places of page 2 that row 1, shorter, would write next; row 2 has pages that are counted outside of the table
+    pool = SharedPool([[0, 2, -1, -1], [0, 2, -1, -1], [3, 4, -1, -1]], [27, 21, 30], [2, 1, 2, 2, 2, 0, 0, 0, 0], 16)
+    pool.refs[1] = 0
+    for counts in ([3, 3, 1], [1, 0, 5], [0, 9, 0], [3, 0, 0]):
+        check_extend(pool, counts)
+
+
+def test_extend_of_many_rows_on_one_page():
+    rows = 3000
+    pool = SharedPool([[5 + i // 3, -1] for i in range(rows)], [3 + i % 2 for i in range(rows)],
+                      [0] * 5 + [3] * 1000 + [0] * 7, 16)
+    check_extend(pool, [i % 4 for i in range(rows)])
+    check_extend(pool, [14] * 100 + [0] * (rows - 100))
+
+
 @pytest.mark.parametrize("pages_", [1, 2, 7, 4095, 4096, 4097, 20000])
 @pytest.mark.parametrize("fill", [0.0, 0.3, 0.9, 1.0])
 def test_compact(pages_, fill):

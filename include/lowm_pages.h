@@ -30,8 +30,8 @@ extern "C" {
  * and dst[i] say what to copy there (-1: nothing).  Where no page is free the page
  * stays shared, src[i] and dst[i] are -1, and missing[0] counts it.
  *   parents       int32 [new_rows]
- *   new_table     int32 [new_rows, width] by row stride, not the old one; entries that
- *                 do not count are set to -1
+ *   new_table     int32 [new_rows, width] by row stride, no memory of the old one;
+ *                 entries that do not count are set to -1
  *   new_lens, src, dst  int32 [new_rows]; missing int32 [1]
  *   rows, new_rows  0..8192
  */

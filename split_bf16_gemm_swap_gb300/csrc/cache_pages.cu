@@ -538,6 +538,22 @@ bool table_ok(const void *entries, int64_t stride, const void *lens, int rows, i
            (rows <= 1 || stride >= width);
 }
 
+// Whether two tables have memory in common.  (Of tables that lie in one another's range only columns of one buffer are known to
+// have none.)
+bool tables_meet(const int32_t *a, int64_t a_stride, int a_rows, const int32_t *b, int64_t b_stride, int b_rows, int width)
+{
+    if (a_rows <= 0 || b_rows <= 0 || width <= 0)
+        return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a) / 4, b0 = reinterpret_cast<uintptr_t>(b) / 4;
+    const uintptr_t a1 = a0 + (uintptr_t)(a_rows - 1) * a_stride + width, b1 = b0 + (uintptr_t)(b_rows - 1) * b_stride + width;
+    if (a1 <= b0 || b1 <= a0)
+        return false;
+    const uintptr_t stride = a_stride, apart = b0 > a0 ? b0 - a0 : a0 - b0;
+    if (a_stride != b_stride || stride < (uintptr_t)width)
+        return true;
+    return apart % stride < (uintptr_t)width || apart % stride + width > stride;
+}
+
 }  // namespace
 }  // namespace lowm
 
@@ -548,8 +564,7 @@ extern "C" lowm_status_t lowm_fork_pages(const int32_t *page_table, int64_t tabl
 {
     using namespace lowm;
     if (!table_ok(page_table, table_stride, lens, rows, width) || !table_ok(new_table, new_table_stride, new_lens, new_rows, width) ||
-        num_pages <= 0 || page_size <= 0 || !refs || !missing || (new_rows && (!parents || !src || !dst)) ||
-        (rows && new_rows && width && page_table == new_table))
+        num_pages <= 0 || page_size <= 0 || !refs || !missing || (new_rows && (!parents || !src || !dst)))
         return LOWM_ERR_INVALID_ARGUMENT;
     if (rows > kMaxRows || new_rows > kMaxRows)
         return LOWM_ERR_UNSUPPORTED_SHAPE;
@@ -557,6 +572,8 @@ extern "C" lowm_status_t lowm_fork_pages(const int32_t *page_table, int64_t tabl
     for (const void *x : all)
         if (!is_aligned(x, 4))
             return LOWM_ERR_MISALIGNED;
+    if (tables_meet(page_table, table_stride, rows, new_table, new_table_stride, new_rows, width))
+        return LOWM_ERR_INVALID_ARGUMENT;
     int sms = 0;
     lowm_status_t st = host_check_device(&sms);
     if (st != LOWM_OK)

@@ -91,8 +91,8 @@ def fork_pages(page_table, lens, parents, refs, page_size: int, *, out=None, str
     page stays with the first of its rows, and the others get one of their own, to
     be copied (:func:`copy_pages`).  Returns ``(table, lens, src, dst, missing)``:
     the new rows, the copies (int32 [rows], -1: none) and an int32 [1] count of
-    pages that were not to be had.  refs is updated in place; ``out`` is another
-    tensor for the new table.
+    pages that were not to be had.  refs is updated in place; ``out`` is memory for
+    the new table, none of it the old one's.
     """
     device = _cuda(page_table, "page_table")
     if stream is not None or _current_device() != device:

@@ -205,6 +205,15 @@ def test_fork_refusals(kw, want):
     assert fork(**kw) == want
 
 
+
+@pytest.mark.parametrize("kw", [
+    dict(out=PTR + 16), dict(out=PTR - 16), dict(out=PTR + 4), dict(ts=8, os=8, out=PTR + 12), dict(ts=8, os=8, out=PTR - 12),
+    dict(ts=8, os=8, out=PTR + 32 + 12), dict(ts=8, os=4, out=PTR + 32), dict(ts=10, os=10, out=PTR + 28, width=5),
+])
+def test_fork_refuses_a_new_table_that_meets_the_old_one(kw):
+    assert fork(**kw) == INVALID
+
+
 def extend(**kw):
     a = dict(table=PTR, ts=4, lens=PTR, rows=2, width=4, cu=PTR, tokens=3, refs=PTR, pages=8, page=16, pos=PTR, slots=PTR,
              missing=PTR, work=PTR, nbytes=1 << 20, stream=0)

@@ -178,6 +178,27 @@ def test_fork_entries_outside_the_pool_and_rows_longer_than_the_table():
     check_fork(Pool(table, [40, 37, 1000], refs, 16), [1, 1, 0, 0, 2, 2])
 
 
+def test_fork_into_memory_beside_the_old_table():
+    lens = [20, 33, 7, 0]
+    table, refs = make(lens, 16, 12, seed=1, width=4)
+    pool = Pool(table, lens, refs, 16)
+    old, n, r = on_gpu(pool)
+    want = pool.fork([0, 0, 2, 1])
+    both = torch.full((8, 11), 77, device="cuda", dtype=I32)
+    for view in (lambda b: (b[:4, :4], b[:4, 4:8]), lambda b: (b[:4, 5:9], b[:4, 1:5]), lambda b: (b[4:, 2:6], b[:4, 2:6]),
+                 lambda b: (b[:4, 7:11], b[1:5, :4])):
+        both.fill_(77)
+        a, b = view(both)
+        a.copy_(old)
+        counts = r.clone()
+        got = pages.fork_pages(a, n, gpu([0, 0, 2, 1]), counts, 16, out=b)
+        assert b.tolist() == pool.table and got[2].tolist() == want[0] and counts.tolist() == pool.refs
+        assert torch.equal(a, old) and int((both == 77).sum()) == 88 - 32
+    for a, b in ((both[:4, :4], both[:4, 3:7]), (both[:4, 3:7], both[:4, :4]), (both[:4, :4], both[3:7, :4])):
+        with pytest.raises(layer.LowmError):
+            pages.fork_pages(a, n, gpu([0, 0, 2, 1]), r.clone(), 16, out=b)
+
+
 def test_fork_most_rows():
     rows = 8192
     lens = [17] * rows

@@ -49,13 +49,6 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ uint32_t half2_to_e4m3x2(__half2 x)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
-    return r;
-}
-
 // Exact: e4m3 is a subset of fp16.
 __device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t x)
 {

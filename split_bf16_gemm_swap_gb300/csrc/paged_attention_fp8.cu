@@ -58,11 +58,6 @@ enum : uint32_t {
     kErrAttn8Base = 1u << 24,                // dynamic shared memory not on a 1024-byte boundary
 };
 
-struct CutItem8 {
-    int parts;                               // shares the item lies in; 0: there is none
-    int q0, q_len, head, q_tile;
-};
-
 struct Attn8Params : LineParams<kWarps * kWarpRows, kItemCost8, kMinShare8> {
     const __nv_bfloat16 *q;
     const float *k_scale, *v_scale;
@@ -75,7 +70,7 @@ struct Attn8Params : LineParams<kWarps * kWarpRows, kItemCost8, kMinShare8> {
     float scale_log2;                        // scale * log2(e)
     bool q_vec, out_vec;                     // 16-byte rows
     float *parts;                            // [2 * ctas][slot_rows][dim] sums, then [2 * ctas][slot_rows] (max, sum) pairs
-    CutItem8 *cuts;                          // [ctas]
+    CutItem *cuts;                          // [ctas]
     unsigned int *status;
 };
 
@@ -657,7 +652,7 @@ __global__ void __launch_bounds__(kJoinThreads8) join_parts_fp8_kernel(const Att
     }
     if (p.batch == 0)
         return;
-    const CutItem8 cut = p.cuts[blockIdx.x];
+    const CutItem cut = p.cuts[blockIdx.x];
     if (cut.parts == 0)
         return;
     const float2 *ml = reinterpret_cast<const float2 *>(p.parts + 2 * (int64_t)ctas * p.slot_rows * DIM);
@@ -996,7 +991,7 @@ extern "C" size_t lowm_paged_attention_fp8_workspace(int batch, int q_tokens, in
     if (widens(batch, q_tokens, heads, kv_heads, dim, page_size, table_width))
         return (size_t)plan_whole_copy(batch, kv_heads, dim, page_size, table_width).bytes() +
                lowm_paged_attention_workspace(batch, q_tokens, heads, kv_heads, dim);
-    return (size_t)2 * kMaxCtas * slot_rows_fp8(q_tokens, heads, kv_heads) * (dim + 2) * sizeof(float) + kMaxCtas * sizeof(CutItem8);
+    return (size_t)2 * kMaxCtas * slot_rows_fp8(q_tokens, heads, kv_heads) * (dim + 2) * sizeof(float) + kMaxCtas * sizeof(CutItem);
 }
 
 extern "C" lowm_status_t lowm_paged_attention_fp8(
@@ -1186,7 +1181,7 @@ extern "C" lowm_status_t lowm_paged_attention_fp8(
     p.q_vec = is_aligned(q, 16) && !((q_token_stride | q_head_stride) & 7);
     p.out_vec = is_aligned(out, 16) && !((out_token_stride | out_head_stride) & 7);
     p.parts = static_cast<float *>(workspace);
-    p.cuts = reinterpret_cast<CutItem8 *>(static_cast<uint8_t *>(workspace) +
+    p.cuts = reinterpret_cast<CutItem *>(static_cast<uint8_t *>(workspace) +
                                           (size_t)2 * kMaxCtas * p.slot_rows * (dim + 2) * sizeof(float));
     p.status = status;
     return dim == 64 ? launch_fp8<64>(map_k, map_v, p, sms, stream) : launch_fp8<128>(map_k, map_v, p, sms, stream);

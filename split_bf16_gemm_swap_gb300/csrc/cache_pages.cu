@@ -433,8 +433,10 @@ __global__ void __launch_bounds__(128) move_entries_kernel(const Table table, co
 }
 
 // A small pool and table: all of it by one CTA, whose threads have kHereEach pages each.  us, one launch and three: 8 rows of 25
-// on 200 pages 3.2, 5.3; 41 of 100 on 4096 5.2, 7.0; 64 of 256 on 8192 7.8, 7.1; 128 of 512 16.8, 6.8.
-constexpr int kHereEach = 4, kHerePages = kHereEach * kPageThreads, kHereEntries = 4096;
+// on 200 pages 3.5, 6.6; 64 of 64 on 1000 5.1, 7.2; 64 of 128 on 1000 6.7, 7.2, on 2000 7.2, 7.8, on 4000 8.3, 8.9; 96 of 128 on
+// 4000 10.0, 9.1; 128 of 256 17.4, 10.0.  Eight pages a thread would take pools of 8000 (32 of 128 9.1, 10.3) and cost the
+// others: 200 pages 4.2, 4000 with 64 of 128 9.2.
+constexpr int kHereEach = 4, kHerePages = kHereEach * kPageThreads, kHereEntries = 8192;
 
 __global__ void __launch_bounds__(kPageThreads) compact_here_kernel(const Table table, const Pool pool, int32_t *ranks, int32_t *src,
                                                                     int32_t *dst, int32_t *used)

@@ -340,6 +340,24 @@ def test_compact(pages_, fill):
     assert t.tolist() == pool.table and refs.tolist() == pool.refs
 
 
+@pytest.mark.parametrize("rows,width", [(64, 128), (64, 129), (1, 8192), (1, 8193), (8192, 1), (8193, 1), (41, 100)])
+def test_compact_of_tables_around_the_size_for_one_launch(rows, width):
+    r, pool_pages = random.Random(rows), 4096
+    used = r.sample(range(pool_pages), 1500)
+    table = [[r.choice(used) for _ in range(width)] for _ in range(rows)]
+    lens = [r.randint(0, 16 * width + 5) for _ in range(rows)]
+    refs = [0] * pool_pages
+    pool = Pool(table, lens, refs, 16)
+    for i, row in enumerate(table):
+        for p in row[:pool.used(i)]:
+            pool.refs[p] += 1
+    t, n, counts = on_gpu(pool)
+    src, dst, total = pages.compact_pages(t, n, counts, 16)
+    want = pool.compact()
+    assert (src.tolist(), dst.tolist(), total.tolist()) == (want[0], want[1], [want[2]])
+    assert t.tolist() == pool.table and counts.tolist() == pool.refs
+
+
 def test_compact_entries_that_no_count_knows():
     table, lens, refs = gpu([[8, 2, 50, -1]]), gpu([64]), gpu([0, 0, 1, 0, 0, 1, 0, 0, 0, 0])
     src, dst, used = pages.compact_pages(table, lens, refs, 16)

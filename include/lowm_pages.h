@@ -9,6 +9,10 @@
  * `width`.  refs[page] (int32 [num_pages]) is how many rows list the page; 0: it is
  * free.  Entries outside [0, num_pages) are passed over.  Free pages are taken in
  * rising order, so results do not depend on timing.  Conventions as in lowm_layer.h.
+ *
+ * Counts that come from outside of the table keep a page from being taken, not from
+ * being written: the row that has it as its unfinished last page goes on in it, and
+ * appending to 8 bits may move its codes to a larger scale.  Keep whole pages so.
  */
 #ifndef LOWM_PAGES_H
 #define LOWM_PAGES_H
@@ -64,7 +68,9 @@ size_t lowm_extend_pages_workspace(int num_pages);
 /*
  * Brings the `used` pages that are not free together at 0 .. used - 1: those behind
  * move, in order, to the free ones before.  page_table and refs are updated in place;
- * src and dst list the moves for lowm_copy_pages, in order, then -1.
+ * src and dst list the moves for lowm_copy_pages, in order, then -1.  Entries of this
+ * table that count follow their pages; those of another table on the same pool, or
+ * behind lens, do not: every sequence of the pool is to be a row of the one table.
  *   src, dst      int32 [num_pages / 2]; used int32 [1]
  *   workspace     lowm_compact_pages_workspace(num_pages) bytes, 4-byte aligned
  */

@@ -146,9 +146,9 @@ def extend_pages(page_table, lens, cu_new, refs, page_size: int, tokens: int, *,
 def compact_pages(page_table, lens, refs, page_size: int, *, stream=None):
     """Brings the pages in use together at the front of the pool.
 
-    page_table and refs are updated in place.  Returns ``(src, dst, used)``: the
-    moves for :func:`copy_pages` (int32 [num_pages / 2], -1 behind the last) and an
-    int32 [1] count of the pages in use.
+    page_table, which is to hold every sequence of the pool, and refs are updated in
+    place.  Returns ``(src, dst, used)``: the moves for :func:`copy_pages` (int32
+    [num_pages / 2], -1 behind the last) and an int32 [1] count of the pages in use.
     """
     device = _cuda(page_table, "page_table")
     if stream is not None or _current_device() != device:

@@ -939,3 +939,66 @@ def test_large_workspaces_are_not_kept():
     assert not layer._kept
     fp8.paged_attention_fp8(q[:1], kc, vc, ks, vs, table, kv, torch.tensor([0, 1], device="cuda", dtype=torch.int32))
     assert len(layer._kept) == 1
+
+
+# The copy has a pair of factors for a tile, for four keys or for a key: each of them at the edges.
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("block", [1, 2, 4, 16, 64])
+@pytest.mark.parametrize("window", [0, 30])
+def test_attention_of_widened_chunks_with_nan_codes(dim, block, window):
+    lens, q_lens, page = [200, 150], [120, 80], 64
+
+    def change(kc, vc, ks, vs, table, q):
+        for b, n in enumerate(lens):
+            for key, d in ((n - 3, 5), (n - 15, 6), (n - q_lens[b], 7), (n - 40, 8), (2, 9)):
+                vc.view(torch.uint8)[int(table[b, key // page]), key % page, 0, d] = 0xff
+    out, _ = check_attention(lens, q_lens, 4, 2, dim, page, block, window=window, seed=32, change=change, width=ROOM // page, wide=True)
+    assert widened(2, 200, 4, 2, dim, page, ROOM // page) and torch.isnan(out).any() and not torch.isnan(out).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("block", [1, 2, 4, 16, 64])
+@pytest.mark.parametrize("window", [0, 30])
+def test_attention_of_widened_chunks_where_no_row_sees(dim, block, window):
+    lens, q_lens, page = [200, 130, 71, 0], [100, 100, 70, 114], 64
+    kc, vc, ks, vs, table = make_cache(lens, page, block, 2, dim, seed=33, width=ROOM // page)
+    clean = vs.clone()                                              # the bound multiplies by what is not seen, too
+    for b, n in enumerate(lens[:3]):
+        last, first_free = int(table[b, (n - 1) // page]), (n - 1) % page + 1
+        for c in (kc, vc):
+            c.view(torch.uint8)[last, first_free:] = 0x7f
+        for s, x in ((ks, math.nan), (vs, -1.0)):
+            s[last, -(-first_free // block):] = x
+    if window:                                                      # of sequence 0 keys 71 .. are seen
+        for c in (kc, vc):
+            c.view(torch.uint8)[int(table[0, 0])] = 0xff
+        ks[int(table[0, 0])] = math.inf
+        vs[int(table[0, 0])] = math.nan
+    free = [i for i in range(kc.shape[0]) if i not in [int(p) for b, n in enumerate(lens) for p in table[b, :-(-n // page)]]]
+    for c in (kc, vc):
+        c.view(torch.uint8)[free] = 0xff
+    table[1, 1] = kc.shape[0]                                       # reads as zeros
+    cu = [sum(q_lens[:i]) for i in range(5)]
+    assert widened(4, cu[-1], 8, 2, dim, page, ROOM // page)
+    q = rand(cu[-1], 8, dim, seed=36)
+    kv, cu_q = torch.tensor(lens, device="cuda", dtype=torch.int32), torch.tensor(cu, device="cuda", dtype=torch.int32)
+    want, tol, lse = attention64(q, kc, vc, ks, clean, table, lens, cu, 0.125, window, True)
+    out, got = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu_q, scale=0.125, window=window, return_lse=True)
+    bounded(out, want, tol, "attention")
+    seen = torch.isfinite(lse)
+    assert torch.equal(torch.isneginf(got), ~seen) and float((got[seen] - lse[seen]).abs().max()) <= 1e-3
+    in_order()
+
+
+@pytest.mark.parametrize("block", [1, 16, 64])
+@pytest.mark.parametrize("room", [ROOM, 1 << 20])                  # at once, in turns
+def test_widened_chunks_repeat_their_bits(block, room):
+    lens, q_lens, page = [500, 300, 400], [200, 100, 90], 64
+    kc, vc, ks, vs, table = make_cache(lens, page, block, 4, 128, seed=34, width=room // page)
+    cu = torch.tensor([0, 200, 300, 390], device="cuda", dtype=torch.int32)
+    q, kv = rand(390, 16, 128, seed=35), torch.tensor(lens, device="cuda", dtype=torch.int32)
+    assert widened(3, 390, 16, 4, 128, page, room // page)
+    first = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu)
+    for _ in range(10):
+        left_in_shared_memory(0xff)
+        assert torch.equal(fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu), first)

@@ -41,7 +41,7 @@ lowm_status_t lowm_quantize_fp8(const void *x, int64_t x_stride, void *codes, fl
  *     C[m,n] = sum_b a_scale[m,b] w_scale[n / 128, b] sum_{k in block b} A[m,k] W[n,k]
  *
  * over the blocks of 128 along K.  Products of a block are summed by the tensor
- * cores, blocks in fp32 in a fixed order; C is rounded once: the result is
+ * cores, blocks in fp32 in a fixed order (and the two scales are multiplied in fp32); C is rounded once: the result is
  * deterministic.
  *   A             [M, K] e4m3, contiguous; a_scale fp32 [M, ceil(K / 128)]
  *   W             [N, K] e4m3, contiguous; w_scale fp32 [ceil(N / 128), ceil(K / 128)]

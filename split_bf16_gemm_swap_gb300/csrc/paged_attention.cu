@@ -40,7 +40,8 @@
 // (kTileFactors) costs nothing, and v is in the exponent, where the largest weight, v included, is 1 and not rounded.  So it is
 // with a pair for four keys (kQuadFactors): a multiply-add for each score, one for the sum, and 12 loads of 16 bytes a row and
 // tile.  A pair for each key (kKeyFactors) would take 48 loads that way (270 us); it has 32 and multiplies the weights.  Chunks
-// of 1537 tokens over 9000 keys, the copy included: 231, 248 and 259 us; errors 0.0021, 0.0022 and 0.0024 of the result.
+// of 1537 tokens over 9000 keys, the copy included: 227, 247 and 258 us; errors 0.00214, 0.00217 and 0.00237 of the result,
+// whose own rounding is 0.00166 (the weights' to bf16 is the rest).
 //
 // Rounding: weights meet V in bf16 (the type of the tensor cores' operand);
 // their sum, which divides, adds the unrounded fp32 weights.

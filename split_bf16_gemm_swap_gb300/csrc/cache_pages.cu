@@ -550,8 +550,8 @@ bool tables_meet(const int32_t *a, int64_t a_stride, int a_rows, const int32_t *
     const uintptr_t a1 = a0 + (uintptr_t)(a_rows - 1) * a_stride + width, b1 = b0 + (uintptr_t)(b_rows - 1) * b_stride + width;
     if (a1 <= b0 || b1 <= a0)
         return false;
-    const uintptr_t stride = a_stride, apart = b0 > a0 ? b0 - a0 : a0 - b0;
-    if (a_stride != b_stride || stride < (uintptr_t)width)
+    const uintptr_t stride = a_rows > 1 ? a_stride : b_stride, apart = b0 > a0 ? b0 - a0 : a0 - b0;
+    if ((a_rows > 1 && b_rows > 1 && a_stride != b_stride) || stride < (uintptr_t)width)
         return true;
     return apart % stride < (uintptr_t)width || apart % stride + width > stride;
 }

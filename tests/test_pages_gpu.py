@@ -194,6 +194,12 @@ def test_fork_into_memory_beside_the_old_table():
         got = pages.fork_pages(a, n, gpu([0, 0, 2, 1]), counts, 16, out=b)
         assert b.tolist() == pool.table and got[2].tolist() == want[0] and counts.tolist() == pool.refs
         assert torch.equal(a, old) and int((both == 77).sum()) == 88 - 32
+    both.fill_(77)
+    both[:4, 2:6].copy_(old)
+    want = Pool(table, lens, refs, 16)
+    want.fork([3])
+    got = pages.fork_pages(both[:4, 2:6], n, gpu([3]), r.clone(), 16, out=both[2:3, 6:10])        # a row in the gap between rows
+    assert got[0].tolist() == want.table and torch.equal(both[:4, 2:6], old)
     for a, b in ((both[:4, :4], both[:4, 3:7]), (both[:4, 3:7], both[:4, :4]), (both[:4, :4], both[3:7, :4])):
         with pytest.raises(layer.LowmError):
             pages.fork_pages(a, n, gpu([0, 0, 2, 1]), r.clone(), 16, out=b)

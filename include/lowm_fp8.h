@@ -41,8 +41,8 @@ lowm_status_t lowm_quantize_fp8(const void *x, int64_t x_stride, void *codes, fl
  *     C[m,n] = sum_b a_scale[m,b] w_scale[n / 128, b] sum_{k in block b} A[m,k] W[n,k]
  *
  * over the blocks of 128 along K.  Products of a block are summed by the tensor
- * cores, blocks in fp32 in a fixed order (and the two scales are multiplied in fp32); C is rounded once: the result is
- * deterministic.
+ * cores, blocks in fp32 in a fixed order (the two scales are multiplied in fp32); C is
+ * rounded once: the result is deterministic.
  *   A             [M, K] e4m3, contiguous; a_scale fp32 [M, ceil(K / 128)]
  *   W             [N, K] e4m3, contiguous; w_scale fp32 [ceil(N / 128), ceil(K / 128)]
  *   C             [M, N] bf16, contiguous
@@ -114,12 +114,11 @@ lowm_status_t lowm_rope_append_fp8(const void *q, int64_t q_token_stride, int64_
  *                 the rows that see its tokens NaN
  *   block         a power of two, at most page_size
  * The other arguments, their limits and what a row that sees nothing gets are
- * those of lowm_paged_attention.  A length that the table has no room for counts as the
- * table's room.  What a page or a scale holds past a sequence's
- * length or before its window does not matter, NaN included; a NaN code reaches the
- * rows that see its token and no others.  An element of q that is not finite makes
- * its row NaN, or zeros where it makes all of the row's scores -inf.  The result is
- * deterministic.
+ * those of lowm_paged_attention.  A length that the table has no room for counts as
+ * the table's room.  What a page or a scale holds past a sequence's length or before
+ * its window does not matter, NaN included; a NaN code reaches the rows that see its
+ * token and no others.  An element of q that is not finite makes its row NaN, or
+ * zeros where it makes all of the row's scores -inf.  The result is deterministic.
  */
 lowm_status_t lowm_paged_attention_fp8(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                                        const void *k_cache, int64_t k_page_stride, int64_t k_place_stride,

@@ -1002,3 +1002,30 @@ def test_widened_chunks_repeat_their_bits(block, room):
     for _ in range(10):
         left_in_shared_memory(0xff)
         assert torch.equal(fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, kv, cu), first)
+
+
+@pytest.mark.parametrize("window", [0, 100])
+def test_a_captured_call_in_turns_follows_the_lengths(window):
+    # which sequences share a turn is decided by the device: other lengths, other tables and other rows of q in a replay
+    page, room, heads, kv_heads, dim = 64, 1 << 20, 8, 2, 64
+    kc, vc, ks, vs, table = make_cache([900, 900, 900, 900], page, 16, kv_heads, dim, seed=37, width=room // page)
+    q = rand(400, heads, dim, seed=38)
+    kv, cu = (torch.zeros(n, device="cuda", dtype=torch.int32) for n in (4, 5))
+    args = (q, kc, vc, ks, vs, table, kv, cu)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        fp8.paged_attention_fp8(*args, window=window)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, got = fp8.paged_attention_fp8(*args, window=window, return_lse=True)
+    for lens, starts in (([900, 0, 500, 70], [0, 100, 200, 300, 400]), ([0, 0, 0, 900], [0, 0, 0, 1, 390]),
+                         ([300, 900, 900, 64], [7, 250, 250, 350, 350]), ([0, 0, 0, 0], [0, 0, 0, 0, 0])):
+        kv.copy_(torch.tensor(lens)), cu.copy_(torch.tensor(starts))
+        table.copy_(table.roll(1, 0))
+        want, tol, lse = attention64(q, kc, vc, ks, vs, table[:, :15], lens, starts, dim ** -0.5, window, True)
+        out.fill_(math.nan), got.fill_(math.nan)
+        graph.replay()
+        bounded(out, want, tol, "attention")
+        assert torch.equal(torch.isneginf(got), torch.isneginf(lse)) and not torch.isnan(got).any()
+    in_order()

@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams 
         stop = p.turns[p.turn + 1];
         for (int i = (int)((blockIdx.y * gridDim.x + blockIdx.x) * kWidenThreads + threadIdx.x); i <= p.batch;
              i += (int)(gridDim.x * gridDim.y * kWidenThreads))
-            p.turn_cu_q[i] = min(max(p.cu_q[i], p.cu_q[begin]), p.cu_q[stop]);
+            p.turn_cu_q[i] = p.cu_q[min(max(i, begin), stop)];
     }
     for (int b = begin + (int)blockIdx.y; b < stop; b += (int)gridDim.y) {
         int first, kv;

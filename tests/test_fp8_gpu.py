@@ -1029,3 +1029,18 @@ def test_a_captured_call_in_turns_follows_the_lengths(window):
         bounded(out, want, tol, "attention")
         assert torch.equal(torch.isneginf(got), torch.isneginf(lse)) and not torch.isnan(got).any()
     in_order()
+
+
+@pytest.mark.parametrize("room", [ROOM, 1 << 20])
+def test_chunks_whose_starts_do_not_rise(room):
+    # not a call that means anything: sequences whose starts fall have no rows, and the others' are as they would be alone
+    page, heads, kv_heads, dim = 64, 8, 2, 64
+    kc, vc, ks, vs, table = make_cache([300, 400, 500, 200], page, 16, kv_heads, dim, seed=39, width=room // page)
+    q, lens = rand(500, heads, dim, seed=40), torch.tensor([300, 400, 500, 200], device="cuda", dtype=torch.int32)
+    cu = torch.tensor([0, 300, 50, 150, 500], device="cuda", dtype=torch.int32)     # sequence 1 falls back; 2 lies in 0's rows
+    assert widened(4, 500, heads, kv_heads, dim, page, room // page)
+    out = fp8.paged_attention_fp8(q, kc, vc, ks, vs, table, lens, cu)
+    alone = torch.tensor([150, 500], device="cuda", dtype=torch.int32)
+    want, tol, _ = attention64(q, kc, vc, ks, vs, table[3:, :8], lens[3:], alone, dim ** -0.5, 0, True)
+    bounded(out[300:], want[300:], tol[300:], "attention")
+    in_order()
